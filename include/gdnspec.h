@@ -59,6 +59,7 @@ extern "C" {
 #define GDN_ERR_DEVICE (-6)   /* current device is not sm_103 */
 #define GDN_ERR_CAPACITY (-7) /* request larger than a fixed on-device capacity (gdn_tree_verify_noalloc's
                                  scratch array) */
+#define GDN_ERR_INDEX (-8)    /* sequence offsets or a state index out of range (device-detected) */
 
 /* ---- q/k/v element types ------------------------------------------------ */
 #define GDN_DTYPE_BF16 0
@@ -442,6 +443,101 @@ int gdn_gla_tree_verify(const void* q, const void* k, const void* v, int dtype, 
                         cudaStream_t stream);
 int gdn_gla_commit(const float* S0, const void* factors, const int32_t* accepted_path, int Lmax,
                    float* S_new, int B, int N, int H, int dk, int dv, int dtype, cudaStream_t stream);
+
+/*
+ * The gated delta rule over packed sequences: prefill and training.
+ *   S' = e^{log_alpha_t} S_{t-1},  S_t = S' + beta_t (v_t - S' k_t) k_t^T,  o_t = S_t q_t
+ * for each (sequence, head), from S0 to the state after the last token.
+ *
+ *   q, k       dtype, token t's row at q + t ldq: [Hk][d_k]; value head h reads head
+ *              h / (H / Hk) of q and k (Hk divides H)
+ *   v          dtype, token t's row at v + t ldv: [H][d_v]
+ *   ldq/ldk/ldv  elements between tokens: at least a row, a multiple of 16 bytes (so q, k and v
+ *              may be columns of one projection)
+ *   log_alpha, beta  fp32 [total][H]; log_alpha <= 0, -inf forgets the state.  The gate is given
+ *              as its logarithm: its gradient keeps its meaning where the decay is close to zero
+ *   S0         fp32 [nseq][H][d_v][d_k], or null for zero
+ *   offsets    int32 [nseq + 1]: sequence s has the tokens offsets[s] .. offsets[s + 1] - 1 (none
+ *              is allowed: its state passes through).  Null: total / nseq tokens each.
+ *              Offsets that decrease or leave [0, total] -> GDN_ERR_INDEX; those sequences'
+ *              outputs are not written
+ *   out        dtype [total][H][d_v]
+ *   S_T        fp32 [nseq][H][d_v][d_k], or null; may be S0 itself
+ *   record     gdn_seq_record_bytes bytes for gdn_seq_backward, or null
+ *   workspace  gdn_seq_workspace_bytes bytes, scratch during the call
+ * log_alpha, beta and offsets need 4-byte alignment only (here and in gdn_seq_step).
+ * 0 <= total, d_k and d_v in {16, 32, ..., 256}; outputs do not overlap inputs or one another.
+ * The products with bf16 q, k, v are exact to fp32 rounding; S_T is fp32 throughout.
+ *
+ * gdn_seq_backward: gradients for dout (dtype [total][H][d_v]) and dS_T (null: zero).  The first
+ * arguments and the record are those of the forward call, unchanged.
+ *   dq, dk_out dtype [total][Hk][d_k], summed over the heads that share them
+ *   dv_out     dtype [total][H][d_v]
+ *   dlog_alpha, dbeta  fp32 [total][H]
+ *   dS0        fp32 [nseq][H][d_v][d_k], or null; may be dS_T itself
+ * Equal inputs give equal bits (no atomics).
+ */
+int gdn_seq_workspace_bytes(int nseq, int total, int H, int Hk, int dk, int dv, int dtype, size_t* bytes);
+int gdn_seq_record_bytes(int nseq, int total, int H, int Hk, int dk, int dv, int dtype, size_t* bytes);
+int gdn_seq_forward(const void* q, int ldq, const void* k, int ldk, const void* v, int ldv, int dtype,
+                    const float* log_alpha, const float* beta, const float* S0, const int32_t* offsets, void* out,
+                    float* S_T, void* record, void* workspace, int nseq, int total, int H, int Hk, int dk, int dv,
+                    cudaStream_t stream);
+int gdn_seq_backward(const void* q, int ldq, const void* k, int ldk, const void* v, int ldv, int dtype,
+                     const float* log_alpha, const float* beta, const int32_t* offsets, const void* dout,
+                     const float* dS_T, const void* record, void* dq, void* dk_out, void* dv_out, float* dlog_alpha,
+                     float* dbeta, float* dS0, void* workspace, int nseq, int total, int H, int Hk, int dk, int dv,
+                     cudaStream_t stream);
+
+/*
+ * One token for each of B sequences, states updated in place (decode).
+ *   q, k       dtype [B][Hk][d_k];  v dtype [B][H][d_v];  log_alpha, beta fp32 [B][H]
+ *   S          fp32 [slots][H][d_v][d_k], the pool of states
+ *   state_index int32 [B]: row b's slot; -1 for an empty row (its output is zero and no state
+ *              changes).  Null: slot b.  Other values outside [0, slots) -> GDN_ERR_INDEX, and the
+ *              row is treated as empty.  Two rows of one call name different slots
+ *   out        dtype [B][H][d_v]
+ */
+int gdn_seq_step(const void* q, const void* k, const void* v, int dtype, const float* log_alpha, const float* beta,
+                 float* S, const int32_t* state_index, void* out, int B, int slots, int H, int Hk, int dk, int dv,
+                 cudaStream_t stream);
+
+/*
+ * Norm of each head's output, with its weight and its gate: y = weight (o r) silu(gate),
+ * r = (mean o^2 + eps)^{-1/2}; rows = tokens x heads of d values (d in {16, 32, ..., 256}).
+ *   o o_dtype [rows][d];  gate, out dtype [rows][d];  weight dtype [d];  rows >= 1, eps > 0
+ * out may be o or gate itself where the types agree.
+ * Backward: dout_y dtype; d_o o_dtype, dgate dtype, dweight fp32 [d], apart from the inputs and
+ * one another.  workspace: gdn_norm_workspace_bytes(rows, d) bytes.
+ */
+int gdn_norm_workspace_bytes(long long rows, int width, size_t* bytes);
+int gdn_gated_norm(const void* o, int o_dtype, const void* gate, const void* weight, void* out, int dtype,
+                   long long rows, int d, float eps, cudaStream_t stream);
+int gdn_gated_norm_backward(const void* o, int o_dtype, const void* gate, const void* weight, const void* dout_y,
+                            void* d_o, void* dgate, float* dweight, void* workspace, int dtype, long long rows, int d,
+                            float eps, cudaStream_t stream);
+
+/*
+ * Between two blocks: the block's output z normed, gated and added to the scaled residual stream,
+ * and the next block's input normed from it:
+ *   x_out = res_scale x + gate (post_weight (z r1)),   h = weight (x_out r2),
+ * r the reciprocal root mean squares (eps inside).  x_out is rounded once, h is formed from the
+ * unrounded sum.
+ *   x, z, x_out, h dtype [rows][width];  post_weight, gate, weight dtype [width]
+ * Before the first block: z, post_weight, gate and x_out null and res_scale 1, and h = weight (x r).
+ * width a multiple of 8, at most 8192; rows >= 1, eps > 0.  x_out or h may be x or z itself.
+ * Backward: the gradients dh of h and dx_out (null: zero) of the stream behind it, at the x_out
+ * that the forward pass wrote (without z: at x).  dx, dz dtype; dpost_weight, dgate, dweight
+ * fp32 [width]; dz, dpost_weight and dgate null where z is; none of them overlaps an input.
+ * workspace: gdn_norm_workspace_bytes(rows, width) bytes.  Equal inputs give equal bits.
+ */
+int gdn_block_norm(const void* x, const void* z, const void* post_weight, const void* gate, const void* weight,
+                   void* x_out, void* h, int dtype, long long rows, int width, float eps, float res_scale,
+                   cudaStream_t stream);
+int gdn_block_norm_backward(const void* x_out, const void* z, const void* post_weight, const void* gate,
+                            const void* weight, const void* dh, const void* dx_out, void* dx, void* dz,
+                            float* dpost_weight, float* dgate, float* dweight, void* workspace, int dtype,
+                            long long rows, int width, float eps, float res_scale, cudaStream_t stream);
 
 /*
  * Launch overlap between consecutive calls (process-wide switch, default off;

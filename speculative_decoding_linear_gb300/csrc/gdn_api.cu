@@ -268,6 +268,7 @@ const char* gdn_strerror(int code) {
         case GDN_ERR_DEVICE: return "current device is not an sm_103 GPU";
         case GDN_ERR_CAPACITY:
             return "request exceeds a fixed on-device capacity (gdn_tree_verify_noalloc's scratch array)";
+        case GDN_ERR_INDEX: return "sequence offsets or a state index out of range";
         default: return "unknown status";
     }
 }

@@ -22,7 +22,8 @@ from . import build as _build
 _lib = None
 _lock = threading.Lock()
 
-OK, ERR_ARG, ERR_TREE, ERR_PATH, ERR_TIMEOUT, ERR_CUDA, ERR_DEVICE, ERR_CAPACITY = 0, -1, -2, -3, -4, -5, -6, -7
+OK, ERR_ARG, ERR_TREE, ERR_PATH, ERR_TIMEOUT, ERR_CUDA, ERR_DEVICE, ERR_CAPACITY, ERR_INDEX = (
+    0, -1, -2, -3, -4, -5, -6, -7, -8)
 DTYPE_BF16, DTYPE_F32 = 0, 1
 
 # (name, restype, argtypes) for every extern "C" symbol of include/gdnspec.h
@@ -61,6 +62,16 @@ SIGNATURES = {
     "gdn_gla_workspace_bytes": (_I, [_I, _I, _I, _I, _I, ctypes.POINTER(_S)]),
     "gdn_gla_tree_verify": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
     "gdn_gla_commit": (_I, [_P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "gdn_seq_workspace_bytes": (_I, [_I] * 7 + [ctypes.POINTER(_S)]),
+    "gdn_seq_record_bytes": (_I, [_I] * 7 + [ctypes.POINTER(_S)]),
+    "gdn_seq_forward": (_I, [_P, _I, _P, _I, _P, _I, _I] + [_P] * 8 + [_I] * 6 + [_P]),
+    "gdn_seq_backward": (_I, [_P, _I, _P, _I, _P, _I, _I] + [_P] * 13 + [_I] * 6 + [_P]),
+    "gdn_seq_step": (_I, [_P, _P, _P, _I] + [_P] * 5 + [_I] * 6 + [_P]),
+    "gdn_norm_workspace_bytes": (_I, [ctypes.c_longlong, _I, ctypes.POINTER(_S)]),
+    "gdn_gated_norm": (_I, [_P, _I, _P, _P, _P, _I, ctypes.c_longlong, _I, ctypes.c_float, _P]),
+    "gdn_gated_norm_backward": (_I, [_P, _I] + [_P] * 7 + [_I, ctypes.c_longlong, _I, ctypes.c_float, _P]),
+    "gdn_block_norm": (_I, [_P] * 7 + [_I, ctypes.c_longlong, _I, ctypes.c_float, ctypes.c_float, _P]),
+    "gdn_block_norm_backward": (_I, [_P] * 13 + [_I, ctypes.c_longlong, _I, ctypes.c_float, ctypes.c_float, _P]),
     "gdn_set_launch_overlap": (_I, [_I]),
     "gdn_set_wait_limit_ns": (_I, [ctypes.c_ulonglong]),
     "gdn_selftest_stuck_wait": (_I, [_P]),
@@ -419,6 +430,192 @@ def gla_factor_views(buf, B, N, H, dk, dv, dtype):
     g = buf[o_g: o_g + BHN * dk * 4].view(torch.float32).view(B, H, N, dk)
     par = buf[o_par: o_par + B * N * 4].view(torch.int32).view(B, N)
     return delta, key, g, par
+
+
+def gdn_seq_workspace_bytes(nseq, total, H, Hk, dk, dv, dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().gdn_seq_workspace_bytes(nseq, total, H, Hk, dk, dv, dtype_code(dtype), ctypes.byref(out)),
+           "gdn_seq_workspace_bytes")
+    return out.value
+
+
+def gdn_seq_record_bytes(nseq, total, H, Hk, dk, dv, dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().gdn_seq_record_bytes(nseq, total, H, Hk, dk, dv, dtype_code(dtype), ctypes.byref(out)),
+           "gdn_seq_record_bytes")
+    return out.value
+
+
+def empty_seq_workspace(nseq, total, H, Hk, dk, dv, dtype, device="cuda"):
+    return torch.empty(max(16, gdn_seq_workspace_bytes(nseq, total, H, Hk, dk, dv, dtype)), dtype=torch.uint8, device=device)
+
+
+def empty_seq_record(nseq, total, H, Hk, dk, dv, dtype, device="cuda"):
+    """Caller-owned record that gdn_seq_forward writes for gdn_seq_backward."""
+    return torch.empty(max(16, gdn_seq_record_bytes(nseq, total, H, Hk, dk, dv, dtype)), dtype=torch.uint8, device=device)
+
+
+def _tokens(x, what):
+    """(pointer, elements between tokens) of [total, heads, d] or [nseq, T, heads, d]; the tokens may be
+    columns of a wider tensor, everything inside a token is dense."""
+    if not x.is_cuda:
+        raise ValueError("%s: expected a CUDA tensor" % what)
+    heads, d = x.shape[-2:]
+    ld = x.stride(-3) if x.shape[-3] > 1 else (x.stride(0) if x.dim() == 4 and x.shape[0] > 1 else heads * d)
+    dense = (d == 1 or x.stride(-1) == 1) and (heads == 1 or x.stride(-2) == d)
+    if x.dim() == 4 and x.shape[0] > 1 and x.shape[1] > 0:
+        dense = dense and x.stride(0) == x.shape[1] * ld
+    if not dense and x.numel() > 0:
+        raise ValueError("%s: heads and channels of a token must be dense, tokens evenly spaced" % what)
+    return x.data_ptr() or None, ld
+
+
+def _seq_dims(q, k, v, log_alpha, beta, offsets):
+    """(nseq, total, H, Hk, dk, dv) of a sequence call, its shapes checked against one another."""
+    if q.dim() not in (3, 4) or v.dim() != q.dim() or k.shape != q.shape or v.shape[:-2] != q.shape[:-2]:
+        raise ValueError("q, k [.., Hk, dk] and v [.., H, dv] must have the same leading dimensions")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must have one type")
+    total = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
+    for x in (log_alpha, beta):
+        if x.dtype != torch.float32 or x.shape != v.shape[:-1]:
+            raise ValueError("log_alpha and beta must be fp32 %s" % (tuple(v.shape[:-1]),))
+    if offsets is None:
+        nseq = q.shape[0] if q.dim() == 4 else 1
+    else:
+        if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2:
+            raise ValueError("offsets must be int32 [nseq + 1]")
+        nseq = offsets.numel() - 1
+    return nseq, total, v.shape[-2], q.shape[-2], q.shape[-1], v.shape[-1]
+
+
+def _same(x, shape, dtype, what):
+    if x is not None and (tuple(x.shape) != tuple(shape) or x.dtype != dtype):
+        raise ValueError("%s must be %s %s" % (what, dtype, tuple(shape)))
+
+
+def _sized(x, nbytes, what):
+    if x is not None and x.numel() * x.element_size() < nbytes:
+        raise ValueError("%s: %d bytes wanted" % (what, nbytes))
+
+
+def gdn_seq_forward(q, k, v, log_alpha, beta, S0, out, S_T, workspace, offsets=None, record=None, stream=None):
+    """The gated delta rule over packed sequences (see include/gdnspec.h): q, k [total, Hk, dk], v [total, H, dv]
+    with offsets int32 [nseq + 1], or [nseq, T, heads, d] without.  S0 and S_T [nseq, H, dv, dk] fp32 may be None."""
+    nseq, total, H, Hk, dk, dv = dims = _seq_dims(q, k, v, log_alpha, beta, offsets)
+    _same(out, v.shape, v.dtype, "out")
+    _same(S0, (nseq, H, dv, dk), torch.float32, "S0")
+    _same(S_T, (nseq, H, dv, dk), torch.float32, "S_T")
+    _sized(workspace, gdn_seq_workspace_bytes(*dims, q.dtype), "workspace")
+    if record is not None:
+        _sized(record, gdn_seq_record_bytes(*dims, q.dtype), "record")
+    qp, ldq = _tokens(q, "q")
+    kp, ldk = _tokens(k, "k")
+    vp, ldv = _tokens(v, "v")
+    _check(lib().gdn_seq_forward(qp, ldq, kp, ldk, vp, ldv, dtype_code(q.dtype), _ptr(log_alpha), _ptr(beta), _ptr(S0),
+                                 _ptr(offsets), _ptr(out), _ptr(S_T), _ptr(record), _ptr(workspace), *dims,
+                                 _stream(stream)), "gdn_seq_forward")
+
+
+def gdn_seq_backward(q, k, v, log_alpha, beta, dout, dS_T, record, dq, dk, dv, dlog_alpha, dbeta, dS0, workspace,
+                     offsets=None, stream=None):
+    """Gradients of gdn_seq_forward at the record that it wrote (see include/gdnspec.h); dS_T and dS0 may be None."""
+    dims = nseq, total, H, Hk, d_k, d_v = _seq_dims(q, k, v, log_alpha, beta, offsets)
+    for x, like, what in ((dout, v, "dout"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv"), (dlog_alpha, log_alpha, "dlog_alpha"),
+                          (dbeta, beta, "dbeta")):
+        _same(x, like.shape, like.dtype, what)
+    _same(dS_T, (nseq, H, d_v, d_k), torch.float32, "dS_T")
+    _same(dS0, (nseq, H, d_v, d_k), torch.float32, "dS0")
+    _sized(workspace, gdn_seq_workspace_bytes(*dims, q.dtype), "workspace")
+    _sized(record, gdn_seq_record_bytes(*dims, q.dtype), "record")
+    qp, ldq = _tokens(q, "q")
+    kp, ldk = _tokens(k, "k")
+    vp, ldv = _tokens(v, "v")
+    _check(lib().gdn_seq_backward(qp, ldq, kp, ldk, vp, ldv, dtype_code(q.dtype), _ptr(log_alpha), _ptr(beta),
+                                  _ptr(offsets), _ptr(dout), _ptr(dS_T), _ptr(record), _ptr(dq), _ptr(dk), _ptr(dv),
+                                  _ptr(dlog_alpha), _ptr(dbeta), _ptr(dS0), _ptr(workspace), *dims, _stream(stream)),
+           "gdn_seq_backward")
+
+
+def gdn_seq_step(q, k, v, log_alpha, beta, S, out, state_index=None, stream=None):
+    """One token for each of B sequences, the states S [slots, H, dv, dk] fp32 updated in place (see
+    include/gdnspec.h); state_index int32 [B], -1 for an empty row."""
+    B, Hk, dk = q.shape
+    H, dv = v.shape[-2:]
+    if k.shape != q.shape or v.shape[0] != B or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k [B, Hk, dk] and v [B, H, dv] must agree in B and type")
+    _same(log_alpha, (B, H), torch.float32, "log_alpha")
+    _same(beta, (B, H), torch.float32, "beta")
+    _same(S, (S.shape[0], H, dv, dk), torch.float32, "S")
+    _same(out, v.shape, v.dtype, "out")
+    _same(state_index, (B,), torch.int32, "state_index")
+    _check(lib().gdn_seq_step(_ptr(q), _ptr(k), _ptr(v), dtype_code(q.dtype), _ptr(log_alpha), _ptr(beta), _ptr(S),
+                              _ptr(state_index), _ptr(out), B, S.shape[0], H, Hk, dk, dv, _stream(stream)), "gdn_seq_step")
+
+
+def empty_norm_workspace(rows, width, device="cuda"):
+    out = ctypes.c_size_t(0)
+    _check(lib().gdn_norm_workspace_bytes(rows, width, ctypes.byref(out)), "gdn_norm_workspace_bytes")
+    return torch.empty(out.value, dtype=torch.uint8, device=device)
+
+
+def _norm_workspace(workspace, rows, width):
+    out = ctypes.c_size_t(0)
+    _check(lib().gdn_norm_workspace_bytes(rows, width, ctypes.byref(out)), "gdn_norm_workspace_bytes")
+    _sized(workspace, out.value, "workspace")
+
+
+def gdn_gated_norm(o, gate, weight, out, eps=1e-6, stream=None):
+    """out = weight * RMSNorm(o) * silu(gate) over the last dimension (see include/gdnspec.h)."""
+    d = o.shape[-1]
+    _same(gate, o.shape, gate.dtype, "gate")
+    _same(weight, (d,), gate.dtype, "weight")
+    _same(out, o.shape, gate.dtype, "out")
+    _check(lib().gdn_gated_norm(_ptr(o), dtype_code(o.dtype), _ptr(gate), _ptr(weight), _ptr(out), dtype_code(gate.dtype),
+                                o.numel() // d, d, eps, _stream(stream)), "gdn_gated_norm")
+
+
+def gdn_gated_norm_backward(o, gate, weight, dout, d_o, dgate, dweight, workspace, eps=1e-6, stream=None):
+    """Gradients of gdn_gated_norm: d_o as o, dgate as gate, dweight fp32 [d] (see include/gdnspec.h)."""
+    d = o.shape[-1]
+    for x, what in ((gate, "gate"), (dout, "dout"), (dgate, "dgate")):
+        _same(x, o.shape, gate.dtype, what)
+    _same(weight, (d,), gate.dtype, "weight")
+    _same(d_o, o.shape, o.dtype, "d_o")
+    _same(dweight, (d,), torch.float32, "dweight")
+    _norm_workspace(workspace, o.numel() // d, d)
+    _check(lib().gdn_gated_norm_backward(_ptr(o), dtype_code(o.dtype), _ptr(gate), _ptr(weight), _ptr(dout), _ptr(d_o),
+                                         _ptr(dgate), _ptr(dweight), _ptr(workspace), dtype_code(gate.dtype),
+                                         o.numel() // d, d, eps, _stream(stream)), "gdn_gated_norm_backward")
+
+
+def gdn_block_norm(x, z, post_weight, gate, weight, x_out, h, eps=1e-6, res_scale=1.0, stream=None):
+    """x_out = res_scale x + gate * post_weight * RMSNorm(z); h = weight * RMSNorm(x_out) (see include/gdnspec.h).
+    z, post_weight, gate and x_out None: h = weight * RMSNorm(x)."""
+    D = x.shape[-1]
+    for t, what in ((z, "z"), (x_out, "x_out"), (h, "h")):
+        _same(t, x.shape, x.dtype, what)
+    for t, what in ((post_weight, "post_weight"), (gate, "gate"), (weight, "weight")):
+        _same(t, (D,), x.dtype, what)
+    _check(lib().gdn_block_norm(_ptr(x), _ptr(z), _ptr(post_weight), _ptr(gate), _ptr(weight), _ptr(x_out), _ptr(h),
+                                dtype_code(x.dtype), x.numel() // D, D, eps, res_scale, _stream(stream)), "gdn_block_norm")
+
+
+def gdn_block_norm_backward(x_out, z, post_weight, gate, weight, dh, dx_out, dx, dz, dpost_weight, dgate, dweight,
+                            workspace, eps=1e-6, res_scale=1.0, stream=None):
+    """Gradients of gdn_block_norm at the x_out that it wrote (see include/gdnspec.h); dx_out may be None."""
+    D = x_out.shape[-1]
+    for t, what in ((z, "z"), (dh, "dh"), (dx_out, "dx_out"), (dx, "dx"), (dz, "dz")):
+        _same(t, x_out.shape, x_out.dtype, what)
+    for t, what in ((post_weight, "post_weight"), (gate, "gate"), (weight, "weight")):
+        _same(t, (D,), x_out.dtype, what)
+    for t, what in ((dpost_weight, "dpost_weight"), (dgate, "dgate"), (dweight, "dweight")):
+        _same(t, (D,), torch.float32, what)
+    _norm_workspace(workspace, x_out.numel() // D, D)
+    _check(lib().gdn_block_norm_backward(_ptr(x_out), _ptr(z), _ptr(post_weight), _ptr(gate), _ptr(weight), _ptr(dh),
+                                         _ptr(dx_out), _ptr(dx), _ptr(dz), _ptr(dpost_weight), _ptr(dgate), _ptr(dweight),
+                                         _ptr(workspace), dtype_code(x_out.dtype), x_out.numel() // D, D, eps, res_scale,
+                                         _stream(stream)), "gdn_block_norm_backward")
 
 
 def gdn_set_launch_overlap(enable: bool) -> bool:
