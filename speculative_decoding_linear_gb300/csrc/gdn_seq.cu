@@ -20,7 +20,7 @@
 //   dbeta_j = sum_t G_tj ((q_t.k_j)(dO_t.eps_j) - [t>j] (k_t.k_j)(dV_t.eps_j)) + k_j.w2_j
 //   dla_t = e^{g_end} <S, dS+> + sum_{s<t} beta_s k_s.w2_s + sum_{s>=t} (q_s.dq_s + k_s.read_s - k_s.write'_s)
 // (write' without the w2 term).  No division by beta or alpha: both may be zero.
-#include "gdn_seq.cuh"
+#include "gdn_seq_tc.cuh"
 
 namespace gdn {
 
@@ -346,18 +346,24 @@ cudaError_t launch_seq_backward_simt(const SeqArgs& a, int dtype, cudaStream_t s
     return dtype == GDN_DTYPE_F32 ? backward_simt<float>(a, L, st) : backward_simt<__nv_bfloat16>(a, L, st);
 }
 
-SeqLayout seq_layout(const SeqShape& s, int) {
+SeqLayout seq_layout(const SeqShape& s, int dtype) {
     SeqLayout L = {};
+    const bool tc = seq_tc_takes(s, dtype);
     const size_t slots = seq_slots(s.nseq, s.total), state = slots * s.H * s.dk * s.dv * 4;
-    const size_t rows = (size_t)s.total * s.H * s.dv * 4, heads = (size_t)s.total * s.Hk * s.dk * 4;
+    // the tensor-core kernels keep rows of tokens for whole chunks
+    const size_t rows = (tc ? slots * kChunk : (size_t)s.total) * s.H * s.dv * 4;
+    const size_t heads = s.H > s.Hk ? (size_t)s.total * s.Hk * s.dk * 4 : 0;
+    const size_t ops = tc ? slots * s.H * seqtc::kOpBytes : 0;
     L.rec_S = 0;
     L.rec_eps = align_up(L.rec_S + state, kSectionAlign);
-    L.rec_total = align_up(L.rec_eps + rows, kSectionAlign);
-    L.ws_dS = 0;
+    L.rec_op = align_up(L.rec_eps + rows, kSectionAlign);
+    L.rec_total = align_up(L.rec_op + ops, kSectionAlign);
+    L.ws_op = 0;
+    L.ws_dS = align_up(L.ws_op + ops, kSectionAlign);
     L.ws_dV = align_up(L.ws_dS + state, kSectionAlign);
     L.ws_dq = align_up(L.ws_dV + rows, kSectionAlign);
-    L.ws_dk = align_up(L.ws_dq + (s.H > s.Hk ? heads : 0), kSectionAlign);
-    L.ws_total = align_up(L.ws_dk + (s.H > s.Hk ? heads : 0), kSectionAlign);
+    L.ws_dk = align_up(L.ws_dq + heads, kSectionAlign);
+    L.ws_total = align_up(L.ws_dk + heads, kSectionAlign);
     return L;
 }
 
@@ -467,7 +473,9 @@ int gdn_seq_forward(const void* q, int ldq, const void* k, int ldk, const void* 
     a.S_T = S_T;
     a.rec = static_cast<char*>(record);
     a.ws = static_cast<char*>(workspace);
-    return launch_seq_forward_simt(a, dtype, stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    const bool tc = total > 0 && record == nullptr && seq_tc_takes(s, dtype);
+    const cudaError_t rc = tc ? launch_seq_forward_tc(a, stream) : launch_seq_forward_simt(a, dtype, stream);
+    return rc == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 int gdn_seq_backward(const void* q, int ldq, const void* k, int ldk, const void* v, int ldv, int dtype,

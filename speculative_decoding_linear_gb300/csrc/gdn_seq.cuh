@@ -90,7 +90,7 @@ struct SeqArgs {
 // Record (kept from the forward pass to the backward one) and workspace of the path that a
 // call's sizes and type take.
 struct SeqLayout {
-    size_t rec_S, rec_eps, rec_total;                    // record: chunk start states, errors
+    size_t rec_S, rec_eps, rec_op, rec_total;            // record: chunk start states, errors, chunk operands
     size_t ws_dS, ws_dV, ws_dq, ws_dk, ws_op, ws_total;  // workspace
 };
 

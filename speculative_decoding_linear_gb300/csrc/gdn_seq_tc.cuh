@@ -1,0 +1,172 @@
+// gdn_seq_tc.cuh -- operand layouts, splits and tcgen05 wrappers shared by the sequence
+// operators' tensor-core kernels.
+//
+// An fp32 operand x enters a product as bf16 terms x = hi + mid (+ low), each the rounding of
+// what the terms before it left; q, k, v and dO are bf16 already and exact.  Two terms leave at
+// most 2^-18 of x (6e-7 of it in the mean square), three 2^-27.  The terms of the B operand lie
+// side by side along N, so that the A operand is read once for all of them, and their products
+// are added in fp32 where the accumulator is read.  A product of two split operands leaves out
+// those of the small terms, 2^-18 of the whole and below.
+#pragma once
+
+#include "gdn_seq.cuh"
+#include "gdn_tc_ptx.cuh"
+
+namespace gdn {
+namespace seqtc {
+
+using namespace tc;
+
+// N consecutive TMEM columns of this warp's 32 lanes; the caller waits (tmem_wait_ld).
+__device__ __forceinline__ void tmem_ld_n(uint32_t t, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(t)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld_n(uint32_t t, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_n(uint32_t t, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(t)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+
+// Sum of T term columns (NT columns apart) of N consecutive columns.
+template <int N, int T>
+__device__ __forceinline__ void tmem_sum(uint32_t t, int apart, float (&x)[N]) {
+    uint32_t r[T][N];
+#pragma unroll
+    for (int i = 0; i < T; ++i) tmem_ld_n(t + i * apart, r[i]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        x[j] = __uint_as_float(r[T - 1][j]);        // the small terms first
+#pragma unroll
+        for (int i = T - 2; i >= 0; --i) x[j] += __uint_as_float(r[i][j]);
+    }
+}
+
+// Shared-memory operand stored as rows (of K) of W bytes with the hardware's W-byte swizzle.
+// Byte offset of 16-byte piece c of row r.
+template <int W>
+__device__ __forceinline__ uint32_t sw_piece(int r, int c) {
+    if constexpr (W == 128) return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
+    if constexpr (W == 64) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+    return (uint32_t)(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
+}
+template <int W>
+constexpr uint64_t kSwCode = W == 128 ? 2 : W == 64 ? 4 : 6;
+
+// Descriptor of an operand whose M or N index runs along the row (MN-major): pieces of W bytes
+// of it `mn_apart` bytes apart, eight rows of K together, the next eight 8 W bytes on.
+template <int W>
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr, uint32_t mn_apart) {
+    uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((mn_apart >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((8 * W) >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= kSwCode<W> << 61;
+    return d;
+}
+// Descriptor of an operand whose K index runs along the row (K-major), rows of W bytes.
+template <int W>
+__device__ __forceinline__ uint64_t k_desc(uint32_t saddr) {
+    uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)1 << 16;
+    d |= (uint64_t)((8 * W) >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= kSwCode<W> << 61;
+    return d;
+}
+constexpr uint32_t kAMn = 1u << 15, kBMn = 1u << 16;      // instruction descriptor: operand is MN-major
+
+__device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// Two values as T packed bf16 terms each; the values become what is left of them.
+template <int T>
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&p)[T]) {
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+        p[i] = pack_bf16(a, b);
+        a -= __uint_as_float(p[i] << 16);
+        b -= __uint_as_float(p[i] & 0xffff0000u);
+    }
+}
+
+// N values of row `row`, columns col0 .. col0 + N - 1, as T terms of a W-byte-row operand.
+template <int W, int T, int N>
+__device__ __forceinline__ void put_terms(uint32_t base, uint32_t term_apart, int row, int col0, const float (&x)[N]) {
+#pragma unroll
+    for (int c = 0; c < N / 8; ++c) {
+        uint32_t p[4][T];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split_pair<T>(x[8 * c + 2 * i], x[8 * c + 2 * i + 1], p[i]);
+        const uint32_t at = base + sw_piece<W>(row, col0 / 8 + c);
+#pragma unroll
+        for (int i = 0; i < T; ++i) st_shared16(at + i * term_apart, p[0][i], p[1][i], p[2][i], p[3][i]);
+    }
+}
+
+__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+}
+__device__ __forceinline__ void bulk_read_done() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+__device__ __forceinline__ void bulk_all_done() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
+
+// Bounded wait that gives up at once after any wait of the CTA has given up.
+__device__ __forceinline__ bool wait_or_dead(uint32_t bar, uint32_t parity, int* err, volatile int* dead) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns(), limit = wait_limit_ns(err);
+    while (true) {
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*dead) return false;
+        if (globaltimer_ns() - t0 > limit) {
+            set_error(err, GDN_ERR_TIMEOUT);
+            *dead = 1;
+            return false;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// per (slot, head): what a chunk needs of its gates and of K K^T, Q K^T
+//   image   [That; Phat], 128 rows of 64, bf16 hi then lo, 128-byte-swizzled K-major (32 KiB)
+//   gates   eg[64] = e^{g_t}, bt[64] = beta_t e^{g_end - g_t}, e^{g_end}   (fp32, 1 KiB)
+// ---------------------------------------------------------------------------
+constexpr uint32_t kOpImage = 2 * 128 * 128;
+constexpr uint32_t kOpBytes = kOpImage + 1024;
+
+}  // namespace seqtc
+
+struct SeqMaps;
+bool seq_tc_takes(const SeqShape& s, int dtype);
+int seq_tc_cols(const SeqShape& s);      // value columns of a CTA
+cudaError_t launch_seq_forward_tc(const SeqArgs& a, cudaStream_t st);
+
+}  // namespace gdn
