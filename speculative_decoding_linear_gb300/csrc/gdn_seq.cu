@@ -353,13 +353,16 @@ SeqLayout seq_layout(const SeqShape& s, int dtype) {
     // the tensor-core kernels keep rows of tokens for whole chunks
     const size_t rows = (tc ? slots * kChunk : (size_t)s.total) * s.H * s.dv * 4;
     const size_t heads = s.H > s.Hk ? (size_t)s.total * s.Hk * s.dk * 4 : 0;
-    const size_t ops = tc ? slots * s.H * seqtc::kOpBytes : 0;
+    const size_t tiles = slots * s.H * (s.dv / 16);        // of 16 value columns at least
     L.rec_S = 0;
     L.rec_eps = align_up(L.rec_S + state, kSectionAlign);
-    L.rec_op = align_up(L.rec_eps + rows, kSectionAlign);
-    L.rec_total = align_up(L.rec_op + ops, kSectionAlign);
+    L.rec_o = align_up(L.rec_eps + rows, kSectionAlign);
+    L.rec_op = align_up(L.rec_o + (tc ? rows : 0), kSectionAlign);
+    L.rec_total = align_up(L.rec_op + (tc ? slots * s.H * seqtc::kOpRecord : 0), kSectionAlign);
     L.ws_op = 0;
-    L.ws_dS = align_up(L.ws_op + ops, kSectionAlign);
+    L.ws_part = align_up(L.ws_op + (tc ? slots * s.H * seqtc::kOpBytes : 0), kSectionAlign);
+    L.ws_phi = align_up(L.ws_part + (tc ? tiles * 4 * kChunk * 4 : 0), kSectionAlign);
+    L.ws_dS = align_up(L.ws_phi + (tc ? tiles * 8 * 4 : 0), kSectionAlign);
     L.ws_dV = align_up(L.ws_dS + state, kSectionAlign);
     L.ws_dq = align_up(L.ws_dV + rows, kSectionAlign);
     L.ws_dk = align_up(L.ws_dq + heads, kSectionAlign);
@@ -473,7 +476,7 @@ int gdn_seq_forward(const void* q, int ldq, const void* k, int ldk, const void* 
     a.S_T = S_T;
     a.rec = static_cast<char*>(record);
     a.ws = static_cast<char*>(workspace);
-    const bool tc = total > 0 && record == nullptr && seq_tc_takes(s, dtype);
+    const bool tc = total > 0 && seq_tc_takes(s, dtype);
     const cudaError_t rc = tc ? launch_seq_forward_tc(a, stream) : launch_seq_forward_simt(a, dtype, stream);
     return rc == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -521,7 +524,9 @@ int gdn_seq_backward(const void* q, int ldq, const void* k, int ldk, const void*
     a.dbeta = dbeta;
     a.dS0 = dS0;
     a.ws = static_cast<char*>(workspace);
-    return launch_seq_backward_simt(a, dtype, stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    const bool tc = total > 0 && seq_tc_takes(s, dtype);
+    const cudaError_t rc = tc ? launch_seq_backward_tc(a, stream) : launch_seq_backward_simt(a, dtype, stream);
+    return rc == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -34,14 +34,15 @@ template <int DK>
 struct PrepGeom {
     static constexpr uint32_t kTile = 128 * 128;                 // [K; Q], 64 columns
     static constexpr uint32_t kKQ = (DK / 64) * kTile;
-    static constexpr uint32_t kMats = 3 * kChunk * kLd * 4;      // A, T, P in fp32 over the tiles
+    static constexpr uint32_t kMats = 4 * kChunk * kLd * 4;      // A, T, P, L in fp32 over the tiles
     static constexpr uint32_t kBuf = kKQ > kMats ? kKQ : ((kMats + 1023) & ~1023u);
     static constexpr uint32_t kSmem = kBuf + 2048 + 1024;
 };
 
 template <int DK>
 __global__ void __launch_bounds__(kPrepThreads)
-    seq_prep_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, SeqArgs a, char* ops) {
+    seq_prep_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, SeqArgs a, char* ops,
+                    uint32_t op_bytes) {
     using G = PrepGeom<DK>;
     extern __shared__ unsigned char raw[];
     const uint32_t r0 = smem_u32(raw), base = (r0 + 1023u) & ~1023u;
@@ -49,6 +50,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     float* A = reinterpret_cast<float*>(sm);
     float* T = A + kChunk * kLd;
     float* P = T + kChunk * kLd;
+    float* Lm = P + kChunk * kLd;
     float* ghi = reinterpret_cast<float*>(sm + G::kBuf);
     float* glo = ghi + kChunk;
     float* bt = glo + kChunk;
@@ -58,7 +60,7 @@ __global__ void __launch_bounds__(kPrepThreads)
 
     const SeqShape& sh = a.sh;
     const int h = blockIdx.x % sh.H, slot = blockIdx.x / sh.H, hk = h / (sh.H / sh.Hk);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
     int s, first, rows;
     if (!slot_chunk(sh, slot, s, first, rows, a.err)) {
         griddep_launch();
@@ -103,16 +105,20 @@ __global__ void __launch_bounds__(kPrepThreads)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *holder;
-    if (tid == 0) {
-        if (wait_or_dead(bar, 0, a.err, dead)) {
+    const uint32_t tmem = warp_uniform(*holder);
+    if (warp == 0) {
+        const bool here = wait_or_dead(bar, 0, a.err, dead);
+        __syncwarp();
+        if (elect_one()) {
+            const uint64_t d = k_desc<128>(base);
+            if (here)
 #pragma unroll
-            for (int k = 0; k < DK / 16; ++k) {
-                const uint32_t t = base + (k / 4) * G::kTile + 32 * (k % 4);
-                mma_bf16(tmem, k_desc<128>(t), k_desc<128>(t), idesc_bf16(128, 64), k != 0);
-            }
+                for (int k = 0; k < DK / 16; ++k) {
+                    const uint64_t t = d + (((k / 4) * G::kTile + 32 * (k % 4)) >> 4);
+                    mma_bf16(tmem, t, t, idesc_bf16(128, 64), k != 0);
+                }
+            mma_commit(bar2);
         }
-        mma_commit(bar2);
     }
     wait_or_dead(bar2, 0, a.err, dead);
     __syncwarp();
@@ -133,8 +139,9 @@ __global__ void __launch_bounds__(kPrepThreads)
             // outside the mask the exponent may be large: it is not evaluated there.  A token past the
             // sequence's end has beta 0 and is selected away, whatever lies in its q and k
             float x = 0.f;
-            if (c + strict <= t && t < rows) x = __uint_as_float(d[j]) * expf((gh - ghi[c]) + (gl - glo[c])) * bt[c];
-            row[j] = x;
+            if (c + strict <= t && t < rows) x = __uint_as_float(d[j]) * expf((gh - ghi[c]) + (gl - glo[c]));
+            row[j] = strict ? x * bt[c] : x;
+            if (strict) Lm[t * kLd + c] = x;
         }
     }
     tc_fence_before();
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(kPrepThreads)
         for (int k = c0; k < t0 + 4; ++k) {
             float u[4], w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) u[i] = P[(t0 + i) * kLd + k];
+            for (int i = 0; i < 4; ++i) u[i] = P[(t0 + i) * kLd + k] * bt[k];
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] = T[k * kLd + c0 + j];
 #pragma unroll
@@ -208,18 +215,18 @@ __global__ void __launch_bounds__(kPrepThreads)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) y[i][j] = fmaf(u[i], w[j], y[i][j]);
         }
-        __syncthreads();
+        // A's place is free: Phat there, P stays
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) P[(t0 + i) * kLd + c0 + j] = y[i][j];
+            for (int j = 0; j < 4; ++j) A[(t0 + i) * kLd + c0 + j] = y[i][j];
     }
     __syncthreads();
-    char* op = ops + (size_t)blockIdx.x * kOpBytes;
+    char* op = ops + (size_t)blockIdx.x * op_bytes;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = (tid >> 3) + 32 * i, c = tid & 7;
-        const float* x = (r < 64 ? T + r * kLd : P + (r - 64) * kLd) + 8 * c;
+        const float* x = (r < 64 ? T + r * kLd : A + (r - 64) * kLd) + 8 * c;
         uint32_t p[4][2];
 #pragma unroll
         for (int j = 0; j < 4; ++j) split_pair<2>(x[2 * j], x[2 * j + 1], p[j]);
@@ -227,12 +234,56 @@ __global__ void __launch_bounds__(kPrepThreads)
         *reinterpret_cast<uint4*>(at) = make_uint4(p[0][0], p[1][0], p[2][0], p[3][0]);
         *reinterpret_cast<uint4*>(at + 16384) = make_uint4(p[0][1], p[1][1], p[2][1], p[3][1]);
     }
-    float* gates = reinterpret_cast<float*>(op + kOpImage);
+    float* gates = reinterpret_cast<float*>(op + kOpTP);
     const float eh = ghi[rows - 1], el = glo[rows - 1];
     if (tid < 64) {
-        gates[tid] = expf(ghi[tid] + glo[tid]);
-        gates[64 + tid] = bt[tid] * expf((eh - ghi[tid]) + (el - glo[tid]));
-        if (tid == 0) gates[128] = expf(eh + el);
+        const float tail = expf((eh - ghi[tid]) + (el - glo[tid]));
+        gates[kGBt + tid] = bt[tid] * tail;
+        gates[kGEg + tid] = expf(ghi[tid] + glo[tid]);
+        gates[kGTail + tid] = tail;
+        gates[kGBeta + tid] = bt[tid];
+        if (tid < 4) gates[kGEnd + tid] = expf(eh + el);
+        gates[kGHi + tid] = ghi[tid];
+        gates[kGLo + tid] = glo[tid];
+    }
+    if (op_bytes == kOpRecord) {
+        // the backward pass's operands: T = (I + diag(beta) L)^-1 = I - diag(beta) That L and
+        // Ptil = P T = P - Phat L, four rows of each and four columns for each thread
+        const int t0 = 4 * (tid / 16), c0 = 4 * (tid % 16);
+        float y[2][4][4] = {};
+        for (int k = c0; k < t0 + 4; ++k) {
+            float u[2][4], w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u[0][i] = T[(t0 + i) * kLd + k];
+                u[1][i] = A[(t0 + i) * kLd + k];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = Lm[k * kLd + c0 + j];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[m][i][j] = fmaf(u[m][i], w[j], y[m][i][j]);
+        }
+        char* tpb = op + kOpBytes;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = t0 + i;
+                float x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[j] = m == 0 ? (t == c0 + j ? 1.f : 0.f) - bt[t] * y[0][i][j] : P[t * kLd + c0 + j] - y[1][i][j];
+                uint32_t p[2][2];
+                split_pair<2>(x[0], x[1], p[0]);
+                split_pair<2>(x[2], x[3], p[1]);
+                char* at = tpb + sw_piece<128>(64 * m + t, c0 / 8) + (c0 & 4) * 2;
+                *reinterpret_cast<uint2*>(at) = make_uint2(p[0][0], p[1][0]);
+                *reinterpret_cast<uint2*>(at + 16384) = make_uint2(p[0][1], p[1][1]);
+            }
     }
     griddep_launch();
     if (warp == 1) {
@@ -245,14 +296,19 @@ __global__ void __launch_bounds__(kPrepThreads)
 // ---------------------------------------------------------------------------
 // seq_fwd_kernel
 // ---------------------------------------------------------------------------
+// Ten warps.  Eight compute: a thread owns a row of the state, and a token's row of K (warps
+// 0, 1, 4, 5) or of Q in the token steps, columns halved between warps 0-3 and 4-7.  One starts the
+// copies of K, Q, V, the gates and [That; Phat], one issues the products.
 template <int DK, int NV>
 struct FwdGeom {
     static constexpr int kMH = DK > 128 ? 2 : 1;                  // halves of 128 rows of d_k
     static constexpr int kW = NV * 2;                             // bytes of an operand row
     static constexpr uint32_t kTile = 128 * 128;                  // [K; Q], 64 columns of d_k
-    static constexpr uint32_t kStage = 2 * kMH * kTile;           // d_k filled up to 128 or 256
+    static constexpr uint32_t kV = 2 * kMH * kTile;               // filled up to 128 or 256 columns, then V, gates
+    static constexpr uint32_t kG = kV + 64 * kW;
+    static constexpr uint32_t kStage = (kG + kGateFwd + 1023) & ~1023u;
     static constexpr uint32_t kTP = 2 * kStage;
-    static constexpr uint32_t kS = kTP + kOpImage;                // two terms
+    static constexpr uint32_t kS = kTP + kOpTP;                   // two terms
     static constexpr uint32_t kSTerm = DK * kW;
     static constexpr uint32_t kR = kS + 2 * kSTerm;               // three terms
     static constexpr uint32_t kRTerm = 64 * kW;
@@ -262,26 +318,28 @@ struct FwdGeom {
     static constexpr int kAlloc = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static_assert(kCols <= 512 && kSmem <= 227 * 1024, "tile");
 };
-constexpr int kFwdThreads = 288;          // eight warps that compute, one that copies
+constexpr int kFwdThreads = 320;
+constexpr int kSMs = 152;
 
 // More than one CTA per SM must not ask for more than the 512 columns of its TMEM.
 template <int DK, int NV>
 constexpr size_t fwd_smem() {
     using G = FwdGeom<DK, NV>;
-    const size_t least = G::kAlloc == 512 ? 116 * 1024 : G::kAlloc == 256 ? 78 * 1024 : 48 * 1024;
+    const size_t least = G::kAlloc == 512 ? 116 * 1024 : G::kAlloc == 256 ? 78 * 1024 : 58 * 1024;
     return G::kSmem > least ? G::kSmem : least;
 }
 
 template <int DK, int NV>
 __global__ void __launch_bounds__(kFwdThreads, 1)
-    seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, SeqArgs a, const char* ops,
-                   char* recS, char* recE) {
+    seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, SeqArgs a, const char* ops, uint32_t op_bytes, char* recS, char* recE, char* recO) {
     using G = FwdGeom<DK, NV>;
     constexpr int W = G::kW, NH = NV / 2;                 // NH: value columns of a thread in the token steps
     constexpr int SC = G::kMH == 2 ? NV : NH;             // value columns of a thread's state row
     extern __shared__ unsigned char raw[];
     const uint32_t r0 = smem_u32(raw), base = (r0 + 1023u) & ~1023u;
     unsigned char* sm = raw + (base - r0);
+    // copies landed (two stages; operands), their places free; products done; operands written
     const uint32_t full0 = base + G::kBar, empty0 = full0 + 16, tpf = full0 + 32, tpe = full0 + 40, b1 = full0 + 48,
                    b2 = full0 + 56, b3 = full0 + 64, drain = full0 + 72;
     uint32_t* holder = reinterpret_cast<uint32_t*>(sm + G::kBar + 128);
@@ -290,9 +348,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int tiles = sh.dv / NV;
     const int tile = blockIdx.x % tiles, h = (blockIdx.x / tiles) % sh.H, s = blockIdx.x / (tiles * sh.H);
     const int hk = h / (sh.H / sh.Hk), v0 = tile * NV;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
     int first, len;
     if (!seq_range(sh, s, first, len, a.err)) return;     // the whole CTA
+    first = warp_uniform(first);
+    len = warp_uniform(len);
     const int chunks = (len + kChunk - 1) / kChunk;
     const size_t slot0 = (size_t)(first / kChunk + s);
 
@@ -307,35 +367,107 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 st_shared16(base + st * G::kStage + (DK / 64) * G::kTile + o, 0, 0, 0, 0);
     }
     fence_proxy_async_smem();
-    if (warp == 8) tmem_alloc(smem_u32(holder), G::kAlloc);
+    if (warp == 9) tmem_alloc(smem_u32(holder), G::kAlloc);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *holder;
+    const uint32_t tmem = warp_uniform(*holder);
 
     if (warp == 8) {
         griddep_wait();
-        if (lane == 0) {
+        if (elect_one()) {
             int issued = 0, ops_issued = 0;
-            for (int c = 0; c < chunks; ++c) {
-                const int st = c & 1;
-                if (c >= 2 && !wait_or_dead(empty0 + 8 * st, ((c >> 1) & 1) ^ 1, a.err, dead)) break;
-                const uint32_t kq = base + st * G::kStage, f = full0 + 8 * st;
-                mbar_expect_tx(f, 2 * DK * 128);
+            // to L2 ahead of time: a copy that has to go to memory takes longer than a chunk
+            auto prefetch = [&](int c) {
 #pragma unroll
                 for (int b = 0; b < DK / 64; ++b) {
-                    tma_2d(kq + b * G::kTile, &tmK, hk * DK + 64 * b, first + c * kChunk, f);
-                    tma_2d(kq + b * G::kTile + 8192, &tmQ, hk * DK + 64 * b, first + c * kChunk, f);
+                    tma_prefetch_2d(&tmK, hk * DK + 64 * b, first + c * kChunk);
+                    tma_prefetch_2d(&tmQ, hk * DK + 64 * b, first + c * kChunk);
                 }
+                tma_prefetch_2d(&tmV, h * sh.dv + v0, first + c * kChunk);
+            };
+            for (int c = 0; c < chunks; ++c) {
+                if (c + 2 < chunks) prefetch(c + 2);
+                if (c >= 2 && !wait_or_dead(empty0 + 8 * (c & 1), ((c >> 1) & 1) ^ 1, a.err, dead)) break;
+                const uint32_t st = base + (c & 1) * G::kStage, f = full0 + 8 * (c & 1);
+                const char* op = ops + ((slot0 + c) * sh.H + h) * op_bytes;
+                mbar_expect_tx(f, 2 * DK * 128 + 64 * W + kGateFwd);
+#pragma unroll
+                for (int b = 0; b < DK / 64; ++b) {
+                    tma_2d(st + b * G::kTile, &tmK, hk * DK + 64 * b, first + c * kChunk, f);
+                    tma_2d(st + b * G::kTile + 8192, &tmQ, hk * DK + 64 * b, first + c * kChunk, f);
+                }
+                tma_2d(st + G::kV, &tmV, h * sh.dv + v0, first + c * kChunk, f);
+                bulk_copy_g2s(st + G::kG, op + kOpTP, kGateFwd, f);
                 issued = c + 1;
                 if (c >= 1 && !wait_or_dead(tpe, (c - 1) & 1, a.err, dead)) break;
-                mbar_expect_tx(tpf, kOpImage);
-                bulk_copy_g2s(base + G::kTP, ops + ((slot0 + c) * sh.H + h) * kOpBytes, kOpImage, tpf);
+                mbar_expect_tx(tpf, kOpTP);
+                bulk_copy_g2s(base + G::kTP, op, kOpTP, tpf);
                 ops_issued = c + 1;
             }
             if (*dead) {                                  // copies in flight land before the CTA ends
                 for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) mbar_wait(full0 + 8 * (c & 1), (c >> 1) & 1, a.err);
                 if (ops_issued > 0) mbar_wait(tpf, (ops_issued - 1) & 1, a.err);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // after a wait that gave up, products run on what is there: the result is void, the error recorded
+        const uint64_t dS = mn_desc<W>(base + G::kS, G::kSTerm), dR = mn_desc<W>(base + G::kR, G::kRTerm), dTP = k_desc<128>(base + G::kTP);
+        const bool leader = elect_one();
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t ph = c & 1, st = base + (c & 1) * G::kStage;
+            wait_or_dead(full0 + 8 * (c & 1), (c >> 1) & 1, a.err, dead);
+            __syncwarp();
+            named_sync(1, 288);
+            tc_fence_after();
+            if (leader) {
+                const uint64_t dKQ = k_desc<128>(st);
+#pragma unroll
+                for (int k = 0; k < DK / 16; ++k)
+                    mma_bf16(tmem + G::kD1, dKQ + (((k / 4) * G::kTile + 32 * (k % 4)) >> 4), dS + (k * 16 * W >> 4),
+                             idesc_bf16(128, 2 * NV) | kBMn, k != 0);
+                mma_commit(b1);
+                if (recS != nullptr)
+                    bulk_s2g(recS + (((slot0 + c) * sh.H + h) * tiles + tile) * (2 * G::kSTerm), base + G::kS, 2 * G::kSTerm);
+            }
+            __syncwarp();
+            wait_or_dead(tpf, ph, a.err, dead);
+            __syncwarp();
+            named_sync(2, 160);
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_bf16(tmem + G::kD2, dTP + 2 * k, dR + (k * 16 * W >> 4), idesc_bf16(128, 3 * NV) | kBMn, k != 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_bf16(tmem + G::kD2, dTP + 1024 + 2 * k, dR + (k * 16 * W >> 4), idesc_bf16(128, 2 * NV) | kBMn, 1);
+                mma_commit(b2);
+                mma_commit(tpe);
+                if (recS != nullptr) bulk_read_done();    // S's image may be written again once b3 is through
+            }
+            __syncwarp();
+            named_sync(3, 160);
+            tc_fence_after();
+            if (leader) {
+                const uint64_t dK = mn_desc<128>(st, G::kTile);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int m = 0; m < G::kMH; ++m)
+                        mma_bf16(tmem + G::kD3 + m * 3 * NV, dK + ((2 * m * G::kTile + k * 2048) >> 4), dR + (k * 16 * W >> 4),
+                                 idesc_bf16(128, 3 * NV) | kAMn | kBMn, k != 0);
+                mma_commit(b3);
+                mma_commit(empty0 + 8 * (c & 1));
+            }
+            __syncwarp();
+        }
+        if (leader) {
+            if (recS != nullptr) bulk_all_done();
+            if (*dead) {                                  // products in flight end before their TMEM is freed
+                mma_commit(drain);
+                mbar_wait(drain, 0, a.err);
             }
         }
         __syncwarp();
@@ -346,57 +478,37 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
         const int srow = (G::kMH == 2 ? 128 * wg : 0) + 32 * w4 + lane, scol = G::kMH == 2 ? 0 : wg * NH;
         const bool owns = srow < DK;
-        const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + (size_t)h * sh.dv + v0 + vc;
         float S[SC];
         {
             const size_t at = (((size_t)s * sh.H + h) * sh.dv + v0 + scol) * DK + srow;
 #pragma unroll
             for (int j = 0; j < SC; ++j) S[j] = owns && a.S0 != nullptr ? a.S0[at + (size_t)j * DK] : 0.f;
         }
-        uint4 vr[NH / 8];
-        auto load_v = [&](int c) {
-            const int t = c * kChunk + tok;
-#pragma unroll
-            for (int i = 0; i < NH / 8; ++i)
-                vr[i] = reads_k && t < len ? reinterpret_cast<const uint4*>(vp + ((size_t)first + t) * sh.ldv)[i] : make_uint4(0, 0, 0, 0);
-        };
-        float eg_n = 0.f, bt_n = 0.f, ee_n = 0.f;
-        auto load_gates = [&](int c) {
-            const float* g = reinterpret_cast<const float*>(ops + ((slot0 + c) * sh.H + h) * kOpBytes + kOpImage);
-            eg_n = g[tok];
-            bt_n = g[64 + tok];
-            ee_n = g[128];
-        };
-        load_v(0);
         griddep_wait();
-        if (chunks > 0) load_gates(0);
         for (int c = 0; c < chunks; ++c) {
-            const uint32_t ph = c & 1, kq = base + (c & 1) * G::kStage;
+            const uint32_t ph = c & 1, st = (c & 1) * G::kStage;
             const int rows = min(kChunk, len - c * kChunk);
-            const float eg = eg_n, bt = bt_n, ee = ee_n;
             // the state as the first product's operand: rows of d_k, value columns along the row
             if (owns) put_terms<W, 2>(base + G::kS, G::kSTerm, srow, scol, S);
             if (rows < kChunk) {
-                // the copies brought tokens of what lies behind: rows of zero instead
+                // the copy brought tokens of what lies behind: rows of zero instead
                 wait_or_dead(full0 + 8 * (c & 1), (c >> 1) & 1, a.err, dead);
                 for (int i = tid; i < (DK / 64) * 2 * (kChunk - rows) * 8; i += 256) {
                     const int p = i & 7, r = rows + (i >> 3) % (kChunk - rows), b = (i >> 3) / (kChunk - rows);
-                    st_shared16(kq + b * 8192 + r * 128 + p * 16, 0, 0, 0, 0);
+                    st_shared16(base + st + b * 8192 + r * 128 + p * 16, 0, 0, 0, 0);
                 }
             }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            named_sync(1, 256);
-            tc_fence_after();
-            if (tid == 0) {
-                if (wait_or_dead(full0 + 8 * (c & 1), (c >> 1) & 1, a.err, dead))
+            operand_ready(1, 288);
+            wait_or_dead(full0 + 8 * (c & 1), (c >> 1) & 1, a.err, dead);
+            const float* gates = reinterpret_cast<const float*>(sm + st + G::kG);
+            const float eg = gates[kGEg + tok], bt = gates[kGBt + tok], ee = gates[kGEnd];
+            uint4 vr[NH / 8];
+            if (reads_k) {
 #pragma unroll
-                    for (int k = 0; k < DK / 16; ++k)
-                        mma_bf16(tmem + G::kD1, k_desc<128>(kq + (k / 4) * G::kTile + 32 * (k % 4)),
-                                 mn_desc<W>(base + G::kS + k * 16 * W, G::kSTerm), idesc_bf16(128, 2 * NV) | kBMn, k != 0);
-                mma_commit(b1);
-                if (recS != nullptr)
-                    bulk_s2g(recS + (((slot0 + c) * sh.H + h) * tiles + tile) * (2 * G::kSTerm), base + G::kS, 2 * G::kSTerm);
+                for (int i = 0; i < NH / 8; ++i) {
+                    vr[i] = reinterpret_cast<const uint4*>(sm + st + G::kV + tok * W + vc * 2)[i];
+                    if (tok >= rows) vr[i] = make_uint4(0, 0, 0, 0);
+                }
             }
             wait_or_dead(b1, ph, a.err, dead);
             __syncwarp();
@@ -414,24 +526,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     }
                 }
                 put_terms<W, 3>(base + G::kR, G::kRTerm, tok, vc, x);
-                fence_proxy_async_smem();
-                tc_fence_before();
-                named_sync(2, 128);
-                tc_fence_after();
-                if (tid == 0) {
-                    if (wait_or_dead(tpf, ph, a.err, dead)) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16(tmem + G::kD2, k_desc<128>(base + G::kTP + 32 * k),
-                                     mn_desc<W>(base + G::kR + k * 16 * W, G::kRTerm), idesc_bf16(128, 3 * NV) | kBMn, k != 0);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16(tmem + G::kD2, k_desc<128>(base + G::kTP + 16384 + 32 * k),
-                                     mn_desc<W>(base + G::kR + k * 16 * W, G::kRTerm), idesc_bf16(128, 2 * NV) | kBMn, 1);
-                    }
-                    mma_commit(b2);
-                    mma_commit(tpe);
-                }
+                operand_ready(2, 160);
             }
             wait_or_dead(b2, ph, a.err, dead);
             __syncwarp();
@@ -442,24 +537,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                 for (int j = 0; j < NH; ++j) x[j] = bt * y[j];
                 put_terms<W, 3>(base + G::kR, G::kRTerm, tok, vc, x);
-                fence_proxy_async_smem();
-                tc_fence_before();
-                if (tid == 0 && recS != nullptr) bulk_read_done();   // S's image is read: it may be written again
-                named_sync(2, 128);
-                tc_fence_after();
-                if (tid == 0) {
-                    if (!*dead)
-#pragma unroll
-                        for (int m = 0; m < G::kMH; ++m)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_bf16(tmem + G::kD3 + m * 3 * NV, mn_desc<128>(kq + 2 * m * G::kTile + k * 2048, G::kTile),
-                                         mn_desc<W>(base + G::kR + k * 16 * W, G::kRTerm),
-                                         idesc_bf16(128, 3 * NV) | kAMn | kBMn, k != 0);
-                    mma_commit(b3);
-                    mma_commit(empty0 + 8 * (c & 1));
-                }
-                __syncwarp();
+                operand_ready(3, 160);
                 if (recE != nullptr) {                    // eps as two bf16 terms [2][64][dv]
                     char* e = recE + ((slot0 + c) * sh.H + h) * (size_t)(2 * kChunk * 2) * sh.dv + ((size_t)tok * sh.dv + v0 + vc) * 2;
 #pragma unroll
@@ -471,19 +549,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         *reinterpret_cast<uint4*>(e + (size_t)kChunk * 2 * sh.dv + 16 * i) = make_uint4(p[0][1], p[1][1], p[2][1], p[3][1]);
                     }
                 }
-                if (c + 1 < chunks) load_v(c + 1);
-            } else if (tok < rows) {
+            } else {
                 __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + (((size_t)first + c * kChunk + tok) * sh.H + h) * sh.dv + v0 + vc;
+                char* e = recO + ((slot0 + c) * sh.H + h) * (size_t)(2 * kChunk * 2) * sh.dv + ((size_t)tok * sh.dv + v0 + vc) * 2;
 #pragma unroll
                 for (int i = 0; i < NH / 8; ++i) {
-                    uint32_t p[4];
+                    uint32_t p[4][2];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        p[j] = pack_bf16(fmaf(eg, x[8 * i + 2 * j], y[8 * i + 2 * j]), fmaf(eg, x[8 * i + 2 * j + 1], y[8 * i + 2 * j + 1]));
-                    *reinterpret_cast<uint4*>(o + 8 * i) = make_uint4(p[0], p[1], p[2], p[3]);
+                        split_pair<2>(fmaf(eg, x[8 * i + 2 * j], y[8 * i + 2 * j]), fmaf(eg, x[8 * i + 2 * j + 1], y[8 * i + 2 * j + 1]), p[j]);
+                    const uint4 hi = make_uint4(p[0][0], p[1][0], p[2][0], p[3][0]);
+                    if (tok < rows) *reinterpret_cast<uint4*>(o + 8 * i) = hi;
+                    if (recO != nullptr) {                // the output as two terms, for the gates' gradient
+                        *reinterpret_cast<uint4*>(e + 16 * i) = hi;
+                        *reinterpret_cast<uint4*>(e + (size_t)kChunk * 2 * sh.dv + 16 * i) = make_uint4(p[0][1], p[1][1], p[2][1], p[3][1]);
+                    }
                 }
             }
-            if (c + 1 < chunks) load_gates(c + 1);
+            __syncwarp();
             wait_or_dead(b3, ph, a.err, dead);
             __syncwarp();
             tc_fence_after();
@@ -499,21 +582,701 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
             for (int j = 0; j < SC; ++j) a.S_T[at + (size_t)j * DK] = S[j];
         }
-        if (tid == 0) {
-            if (recS != nullptr) bulk_all_done();
+    }
+    griddep_launch();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, G::kAlloc);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// seq_bwd_kernel: the chunks of a sequence from its end
+// ---------------------------------------------------------------------------
+// With dS+ the gradient at a chunk's end (d_k x d_v, in registers like the state), x = tail (K dS+),
+//   w = T^T x + Ptil^T dO,  dV = beta w,  dS = e^{g_end} dS+ + Q^T (e^g dO) - K^T (e^g dV).
+// w is the gradient of beta eps: T takes That's place so that it comes without beta, which may be
+// zero.  Three dependent products again: K dS+ -> T^T x -> K^T (-e^g dV); Ptil^T dO and
+// Q^T (e^g dO) run behind the first.  dS+ goes to the workspace as the operand that it is in shared
+// memory, dV as two bf16 terms; seq_grad_kernel takes both.
+//
+// The gates' gradients are dots over d_v and come from here, where w and dS are fp32:
+//   dbeta_t = w_t.eps_t,   dlog_alpha_t = dlog_alpha_{t+1} + dO_t.o_t - dV_t.v_t,
+// the second since <S_t, dS_t> changes from token to token by just these; its value at a chunk's
+// first token is <S, dS>, S the chunk's start state.  Each CTA writes its columns' parts.
+template <int DK, int NV>
+struct BwdGeom {
+    static constexpr int kMH = DK > 128 ? 2 : 1;
+    static constexpr int kW = NV * 2;
+    static constexpr uint32_t kTile = 128 * 128;                  // [K; Q], 64 columns of d_k
+    static constexpr uint32_t kO = 2 * kMH * kTile;               // dO as an operand, then the gates
+    static constexpr uint32_t kG = kO + 64 * kW;
+    static constexpr uint32_t kBar = kG + 800;                    // of the first stage: barriers behind its gates
+    static constexpr uint32_t kStage = (kG + kGateBwd + 1023) & ~1023u;
+    static_assert(kG + 1024 <= kStage && kGateBwd <= 800, "gates and barriers share the end of a stage");
+    static constexpr uint32_t kTP = 2 * kStage;
+    static constexpr uint32_t kS = kTP + kOpTP;                   // two terms
+    static constexpr uint32_t kSTerm = DK * kW;
+    static constexpr uint32_t kR = kS + 2 * kSTerm;               // three terms of w, then of -e^g dV
+    static constexpr uint32_t kRTerm = 64 * kW;
+    static constexpr uint32_t kE = kR + 3 * kRTerm;               // three terms of e^g dO
+    static constexpr uint32_t kSmem = kE + 3 * kRTerm + 1024;
+    static constexpr int kD1 = 0, kD2 = 2 * NV, kDP = kD2 + 3 * NV, kD3 = kDP + NV, kCols = kD3 + kMH * 3 * NV;
+    static constexpr int kAlloc = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+    static_assert(kCols <= 512 && kSmem <= 227 * 1024, "tile");
+};
+
+template <int DK, int NV>
+constexpr size_t bwd_smem() {
+    using G = BwdGeom<DK, NV>;
+    const size_t least = G::kAlloc == 512 ? 116 * 1024 : G::kAlloc == 256 ? 78 * 1024 : 58 * 1024;
+    return G::kSmem > least ? G::kSmem : least;
+}
+
+template <int DK, int NV>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    seq_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmO, SeqArgs a, const char* ops, const char* recS, const char* recE, const char* recO,
+                   char* wsS, char* wsV, float* part, float* phi) {
+    using G = BwdGeom<DK, NV>;
+    constexpr int W = G::kW, NH = NV / 2;
+    constexpr int SC = G::kMH == 2 ? NV : NH;
+    extern __shared__ unsigned char raw[];
+    const uint32_t r0 = smem_u32(raw), base = (r0 + 1023u) & ~1023u;
+    unsigned char* sm = raw + (base - r0);
+    const uint32_t full0 = base + G::kBar, empty0 = full0 + 16, tpf = full0 + 32, tpe = full0 + 40, b1 = full0 + 48,
+                   b2 = full0 + 56, b3 = full0 + 64, drain = full0 + 72;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(sm + G::kBar + 128);
+    volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
+    const SeqShape& sh = a.sh;
+    const int tiles = sh.dv / NV;
+    const int tile = blockIdx.x % tiles, h = (blockIdx.x / tiles) % sh.H, s = blockIdx.x / (tiles * sh.H);
+    const int hk = h / (sh.H / sh.Hk), v0 = tile * NV;
+    const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
+    int first, len;
+    if (!seq_range(sh, s, first, len, a.err)) return;     // the whole CTA
+    first = warp_uniform(first);
+    len = warp_uniform(len);
+    const int chunks = (len + kChunk - 1) / kChunk;
+    const size_t slot0 = (size_t)(first / kChunk + s);
+
+    if (tid == 0) {
+        for (int i = 0; i < 10; ++i) mbar_init(full0 + 8 * i, 1);
+        *dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (DK % 128 != 0) {                                  // columns of d_k that no copy fills
+        for (int st = 0; st < 2; ++st)
+            for (uint32_t o = tid * 16; o < G::kTile; o += kFwdThreads * 16)
+                st_shared16(base + st * G::kStage + (DK / 64) * G::kTile + o, 0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    if (warp == 9) tmem_alloc(smem_u32(holder), G::kAlloc);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = warp_uniform(*holder);
+
+    // i counts the chunks as they are taken, c = chunks - 1 - i is the chunk
+    if (warp == 8) {
+        if (elect_one()) {
+            int issued = 0, ops_issued = 0;
+            for (int i = 0; i < chunks; ++i) {
+                const int c = chunks - 1 - i;
+                if (i >= 2 && !wait_or_dead(empty0 + 8 * (i & 1), ((i >> 1) & 1) ^ 1, a.err, dead)) break;
+                const uint32_t st = base + (i & 1) * G::kStage, f = full0 + 8 * (i & 1);
+                const char* op = ops + ((slot0 + c) * sh.H + h) * kOpRecord;
+                mbar_expect_tx(f, 2 * DK * 128 + 64 * W + kGateBwd);
+#pragma unroll
+                for (int b = 0; b < DK / 64; ++b) {
+                    tma_2d(st + b * G::kTile, &tmK, hk * DK + 64 * b, first + c * kChunk, f);
+                    tma_2d(st + b * G::kTile + 8192, &tmQ, hk * DK + 64 * b, first + c * kChunk, f);
+                }
+                tma_2d(st + G::kO, &tmO, h * sh.dv + v0, first + c * kChunk, f);
+                bulk_copy_g2s(st + G::kG, op + kOpTP + 4 * kGEg, kGateBwd, f);
+                bulk_prefetch_l2(recS + (((slot0 + c) * sh.H + h) * tiles + tile) * (2 * G::kSTerm), 2 * G::kSTerm);
+                issued = i + 1;
+                if (i >= 1 && !wait_or_dead(tpe, (i - 1) & 1, a.err, dead)) break;
+                mbar_expect_tx(tpf, kOpTP);
+                bulk_copy_g2s(base + G::kTP, op + kOpBytes, kOpTP, tpf);
+                ops_issued = i + 1;
+            }
+            if (*dead) {                                  // copies in flight land before the CTA ends
+                for (int i = issued > 2 ? issued - 2 : 0; i < issued; ++i) mbar_wait(full0 + 8 * (i & 1), (i >> 1) & 1, a.err);
+                if (ops_issued > 0) mbar_wait(tpf, (ops_issued - 1) & 1, a.err);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        const uint64_t dS = mn_desc<W>(base + G::kS, G::kSTerm), dR = mn_desc<W>(base + G::kR, G::kRTerm),
+                       dE = mn_desc<W>(base + G::kE, G::kRTerm);
+        // [T; Ptil]^T: the index of M runs along the 64 columns of a row, and its second 64 are the
+        // first again, so that lanes 64 .. 127 of the result repeat lanes 0 .. 63
+        const uint64_t dTP = mn_desc<128>(base + G::kTP, 0);
+        const bool leader = elect_one();
+        for (int i = 0; i < chunks; ++i) {
+            const uint32_t ph = i & 1, st = base + (i & 1) * G::kStage;
+            wait_or_dead(full0 + 8 * (i & 1), (i >> 1) & 1, a.err, dead);
+            wait_or_dead(tpf, ph, a.err, dead);
+            __syncwarp();
+            named_sync(1, 288);
+            tc_fence_after();
+            const uint64_t dK = mn_desc<128>(st, G::kTile);
+            if (leader) {
+                const uint64_t dKQ = k_desc<128>(st), dO = mn_desc<W>(st + G::kO, 0);
+#pragma unroll
+                for (int k = 0; k < DK / 16; ++k)
+                    mma_bf16(tmem + G::kD1, dKQ + (((k / 4) * G::kTile + 32 * (k % 4)) >> 4), dS + (k * 16 * W >> 4),
+                             idesc_bf16(128, 2 * NV) | kBMn, k != 0);
+                mma_commit(b1);
+                bulk_s2g(wsS + (((slot0 + chunks - 1 - i) * sh.H + h) * tiles + tile) * (2 * G::kSTerm), base + G::kS, 2 * G::kSTerm);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_bf16(tmem + G::kDP, dTP + (k / 4) * 1024 + (8192 + (k % 4) * 2048 >> 4), dO + ((k % 4) * 16 * W >> 4),
+                             idesc_bf16(128, NV) | kAMn | kBMn, k != 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int m = 0; m < G::kMH; ++m)
+                        mma_bf16(tmem + G::kD3 + m * 3 * NV, dK + ((2 * m * G::kTile + 8192 + k * 2048) >> 4), dE + (k * 16 * W >> 4),
+                                 idesc_bf16(128, 3 * NV) | kAMn | kBMn, k != 0);
+            }
+            __syncwarp();
+            named_sync(2, 160);
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_bf16(tmem + G::kD2, dTP + (k * 2048 >> 4), dR + (k * 16 * W >> 4), idesc_bf16(128, 3 * NV) | kAMn | kBMn, k != 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_bf16(tmem + G::kD2, dTP + 1024 + (k * 2048 >> 4), dR + (k * 16 * W >> 4),
+                             idesc_bf16(128, 2 * NV) | kAMn | kBMn, 1);
+                mma_commit(b2);
+                mma_commit(tpe);
+                bulk_read_done();                         // dS's image may be written again once b3 is through
+            }
+            __syncwarp();
+            named_sync(3, 160);
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int m = 0; m < G::kMH; ++m)
+                        mma_bf16(tmem + G::kD3 + m * 3 * NV, dK + ((2 * m * G::kTile + k * 2048) >> 4), dR + (k * 16 * W >> 4),
+                                 idesc_bf16(128, 3 * NV) | kAMn | kBMn, 1);
+                mma_commit(b3);
+                mma_commit(empty0 + 8 * (i & 1));
+            }
+            __syncwarp();
+        }
+        if (leader) {
+            bulk_all_done();
             if (*dead) {                                  // products in flight end before their TMEM is freed
                 mma_commit(drain);
                 mbar_wait(drain, 0, a.err);
             }
         }
+        __syncwarp();
+    } else {
+        const int wg = warp >> 2, w4 = warp & 3;
+        const bool reads_k = w4 < 2;                      // x and -e^g dV of a token, else e^g dO, outputs and dots
+        const int tok = 32 * (w4 & 1) + lane, vc = wg * NH;
+        const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+        const int srow = (G::kMH == 2 ? 128 * wg : 0) + 32 * w4 + lane, scol = G::kMH == 2 ? 0 : wg * NH;
+        const bool owns = srow < DK;
+        float S[SC];
+        {
+            const size_t at = (((size_t)s * sh.H + h) * sh.dv + v0 + scol) * DK + srow;
+#pragma unroll
+            for (int j = 0; j < SC; ++j) S[j] = owns && a.dS_T != nullptr ? a.dS_T[at + (size_t)j * DK] : 0.f;
+        }
+        // this CTA's part of <S, dS> at the start of chunk c; S's image is swizzled as in shared memory
+        auto state_dot = [&](int c) {
+            const char* p = recS + (((slot0 + c) * sh.H + h) * tiles + tile) * (2 * G::kSTerm);
+            float d = 0.f;
+            if (owns)
+#pragma unroll
+                for (int j = 0; j < SC / 8; ++j) {
+                    const char* q = p + sw_piece<W>(srow, scol / 8 + j);
+                    const uint4 u = *reinterpret_cast<const uint4*>(q), l = *reinterpret_cast<const uint4*>(q + G::kSTerm);
+                    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ll[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        d = fmaf(__uint_as_float(uu[e] << 16) + __uint_as_float(ll[e] << 16), S[8 * j + 2 * e], d);
+                        d = fmaf(__uint_as_float(uu[e] & 0xffff0000u) + __uint_as_float(ll[e] & 0xffff0000u), S[8 * j + 2 * e + 1], d);
+                    }
+                }
+            d = warp_sum(d);
+            if (lane == 0) phi[(((slot0 + c) * sh.H + h) * tiles + tile) * 8 + warp] = d;
+        };
+        for (int i = 0; i < chunks; ++i) {
+            const int c = chunks - 1 - i;
+            const uint32_t ph = i & 1, st = (i & 1) * G::kStage;
+            const int rows = min(kChunk, len - c * kChunk);
+            if (owns) put_terms<W, 2>(base + G::kS, G::kSTerm, srow, scol, S);
+            wait_or_dead(full0 + 8 * (i & 1), (i >> 1) & 1, a.err, dead);
+            __syncwarp();
+            if (rows < kChunk) {
+                // the copies brought tokens of what lies behind: rows of zero instead
+                for (int j = tid; j < (DK / 64) * 2 * (kChunk - rows) * 8; j += 256) {
+                    const int p = j & 7, r = rows + (j >> 3) % (kChunk - rows), b = (j >> 3) / (kChunk - rows);
+                    st_shared16(base + st + b * 8192 + r * 128 + p * 16, 0, 0, 0, 0);
+                }
+            }
+            const float* gates = reinterpret_cast<const float*>(sm + st + G::kG);
+            const float eg = gates[tok], tail = gates[kGTail - kGEg + tok], beta = gates[kGBeta - kGEg + tok], ee = gates[kGEnd - kGEg];
+            float x[NH];
+            if (!reads_k) {
+#pragma unroll
+                for (int p = 0; p < NH / 8; ++p) {
+                    uint4* at = reinterpret_cast<uint4*>(sm + st + G::kO + sw_piece<W>(tok, vc / 8 + p));
+                    uint4 u = *at;
+                    if (tok >= rows) *at = u = make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[8 * p + 2 * j] = eg * __uint_as_float(w[j] << 16);
+                        x[8 * p + 2 * j + 1] = eg * __uint_as_float(w[j] & 0xffff0000u);
+                    }
+                }
+                put_terms<W, 3>(base + G::kE, G::kRTerm, tok, vc, x);
+            }
+            operand_ready(1, 288);
+            if (i > 0) state_dot(c + 1);
+            // eps and o as two terms each, v and dO of this thread's token and columns
+            uint4 te[2][NH / 8], to[2][NH / 8], tv[NH / 8], td[NH / 8];
+            if (!reads_k) {
+                const size_t at = ((slot0 + c) * sh.H + h) * (size_t)(2 * kChunk * 2) * sh.dv + ((size_t)tok * sh.dv + v0 + vc) * 2;
+                const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + ((size_t)first + c * kChunk + tok) * sh.ldv + (size_t)h * sh.dv + v0 + vc;
+#pragma unroll
+                for (int p = 0; p < NH / 8; ++p) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        te[t][p] = *reinterpret_cast<const uint4*>(recE + at + (size_t)t * kChunk * 2 * sh.dv + 16 * p);
+                        to[t][p] = *reinterpret_cast<const uint4*>(recO + at + (size_t)t * kChunk * 2 * sh.dv + 16 * p);
+                    }
+                    tv[p] = make_uint4(0, 0, 0, 0);
+                    if (tok < rows) tv[p] = *reinterpret_cast<const uint4*>(vp + 8 * p);
+                    td[p] = *reinterpret_cast<const uint4*>(sm + st + G::kO + sw_piece<W>(tok, vc / 8 + p));
+                }
+            }
+            wait_or_dead(b1, ph, a.err, dead);
+            __syncwarp();
+            tc_fence_after();
+            if (reads_k) {
+                tmem_sum<NH, 2>(tmem + G::kD1 + lanes + vc, NV, x);
+#pragma unroll
+                for (int j = 0; j < NH; ++j) x[j] *= tail;
+                put_terms<W, 3>(base + G::kR, G::kRTerm, tok, vc, x);
+                operand_ready(2, 160);
+            }
+            wait_or_dead(b2, ph, a.err, dead);
+            __syncwarp();
+            tc_fence_after();
+            {
+                // T^T x (three terms) and, in the columns behind, Ptil^T dO
+                uint32_t u[4][NH];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) tmem_ld_n(tmem + G::kD2 + lanes + vc + t * NV, u[t]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < NH; ++j)
+                    x[j] = ((__uint_as_float(u[2][j]) + __uint_as_float(u[1][j])) + __uint_as_float(u[3][j])) + __uint_as_float(u[0][j]);
+            }
+            if (reads_k) {
+#pragma unroll
+                for (int j = 0; j < NH; ++j) x[j] *= -eg * beta;
+                put_terms<W, 3>(base + G::kR, G::kRTerm, tok, vc, x);
+                operand_ready(3, 160);
+            } else {
+                char* e = wsV + ((slot0 + c) * sh.H + h) * (size_t)(2 * kChunk * 2) * sh.dv + ((size_t)tok * sh.dv + v0 + vc) * 2;
+                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.dv) + (((size_t)first + c * kChunk + tok) * sh.H + h) * sh.dv + v0 + vc;
+                float db = 0.f, dl = 0.f;
+#pragma unroll
+                for (int p = 0; p < NH / 8; ++p) {
+                    const uint32_t *e0 = &te[0][p].x, *e1 = &te[1][p].x, *o0 = &to[0][p].x, *o1 = &to[1][p].x, *v4 = &tv[p].x, *d4 = &td[p].x;
+                    uint32_t u[4][2];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            auto half = [&](uint32_t w) { return __uint_as_float(z ? w & 0xffff0000u : w << 16); };
+                            float& w = x[8 * p + 2 * j + z];
+                            db = fmaf(w, half(e0[j]) + half(e1[j]), db);
+                            w *= beta;
+                            dl = fmaf(half(d4[j]), half(o0[j]) + half(o1[j]), fmaf(-w, half(v4[j]), dl));
+                        }
+                        split_pair<2>(x[8 * p + 2 * j], x[8 * p + 2 * j + 1], u[j]);
+                    }
+                    const uint4 hi = make_uint4(u[0][0], u[1][0], u[2][0], u[3][0]);
+                    *reinterpret_cast<uint4*>(e + 16 * p) = hi;
+                    *reinterpret_cast<uint4*>(e + (size_t)kChunk * 2 * sh.dv + 16 * p) = make_uint4(u[0][1], u[1][1], u[2][1], u[3][1]);
+                    if (tok < rows) *reinterpret_cast<uint4*>(o + 8 * p) = hi;
+                }
+                float* q = part + ((((slot0 + c) * sh.H + h) * tiles + tile) * 2 + wg) * (2 * kChunk) + tok;
+                q[0] = db;
+                q[kChunk] = dl;
+            }
+            __syncwarp();
+            wait_or_dead(b3, ph, a.err, dead);
+            __syncwarp();
+            tc_fence_after();
+            {
+                float d[SC];
+                tmem_sum<SC, 3>(tmem + G::kD3 + (G::kMH == 2 ? wg * 3 * NV : 0) + lanes + scol, NV, d);
+#pragma unroll
+                for (int j = 0; j < SC; ++j) S[j] = fmaf(ee, S[j], d[j]);
+            }
+        }
+        if (chunks > 0) state_dot(0);
+        if (a.dS0 != nullptr && owns) {
+            const size_t at = (((size_t)s * sh.H + h) * sh.dv + v0 + scol) * DK + srow;
+#pragma unroll
+            for (int j = 0; j < SC; ++j) a.dS0[at + (size_t)j * DK] = S[j];
+        }
     }
     griddep_launch();
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
-        __syncwarp();
+    if (warp == 9) {
         tc_fence_after();
         tmem_dealloc(tmem, G::kAlloc);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// seq_grad_kernel: dq and dk of one (chunk, head) after another
+// ---------------------------------------------------------------------------
+// With S the chunk's start state and dS+ the gradient at its end (d_k x d_v), both as the scans
+// left them, E = dO eps^T, F = dV eps^T, MP = lower G E beta, ME = strictly lower G F beta:
+//   dq      = e^g dO S^T + MP K                     lanes 0..63 of one accumulator, rows dO and MP,
+//   k_read  = -e^g dV S^T - ME K                    lanes 64..127, rows dV and -ME
+//   k_write = bt eps dS+^T + MP^T Q - ME^T K        of another (in both halves)
+// and dk their sum.  The rows' factors e^g and bt are applied in place between the products over
+// d_v and those over the chunk's tokens: the operands stay what the scans stored, dO exact.
+// The gates' gradients are added up here from the parts that the backward scan left.
+//
+// Bound by its reads: 4 bytes for each element of S and dS+ of every chunk.  One CTA per SM goes
+// through the chunks; a ring of two slots takes NV columns of d_v at a time.
+template <int DK, int NV>
+struct GradGeom {
+    static constexpr int kW = NV * 2;
+    static constexpr uint32_t kTile = 128 * 128;                  // [Q; K], 64 columns of d_k
+    static constexpr uint32_t kBlk = 64 * kW;                     // 64 rows of an operand over d_v
+    static constexpr uint32_t kM = (DK / 64) * kTile;             // [MP; -ME], two terms
+    static constexpr uint32_t kSlot0 = kM + 2 * 16384;
+    // blocks of a slot: dO, dV hi, zero, dV lo, -, or eps hi twice, zero, eps lo twice; then S or dS+, or eps hi, lo
+    static constexpr uint32_t kImg = 5 * kBlk;
+    static constexpr uint32_t kSlot = kImg + 2 * DK * kW;
+    static constexpr uint32_t kGates = kSlot0 + 2 * kSlot;
+    static constexpr uint32_t kMisc = kGates + kOpGates;          // 64 floats
+    static constexpr uint32_t kBar = kMisc + 256;
+    static constexpr uint32_t kUsed = kBar + 256 + 1024;
+    static constexpr uint32_t kSmem = kUsed > 116 * 1024 ? kUsed : 116 * 1024;      // one CTA per SM: it takes the whole TMEM
+    static constexpr int kDa = 0, kDw = DK, kE = 2 * DK <= 256 ? 256 : 0;
+    static_assert(kSmem <= 227 * 1024 && kSlot % 1024 == 0, "slots");
+};
+
+template <int DK, int NV>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    seq_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmE,
+                    const __grid_constant__ CUtensorMap tmV, SeqArgs a, const char* ops, const char* recS, const char* wsS,
+                    const float* part, const float* phi, float* dqf, float* dkf) {
+    using G = GradGeom<DK, NV>;
+    constexpr int W = G::kW, HC = DK / 2;                 // HC: columns of d_k of a thread
+    extern __shared__ unsigned char raw[];
+    const uint32_t r0 = smem_u32(raw), base = (r0 + 1023u) & ~1023u;
+    unsigned char* sm = raw + (base - r0);
+    const uint32_t kqf = base + G::kBar, kqe = kqf + 8, full0 = kqf + 16, empty0 = kqf + 32, ef = kqf + 48, p2 = kqf + 56,
+                   fin = kqf + 64, drain = kqf + 72;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(sm + G::kBar + 128);
+    volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
+    const SeqShape& sh = a.sh;
+    const int tiles = sh.dv / NV, rep = sh.H / sh.Hk;
+    const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
+    const int items = seq_slots(sh.nseq, sh.total) * sh.Hk;
+
+    if (tid == 0) {
+        for (int i = 0; i < 10; ++i) mbar_init(kqf + 8 * i, 1);
+        mbar_init(kqe, 8);
+        *dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    for (int sl = 0; sl < 2; ++sl)
+        for (uint32_t o = tid * 16; o < G::kBlk; o += kFwdThreads * 16)
+            st_shared16(base + G::kSlot0 + sl * G::kSlot + 2 * G::kBlk + o, 0, 0, 0, 0);
+    fence_proxy_async_smem();
+    if (warp == 9) tmem_alloc(smem_u32(holder), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = warp_uniform(*holder);
+    griddep_wait();
+
+    if (warp == 8) {
+        if (elect_one()) {
+            int n = 0, it = 0;
+            bool ok = true;
+            for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+                int s, first, rows;
+                if (!slot_chunk(sh, item / sh.Hk, s, first, rows, a.err)) continue;
+                const int hk = item % sh.Hk;
+                for (int r = 0; r < rep && ok; ++r, ++n) {
+                    const int h = hk * rep + r;
+                    const size_t sh_at = (size_t)(item / sh.Hk) * sh.H + h;
+                    const int erow = (int)(sh_at * 2 * kChunk);
+                    if (n >= 1 && !(ok = wait_or_dead(kqe, (n - 1) & 1, a.err, dead))) break;
+                    mbar_expect_tx(kqf, 2 * DK * 128 + kOpGates);
+#pragma unroll
+                    for (int b = 0; b < DK / 64; ++b) {
+                        tma_2d(base + b * G::kTile, &tmQ, hk * DK + 64 * b, first, kqf);
+                        tma_2d(base + b * G::kTile + 8192, &tmK, hk * DK + 64 * b, first, kqf);
+                    }
+                    bulk_copy_g2s(base + G::kGates, ops + sh_at * kOpRecord + kOpTP, kOpGates, kqf);
+                    for (int j = 0; j < 3 * tiles; ++j, ++it) {
+                        const uint32_t sl = base + G::kSlot0 + (it & 1) * G::kSlot, f = full0 + 8 * (it & 1);
+                        if (it >= 2 && !(ok = wait_or_dead(empty0 + 8 * (it & 1), ((it >> 1) & 1) ^ 1, a.err, dead))) break;
+                        const int v = (j < tiles ? j : (j - tiles) >> 1), v0 = v * NV;
+                        if (j < tiles || ((j - tiles) & 1) == 0) {
+                            mbar_expect_tx(f, 3 * G::kBlk + (j < tiles ? 2 * G::kBlk : 2 * DK * W));
+                            tma_2d(sl, &tmO, h * sh.dv + v0, first, f);
+                            tma_2d(sl + G::kBlk, &tmV, v0, erow, f);
+                            tma_2d(sl + 3 * G::kBlk, &tmV, v0, erow + kChunk, f);
+                            if (j < tiles) {
+                                tma_2d(sl + G::kImg, &tmE, v0, erow, f);
+                                tma_2d(sl + G::kImg + G::kBlk, &tmE, v0, erow + kChunk, f);
+                            } else {
+                                bulk_copy_g2s(sl + G::kImg, recS + (sh_at * tiles + v) * (2 * DK * W), 2 * DK * W, f);
+                            }
+                        } else {
+                            mbar_expect_tx(f, 4 * G::kBlk + 2 * DK * W);
+                            tma_2d(sl, &tmE, v0, erow, f);
+                            tma_2d(sl + G::kBlk, &tmE, v0, erow, f);
+                            tma_2d(sl + 3 * G::kBlk, &tmE, v0, erow + kChunk, f);
+                            tma_2d(sl + 4 * G::kBlk, &tmE, v0, erow + kChunk, f);
+                            bulk_copy_g2s(sl + G::kImg, wsS + (sh_at * tiles + v) * (2 * DK * W), 2 * DK * W, f);
+                        }
+                    }
+                }
+            }
+            if (*dead) {                                  // copies in flight land before the CTA ends
+                mbar_wait(kqf, n & 1, a.err);
+                for (int j = it > 2 ? it - 2 : 0; j < it; ++j) mbar_wait(full0 + 8 * (j & 1), (j >> 1) & 1, a.err);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        const bool leader = elect_one();
+        const uint64_t dM = k_desc<128>(base + G::kM), dMt = mn_desc<128>(base + G::kM, 0),
+                       dQKt = mn_desc<128>(base, G::kTile);
+        int n = 0, it = 0;
+        for (int item = blockIdx.x; item < items; item += gridDim.x) {
+            int s, first, rows;
+            if (!slot_chunk(sh, item / sh.Hk, s, first, rows, a.err)) continue;
+            for (int r = 0; r < rep; ++r, ++n) {
+                wait_or_dead(kqf, n & 1, a.err, dead);
+                __syncwarp();
+                for (int j = 0; j < tiles; ++j, ++it) {
+                    const uint32_t sl = base + G::kSlot0 + (it & 1) * G::kSlot;
+                    wait_or_dead(full0 + 8 * (it & 1), (it >> 1) & 1, a.err, dead);
+                    __syncwarp();
+                    if (leader) {
+                        const uint64_t dA = k_desc<W>(sl), dB = k_desc<W>(sl + G::kImg);
+#pragma unroll
+                        for (int k = 0; k < NV / 16; ++k) {
+                            mma_bf16(tmem + G::kE, dA + 2 * k, dB + 2 * k, idesc_bf16(128, 128), j + k != 0);
+                            mma_bf16(tmem + G::kE, dA + (2 * G::kBlk >> 4) + 2 * k, dB + 2 * k, idesc_bf16(128, 64), 1);
+                        }
+                        mma_commit(empty0 + 8 * (it & 1));
+                    }
+                    __syncwarp();
+                }
+                if (leader) mma_commit(ef);
+                __syncwarp();
+                named_sync(1, 288);                       // E and F are read
+                tc_fence_after();
+                for (int j = 0; j < 2 * tiles; ++j, ++it) {
+                    const uint32_t sl = base + G::kSlot0 + (it & 1) * G::kSlot, d = tmem + (j & 1 ? G::kDw : G::kDa);
+                    wait_or_dead(full0 + 8 * (it & 1), (it >> 1) & 1, a.err, dead);
+                    __syncwarp();
+                    if (leader) {
+                        const uint64_t dA = k_desc<W>(sl), dB = k_desc<W>(sl + G::kImg),
+                                       dA2 = dA + ((j & 1 ? 3 : 2) * G::kBlk >> 4);
+#pragma unroll
+                        for (int k = 0; k < NV / 16; ++k) {
+                            mma_bf16(d, dA + 2 * k, dB + 2 * k, idesc_bf16(128, DK), (j >> 1) + k != 0);
+                            mma_bf16(d, dA + 2 * k, dB + (DK * W >> 4) + 2 * k, idesc_bf16(128, DK), 1);
+                            mma_bf16(d, dA2 + 2 * k, dB + 2 * k, idesc_bf16(128, DK), 1);
+                        }
+                        mma_commit(empty0 + 8 * (it & 1));
+                    }
+                    __syncwarp();
+                }
+                if (leader) mma_commit(p2);
+                __syncwarp();
+                named_sync(2, 288);                       // rows scaled, [MP; -ME] written
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)           // [MP; -ME] K
+                        mma_bf16(tmem + G::kDa, dM + (k / 4) * 1024 + 2 * (k % 4), dQKt + (8192 + (k % 4) * 2048 >> 4),
+                                 idesc_bf16(128, DK) | kBMn, 1);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)          // [MP; -ME]^T [Q; K]
+                        mma_bf16(tmem + G::kDw, dMt + (k / 8) * 1024 + ((k % 8) * 2048 >> 4), dQKt + ((k % 8) * 2048 >> 4),
+                                 idesc_bf16(128, DK) | kAMn | kBMn, 1);
+                    mma_commit(fin);
+                }
+                __syncwarp();
+                named_sync(3, 288);                       // results read
+                tc_fence_after();
+            }
+        }
+        if (leader && *dead) {                            // products in flight end before their TMEM is freed
+            mma_commit(drain);
+            mbar_wait(drain, 0, a.err);
+        }
+        __syncwarp();
+    } else {
+        const int wg = warp >> 2, w4 = warp & 3, L = 32 * w4 + lane, t = L & 63;
+        const bool is_k = w4 >= 2;                        // this thread's row: of dV, ME, dk, else of dO, MP, dq
+        const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+        const float* gates = reinterpret_cast<const float*>(sm + G::kGates);
+        float* ys = reinterpret_cast<float*>(sm + G::kMisc);
+        int n = 0;
+        for (int item = blockIdx.x; item < items; item += gridDim.x) {
+            int s, first, rows;
+            if (!slot_chunk(sh, item / sh.Hk, s, first, rows, a.err)) continue;
+            const int hk = item % sh.Hk;
+            for (int r = 0; r < rep; ++r, ++n) {
+                const int h = hk * rep + r;
+                const size_t sh_at = (size_t)(item / sh.Hk) * sh.H + h;
+                double dla = 0.0;
+                if (tid < kChunk) {
+                    // dbeta, and the terms of dlog_alpha
+                    const float* q = part + sh_at * tiles * (4 * kChunk) + tid;
+                    float db = 0.f, dl = 0.f;
+                    for (int j = 0; j < 2 * tiles; ++j) {
+                        db += q[j * 2 * kChunk];
+                        dl += q[j * 2 * kChunk + kChunk];
+                    }
+                    ys[tid] = dl;
+                    if (tid < rows) a.dbeta[((size_t)first + tid) * sh.H + h] = db;
+                    for (int j = 0; j < 8 * tiles; ++j) dla += (double)phi[sh_at * tiles * 8 + j];
+                }
+                named_sync(4, 256);
+                if (tid < rows) {
+                    for (int i = 0; i < tid; ++i) dla -= (double)ys[i];
+                    a.dla[((size_t)first + tid) * sh.H + h] = (float)dla;
+                }
+                wait_or_dead(kqf, n & 1, a.err, dead);
+                wait_or_dead(ef, n & 1, a.err, dead);
+                __syncwarp();
+                tc_fence_after();
+                const float eg = gates[kGEg + t], bt = gates[kGBt + t];
+                {
+                    uint32_t e0[32], e1[32];
+                    tmem_ld_n(tmem + G::kE + lanes + 32 * wg, e0);
+                    tmem_ld_n(tmem + G::kE + lanes + 64 + 32 * wg, e1);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    asm volatile("bar.arrive 1, 288;\n" ::: "memory");
+                    const float gh = gates[kGHi + t], gl = gates[kGLo + t];
+                    float m[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int c = 32 * wg + j;
+                        m[j] = 0.f;
+                        if (t < rows && (is_k ? c < t : c <= t)) {
+                            const float e = __uint_as_float(e0[j]) + __uint_as_float(e1[j]);
+                            m[j] = (is_k ? -e : e) * expf((gh - gates[kGHi + c]) + (gl - gates[kGLo + c])) * gates[kGBeta + c];
+                        }
+                    }
+                    put_terms<128, 2>(base + G::kM, 16384, L, 32 * wg, m);
+                }
+                if (rows < kChunk)                        // tokens of what lies behind: rows of zero instead
+                    for (int j = tid; j < (DK / 64) * 2 * (kChunk - rows) * 8; j += 256) {
+                        const int p = j & 7, q = rows + (j >> 3) % (kChunk - rows), b = (j >> 3) / (kChunk - rows);
+                        st_shared16(base + b * 8192 + q * 128 + p * 16, 0, 0, 0, 0);
+                    }
+                wait_or_dead(p2, n & 1, a.err, dead);
+                __syncwarp();
+                tc_fence_after();
+                const float fa = is_k ? -eg : eg;
+#pragma unroll 1
+                for (int g = 0; g < HC / 32; ++g) {
+                    const int c0 = HC * wg + 32 * g;
+                    uint32_t x[32], y[32];
+                    tmem_ld_n(tmem + G::kDa + lanes + c0, x);
+                    tmem_ld_n(tmem + G::kDw + lanes + c0, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        x[j] = __float_as_uint(fa * __uint_as_float(x[j]));
+                        y[j] = __float_as_uint(bt * __uint_as_float(y[j]));
+                    }
+                    tmem_st32(tmem + G::kDa + lanes + c0, x);
+                    tmem_st32(tmem + G::kDw + lanes + c0, y);
+                }
+                tmem_wait_st();
+                operand_ready(2, 288);
+                wait_or_dead(fin, n & 1, a.err, dead);
+                __syncwarp();
+                tc_fence_after();
+                const size_t at = ((size_t)(first + t) * sh.Hk + hk) * DK;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(is_k ? a.dk : a.dq) + at;
+                float* acc = (is_k ? dkf : dqf) + at;
+#pragma unroll 1
+                for (int g = 0; g < HC / 32; ++g) {
+                    const int c0 = HC * wg + 32 * g;
+                    uint32_t x[32], y[32];
+                    tmem_ld_n(tmem + G::kDa + lanes + c0, x);
+                    if (is_k) tmem_ld_n(tmem + G::kDw + lanes + c0, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int c = c0 + 8 * p;
+                        float o[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = __uint_as_float(x[8 * p + e]) + (is_k ? __uint_as_float(y[8 * p + e]) : 0.f);
+                        if (t < rows) {
+                            if (rep > 1) {                // the group's heads in their order
+                                float4* f = reinterpret_cast<float4*>(acc + c);
+                                if (r > 0) {
+                                    const float4 f0 = f[0], f1 = f[1];
+                                    o[0] += f0.x; o[1] += f0.y; o[2] += f0.z; o[3] += f0.w;
+                                    o[4] += f1.x; o[5] += f1.y; o[6] += f1.z; o[7] += f1.w;
+                                }
+                                if (r + 1 < rep) {
+                                    f[0] = make_float4(o[0], o[1], o[2], o[3]);
+                                    f[1] = make_float4(o[4], o[5], o[6], o[7]);
+                                }
+                            }
+                            if (r + 1 == rep)
+                                *reinterpret_cast<uint4*>(out + c) = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]),
+                                                                                pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(kqe);          // Q, K, the gates and ys may be overwritten
+                __syncwarp();
+                asm volatile("bar.arrive 3, 288;\n" ::: "memory");
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -530,63 +1293,121 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// Rows of tokens, 64 columns (128 bytes, swizzled) x 64 tokens a box.
-bool token_map(CUtensorMap* m, const void* p, int total, int width, int ld) {
+// Rows of tokens, 64 a box, of `cols` columns; swizzled by 128, 64 or 32 bytes, or (0) as they are.
+bool token_map(CUtensorMap* m, const void* p, long long total, int width, long long ld, int cols, int swizzle) {
     const auto enc = encode_fn();
     if (enc == nullptr) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)total}, strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64u, (cuuint32_t)kChunk}, estr[2] = {1u, 1u};
+    const cuuint32_t box[2] = {(cuuint32_t)cols, (cuuint32_t)kChunk}, estr[2] = {1u, 1u};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               swizzle == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+               : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+               : swizzle == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                               : CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool qk_maps(const SeqArgs& a, CUtensorMap* q, CUtensorMap* k) {
+    return token_map(q, a.q, a.sh.total, a.sh.Hk * a.sh.dk, a.sh.ldq, 64, 128) &&
+           token_map(k, a.k, a.sh.total, a.sh.Hk * a.sh.dk, a.sh.ldk, 64, 128);
 }
 
 template <int DK>
-cudaError_t prep_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a, char* ops, cudaStream_t st) {
+cudaError_t prep_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a, char* ops, uint32_t op_bytes, cudaStream_t st) {
     static bool done[64];
     cudaError_t e = ensure_smem(seq_prep_kernel<DK>, PrepGeom<DK>::kSmem, done);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((size_t)seq_slots(a.sh.nseq, a.sh.total) * a.sh.H);
-    return launch_kernel(seq_prep_kernel<DK>, dim3(grid), dim3(kPrepThreads), PrepGeom<DK>::kSmem, st, false, q, k, a, ops);
+    return launch_kernel(seq_prep_kernel<DK>, dim3(grid), dim3(kPrepThreads), PrepGeom<DK>::kSmem, st, false, q, k, a, ops,
+                         op_bytes);
 }
 
 template <int DK, int NV>
-cudaError_t fwd_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a, char* ops, char* recS, char* recE, cudaStream_t st) {
+cudaError_t fwd_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a, cudaStream_t st) {
+    const SeqLayout L = seq_layout(a.sh, GDN_DTYPE_BF16);
+    const bool rec = a.rec != nullptr;
+    const char* ops = rec ? a.rec + L.rec_op : a.ws + L.ws_op;
+    char *recS = rec ? a.rec + L.rec_S : nullptr, *recE = rec ? a.rec + L.rec_eps : nullptr, *recO = rec ? a.rec + L.rec_o : nullptr;
     static bool done[64];
     cudaError_t e = ensure_smem(seq_fwd_kernel<DK, NV>, fwd_smem<DK, NV>(), done);
     if (e != cudaSuccess) return e;
+    CUtensorMap v;
+    if (!token_map(&v, a.v, a.sh.total, a.sh.H * a.sh.dv, a.sh.ldv, NV, 0)) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)((size_t)a.sh.nseq * a.sh.H * (a.sh.dv / NV));
-    return launch_kernel(seq_fwd_kernel<DK, NV>, dim3(grid), dim3(kFwdThreads), fwd_smem<DK, NV>(), st, true, q, k, a, (const char*)ops,
-                         recS, recE);
+    return launch_kernel(seq_fwd_kernel<DK, NV>, dim3(grid), dim3(kFwdThreads), fwd_smem<DK, NV>(), st, true, q, k, v, a,
+                         ops, rec ? kOpRecord : kOpBytes, recS, recE, recO);
 }
 
 template <int DK>
-cudaError_t forward_dk(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a, char* ops, char* recS, char* recE, cudaStream_t st) {
-    const cudaError_t e = prep_go<DK>(q, k, a, ops, st);
+cudaError_t forward_dk(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a, cudaStream_t st) {
+    const SeqLayout L = seq_layout(a.sh, GDN_DTYPE_BF16);
+    const cudaError_t e = a.rec != nullptr ? prep_go<DK>(q, k, a, a.rec + L.rec_op, kOpRecord, st)
+                                           : prep_go<DK>(q, k, a, a.ws + L.ws_op, kOpBytes, st);
     if (e != cudaSuccess) return e;
-    return seq_tc_cols(a.sh) == 32 ? fwd_go<DK, 32>(q, k, a, ops, recS, recE, st) : fwd_go<DK, 16>(q, k, a, ops, recS, recE, st);
+    return seq_tc_cols(a.sh) == 32 ? fwd_go<DK, 32>(q, k, a, st) : fwd_go<DK, 16>(q, k, a, st);
+}
+
+template <int DK, int NV>
+cudaError_t bwd_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a, const SeqLayout& L, cudaStream_t st) {
+    static bool done_scan[64], done_grad[64];
+    cudaError_t e = ensure_smem(seq_bwd_kernel<DK, NV>, bwd_smem<DK, NV>(), done_scan);
+    if (e == cudaSuccess) e = ensure_smem(seq_grad_kernel<DK, NV>, GradGeom<DK, NV>::kSmem, done_grad);
+    if (e != cudaSuccess) return e;
+    const SeqShape& sh = a.sh;
+    const long long rows = (long long)seq_slots(sh.nseq, sh.total) * sh.H * 2 * kChunk;
+    CUtensorMap o, ev, vv;
+    if (!token_map(&o, a.dout, sh.total, sh.H * sh.dv, sh.H * sh.dv, NV, 2 * NV) ||
+        !token_map(&ev, a.rec + L.rec_eps, rows, sh.dv, sh.dv, NV, 2 * NV) || !token_map(&vv, a.ws + L.ws_dV, rows, sh.dv, sh.dv, NV, 2 * NV))
+        return cudaErrorInvalidValue;
+    const char* ops = a.rec + L.rec_op;
+    float *part = reinterpret_cast<float*>(a.ws + L.ws_part), *phi = reinterpret_cast<float*>(a.ws + L.ws_phi);
+    e = launch_kernel(seq_bwd_kernel<DK, NV>, dim3((unsigned)((size_t)sh.nseq * sh.H * (sh.dv / NV))), dim3(kFwdThreads),
+                      bwd_smem<DK, NV>(), st, false, q, k, o, a, ops, (const char*)(a.rec + L.rec_S), (const char*)(a.rec + L.rec_eps),
+                      (const char*)(a.rec + L.rec_o), a.ws + L.ws_dS, a.ws + L.ws_dV, part, phi);
+    if (e != cudaSuccess) return e;
+    const long long items = (long long)seq_slots(sh.nseq, sh.total) * sh.Hk;
+    return launch_kernel(seq_grad_kernel<DK, NV>, dim3((unsigned)(items < kSMs ? items : kSMs)), dim3(kFwdThreads),
+                         GradGeom<DK, NV>::kSmem, st, true, q, k, o, ev, vv, a, ops, (const char*)(a.rec + L.rec_S),
+                         (const char*)(a.ws + L.ws_dS), (const float*)part, (const float*)phi, reinterpret_cast<float*>(a.ws + L.ws_dq), reinterpret_cast<float*>(a.ws + L.ws_dk));
+}
+
+template <int DK>
+cudaError_t backward_dk(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a, const SeqLayout& L, cudaStream_t st) {
+    return seq_tc_cols(a.sh) == 32 ? bwd_go<DK, 32>(q, k, a, L, st) : bwd_go<DK, 16>(q, k, a, L, st);
 }
 
 }  // namespace
 
-bool seq_tc_takes(const SeqShape& s, int dtype) { return dtype == GDN_DTYPE_BF16 && s.dk % 64 == 0; }
+// bf16 with d_k in 64-column tiles; the rows of a call's chunks are numbered in 32 bits.
+bool seq_tc_takes(const SeqShape& s, int dtype) {
+    return dtype == GDN_DTYPE_BF16 && s.dk % 64 == 0 && (long long)seq_slots(s.nseq, s.total) * s.H * 2 * kChunk <= 0x7fffffffLL;
+}
 
 int seq_tc_cols(const SeqShape& s) {
-    return s.dv % 32 == 0 && (size_t)s.nseq * s.H * (s.dv / 16) > 152 ? 32 : 16;
+    return s.dv % 32 == 0 && (size_t)s.nseq * s.H * (s.dv / 16) > kSMs ? 32 : 16;
 }
 
 cudaError_t launch_seq_forward_tc(const SeqArgs& a, cudaStream_t st) {
-    const SeqLayout L = seq_layout(a.sh, GDN_DTYPE_BF16);
-    char* ops = a.rec != nullptr ? a.rec + L.rec_op : a.ws + L.ws_op;
-    char* recS = a.rec != nullptr ? a.rec + L.rec_S : nullptr;
-    char* recE = a.rec != nullptr ? a.rec + L.rec_eps : nullptr;
     CUtensorMap q, k;
-    if (!token_map(&q, a.q, a.sh.total, a.sh.Hk * a.sh.dk, a.sh.ldq) || !token_map(&k, a.k, a.sh.total, a.sh.Hk * a.sh.dk, a.sh.ldk))
-        return cudaErrorInvalidValue;
+    if (!qk_maps(a, &q, &k)) return cudaErrorInvalidValue;
     switch (a.sh.dk) {
-        case 64: return forward_dk<64>(q, k, a, ops, recS, recE, st);
-        case 128: return forward_dk<128>(q, k, a, ops, recS, recE, st);
-        case 192: return forward_dk<192>(q, k, a, ops, recS, recE, st);
-        default: return forward_dk<256>(q, k, a, ops, recS, recE, st);
+        case 64: return forward_dk<64>(q, k, a, st);
+        case 128: return forward_dk<128>(q, k, a, st);
+        case 192: return forward_dk<192>(q, k, a, st);
+        default: return forward_dk<256>(q, k, a, st);
+    }
+}
+
+cudaError_t launch_seq_backward_tc(const SeqArgs& a, cudaStream_t st) {
+    const SeqLayout L = seq_layout(a.sh, GDN_DTYPE_BF16);
+    CUtensorMap q, k;
+    if (!qk_maps(a, &q, &k)) return cudaErrorInvalidValue;
+    switch (a.sh.dk) {
+        case 64: return backward_dk<64>(q, k, a, L, st);
+        case 128: return backward_dk<128>(q, k, a, L, st);
+        case 192: return backward_dk<192>(q, k, a, L, st);
+        default: return backward_dk<256>(q, k, a, L, st);
     }
 }
 

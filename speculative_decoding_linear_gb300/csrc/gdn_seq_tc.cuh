@@ -138,13 +138,25 @@ __device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes
 __device__ __forceinline__ void bulk_read_done() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
 __device__ __forceinline__ void bulk_all_done() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
 
-// Bounded wait that gives up at once after any wait of the CTA has given up.
-__device__ __forceinline__ bool wait_or_dead(uint32_t bar, uint32_t parity, int* err, volatile int* dead) {
-    if (mbar_try_wait(bar, parity)) return true;
+// Bounded wait that gives up at once after any wait of the CTA has given up.  It polls with
+// test_wait: a waiting thread that try_wait suspends comes back some 340 cycles late (a product's
+// end seen 160 cycles after its last instruction instead of 500), three times in a chunk.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+static __device__ __noinline__ bool poll_slow(uint32_t bar, uint32_t parity, int* err, volatile int* dead) {
     const uint64_t t0 = globaltimer_ns(), limit = wait_limit_ns(err);
     while (true) {
-        for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
+        for (int i = 0; i < 256; ++i)
+            if (mbar_test(bar, parity)) return true;
         if (*dead) return false;
         if (globaltimer_ns() - t0 > limit) {
             set_error(err, GDN_ERR_TIMEOUT);
@@ -153,20 +165,78 @@ __device__ __forceinline__ bool wait_or_dead(uint32_t bar, uint32_t parity, int*
         }
     }
 }
+__device__ __forceinline__ bool wait_or_dead(uint32_t bar, uint32_t parity, int* err, volatile int* dead) {
+#pragma unroll 1
+    for (int i = 0; i < 512; ++i)
+        if (mbar_test(bar, parity)) return true;
+    return poll_slow(bar, parity, err, dead);
+}
+
+// A value that is the same in the whole warp, known so to the compiler, and one thread of the warp.
+// tcgen05.mma takes its descriptors from uniform registers: built from values that the compiler
+// knows to be uniform, an issue takes about 20 cycles, else 80 to 200 (measured), more than the
+// product itself at the N of these kernels.
+__device__ __forceinline__ int warp_uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(e));
+    return e != 0;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+// A warp's generic writes of an operand are done, told to the warp that issues the products (which
+// waits in named_sync with the same id and count).  A barrier of the SM hands over in some 30
+// cycles, an mbarrier that is polled in 200 and more.
+__device__ __forceinline__ void operand_ready(int id, int n) {
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    asm volatile("bar.arrive %0, %1;\n" ::"r"(id), "r"(n) : "memory");
+}
+
+// 32 consecutive TMEM columns of this warp's 32 lanes; tmem_wait_st before they are used.
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n" ::"r"(t),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// Bring a box into L2; nothing waits for it.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0),
+                 "r"(c1)
+                 : "memory");
+}
 
 // ---------------------------------------------------------------------------
 // per (slot, head): what a chunk needs of its gates and of K K^T, Q K^T
-//   image   [That; Phat], 128 rows of 64, bf16 hi then lo, 128-byte-swizzled K-major (32 KiB)
-//   gates   eg[64] = e^{g_t}, bt[64] = beta_t e^{g_end - g_t}, e^{g_end}   (fp32, 1 KiB)
+//   tp      [That; Phat], 128 rows of 64, bf16 hi then lo, 128-byte-swizzled K-major (32 KiB)
+//   gates   fp32: bt = beta_t e^{g_end - g_t}, eg = e^{g_t}, tail = e^{g_end - g_t}, beta, e^{g_end},
+//           g as two floats
+//   tpb     in a record: [T; Ptil] of the backward pass, as tp
 // ---------------------------------------------------------------------------
-constexpr uint32_t kOpImage = 2 * 128 * 128;
-constexpr uint32_t kOpBytes = kOpImage + 1024;
+constexpr uint32_t kOpTP = 128 * 256;
+constexpr uint32_t kOpGates = 2048;
+constexpr uint32_t kOpBytes = kOpTP + kOpGates;             // without a record
+constexpr uint32_t kOpRecord = kOpBytes + kOpTP;            // in a record
+constexpr int kGBt = 0, kGEg = 64, kGTail = 128, kGBeta = 192, kGEnd = 256, kGHi = 260, kGLo = 324;
+constexpr uint32_t kGateFwd = 1040;                         // bytes that the forward scan takes
+constexpr uint32_t kGateBwd = 784;                          // and the backward scan, from kGEg
 
 }  // namespace seqtc
 
-struct SeqMaps;
 bool seq_tc_takes(const SeqShape& s, int dtype);
 int seq_tc_cols(const SeqShape& s);      // value columns of a CTA
 cudaError_t launch_seq_forward_tc(const SeqArgs& a, cudaStream_t st);
+cudaError_t launch_seq_backward_tc(const SeqArgs& a, cudaStream_t st);
 
 }  // namespace gdn
