@@ -355,8 +355,9 @@ SeqLayout seq_layout(const SeqShape& s, int dtype) {
     const size_t heads = s.H > s.Hk ? (size_t)s.total * s.Hk * s.dk * 4 : 0;
     const size_t tiles = slots * s.H * (s.dv / 16);        // of 16 value columns at least
     L.rec_S = 0;
-    L.rec_eps = align_up(L.rec_S + state, kSectionAlign);
-    L.rec_o = align_up(L.rec_eps + rows, kSectionAlign);
+    // three bf16 terms of the tensor-core kernels' operands, or fp32
+    L.rec_eps = align_up(L.rec_S + (tc ? state / 2 * 3 : state), kSectionAlign);
+    L.rec_o = align_up(L.rec_eps + (tc ? rows / 2 * 3 : rows), kSectionAlign);
     L.rec_op = align_up(L.rec_o + (tc ? rows : 0), kSectionAlign);
     L.rec_total = align_up(L.rec_op + (tc ? slots * s.H * seqtc::kOpRecord : 0), kSectionAlign);
     L.ws_op = 0;

@@ -38,6 +38,10 @@ __device__ __forceinline__ bool seq_range(const SeqShape& a, int s, int& first, 
     return true;
 }
 
+__device__ __forceinline__ int seq_slot0(const SeqShape& a, int s) {
+    return (a.offsets == nullptr ? s * (a.total / a.nseq) : a.offsets[s]) / kChunk + s;
+}
+
 // Sequence and chunk of a slot: false for an empty slot.  The search is for the last
 // sequence whose first slot is not behind `slot`; it ends for any content of the offsets,
 // and seq_range checks the one that it finds.

@@ -12,7 +12,8 @@
 //   [K; Q] S  ->  [That; Phat] r  ->  K^T (bt eps),
 // and what bounds a long sequence is their latency: a chain of T / 64 chunks.  S stays in
 // registers in fp32 (a row of d_k for each thread, NV columns of it) and goes to shared memory as
-// two bf16 terms for the first product; r and bt eps as three.
+// two bf16 terms for the first product; r and bt eps as three.  A pass that keeps a record takes three
+// of S as well: the gates' gradients are differences of dots with o and eps.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -223,18 +224,21 @@ __global__ void __launch_bounds__(kPrepThreads)
     }
     __syncthreads();
     char* op = ops + (size_t)blockIdx.x * op_bytes;
+    const bool record = op_bytes == kOpRecord;
+    const int odd = (slot - seq_slot0(sh, s)) & 1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = (tid >> 3) + 32 * i, c = tid & 7;
-        const float* x = (r < 64 ? T + r * kLd : A + (r - 64) * kLd) + 8 * c;
-        uint32_t p[4][2];
+        const float* x = ((r < 64) != (odd != 0) ? T : A) + (r & 63) * kLd + 8 * c;
+        uint32_t p[4][3];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) split_pair<2>(x[2 * j], x[2 * j + 1], p[j]);
-        char* at = op + sw_piece<128>(r, c);
-        *reinterpret_cast<uint4*>(at) = make_uint4(p[0][0], p[1][0], p[2][0], p[3][0]);
-        *reinterpret_cast<uint4*>(at + 16384) = make_uint4(p[0][1], p[1][1], p[2][1], p[3][1]);
+        for (int j = 0; j < 4; ++j) split_pair<3>(x[2 * j], x[2 * j + 1], p[j]);
+        char* at = op + kOpGates + sw_piece<128>(r, c);
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+            if (t < 2 || record) *reinterpret_cast<uint4*>(at + t * kOpTerm) = make_uint4(p[0][t], p[1][t], p[2][t], p[3][t]);
     }
-    float* gates = reinterpret_cast<float*>(op + kOpTP);
+    float* gates = reinterpret_cast<float*>(op);
     const float eh = ghi[rows - 1], el = glo[rows - 1];
     if (tid < 64) {
         const float tail = expf((eh - ghi[tid]) + (el - glo[tid]));
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(kPrepThreads)
         gates[kGHi + tid] = ghi[tid];
         gates[kGLo + tid] = glo[tid];
     }
-    if (op_bytes == kOpRecord) {
+    if (record) {
         // the backward pass's operands: T = (I + diag(beta) L)^-1 = I - diag(beta) That L and
         // Ptil = P T = P - Phat L, four rows of each and four columns for each thread
         const int t0 = 4 * (tid / 16), c0 = 4 * (tid % 16);
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(kPrepThreads)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) y[m][i][j] = fmaf(u[m][i], w[j], y[m][i][j]);
         }
-        char* tpb = op + kOpBytes;
+        char* tpb = op + kOpBack;
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -277,12 +281,12 @@ __global__ void __launch_bounds__(kPrepThreads)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     x[j] = m == 0 ? (t == c0 + j ? 1.f : 0.f) - bt[t] * y[0][i][j] : P[t * kLd + c0 + j] - y[1][i][j];
-                uint32_t p[2][2];
-                split_pair<2>(x[0], x[1], p[0]);
-                split_pair<2>(x[2], x[3], p[1]);
+                uint32_t p[2][3];
+                split_pair<3>(x[0], x[1], p[0]);
+                split_pair<3>(x[2], x[3], p[1]);
                 char* at = tpb + sw_piece<128>(64 * m + t, c0 / 8) + (c0 & 4) * 2;
-                *reinterpret_cast<uint2*>(at) = make_uint2(p[0][0], p[1][0]);
-                *reinterpret_cast<uint2*>(at + 16384) = make_uint2(p[0][1], p[1][1]);
+#pragma unroll
+                for (int z = 0; z < 3; ++z) *reinterpret_cast<uint2*>(at + z * kOpTerm) = make_uint2(p[0][z], p[1][z]);
             }
     }
     griddep_launch();
@@ -297,24 +301,26 @@ __global__ void __launch_bounds__(kPrepThreads)
 // seq_fwd_kernel
 // ---------------------------------------------------------------------------
 // Ten warps.  Eight compute: a thread owns a row of the state, and a token's row of K (warps
-// 0, 1, 4, 5) or of Q in the token steps, columns halved between warps 0-3 and 4-7.  One starts the
+// 0, 1, 4, 5; in odd chunks the others) or of Q in the token steps, columns halved between warps 0-3
+// and 4-7.  One starts the
 // copies of K, Q, V, the gates and [That; Phat], one issues the products.
-template <int DK, int NV>
+template <int DK, int NV, int ST>
 struct FwdGeom {
     static constexpr int kMH = DK > 128 ? 2 : 1;                  // halves of 128 rows of d_k
     static constexpr int kW = NV * 2;                             // bytes of an operand row
-    static constexpr uint32_t kTile = 128 * 128;                  // [K; Q], 64 columns of d_k
-    static constexpr uint32_t kV = 2 * kMH * kTile;               // filled up to 128 or 256 columns, then V, gates
-    static constexpr uint32_t kG = kV + 64 * kW;
-    static constexpr uint32_t kStage = (kG + kGateFwd + 1023) & ~1023u;
-    static constexpr uint32_t kTP = 2 * kStage;
-    static constexpr uint32_t kS = kTP + kOpTP;                   // two terms
+    // 64 columns of d_k: 64 rows of an even chunk's K, of Q, of an odd chunk's K.  [K; Q] and [Q; K] are
+    // 128 rows behind one another, K is there for two chunks and Q for one
+    static constexpr uint32_t kTile = 192 * 128;
+    static constexpr uint32_t kTP = 2 * kMH * kTile;              // filled up to 128 or 256 columns
+    static constexpr uint32_t kS = kTP + ST * kOpTerm;            // ST terms
     static constexpr uint32_t kSTerm = DK * kW;
-    static constexpr uint32_t kR = kS + 2 * kSTerm;               // three terms
+    static constexpr uint32_t kR = kS + ST * kSTerm;              // three terms
     static constexpr uint32_t kRTerm = 64 * kW;
-    static constexpr uint32_t kBar = kR + 3 * kRTerm;
+    static constexpr uint32_t kV = kR + 3 * kRTerm;               // one V; gates of two chunks
+    static constexpr uint32_t kG = kV + 64 * kW;
+    static constexpr uint32_t kBar = kG + 2 * kGateFwd;
     static constexpr uint32_t kSmem = kBar + 256 + 1024;
-    static constexpr int kD1 = 0, kD2 = 2 * NV, kD3 = kD2 + 3 * NV, kCols = kD3 + kMH * 3 * NV;
+    static constexpr int kD1 = 0, kD2 = ST * NV, kD3 = kD2 + 3 * NV, kCols = kD3 + kMH * 3 * NV;
     static constexpr int kAlloc = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static_assert(kCols <= 512 && kSmem <= 227 * 1024, "tile");
 };
@@ -322,18 +328,18 @@ constexpr int kFwdThreads = 320;
 constexpr int kSMs = 152;
 
 // More than one CTA per SM must not ask for more than the 512 columns of its TMEM.
-template <int DK, int NV>
+template <int DK, int NV, int ST>
 constexpr size_t fwd_smem() {
-    using G = FwdGeom<DK, NV>;
+    using G = FwdGeom<DK, NV, ST>;
     const size_t least = G::kAlloc == 512 ? 116 * 1024 : G::kAlloc == 256 ? 78 * 1024 : 58 * 1024;
     return G::kSmem > least ? G::kSmem : least;
 }
 
-template <int DK, int NV>
+template <int DK, int NV, int ST>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmV, SeqArgs a, const char* ops, uint32_t op_bytes, char* recS, char* recE, char* recO) {
-    using G = FwdGeom<DK, NV>;
+                   const __grid_constant__ CUtensorMap tmV, SeqArgs a, const char* ops, uint32_t op_bytes, char* recS, char* recE, float* recO) {
+    using G = FwdGeom<DK, NV, ST>;
     constexpr int W = G::kW, NH = NV / 2;                 // NH: value columns of a thread in the token steps
     constexpr int SC = G::kMH == 2 ? NV : NH;             // value columns of a thread's state row
     extern __shared__ unsigned char raw[];
@@ -341,7 +347,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     unsigned char* sm = raw + (base - r0);
     // copies landed (two stages; operands), their places free; products done; operands written
     const uint32_t full0 = base + G::kBar, empty0 = full0 + 16, tpf = full0 + 32, tpe = full0 + 40, b1 = full0 + 48,
-                   b2 = full0 + 56, b3 = full0 + 64, drain = full0 + 72;
+                   b2 = full0 + 56, b3 = full0 + 64, drain = full0 + 72, vf = full0 + 80, ve = full0 + 88, qf = full0 + 96, qe = full0 + 104;
     uint32_t* holder = reinterpret_cast<uint32_t*>(sm + G::kBar + 128);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const SeqShape& sh = a.sh;
@@ -357,14 +363,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const size_t slot0 = (size_t)(first / kChunk + s);
 
     if (tid == 0) {
-        for (int i = 0; i < 10; ++i) mbar_init(full0 + 8 * i, 1);
+        for (int i = 0; i < 14; ++i) mbar_init(full0 + 8 * i, 1);
+        mbar_init(ve, 4);
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (DK % 128 != 0) {                                  // columns of d_k that no copy fills
-        for (int st = 0; st < 2; ++st)
-            for (uint32_t o = tid * 16; o < G::kTile; o += kFwdThreads * 16)
-                st_shared16(base + st * G::kStage + (DK / 64) * G::kTile + o, 0, 0, 0, 0);
+        for (uint32_t o = tid * 16; o < G::kTile; o += kFwdThreads * 16) st_shared16(base + (DK / 64) * G::kTile + o, 0, 0, 0, 0);
     }
     fence_proxy_async_smem();
     if (warp == 9) tmem_alloc(smem_u32(holder), G::kAlloc);
@@ -376,7 +381,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (warp == 8) {
         griddep_wait();
         if (elect_one()) {
-            int issued = 0, ops_issued = 0;
+            int issued = 0, q_issued = 0, v_issued = 0, ops_issued = 0;
             // to L2 ahead of time: a copy that has to go to memory takes longer than a chunk
             auto prefetch = [&](int c) {
 #pragma unroll
@@ -389,24 +394,32 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             for (int c = 0; c < chunks; ++c) {
                 if (c + 2 < chunks) prefetch(c + 2);
                 if (c >= 2 && !wait_or_dead(empty0 + 8 * (c & 1), ((c >> 1) & 1) ^ 1, a.err, dead)) break;
-                const uint32_t st = base + (c & 1) * G::kStage, f = full0 + 8 * (c & 1);
+                const uint32_t f = full0 + 8 * (c & 1);
                 const char* op = ops + ((slot0 + c) * sh.H + h) * op_bytes;
-                mbar_expect_tx(f, 2 * DK * 128 + 64 * W + kGateFwd);
+                mbar_expect_tx(f, DK * 128 + kGateFwd);
 #pragma unroll
-                for (int b = 0; b < DK / 64; ++b) {
-                    tma_2d(st + b * G::kTile, &tmK, hk * DK + 64 * b, first + c * kChunk, f);
-                    tma_2d(st + b * G::kTile + 8192, &tmQ, hk * DK + 64 * b, first + c * kChunk, f);
-                }
-                tma_2d(st + G::kV, &tmV, h * sh.dv + v0, first + c * kChunk, f);
-                bulk_copy_g2s(st + G::kG, op + kOpTP, kGateFwd, f);
+                for (int b = 0; b < DK / 64; ++b)
+                    tma_2d(base + (c & 1) * 16384 + b * G::kTile, &tmK, hk * DK + 64 * b, first + c * kChunk, f);
+                bulk_copy_g2s(base + G::kG + (c & 1) * kGateFwd, op, kGateFwd, f);
                 issued = c + 1;
+                if (c >= 1 && !wait_or_dead(qe, (c - 1) & 1, a.err, dead)) break;
+                mbar_expect_tx(qf, DK * 128);
+#pragma unroll
+                for (int b = 0; b < DK / 64; ++b) tma_2d(base + 8192 + b * G::kTile, &tmQ, hk * DK + 64 * b, first + c * kChunk, qf);
+                q_issued = c + 1;
+                if (c >= 1 && !wait_or_dead(ve, (c - 1) & 1, a.err, dead)) break;
+                mbar_expect_tx(vf, 64 * W);
+                tma_2d(base + G::kV, &tmV, h * sh.dv + v0, first + c * kChunk, vf);
+                v_issued = c + 1;
                 if (c >= 1 && !wait_or_dead(tpe, (c - 1) & 1, a.err, dead)) break;
-                mbar_expect_tx(tpf, kOpTP);
-                bulk_copy_g2s(base + G::kTP, op, kOpTP, tpf);
+                mbar_expect_tx(tpf, ST * kOpTerm);
+                bulk_copy_g2s(base + G::kTP, op + kOpGates, ST * kOpTerm, tpf);
                 ops_issued = c + 1;
             }
             if (*dead) {                                  // copies in flight land before the CTA ends
                 for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) mbar_wait(full0 + 8 * (c & 1), (c >> 1) & 1, a.err);
+                if (q_issued > 0) mbar_wait(qf, (q_issued - 1) & 1, a.err);
+                if (v_issued > 0) mbar_wait(vf, (v_issued - 1) & 1, a.err);
                 if (ops_issued > 0) mbar_wait(tpf, (ops_issued - 1) & 1, a.err);
             }
         }
@@ -416,20 +429,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const uint64_t dS = mn_desc<W>(base + G::kS, G::kSTerm), dR = mn_desc<W>(base + G::kR, G::kRTerm), dTP = k_desc<128>(base + G::kTP);
         const bool leader = elect_one();
         for (int c = 0; c < chunks; ++c) {
-            const uint32_t ph = c & 1, st = base + (c & 1) * G::kStage;
+            const uint32_t ph = c & 1;
             wait_or_dead(full0 + 8 * (c & 1), (c >> 1) & 1, a.err, dead);
+            wait_or_dead(qf, ph, a.err, dead);
             __syncwarp();
             named_sync(1, 288);
             tc_fence_after();
             if (leader) {
-                const uint64_t dKQ = k_desc<128>(st);
+                const uint64_t dKQ = k_desc<128>(base + (c & 1) * 8192);
 #pragma unroll
                 for (int k = 0; k < DK / 16; ++k)
                     mma_bf16(tmem + G::kD1, dKQ + (((k / 4) * G::kTile + 32 * (k % 4)) >> 4), dS + (k * 16 * W >> 4),
-                             idesc_bf16(128, 2 * NV) | kBMn, k != 0);
+                             idesc_bf16(128, ST * NV) | kBMn, k != 0);
                 mma_commit(b1);
-                if (recS != nullptr)
-                    bulk_s2g(recS + (((slot0 + c) * sh.H + h) * tiles + tile) * (2 * G::kSTerm), base + G::kS, 2 * G::kSTerm);
+                mma_commit(qe);
+                if (ST == 3)
+                    bulk_s2g(recS + (((slot0 + c) * sh.H + h) * tiles + tile) * (ST * G::kSTerm), base + G::kS, ST * G::kSTerm);
             }
             __syncwarp();
             wait_or_dead(tpf, ph, a.err, dead);
@@ -438,20 +453,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             tc_fence_after();
             if (leader) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_bf16(tmem + G::kD2, dTP + 2 * k, dR + (k * 16 * W >> 4), idesc_bf16(128, 3 * NV) | kBMn, k != 0);
+                for (int t = 0; t < ST; ++t)              // term t with the first 3 - t of r
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_bf16(tmem + G::kD2, dTP + 1024 + 2 * k, dR + (k * 16 * W >> 4), idesc_bf16(128, 2 * NV) | kBMn, 1);
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(tmem + G::kD2, dTP + t * (kOpTerm >> 4) + 2 * k, dR + (k * 16 * W >> 4),
+                                 idesc_bf16(128, (3 - t) * NV) | kBMn, t + k != 0);
                 mma_commit(b2);
                 mma_commit(tpe);
-                if (recS != nullptr) bulk_read_done();    // S's image may be written again once b3 is through
+                if (ST == 3) bulk_read_done();    // S's image may be written again once b3 is through
             }
             __syncwarp();
             named_sync(3, 160);
             tc_fence_after();
             if (leader) {
-                const uint64_t dK = mn_desc<128>(st, G::kTile);
+                const uint64_t dK = mn_desc<128>(base + (c & 1) * 16384, G::kTile);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -464,7 +479,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             __syncwarp();
         }
         if (leader) {
-            if (recS != nullptr) bulk_all_done();
+            if (ST == 3) bulk_all_done();
             if (*dead) {                                  // products in flight end before their TMEM is freed
                 mma_commit(drain);
                 mbar_wait(drain, 0, a.err);
@@ -473,7 +488,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         __syncwarp();
     } else {
         const int wg = warp >> 2, w4 = warp & 3;
-        const bool reads_k = w4 < 2;                      // token rows of K, else of Q
         const int tok = 32 * (w4 & 1) + lane, vc = wg * NH;
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
         const int srow = (G::kMH == 2 ? 128 * wg : 0) + 32 * w4 + lane, scol = G::kMH == 2 ? 0 : wg * NH;
@@ -486,35 +500,41 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         griddep_wait();
         for (int c = 0; c < chunks; ++c) {
-            const uint32_t ph = c & 1, st = (c & 1) * G::kStage;
+            const uint32_t ph = c & 1;
+            const bool reads_k = (w4 < 2) == ((c & 1) == 0);      // token rows of K, else of Q
             const int rows = min(kChunk, len - c * kChunk);
             // the state as the first product's operand: rows of d_k, value columns along the row
-            if (owns) put_terms<W, 2>(base + G::kS, G::kSTerm, srow, scol, S);
+            if (owns) put_terms<W, ST>(base + G::kS, G::kSTerm, srow, scol, S);
             if (rows < kChunk) {
                 // the copy brought tokens of what lies behind: rows of zero instead
                 wait_or_dead(full0 + 8 * (c & 1), (c >> 1) & 1, a.err, dead);
+                wait_or_dead(qf, ph, a.err, dead);
                 for (int i = tid; i < (DK / 64) * 2 * (kChunk - rows) * 8; i += 256) {
                     const int p = i & 7, r = rows + (i >> 3) % (kChunk - rows), b = (i >> 3) / (kChunk - rows);
-                    st_shared16(base + st + b * 8192 + r * 128 + p * 16, 0, 0, 0, 0);
+                    st_shared16(base + (b >> 1) * G::kTile + (b & 1 ? 8192 : (c & 1) * 16384) + r * 128 + p * 16, 0, 0, 0, 0);
                 }
             }
             operand_ready(1, 288);
             wait_or_dead(full0 + 8 * (c & 1), (c >> 1) & 1, a.err, dead);
-            const float* gates = reinterpret_cast<const float*>(sm + st + G::kG);
+            const float* gates = reinterpret_cast<const float*>(sm + G::kG + (c & 1) * kGateFwd);
             const float eg = gates[kGEg + tok], bt = gates[kGBt + tok], ee = gates[kGEnd];
             uint4 vr[NH / 8];
             if (reads_k) {
+                wait_or_dead(vf, ph, a.err, dead);
+                __syncwarp();
 #pragma unroll
                 for (int i = 0; i < NH / 8; ++i) {
-                    vr[i] = reinterpret_cast<const uint4*>(sm + st + G::kV + tok * W + vc * 2)[i];
+                    vr[i] = reinterpret_cast<const uint4*>(sm + G::kV + tok * W + vc * 2)[i];
                     if (tok >= rows) vr[i] = make_uint4(0, 0, 0, 0);
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ve);
             }
             wait_or_dead(b1, ph, a.err, dead);
             __syncwarp();
             tc_fence_after();
             float x[NH];
-            tmem_sum<NH, 2>(tmem + G::kD1 + lanes + vc, NV, x);
+            tmem_sum<NH, ST>(tmem + G::kD1 + lanes + vc, NV, x);
             if (reads_k) {
 #pragma unroll
                 for (int i = 0; i < NH / 8; ++i) {
@@ -538,31 +558,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 for (int j = 0; j < NH; ++j) x[j] = bt * y[j];
                 put_terms<W, 3>(base + G::kR, G::kRTerm, tok, vc, x);
                 operand_ready(3, 160);
-                if (recE != nullptr) {                    // eps as two bf16 terms [2][64][dv]
-                    char* e = recE + ((slot0 + c) * sh.H + h) * (size_t)(2 * kChunk * 2) * sh.dv + ((size_t)tok * sh.dv + v0 + vc) * 2;
+                if constexpr (ST == 3) {                  // eps as three bf16 terms [3][64][dv]
+                    char* e = recE + ((slot0 + c) * sh.H + h) * (size_t)(3 * kChunk * 2) * sh.dv + ((size_t)tok * sh.dv + v0 + vc) * 2;
 #pragma unroll
                     for (int i = 0; i < NH / 8; ++i) {
-                        uint32_t p[4][2];
+                        uint32_t p[4][3];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) split_pair<2>(y[8 * i + 2 * j], y[8 * i + 2 * j + 1], p[j]);
-                        *reinterpret_cast<uint4*>(e + 16 * i) = make_uint4(p[0][0], p[1][0], p[2][0], p[3][0]);
-                        *reinterpret_cast<uint4*>(e + (size_t)kChunk * 2 * sh.dv + 16 * i) = make_uint4(p[0][1], p[1][1], p[2][1], p[3][1]);
+                        for (int j = 0; j < 4; ++j) split_pair<3>(y[8 * i + 2 * j], y[8 * i + 2 * j + 1], p[j]);
+#pragma unroll
+                        for (int t = 0; t < 3; ++t)
+                            *reinterpret_cast<uint4*>(e + (size_t)t * kChunk * 2 * sh.dv + 16 * i) = make_uint4(p[0][t], p[1][t], p[2][t], p[3][t]);
                     }
                 }
             } else {
                 __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + (((size_t)first + c * kChunk + tok) * sh.H + h) * sh.dv + v0 + vc;
-                char* e = recO + ((slot0 + c) * sh.H + h) * (size_t)(2 * kChunk * 2) * sh.dv + ((size_t)tok * sh.dv + v0 + vc) * 2;
+                float* e = recO + ((slot0 + c) * sh.H + h) * (size_t)kChunk * sh.dv + (size_t)tok * sh.dv + v0 + vc;
+#pragma unroll
+                for (int j = 0; j < NH; ++j) y[j] = fmaf(eg, x[j], y[j]);
 #pragma unroll
                 for (int i = 0; i < NH / 8; ++i) {
-                    uint32_t p[4][2];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        split_pair<2>(fmaf(eg, x[8 * i + 2 * j], y[8 * i + 2 * j]), fmaf(eg, x[8 * i + 2 * j + 1], y[8 * i + 2 * j + 1]), p[j]);
-                    const uint4 hi = make_uint4(p[0][0], p[1][0], p[2][0], p[3][0]);
-                    if (tok < rows) *reinterpret_cast<uint4*>(o + 8 * i) = hi;
-                    if (recO != nullptr) {                // the output as two terms, for the gates' gradient
-                        *reinterpret_cast<uint4*>(e + 16 * i) = hi;
-                        *reinterpret_cast<uint4*>(e + (size_t)kChunk * 2 * sh.dv + 16 * i) = make_uint4(p[0][1], p[1][1], p[2][1], p[3][1]);
+                    if (tok < rows)
+                        *reinterpret_cast<uint4*>(o + 8 * i) = make_uint4(pack_bf16(y[8 * i], y[8 * i + 1]), pack_bf16(y[8 * i + 2], y[8 * i + 3]),
+                                                                          pack_bf16(y[8 * i + 4], y[8 * i + 5]), pack_bf16(y[8 * i + 6], y[8 * i + 7]));
+                    if constexpr (ST == 3) {              // unrounded, for the gates' gradient
+                        *reinterpret_cast<float4*>(e + 8 * i) = make_float4(y[8 * i], y[8 * i + 1], y[8 * i + 2], y[8 * i + 3]);
+                        *reinterpret_cast<float4*>(e + 8 * i + 4) = make_float4(y[8 * i + 4], y[8 * i + 5], y[8 * i + 6], y[8 * i + 7]);
                     }
                 }
             }
@@ -610,20 +630,22 @@ template <int DK, int NV>
 struct BwdGeom {
     static constexpr int kMH = DK > 128 ? 2 : 1;
     static constexpr int kW = NV * 2;
-    static constexpr uint32_t kTile = 128 * 128;                  // [K; Q], 64 columns of d_k
-    static constexpr uint32_t kO = 2 * kMH * kTile;               // dO as an operand, then the gates
+    static constexpr uint32_t kTile = 64 * 128;                   // K or Q, 64 columns of d_k
+    static constexpr uint32_t kQK = 2 * kMH * kTile;              // filled up to 128 or 256 columns
+    static constexpr uint32_t kO = kQK;                           // a stage: K, dO as an operand, gates
     static constexpr uint32_t kG = kO + 64 * kW;
-    static constexpr uint32_t kBar = kG + 800;                    // of the first stage: barriers behind its gates
     static constexpr uint32_t kStage = (kG + kGateBwd + 1023) & ~1023u;
-    static_assert(kG + 1024 <= kStage && kGateBwd <= 800, "gates and barriers share the end of a stage");
-    static constexpr uint32_t kTP = 2 * kStage;
-    static constexpr uint32_t kS = kTP + kOpTP;                   // two terms
+    static constexpr uint32_t kBar = kG + kGateBwd;               // barriers behind the first stage's gates
+    static_assert(kBar + 192 <= kStage, "gates and barriers share the end of a stage");
+    static constexpr uint32_t kQ = 2 * kStage;                    // one Q
+    static constexpr uint32_t kTP = kQ + kQK;
+    static constexpr uint32_t kS = kTP + 3 * kOpTerm;             // three terms
     static constexpr uint32_t kSTerm = DK * kW;
-    static constexpr uint32_t kR = kS + 2 * kSTerm;               // three terms of w, then of -e^g dV
+    static constexpr uint32_t kR = kS + 3 * kSTerm;               // three terms of x, then of -e^g dV
     static constexpr uint32_t kRTerm = 64 * kW;
     static constexpr uint32_t kE = kR + 3 * kRTerm;               // three terms of e^g dO
     static constexpr uint32_t kSmem = kE + 3 * kRTerm + 1024;
-    static constexpr int kD1 = 0, kD2 = 2 * NV, kDP = kD2 + 3 * NV, kD3 = kDP + NV, kCols = kD3 + kMH * 3 * NV;
+    static constexpr int kD1 = 0, kD2 = 3 * NV, kDP = kD2 + 3 * NV, kD3 = kDP + NV, kCols = kD3 + kMH * 3 * NV;
     static constexpr int kAlloc = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static_assert(kCols <= 512 && kSmem <= 227 * 1024, "tile");
 };
@@ -638,7 +660,7 @@ constexpr size_t bwd_smem() {
 template <int DK, int NV>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     seq_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmO, SeqArgs a, const char* ops, const char* recS, const char* recE, const char* recO,
+                   const __grid_constant__ CUtensorMap tmO, SeqArgs a, const char* ops, const char* recS, const char* recE, const float* recO,
                    char* wsS, char* wsV, float* part, float* phi) {
     using G = BwdGeom<DK, NV>;
     constexpr int W = G::kW, NH = NV / 2;
@@ -647,8 +669,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t r0 = smem_u32(raw), base = (r0 + 1023u) & ~1023u;
     unsigned char* sm = raw + (base - r0);
     const uint32_t full0 = base + G::kBar, empty0 = full0 + 16, tpf = full0 + 32, tpe = full0 + 40, b1 = full0 + 48,
-                   b2 = full0 + 56, b3 = full0 + 64, drain = full0 + 72;
-    uint32_t* holder = reinterpret_cast<uint32_t*>(sm + G::kBar + 128);
+                   b2 = full0 + 56, b3 = full0 + 64, drain = full0 + 72, qf = full0 + 80, qe = full0 + 88;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(sm + G::kBar + 96);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const SeqShape& sh = a.sh;
     const int tiles = sh.dv / NV;
@@ -663,14 +685,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const size_t slot0 = (size_t)(first / kChunk + s);
 
     if (tid == 0) {
-        for (int i = 0; i < 10; ++i) mbar_init(full0 + 8 * i, 1);
+        for (int i = 0; i < 12; ++i) mbar_init(full0 + 8 * i, 1);
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (DK % 128 != 0) {                                  // columns of d_k that no copy fills
-        for (int st = 0; st < 2; ++st)
+        for (int st = 0; st < 3; ++st)
             for (uint32_t o = tid * 16; o < G::kTile; o += kFwdThreads * 16)
-                st_shared16(base + st * G::kStage + (DK / 64) * G::kTile + o, 0, 0, 0, 0);
+                st_shared16(base + (st < 2 ? st * G::kStage : G::kQ) + (DK / 64) * G::kTile + o, 0, 0, 0, 0);
     }
     fence_proxy_async_smem();
     if (warp == 9) tmem_alloc(smem_u32(holder), G::kAlloc);
@@ -682,29 +704,32 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // i counts the chunks as they are taken, c = chunks - 1 - i is the chunk
     if (warp == 8) {
         if (elect_one()) {
-            int issued = 0, ops_issued = 0;
+            int issued = 0, q_issued = 0, ops_issued = 0;
             for (int i = 0; i < chunks; ++i) {
                 const int c = chunks - 1 - i;
                 if (i >= 2 && !wait_or_dead(empty0 + 8 * (i & 1), ((i >> 1) & 1) ^ 1, a.err, dead)) break;
                 const uint32_t st = base + (i & 1) * G::kStage, f = full0 + 8 * (i & 1);
                 const char* op = ops + ((slot0 + c) * sh.H + h) * kOpRecord;
-                mbar_expect_tx(f, 2 * DK * 128 + 64 * W + kGateBwd);
+                mbar_expect_tx(f, DK * 128 + 64 * W + kGateBwd);
 #pragma unroll
-                for (int b = 0; b < DK / 64; ++b) {
-                    tma_2d(st + b * G::kTile, &tmK, hk * DK + 64 * b, first + c * kChunk, f);
-                    tma_2d(st + b * G::kTile + 8192, &tmQ, hk * DK + 64 * b, first + c * kChunk, f);
-                }
+                for (int b = 0; b < DK / 64; ++b) tma_2d(st + b * G::kTile, &tmK, hk * DK + 64 * b, first + c * kChunk, f);
                 tma_2d(st + G::kO, &tmO, h * sh.dv + v0, first + c * kChunk, f);
-                bulk_copy_g2s(st + G::kG, op + kOpTP + 4 * kGEg, kGateBwd, f);
-                bulk_prefetch_l2(recS + (((slot0 + c) * sh.H + h) * tiles + tile) * (2 * G::kSTerm), 2 * G::kSTerm);
+                bulk_copy_g2s(st + G::kG, op + 4 * kGEg, kGateBwd, f);
+                bulk_prefetch_l2(recS + (((slot0 + c) * sh.H + h) * tiles + tile) * (3 * G::kSTerm), 3 * G::kSTerm);
                 issued = i + 1;
+                if (i >= 1 && !wait_or_dead(qe, (i - 1) & 1, a.err, dead)) break;
+                mbar_expect_tx(qf, DK * 128);
+#pragma unroll
+                for (int b = 0; b < DK / 64; ++b) tma_2d(base + G::kQ + b * G::kTile, &tmQ, hk * DK + 64 * b, first + c * kChunk, qf);
+                q_issued = i + 1;
                 if (i >= 1 && !wait_or_dead(tpe, (i - 1) & 1, a.err, dead)) break;
-                mbar_expect_tx(tpf, kOpTP);
-                bulk_copy_g2s(base + G::kTP, op + kOpBytes, kOpTP, tpf);
+                mbar_expect_tx(tpf, 3 * kOpTerm);
+                bulk_copy_g2s(base + G::kTP, op + kOpBack, 3 * kOpTerm, tpf);
                 ops_issued = i + 1;
             }
             if (*dead) {                                  // copies in flight land before the CTA ends
                 for (int i = issued > 2 ? issued - 2 : 0; i < issued; ++i) mbar_wait(full0 + 8 * (i & 1), (i >> 1) & 1, a.err);
+                if (q_issued > 0) mbar_wait(qf, (q_issued - 1) & 1, a.err);
                 if (ops_issued > 0) mbar_wait(tpf, (ops_issued - 1) & 1, a.err);
             }
         }
@@ -720,40 +745,42 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const uint32_t ph = i & 1, st = base + (i & 1) * G::kStage;
             wait_or_dead(full0 + 8 * (i & 1), (i >> 1) & 1, a.err, dead);
             wait_or_dead(tpf, ph, a.err, dead);
+            wait_or_dead(qf, ph, a.err, dead);
             __syncwarp();
             named_sync(1, 288);
             tc_fence_after();
-            const uint64_t dK = mn_desc<128>(st, G::kTile);
+            const uint64_t dK = mn_desc<128>(st, G::kTile), dQ = mn_desc<128>(base + G::kQ, G::kTile);
             if (leader) {
-                const uint64_t dKQ = k_desc<128>(st), dO = mn_desc<W>(st + G::kO, 0);
+                // 128 rows: K's 64 and whatever lies behind, lanes that nothing reads
+                const uint64_t dKr = k_desc<128>(st), dO = mn_desc<W>(st + G::kO, 0);
 #pragma unroll
                 for (int k = 0; k < DK / 16; ++k)
-                    mma_bf16(tmem + G::kD1, dKQ + (((k / 4) * G::kTile + 32 * (k % 4)) >> 4), dS + (k * 16 * W >> 4),
-                             idesc_bf16(128, 2 * NV) | kBMn, k != 0);
+                    mma_bf16(tmem + G::kD1, dKr + (((k / 4) * G::kTile + 32 * (k % 4)) >> 4), dS + (k * 16 * W >> 4),
+                             idesc_bf16(128, 3 * NV) | kBMn, k != 0);
                 mma_commit(b1);
                 bulk_s2g(wsS + (((slot0 + chunks - 1 - i) * sh.H + h) * tiles + tile) * (2 * G::kSTerm), base + G::kS, 2 * G::kSTerm);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_bf16(tmem + G::kDP, dTP + (k / 4) * 1024 + (8192 + (k % 4) * 2048 >> 4), dO + ((k % 4) * 16 * W >> 4),
+                for (int k = 0; k < 12; ++k)
+                    mma_bf16(tmem + G::kDP, dTP + (k / 4) * (kOpTerm >> 4) + (8192 + (k % 4) * 2048 >> 4), dO + ((k % 4) * 16 * W >> 4),
                              idesc_bf16(128, NV) | kAMn | kBMn, k != 0);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
                     for (int m = 0; m < G::kMH; ++m)
-                        mma_bf16(tmem + G::kD3 + m * 3 * NV, dK + ((2 * m * G::kTile + 8192 + k * 2048) >> 4), dE + (k * 16 * W >> 4),
+                        mma_bf16(tmem + G::kD3 + m * 3 * NV, dQ + ((2 * m * G::kTile + k * 2048) >> 4), dE + (k * 16 * W >> 4),
                                  idesc_bf16(128, 3 * NV) | kAMn | kBMn, k != 0);
+                mma_commit(qe);
             }
             __syncwarp();
             named_sync(2, 160);
             tc_fence_after();
             if (leader) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_bf16(tmem + G::kD2, dTP + (k * 2048 >> 4), dR + (k * 16 * W >> 4), idesc_bf16(128, 3 * NV) | kAMn | kBMn, k != 0);
+                for (int t = 0; t < 3; ++t)               // term t with the first 3 - t of x
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_bf16(tmem + G::kD2, dTP + 1024 + (k * 2048 >> 4), dR + (k * 16 * W >> 4),
-                             idesc_bf16(128, 2 * NV) | kAMn | kBMn, 1);
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(tmem + G::kD2, dTP + t * (kOpTerm >> 4) + (k * 2048 >> 4), dR + (k * 16 * W >> 4),
+                                 idesc_bf16(128, (3 - t) * NV) | kAMn | kBMn, t + k != 0);
                 mma_commit(b2);
                 mma_commit(tpe);
                 bulk_read_done();                         // dS's image may be written again once b3 is through
@@ -796,18 +823,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         // this CTA's part of <S, dS> at the start of chunk c; S's image is swizzled as in shared memory
         auto state_dot = [&](int c) {
-            const char* p = recS + (((slot0 + c) * sh.H + h) * tiles + tile) * (2 * G::kSTerm);
+            const char* p = recS + (((slot0 + c) * sh.H + h) * tiles + tile) * (3 * G::kSTerm);
             float d = 0.f;
             if (owns)
 #pragma unroll
                 for (int j = 0; j < SC / 8; ++j) {
                     const char* q = p + sw_piece<W>(srow, scol / 8 + j);
-                    const uint4 u = *reinterpret_cast<const uint4*>(q), l = *reinterpret_cast<const uint4*>(q + G::kSTerm);
-                    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ll[4] = {l.x, l.y, l.z, l.w};
+                    const uint4 u = *reinterpret_cast<const uint4*>(q), m = *reinterpret_cast<const uint4*>(q + G::kSTerm),
+                                l = *reinterpret_cast<const uint4*>(q + 2 * G::kSTerm);
+                    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, mm[4] = {m.x, m.y, m.z, m.w}, ll[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        d = fmaf(__uint_as_float(uu[e] << 16) + __uint_as_float(ll[e] << 16), S[8 * j + 2 * e], d);
-                        d = fmaf(__uint_as_float(uu[e] & 0xffff0000u) + __uint_as_float(ll[e] & 0xffff0000u), S[8 * j + 2 * e + 1], d);
+                        d = fmaf(__uint_as_float(uu[e] << 16) + (__uint_as_float(mm[e] << 16) + __uint_as_float(ll[e] << 16)), S[8 * j + 2 * e], d);
+                        d = fmaf(__uint_as_float(uu[e] & 0xffff0000u) +
+                                     (__uint_as_float(mm[e] & 0xffff0000u) + __uint_as_float(ll[e] & 0xffff0000u)), S[8 * j + 2 * e + 1], d);
                     }
                 }
             d = warp_sum(d);
@@ -817,14 +846,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const int c = chunks - 1 - i;
             const uint32_t ph = i & 1, st = (i & 1) * G::kStage;
             const int rows = min(kChunk, len - c * kChunk);
-            if (owns) put_terms<W, 2>(base + G::kS, G::kSTerm, srow, scol, S);
+            if (owns) put_terms<W, 3>(base + G::kS, G::kSTerm, srow, scol, S);
             wait_or_dead(full0 + 8 * (i & 1), (i >> 1) & 1, a.err, dead);
             __syncwarp();
             if (rows < kChunk) {
                 // the copies brought tokens of what lies behind: rows of zero instead
+                wait_or_dead(qf, ph, a.err, dead);
                 for (int j = tid; j < (DK / 64) * 2 * (kChunk - rows) * 8; j += 256) {
                     const int p = j & 7, r = rows + (j >> 3) % (kChunk - rows), b = (j >> 3) / (kChunk - rows);
-                    st_shared16(base + st + b * 8192 + r * 128 + p * 16, 0, 0, 0, 0);
+                    st_shared16(base + (b & 1 ? G::kQ : st) + (b >> 1) * G::kTile + r * 128 + p * 16, 0, 0, 0, 0);
                 }
             }
             const float* gates = reinterpret_cast<const float*>(sm + st + G::kG);
@@ -847,18 +877,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
             operand_ready(1, 288);
             if (i > 0) state_dot(c + 1);
-            // eps and o as two terms each, v and dO of this thread's token and columns
-            uint4 te[2][NH / 8], to[2][NH / 8], tv[NH / 8], td[NH / 8];
+            // eps (three terms), o, v and dO of this thread's token and columns
+            // (from the stage now: it may be filled again once the last product is done)
+            uint4 te[3][NH / 8], to[NH / 4], tv[NH / 8], td[NH / 8];
             if (!reads_k) {
-                const size_t at = ((slot0 + c) * sh.H + h) * (size_t)(2 * kChunk * 2) * sh.dv + ((size_t)tok * sh.dv + v0 + vc) * 2;
+                const size_t at = (slot0 + c) * sh.H + h, row = (size_t)tok * sh.dv + v0 + vc;
                 const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + ((size_t)first + c * kChunk + tok) * sh.ldv + (size_t)h * sh.dv + v0 + vc;
 #pragma unroll
                 for (int p = 0; p < NH / 8; ++p) {
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        te[t][p] = *reinterpret_cast<const uint4*>(recE + at + (size_t)t * kChunk * 2 * sh.dv + 16 * p);
-                        to[t][p] = *reinterpret_cast<const uint4*>(recO + at + (size_t)t * kChunk * 2 * sh.dv + 16 * p);
-                    }
+                    for (int t = 0; t < 3; ++t)
+                        te[t][p] = *reinterpret_cast<const uint4*>(recE + ((at * 3 + t) * kChunk * sh.dv + row) * 2 + 16 * p);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) to[2 * p + t] = *reinterpret_cast<const uint4*>(recO + at * kChunk * sh.dv + row + 8 * p + 4 * t);
                     tv[p] = make_uint4(0, 0, 0, 0);
                     if (tok < rows) tv[p] = *reinterpret_cast<const uint4*>(vp + 8 * p);
                     td[p] = *reinterpret_cast<const uint4*>(sm + st + G::kO + sw_piece<W>(tok, vc / 8 + p));
@@ -868,7 +899,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             __syncwarp();
             tc_fence_after();
             if (reads_k) {
-                tmem_sum<NH, 2>(tmem + G::kD1 + lanes + vc, NV, x);
+                tmem_sum<NH, 3>(tmem + G::kD1 + lanes + vc, NV, x);
 #pragma unroll
                 for (int j = 0; j < NH; ++j) x[j] *= tail;
                 put_terms<W, 3>(base + G::kR, G::kRTerm, tok, vc, x);
@@ -898,7 +929,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 float db = 0.f, dl = 0.f;
 #pragma unroll
                 for (int p = 0; p < NH / 8; ++p) {
-                    const uint32_t *e0 = &te[0][p].x, *e1 = &te[1][p].x, *o0 = &to[0][p].x, *o1 = &to[1][p].x, *v4 = &tv[p].x, *d4 = &td[p].x;
+                    const uint32_t *e0 = &te[0][p].x, *e1 = &te[1][p].x, *e2 = &te[2][p].x, *o4 = &to[2 * p].x, *v4 = &tv[p].x, *d4 = &td[p].x;
                     uint32_t u[4][2];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -906,9 +937,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         for (int z = 0; z < 2; ++z) {
                             auto half = [&](uint32_t w) { return __uint_as_float(z ? w & 0xffff0000u : w << 16); };
                             float& w = x[8 * p + 2 * j + z];
-                            db = fmaf(w, half(e0[j]) + half(e1[j]), db);
+                            db = fmaf(w, half(e0[j]) + (half(e1[j]) + half(e2[j])), db);
                             w *= beta;
-                            dl = fmaf(half(d4[j]), half(o0[j]) + half(o1[j]), fmaf(-w, half(v4[j]), dl));
+                            dl = fmaf(half(d4[j]), __uint_as_float(o4[2 * j + z]), fmaf(-w, half(v4[j]), dl));
                         }
                         split_pair<2>(x[8 * p + 2 * j], x[8 * p + 2 * j + 1], u[j]);
                     }
@@ -1029,7 +1060,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 for (int r = 0; r < rep && ok; ++r, ++n) {
                     const int h = hk * rep + r;
                     const size_t sh_at = (size_t)(item / sh.Hk) * sh.H + h;
-                    const int erow = (int)(sh_at * 2 * kChunk);
+                    const int erow = (int)(sh_at * 3 * kChunk), vrow = (int)(sh_at * 2 * kChunk);
                     if (n >= 1 && !(ok = wait_or_dead(kqe, (n - 1) & 1, a.err, dead))) break;
                     mbar_expect_tx(kqf, 2 * DK * 128 + kOpGates);
 #pragma unroll
@@ -1037,7 +1068,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         tma_2d(base + b * G::kTile, &tmQ, hk * DK + 64 * b, first, kqf);
                         tma_2d(base + b * G::kTile + 8192, &tmK, hk * DK + 64 * b, first, kqf);
                     }
-                    bulk_copy_g2s(base + G::kGates, ops + sh_at * kOpRecord + kOpTP, kOpGates, kqf);
+                    bulk_copy_g2s(base + G::kGates, ops + sh_at * kOpRecord, kOpGates, kqf);
                     for (int j = 0; j < 3 * tiles; ++j, ++it) {
                         const uint32_t sl = base + G::kSlot0 + (it & 1) * G::kSlot, f = full0 + 8 * (it & 1);
                         if (it >= 2 && !(ok = wait_or_dead(empty0 + 8 * (it & 1), ((it >> 1) & 1) ^ 1, a.err, dead))) break;
@@ -1045,13 +1076,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         if (j < tiles || ((j - tiles) & 1) == 0) {
                             mbar_expect_tx(f, 3 * G::kBlk + (j < tiles ? 2 * G::kBlk : 2 * DK * W));
                             tma_2d(sl, &tmO, h * sh.dv + v0, first, f);
-                            tma_2d(sl + G::kBlk, &tmV, v0, erow, f);
-                            tma_2d(sl + 3 * G::kBlk, &tmV, v0, erow + kChunk, f);
+                            tma_2d(sl + G::kBlk, &tmV, v0, vrow, f);
+                            tma_2d(sl + 3 * G::kBlk, &tmV, v0, vrow + kChunk, f);
                             if (j < tiles) {
                                 tma_2d(sl + G::kImg, &tmE, v0, erow, f);
                                 tma_2d(sl + G::kImg + G::kBlk, &tmE, v0, erow + kChunk, f);
                             } else {
-                                bulk_copy_g2s(sl + G::kImg, recS + (sh_at * tiles + v) * (2 * DK * W), 2 * DK * W, f);
+                                bulk_copy_g2s(sl + G::kImg, recS + (sh_at * tiles + v) * (3 * DK * W), 2 * DK * W, f);
                             }
                         } else {
                             mbar_expect_tx(f, 4 * G::kBlk + 2 * DK * W);
@@ -1323,20 +1354,19 @@ cudaError_t prep_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a
                          op_bytes);
 }
 
-template <int DK, int NV>
+template <int DK, int NV, int ST>
 cudaError_t fwd_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a, cudaStream_t st) {
-    const SeqLayout L = seq_layout(a.sh, GDN_DTYPE_BF16);
-    const bool rec = a.rec != nullptr;
-    const char* ops = rec ? a.rec + L.rec_op : a.ws + L.ws_op;
-    char *recS = rec ? a.rec + L.rec_S : nullptr, *recE = rec ? a.rec + L.rec_eps : nullptr, *recO = rec ? a.rec + L.rec_o : nullptr;
     static bool done[64];
-    cudaError_t e = ensure_smem(seq_fwd_kernel<DK, NV>, fwd_smem<DK, NV>(), done);
+    cudaError_t e = ensure_smem(seq_fwd_kernel<DK, NV, ST>, fwd_smem<DK, NV, ST>(), done);
     if (e != cudaSuccess) return e;
     CUtensorMap v;
     if (!token_map(&v, a.v, a.sh.total, a.sh.H * a.sh.dv, a.sh.ldv, NV, 0)) return cudaErrorInvalidValue;
+    const SeqLayout L = seq_layout(a.sh, GDN_DTYPE_BF16);
     const unsigned grid = (unsigned)((size_t)a.sh.nseq * a.sh.H * (a.sh.dv / NV));
-    return launch_kernel(seq_fwd_kernel<DK, NV>, dim3(grid), dim3(kFwdThreads), fwd_smem<DK, NV>(), st, true, q, k, v, a,
-                         ops, rec ? kOpRecord : kOpBytes, recS, recE, recO);
+    return launch_kernel(seq_fwd_kernel<DK, NV, ST>, dim3(grid), dim3(kFwdThreads), fwd_smem<DK, NV, ST>(), st, true, q, k, v, a,
+                         (const char*)(ST == 3 ? a.rec + L.rec_op : a.ws + L.ws_op), ST == 3 ? kOpRecord : kOpBytes,
+                         ST == 3 ? a.rec + L.rec_S : nullptr, ST == 3 ? a.rec + L.rec_eps : nullptr,
+                         ST == 3 ? reinterpret_cast<float*>(a.rec + L.rec_o) : nullptr);
 }
 
 template <int DK>
@@ -1345,7 +1375,8 @@ cudaError_t forward_dk(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs
     const cudaError_t e = a.rec != nullptr ? prep_go<DK>(q, k, a, a.rec + L.rec_op, kOpRecord, st)
                                            : prep_go<DK>(q, k, a, a.ws + L.ws_op, kOpBytes, st);
     if (e != cudaSuccess) return e;
-    return seq_tc_cols(a.sh) == 32 ? fwd_go<DK, 32>(q, k, a, st) : fwd_go<DK, 16>(q, k, a, st);
+    if (a.rec != nullptr) return seq_tc_cols(a.sh) == 32 ? fwd_go<DK, 32, 3>(q, k, a, st) : fwd_go<DK, 16, 3>(q, k, a, st);
+    return seq_tc_cols(a.sh) == 32 ? fwd_go<DK, 32, 2>(q, k, a, st) : fwd_go<DK, 16, 2>(q, k, a, st);
 }
 
 template <int DK, int NV>
@@ -1358,13 +1389,13 @@ cudaError_t bwd_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a,
     const long long rows = (long long)seq_slots(sh.nseq, sh.total) * sh.H * 2 * kChunk;
     CUtensorMap o, ev, vv;
     if (!token_map(&o, a.dout, sh.total, sh.H * sh.dv, sh.H * sh.dv, NV, 2 * NV) ||
-        !token_map(&ev, a.rec + L.rec_eps, rows, sh.dv, sh.dv, NV, 2 * NV) || !token_map(&vv, a.ws + L.ws_dV, rows, sh.dv, sh.dv, NV, 2 * NV))
+        !token_map(&ev, a.rec + L.rec_eps, rows / 2 * 3, sh.dv, sh.dv, NV, 2 * NV) || !token_map(&vv, a.ws + L.ws_dV, rows, sh.dv, sh.dv, NV, 2 * NV))
         return cudaErrorInvalidValue;
     const char* ops = a.rec + L.rec_op;
     float *part = reinterpret_cast<float*>(a.ws + L.ws_part), *phi = reinterpret_cast<float*>(a.ws + L.ws_phi);
     e = launch_kernel(seq_bwd_kernel<DK, NV>, dim3((unsigned)((size_t)sh.nseq * sh.H * (sh.dv / NV))), dim3(kFwdThreads),
                       bwd_smem<DK, NV>(), st, false, q, k, o, a, ops, (const char*)(a.rec + L.rec_S), (const char*)(a.rec + L.rec_eps),
-                      (const char*)(a.rec + L.rec_o), a.ws + L.ws_dS, a.ws + L.ws_dV, part, phi);
+                      (const float*)(a.rec + L.rec_o), a.ws + L.ws_dS, a.ws + L.ws_dV, part, phi);
     if (e != cudaSuccess) return e;
     const long long items = (long long)seq_slots(sh.nseq, sh.total) * sh.Hk;
     return launch_kernel(seq_grad_kernel<DK, NV>, dim3((unsigned)(items < kSMs ? items : kSMs)), dim3(kFwdThreads),
@@ -1381,7 +1412,7 @@ cudaError_t backward_dk(const CUtensorMap& q, const CUtensorMap& k, const SeqArg
 
 // bf16 with d_k in 64-column tiles; the rows of a call's chunks are numbered in 32 bits.
 bool seq_tc_takes(const SeqShape& s, int dtype) {
-    return dtype == GDN_DTYPE_BF16 && s.dk % 64 == 0 && (long long)seq_slots(s.nseq, s.total) * s.H * 2 * kChunk <= 0x7fffffffLL;
+    return dtype == GDN_DTYPE_BF16 && s.dk % 64 == 0 && (long long)seq_slots(s.nseq, s.total) * s.H * 3 * kChunk <= 0x7fffffffLL;
 }
 
 int seq_tc_cols(const SeqShape& s) {

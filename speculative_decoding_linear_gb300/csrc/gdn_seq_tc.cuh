@@ -3,10 +3,10 @@
 //
 // An fp32 operand x enters a product as bf16 terms x = hi + mid (+ low), each the rounding of
 // what the terms before it left; q, k, v and dO are bf16 already and exact.  Two terms leave at
-// most 2^-18 of x (6e-7 of it in the mean square), three 2^-27.  The terms of the B operand lie
+// most 2^-16 of x (3e-6 of it in the mean square), three 2^-24.  The terms of the B operand lie
 // side by side along N, so that the A operand is read once for all of them, and their products
 // are added in fp32 where the accumulator is read.  A product of two split operands leaves out
-// those of the small terms, 2^-18 of the whole and below.
+// those of the small terms, 2^-16 of the whole and below.
 #pragma once
 
 #include "gdn_seq.cuh"
@@ -219,17 +219,18 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, 
 
 // ---------------------------------------------------------------------------
 // per (slot, head): what a chunk needs of its gates and of K K^T, Q K^T
-//   tp      [That; Phat], 128 rows of 64, bf16 hi then lo, 128-byte-swizzled K-major (32 KiB)
-//   gates   fp32: bt = beta_t e^{g_end - g_t}, eg = e^{g_t}, tail = e^{g_end - g_t}, beta, e^{g_end},
+//   gates   fp32: bt = beta_t e^{g_end - g_t}, eg = e^{g_t}, e^{g_end}, tail = e^{g_end - g_t}, beta,
 //           g as two floats
-//   tpb     in a record: [T; Ptil] of the backward pass, as tp
+//   tp      [That; Phat] ([Phat; That] for a sequence's odd chunks), 128 rows of 64, 128-byte-swizzled
+//           K-major, bf16 terms of 16 KiB: two, or in a record three
+//   tpb     in a record: [T; Ptil] of the backward pass, three terms
 // ---------------------------------------------------------------------------
-constexpr uint32_t kOpTP = 128 * 256;
-constexpr uint32_t kOpGates = 2048;
-constexpr uint32_t kOpBytes = kOpTP + kOpGates;             // without a record
-constexpr uint32_t kOpRecord = kOpBytes + kOpTP;            // in a record
-constexpr int kGBt = 0, kGEg = 64, kGTail = 128, kGBeta = 192, kGEnd = 256, kGHi = 260, kGLo = 324;
-constexpr uint32_t kGateFwd = 1040;                         // bytes that the forward scan takes
+constexpr uint32_t kOpGates = 2048, kOpTerm = 16384;
+constexpr uint32_t kOpBytes = kOpGates + 2 * kOpTerm;       // without a record
+constexpr uint32_t kOpBack = kOpGates + 3 * kOpTerm;        // tpb's place in a record
+constexpr uint32_t kOpRecord = kOpBack + 3 * kOpTerm;
+constexpr int kGBt = 0, kGEg = 64, kGEnd = 128, kGTail = 132, kGBeta = 196, kGHi = 260, kGLo = 324;
+constexpr uint32_t kGateFwd = 528;                          // bytes that the forward scan takes
 constexpr uint32_t kGateBwd = 784;                          // and the backward scan, from kGEg
 
 }  // namespace seqtc

@@ -3,7 +3,7 @@
 Tolerances, before any run: with u = 2^-24, a product sum of n terms is off by at most n u times the sum of the
 terms' sizes, which for a token is d_k, d_v and the 64 tokens of a chunk together; errors of earlier tokens pass
 through a recurrence that does not grow them, and a factor 8 covers their sum and the largest element against the
-root mean square.  An operand carried as two bf16 terms is off by 2^-18 of itself, below the same allowance.  A bf16
+root mean square.  An operand carried as two bf16 terms is off by 2^-16 of itself, below the same allowance.  A bf16
 output adds its rounding, 2^-8 of the value.
 """
 import numpy as np
