@@ -29,29 +29,87 @@ namespace {
 // seq_prep_kernel: That, Phat and the gates of one (chunk, head)
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
-constexpr int kLd = kChunk + 1;
+constexpr int kLd = kChunk + 4;          // fp32 rows on 16 bytes; 16-byte accesses of 8 rows meet no bank twice
 
-template <int DK>
+template <int DK, bool REC>
 struct PrepGeom {
     static constexpr uint32_t kTile = 128 * 128;                 // [K; Q], 64 columns
     static constexpr uint32_t kKQ = (DK / 64) * kTile;
-    static constexpr uint32_t kMats = 4 * kChunk * kLd * 4;      // A, T, P, L in fp32 over the tiles
+    static constexpr uint32_t kMats = (REC ? 5 : 3) * kChunk * kLd * 4;      // fp32, over the tiles
     static constexpr uint32_t kBuf = kKQ > kMats ? kKQ : ((kMats + 1023) & ~1023u);
     static constexpr uint32_t kSmem = kBuf + 2048 + 1024;
 };
 
-template <int DK>
+// (h, l) += (yh, yl), each pair the sum of a float and the rounding error of it (Knuth's two-sum)
+__device__ __forceinline__ void add2(float& h, float& l, float yh, float yl) {
+    const float s = __fadd_rn(h, yh), z = __fsub_rn(s, h);
+    const float e = __fadd_rn(__fsub_rn(h, __fsub_rn(s, z)), __fsub_rn(yh, z));
+    const float t = __fadd_rn(e, __fadd_rn(l, yl));
+    h = __fadd_rn(s, t);
+    l = __fsub_rn(t, __fsub_rn(h, s));
+}
+// y + row (16 values) times four columns (rows kLd apart)
+__device__ __forceinline__ void row16(const float* row, const float* cols, float2 (&y)[2]) {
+#pragma unroll
+    for (int k = 0; k < 16; k += 4) {
+        const float4 u = *reinterpret_cast<const float4*>(row + k);
+        const float uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float4 w = *reinterpret_cast<const float4*>(cols + (k + e) * kLd);
+            y[0] = ffma2(make_float2(uu[e], uu[e]), make_float2(w.x, w.y), y[0]);
+            y[1] = ffma2(make_float2(uu[e], uu[e]), make_float2(w.z, w.w), y[1]);
+        }
+    }
+}
+// y += (4 x 4 of u, its columns scaled by b) (4 x 4 of w)
+__device__ __forceinline__ void tile4(const float* u, const float* w, float4 b, float2 (&y)[4][2]) {
+    float4 w4[4];
+    const float bb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        w4[k] = *reinterpret_cast<const float4*>(w + k * kLd);
+        const float2 x = fmul2(make_float2(bb[k], bb[k]), make_float2(w4[k].x, w4[k].y)),
+                     z = fmul2(make_float2(bb[k], bb[k]), make_float2(w4[k].z, w4[k].w));
+        w4[k] = make_float4(x.x, x.y, z.x, z.y);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 u4 = *reinterpret_cast<const float4*>(u + i * kLd);
+        const float uu[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            y[i][0] = ffma2(make_float2(uu[k], uu[k]), make_float2(w4[k].x, w4[k].y), y[i][0]);
+            y[i][1] = ffma2(make_float2(uu[k], uu[k]), make_float2(w4[k].z, w4[k].w), y[i][1]);
+        }
+    }
+}
+// A block of 16 of T = (I + A)^-1 on the diagonal, a column for each of 16 lanes: each value found
+// takes its part from all rows below it.
+__device__ __forceinline__ void diagonal16(const float* A, float* T, int o, int lane) {
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = i == lane ? 1.f : 0.f;
+#pragma unroll
+    for (int k = 0; k < 15; ++k)
+#pragma unroll
+        for (int i = k + 1; i < 16; ++i) x[i] = fmaf(-A[(o + i) * kLd + o + k], x[k], x[i]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) T[(o + i) * kLd + o + lane] = x[i];
+}
+
+template <int DK, bool REC>
 __global__ void __launch_bounds__(kPrepThreads)
-    seq_prep_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, SeqArgs a, char* ops,
-                    uint32_t op_bytes) {
-    using G = PrepGeom<DK>;
+    seq_prep_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, SeqArgs a, char* ops) {
+    using G = PrepGeom<DK, REC>;
     extern __shared__ unsigned char raw[];
     const uint32_t r0 = smem_u32(raw), base = (r0 + 1023u) & ~1023u;
     unsigned char* sm = raw + (base - r0);
     float* A = reinterpret_cast<float*>(sm);
     float* T = A + kChunk * kLd;
     float* P = T + kChunk * kLd;
-    float* Lm = P + kChunk * kLd;
+    float* B = P + kChunk * kLd;             // with a record: diag(beta) L and its (I + B)^-1
+    float* Tb = B + kChunk * kLd;
     float* ghi = reinterpret_cast<float*>(sm + G::kBuf);
     float* glo = ghi + kChunk;
     float* bt = glo + kChunk;
@@ -82,25 +140,29 @@ __global__ void __launch_bounds__(kPrepThreads)
     }
     if (warp == 1) tmem_alloc(smem_u32(holder), 64);
     if (warp == 2) {
-        // inclusive sum of the log gates in 64 bits, kept as two floats: differences of far tokens
-        double x[2];
+        // inclusive sum of the log gates as two floats, their difference exact to 2^-48 of the sum: the
+        // exponents are differences of far tokens.  (In 64 bits this took 5 us, longer than all the rest.)
+        float xh[2], xl[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int t = lane + 32 * i;
-            x[i] = t < rows ? (double)gate_log(a.la[((size_t)first + t) * sh.H + h]) : 0.0;
+            xh[i] = t < rows ? gate_log(a.la[((size_t)first + t) * sh.H + h]) : 0.f;
+            xl[i] = 0.f;
+            bt[t] = t < rows ? a.beta[((size_t)first + t) * sh.H + h] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, x[i], o);
-                if (lane >= o) x[i] += y;
+                const float yh = __shfl_up_sync(0xffffffffu, xh[i], o), yl = __shfl_up_sync(0xffffffffu, xl[i], o);
+                if (lane >= o) add2(xh[i], xl[i], yh, yl);
             }
         }
-        x[1] += __shfl_sync(0xffffffffu, x[0], 31);
+        add2(xh[1], xl[1], __shfl_sync(0xffffffffu, xh[0], 31), __shfl_sync(0xffffffffu, xl[0], 31));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int t = lane + 32 * i;
-            ghi[t] = (float)x[i];
-            glo[t] = (float)(x[i] - (double)(float)x[i]);
-            bt[t] = t < rows ? a.beta[((size_t)first + t) * sh.H + h] : 0.f;
+            ghi[lane + 32 * i] = xh[i];
+            glo[lane + 32 * i] = xl[i];
         }
     }
     tc_fence_before();
@@ -130,113 +192,111 @@ __global__ void __launch_bounds__(kPrepThreads)
         uint32_t d[32];
         tmem_ld_n(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c0, d);
         tmem_wait_ld();
-        float* out = (warp & 2) ? P : A;
-        const int strict = (warp & 2) ? 0 : 1;
+        const bool strict = !(warp & 2);
+        float* out = strict ? A : P;
         const float gh = ghi[t], gl = glo[t];
-        float* row = out + t * kLd + c0;
+        // rows 0..31 see no column of the second half
+        const bool none = (warp & 1) == 0 && c0 != 0;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const int c = c0 + j;
-            // outside the mask the exponent may be large: it is not evaluated there.  A token past the
-            // sequence's end has beta 0 and is selected away, whatever lies in its q and k
-            float x = 0.f;
-            if (c + strict <= t && t < rows) x = __uint_as_float(d[j]) * expf((gh - ghi[c]) + (gl - glo[c]));
-            row[j] = strict ? x * bt[c] : x;
-            if (strict) Lm[t * kLd + c] = x;
+        for (int j = 0; j < 32; j += 4) {
+            float x[4] = {};
+            if (!none) {
+                const float4 ch = *reinterpret_cast<const float4*>(ghi + c0 + j), cl = *reinterpret_cast<const float4*>(glo + c0 + j),
+                             cb = *reinterpret_cast<const float4*>(bt + c0 + j);
+                const float hh[4] = {ch.x, ch.y, ch.z, ch.w}, ll[4] = {cl.x, cl.y, cl.z, cl.w}, bb[4] = {cb.x, cb.y, cb.z, cb.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = c0 + j + e;
+                    // outside the mask the exponent may be large: it is not evaluated there.  A token past the
+                    // sequence's end has beta 0 and is selected away, whatever lies in its q and k
+                    const bool in = (strict ? c < t : c <= t) && t < rows;
+                    const float ex = expf(in ? (gh - hh[e]) + (gl - ll[e]) : 0.f);
+                    x[e] = in ? __uint_as_float(d[j + e]) * ex : 0.f;
+                }
+                if (strict) {
+                    if (REC) *reinterpret_cast<float4*>(B + t * kLd + c0 + j) = make_float4(bt[t] * x[0], bt[t] * x[1], bt[t] * x[2], bt[t] * x[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] *= bb[e];
+                }
+            }
+            *reinterpret_cast<float4*>(out + t * kLd + c0 + j) = make_float4(x[0], x[1], x[2], x[3]);
         }
     }
     tc_fence_before();
     __syncthreads();
-    // That = (I + A)^-1: blocks of 16 on the diagonal by substitution, a column for each thread
-    if (lane < 16 && warp < 4) {
-        const int o = 16 * warp;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float y = i == lane ? 1.f : 0.f;
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-                if (k < i) y = fmaf(-A[(o + i) * kLd + o + k], x[k], y);
-            x[i] = y;
-            T[(o + i) * kLd + o + lane] = y;
-        }
-    } else if (warp >= 4) {
-        // above the diagonal blocks That is zero
-        for (int i = tid - 128; i < kChunk * kChunk; i += 128) {
-            const int t = i / kChunk, c = i % kChunk;
-            if (c / 16 > t / 16) T[t * kLd + c] = 0.f;
-        }
+    // That = (I + A)^-1 and, with a record, T = (I + B)^-1 by blocks of 16: first those on the diagonal
+    if (lane < 16) {
+        if (warp < 4) diagonal16(A, T, 16 * warp, lane);
+        else if (REC) diagonal16(B, Tb, 16 * (warp - 4), lane);
     }
     __syncthreads();
-    // then blocks of 32 and 64: lower left = - T22 (A21 T11); A21 T11 goes over A21
-#pragma unroll
-    for (int b = 16; b < kChunk; b *= 2) {
-        const int n = (kChunk / (2 * b)) * b * b;
-        float y[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = tid + u * kPrepThreads;
-            y[u] = 0.f;
-            if (i < n) {
-                const int blk = i / (b * b), t = (i / b) % b, c = i % b, o = blk * 2 * b;
-                for (int k = c; k < b; ++k) y[u] = fmaf(A[(o + b + t) * kLd + o + k], T[(o + k) * kLd + o + c], y[u]);
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = tid + u * kPrepThreads;
-            if (i < n) A[(i / (b * b) * 2 * b + b + (i / b) % b) * kLd + i / (b * b) * 2 * b + i % b] = y[u];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = tid + u * kPrepThreads;
-            if (i < n) {
-                const int blk = i / (b * b), t = (i / b) % b, c = i % b, o = blk * 2 * b;
-                float z = 0.f;
-                for (int k = 0; k <= t; ++k) z = fmaf(-T[(o + b + t) * kLd + o + b + k], A[(o + b + k) * kLd + o + c], z);
-                T[(o + b + t) * kLd + o + c] = z;
-            }
-        }
-        __syncthreads();
-    }
-    // Phat = (P diag(beta)) That, four rows and four columns for each thread
+    // then those below, a diagonal of them after another: T_ij = - T_ii sum_{j <= k < i} A_ik T_kj, 64
+    // threads for a block, four columns of a row each; the sum goes to A_ji's place, above the diagonal
     {
-        const int t0 = 4 * (tid / 16), c0 = 4 * (tid % 16);
-        float y[4][4] = {};
-        for (int k = c0; k < t0 + 4; ++k) {
-            float u[4], w[4];
+        const int g = tid >> 6, t = (tid >> 2) & 15, c = 4 * (tid & 3);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) u[i] = P[(t0 + i) * kLd + k] * bt[k];
+        for (int d = 1; d < 4; ++d) {
+            const int blocks = (REC ? 2 : 1) * (4 - d);
+            for (int b = g; b < blocks; b += 4) {
+                const int j = b < 4 - d ? b : b - (4 - d);
+                float *A_ = b < 4 - d ? A : B, *T_ = b < 4 - d ? T : Tb;
+                float2 y[2] = {};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = T[k * kLd + c0 + j];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[i][j] = fmaf(u[i], w[j], y[i][j]);
+                for (int k = 0; k < d; ++k) row16(A_ + (16 * (j + d) + t) * kLd + 16 * (j + k), T_ + 16 * (j + k) * kLd + 16 * j + c, y);
+                *reinterpret_cast<float4*>(A_ + (16 * j + t) * kLd + 16 * (j + d) + c) = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+            }
+            __syncthreads();
+            for (int b = g; b < blocks; b += 4) {
+                const int j = b < 4 - d ? b : b - (4 - d);
+                float *A_ = b < 4 - d ? A : B, *T_ = b < 4 - d ? T : Tb;
+                float2 y[2] = {};
+                row16(T_ + (16 * (j + d) + t) * kLd + 16 * (j + d), A_ + 16 * j * kLd + 16 * (j + d) + c, y);
+                *reinterpret_cast<float4*>(T_ + (16 * (j + d) + t) * kLd + 16 * j + c) = make_float4(-y[0].x, -y[0].y, -y[1].x, -y[1].y);
+            }
+            __syncthreads();
         }
-        // A's place is free: Phat there, P stays
+    }
+    // Phat = P diag(beta) That, with a record Ptil = P T (Phat = Ptil diag(beta) then, as
+    // diag(beta) That = T diag(beta)): four rows and four columns for each thread, to A's place
+    {
+        const int t0 = 4 * (tid >> 4), c0 = 4 * (tid & 15);
+        float2 y[4][2] = {};
+        for (int k = c0; k <= t0; k += 4)
+            tile4(P + t0 * kLd + k, (REC ? Tb : T) + k * kLd + c0,
+                  REC ? make_float4(1.f, 1.f, 1.f, 1.f) : *reinterpret_cast<const float4*>(bt + k), y);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) A[(t0 + i) * kLd + c0 + j] = y[i][j];
+            *reinterpret_cast<float4*>(A + (t0 + i) * kLd + c0) = make_float4(y[i][0].x, y[i][0].y, y[i][1].x, y[i][1].y);
     }
     __syncthreads();
-    char* op = ops + (size_t)blockIdx.x * op_bytes;
-    const bool record = op_bytes == kOpRecord;
-    const int odd = (slot - seq_slot0(sh, s)) & 1;
+    char* op = ops + (size_t)blockIdx.x * (REC ? kOpRecord : kOpBytes);
+    // eight values of a row of an operand as terms; above a triangle's blocks of 16 stands a zero
+    auto store = [&](char* image, int r, int c, const float* m, int t, const float* scale) {
+        float x[8] = {};
+        if (c / 2 <= t / 16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = (tid >> 3) + 32 * i, c = tid & 7;
-        const float* x = ((r < 64) != (odd != 0) ? T : A) + (r & 63) * kLd + 8 * c;
+            for (int j = 0; j < 8; j += 4) {
+                const float4 u = *reinterpret_cast<const float4*>(m + t * kLd + 8 * c + j);
+                x[j] = u.x; x[j + 1] = u.y; x[j + 2] = u.z; x[j + 3] = u.w;
+            }
+            if (scale != nullptr)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] *= scale[8 * c + j];
+        }
         uint32_t p[4][3];
 #pragma unroll
         for (int j = 0; j < 4; ++j) split_pair<3>(x[2 * j], x[2 * j + 1], p[j]);
-        char* at = op + kOpGates + sw_piece<128>(r, c);
 #pragma unroll
-        for (int t = 0; t < 3; ++t)
-            if (t < 2 || record) *reinterpret_cast<uint4*>(at + t * kOpTerm) = make_uint4(p[0][t], p[1][t], p[2][t], p[3][t]);
+        for (int z = 0; z < (REC ? 3 : 2); ++z)
+            *reinterpret_cast<uint4*>(image + z * kOpTerm + sw_piece<128>(r, c)) = make_uint4(p[0][z], p[1][z], p[2][z], p[3][z]);
+    };
+    const int odd = (slot - seq_slot0(sh, s)) & 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (tid >> 3) + 32 * i, c = tid & 7, t = r & 63;
+        const bool that = (r < 64) != (odd != 0);
+        store(op + kOpGates, r, c, that ? T : A, t, REC && !that ? bt : nullptr);
+        if (REC) store(op + kOpBack, r, c, r < 64 ? Tb : A, t, nullptr);
     }
     float* gates = reinterpret_cast<float*>(op);
     const float eh = ghi[rows - 1], el = glo[rows - 1];
@@ -249,45 +309,6 @@ __global__ void __launch_bounds__(kPrepThreads)
         if (tid < 4) gates[kGEnd + tid] = expf(eh + el);
         gates[kGHi + tid] = ghi[tid];
         gates[kGLo + tid] = glo[tid];
-    }
-    if (record) {
-        // the backward pass's operands: T = (I + diag(beta) L)^-1 = I - diag(beta) That L and
-        // Ptil = P T = P - Phat L, four rows of each and four columns for each thread
-        const int t0 = 4 * (tid / 16), c0 = 4 * (tid % 16);
-        float y[2][4][4] = {};
-        for (int k = c0; k < t0 + 4; ++k) {
-            float u[2][4], w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                u[0][i] = T[(t0 + i) * kLd + k];
-                u[1][i] = A[(t0 + i) * kLd + k];
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = Lm[k * kLd + c0 + j];
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) y[m][i][j] = fmaf(u[m][i], w[j], y[m][i][j]);
-        }
-        char* tpb = op + kOpBack;
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = t0 + i;
-                float x[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    x[j] = m == 0 ? (t == c0 + j ? 1.f : 0.f) - bt[t] * y[0][i][j] : P[t * kLd + c0 + j] - y[1][i][j];
-                uint32_t p[2][3];
-                split_pair<3>(x[0], x[1], p[0]);
-                split_pair<3>(x[2], x[3], p[1]);
-                char* at = tpb + sw_piece<128>(64 * m + t, c0 / 8) + (c0 & 4) * 2;
-#pragma unroll
-                for (int z = 0; z < 3; ++z) *reinterpret_cast<uint2*>(at + z * kOpTerm) = make_uint2(p[0][z], p[1][z]);
-            }
     }
     griddep_launch();
     if (warp == 1) {
@@ -1344,14 +1365,14 @@ bool qk_maps(const SeqArgs& a, CUtensorMap* q, CUtensorMap* k) {
            token_map(k, a.k, a.sh.total, a.sh.Hk * a.sh.dk, a.sh.ldk, 64, 128);
 }
 
-template <int DK>
-cudaError_t prep_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a, char* ops, uint32_t op_bytes, cudaStream_t st) {
+template <int DK, bool REC>
+cudaError_t prep_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a, char* ops, cudaStream_t st) {
     static bool done[64];
-    cudaError_t e = ensure_smem(seq_prep_kernel<DK>, PrepGeom<DK>::kSmem, done);
+    constexpr size_t smem = PrepGeom<DK, REC>::kSmem;
+    cudaError_t e = ensure_smem(seq_prep_kernel<DK, REC>, smem, done);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((size_t)seq_slots(a.sh.nseq, a.sh.total) * a.sh.H);
-    return launch_kernel(seq_prep_kernel<DK>, dim3(grid), dim3(kPrepThreads), PrepGeom<DK>::kSmem, st, false, q, k, a, ops,
-                         op_bytes);
+    return launch_kernel(seq_prep_kernel<DK, REC>, dim3(grid), dim3(kPrepThreads), smem, st, false, q, k, a, ops);
 }
 
 template <int DK, int NV, int ST>
@@ -1372,8 +1393,8 @@ cudaError_t fwd_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a,
 template <int DK>
 cudaError_t forward_dk(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a, cudaStream_t st) {
     const SeqLayout L = seq_layout(a.sh, GDN_DTYPE_BF16);
-    const cudaError_t e = a.rec != nullptr ? prep_go<DK>(q, k, a, a.rec + L.rec_op, kOpRecord, st)
-                                           : prep_go<DK>(q, k, a, a.ws + L.ws_op, kOpBytes, st);
+    const cudaError_t e = a.rec != nullptr ? prep_go<DK, true>(q, k, a, a.rec + L.rec_op, st)
+                                           : prep_go<DK, false>(q, k, a, a.ws + L.ws_op, st);
     if (e != cudaSuccess) return e;
     if (a.rec != nullptr) return seq_tc_cols(a.sh) == 32 ? fwd_go<DK, 32, 3>(q, k, a, st) : fwd_go<DK, 16, 3>(q, k, a, st);
     return seq_tc_cols(a.sh) == 32 ? fwd_go<DK, 32, 2>(q, k, a, st) : fwd_go<DK, 16, 2>(q, k, a, st);
