@@ -26,18 +26,32 @@ using namespace seqtc;
 namespace {
 
 // ---------------------------------------------------------------------------
-// seq_prep_kernel: That, Phat and the gates of one (chunk, head)
+// seq_prep_kernel: the operands and gates of one (chunk, head)
 // ---------------------------------------------------------------------------
+// K K^T and Q K^T are one product [K; Q] K^T.  (I + A)^-1 of a strictly lower A is found in two
+// blocks of 32, each by substitution, a column for each thread in registers, row after row: no step
+// waits for another thread, and what a row adds to those below it is independent of one another.
+// Phat then is a second product.  With a record T = (I + diag(beta) L)^-1 is found beside That by other
+// warps, Ptil = P T, and Phat = Ptil diag(beta) since diag(beta) That = T diag(beta).
+// Bound by the instructions of the exponentials, substitutions and splits.
 constexpr int kPrepThreads = 256;
-constexpr int kLd = kChunk + 4;          // fp32 rows on 16 bytes; 16-byte accesses of 8 rows meet no bank twice
+constexpr int kLd = kChunk + 4;          // fp32 rows on 16 bytes
 
 template <int DK, bool REC>
 struct PrepGeom {
+    static constexpr int kSides = REC ? 2 : 1;
     static constexpr uint32_t kTile = 128 * 128;                 // [K; Q], 64 columns
     static constexpr uint32_t kKQ = (DK / 64) * kTile;
-    static constexpr uint32_t kMats = (REC ? 5 : 3) * kChunk * kLd * 4;      // fp32, over the tiles
-    static constexpr uint32_t kBuf = kKQ > kMats ? kKQ : ((kMats + 1023) & ~1023u);
+    // over them: A^T (with a record diag(beta) L behind it), in its place That and T; the images of P
+    // (later of Phat), of That, and of T; Ptil's image takes the place of That and T
+    static constexpr uint32_t kMat = kChunk * kLd * 4;
+    static constexpr uint32_t kImage = 3 * 64 * 128;             // 64 rows of 64, three terms
+    static constexpr uint32_t kP = (kSides * kMat + 1023) & ~1023u;
+    static constexpr uint32_t kT = kP + kImage;
+    static constexpr uint32_t kMats = kT + kSides * kImage;
+    static constexpr uint32_t kBuf = kKQ > kMats ? kKQ : kMats;
     static constexpr uint32_t kSmem = kBuf + 2048 + 1024;
+    static_assert(kP >= (REC ? kImage : 0) && kBuf % 1024 == 0, "images");
 };
 
 // (h, l) += (yh, yl), each pair the sum of a float and the rounding error of it (Knuth's two-sum)
@@ -48,74 +62,22 @@ __device__ __forceinline__ void add2(float& h, float& l, float yh, float yl) {
     h = __fadd_rn(s, t);
     l = __fsub_rn(t, __fsub_rn(h, s));
 }
-// y + row (16 values) times four columns (rows kLd apart)
-__device__ __forceinline__ void row16(const float* row, const float* cols, float2 (&y)[2]) {
-#pragma unroll
-    for (int k = 0; k < 16; k += 4) {
-        const float4 u = *reinterpret_cast<const float4*>(row + k);
-        const float uu[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float4 w = *reinterpret_cast<const float4*>(cols + (k + e) * kLd);
-            y[0] = ffma2(make_float2(uu[e], uu[e]), make_float2(w.x, w.y), y[0]);
-            y[1] = ffma2(make_float2(uu[e], uu[e]), make_float2(w.z, w.w), y[1]);
-        }
-    }
-}
-// y += (4 x 4 of u, its columns scaled by b) (4 x 4 of w)
-__device__ __forceinline__ void tile4(const float* u, const float* w, float4 b, float2 (&y)[4][2]) {
-    float4 w4[4];
-    const float bb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        w4[k] = *reinterpret_cast<const float4*>(w + k * kLd);
-        const float2 x = fmul2(make_float2(bb[k], bb[k]), make_float2(w4[k].x, w4[k].y)),
-                     z = fmul2(make_float2(bb[k], bb[k]), make_float2(w4[k].z, w4[k].w));
-        w4[k] = make_float4(x.x, x.y, z.x, z.y);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 u4 = *reinterpret_cast<const float4*>(u + i * kLd);
-        const float uu[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            y[i][0] = ffma2(make_float2(uu[k], uu[k]), make_float2(w4[k].x, w4[k].y), y[i][0]);
-            y[i][1] = ffma2(make_float2(uu[k], uu[k]), make_float2(w4[k].z, w4[k].w), y[i][1]);
-        }
-    }
-}
-// A block of 16 of T = (I + A)^-1 on the diagonal, a column for each of 16 lanes: each value found
-// takes its part from all rows below it.
-__device__ __forceinline__ void diagonal16(const float* A, float* T, int o, int lane) {
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = i == lane ? 1.f : 0.f;
-#pragma unroll
-    for (int k = 0; k < 15; ++k)
-#pragma unroll
-        for (int i = k + 1; i < 16; ++i) x[i] = fmaf(-A[(o + i) * kLd + o + k], x[k], x[i]);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) T[(o + i) * kLd + o + lane] = x[i];
-}
 
 template <int DK, bool REC>
-__global__ void __launch_bounds__(kPrepThreads)
+__global__ void __launch_bounds__(kPrepThreads, REC ? 2 : 3)
     seq_prep_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, SeqArgs a, char* ops) {
     using G = PrepGeom<DK, REC>;
+    constexpr uint32_t kHalf = 64 * 128;                  // one term of an image
     extern __shared__ unsigned char raw[];
     const uint32_t r0 = smem_u32(raw), base = (r0 + 1023u) & ~1023u;
     unsigned char* sm = raw + (base - r0);
-    float* A = reinterpret_cast<float*>(sm);
-    float* T = A + kChunk * kLd;
-    float* P = T + kChunk * kLd;
-    float* B = P + kChunk * kLd;             // with a record: diag(beta) L and its (I + B)^-1
-    float* Tb = B + kChunk * kLd;
+    float* M = reinterpret_cast<float*>(sm);              // A^T, then That; behind it diag(beta) L, then T
     float* ghi = reinterpret_cast<float*>(sm + G::kBuf);
     float* glo = ghi + kChunk;
     float* bt = glo + kChunk;
     uint32_t* holder = reinterpret_cast<uint32_t*>(bt + kChunk);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
-    const uint32_t bar = base + G::kBuf + 1024, bar2 = bar + 8;
+    const uint32_t bar = base + G::kBuf + 1024, bar2 = bar + 8, bar3 = bar + 16;
 
     const SeqShape& sh = a.sh;
     const int h = blockIdx.x % sh.H, slot = blockIdx.x / sh.H, hk = h / (sh.H / sh.Hk);
@@ -128,6 +90,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     if (tid == 0) {
         mbar_init(bar, 1);
         mbar_init(bar2, 1);
+        mbar_init(bar3, 1);
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         fence_proxy_async_smem();
@@ -138,7 +101,7 @@ __global__ void __launch_bounds__(kPrepThreads)
             tma_2d(base + b * G::kTile + 8192, &tmQ, hk * DK + 64 * b, first, bar);
         }
     }
-    if (warp == 1) tmem_alloc(smem_u32(holder), 64);
+    if (warp == 1) tmem_alloc(smem_u32(holder), 128);
     if (warp == 2) {
         // inclusive sum of the log gates as two floats, their difference exact to 2^-48 of the sum: the
         // exponents are differences of far tokens.  (In 64 bits this took 5 us, longer than all the rest.)
@@ -170,151 +133,220 @@ __global__ void __launch_bounds__(kPrepThreads)
     tc_fence_after();
     const uint32_t tmem = warp_uniform(*holder);
     if (warp == 0) {
-        const bool here = wait_or_dead(bar, 0, a.err, dead);
+        wait_or_dead(bar, 0, a.err, dead);
         __syncwarp();
         if (elect_one()) {
             const uint64_t d = k_desc<128>(base);
-            if (here)
 #pragma unroll
-                for (int k = 0; k < DK / 16; ++k) {
-                    const uint64_t t = d + (((k / 4) * G::kTile + 32 * (k % 4)) >> 4);
-                    mma_bf16(tmem, t, t, idesc_bf16(128, 64), k != 0);
-                }
+            for (int k = 0; k < DK / 16; ++k) {
+                const uint64_t t = d + (((k / 4) * G::kTile + 32 * (k % 4)) >> 4);
+                mma_bf16(tmem, t, t, idesc_bf16(128, 64), k != 0);
+            }
             mma_commit(bar2);
         }
+    }
+    // the gates, while the product runs
+    char* op = ops + (size_t)blockIdx.x * (REC ? kOpRecord : kOpBytes);
+    if (tid >= 64 && tid < 128) {
+        const int t = tid - 64;
+        float* gates = reinterpret_cast<float*>(op);
+        const float eh = ghi[rows - 1], el = glo[rows - 1], tail = expf((eh - ghi[t]) + (el - glo[t]));
+        gates[kGBt + t] = bt[t] * tail;
+        gates[kGEg + t] = expf(ghi[t] + glo[t]);
+        gates[kGTail + t] = tail;
+        gates[kGBeta + t] = bt[t];
+        if (t < 4) gates[kGEnd + t] = expf(eh + el);
+        gates[kGHi + t] = ghi[t];
+        gates[kGLo + t] = glo[t];
     }
     wait_or_dead(bar2, 0, a.err, dead);
     __syncwarp();
     tc_fence_after();
-    // row t of K K^T (lanes 0..63) and of Q K^T (lanes 64..127); 32 columns for each half of the warps
+    // row t of K K^T (lanes 0..63) and of Q K^T (lanes 64..127); 32 columns for each half of the warps,
+    // eight at a time (a loop: code that runs once a chunk costs its fetches)
     {
         const int t = 32 * (warp & 1) + lane, c0 = 32 * (warp >> 2);
-        uint32_t d[32];
-        tmem_ld_n(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c0, d);
-        tmem_wait_ld();
         const bool strict = !(warp & 2);
-        float* out = strict ? A : P;
-        const float gh = ghi[t], gl = glo[t];
-        // rows 0..31 see no column of the second half
+        const float gh = ghi[t], gl = glo[t], bb = bt[t];
+        // rows 0..31 see no column of the second half; a token past the sequence's end sees none, whatever
+        // lies in its q and k
+        const int seen = t < rows ? t + (strict ? 0 : 1) : 0;
         const bool none = (warp & 1) == 0 && c0 != 0;
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            float x[4] = {};
+#pragma unroll 1
+        for (int j = c0; j < c0 + 32; j += 8) {
+            float x[8] = {};
             if (!none) {
-                const float4 ch = *reinterpret_cast<const float4*>(ghi + c0 + j), cl = *reinterpret_cast<const float4*>(glo + c0 + j),
-                             cb = *reinterpret_cast<const float4*>(bt + c0 + j);
-                const float hh[4] = {ch.x, ch.y, ch.z, ch.w}, ll[4] = {cl.x, cl.y, cl.z, cl.w}, bb[4] = {cb.x, cb.y, cb.z, cb.w};
+                uint32_t d[8];
+                tmem_ld_n(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + j, d);
+                const float4 h0 = *reinterpret_cast<const float4*>(ghi + j), h1 = *reinterpret_cast<const float4*>(ghi + j + 4),
+                             l0 = *reinterpret_cast<const float4*>(glo + j), l1 = *reinterpret_cast<const float4*>(glo + j + 4);
+                const float hh[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w}, ll[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
+                tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int c = c0 + j + e;
-                    // outside the mask the exponent may be large: it is not evaluated there.  A token past the
-                    // sequence's end has beta 0 and is selected away, whatever lies in its q and k
-                    const bool in = (strict ? c < t : c <= t) && t < rows;
+                for (int e = 0; e < 8; ++e) {
+                    // outside the mask the exponent may be large: it is not evaluated there
+                    const bool in = j + e < seen;
                     const float ex = expf(in ? (gh - hh[e]) + (gl - ll[e]) : 0.f);
-                    x[e] = in ? __uint_as_float(d[j + e]) * ex : 0.f;
-                }
-                if (strict) {
-                    if (REC) *reinterpret_cast<float4*>(B + t * kLd + c0 + j) = make_float4(bt[t] * x[0], bt[t] * x[1], bt[t] * x[2], bt[t] * x[3]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] *= bb[e];
+                    x[e] = in ? __uint_as_float(d[e]) * ex : 0.f;
                 }
             }
-            *reinterpret_cast<float4*>(out + t * kLd + c0 + j) = make_float4(x[0], x[1], x[2], x[3]);
+            const float4 b0 = *reinterpret_cast<const float4*>(bt + j), b1 = *reinterpret_cast<const float4*>(bt + j + 4);
+            const float be[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+            if (strict) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    M[(j + e) * kLd + t] = x[e] * be[e];
+                    if (REC) M[kChunk * kLd + (j + e) * kLd + t] = x[e] * bb;
+                }
+            } else {
+                if (!REC)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= be[e];
+                put_terms<128, 3>(base + G::kP, kHalf, t, j, x);
+            }
         }
     }
     tc_fence_before();
     __syncthreads();
-    // That = (I + A)^-1 and, with a record, T = (I + B)^-1 by blocks of 16: first those on the diagonal
-    if (lane < 16) {
-        if (warp < 4) diagonal16(A, T, 16 * warp, lane);
-        else if (REC) diagonal16(B, Tb, 16 * (warp - 4), lane);
+    // (I + A)^-1 in two steps: by substitution the blocks of 32 on the diagonal, a column of one for each
+    // of 64 threads (128 with a record), two rows an instruction ...
+    const bool solves = warp < 2 * G::kSides;
+    float* mine = M + (warp >> 1) * kChunk * kLd;
+    {
+        const int o = warp & 1 ? 32 : 0;
+        float2 x[16];
+        if (solves) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = make_float2(2 * i == lane ? 1.f : 0.f, 2 * i + 1 == lane ? 1.f : 0.f);
+            const float* m = mine + o * kLd + o;
+#pragma unroll
+            for (int k = 0; k < 31; ++k) {
+                const float xk = k & 1 ? x[k / 2].y : x[k / 2].x;
+                const float2 nx = make_float2(-xk, -xk);
+#pragma unroll
+                for (int i = (k + 1) & ~3; i < 32; i += 4) {      // rows up to k in the first four meet zeros
+                    const float4 w = *reinterpret_cast<const float4*>(m + k * kLd + i);
+                    if (i + 1 > k) x[i / 2] = ffma2(make_float2(w.x, w.y), nx, x[i / 2]);
+                    x[i / 2 + 1] = ffma2(make_float2(w.z, w.w), nx, x[i / 2 + 1]);
+                }
+            }
+        }
+        // ... each into its place (in rows now; the transposed A21 in the upper right stays) ...
+        __syncwarp();
+        if (solves)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                mine[(o + 2 * i) * kLd + o + lane] = x[i].x;
+                mine[(o + 2 * i + 1) * kLd + o + lane] = x[i].y;
+            }
     }
     __syncthreads();
-    // then those below, a diagonal of them after another: T_ij = - T_ii sum_{j <= k < i} A_ik T_kj, 64
-    // threads for a block, four columns of a row each; the sum goes to A_ji's place, above the diagonal
+    // ... then T21 = - T22 (A21 T11), four columns of a row for each thread
     {
-        const int g = tid >> 6, t = (tid >> 2) & 15, c = 4 * (tid & 3);
+        const int t = (tid >> 3) & 31, c = 4 * (tid & 7);
+        float2 y[G::kSides][2] = {};
 #pragma unroll
-        for (int d = 1; d < 4; ++d) {
-            const int blocks = (REC ? 2 : 1) * (4 - d);
-            for (int b = g; b < blocks; b += 4) {
-                const int j = b < 4 - d ? b : b - (4 - d);
-                float *A_ = b < 4 - d ? A : B, *T_ = b < 4 - d ? T : Tb;
-                float2 y[2] = {};
-#pragma unroll
-                for (int k = 0; k < d; ++k) row16(A_ + (16 * (j + d) + t) * kLd + 16 * (j + k), T_ + 16 * (j + k) * kLd + 16 * j + c, y);
-                *reinterpret_cast<float4*>(A_ + (16 * j + t) * kLd + 16 * (j + d) + c) = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+        for (int z = 0; z < G::kSides; ++z) {
+            float* m = M + z * kChunk * kLd;
+#pragma unroll 8
+            for (int k = 0; k < 32; ++k) {
+                const float u = m[k * kLd + 32 + t];              // A21[t][k], transposed
+                const float4 w = *reinterpret_cast<const float4*>(m + k * kLd + c);
+                y[z][0] = ffma2(make_float2(u, u), make_float2(w.x, w.y), y[z][0]);
+                y[z][1] = ffma2(make_float2(u, u), make_float2(w.z, w.w), y[z][1]);
             }
-            __syncthreads();
-            for (int b = g; b < blocks; b += 4) {
-                const int j = b < 4 - d ? b : b - (4 - d);
-                float *A_ = b < 4 - d ? A : B, *T_ = b < 4 - d ? T : Tb;
-                float2 y[2] = {};
-                row16(T_ + (16 * (j + d) + t) * kLd + 16 * (j + d), A_ + 16 * j * kLd + 16 * (j + d) + c, y);
-                *reinterpret_cast<float4*>(T_ + (16 * (j + d) + t) * kLd + 16 * j + c) = make_float4(-y[0].x, -y[0].y, -y[1].x, -y[1].y);
-            }
-            __syncthreads();
         }
-    }
-    // Phat = P diag(beta) That, with a record Ptil = P T (Phat = Ptil diag(beta) then, as
-    // diag(beta) That = T diag(beta)): four rows and four columns for each thread, to A's place
-    {
-        const int t0 = 4 * (tid >> 4), c0 = 4 * (tid & 15);
-        float2 y[4][2] = {};
-        for (int k = c0; k <= t0; k += 4)
-            tile4(P + t0 * kLd + k, (REC ? Tb : T) + k * kLd + c0,
-                  REC ? make_float4(1.f, 1.f, 1.f, 1.f) : *reinterpret_cast<const float4*>(bt + k), y);
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4*>(A + (t0 + i) * kLd + c0) = make_float4(y[i][0].x, y[i][0].y, y[i][1].x, y[i][1].y);
+        for (int z = 0; z < G::kSides; ++z)
+            *reinterpret_cast<float4*>(M + z * kChunk * kLd + t * kLd + 32 + c) = make_float4(y[z][0].x, y[z][0].y, y[z][1].x, y[z][1].y);
+        __syncthreads();
+#pragma unroll
+        for (int z = 0; z < G::kSides; ++z) {
+            float* m = M + z * kChunk * kLd;
+            y[z][0] = y[z][1] = make_float2(0.f, 0.f);
+#pragma unroll 8
+            for (int k = 0; k < 32; ++k) {
+                const float u = -m[(32 + t) * kLd + 32 + k];
+                const float4 w = *reinterpret_cast<const float4*>(m + k * kLd + 32 + c);
+                y[z][0] = ffma2(make_float2(u, u), make_float2(w.x, w.y), y[z][0]);
+                y[z][1] = ffma2(make_float2(u, u), make_float2(w.z, w.w), y[z][1]);
+            }
+            *reinterpret_cast<float4*>(m + (32 + t) * kLd + c) = make_float4(y[z][0].x, y[z][0].y, y[z][1].x, y[z][1].y);
+        }
     }
     __syncthreads();
-    char* op = ops + (size_t)blockIdx.x * (REC ? kOpRecord : kOpBytes);
-    // eight values of a row of an operand as terms; above a triangle's blocks of 16 stands a zero
-    auto store = [&](char* image, int r, int c, const float* m, int t, const float* scale) {
-        float x[8] = {};
-        if (c / 2 <= t / 16) {
+    // That (and T) as operands
+#pragma unroll 1
+    for (int i = 0; i < 2 * G::kSides; ++i) {
+        const int r = (tid >> 3) + 32 * (i & 1), c = tid & 7;
+        const float* m = M + (i >> 1) * kChunk * kLd + r * kLd + 8 * c;
+        const float4 u = *reinterpret_cast<const float4*>(m), w = *reinterpret_cast<const float4*>(m + 4);
+        float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+        if (r < 32 && c >= 4)                             // above the diagonal blocks
 #pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-                const float4 u = *reinterpret_cast<const float4*>(m + t * kLd + 8 * c + j);
-                x[j] = u.x; x[j + 1] = u.y; x[j + 2] = u.z; x[j + 3] = u.w;
-            }
-            if (scale != nullptr)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] *= scale[8 * c + j];
-        }
-        uint32_t p[4][3];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) split_pair<3>(x[2 * j], x[2 * j + 1], p[j]);
-#pragma unroll
-        for (int z = 0; z < (REC ? 3 : 2); ++z)
-            *reinterpret_cast<uint4*>(image + z * kOpTerm + sw_piece<128>(r, c)) = make_uint4(p[0][z], p[1][z], p[2][z], p[3][z]);
-    };
+            for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        put_terms<128, 3>(base + G::kT + (i >> 1) * G::kImage, kHalf, r, 8 * c, v);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
     const int odd = (slot - seq_slot0(sh, s)) & 1;
+    if (warp == 0) {
+        if (elect_one()) {
+            // P's 64 rows and whatever lies behind (lanes that nothing reads), term t with the first 3 - t
+            // of the other, the small products first
+            const uint64_t dP = k_desc<128>(base + G::kP), dT = mn_desc<128>(base + G::kT + (REC ? G::kImage : 0), 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = (tid >> 3) + 32 * i, c = tid & 7, t = r & 63;
-        const bool that = (r < 64) != (odd != 0);
-        store(op + kOpGates, r, c, that ? T : A, t, REC && !that ? bt : nullptr);
-        if (REC) store(op + kOpBack, r, c, r < 64 ? Tb : A, t, nullptr);
+            for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+                for (int t = 0; t <= sum; ++t)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(tmem + 64, dP + ((t * kHalf + 32 * k) >> 4), dT + (((sum - t) * kHalf + k * 2048) >> 4),
+                                 idesc_bf16(128, 64) | kBMn, sum != 2 || t + k != 0);
+            mma_commit(bar3);
+            // the operands' halves are 64 rows of each term
+#pragma unroll
+            for (int z = 0; z < (REC ? 3 : 2); ++z) bulk_s2g(op + kOpGates + z * kOpTerm + (odd ? kHalf : 0), base + G::kT + z * kHalf, kHalf);
+            if (REC)
+#pragma unroll
+                for (int z = 0; z < 3; ++z) bulk_s2g(op + kOpBack + z * kOpTerm, base + G::kT + G::kImage + z * kHalf, kHalf);
+        }
+        __syncwarp();
     }
-    float* gates = reinterpret_cast<float*>(op);
-    const float eh = ghi[rows - 1], el = glo[rows - 1];
-    if (tid < 64) {
-        const float tail = expf((eh - ghi[tid]) + (el - glo[tid]));
-        gates[kGBt + tid] = bt[tid] * tail;
-        gates[kGEg + tid] = expf(ghi[tid] + glo[tid]);
-        gates[kGTail + tid] = tail;
-        gates[kGBeta + tid] = bt[tid];
-        if (tid < 4) gates[kGEnd + tid] = expf(eh + el);
-        gates[kGHi + tid] = ghi[tid];
-        gates[kGLo + tid] = glo[tid];
+    wait_or_dead(bar3, 0, a.err, dead);
+    __syncwarp();
+    tc_fence_after();
+    if ((warp & 2) == 0) {
+        const int t = 32 * (warp & 1) + lane, c0 = 32 * (warp >> 2);
+        float y[32];
+        tmem_sum<32, 1>(tmem + 64 + ((uint32_t)(32 * (warp & 3)) << 16) + c0, 0, y);
+        if (REC) {
+            put_terms<128, 3>(base, kHalf, t, c0, y);     // over That and T, which the images hold
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] *= bt[c0 + j];
+        }
+        put_terms<128, REC ? 3 : 2>(base + G::kP, kHalf, t, c0, y);
     }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0 && elect_one()) {
+#pragma unroll
+        for (int z = 0; z < (REC ? 3 : 2); ++z) bulk_s2g(op + kOpGates + z * kOpTerm + (odd ? 0 : kHalf), base + G::kP + z * kHalf, kHalf);
+        if (REC)
+#pragma unroll
+            for (int z = 0; z < 3; ++z) bulk_s2g(op + kOpBack + z * kOpTerm + kHalf, base + z * kHalf, kHalf);
+        bulk_all_done();
+    }
+    __syncwarp();
     griddep_launch();
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem, 64);
+        tmem_dealloc(tmem, 128);
     }
 }
 
