@@ -95,7 +95,7 @@ struct SeqArgs {
 // call's sizes and type take.
 struct SeqLayout {
     size_t rec_S, rec_eps, rec_o, rec_op, rec_total;     // record: chunk start states, errors, outputs, chunk operands
-    size_t ws_dS, ws_dV, ws_dq, ws_dk, ws_op, ws_part, ws_phi, ws_total;   // workspace
+    size_t ws_dS, ws_dV, ws_dq, ws_dk, ws_op, ws_part, ws_phi, ws_ysum, ws_total;   // workspace
 };
 
 SeqLayout seq_layout(const SeqShape& s, int dtype);

@@ -611,8 +611,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 for (int j = 0; j < NH; ++j) x[j] = bt * y[j];
                 put_terms<W, 3>(base + G::kR, G::kRTerm, tok, vc, x);
                 operand_ready(3, 160);
-                if constexpr (ST == 3) {                  // eps as three bf16 terms [3][64][dv]
-                    char* e = recE + ((slot0 + c) * sh.H + h) * (size_t)(3 * kChunk * 2) * sh.dv + ((size_t)tok * sh.dv + v0 + vc) * 2;
+                if constexpr (ST == 3) {                  // eps as three bf16 terms, operands of 64 rows
+                    char* e = recE + (((slot0 + c) * sh.H + h) * tiles + tile) * (size_t)(3 * kChunk * W);
 #pragma unroll
                     for (int i = 0; i < NH / 8; ++i) {
                         uint32_t p[4][3];
@@ -620,12 +620,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         for (int j = 0; j < 4; ++j) split_pair<3>(y[8 * i + 2 * j], y[8 * i + 2 * j + 1], p[j]);
 #pragma unroll
                         for (int t = 0; t < 3; ++t)
-                            *reinterpret_cast<uint4*>(e + (size_t)t * kChunk * 2 * sh.dv + 16 * i) = make_uint4(p[0][t], p[1][t], p[2][t], p[3][t]);
+                            *reinterpret_cast<uint4*>(e + t * kChunk * W + sw_piece<W>(tok, vc / 8 + i)) = make_uint4(p[0][t], p[1][t], p[2][t], p[3][t]);
                     }
                 }
             } else {
                 __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + (((size_t)first + c * kChunk + tok) * sh.H + h) * sh.dv + v0 + vc;
-                float* e = recO + ((slot0 + c) * sh.H + h) * (size_t)kChunk * sh.dv + (size_t)tok * sh.dv + v0 + vc;
+                float* e = recO + (((slot0 + c) * sh.H + h) * tiles + tile) * (size_t)(kChunk * NV) + tok * NV + vc;
 #pragma unroll
                 for (int j = 0; j < NH; ++j) y[j] = fmaf(eg, x[j], y[j]);
 #pragma unroll
@@ -678,7 +678,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 // The gates' gradients are dots over d_v and come from here, where w and dS are fp32:
 //   dbeta_t = w_t.eps_t,   dlog_alpha_t = dlog_alpha_{t+1} + dO_t.o_t - dV_t.v_t,
 // the second since <S_t, dS_t> changes from token to token by just these; its value at a chunk's
-// first token is <S, dS>, S the chunk's start state.  Each CTA writes its columns' parts.
+// first token is <S, dS>, S the chunk's start state, which every kAnchor-th chunk takes (S has to be
+// read for it), the others from the sums between.  Each CTA writes its columns' parts.
+constexpr int kAnchor = 8;
+
 template <int DK, int NV>
 struct BwdGeom {
     static constexpr int kMH = DK > 128 ? 2 : 1;
@@ -714,7 +717,7 @@ template <int DK, int NV>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     seq_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmO, SeqArgs a, const char* ops, const char* recS, const char* recE, const float* recO,
-                   char* wsS, char* wsV, float* part, float* phi) {
+                   char* wsS, char* wsV, float* part, float* phi, float* ysum) {
     using G = BwdGeom<DK, NV>;
     constexpr int W = G::kW, NH = NV / 2;
     constexpr int SC = G::kMH == 2 ? NV : NH;
@@ -929,20 +932,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 put_terms<W, 3>(base + G::kE, G::kRTerm, tok, vc, x);
             }
             operand_ready(1, 288);
-            if (i > 0) state_dot(c + 1);
+            if (i > 0 && (c + 1) % kAnchor == 0) state_dot(c + 1);
             // eps (three terms), o, v and dO of this thread's token and columns
             // (from the stage now: it may be filled again once the last product is done)
             uint4 te[3][NH / 8], to[NH / 4], tv[NH / 8], td[NH / 8];
             if (!reads_k) {
-                const size_t at = (slot0 + c) * sh.H + h, row = (size_t)tok * sh.dv + v0 + vc;
+                const size_t at = ((slot0 + c) * sh.H + h) * tiles + tile;
                 const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + ((size_t)first + c * kChunk + tok) * sh.ldv + (size_t)h * sh.dv + v0 + vc;
 #pragma unroll
                 for (int p = 0; p < NH / 8; ++p) {
 #pragma unroll
                     for (int t = 0; t < 3; ++t)
-                        te[t][p] = *reinterpret_cast<const uint4*>(recE + ((at * 3 + t) * kChunk * sh.dv + row) * 2 + 16 * p);
+                        te[t][p] = *reinterpret_cast<const uint4*>(recE + (at * 3 + t) * (kChunk * W) + sw_piece<W>(tok, vc / 8 + p));
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) to[2 * p + t] = *reinterpret_cast<const uint4*>(recO + at * kChunk * sh.dv + row + 8 * p + 4 * t);
+                    for (int t = 0; t < 2; ++t) to[2 * p + t] = *reinterpret_cast<const uint4*>(recO + at * (kChunk * NV) + tok * NV + vc + 8 * p + 4 * t);
                     tv[p] = make_uint4(0, 0, 0, 0);
                     if (tok < rows) tv[p] = *reinterpret_cast<const uint4*>(vp + 8 * p);
                     td[p] = *reinterpret_cast<const uint4*>(sm + st + G::kO + sw_piece<W>(tok, vc / 8 + p));
@@ -977,7 +980,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 put_terms<W, 3>(base + G::kR, G::kRTerm, tok, vc, x);
                 operand_ready(3, 160);
             } else {
-                char* e = wsV + ((slot0 + c) * sh.H + h) * (size_t)(2 * kChunk * 2) * sh.dv + ((size_t)tok * sh.dv + v0 + vc) * 2;
+                char* e = wsV + (((slot0 + c) * sh.H + h) * tiles + tile) * (size_t)(2 * kChunk * W);
                 __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.dv) + (((size_t)first + c * kChunk + tok) * sh.H + h) * sh.dv + v0 + vc;
                 float db = 0.f, dl = 0.f;
 #pragma unroll
@@ -997,13 +1000,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         split_pair<2>(x[8 * p + 2 * j], x[8 * p + 2 * j + 1], u[j]);
                     }
                     const uint4 hi = make_uint4(u[0][0], u[1][0], u[2][0], u[3][0]);
-                    *reinterpret_cast<uint4*>(e + 16 * p) = hi;
-                    *reinterpret_cast<uint4*>(e + (size_t)kChunk * 2 * sh.dv + 16 * p) = make_uint4(u[0][1], u[1][1], u[2][1], u[3][1]);
+                    *reinterpret_cast<uint4*>(e + sw_piece<W>(tok, vc / 8 + p)) = hi;
+                    *reinterpret_cast<uint4*>(e + kChunk * W + sw_piece<W>(tok, vc / 8 + p)) = make_uint4(u[0][1], u[1][1], u[2][1], u[3][1]);
                     if (tok < rows) *reinterpret_cast<uint4*>(o + 8 * p) = hi;
                 }
                 float* q = part + ((((slot0 + c) * sh.H + h) * tiles + tile) * 2 + wg) * (2 * kChunk) + tok;
                 q[0] = db;
                 q[kChunk] = dl;
+                dl = warp_sum(dl);
+                if (lane == 0) ysum[(((slot0 + c) * sh.H + h) * tiles + tile) * 4 + 2 * wg + (w4 & 1)] = dl;
             }
             __syncwarp();
             wait_or_dead(b3, ph, a.err, dead);
@@ -1057,8 +1062,8 @@ struct GradGeom {
     static constexpr uint32_t kImg = 5 * kBlk;
     static constexpr uint32_t kSlot = kImg + 2 * DK * kW;
     static constexpr uint32_t kGates = kSlot0 + 2 * kSlot;
-    static constexpr uint32_t kMisc = kGates + kOpGates;          // 64 floats
-    static constexpr uint32_t kBar = kMisc + 256;
+    static constexpr uint32_t kMisc = kGates + kOpGates;          // a pair of floats
+    static constexpr uint32_t kBar = kMisc + 16;
     static constexpr uint32_t kUsed = kBar + 256 + 1024;
     static constexpr uint32_t kSmem = kUsed > 116 * 1024 ? kUsed : 116 * 1024;      // one CTA per SM: it takes the whole TMEM
     static constexpr int kDa = 0, kDw = DK, kE = 2 * DK <= 256 ? 256 : 0;
@@ -1068,9 +1073,8 @@ struct GradGeom {
 template <int DK, int NV>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     seq_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmE,
-                    const __grid_constant__ CUtensorMap tmV, SeqArgs a, const char* ops, const char* recS, const char* wsS,
-                    const float* part, const float* phi, float* dqf, float* dkf) {
+                    const __grid_constant__ CUtensorMap tmO, SeqArgs a, const char* ops, const char* recS, const char* recE,
+                    const char* wsS, const char* wsV, const float* part, const float* phi, const float* ysum, float* dqf, float* dkf) {
     using G = GradGeom<DK, NV>;
     constexpr int W = G::kW, HC = DK / 2;                 // HC: columns of d_k of a thread
     extern __shared__ unsigned char raw[];
@@ -1113,7 +1117,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 for (int r = 0; r < rep && ok; ++r, ++n) {
                     const int h = hk * rep + r;
                     const size_t sh_at = (size_t)(item / sh.Hk) * sh.H + h;
-                    const int erow = (int)(sh_at * 3 * kChunk), vrow = (int)(sh_at * 2 * kChunk);
                     if (n >= 1 && !(ok = wait_or_dead(kqe, (n - 1) & 1, a.err, dead))) break;
                     mbar_expect_tx(kqf, 2 * DK * 128 + kOpGates);
 #pragma unroll
@@ -1126,23 +1129,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         const uint32_t sl = base + G::kSlot0 + (it & 1) * G::kSlot, f = full0 + 8 * (it & 1);
                         if (it >= 2 && !(ok = wait_or_dead(empty0 + 8 * (it & 1), ((it >> 1) & 1) ^ 1, a.err, dead))) break;
                         const int v = (j < tiles ? j : (j - tiles) >> 1), v0 = v * NV;
+                        const char *e = recE + (sh_at * tiles + v) * (3 * G::kBlk), *w = wsV + (sh_at * tiles + v) * (2 * G::kBlk);
                         if (j < tiles || ((j - tiles) & 1) == 0) {
                             mbar_expect_tx(f, 3 * G::kBlk + (j < tiles ? 2 * G::kBlk : 2 * DK * W));
                             tma_2d(sl, &tmO, h * sh.dv + v0, first, f);
-                            tma_2d(sl + G::kBlk, &tmV, v0, vrow, f);
-                            tma_2d(sl + 3 * G::kBlk, &tmV, v0, vrow + kChunk, f);
+                            bulk_copy_g2s(sl + G::kBlk, w, G::kBlk, f);
+                            bulk_copy_g2s(sl + 3 * G::kBlk, w + G::kBlk, G::kBlk, f);
                             if (j < tiles) {
-                                tma_2d(sl + G::kImg, &tmE, v0, erow, f);
-                                tma_2d(sl + G::kImg + G::kBlk, &tmE, v0, erow + kChunk, f);
+                                bulk_copy_g2s(sl + G::kImg, e, 2 * G::kBlk, f);
                             } else {
                                 bulk_copy_g2s(sl + G::kImg, recS + (sh_at * tiles + v) * (3 * DK * W), 2 * DK * W, f);
                             }
                         } else {
                             mbar_expect_tx(f, 4 * G::kBlk + 2 * DK * W);
-                            tma_2d(sl, &tmE, v0, erow, f);
-                            tma_2d(sl + G::kBlk, &tmE, v0, erow, f);
-                            tma_2d(sl + 3 * G::kBlk, &tmE, v0, erow + kChunk, f);
-                            tma_2d(sl + 4 * G::kBlk, &tmE, v0, erow + kChunk, f);
+                            bulk_copy_g2s(sl, e, G::kBlk, f);
+                            bulk_copy_g2s(sl + G::kBlk, e, G::kBlk, f);
+                            bulk_copy_g2s(sl + 3 * G::kBlk, e + G::kBlk, G::kBlk, f);
+                            bulk_copy_g2s(sl + 4 * G::kBlk, e + G::kBlk, G::kBlk, f);
                             bulk_copy_g2s(sl + G::kImg, wsS + (sh_at * tiles + v) * (2 * DK * W), 2 * DK * W, f);
                         }
                     }
@@ -1240,23 +1243,66 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             for (int r = 0; r < rep; ++r, ++n) {
                 const int h = hk * rep + r;
                 const size_t sh_at = (size_t)(item / sh.Hk) * sh.H + h;
-                double dla = 0.0;
-                if (tid < kChunk) {
-                    // dbeta, and the terms of dlog_alpha
-                    const float* q = part + sh_at * tiles * (4 * kChunk) + tid;
-                    float db = 0.f, dl = 0.f;
-                    for (int j = 0; j < 2 * tiles; ++j) {
-                        db += q[j * 2 * kChunk];
-                        dl += q[j * 2 * kChunk + kChunk];
+                if (warp == 7) {
+                    // <S, dS> at the chunk's first token, from the anchor before it
+                    const int c = item / sh.Hk - seq_slot0(sh, s), back = c % kAnchor;
+                    const float *p = phi + (sh_at - (size_t)back * sh.H) * tiles * 8, *y = ysum + (sh_at - (size_t)back * sh.H) * tiles * 4;
+                    float ph = 0.f, pl = 0.f;
+                    for (int j = lane; j < 8 * tiles; j += 32) add2(ph, pl, p[j], 0.f);
+                    for (int i = 0; i < back; ++i)
+                        for (int j = lane; j < 4 * tiles; j += 32) add2(ph, pl, -y[(size_t)i * sh.H * tiles * 4 + j], 0.f);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) {
+                        const float qh = __shfl_xor_sync(0xffffffffu, ph, o), ql = __shfl_xor_sync(0xffffffffu, pl, o);
+                        add2(ph, pl, qh, ql);
                     }
-                    ys[tid] = dl;
-                    if (tid < rows) a.dbeta[((size_t)first + tid) * sh.H + h] = db;
-                    for (int j = 0; j < 8 * tiles; ++j) dla += (double)phi[sh_at * tiles * 8 + j];
+                    if (lane == 0) {
+                        ys[0] = ph;
+                        ys[1] = pl;
+                    }
                 }
                 named_sync(4, 256);
-                if (tid < rows) {
-                    for (int i = 0; i < tid; ++i) dla -= (double)ys[i];
-                    a.dla[((size_t)first + tid) * sh.H + h] = (float)dla;
+                if (warp == 0) {
+                    // dbeta, and dlog_alpha from the sums up to each token
+                    float yh[2], yl[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int t = lane + 32 * i;
+                        const float* q = part + sh_at * tiles * (4 * kChunk) + t;
+                        float db = 0.f;
+                        yh[i] = yl[i] = 0.f;
+#pragma unroll 8
+                        for (int j = 0; j < 2 * tiles; ++j) {
+                            db += q[j * 2 * kChunk];
+                            add2(yh[i], yl[i], q[j * 2 * kChunk + kChunk], 0.f);
+                        }
+                        if (t < rows) a.dbeta[((size_t)first + t) * sh.H + h] = db;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float zh = yh[i], zl = yl[i];     // inclusive, then without this token's own
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const float uh = __shfl_up_sync(0xffffffffu, zh, o), ul = __shfl_up_sync(0xffffffffu, zl, o);
+                            if (lane >= o) add2(zh, zl, uh, ul);
+                        }
+                        float bh = ys[0], bl = ys[1];
+                        add2(bh, bl, yh[i], yl[i]);
+                        add2(bh, bl, -zh, -zl);
+                        if (lane + 32 * i < rows) a.dla[((size_t)first + lane + 32 * i) * sh.H + h] = bh + bl;
+                        if (i == 0) {
+                            // the second half goes on from the first's sum
+                            const float th = __shfl_sync(0xffffffffu, zh, 31), tl = __shfl_sync(0xffffffffu, zl, 31);
+                            __syncwarp();
+                            if (lane == 0) {
+                                float nh = ys[0], nl = ys[1];
+                                add2(nh, nl, -th, -tl);
+                                ys[0] = nh;
+                                ys[1] = nl;
+                            }
+                            __syncwarp();
+                        }
+                    }
                 }
                 wait_or_dead(kqf, n & 1, a.err, dead);
                 wait_or_dead(ef, n & 1, a.err, dead);
@@ -1439,21 +1485,20 @@ cudaError_t bwd_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a,
     if (e == cudaSuccess) e = ensure_smem(seq_grad_kernel<DK, NV>, GradGeom<DK, NV>::kSmem, done_grad);
     if (e != cudaSuccess) return e;
     const SeqShape& sh = a.sh;
-    const long long rows = (long long)seq_slots(sh.nseq, sh.total) * sh.H * 2 * kChunk;
-    CUtensorMap o, ev, vv;
-    if (!token_map(&o, a.dout, sh.total, sh.H * sh.dv, sh.H * sh.dv, NV, 2 * NV) ||
-        !token_map(&ev, a.rec + L.rec_eps, rows / 2 * 3, sh.dv, sh.dv, NV, 2 * NV) || !token_map(&vv, a.ws + L.ws_dV, rows, sh.dv, sh.dv, NV, 2 * NV))
-        return cudaErrorInvalidValue;
+    CUtensorMap o;
+    if (!token_map(&o, a.dout, sh.total, sh.H * sh.dv, sh.H * sh.dv, NV, 2 * NV)) return cudaErrorInvalidValue;
     const char* ops = a.rec + L.rec_op;
-    float *part = reinterpret_cast<float*>(a.ws + L.ws_part), *phi = reinterpret_cast<float*>(a.ws + L.ws_phi);
+    float *part = reinterpret_cast<float*>(a.ws + L.ws_part), *phi = reinterpret_cast<float*>(a.ws + L.ws_phi), *ysum = reinterpret_cast<float*>(a.ws + L.ws_ysum);
     e = launch_kernel(seq_bwd_kernel<DK, NV>, dim3((unsigned)((size_t)sh.nseq * sh.H * (sh.dv / NV))), dim3(kFwdThreads),
                       bwd_smem<DK, NV>(), st, false, q, k, o, a, ops, (const char*)(a.rec + L.rec_S), (const char*)(a.rec + L.rec_eps),
-                      (const float*)(a.rec + L.rec_o), a.ws + L.ws_dS, a.ws + L.ws_dV, part, phi);
+                      (const float*)(a.rec + L.rec_o), a.ws + L.ws_dS, a.ws + L.ws_dV, part, phi, ysum);
     if (e != cudaSuccess) return e;
     const long long items = (long long)seq_slots(sh.nseq, sh.total) * sh.Hk;
     return launch_kernel(seq_grad_kernel<DK, NV>, dim3((unsigned)(items < kSMs ? items : kSMs)), dim3(kFwdThreads),
-                         GradGeom<DK, NV>::kSmem, st, true, q, k, o, ev, vv, a, ops, (const char*)(a.rec + L.rec_S),
-                         (const char*)(a.ws + L.ws_dS), (const float*)part, (const float*)phi, reinterpret_cast<float*>(a.ws + L.ws_dq), reinterpret_cast<float*>(a.ws + L.ws_dk));
+                         GradGeom<DK, NV>::kSmem, st, true, q, k, o, a, ops, (const char*)(a.rec + L.rec_S),
+                         (const char*)(a.rec + L.rec_eps), (const char*)(a.ws + L.ws_dS), (const char*)(a.ws + L.ws_dV),
+                         (const float*)part, (const float*)phi, (const float*)ysum, reinterpret_cast<float*>(a.ws + L.ws_dq),
+                         reinterpret_cast<float*>(a.ws + L.ws_dk));
 }
 
 template <int DK>
@@ -1463,10 +1508,8 @@ cudaError_t backward_dk(const CUtensorMap& q, const CUtensorMap& k, const SeqArg
 
 }  // namespace
 
-// bf16 with d_k in 64-column tiles; the rows of a call's chunks are numbered in 32 bits.
-bool seq_tc_takes(const SeqShape& s, int dtype) {
-    return dtype == GDN_DTYPE_BF16 && s.dk % 64 == 0 && (long long)seq_slots(s.nseq, s.total) * s.H * 3 * kChunk <= 0x7fffffffLL;
-}
+// bf16 with d_k in 64-column tiles
+bool seq_tc_takes(const SeqShape& s, int dtype) { return dtype == GDN_DTYPE_BF16 && s.dk % 64 == 0; }
 
 int seq_tc_cols(const SeqShape& s) {
     return s.dv % 32 == 0 && (size_t)s.nseq * s.H * (s.dv / 16) > kSMs ? 32 : 16;
