@@ -42,6 +42,10 @@ __device__ __forceinline__ int seq_slot0(const SeqShape& a, int s) {
     return (a.offsets == nullptr ? s * (a.total / a.nseq) : a.offsets[s]) / kChunk + s;
 }
 
+__device__ __forceinline__ int seq_end(const SeqShape& a, int s) {
+    return a.offsets == nullptr ? (s + 1) * (a.total / a.nseq) : a.offsets[s + 1];
+}
+
 // Sequence and chunk of a slot: false for an empty slot.  The search is for the last
 // sequence whose first slot is not behind `slot`; it ends for any content of the offsets,
 // and seq_range checks the one that it finds.
@@ -95,7 +99,7 @@ struct SeqArgs {
 // call's sizes and type take.
 struct SeqLayout {
     size_t rec_S, rec_eps, rec_o, rec_op, rec_total;     // record: chunk start states, errors, outputs, chunk operands
-    size_t ws_dS, ws_dV, ws_dq, ws_dk, ws_op, ws_part, ws_phi, ws_ysum, ws_total;   // workspace
+    size_t ws_dS, ws_dV, ws_dq, ws_dk, ws_op, ws_part, ws_phi, ws_total;   // workspace
 };
 
 SeqLayout seq_layout(const SeqShape& s, int dtype);

@@ -545,6 +545,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
         const int srow = (G::kMH == 2 ? 128 * wg : 0) + 32 * w4 + lane, scol = G::kMH == 2 ? 0 : wg * NH;
         const bool owns = srow < DK;
+        const bool whole = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;      // 32-byte rows of columns
         float S[SC];
         {
             const size_t at = (((size_t)s * sh.H + h) * sh.dv + v0 + scol) * DK + srow;
@@ -567,10 +568,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     st_shared16(base + (b >> 1) * G::kTile + (b & 1 ? 8192 : (c & 1) * 16384) + r * 128 + p * 16, 0, 0, 0, 0);
                 }
             }
-            operand_ready(1, 288);
+            // the gates before operand_ready: nothing keeps their place from being filled again until these
+            // warps have come further
             wait_or_dead(full0 + 8 * (c & 1), (c >> 1) & 1, a.err, dead);
             const float* gates = reinterpret_cast<const float*>(sm + G::kG + (c & 1) * kGateFwd);
             const float eg = gates[kGEg + tok], bt = gates[kGBt + tok], ee = gates[kGEnd];
+            operand_ready(1, 288);
             uint4 vr[NH / 8];
             if (reads_k) {
                 wait_or_dead(vf, ph, a.err, dead);
@@ -612,15 +615,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 put_terms<W, 3>(base + G::kR, G::kRTerm, tok, vc, x);
                 operand_ready(3, 160);
                 if constexpr (ST == 3) {                  // eps as three bf16 terms, operands of 64 rows
-                    char* e = recE + (((slot0 + c) * sh.H + h) * tiles + tile) * (size_t)(3 * kChunk * W);
+                    bool swap;
+                    char* e = recE + (((slot0 + c) * sh.H + h) * tiles + tile) * (size_t)(3 * kChunk * W) + pieces_at<W, NH>(tok, vc, swap);
+                    uint32_t p[NH / 2][3];
 #pragma unroll
-                    for (int i = 0; i < NH / 8; ++i) {
-                        uint32_t p[4][3];
+                    for (int j = 0; j < NH / 2; ++j) split_pair<3>(y[2 * j], y[2 * j + 1], p[j]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) split_pair<3>(y[8 * i + 2 * j], y[8 * i + 2 * j + 1], p[j]);
+                    for (int t = 0; t < 3; ++t) {
+                        uint4 u[NH / 8];
 #pragma unroll
-                        for (int t = 0; t < 3; ++t)
-                            *reinterpret_cast<uint4*>(e + t * kChunk * W + sw_piece<W>(tok, vc / 8 + i)) = make_uint4(p[0][t], p[1][t], p[2][t], p[3][t]);
+                        for (int i = 0; i < NH / 8; ++i) u[i] = make_uint4(p[4 * i][t], p[4 * i + 1][t], p[4 * i + 2][t], p[4 * i + 3][t]);
+                        stg_pieces(e + t * kChunk * W, u, swap);
                     }
                 }
             } else {
@@ -628,26 +633,35 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 float* e = recO + (((slot0 + c) * sh.H + h) * tiles + tile) * (size_t)(kChunk * NV) + tok * NV + vc;
 #pragma unroll
                 for (int j = 0; j < NH; ++j) y[j] = fmaf(eg, x[j], y[j]);
+                uint4 u[NH / 8], f[NH / 4];
 #pragma unroll
-                for (int i = 0; i < NH / 8; ++i) {
-                    if (tok < rows)
-                        *reinterpret_cast<uint4*>(o + 8 * i) = make_uint4(pack_bf16(y[8 * i], y[8 * i + 1]), pack_bf16(y[8 * i + 2], y[8 * i + 3]),
-                                                                          pack_bf16(y[8 * i + 4], y[8 * i + 5]), pack_bf16(y[8 * i + 6], y[8 * i + 7]));
-                    if constexpr (ST == 3) {              // unrounded, for the gates' gradient
-                        *reinterpret_cast<float4*>(e + 8 * i) = make_float4(y[8 * i], y[8 * i + 1], y[8 * i + 2], y[8 * i + 3]);
-                        *reinterpret_cast<float4*>(e + 8 * i + 4) = make_float4(y[8 * i + 4], y[8 * i + 5], y[8 * i + 6], y[8 * i + 7]);
-                    }
+                for (int i = 0; i < NH / 8; ++i)
+                    u[i] = make_uint4(pack_bf16(y[8 * i], y[8 * i + 1]), pack_bf16(y[8 * i + 2], y[8 * i + 3]), pack_bf16(y[8 * i + 4], y[8 * i + 5]),
+                                      pack_bf16(y[8 * i + 6], y[8 * i + 7]));
+                if (tok < rows) {
+                    if (whole) stg_pieces(o, u, false);
+                    else
+#pragma unroll
+                        for (int i = 0; i < NH / 8; ++i) reinterpret_cast<uint4*>(o)[i] = u[i];
+                }
+                if constexpr (ST == 3) {                  // unrounded, for the gates' gradient
+#pragma unroll
+                    for (int i = 0; i < NH / 4; ++i)
+                        f[i] = make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]), __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3]));
+                    stg_pieces(e, f, false);
                 }
             }
             __syncwarp();
             wait_or_dead(b3, ph, a.err, dead);
             __syncwarp();
             tc_fence_after();
-            {
-                float d[SC];
-                tmem_sum<SC, 3>(tmem + G::kD3 + (G::kMH == 2 ? wg * 3 * NV : 0) + lanes + scol, NV, d);
+            constexpr int kStep = SC < 16 ? SC : 16;      // columns read at a time: registers
 #pragma unroll
-                for (int j = 0; j < SC; ++j) S[j] = fmaf(ee, S[j], d[j]);
+            for (int g = 0; g < SC; g += kStep) {
+                float d[kStep];
+                tmem_sum<kStep, 3>(tmem + G::kD3 + (G::kMH == 2 ? wg * 3 * NV : 0) + lanes + scol + g, NV, d);
+#pragma unroll
+                for (int j = 0; j < kStep; ++j) S[g + j] = fmaf(ee, S[g + j], d[j]);
             }
         }
         if (a.S_T != nullptr && owns) {
@@ -678,10 +692,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 // The gates' gradients are dots over d_v and come from here, where w and dS are fp32:
 //   dbeta_t = w_t.eps_t,   dlog_alpha_t = dlog_alpha_{t+1} + dO_t.o_t - dV_t.v_t,
 // the second since <S_t, dS_t> changes from token to token by just these; its value at a chunk's
-// first token is <S, dS>, S the chunk's start state, which every kAnchor-th chunk takes (S has to be
-// read for it), the others from the sums between.  Each CTA writes its columns' parts.
-constexpr int kAnchor = 8;
-
+// first token is <S, dS>, S the chunk's start state.  Each CTA writes its columns' parts.
 template <int DK, int NV>
 struct BwdGeom {
     static constexpr int kMH = DK > 128 ? 2 : 1;
@@ -717,7 +728,7 @@ template <int DK, int NV>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     seq_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmO, SeqArgs a, const char* ops, const char* recS, const char* recE, const float* recO,
-                   char* wsS, char* wsV, float* part, float* phi, float* ysum) {
+                   char* wsS, char* wsV, float* part, float* phi) {
     using G = BwdGeom<DK, NV>;
     constexpr int W = G::kW, NH = NV / 2;
     constexpr int SC = G::kMH == 2 ? NV : NH;
@@ -771,7 +782,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 for (int b = 0; b < DK / 64; ++b) tma_2d(st + b * G::kTile, &tmK, hk * DK + 64 * b, first + c * kChunk, f);
                 tma_2d(st + G::kO, &tmO, h * sh.dv + v0, first + c * kChunk, f);
                 bulk_copy_g2s(st + G::kG, op + 4 * kGEg, kGateBwd, f);
-                bulk_prefetch_l2(recS + (((slot0 + c) * sh.H + h) * tiles + tile) * (3 * G::kSTerm), 3 * G::kSTerm);
+                const size_t at = ((slot0 + c) * sh.H + h) * tiles + tile;     // what the compute warps will read themselves
+                bulk_prefetch_l2(recE + at * (3 * kChunk * W), 3 * kChunk * W);
+                bulk_prefetch_l2(recO + at * (kChunk * NV), kChunk * NV * 4);
+                bulk_prefetch_l2(recS + at * (3 * G::kSTerm), 3 * G::kSTerm);
                 issued = i + 1;
                 if (i >= 1 && !wait_or_dead(qe, (i - 1) & 1, a.err, dead)) break;
                 mbar_expect_tx(qf, DK * 128);
@@ -871,6 +885,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
         const int srow = (G::kMH == 2 ? 128 * wg : 0) + 32 * w4 + lane, scol = G::kMH == 2 ? 0 : wg * NH;
         const bool owns = srow < DK;
+        const bool whole = (reinterpret_cast<uintptr_t>(a.dv) & 31u) == 0;      // 32-byte rows of columns
         float S[SC];
         {
             const size_t at = (((size_t)s * sh.H + h) * sh.dv + v0 + scol) * DK + srow;
@@ -883,16 +898,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             float d = 0.f;
             if (owns)
 #pragma unroll
-                for (int j = 0; j < SC / 8; ++j) {
-                    const char* q = p + sw_piece<W>(srow, scol / 8 + j);
-                    const uint4 u = *reinterpret_cast<const uint4*>(q), m = *reinterpret_cast<const uint4*>(q + G::kSTerm),
-                                l = *reinterpret_cast<const uint4*>(q + 2 * G::kSTerm);
-                    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, mm[4] = {m.x, m.y, m.z, m.w}, ll[4] = {l.x, l.y, l.z, l.w};
+                for (int g = 0; g < SC; g += 16) {
+                    constexpr int N = SC < 16 ? SC : 16;
+                    bool swap;
+                    const char* q = p + pieces_at<W, N>(srow, scol + g, swap);
+                    uint4 u[3][N / 8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        d = fmaf(__uint_as_float(uu[e] << 16) + (__uint_as_float(mm[e] << 16) + __uint_as_float(ll[e] << 16)), S[8 * j + 2 * e], d);
-                        d = fmaf(__uint_as_float(uu[e] & 0xffff0000u) +
-                                     (__uint_as_float(mm[e] & 0xffff0000u) + __uint_as_float(ll[e] & 0xffff0000u)), S[8 * j + 2 * e + 1], d);
+                    for (int t = 0; t < 3; ++t) ldg_pieces(q + t * G::kSTerm, u[t]);
+#pragma unroll
+                    for (int j = 0; j < N / 8; ++j) {
+                        const int z = N == 16 ? j ^ 1 : j;
+                        const uint4 a0 = swap ? u[0][z] : u[0][j], a1 = swap ? u[1][z] : u[1][j], a2 = swap ? u[2][z] : u[2][j];
+                        const uint32_t uu[4] = {a0.x, a0.y, a0.z, a0.w}, mm[4] = {a1.x, a1.y, a1.z, a1.w}, ll[4] = {a2.x, a2.y, a2.z, a2.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            d = fmaf(__uint_as_float(uu[e] << 16) + (__uint_as_float(mm[e] << 16) + __uint_as_float(ll[e] << 16)),
+                                     S[g + 8 * j + 2 * e], d);
+                            d = fmaf(__uint_as_float(uu[e] & 0xffff0000u) +
+                                         (__uint_as_float(mm[e] & 0xffff0000u) + __uint_as_float(ll[e] & 0xffff0000u)),
+                                     S[g + 8 * j + 2 * e + 1], d);
+                        }
                     }
                 }
             d = warp_sum(d);
@@ -915,6 +940,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
             const float* gates = reinterpret_cast<const float*>(sm + st + G::kG);
             const float eg = gates[tok], tail = gates[kGTail - kGEg + tok], beta = gates[kGBeta - kGEg + tok], ee = gates[kGEnd - kGEg];
+            // dO for the dots, taken before operand_ready: nothing keeps the stage from being filled again
+            // until these warps have come further
+            uint4 td[NH / 8];
             float x[NH];
             if (!reads_k) {
 #pragma unroll
@@ -922,6 +950,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     uint4* at = reinterpret_cast<uint4*>(sm + st + G::kO + sw_piece<W>(tok, vc / 8 + p));
                     uint4 u = *at;
                     if (tok >= rows) *at = u = make_uint4(0, 0, 0, 0);
+                    td[p] = u;
                     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -932,23 +961,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 put_terms<W, 3>(base + G::kE, G::kRTerm, tok, vc, x);
             }
             operand_ready(1, 288);
-            if (i > 0 && (c + 1) % kAnchor == 0) state_dot(c + 1);
-            // eps (three terms), o, v and dO of this thread's token and columns
-            // (from the stage now: it may be filled again once the last product is done)
-            uint4 te[3][NH / 8], to[NH / 4], tv[NH / 8], td[NH / 8];
+            if (i > 0) state_dot(c + 1);
+            // eps (three terms), o and v of this thread's token and columns
+            uint4 te[3][NH / 8], to[NH / 4], tv[NH / 8];
+            bool swap = false;
             if (!reads_k) {
                 const size_t at = ((slot0 + c) * sh.H + h) * tiles + tile;
                 const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + ((size_t)first + c * kChunk + tok) * sh.ldv + (size_t)h * sh.dv + v0 + vc;
+                const char* e = recE + at * (3 * kChunk * W) + pieces_at<W, NH>(tok, vc, swap);
+#pragma unroll
+                for (int t = 0; t < 3; ++t) ldg_pieces(e + t * kChunk * W, te[t]);
+                ldg_pieces(recO + at * (kChunk * NV) + tok * NV + vc, to);
 #pragma unroll
                 for (int p = 0; p < NH / 8; ++p) {
-#pragma unroll
-                    for (int t = 0; t < 3; ++t)
-                        te[t][p] = *reinterpret_cast<const uint4*>(recE + (at * 3 + t) * (kChunk * W) + sw_piece<W>(tok, vc / 8 + p));
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) to[2 * p + t] = *reinterpret_cast<const uint4*>(recO + at * (kChunk * NV) + tok * NV + vc + 8 * p + 4 * t);
                     tv[p] = make_uint4(0, 0, 0, 0);
                     if (tok < rows) tv[p] = *reinterpret_cast<const uint4*>(vp + 8 * p);
-                    td[p] = *reinterpret_cast<const uint4*>(sm + st + G::kO + sw_piece<W>(tok, vc / 8 + p));
                 }
             }
             wait_or_dead(b1, ph, a.err, dead);
@@ -966,13 +993,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             tc_fence_after();
             {
                 // T^T x (three terms) and, in the columns behind, Ptil^T dO
-                uint32_t u[4][NH];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) tmem_ld_n(tmem + G::kD2 + lanes + vc + t * NV, u[t]);
-                tmem_wait_ld();
+                for (int g = 0; g < NH; g += 8) {
+                    uint32_t u[4][8];
 #pragma unroll
-                for (int j = 0; j < NH; ++j)
-                    x[j] = ((__uint_as_float(u[2][j]) + __uint_as_float(u[1][j])) + __uint_as_float(u[3][j])) + __uint_as_float(u[0][j]);
+                    for (int t = 0; t < 4; ++t) tmem_ld_n(tmem + G::kD2 + lanes + vc + g + t * NV, u[t]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        x[g + j] = ((__uint_as_float(u[2][j]) + __uint_as_float(u[1][j])) + __uint_as_float(u[3][j])) + __uint_as_float(u[0][j]);
+                }
             }
             if (reads_k) {
 #pragma unroll
@@ -980,12 +1010,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 put_terms<W, 3>(base + G::kR, G::kRTerm, tok, vc, x);
                 operand_ready(3, 160);
             } else {
-                char* e = wsV + (((slot0 + c) * sh.H + h) * tiles + tile) * (size_t)(2 * kChunk * W);
+                char* e = wsV + (((slot0 + c) * sh.H + h) * tiles + tile) * (size_t)(2 * kChunk * W) + pieces_at<W, NH>(tok, vc, swap);
                 __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.dv) + (((size_t)first + c * kChunk + tok) * sh.H + h) * sh.dv + v0 + vc;
                 float db = 0.f, dl = 0.f;
+                uint4 hi[NH / 8], lo[NH / 8];
 #pragma unroll
                 for (int p = 0; p < NH / 8; ++p) {
-                    const uint32_t *e0 = &te[0][p].x, *e1 = &te[1][p].x, *e2 = &te[2][p].x, *o4 = &to[2 * p].x, *v4 = &tv[p].x, *d4 = &td[p].x;
+                    const int q = NH == 16 ? p ^ 1 : p;   // where the pieces changed places
+                    const uint4 ea = swap ? te[0][q] : te[0][p], eb = swap ? te[1][q] : te[1][p], ec = swap ? te[2][q] : te[2][p];
+                    const uint32_t *e0 = &ea.x, *e1 = &eb.x, *e2 = &ec.x, *o4 = &to[2 * p].x, *v4 = &tv[p].x, *d4 = &td[p].x;
                     uint32_t u[4][2];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -999,26 +1032,32 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         }
                         split_pair<2>(x[8 * p + 2 * j], x[8 * p + 2 * j + 1], u[j]);
                     }
-                    const uint4 hi = make_uint4(u[0][0], u[1][0], u[2][0], u[3][0]);
-                    *reinterpret_cast<uint4*>(e + sw_piece<W>(tok, vc / 8 + p)) = hi;
-                    *reinterpret_cast<uint4*>(e + kChunk * W + sw_piece<W>(tok, vc / 8 + p)) = make_uint4(u[0][1], u[1][1], u[2][1], u[3][1]);
-                    if (tok < rows) *reinterpret_cast<uint4*>(o + 8 * p) = hi;
+                    hi[p] = make_uint4(u[0][0], u[1][0], u[2][0], u[3][0]);
+                    lo[p] = make_uint4(u[0][1], u[1][1], u[2][1], u[3][1]);
+                }
+                stg_pieces(e, hi, swap);
+                stg_pieces(e + kChunk * W, lo, swap);
+                if (tok < rows) {
+                    if (whole) stg_pieces(o, hi, false);
+                    else
+#pragma unroll
+                        for (int p = 0; p < NH / 8; ++p) reinterpret_cast<uint4*>(o)[p] = hi[p];
                 }
                 float* q = part + ((((slot0 + c) * sh.H + h) * tiles + tile) * 2 + wg) * (2 * kChunk) + tok;
                 q[0] = db;
                 q[kChunk] = dl;
-                dl = warp_sum(dl);
-                if (lane == 0) ysum[(((slot0 + c) * sh.H + h) * tiles + tile) * 4 + 2 * wg + (w4 & 1)] = dl;
             }
             __syncwarp();
             wait_or_dead(b3, ph, a.err, dead);
             __syncwarp();
             tc_fence_after();
-            {
-                float d[SC];
-                tmem_sum<SC, 3>(tmem + G::kD3 + (G::kMH == 2 ? wg * 3 * NV : 0) + lanes + scol, NV, d);
+            constexpr int kStep = SC < 16 ? SC : 16;      // columns read at a time: registers
 #pragma unroll
-                for (int j = 0; j < SC; ++j) S[j] = fmaf(ee, S[j], d[j]);
+            for (int g = 0; g < SC; g += kStep) {
+                float d[kStep];
+                tmem_sum<kStep, 3>(tmem + G::kD3 + (G::kMH == 2 ? wg * 3 * NV : 0) + lanes + scol + g, NV, d);
+#pragma unroll
+                for (int j = 0; j < kStep; ++j) S[g + j] = fmaf(ee, S[g + j], d[j]);
             }
         }
         if (chunks > 0) state_dot(0);
@@ -1050,7 +1089,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 // The gates' gradients are added up here from the parts that the backward scan left.
 //
 // Bound by its reads: 4 bytes for each element of S and dS+ of every chunk.  One CTA per SM goes
-// through the chunks; a ring of two slots takes NV columns of d_v at a time.
+// through the chunks; a ring of slots, 100 KB in all, takes NV columns of d_v at a time.
 template <int DK, int NV>
 struct GradGeom {
     static constexpr int kW = NV * 2;
@@ -1061,8 +1100,9 @@ struct GradGeom {
     // blocks of a slot: dO, dV hi, zero, dV lo, -, or eps hi twice, zero, eps lo twice; then S or dS+, or eps hi, lo
     static constexpr uint32_t kImg = 5 * kBlk;
     static constexpr uint32_t kSlot = kImg + 2 * DK * kW;
-    static constexpr uint32_t kGates = kSlot0 + 2 * kSlot;
-    static constexpr uint32_t kMisc = kGates + kOpGates;          // a pair of floats
+    static constexpr int kSlots = NV == 16 ? 4 : 2;
+    static constexpr uint32_t kGates = kSlot0 + kSlots * kSlot;
+    static constexpr uint32_t kMisc = kGates + kOpGates;          // four floats
     static constexpr uint32_t kBar = kMisc + 16;
     static constexpr uint32_t kUsed = kBar + 256 + 1024;
     static constexpr uint32_t kSmem = kUsed > 116 * 1024 ? kUsed : 116 * 1024;      // one CTA per SM: it takes the whole TMEM
@@ -1074,14 +1114,14 @@ template <int DK, int NV>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     seq_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmO, SeqArgs a, const char* ops, const char* recS, const char* recE,
-                    const char* wsS, const char* wsV, const float* part, const float* phi, const float* ysum, float* dqf, float* dkf) {
+                    const char* wsS, const char* wsV, const float* part, const float* phi, float* dqf, float* dkf) {
     using G = GradGeom<DK, NV>;
     constexpr int W = G::kW, HC = DK / 2;                 // HC: columns of d_k of a thread
     extern __shared__ unsigned char raw[];
     const uint32_t r0 = smem_u32(raw), base = (r0 + 1023u) & ~1023u;
     unsigned char* sm = raw + (base - r0);
-    const uint32_t kqf = base + G::kBar, kqe = kqf + 8, full0 = kqf + 16, empty0 = kqf + 32, ef = kqf + 48, p2 = kqf + 56,
-                   fin = kqf + 64, drain = kqf + 72;
+    const uint32_t kqf = base + G::kBar, kqe = kqf + 8, ef = kqf + 16, p2 = kqf + 24, fin = kqf + 32,
+                   drain = kqf + 40, full0 = kqf + 48, empty0 = full0 + 8 * G::kSlots;
     uint32_t* holder = reinterpret_cast<uint32_t*>(sm + G::kBar + 128);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const SeqShape& sh = a.sh;
@@ -1090,12 +1130,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int items = seq_slots(sh.nseq, sh.total) * sh.Hk;
 
     if (tid == 0) {
-        for (int i = 0; i < 10; ++i) mbar_init(kqf + 8 * i, 1);
+        for (int i = 0; i < 6 + 2 * G::kSlots; ++i) mbar_init(kqf + 8 * i, 1);
         mbar_init(kqe, 8);
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    for (int sl = 0; sl < 2; ++sl)
+    for (int sl = 0; sl < G::kSlots; ++sl)
         for (uint32_t o = tid * 16; o < G::kBlk; o += kFwdThreads * 16)
             st_shared16(base + G::kSlot0 + sl * G::kSlot + 2 * G::kBlk + o, 0, 0, 0, 0);
     fence_proxy_async_smem();
@@ -1126,8 +1166,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     }
                     bulk_copy_g2s(base + G::kGates, ops + sh_at * kOpRecord, kOpGates, kqf);
                     for (int j = 0; j < 3 * tiles; ++j, ++it) {
-                        const uint32_t sl = base + G::kSlot0 + (it & 1) * G::kSlot, f = full0 + 8 * (it & 1);
-                        if (it >= 2 && !(ok = wait_or_dead(empty0 + 8 * (it & 1), ((it >> 1) & 1) ^ 1, a.err, dead))) break;
+                        const uint32_t sl = base + G::kSlot0 + (it % G::kSlots) * G::kSlot, f = full0 + 8 * (it % G::kSlots);
+                        if (it >= G::kSlots && !(ok = wait_or_dead(empty0 + 8 * (it % G::kSlots), ((it / G::kSlots) & 1) ^ 1, a.err, dead))) break;
                         const int v = (j < tiles ? j : (j - tiles) >> 1), v0 = v * NV;
                         const char *e = recE + (sh_at * tiles + v) * (3 * G::kBlk), *w = wsV + (sh_at * tiles + v) * (2 * G::kBlk);
                         if (j < tiles || ((j - tiles) & 1) == 0) {
@@ -1153,7 +1193,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
             if (*dead) {                                  // copies in flight land before the CTA ends
                 mbar_wait(kqf, n & 1, a.err);
-                for (int j = it > 2 ? it - 2 : 0; j < it; ++j) mbar_wait(full0 + 8 * (j & 1), (j >> 1) & 1, a.err);
+                for (int j = it > G::kSlots ? it - G::kSlots : 0; j < it; ++j)
+                    mbar_wait(full0 + 8 * (j % G::kSlots), (j / G::kSlots) & 1, a.err);
             }
         }
         __syncwarp();
@@ -1169,8 +1210,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 wait_or_dead(kqf, n & 1, a.err, dead);
                 __syncwarp();
                 for (int j = 0; j < tiles; ++j, ++it) {
-                    const uint32_t sl = base + G::kSlot0 + (it & 1) * G::kSlot;
-                    wait_or_dead(full0 + 8 * (it & 1), (it >> 1) & 1, a.err, dead);
+                    const uint32_t sl = base + G::kSlot0 + (it % G::kSlots) * G::kSlot;
+                    wait_or_dead(full0 + 8 * (it % G::kSlots), (it / G::kSlots) & 1, a.err, dead);
                     __syncwarp();
                     if (leader) {
                         const uint64_t dA = k_desc<W>(sl), dB = k_desc<W>(sl + G::kImg);
@@ -1179,7 +1220,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                             mma_bf16(tmem + G::kE, dA + 2 * k, dB + 2 * k, idesc_bf16(128, 128), j + k != 0);
                             mma_bf16(tmem + G::kE, dA + (2 * G::kBlk >> 4) + 2 * k, dB + 2 * k, idesc_bf16(128, 64), 1);
                         }
-                        mma_commit(empty0 + 8 * (it & 1));
+                        mma_commit(empty0 + 8 * (it % G::kSlots));
                     }
                     __syncwarp();
                 }
@@ -1188,8 +1229,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 named_sync(1, 288);                       // E and F are read
                 tc_fence_after();
                 for (int j = 0; j < 2 * tiles; ++j, ++it) {
-                    const uint32_t sl = base + G::kSlot0 + (it & 1) * G::kSlot, d = tmem + (j & 1 ? G::kDw : G::kDa);
-                    wait_or_dead(full0 + 8 * (it & 1), (it >> 1) & 1, a.err, dead);
+                    const uint32_t sl = base + G::kSlot0 + (it % G::kSlots) * G::kSlot, d = tmem + (j & 1 ? G::kDw : G::kDa);
+                    wait_or_dead(full0 + 8 * (it % G::kSlots), (it / G::kSlots) & 1, a.err, dead);
                     __syncwarp();
                     if (leader) {
                         const uint64_t dA = k_desc<W>(sl), dB = k_desc<W>(sl + G::kImg),
@@ -1200,7 +1241,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                             mma_bf16(d, dA + 2 * k, dB + (DK * W >> 4) + 2 * k, idesc_bf16(128, DK), 1);
                             mma_bf16(d, dA2 + 2 * k, dB + 2 * k, idesc_bf16(128, DK), 1);
                         }
-                        mma_commit(empty0 + 8 * (it & 1));
+                        mma_commit(empty0 + 8 * (it % G::kSlots));
                     }
                     __syncwarp();
                 }
@@ -1239,32 +1280,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int item = blockIdx.x; item < items; item += gridDim.x) {
             int s, first, rows;
             if (!slot_chunk(sh, item / sh.Hk, s, first, rows, a.err)) continue;
+            const bool more = seq_end(sh, s) - first > kChunk;
             const int hk = item % sh.Hk;
             for (int r = 0; r < rep; ++r, ++n) {
                 const int h = hk * rep + r;
                 const size_t sh_at = (size_t)(item / sh.Hk) * sh.H + h;
                 if (warp == 7) {
-                    // <S, dS> at the chunk's first token, from the anchor before it
-                    const int c = item / sh.Hk - seq_slot0(sh, s), back = c % kAnchor;
-                    const float *p = phi + (sh_at - (size_t)back * sh.H) * tiles * 8, *y = ysum + (sh_at - (size_t)back * sh.H) * tiles * 4;
-                    float ph = 0.f, pl = 0.f;
-                    for (int j = lane; j < 8 * tiles; j += 32) add2(ph, pl, p[j], 0.f);
-                    for (int i = 0; i < back; ++i)
-                        for (int j = lane; j < 4 * tiles; j += 32) add2(ph, pl, -y[(size_t)i * sh.H * tiles * 4 + j], 0.f);
+                    // <S, dS> at this chunk's first token and at the next one's
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) {
-                        const float qh = __shfl_xor_sync(0xffffffffu, ph, o), ql = __shfl_xor_sync(0xffffffffu, pl, o);
-                        add2(ph, pl, qh, ql);
-                    }
-                    if (lane == 0) {
-                        ys[0] = ph;
-                        ys[1] = pl;
+                    for (int i = 0; i < 2; ++i) {
+                        const float* p = phi + (sh_at + (size_t)i * sh.H) * tiles * 8;
+                        float ph = 0.f, pl = 0.f;
+                        if (i == 0 || more)
+                            for (int j = lane; j < 8 * tiles; j += 32) add2(ph, pl, p[j], 0.f);
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) {
+                            const float qh = __shfl_xor_sync(0xffffffffu, ph, o), ql = __shfl_xor_sync(0xffffffffu, pl, o);
+                            add2(ph, pl, qh, ql);
+                        }
+                        if (lane == 0) {
+                            ys[2 * i] = ph;
+                            ys[2 * i + 1] = pl;
+                        }
                     }
                 }
                 named_sync(4, 256);
                 if (warp == 0) {
-                    // dbeta, and dlog_alpha from the sums up to each token
-                    float yh[2], yl[2];
+                    // dbeta; dlog_alpha from the nearer end of the chunk: the sums' errors grow with their length
+                    float yh[2], yl[2], zh[2], zl[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int t = lane + 32 * i;
@@ -1277,31 +1320,25 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                             add2(yh[i], yl[i], q[j * 2 * kChunk + kChunk], 0.f);
                         }
                         if (t < rows) a.dbeta[((size_t)first + t) * sh.H + h] = db;
+                        zh[i] = yh[i];                    // sums up to and with this token, of each half
+                        zl[i] = yl[i];
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const float uh = __shfl_up_sync(0xffffffffu, zh[i], o), ul = __shfl_up_sync(0xffffffffu, zl[i], o);
+                            if (lane >= o) add2(zh[i], zl[i], uh, ul);
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float zh = yh[i], zl = yl[i];     // inclusive, then without this token's own
-#pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) {
-                            const float uh = __shfl_up_sync(0xffffffffu, zh, o), ul = __shfl_up_sync(0xffffffffu, zl, o);
-                            if (lane >= o) add2(zh, zl, uh, ul);
-                        }
-                        float bh = ys[0], bl = ys[1];
+                        // - (the sum before this token) from the start, + the sum from it on from the end
+                        const bool end = i == 1 && more;
+                        float bh = ys[end ? 2 : 0], bl = ys[end ? 3 : 1];
                         add2(bh, bl, yh[i], yl[i]);
-                        add2(bh, bl, -zh, -zl);
+                        add2(bh, bl, -zh[i], -zl[i]);
+                        const float th = __shfl_sync(0xffffffffu, zh[i], 31), tl = __shfl_sync(0xffffffffu, zl[i], 31);
+                        if (end) add2(bh, bl, th, tl);
+                        if (i == 1 && !more) add2(bh, bl, -__shfl_sync(0xffffffffu, zh[0], 31), -__shfl_sync(0xffffffffu, zl[0], 31));
                         if (lane + 32 * i < rows) a.dla[((size_t)first + lane + 32 * i) * sh.H + h] = bh + bl;
-                        if (i == 0) {
-                            // the second half goes on from the first's sum
-                            const float th = __shfl_sync(0xffffffffu, zh, 31), tl = __shfl_sync(0xffffffffu, zl, 31);
-                            __syncwarp();
-                            if (lane == 0) {
-                                float nh = ys[0], nl = ys[1];
-                                add2(nh, nl, -th, -tl);
-                                ys[0] = nh;
-                                ys[1] = nl;
-                            }
-                            __syncwarp();
-                        }
                     }
                 }
                 wait_or_dead(kqf, n & 1, a.err, dead);
@@ -1488,16 +1525,16 @@ cudaError_t bwd_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a,
     CUtensorMap o;
     if (!token_map(&o, a.dout, sh.total, sh.H * sh.dv, sh.H * sh.dv, NV, 2 * NV)) return cudaErrorInvalidValue;
     const char* ops = a.rec + L.rec_op;
-    float *part = reinterpret_cast<float*>(a.ws + L.ws_part), *phi = reinterpret_cast<float*>(a.ws + L.ws_phi), *ysum = reinterpret_cast<float*>(a.ws + L.ws_ysum);
+    float *part = reinterpret_cast<float*>(a.ws + L.ws_part), *phi = reinterpret_cast<float*>(a.ws + L.ws_phi);
     e = launch_kernel(seq_bwd_kernel<DK, NV>, dim3((unsigned)((size_t)sh.nseq * sh.H * (sh.dv / NV))), dim3(kFwdThreads),
                       bwd_smem<DK, NV>(), st, false, q, k, o, a, ops, (const char*)(a.rec + L.rec_S), (const char*)(a.rec + L.rec_eps),
-                      (const float*)(a.rec + L.rec_o), a.ws + L.ws_dS, a.ws + L.ws_dV, part, phi, ysum);
+                      (const float*)(a.rec + L.rec_o), a.ws + L.ws_dS, a.ws + L.ws_dV, part, phi);
     if (e != cudaSuccess) return e;
     const long long items = (long long)seq_slots(sh.nseq, sh.total) * sh.Hk;
     return launch_kernel(seq_grad_kernel<DK, NV>, dim3((unsigned)(items < kSMs ? items : kSMs)), dim3(kFwdThreads),
                          GradGeom<DK, NV>::kSmem, st, true, q, k, o, a, ops, (const char*)(a.rec + L.rec_S),
                          (const char*)(a.rec + L.rec_eps), (const char*)(a.ws + L.ws_dS), (const char*)(a.ws + L.ws_dV),
-                         (const float*)part, (const float*)phi, (const float*)ysum, reinterpret_cast<float*>(a.ws + L.ws_dq),
+                         (const float*)part, (const float*)phi, reinterpret_cast<float*>(a.ws + L.ws_dq),
                          reinterpret_cast<float*>(a.ws + L.ws_dk));
 }
 

@@ -210,6 +210,45 @@ __device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
+// N/8 pieces of 16 bytes that are neighbours in memory: whole sectors where there are two, with a
+// 32-byte access (a warp's rows lie apart, so that half sectors cost as much as whole ones).  `swap`:
+// the pieces of a pair change places.
+template <int P>
+__device__ __forceinline__ void stg_pieces(void* p, const uint4 (&x)[P], bool swap) {
+    if constexpr (P == 1) {
+        *reinterpret_cast<uint4*>(p) = x[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+            const uint4 a = swap ? x[i + 1] : x[i], b = swap ? x[i] : x[i + 1];
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(static_cast<char*>(p) + 16 * i), "r"(a.x), "r"(a.y),
+                         "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                         : "memory");
+        }
+    }
+}
+template <int P>
+__device__ __forceinline__ void ldg_pieces(const void* p, uint4 (&x)[P]) {
+    if constexpr (P == 1) {
+        x[0] = *reinterpret_cast<const uint4*>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                         : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w), "=r"(x[i + 1].x), "=r"(x[i + 1].y), "=r"(x[i + 1].z),
+                           "=r"(x[i + 1].w)
+                         : "l"(static_cast<const char*>(p) + 16 * i));
+        }
+    }
+}
+// Place of a thread's NH columns from vc on in row `tok` of a W-byte operand, as stg_pieces takes them.
+template <int W, int NH>
+__device__ __forceinline__ uint32_t pieces_at(int tok, int vc, bool& swap) {
+    const uint32_t at = sw_piece<W>(tok, vc / 8);
+    swap = NH == 16 && (at & 16) != 0;
+    return NH == 16 ? at & ~16u : at;
+}
+
 // Bring a box into L2; nothing waits for it.
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0),

@@ -323,3 +323,25 @@ def test_steps_follow_a_prompt():
         check(o1, ref[t:t + 1], "step %d" % t, n)
     check(S, refS, "S", n)
     check(S_T, refS, "S_T", n)
+
+
+def test_long_batch_gives_equal_bits_and_exact_gates():
+    """More CTAs than the GPU has SMs, many chunks each: warps and CTAs drift apart, nothing may depend on it."""
+    lengths = [1024, 700, 1000, 640]
+    x, off = make(lengths, 8, 8, 256, 256, "bf16", seed=41)
+    out, S_T, ws, rec = forward(x, off, record=True)
+    dout, dS = torch.randn_like(out), 0.1 * torch.randn_like(S_T)
+    d = backward(x, off, dout, dS, ws, rec)
+    for _ in range(4):
+        o2, S2, ws2, rec2 = forward(x, off, record=True)
+        d2 = backward(x, off, dout, dS, ws2, rec2)
+        assert torch.equal(out, o2) and torch.equal(S_T, S2)
+        for m in OUT:
+            assert torch.equal(d[m], d2[m]), m
+    # one sequence and two heads against fp64
+    a, b = sum(lengths[:1]), sum(lengths[:2])
+    one = {m: (y[1:2, 2:4] if m == "S0" else y[a:b, 2:4]).double().cpu().numpy() for m, y in x.items()}
+    want = seq.seq_backward(**one, lengths=lengths[1:2], dout=dout[a:b, 2:4].double().cpu().numpy(),
+                            dS_T=dS[1:2, 2:4].double().cpu().numpy())
+    for m in OUT:
+        check(d[m][1:2, 2:4] if m == "S0" else d[m][a:b, 2:4], want[m], "d" + m, 256 + 256 + 64)
