@@ -400,8 +400,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     unsigned char* sm = raw + (base - r0);
     // copies landed (two stages; operands), their places free; products done; operands written
     const uint32_t full0 = base + G::kBar, empty0 = full0 + 16, tpf = full0 + 32, tpe = full0 + 40, b1 = full0 + 48,
-                   b2 = full0 + 56, b3 = full0 + 64, drain = full0 + 72, vf = full0 + 80, ve = full0 + 88, qf = full0 + 96, qe = full0 + 104;
-    uint32_t* holder = reinterpret_cast<uint32_t*>(sm + G::kBar + 128);
+                   b2 = full0 + 56, b3 = full0 + 64, drain = full0 + 72, vf = full0 + 80, ve = full0 + 88, qf = full0 + 96, qe = full0 + 104, ge0 = full0 + 112;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(sm + G::kBar + 160);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const SeqShape& sh = a.sh;
     const int tiles = sh.dv / NV;
@@ -416,8 +416,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const size_t slot0 = (size_t)(first / kChunk + s);
 
     if (tid == 0) {
-        for (int i = 0; i < 14; ++i) mbar_init(full0 + 8 * i, 1);
+        for (int i = 0; i < 16; ++i) mbar_init(full0 + 8 * i, 1);
         mbar_init(ve, 4);
+        mbar_init(ge0, 8);
+        mbar_init(ge0 + 8, 8);
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -446,7 +448,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             };
             for (int c = 0; c < chunks; ++c) {
                 if (c + 2 < chunks) prefetch(c + 2);
-                if (c >= 2 && !wait_or_dead(empty0 + 8 * (c & 1), ((c >> 1) & 1) ^ 1, a.err, dead)) break;
+                if (c >= 2 && !(wait_or_dead(empty0 + 8 * (c & 1), ((c >> 1) & 1) ^ 1, a.err, dead) &&
+                                wait_or_dead(ge0 + 8 * (c & 1), ((c >> 1) & 1) ^ 1, a.err, dead)))
+                    break;
                 const uint32_t f = full0 + 8 * (c & 1);
                 const char* op = ops + ((slot0 + c) * sh.H + h) * op_bytes;
                 mbar_expect_tx(f, DK * 128 + kGateFwd);
@@ -568,12 +572,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     st_shared16(base + (b >> 1) * G::kTile + (b & 1 ? 8192 : (c & 1) * 16384) + r * 128 + p * 16, 0, 0, 0, 0);
                 }
             }
-            // the gates before operand_ready: nothing keeps their place from being filled again until these
-            // warps have come further
+            operand_ready(1, 288);
             wait_or_dead(full0 + 8 * (c & 1), (c >> 1) & 1, a.err, dead);
             const float* gates = reinterpret_cast<const float*>(sm + G::kG + (c & 1) * kGateFwd);
             const float eg = gates[kGEg + tok], bt = gates[kGBt + tok], ee = gates[kGEnd];
-            operand_ready(1, 288);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ge0 + 8 * (c & 1));
             uint4 vr[NH / 8];
             if (reads_k) {
                 wait_or_dead(vf, ph, a.err, dead);
@@ -724,8 +728,12 @@ constexpr size_t bwd_smem() {
     return G::kSmem > least ? G::kSmem : least;
 }
 
+// Twelve warps: eight that compute, one for the copies, one that issues products, two for the outputs and
+// the gates' dots (lanes 64 .. 127 of the second product repeat dV for them).
+constexpr int kBwdThreads = 384;
+
 template <int DK, int NV>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     seq_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmO, SeqArgs a, const char* ops, const char* recS, const char* recE, const float* recO,
                    char* wsS, char* wsV, float* part, float* phi) {
@@ -736,8 +744,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t r0 = smem_u32(raw), base = (r0 + 1023u) & ~1023u;
     unsigned char* sm = raw + (base - r0);
     const uint32_t full0 = base + G::kBar, empty0 = full0 + 16, tpf = full0 + 32, tpe = full0 + 40, b1 = full0 + 48,
-                   b2 = full0 + 56, b3 = full0 + 64, drain = full0 + 72, qf = full0 + 80, qe = full0 + 88;
-    uint32_t* holder = reinterpret_cast<uint32_t*>(sm + G::kBar + 96);
+                   b2 = full0 + 56, b3 = full0 + 64, drain = full0 + 72, qf = full0 + 80, qe = full0 + 88, he0 = full0 + 96;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(sm + G::kBar + 128);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const SeqShape& sh = a.sh;
     const int tiles = sh.dv / NV;
@@ -752,13 +760,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const size_t slot0 = (size_t)(first / kChunk + s);
 
     if (tid == 0) {
-        for (int i = 0; i < 12; ++i) mbar_init(full0 + 8 * i, 1);
+        for (int i = 0; i < 14; ++i) mbar_init(full0 + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(he0 + 8 * i, 2);
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (DK % 128 != 0) {                                  // columns of d_k that no copy fills
         for (int st = 0; st < 3; ++st)
-            for (uint32_t o = tid * 16; o < G::kTile; o += kFwdThreads * 16)
+            for (uint32_t o = tid * 16; o < G::kTile; o += kBwdThreads * 16)
                 st_shared16(base + (st < 2 ? st * G::kStage : G::kQ) + (DK / 64) * G::kTile + o, 0, 0, 0, 0);
     }
     fence_proxy_async_smem();
@@ -768,13 +777,111 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     tc_fence_after();
     const uint32_t tmem = warp_uniform(*holder);
 
+    // eight columns of w: T^T x (three terms) and, in the columns behind, Ptil^T dO
+    auto read_w = [&](int col, uint32_t lanes, float* x) {
+        uint32_t u[4][8];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) tmem_ld_n(tmem + G::kD2 + lanes + col + t * NV, u[t]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] = ((__uint_as_float(u[2][j]) + __uint_as_float(u[1][j])) + __uint_as_float(u[3][j])) + __uint_as_float(u[0][j]);
+    };
     // i counts the chunks as they are taken, c = chunks - 1 - i is the chunk
-    if (warp == 8) {
+    if (warp >= 10) {
+        // a token's dV and its dots, NH columns at a time
+        const int w4 = warp & 3, tok = 32 * (w4 & 1) + lane;
+        const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+        const bool whole = (reinterpret_cast<uintptr_t>(a.dv) & 31u) == 0;      // 32-byte rows of columns
+        if (chunks > 0) asm volatile("bar.arrive 1, 352;\n" ::: "memory");
+        for (int i = 0; i < chunks; ++i) {
+            const int c = chunks - 1 - i;
+            const uint32_t ph = i & 1, st = (i & 1) * G::kStage;
+            const int rows = min(kChunk, len - c * kChunk);
+            const size_t at = ((slot0 + c) * sh.H + h) * tiles + tile;
+            const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + ((size_t)first + c * kChunk + tok) * sh.ldv + (size_t)h * sh.dv + v0;
+            uint4 te[3][NH / 8], to[NH / 4], tv[NH / 8];
+            bool swap = false;
+            auto load = [&](int vc) {                     // eps (three terms), o and v
+                const char* e = recE + at * (3 * kChunk * W) + pieces_at<W, NH>(tok, vc, swap);
+#pragma unroll
+                for (int t = 0; t < 3; ++t) ldg_pieces(e + t * kChunk * W, te[t]);
+                ldg_pieces(recO + at * (kChunk * NV) + tok * NV + vc, to);
+#pragma unroll
+                for (int p = 0; p < NH / 8; ++p) {
+                    tv[p] = make_uint4(0, 0, 0, 0);
+                    if (tok < rows) tv[p] = *reinterpret_cast<const uint4*>(vp + vc + 8 * p);
+                }
+            };
+            load(0);
+            wait_or_dead(full0 + 8 * (i & 1), (i >> 1) & 1, a.err, dead);
+            const float beta = reinterpret_cast<const float*>(sm + st + G::kG)[kGBeta - kGEg + tok];
+            wait_or_dead(b2, ph, a.err, dead);
+            __syncwarp();
+            tc_fence_after();
+            float all[NV];
+#pragma unroll
+            for (int g = 0; g < NV; g += 8) read_w(g, lanes, all + g);
+            tc_fence_before();
+            __syncwarp();
+            // read: the next chunk's products may come
+            if (i + 1 < chunks) asm volatile("bar.arrive 1, 352;\n" ::: "memory");
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int vc = half * NH;
+                if (half > 0) load(vc);
+                float *x = all + vc, db = 0.f, dl = 0.f;
+                uint4 hi[NH / 8], lo[NH / 8];
+#pragma unroll
+                for (int p = 0; p < NH / 8; ++p) {
+                    const int q = NH == 16 ? p ^ 1 : p;   // where the pieces changed places
+                    uint4 td = *reinterpret_cast<const uint4*>(sm + st + G::kO + sw_piece<W>(tok, vc / 8 + p));
+                    if (tok >= rows) td = make_uint4(0, 0, 0, 0);
+                    const uint4 ea = swap ? te[0][q] : te[0][p], eb = swap ? te[1][q] : te[1][p], ec = swap ? te[2][q] : te[2][p];
+                    const uint32_t *e0 = &ea.x, *e1 = &eb.x, *e2 = &ec.x, *o4 = &to[2 * p].x, *v4 = &tv[p].x, *d4 = &td.x;
+                    uint32_t u[4][2];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            auto part16 = [&](uint32_t w) { return __uint_as_float(z ? w & 0xffff0000u : w << 16); };
+                            float& w = x[8 * p + 2 * j + z];
+                            db = fmaf(w, part16(e0[j]) + (part16(e1[j]) + part16(e2[j])), db);
+                            w *= beta;
+                            dl = fmaf(part16(d4[j]), __uint_as_float(o4[2 * j + z]), fmaf(-w, part16(v4[j]), dl));
+                        }
+                        split_pair<2>(x[8 * p + 2 * j], x[8 * p + 2 * j + 1], u[j]);
+                    }
+                    hi[p] = make_uint4(u[0][0], u[1][0], u[2][0], u[3][0]);
+                    lo[p] = make_uint4(u[0][1], u[1][1], u[2][1], u[3][1]);
+                }
+                bool turn;
+                char* e = wsV + at * (size_t)(2 * kChunk * W) + pieces_at<W, NH>(tok, vc, turn);
+                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.dv) + (((size_t)first + c * kChunk + tok) * sh.H + h) * sh.dv + v0 + vc;
+                stg_pieces(e, hi, turn);
+                stg_pieces(e + kChunk * W, lo, turn);
+                if (tok < rows) {
+                    if (whole) stg_pieces(o, hi, false);
+                    else
+#pragma unroll
+                        for (int p = 0; p < NH / 8; ++p) reinterpret_cast<uint4*>(o)[p] = hi[p];
+                }
+                float* q = part + (at * 2 + half) * (2 * kChunk) + tok;
+                q[0] = db;
+                q[kChunk] = dl;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(he0 + 8 * (i & 1));               // dO and the gates may be overwritten
+            __syncwarp();
+        }
+    } else if (warp == 8) {
         if (elect_one()) {
             int issued = 0, q_issued = 0, ops_issued = 0;
             for (int i = 0; i < chunks; ++i) {
                 const int c = chunks - 1 - i;
-                if (i >= 2 && !wait_or_dead(empty0 + 8 * (i & 1), ((i >> 1) & 1) ^ 1, a.err, dead)) break;
+                if (i >= 2 && !(wait_or_dead(empty0 + 8 * (i & 1), ((i >> 1) & 1) ^ 1, a.err, dead) &&
+                                wait_or_dead(he0 + 8 * (i & 1), ((i >> 1) & 1) ^ 1, a.err, dead)))
+                    break;
                 const uint32_t st = base + (i & 1) * G::kStage, f = full0 + 8 * (i & 1);
                 const char* op = ops + ((slot0 + c) * sh.H + h) * kOpRecord;
                 mbar_expect_tx(f, DK * 128 + 64 * W + kGateBwd);
@@ -817,7 +924,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             wait_or_dead(tpf, ph, a.err, dead);
             wait_or_dead(qf, ph, a.err, dead);
             __syncwarp();
-            named_sync(1, 288);
+            named_sync(1, 352);
             tc_fence_after();
             const uint64_t dK = mn_desc<128>(st, G::kTile), dQ = mn_desc<128>(base + G::kQ, G::kTile);
             if (leader) {
@@ -880,48 +987,62 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         __syncwarp();
     } else {
         const int wg = warp >> 2, w4 = warp & 3;
-        const bool reads_k = w4 < 2;                      // x and -e^g dV of a token, else e^g dO, outputs and dots
+        const bool reads_k = w4 < 2;                      // x and -e^g dV of a token, else e^g dO
         const int tok = 32 * (w4 & 1) + lane, vc = wg * NH;
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
         const int srow = (G::kMH == 2 ? 128 * wg : 0) + 32 * w4 + lane, scol = G::kMH == 2 ? 0 : wg * NH;
         const bool owns = srow < DK;
-        const bool whole = (reinterpret_cast<uintptr_t>(a.dv) & 31u) == 0;      // 32-byte rows of columns
         float S[SC];
         {
             const size_t at = (((size_t)s * sh.H + h) * sh.dv + v0 + scol) * DK + srow;
 #pragma unroll
             for (int j = 0; j < SC; ++j) S[j] = owns && a.dS_T != nullptr ? a.dS_T[at + (size_t)j * DK] : 0.f;
         }
-        // this CTA's part of <S, dS> at the start of chunk c; S's image is swizzled as in shared memory
-        auto state_dot = [&](int c) {
-            const char* p = recS + (((slot0 + c) * sh.H + h) * tiles + tile) * (3 * G::kSTerm);
+        // This CTA's part of <S, dS> at the start of chunk c: N columns from g on of the thread's row, three
+        // terms, in S's image, swizzled as it was in shared memory.
+        constexpr int N = SC < 16 ? SC : 16;
+        auto load_state = [&](int c, int g, uint4 (&u)[3][N / 8]) {
+            bool swap;
+            const char* p = recS + (((slot0 + c) * sh.H + h) * tiles + tile) * (3 * G::kSTerm) + pieces_at<W, N>(srow, scol + g, swap);
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+                if (owns) ldg_pieces(p + t * G::kSTerm, u[t]);
+                else
+#pragma unroll
+                    for (int k = 0; k < N / 8; ++k) u[t][k] = make_uint4(0, 0, 0, 0);
+            }
+        };
+        auto dot_state = [&](int g, const uint4 (&u)[3][N / 8]) {
+            bool swap;
+            pieces_at<W, N>(srow, scol + g, swap);
             float d = 0.f;
-            if (owns)
 #pragma unroll
-                for (int g = 0; g < SC; g += 16) {
-                    constexpr int N = SC < 16 ? SC : 16;
-                    bool swap;
-                    const char* q = p + pieces_at<W, N>(srow, scol + g, swap);
-                    uint4 u[3][N / 8];
+            for (int j = 0; j < N / 8; ++j) {
+                const int z = N == 16 ? j ^ 1 : j;
+                const uint4 a0 = swap ? u[0][z] : u[0][j], a1 = swap ? u[1][z] : u[1][j], a2 = swap ? u[2][z] : u[2][j];
+                const uint32_t uu[4] = {a0.x, a0.y, a0.z, a0.w}, mm[4] = {a1.x, a1.y, a1.z, a1.w}, ll[4] = {a2.x, a2.y, a2.z, a2.w};
 #pragma unroll
-                    for (int t = 0; t < 3; ++t) ldg_pieces(q + t * G::kSTerm, u[t]);
-#pragma unroll
-                    for (int j = 0; j < N / 8; ++j) {
-                        const int z = N == 16 ? j ^ 1 : j;
-                        const uint4 a0 = swap ? u[0][z] : u[0][j], a1 = swap ? u[1][z] : u[1][j], a2 = swap ? u[2][z] : u[2][j];
-                        const uint32_t uu[4] = {a0.x, a0.y, a0.z, a0.w}, mm[4] = {a1.x, a1.y, a1.z, a1.w}, ll[4] = {a2.x, a2.y, a2.z, a2.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            d = fmaf(__uint_as_float(uu[e] << 16) + (__uint_as_float(mm[e] << 16) + __uint_as_float(ll[e] << 16)),
-                                     S[g + 8 * j + 2 * e], d);
-                            d = fmaf(__uint_as_float(uu[e] & 0xffff0000u) +
-                                         (__uint_as_float(mm[e] & 0xffff0000u) + __uint_as_float(ll[e] & 0xffff0000u)),
-                                     S[g + 8 * j + 2 * e + 1], d);
-                        }
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    d = fmaf(__uint_as_float(uu[e] << 16) + (__uint_as_float(mm[e] << 16) + __uint_as_float(ll[e] << 16)), S[g + 8 * j + 2 * e], d);
+                    d = fmaf(__uint_as_float(uu[e] & 0xffff0000u) + (__uint_as_float(mm[e] & 0xffff0000u) + __uint_as_float(ll[e] & 0xffff0000u)),
+                             S[g + 8 * j + 2 * e + 1], d);
                 }
+            }
+            return d;
+        };
+        auto store_phi = [&](int c, float d) {
             d = warp_sum(d);
             if (lane == 0) phi[(((slot0 + c) * sh.H + h) * tiles + tile) * 8 + warp] = d;
+        };
+        auto state_dot = [&](int c) {
+            float d = 0.f;
+#pragma unroll
+            for (int g = 0; g < SC; g += N) {
+                uint4 u[3][N / 8];
+                load_state(c, g, u);
+                d += dot_state(g, u);
+            }
+            store_phi(c, d);
         };
         for (int i = 0; i < chunks; ++i) {
             const int c = chunks - 1 - i;
@@ -940,9 +1061,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
             const float* gates = reinterpret_cast<const float*>(sm + st + G::kG);
             const float eg = gates[tok], tail = gates[kGTail - kGEg + tok], beta = gates[kGBeta - kGEg + tok], ee = gates[kGEnd - kGEg];
-            // dO for the dots, taken before operand_ready: nothing keeps the stage from being filled again
-            // until these warps have come further
-            uint4 td[NH / 8];
             float x[NH];
             if (!reads_k) {
 #pragma unroll
@@ -950,7 +1068,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     uint4* at = reinterpret_cast<uint4*>(sm + st + G::kO + sw_piece<W>(tok, vc / 8 + p));
                     uint4 u = *at;
                     if (tok >= rows) *at = u = make_uint4(0, 0, 0, 0);
-                    td[p] = u;
                     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -960,92 +1077,40 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
                 put_terms<W, 3>(base + G::kE, G::kRTerm, tok, vc, x);
             }
-            operand_ready(1, 288);
-            if (i > 0) state_dot(c + 1);
-            // eps (three terms), o and v of this thread's token and columns
-            uint4 te[3][NH / 8], to[NH / 4], tv[NH / 8];
-            bool swap = false;
-            if (!reads_k) {
-                const size_t at = ((slot0 + c) * sh.H + h) * tiles + tile;
-                const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + ((size_t)first + c * kChunk + tok) * sh.ldv + (size_t)h * sh.dv + v0 + vc;
-                const char* e = recE + at * (3 * kChunk * W) + pieces_at<W, NH>(tok, vc, swap);
+            operand_ready(1, 352);
+            // The warps that read K load the state that belongs to dS now and form its dot behind the third
+            // product's start, the others at once.
+            uint4 pre[SC / N][3][N / 8];
+            if (i > 0) {
+                if (reads_k)
 #pragma unroll
-                for (int t = 0; t < 3; ++t) ldg_pieces(e + t * kChunk * W, te[t]);
-                ldg_pieces(recO + at * (kChunk * NV) + tok * NV + vc, to);
-#pragma unroll
-                for (int p = 0; p < NH / 8; ++p) {
-                    tv[p] = make_uint4(0, 0, 0, 0);
-                    if (tok < rows) tv[p] = *reinterpret_cast<const uint4*>(vp + 8 * p);
-                }
+                    for (int g = 0; g < SC / N; ++g) load_state(c + 1, g * N, pre[g]);
+                else state_dot(c + 1);
             }
-            wait_or_dead(b1, ph, a.err, dead);
-            __syncwarp();
-            tc_fence_after();
             if (reads_k) {
+                wait_or_dead(b1, ph, a.err, dead);
+                __syncwarp();
+                tc_fence_after();
                 tmem_sum<NH, 3>(tmem + G::kD1 + lanes + vc, NV, x);
 #pragma unroll
                 for (int j = 0; j < NH; ++j) x[j] *= tail;
                 put_terms<W, 3>(base + G::kR, G::kRTerm, tok, vc, x);
                 operand_ready(2, 160);
-            }
-            wait_or_dead(b2, ph, a.err, dead);
-            __syncwarp();
-            tc_fence_after();
-            {
-                // T^T x (three terms) and, in the columns behind, Ptil^T dO
+                wait_or_dead(b2, ph, a.err, dead);
+                __syncwarp();
+                tc_fence_after();
 #pragma unroll
-                for (int g = 0; g < NH; g += 8) {
-                    uint32_t u[4][8];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) tmem_ld_n(tmem + G::kD2 + lanes + vc + g + t * NV, u[t]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        x[g + j] = ((__uint_as_float(u[2][j]) + __uint_as_float(u[1][j])) + __uint_as_float(u[3][j])) + __uint_as_float(u[0][j]);
-                }
-            }
-            if (reads_k) {
+                for (int g = 0; g < NH; g += 8) read_w(vc + g, lanes, x + g);
 #pragma unroll
                 for (int j = 0; j < NH; ++j) x[j] *= -eg * beta;
                 put_terms<W, 3>(base + G::kR, G::kRTerm, tok, vc, x);
                 operand_ready(3, 160);
-            } else {
-                char* e = wsV + (((slot0 + c) * sh.H + h) * tiles + tile) * (size_t)(2 * kChunk * W) + pieces_at<W, NH>(tok, vc, swap);
-                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.dv) + (((size_t)first + c * kChunk + tok) * sh.H + h) * sh.dv + v0 + vc;
-                float db = 0.f, dl = 0.f;
-                uint4 hi[NH / 8], lo[NH / 8];
+                if (i > 0) {
+                    float d = 0.f;
 #pragma unroll
-                for (int p = 0; p < NH / 8; ++p) {
-                    const int q = NH == 16 ? p ^ 1 : p;   // where the pieces changed places
-                    const uint4 ea = swap ? te[0][q] : te[0][p], eb = swap ? te[1][q] : te[1][p], ec = swap ? te[2][q] : te[2][p];
-                    const uint32_t *e0 = &ea.x, *e1 = &eb.x, *e2 = &ec.x, *o4 = &to[2 * p].x, *v4 = &tv[p].x, *d4 = &td[p].x;
-                    uint32_t u[4][2];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            auto half = [&](uint32_t w) { return __uint_as_float(z ? w & 0xffff0000u : w << 16); };
-                            float& w = x[8 * p + 2 * j + z];
-                            db = fmaf(w, half(e0[j]) + (half(e1[j]) + half(e2[j])), db);
-                            w *= beta;
-                            dl = fmaf(half(d4[j]), __uint_as_float(o4[2 * j + z]), fmaf(-w, half(v4[j]), dl));
-                        }
-                        split_pair<2>(x[8 * p + 2 * j], x[8 * p + 2 * j + 1], u[j]);
-                    }
-                    hi[p] = make_uint4(u[0][0], u[1][0], u[2][0], u[3][0]);
-                    lo[p] = make_uint4(u[0][1], u[1][1], u[2][1], u[3][1]);
+                    for (int g = 0; g < SC / N; ++g) d += dot_state(g * N, pre[g]);
+                    store_phi(c + 1, d);
                 }
-                stg_pieces(e, hi, swap);
-                stg_pieces(e + kChunk * W, lo, swap);
-                if (tok < rows) {
-                    if (whole) stg_pieces(o, hi, false);
-                    else
-#pragma unroll
-                        for (int p = 0; p < NH / 8; ++p) reinterpret_cast<uint4*>(o)[p] = hi[p];
-                }
-                float* q = part + ((((slot0 + c) * sh.H + h) * tiles + tile) * 2 + wg) * (2 * kChunk) + tok;
-                q[0] = db;
-                q[kChunk] = dl;
             }
             __syncwarp();
             wait_or_dead(b3, ph, a.err, dead);
@@ -1526,7 +1591,7 @@ cudaError_t bwd_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a,
     if (!token_map(&o, a.dout, sh.total, sh.H * sh.dv, sh.H * sh.dv, NV, 2 * NV)) return cudaErrorInvalidValue;
     const char* ops = a.rec + L.rec_op;
     float *part = reinterpret_cast<float*>(a.ws + L.ws_part), *phi = reinterpret_cast<float*>(a.ws + L.ws_phi);
-    e = launch_kernel(seq_bwd_kernel<DK, NV>, dim3((unsigned)((size_t)sh.nseq * sh.H * (sh.dv / NV))), dim3(kFwdThreads),
+    e = launch_kernel(seq_bwd_kernel<DK, NV>, dim3((unsigned)((size_t)sh.nseq * sh.H * (sh.dv / NV))), dim3(kBwdThreads),
                       bwd_smem<DK, NV>(), st, false, q, k, o, a, ops, (const char*)(a.rec + L.rec_S), (const char*)(a.rec + L.rec_eps),
                       (const float*)(a.rec + L.rec_o), a.ws + L.ws_dS, a.ws + L.ws_dV, part, phi);
     if (e != cudaSuccess) return e;
