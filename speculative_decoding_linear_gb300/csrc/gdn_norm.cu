@@ -18,7 +18,11 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPartialRows = 304;        // CTAs of a gradient kernel at most: two per SM
+// CTAs of a gradient kernel at most, each a row of partial sums (the block norm: two): as many as are
+// resident together, so that none begins when others have ended.  The block norm's kernel holds two rows
+// in some 128 registers a thread: 512 threads an SM.
+constexpr int kSMs = 152, kGatedCtas = 3 * kSMs;
+constexpr int block_ctas(int threads) { return kSMs * (512 / threads); }
 
 template <typename T>
 __device__ __forceinline__ void st8(T* p, const float (&x)[8]);
@@ -39,6 +43,30 @@ __device__ __forceinline__ void st8<__nv_bfloat16>(__nv_bfloat16* p, const float
     *reinterpret_cast<uint4*>(p) = u;
 }
 
+// Eight values as they lie in memory: held back a row ahead, and widened where they are used.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ float operator[](int i) const {
+        const uint32_t w = (&u.x)[i / 2];
+        return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+    }
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ float operator[](int i) const { return i < 4 ? (&a.x)[i] : (&b.x)[i - 4]; }
+};
+
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float x) {
 #pragma unroll
@@ -46,7 +74,13 @@ __device__ __forceinline__ float lanes_sum(float x) {
     return x;
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+// bf16 results are rounded by 2^-8: the hardware's exponential and reciprocal (some 2^-21 here) do for
+// them, and the exact ones would take as long as the reads; fp32 results take the exact ones.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float z) {
+    if constexpr (sizeof(T) == 2) return __fdividef(1.f, 1.f + __expf(-z));
+    return 1.f / (1.f + expf(-z));
+}
 
 // ---------------------------------------------------------------------------
 // gated norm: LANES lanes per row of d <= 8 LANES values
@@ -76,49 +110,59 @@ __global__ void __launch_bounds__(kThreads) gated_norm_kernel(GatedArgs a) {
     for (int i = 0; i < 8; ++i) s = fmaf(o[i], o[i], s);
     const float r = rsqrtf(lanes_sum<LANES>(s) / a.d + a.eps);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = o[i] * r * w[i] * (z[i] * sigmoid(z[i]));
+    for (int i = 0; i < 8; ++i) o[i] = o[i] * r * w[i] * (z[i] * sigmoid<T>(z[i]));
     if (in) st8<T>(static_cast<T*>(a.y) + row * a.d + c, o);
 }
 
 template <typename TO, typename T, int LANES>
-__global__ void __launch_bounds__(kThreads) gated_norm_back_kernel(GatedArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) gated_norm_back_kernel(GatedArgs a) {
     __shared__ float sw[kThreads][8];
     const int c = 8 * (threadIdx.x % LANES);
-    float w[8] = {}, dw[8] = {};
-    if (c < a.d) ld8<T>(static_cast<const T*>(a.w) + c, w);
+    const float inv_d = 1.f / a.d;
+    Raw8<T> w;
+    float dw[8] = {};
+    w.zero();
+    if (c < a.d) w.load(static_cast<const T*>(a.w) + c);
     const long long step = (long long)gridDim.x * (kThreads / LANES);
-    // whole warps stay in the loop together: the bound is the one of the CTA's first row
-    for (long long base = (long long)blockIdx.x * (kThreads / LANES); base < a.rows; base += step) {
-        const long long row = base + threadIdx.x / LANES;
-        const bool in = row < a.rows && c < a.d;
-        float o[8] = {}, z[8] = {}, dy[8] = {};
-        if (in) {
-            ld8<TO>(static_cast<const TO*>(a.o) + row * a.d + c, o);
-            ld8<T>(static_cast<const T*>(a.z) + row * a.d + c, z);
-            ld8<T>(static_cast<const T*>(a.dy) + row * a.d + c, dy);
+    Raw8<TO> on;
+    Raw8<T> zn, yn;
+    auto load = [&](long long row) {
+        on.zero();
+        zn.zero();
+        yn.zero();
+        if (row < a.rows && c < a.d) {
+            on.load(static_cast<const TO*>(a.o) + row * a.d + c);
+            zn.load(static_cast<const T*>(a.z) + row * a.d + c);
+            yn.load(static_cast<const T*>(a.dy) + row * a.d + c);
         }
-        float s = 0.f, t = 0.f;
+    };
+    // whole warps stay in the loop together: the bound is the one of the CTA's first row
+    const long long mine = threadIdx.x / LANES;
+    long long base = (long long)blockIdx.x * (kThreads / LANES);
+    load(base + mine);
+    for (; base < a.rows; base += step) {
+        const long long row = base + mine;
+        const Raw8<TO> o = on;
+        const Raw8<T> z = zn, y = yn;
+        load(row + step);                                // the next row's reads, before this one's sums wait
+        float s = 0.f, t = 0.f, sg[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float sg = sigmoid(z[i]), silu = z[i] * sg, wy = dy[i] * w[i];
+            sg[i] = sigmoid<T>(z[i]);
             s = fmaf(o[i], o[i], s);
-            t = fmaf(o[i], wy * silu, t);
-            z[i] = sg * fmaf(z[i], 1.f - sg, 1.f);       // silu'
-            dy[i] = dy[i] * silu;                        // the norm's own gradient, before w
+            t = fmaf(o[i], y[i] * w[i] * (z[i] * sg[i]), t);
         }
-        const float r = rsqrtf(lanes_sum<LANES>(s) / a.d + a.eps);
-        const float m = lanes_sum<LANES>(t) * r / a.d;   // mean of n dn
+        const float r = rsqrtf(lanes_sum<LANES>(s) * inv_d + a.eps);
+        const float m = lanes_sum<LANES>(t) * r * inv_d;     // mean of n dn
         float g[8], dz[8];
-        if (in) {
-            float y[8];
-            ld8<T>(static_cast<const T*>(a.dy) + row * a.d + c, y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float n = o[i] * r;
-                g[i] = r * (dy[i] * w[i] - n * m);
-                dz[i] = y[i] * n * w[i] * z[i];
-                dw[i] = fmaf(dy[i], n, dw[i]);
-            }
+        for (int i = 0; i < 8; ++i) {
+            const float n = o[i] * r, silu = z[i] * sg[i], dn = y[i] * silu;     // dn: before w
+            g[i] = r * (dn * w[i] - n * m);
+            dz[i] = y[i] * n * w[i] * (sg[i] * fmaf(z[i], 1.f - sg[i], 1.f));    // silu' = sg (1 + z (1 - sg))
+            dw[i] = fmaf(dn, n, dw[i]);
+        }
+        if (row < a.rows && c < a.d) {
             st8<TO>(static_cast<TO*>(a.dout) + row * a.d + c, g);
             st8<T>(static_cast<T*>(a.dz) + row * a.d + c, dz);
         }
@@ -131,27 +175,39 @@ __global__ void __launch_bounds__(kThreads) gated_norm_back_kernel(GatedArgs a) 
         for (int g = 0; g < kThreads / LANES; ++g) s += sw[g * LANES + x / 8][x % 8];
         a.part[(size_t)blockIdx.x * a.d + x] = s;
     }
+    griddep_launch();
 }
 
-// Column sums of `n` rows of partial sums, up to three arrays of them behind one another.
-__global__ void __launch_bounds__(256) sum_rows_kernel(const float* part, int n, int D, float* out0, float* out1, float* out2) {
-    __shared__ float sm[8][32];
-    const int x = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
-    float* out = blockIdx.y == 0 ? out0 : blockIdx.y == 1 ? out1 : out2;
+// Column sums of `n` rows of partial sums, 32 columns to a CTA, its warps' rows added in their order;
+// of a second array behind the first too, times each of two rows of weights.
+template <typename T>
+__global__ void __launch_bounds__(1024) sum_rows_kernel(const float* part, int n, int D, float* out, const T* f1, float* out1,
+                                                        const T* f2, float* out2) {
+    __shared__ float sm[32][33];
+    const int lane = threadIdx.x & 31, g = threadIdx.x >> 5, x = blockIdx.x * 32 + lane;
     const float* p = part + (size_t)blockIdx.y * n * D;
     float s = 0.f;
+    griddep_wait();
     if (x < D)
-        for (int i = g; i < n; i += 8) s += p[(size_t)i * D + x];
-    sm[g][threadIdx.x & 31] = s;
+#pragma unroll 8
+        for (int i = g; i < n; i += 32) s += p[(size_t)i * D + x];
+    sm[g][lane] = s;
     __syncthreads();
-    if (g == 0 && x < D) {
-        for (int i = 1; i < 8; ++i) s += sm[i][threadIdx.x & 31];
-        out[x] = s;
+    // warp w: column w's 32 sums
+    s = warp_sum(sm[lane][g]);
+    const int c = blockIdx.x * 32 + g;
+    if (lane == 0 && c < D) {
+        if (blockIdx.y == 0) {
+            out[c] = s;
+        } else {
+            out1[c] = s * ld_elem<T>(f1, c);
+            out2[c] = s * ld_elem<T>(f2, c);
+        }
     }
 }
 
 // ---------------------------------------------------------------------------
-// block norm: a row of D values by a warp (D <= 1024) or by the whole CTA
+// block norm: a row of D values by the TPR threads of a CTA, or (TPR 32) by one of its eight warps
 // ---------------------------------------------------------------------------
 struct BlockArgs {
     const void *x, *z, *wp, *gate, *w, *dh, *dx2;
@@ -162,12 +218,15 @@ struct BlockArgs {
     float eps, rho;
 };
 
-// Sums of N values over a row's threads (a warp or the CTA); every thread gets them.
-template <bool CTA, int N>
-__device__ __forceinline__ void row_sums(float (&s)[N], float (*sm)[kThreads / 32]) {
+template <int TPR>
+constexpr int kBlockThreads = TPR == 32 ? 256 : TPR;
+
+// Sums of N values over a row's threads; every thread gets them.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sums(float (&s)[N], float (*sm)[16]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) s[i] = warp_sum(s[i]);
-    if constexpr (CTA) {
+    if constexpr (TPR > 32) {
         __syncthreads();                     // the last reduction's reads are done
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
@@ -177,51 +236,56 @@ __device__ __forceinline__ void row_sums(float (&s)[N], float (*sm)[kThreads / 3
         for (int i = 0; i < N; ++i) {
             float t = 0.f;
 #pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w) t += sm[i][w];
+            for (int w = 0; w < TPR / 32; ++w) t += sm[i][w];
             s[i] = t;
         }
     }
 }
 
-template <typename T, bool CTA, int V, bool POST>
-__global__ void __launch_bounds__(kThreads) block_norm_kernel(BlockArgs a) {
-    __shared__ float sm[3][kThreads / 32];
-    constexpr int TPR = CTA ? kThreads : 32, RPC = kThreads / TPR;
+template <typename T, int TPR, int V, bool POST>
+__global__ void __launch_bounds__(kBlockThreads<TPR>) block_norm_kernel(BlockArgs a) {
+    __shared__ float sm[1][16];
+    constexpr int RPC = kBlockThreads<TPR> / TPR;
     const int t = threadIdx.x % TPR;
     const long long row = (long long)blockIdx.x * RPC + threadIdx.x / TPR;
     if (row >= a.rows) return;               // a whole warp, or nobody
     float x[V][8];
     float s[1] = {0.f};
     const T* xr = static_cast<const T*>(a.x) + row * a.D;
+    Raw8<T> w[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = 8 * (t + i * TPR);
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
-        if (c < a.D) ld8<T>(xr + c, x[i]);
+        w[i].zero();
+        if (c < a.D) {
+            ld8<T>(xr + c, x[i]);
+            w[i].load(static_cast<const T*>(a.w) + c);
+        }
     }
     if constexpr (POST) {
-        float z[V][8];
+        Raw8<T> z[V], wp[V], g[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = 8 * (t + i * TPR);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) z[i][j] = 0.f;
-            if (c < a.D) ld8<T>(static_cast<const T*>(a.z) + row * a.D + c, z[i]);
+            z[i].zero();
+            if (c < a.D) {
+                z[i].load(static_cast<const T*>(a.z) + row * a.D + c);
+                wp[i].load(static_cast<const T*>(a.wp) + c);
+                g[i].load(static_cast<const T*>(a.gate) + c);
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[0] = fmaf(z[i][j], z[i][j], s[0]);
         }
-        row_sums<CTA, 1>(s, sm);
+        row_sums<TPR, 1>(s, sm);
         const float r = rsqrtf(s[0] / a.D + a.eps);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = 8 * (t + i * TPR);
             if (c < a.D) {
-                float w[8], g[8];
-                ld8<T>(static_cast<const T*>(a.wp) + c, w);
-                ld8<T>(static_cast<const T*>(a.gate) + c, g);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[i][j] = fmaf(g[j], z[i][j] * r * w[j], a.rho * x[i][j]);
+                for (int j = 0; j < 8; ++j) x[i][j] = fmaf(g[i][j], z[i][j] * r * wp[i][j], a.rho * x[i][j]);
                 st8<T>(static_cast<T*>(a.x2) + row * a.D + c, x[i]);
             }
         }
@@ -231,106 +295,126 @@ __global__ void __launch_bounds__(kThreads) block_norm_kernel(BlockArgs a) {
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[0] = fmaf(x[i][j], x[i][j], s[0]);
-    row_sums<CTA, 1>(s, sm);
+    row_sums<TPR, 1>(s, sm);
     const float r = rsqrtf(s[0] / a.D + a.eps);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = 8 * (t + i * TPR);
         if (c < a.D) {
-            float w[8];
-            ld8<T>(static_cast<const T*>(a.w) + c, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[i][j] *= r * w[j];
+            for (int j = 0; j < 8; ++j) x[i][j] *= r * w[i][j];
             st8<T>(static_cast<T*>(a.h) + row * a.D + c, x[i]);
         }
     }
 }
 
-template <typename T, bool CTA, int V, bool POST>
-__global__ void __launch_bounds__(kThreads) block_norm_back_kernel(BlockArgs a) {
-    __shared__ float sm[3][kThreads / 32];
-    constexpr int TPR = CTA ? kThreads : 32, RPC = kThreads / TPR;
+// With n = x' r, y = dh w, m = mean(y n), k = gamma w_post and n_z = z r_z:
+//   d = dx' + r (y - n m),  dx = rho d,  dz = r_z (d k - n_z mean(d k n_z)).
+// The last mean needs d, which needs the sums of the row before: it is put together from sums that
+// do not, of dx' k z, y k z and x' k z, so that a row waits for one reduction, not for two.
+// The gradients of w_post and gamma are one sum, of d n_z, times the other of the two.
+template <typename T, int TPR, int V, bool POST>
+__global__ void __launch_bounds__(kBlockThreads<TPR>) block_norm_back_kernel(BlockArgs a) {
+    __shared__ float sm[6][16];
+    constexpr int RPC = kBlockThreads<TPR> / TPR;
+    constexpr int VP = POST ? V : 1;
     const int t = threadIdx.x % TPR;
-    float dw[V][8] = {}, dwp[POST ? V : 1][8] = {}, dg[POST ? V : 1][8] = {};
-    for (long long row = (long long)blockIdx.x * RPC + threadIdx.x / TPR; row < a.rows; row += (long long)gridDim.x * RPC) {
-        float x[V][8], y[V][8], z[POST ? V : 1][8];
-        float s[3] = {0.f, 0.f, 0.f};
+    const float inv_d = 1.f / a.D;
+    float dw[V][8] = {}, de[VP][8] = {};
+    Raw8<T> xn[V], yn[V], dn[V], zn[VP], w[V], wp[VP], gt[VP];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = 8 * (t + i * TPR);
-            const size_t at = (size_t)row * a.D + c;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[i][j] = y[i][j] = 0.f;
-                if constexpr (POST) z[i][j] = 0.f;
-            }
-            if (c < a.D) {
-                float w[8];
-                ld8<T>(static_cast<const T*>(a.x) + at, x[i]);
-                ld8<T>(static_cast<const T*>(a.dh) + at, y[i]);
-                ld8<T>(static_cast<const T*>(a.w) + c, w);
-                if constexpr (POST) ld8<T>(static_cast<const T*>(a.z) + at, z[i]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    s[0] = fmaf(x[i][j], x[i][j], s[0]);
-                    s[1] = fmaf(x[i][j], y[i][j] * w[j], s[1]);
-                    if constexpr (POST) s[2] = fmaf(z[i][j], z[i][j], s[2]);
-                }
-            }
-        }
-        row_sums<CTA, 3>(s, sm);
-        const float r = rsqrtf(s[0] / a.D + a.eps), m = s[1] * r / a.D;
-        const float rz = POST ? rsqrtf(s[2] / a.D + a.eps) : 0.f;
-        float u[1] = {0.f};
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = 8 * (t + i * TPR);
-            const size_t at = (size_t)row * a.D + c;
-            if (c < a.D) {
-                float w[8], d[8] = {}, dx[8];
-                ld8<T>(static_cast<const T*>(a.w) + c, w);
-                if (a.dx2 != nullptr) ld8<T>(static_cast<const T*>(a.dx2) + at, d);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float n = x[i][j] * r;
-                    dw[i][j] = fmaf(y[i][j], n, dw[i][j]);
-                    d[j] += r * (y[i][j] * w[j] - n * m);
-                    dx[j] = a.rho * d[j];
-                }
-                st8<T>(static_cast<T*>(a.dx) + at, dx);
-                if constexpr (POST) {
-                    float wp[8], g[8];
-                    ld8<T>(static_cast<const T*>(a.wp) + c, wp);
-                    ld8<T>(static_cast<const T*>(a.gate) + c, g);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float n = z[i][j] * rz;
-                        dwp[i][j] = fmaf(d[j] * g[j], n, dwp[i][j]);
-                        dg[i][j] = fmaf(d[j] * wp[j], n, dg[i][j]);
-                        x[i][j] = d[j] * g[j] * wp[j];
-                        u[0] = fmaf(x[i][j], n, u[0]);
-                    }
-                }
-            }
-        }
+    for (int i = 0; i < V; ++i) {
+        const int c = 8 * (t + i * TPR);
+        w[i].zero();
+        if (c < a.D) w[i].load(static_cast<const T*>(a.w) + c);
         if constexpr (POST) {
-            row_sums<CTA, 1>(u, sm);
-            const float mz = u[0] / a.D;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = 8 * (t + i * TPR);
-                if (c < a.D) {
-                    float dz[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) dz[j] = rz * (x[i][j] - z[i][j] * rz * mz);
-                    st8<T>(static_cast<T*>(a.dz) + (size_t)row * a.D + c, dz);
-                }
+            wp[i].zero();
+            gt[i].zero();
+            if (c < a.D) {
+                wp[i].load(static_cast<const T*>(a.wp) + c);
+                gt[i].load(static_cast<const T*>(a.gate) + c);
             }
         }
     }
-    // partial sums [3][gridDim.x][D]; the warps of a CTA in their order
+    auto load = [&](long long row) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = 8 * (t + i * TPR);
+            const size_t at = (size_t)row * a.D + c;
+            xn[i].zero();
+            yn[i].zero();
+            dn[i].zero();
+            if constexpr (POST) zn[i].zero();
+            if (c < a.D && row < a.rows) {
+                xn[i].load(static_cast<const T*>(a.x) + at);
+                yn[i].load(static_cast<const T*>(a.dh) + at);
+                if (a.dx2 != nullptr) dn[i].load(static_cast<const T*>(a.dx2) + at);
+                if constexpr (POST) zn[i].load(static_cast<const T*>(a.z) + at);
+            }
+        }
+    };
+    const long long step = (long long)gridDim.x * RPC;
+    long long row = (long long)blockIdx.x * RPC + threadIdx.x / TPR;
+    load(row);
+    for (; row < a.rows; row += step) {
+        Raw8<T> x[V], y[V], dx2[V], z[VP];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i] = xn[i];
+            y[i] = yn[i];
+            dx2[i] = dn[i];
+            if constexpr (POST) z[i] = zn[i];
+        }
+        if (V == 1) load(row + step);                    // the next row's reads, before this one's sums wait
+        float s[POST ? 6 : 2] = {};
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float yw = y[i][j] * w[i][j];
+                s[0] = fmaf(x[i][j], x[i][j], s[0]);
+                s[1] = fmaf(x[i][j], yw, s[1]);
+                if constexpr (POST) {
+                    const float kz = gt[i][j] * wp[i][j] * z[i][j];
+                    s[2] = fmaf(z[i][j], z[i][j], s[2]);
+                    s[3] = fmaf(dx2[i][j], kz, s[3]);
+                    s[4] = fmaf(yw, kz, s[4]);
+                    s[5] = fmaf(x[i][j], kz, s[5]);
+                }
+            }
+        row_sums<TPR, POST ? 6 : 2>(s, sm);
+        const float r = rsqrtf(s[0] * inv_d + a.eps), m = s[1] * r * inv_d;
+        float rz = 0.f, mz = 0.f;
+        if constexpr (POST) {
+            rz = rsqrtf(s[2] * inv_d + a.eps);
+            mz = rz * inv_d * (s[3] + r * (s[4] - r * m * s[5]));
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = 8 * (t + i * TPR);
+            const size_t at = (size_t)row * a.D + c;
+            float dx[8], dz[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float n = x[i][j] * r, d = dx2[i][j] + r * (y[i][j] * w[i][j] - n * m);
+                dw[i][j] = fmaf(y[i][j], n, dw[i][j]);
+                dx[j] = a.rho * d;
+                if constexpr (POST) {
+                    const float nz = z[i][j] * rz;
+                    de[i][j] = fmaf(d, nz, de[i][j]);
+                    dz[j] = rz * (d * gt[i][j] * wp[i][j] - nz * mz);
+                }
+            }
+            if (c < a.D) {
+                st8<T>(static_cast<T*>(a.dx) + at, dx);
+                if constexpr (POST) st8<T>(static_cast<T*>(a.dz) + at, dz);
+            }
+        }
+        if (V > 1) load(row + step);
+    }
+    // partial sums [2][gridDim.x][D]; the warps of a CTA in their order
     extern __shared__ float acc[];
-    for (int p = 0; p < (POST ? 3 : 1); ++p) {
+    for (int p = 0; p < (POST ? 2 : 1); ++p) {
         float* out = a.part + ((size_t)p * gridDim.x + blockIdx.x) * a.D;
         for (int g = 0; g < RPC; ++g) {
             if (threadIdx.x / TPR == g)
@@ -341,16 +425,17 @@ __global__ void __launch_bounds__(kThreads) block_norm_back_kernel(BlockArgs a) 
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             float v = dw[i][j];
-                            if constexpr (POST) v = p == 0 ? v : p == 1 ? dwp[i][j] : dg[i][j];
-                            if constexpr (CTA) out[c + j] = v;
+                            if constexpr (POST) v = p == 0 ? v : de[i][j];
+                            if constexpr (TPR > 32) out[c + j] = v;
                             else if (g == 0) acc[c + j] = v;
                             else if (g < RPC - 1) acc[c + j] += v;
                             else out[c + j] = acc[c + j] + v;
                         }
                 }
-            if constexpr (!CTA) __syncthreads();
+            if constexpr (TPR == 32) __syncthreads();
         }
     }
+    griddep_launch();
 }
 
 // ---------------------------------------------------------------------------
@@ -360,11 +445,11 @@ template <typename TO, typename T, int LANES>
 cudaError_t gated_go(const GatedArgs& a, float* dw, bool back, cudaStream_t st) {
     const long long per = kThreads / LANES, ctas = (a.rows + per - 1) / per;
     if (!back) return launch_kernel(gated_norm_kernel<TO, T, LANES>, dim3((unsigned)ctas), dim3(kThreads), 0, st, false, a);
-    const int n = (int)(ctas < kPartialRows ? ctas : kPartialRows);
+    const int n = (int)(ctas < kGatedCtas ? ctas : kGatedCtas);
     cudaError_t e = launch_kernel(gated_norm_back_kernel<TO, T, LANES>, dim3((unsigned)n), dim3(kThreads), 0, st, false, a);
     if (e != cudaSuccess) return e;
-    return launch_kernel(sum_rows_kernel, dim3((a.d + 31) / 32, 1), dim3(256), 0, st, false, (const float*)a.part, n, a.d, dw,
-                         (float*)nullptr, (float*)nullptr);
+    return launch_kernel(sum_rows_kernel<T>, dim3((a.d + 31) / 32, 1), dim3(1024), 0, st, true, (const float*)a.part, n, a.d, dw,
+                         (const T*)nullptr, (float*)nullptr, (const T*)nullptr, (float*)nullptr);
 }
 
 template <typename TO, typename T>
@@ -384,27 +469,27 @@ cudaError_t gated(const GatedArgs& a, float* dw, bool back, int odtype, int dtyp
                                   : gated_lanes<__nv_bfloat16, __nv_bfloat16>(a, dw, back, st);
 }
 
-template <typename T, bool CTA, int V, bool POST>
+template <typename T, int TPR, int V, bool POST>
 cudaError_t block_go(const BlockArgs& a, float* dw, float* dwp, float* dgate, bool back, cudaStream_t st) {
-    const long long per = CTA ? 1 : kThreads / 32, ctas = (a.rows + per - 1) / per;
-    if (!back) return launch_kernel(block_norm_kernel<T, CTA, V, POST>, dim3((unsigned)ctas), dim3(kThreads), 0, st, false, a);
-    const int n = (int)(ctas < kPartialRows ? ctas : kPartialRows);
-    cudaError_t e = launch_kernel(block_norm_back_kernel<T, CTA, V, POST>, dim3((unsigned)n), dim3(kThreads),
-                                  CTA ? 0 : (size_t)a.D * 4, st, false, a);
+    constexpr int threads = kBlockThreads<TPR>;
+    const long long per = threads / TPR, ctas = (a.rows + per - 1) / per;
+    if (!back) return launch_kernel(block_norm_kernel<T, TPR, V, POST>, dim3((unsigned)ctas), dim3(threads), 0, st, false, a);
+    const int n = (int)(ctas < block_ctas(threads) ? ctas : block_ctas(threads));
+    cudaError_t e = launch_kernel(block_norm_back_kernel<T, TPR, V, POST>, dim3((unsigned)n), dim3(threads),
+                                  TPR == 32 ? (size_t)a.D * 4 : 0, st, false, a);
     if (e != cudaSuccess) return e;
-    return launch_kernel(sum_rows_kernel, dim3((a.D + 31) / 32, POST ? 3 : 1), dim3(256), 0, st, false, (const float*)a.part,
-                         n, a.D, dw, dwp, dgate);
+    return launch_kernel(sum_rows_kernel<T>, dim3((a.D + 31) / 32, POST ? 2 : 1), dim3(1024), 0, st, true, (const float*)a.part, n,
+                         a.D, dw, static_cast<const T*>(a.gate), dwp, static_cast<const T*>(a.wp), dgate);
 }
 
-// V vectors of eight values per thread: the fewest that hold the row
+// The fewest threads that hold a row in one vector of eight values each, from 4096 values on in two
 template <typename T, bool POST>
 cudaError_t block_v(const BlockArgs& a, float* dw, float* dwp, float* dgate, bool back, cudaStream_t st) {
-    if (a.D <= 256) return block_go<T, false, 1, POST>(a, dw, dwp, dgate, back, st);
-    if (a.D <= 512) return block_go<T, false, 2, POST>(a, dw, dwp, dgate, back, st);
-    if (a.D <= 1024) return block_go<T, false, 4, POST>(a, dw, dwp, dgate, back, st);
-    if (a.D <= 2048) return block_go<T, true, 1, POST>(a, dw, dwp, dgate, back, st);
-    if (a.D <= 4096) return block_go<T, true, 2, POST>(a, dw, dwp, dgate, back, st);
-    return block_go<T, true, 4, POST>(a, dw, dwp, dgate, back, st);
+    if (a.D <= 256) return block_go<T, 32, 1, POST>(a, dw, dwp, dgate, back, st);
+    if (a.D <= 1024) return block_go<T, 128, 1, POST>(a, dw, dwp, dgate, back, st);
+    if (a.D <= 2048) return block_go<T, 256, 1, POST>(a, dw, dwp, dgate, back, st);
+    if (a.D <= 4096) return block_go<T, 512, 1, POST>(a, dw, dwp, dgate, back, st);
+    return block_go<T, 512, 2, POST>(a, dw, dwp, dgate, back, st);
 }
 
 cudaError_t block(const BlockArgs& a, float* dw, float* dwp, float* dgate, bool back, int dtype, cudaStream_t st) {
@@ -414,7 +499,7 @@ cudaError_t block(const BlockArgs& a, float* dw, float* dwp, float* dgate, bool 
                           : block_v<__nv_bfloat16, false>(a, dw, dwp, dgate, back, st);
 }
 
-constexpr int kMaxWidth = 8192;          // D of the block norm: four vectors for each of 256 threads
+constexpr int kMaxWidth = 8192;          // D of the block norm: two vectors for each of 512 threads
 constexpr long long kMaxRows = 1LL << 31;
 
 bool given(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -457,7 +542,8 @@ extern "C" {
 
 int gdn_norm_workspace_bytes(long long rows, int width, size_t* bytes) {
     if (bytes == nullptr || !block_ok(rows, width, 1.f)) return GDN_ERR_ARG;
-    *bytes = align_up((size_t)(rows < kPartialRows ? rows : kPartialRows) * 3 * width * 4, kSectionAlign);
+    const long long most = block_ctas(width <= 1024 ? 128 : width <= 2048 ? 256 : 512);
+    *bytes = align_up((size_t)(rows < most ? rows : most) * 2 * width * 4, kSectionAlign);
     return GDN_OK;
 }
 

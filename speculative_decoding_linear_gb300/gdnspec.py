@@ -137,24 +137,27 @@ def _ptr(x):
 # The current stream as a raw handle without building a Stream object (a few
 # microseconds per call otherwise, more than a chain verification on the GPU).
 _raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None:
         if _raw_current_stream is not None:
-            return _raw_current_stream(torch.cuda.current_device())
+            return _raw_current_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
 
 
+_DTYPE_CODES = {torch.bfloat16: DTYPE_BF16, "bf16": DTYPE_BF16, torch.float32: DTYPE_F32, "f32": DTYPE_F32}
+
+
 def dtype_code(t) -> int:
-    if t in (torch.bfloat16, "bf16"):
-        return DTYPE_BF16
-    if t in (torch.float32, "f32"):
-        return DTYPE_F32
-    raise ValueError("q/k/v must be bf16 or fp32, got %s" % (t,))
+    code = _DTYPE_CODES.get(t)
+    if code is None:
+        raise ValueError("q/k/v must be bf16 or fp32, got %s" % (t,))
+    return code
 
 
 # ---------------------------------------------------------------------------
@@ -490,7 +493,7 @@ def _seq_dims(q, k, v, log_alpha, beta, offsets):
 
 
 def _same(x, shape, dtype, what):
-    if x is not None and (tuple(x.shape) != tuple(shape) or x.dtype != dtype):
+    if x is not None and (x.shape != shape or x.dtype is not dtype):
         raise ValueError("%s must be %s %s" % (what, dtype, tuple(shape)))
 
 
@@ -540,17 +543,24 @@ def gdn_seq_backward(q, k, v, log_alpha, beta, dout, dS_T, record, dq, dk, dv, d
 def gdn_seq_step(q, k, v, log_alpha, beta, S, out, state_index=None, stream=None):
     """One token for each of B sequences, the states S [slots, H, dv, dk] fp32 updated in place (see
     include/gdnspec.h); state_index int32 [B], -1 for an empty row."""
-    B, Hk, dk = q.shape
-    H, dv = v.shape[-2:]
-    if k.shape != q.shape or v.shape[0] != B or k.dtype != q.dtype or v.dtype != q.dtype:
+    qs, vs, ss, t, f32 = q.shape, v.shape, S.shape, q.dtype, torch.float32
+    B, Hk, dk = qs
+    _, H, dv = vs
+    if k.shape != qs or vs[0] != B or k.dtype is not t or v.dtype is not t:
         raise ValueError("q, k [B, Hk, dk] and v [B, H, dv] must agree in B and type")
-    _same(log_alpha, (B, H), torch.float32, "log_alpha")
-    _same(beta, (B, H), torch.float32, "beta")
-    _same(S, (S.shape[0], H, dv, dk), torch.float32, "S")
-    _same(out, v.shape, v.dtype, "out")
-    _same(state_index, (B,), torch.int32, "state_index")
-    _check(lib().gdn_seq_step(_ptr(q), _ptr(k), _ptr(v), dtype_code(q.dtype), _ptr(log_alpha), _ptr(beta), _ptr(S),
-                              _ptr(state_index), _ptr(out), B, S.shape[0], H, Hk, dk, dv, _stream(stream)), "gdn_seq_step")
+    gates = vs[:2]
+    if log_alpha.shape != gates or beta.shape != gates or log_alpha.dtype is not f32 or beta.dtype is not f32:
+        raise ValueError("log_alpha and beta must be fp32 %s" % (tuple(gates),))
+    if len(ss) != 4 or ss[1:] != (H, dv, dk) or S.dtype is not f32:
+        raise ValueError("S must be fp32 [slots, %d, %d, %d]" % (H, dv, dk))
+    if out.shape != vs or out.dtype is not t:
+        raise ValueError("out must be %s %s" % (t, tuple(vs)))
+    if state_index is not None and (state_index.shape != (B,) or state_index.dtype is not torch.int32):
+        raise ValueError("state_index must be int32 [%d]" % B)
+    rc = lib().gdn_seq_step(_ptr(q), _ptr(k), _ptr(v), dtype_code(q.dtype), _ptr(log_alpha), _ptr(beta), _ptr(S),
+                            _ptr(state_index), _ptr(out), B, ss[0], H, Hk, dk, dv, _stream(stream))
+    if rc != OK:
+        raise GdnError(rc, "gdn_seq_step")
 
 
 def empty_norm_workspace(rows, width, device="cuda"):
