@@ -345,3 +345,50 @@ def test_long_batch_gives_equal_bits_and_exact_gates():
                             dS_T=dS[1:2, 2:4].double().cpu().numpy())
     for m in OUT:
         check(d[m][1:2, 2:4] if m == "S0" else d[m][a:b, 2:4], want[m], "d" + m, 256 + 256 + 64)
+
+
+def test_rows_that_start_on_16_bytes_only():
+    """Outputs and inputs whose rows are not 32-byte aligned take the narrower accesses."""
+    lengths = [70, 65]
+    x, off = make(lengths, 2, 2, 128, 128, "bf16", seed=13)
+    out, S_T, ws, rec = forward(x, off, record=True)
+    dout = torch.randn_like(out)
+    d = backward(x, off, dout, None, ws, rec)
+
+    def shifted(y):
+        z = torch.empty(y.numel() + 8, dtype=y.dtype, device="cuda")[8:].view(y.shape)
+        return z.copy_(y)
+    x2 = dict(x, **{m: shifted(x[m]) for m in ("q", "k", "v")})
+    o2, dv2, dq2, dk2 = shifted(out), shifted(out), shifted(x["q"]), shifted(x["k"])
+    for y in (o2, dv2, dq2, dk2):
+        y.zero_()
+    S2 = torch.empty_like(S_T)
+    gdnspec.gdn_seq_forward(x2["q"], x2["k"], x2["v"], x["log_alpha"], x["beta"], x["S0"], o2, S2, ws, offsets=off, record=rec)
+    assert torch.equal(out, o2) and torch.equal(S_T, S2)
+    g = {m: torch.empty_like(x[m]) for m in ("log_alpha", "beta", "S0")}
+    gdnspec.gdn_seq_backward(x2["q"], x2["k"], x2["v"], x["log_alpha"], x["beta"], shifted(dout), None, rec, dq2, dk2, dv2, g["log_alpha"],
+                             g["beta"], g["S0"], ws, offsets=off)
+    assert torch.equal(dv2, d["v"]) and torch.equal(dq2, d["q"]) and torch.equal(dk2, d["k"])
+    for m in g:
+        assert torch.equal(g[m], d[m])
+
+
+def test_what_lies_behind_a_sequence_stays_out():
+    """NaN and infinities in one sequence's tokens reach no other sequence."""
+    lengths = [70, 64, 33]
+    x, off = make(lengths, 2, 1, 128, 128, "bf16", seed=17)
+    out, S_T, ws, rec = forward(x, off, record=True)
+    dout = torch.randn_like(out)
+    d = backward(x, off, dout, None, ws, rec)
+    y = {m: v.clone() for m, v in x.items()}
+    y["q"][70:134], y["k"][70:100], y["v"][80:134] = float("nan"), float("inf"), float("nan")
+    y["beta"][70:], y["log_alpha"][70:134] = x["beta"][70:], x["log_alpha"][70:134]
+    dout2 = dout.clone()
+    dout2[70:134] = float("nan")
+    o2, S2, ws2, rec2 = forward(y, off, record=True)
+    d2 = backward(y, off, dout2, None, ws2, rec2)
+    clean = torch.cat([torch.arange(70), torch.arange(134, 167)]).cuda()
+    assert torch.equal(out[clean], o2[clean]) and torch.equal(S_T[[0, 2]], S2[[0, 2]])
+    for m in OUT[:-1]:
+        assert torch.equal(d[m][clean], d2[m][clean]), m
+    assert torch.equal(d["S0"][[0, 2]], d2["S0"][[0, 2]])
