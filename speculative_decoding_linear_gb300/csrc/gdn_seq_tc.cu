@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(kPrepThreads, REC ? 2 : 3)
         mbar_expect_tx(bar, G::kKQ);
 #pragma unroll
         for (int b = 0; b < DK / 64; ++b) {
-            tma_2d(base + b * G::kTile, &tmK, hk * DK + 64 * b, first, bar);
-            tma_2d(base + b * G::kTile + 8192, &tmQ, hk * DK + 64 * b, first, bar);
+            tma_3d(base + b * G::kTile, &tmK, 64 * b, hk, first, bar);
+            tma_3d(base + b * G::kTile + 8192, &tmQ, 64 * b, hk, first, bar);
         }
     }
     if (warp == 1) tmem_alloc(smem_u32(holder), 128);
@@ -441,8 +441,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             auto prefetch = [&](int c) {
 #pragma unroll
                 for (int b = 0; b < DK / 64; ++b) {
-                    tma_prefetch_2d(&tmK, hk * DK + 64 * b, first + c * kChunk);
-                    tma_prefetch_2d(&tmQ, hk * DK + 64 * b, first + c * kChunk);
+                    tma_prefetch_3d(&tmK, 64 * b, hk, first + c * kChunk);
+                    tma_prefetch_3d(&tmQ, 64 * b, hk, first + c * kChunk);
                 }
                 tma_prefetch_2d(&tmV, h * sh.dv + v0, first + c * kChunk);
             };
@@ -456,13 +456,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 mbar_expect_tx(f, DK * 128 + kGateFwd);
 #pragma unroll
                 for (int b = 0; b < DK / 64; ++b)
-                    tma_2d(base + (c & 1) * 16384 + b * G::kTile, &tmK, hk * DK + 64 * b, first + c * kChunk, f);
+                    tma_3d(base + (c & 1) * 16384 + b * G::kTile, &tmK, 64 * b, hk, first + c * kChunk, f);
                 bulk_copy_g2s(base + G::kG + (c & 1) * kGateFwd, op, kGateFwd, f);
                 issued = c + 1;
                 if (c >= 1 && !wait_or_dead(qe, (c - 1) & 1, a.err, dead)) break;
                 mbar_expect_tx(qf, DK * 128);
 #pragma unroll
-                for (int b = 0; b < DK / 64; ++b) tma_2d(base + 8192 + b * G::kTile, &tmQ, hk * DK + 64 * b, first + c * kChunk, qf);
+                for (int b = 0; b < DK / 64; ++b) tma_3d(base + 8192 + b * G::kTile, &tmQ, 64 * b, hk, first + c * kChunk, qf);
                 q_issued = c + 1;
                 if (c >= 1 && !wait_or_dead(ve, (c - 1) & 1, a.err, dead)) break;
                 mbar_expect_tx(vf, 64 * W);
@@ -552,9 +552,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const bool whole = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;      // 32-byte rows of columns
         float S[SC];
         {
-            const size_t at = (((size_t)s * sh.H + h) * sh.dv + v0 + scol) * DK + srow;
+            const size_t at = (((size_t)s * sh.H + h) * sh.dv + v0 + scol) * sh.dk + srow;
 #pragma unroll
-            for (int j = 0; j < SC; ++j) S[j] = owns && a.S0 != nullptr ? a.S0[at + (size_t)j * DK] : 0.f;
+            for (int j = 0; j < SC; ++j) S[j] = srow < sh.dk && a.S0 != nullptr ? a.S0[at + (size_t)j * sh.dk] : 0.f;
         }
         griddep_wait();
         for (int c = 0; c < chunks; ++c) {
@@ -668,10 +668,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 for (int j = 0; j < kStep; ++j) S[g + j] = fmaf(ee, S[g + j], d[j]);
             }
         }
-        if (a.S_T != nullptr && owns) {
-            const size_t at = (((size_t)s * sh.H + h) * sh.dv + v0 + scol) * DK + srow;
+        if (a.S_T != nullptr && srow < sh.dk) {
+            const size_t at = (((size_t)s * sh.H + h) * sh.dv + v0 + scol) * sh.dk + srow;
 #pragma unroll
-            for (int j = 0; j < SC; ++j) a.S_T[at + (size_t)j * DK] = S[j];
+            for (int j = 0; j < SC; ++j) a.S_T[at + (size_t)j * sh.dk] = S[j];
         }
     }
     griddep_launch();
@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const char* op = ops + ((slot0 + c) * sh.H + h) * kOpRecord;
                 mbar_expect_tx(f, DK * 128 + 64 * W + kGateBwd);
 #pragma unroll
-                for (int b = 0; b < DK / 64; ++b) tma_2d(st + b * G::kTile, &tmK, hk * DK + 64 * b, first + c * kChunk, f);
+                for (int b = 0; b < DK / 64; ++b) tma_3d(st + b * G::kTile, &tmK, 64 * b, hk, first + c * kChunk, f);
                 tma_2d(st + G::kO, &tmO, h * sh.dv + v0, first + c * kChunk, f);
                 bulk_copy_g2s(st + G::kG, op + 4 * kGEg, kGateBwd, f);
                 const size_t at = ((slot0 + c) * sh.H + h) * tiles + tile;     // what the compute warps will read themselves
@@ -897,7 +897,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (i >= 1 && !wait_or_dead(qe, (i - 1) & 1, a.err, dead)) break;
                 mbar_expect_tx(qf, DK * 128);
 #pragma unroll
-                for (int b = 0; b < DK / 64; ++b) tma_2d(base + G::kQ + b * G::kTile, &tmQ, hk * DK + 64 * b, first + c * kChunk, qf);
+                for (int b = 0; b < DK / 64; ++b) tma_3d(base + G::kQ + b * G::kTile, &tmQ, 64 * b, hk, first + c * kChunk, qf);
                 q_issued = i + 1;
                 if (i >= 1 && !wait_or_dead(tpe, (i - 1) & 1, a.err, dead)) break;
                 mbar_expect_tx(tpf, 3 * kOpTerm);
@@ -994,9 +994,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const bool owns = srow < DK;
         float S[SC];
         {
-            const size_t at = (((size_t)s * sh.H + h) * sh.dv + v0 + scol) * DK + srow;
+            const size_t at = (((size_t)s * sh.H + h) * sh.dv + v0 + scol) * sh.dk + srow;
 #pragma unroll
-            for (int j = 0; j < SC; ++j) S[j] = owns && a.dS_T != nullptr ? a.dS_T[at + (size_t)j * DK] : 0.f;
+            for (int j = 0; j < SC; ++j) S[j] = srow < sh.dk && a.dS_T != nullptr ? a.dS_T[at + (size_t)j * sh.dk] : 0.f;
         }
         // This CTA's part of <S, dS> at the start of chunk c: N columns from g on of the thread's row, three
         // terms, in S's image, swizzled as it was in shared memory.
@@ -1126,10 +1126,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
         }
         if (chunks > 0) state_dot(0);
-        if (a.dS0 != nullptr && owns) {
-            const size_t at = (((size_t)s * sh.H + h) * sh.dv + v0 + scol) * DK + srow;
+        if (a.dS0 != nullptr && srow < sh.dk) {
+            const size_t at = (((size_t)s * sh.H + h) * sh.dv + v0 + scol) * sh.dk + srow;
 #pragma unroll
-            for (int j = 0; j < SC; ++j) a.dS0[at + (size_t)j * DK] = S[j];
+            for (int j = 0; j < SC; ++j) a.dS0[at + (size_t)j * sh.dk] = S[j];
         }
     }
     griddep_launch();
@@ -1226,8 +1226,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     mbar_expect_tx(kqf, 2 * DK * 128 + kOpGates);
 #pragma unroll
                     for (int b = 0; b < DK / 64; ++b) {
-                        tma_2d(base + b * G::kTile, &tmQ, hk * DK + 64 * b, first, kqf);
-                        tma_2d(base + b * G::kTile + 8192, &tmK, hk * DK + 64 * b, first, kqf);
+                        tma_3d(base + b * G::kTile, &tmQ, 64 * b, hk, first, kqf);
+                        tma_3d(base + b * G::kTile + 8192, &tmK, 64 * b, hk, first, kqf);
                     }
                     bulk_copy_g2s(base + G::kGates, ops + sh_at * kOpRecord, kOpGates, kqf);
                     for (int j = 0; j < 3 * tiles; ++j, ++it) {
@@ -1461,7 +1461,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 wait_or_dead(fin, n & 1, a.err, dead);
                 __syncwarp();
                 tc_fence_after();
-                const size_t at = ((size_t)(first + t) * sh.Hk + hk) * DK;
+                const size_t at = ((size_t)(first + t) * sh.Hk + hk) * sh.dk;
                 __nv_bfloat16* out = static_cast<__nv_bfloat16*>(is_k ? a.dk : a.dq) + at;
                 float* acc = (is_k ? dkf : dqf) + at;
 #pragma unroll 1
@@ -1477,7 +1477,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         float o[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) o[e] = __uint_as_float(x[8 * p + e]) + (is_k ? __uint_as_float(y[8 * p + e]) : 0.f);
-                        if (t < rows) {
+                        if (t < rows && c < sh.dk) {
                             if (rep > 1) {                // the group's heads in their order
                                 float4* f = reinterpret_cast<float4*>(acc + c);
                                 if (r > 0) {
@@ -1540,9 +1540,20 @@ bool token_map(CUtensorMap* m, const void* p, long long total, int width, long l
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of tokens of one q/k head, 64 a box, in boxes of 64 columns: those behind d_k come as zeros, so that
+// a d_k between the kernels' widths is one whose last columns are zero.
+bool head_map(CUtensorMap* m, const void* p, const SeqShape& sh, long long ld) {
+    const auto enc = encode_fn();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)sh.dk, (cuuint64_t)sh.Hk, (cuuint64_t)sh.total},
+                     strides[2] = {(cuuint64_t)sh.dk * 2, (cuuint64_t)ld * 2};
+    const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)kChunk}, estr[3] = {1u, 1u, 1u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool qk_maps(const SeqArgs& a, CUtensorMap* q, CUtensorMap* k) {
-    return token_map(q, a.q, a.sh.total, a.sh.Hk * a.sh.dk, a.sh.ldq, 64, 128) &&
-           token_map(k, a.k, a.sh.total, a.sh.Hk * a.sh.dk, a.sh.ldk, 64, 128);
+    return head_map(q, a.q, a.sh, a.sh.ldq) && head_map(k, a.k, a.sh, a.sh.ldk);
 }
 
 template <int DK, bool REC>
@@ -1610,8 +1621,7 @@ cudaError_t backward_dk(const CUtensorMap& q, const CUtensorMap& k, const SeqArg
 
 }  // namespace
 
-// bf16 with d_k in 64-column tiles
-bool seq_tc_takes(const SeqShape& s, int dtype) { return dtype == GDN_DTYPE_BF16 && s.dk % 64 == 0; }
+bool seq_tc_takes(int dtype) { return dtype == GDN_DTYPE_BF16; }
 
 int seq_tc_cols(const SeqShape& s) {
     return s.dv % 32 == 0 && (size_t)s.nseq * s.H * (s.dv / 16) > kSMs ? 32 : 16;
@@ -1620,7 +1630,7 @@ int seq_tc_cols(const SeqShape& s) {
 cudaError_t launch_seq_forward_tc(const SeqArgs& a, cudaStream_t st) {
     CUtensorMap q, k;
     if (!qk_maps(a, &q, &k)) return cudaErrorInvalidValue;
-    switch (a.sh.dk) {
+    switch (seq_tc_dk(a.sh.dk)) {
         case 64: return forward_dk<64>(q, k, a, st);
         case 128: return forward_dk<128>(q, k, a, st);
         case 192: return forward_dk<192>(q, k, a, st);
@@ -1632,7 +1642,7 @@ cudaError_t launch_seq_backward_tc(const SeqArgs& a, cudaStream_t st) {
     const SeqLayout L = seq_layout(a.sh, GDN_DTYPE_BF16);
     CUtensorMap q, k;
     if (!qk_maps(a, &q, &k)) return cudaErrorInvalidValue;
-    switch (a.sh.dk) {
+    switch (seq_tc_dk(a.sh.dk)) {
         case 64: return backward_dk<64>(q, k, a, L, st);
         case 128: return backward_dk<128>(q, k, a, L, st);
         case 192: return backward_dk<192>(q, k, a, L, st);

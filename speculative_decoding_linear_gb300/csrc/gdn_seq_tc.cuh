@@ -131,6 +131,12 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
     asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
@@ -255,6 +261,11 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, 
                  "r"(c1)
                  : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];\n" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
 
 // ---------------------------------------------------------------------------
 // per (slot, head): what a chunk needs of its gates and of K K^T, Q K^T
@@ -274,7 +285,8 @@ constexpr uint32_t kGateBwd = 784;                          // and the backward 
 
 }  // namespace seqtc
 
-bool seq_tc_takes(const SeqShape& s, int dtype);
+bool seq_tc_takes(int dtype);
+inline int seq_tc_dk(int dk) { return (dk + 63) / 64 * 64; }      // d_k as the kernels keep it: zeros behind
 int seq_tc_cols(const SeqShape& s);      // value columns of a CTA
 cudaError_t launch_seq_forward_tc(const SeqArgs& a, cudaStream_t st);
 cudaError_t launch_seq_backward_tc(const SeqArgs& a, cudaStream_t st);
