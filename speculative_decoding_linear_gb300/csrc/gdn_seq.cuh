@@ -7,6 +7,7 @@
 namespace gdn {
 
 constexpr int kChunk = 64;        // tokens per chunk of the sequence operators
+constexpr int kSMs = 152;
 
 struct SeqShape {
     int nseq, total, H, Hk, dk, dv;
@@ -108,7 +109,7 @@ SeqLayout seq_layout(const SeqShape& s, int dtype);
 // fp32, and stays finite in differences; a NaN stays one.
 __device__ __forceinline__ float gate_log(float la) { return la < -200.f ? -200.f : la; }
 
-cudaError_t launch_seq_forward_simt(const SeqArgs& a, int dtype, cudaStream_t st);
-cudaError_t launch_seq_backward_simt(const SeqArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_seq_forward_f32(const SeqArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_seq_backward_f32(const SeqArgs& a, int dtype, cudaStream_t st);
 
 }  // namespace gdn

@@ -378,7 +378,6 @@ struct FwdGeom {
     static_assert(kCols <= 512 && kSmem <= 227 * 1024, "tile");
 };
 constexpr int kFwdThreads = 320;
-constexpr int kSMs = 152;
 
 // More than one CTA per SM must not ask for more than the 512 columns of its TMEM.
 template <int DK, int NV, int ST>
