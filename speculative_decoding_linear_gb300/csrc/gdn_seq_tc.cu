@@ -1,5 +1,5 @@
-// gdn_seq_tc.cu -- the gated delta rule over packed sequences on the tensor core (bf16 inputs,
-// d_k a multiple of 64): forward pass.
+// gdn_seq_tc.cu -- the gated delta rule over packed sequences on the tensor core (bf16 inputs;
+// d_k is taken up to 64, 128, 192 or 256 with columns of zero): forward and backward pass.
 //
 // In a chunk of C = 64 tokens with start state S (here d_k x d_v), g the cumulative log gate,
 // G_tj = e^{g_t - g_j}, L = strictly lower G (.) K K^T, P = lower G (.) Q K^T:
@@ -33,7 +33,8 @@ namespace {
 // waits for another thread, and what a row adds to those below it is independent of one another.
 // Phat then is a second product.  With a record T = (I + diag(beta) L)^-1 is found beside That by other
 // warps, Ptil = P T, and Phat = Ptil diag(beta) since diag(beta) That = T diag(beta).
-// Bound by the instructions of the exponentials, substitutions and splits.
+// Bound by the instructions of the exponentials, substitutions and splits: 8192 tokens of 8 heads of 256 36 us
+// (100 MB: 2.8 TB/s), with a record 58; one chunk alone 10 us, a chain of its stages.
 constexpr int kPrepThreads = 256;
 constexpr int kLd = kChunk + 4;          // fp32 rows on 16 bytes
 
@@ -355,8 +356,11 @@ __global__ void __launch_bounds__(kPrepThreads, REC ? 2 : 3)
 // ---------------------------------------------------------------------------
 // Ten warps.  Eight compute: a thread owns a row of the state, and a token's row of K (warps
 // 0, 1, 4, 5; in odd chunks the others) or of Q in the token steps, columns halved between warps 0-3
-// and 4-7.  One starts the
-// copies of K, Q, V, the gates and [That; Phat], one issues the products.
+// and 4-7.  One starts the copies of K, Q, V, the gates and [That; Phat], one issues the products.
+//
+// Bound by a chunk's chain: some 1.5 us with 16 columns and heads of 256, of which the three products and their
+// handovers between warps are the larger part.  1 x 8192, 8 heads of 256 (16 columns, 128 CTAs): 196 us.
+// 4 x 2048 (32 columns, 256 CTAs): 142 us, with a record 188.
 template <int DK, int NV, int ST>
 struct FwdGeom {
     static constexpr int kMH = DK > 128 ? 2 : 1;                  // halves of 128 rows of d_k
@@ -387,6 +391,27 @@ constexpr size_t fwd_smem() {
     return G::kSmem > least ? G::kSmem : least;
 }
 
+// The sequence of the r-th place by length, the longest first: a long one that begins when others have ended would
+// work on alone.  In the order given where all CTAs begin at once, lengths are equal or there are too many to count
+// (many sequences even out by themselves).  buf: 1028 bytes of shared memory.  Prep and scan of
+// 24 prompts, 16000 tokens, 8 heads of 128: 169 to 171 us, in the order given 182 to 194; 9 sequences with the
+// longest, of 2000, at the end, 8 heads of 256: 142 against 169.
+constexpr int kMaxRanked = 256;
+__device__ __forceinline__ int seq_by_length(const SeqShape& sh, int r, int* buf) {
+    if (sh.offsets == nullptr || sh.nseq > kMaxRanked || gridDim.x <= kSMs) return r;
+    const int t = threadIdx.x;
+    int n = 0;
+    if (t < sh.nseq) buf[t] = n = (int)((uint32_t)sh.offsets[t + 1] - (uint32_t)sh.offsets[t]);
+    __syncthreads();
+    if (t < sh.nseq) {
+        int rank = 0;
+        for (int j = 0; j < sh.nseq; ++j) rank += buf[j] > n || (buf[j] == n && j < t);
+        if (rank == r) buf[kMaxRanked] = t;
+    }
+    __syncthreads();
+    return warp_uniform(buf[kMaxRanked]);
+}
+
 template <int DK, int NV, int ST>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -404,7 +429,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const SeqShape& sh = a.sh;
     const int tiles = sh.dv / NV;
-    const int tile = blockIdx.x % tiles, h = (blockIdx.x / tiles) % sh.H, s = blockIdx.x / (tiles * sh.H);
+    const int tile = blockIdx.x % tiles, h = (blockIdx.x / tiles) % sh.H;
+    const int s = seq_by_length(sh, blockIdx.x / (tiles * sh.H), reinterpret_cast<int*>(sm + G::kS));
     const int hk = h / (sh.H / sh.Hk), v0 = tile * NV;
     const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
     int first, len;
@@ -696,6 +722,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 //   dbeta_t = w_t.eps_t,   dlog_alpha_t = dlog_alpha_{t+1} + dO_t.o_t - dV_t.v_t,
 // the second since <S_t, dS_t> changes from token to token by just these; its value at a chunk's
 // first token is <S, dS>, S the chunk's start state.  Each CTA writes its columns' parts.
+//
+// Bound like the forward scan by a chunk's chain, 2.3 us with 16 columns and heads of 256: 1 x 8192, 8 heads of 256
+// 289 us, 4 x 2048 (32 columns) 283 us.
 template <int DK, int NV>
 struct BwdGeom {
     static constexpr int kMH = DK > 128 ? 2 : 1;
@@ -748,7 +777,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const SeqShape& sh = a.sh;
     const int tiles = sh.dv / NV;
-    const int tile = blockIdx.x % tiles, h = (blockIdx.x / tiles) % sh.H, s = blockIdx.x / (tiles * sh.H);
+    const int tile = blockIdx.x % tiles, h = (blockIdx.x / tiles) % sh.H;
+    const int s = seq_by_length(sh, blockIdx.x / (tiles * sh.H), reinterpret_cast<int*>(sm + G::kS));
     const int hk = h / (sh.H / sh.Hk), v0 = tile * NV;
     const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
     int first, len;
@@ -1153,7 +1183,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // The gates' gradients are added up here from the parts that the backward scan left.
 //
 // Bound by its reads: 4 bytes for each element of S and dS+ of every chunk.  One CTA per SM goes
-// through the chunks; a ring of slots, 100 KB in all, takes NV columns of d_v at a time.
+// through the chunks; a ring of slots, 100 KB in all, takes NV columns of d_v at a time.  4 x 1024 tokens, 8
+// heads of 256: 113 us, 398 MB read (3.5 TB/s); 4 x 2048: 194 us.
 template <int DK, int NV>
 struct GradGeom {
     static constexpr int kW = NV * 2;
@@ -1587,7 +1618,12 @@ cudaError_t forward_dk(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs
                                            : prep_go<DK, false>(q, k, a, a.ws + L.ws_op, st);
     if (e != cudaSuccess) return e;
     if (a.rec != nullptr) return seq_tc_cols(a.sh) == 32 ? fwd_go<DK, 32, 3>(q, k, a, st) : fwd_go<DK, 16, 3>(q, k, a, st);
-    return seq_tc_cols(a.sh) == 32 ? fwd_go<DK, 32, 2>(q, k, a, st) : fwd_go<DK, 16, 2>(q, k, a, st);
+    // without a record two CTAs of 16 columns fit an SM where d_k is no more than 128, and what one waits the other
+    // works: prep and scan of 16 x 1024, 8 heads of 128, 174 us against 187 with 32 columns
+    if constexpr (DK <= 128)
+        return fwd_go<DK, 16, 2>(q, k, a, st);
+    else
+        return seq_tc_cols(a.sh) == 32 ? fwd_go<DK, 32, 2>(q, k, a, st) : fwd_go<DK, 16, 2>(q, k, a, st);
 }
 
 template <int DK, int NV>
@@ -1622,6 +1658,10 @@ cudaError_t backward_dk(const CUtensorMap& q, const CUtensorMap& k, const SeqArg
 
 bool seq_tc_takes(int dtype) { return dtype == GDN_DTYPE_BF16; }
 
+// Value columns of a scan's CTA.  A chunk takes some 1.4 times as long with 32 as with 16, so 16 where they all
+// run at once, one CTA an SM, and 32 where 16 would take another turn.  Prep and scan of 8 heads of 256, with a record
+// and then backward: 1 x 8192 314 and 491 us with 16, 442 and 713 with 32; 4 x 2048 321 and 518 with 16, 259 and
+// 488 with 32.
 int seq_tc_cols(const SeqShape& s) {
     return s.dv % 32 == 0 && (size_t)s.nseq * s.H * (s.dv / 16) > kSMs ? 32 : 16;
 }

@@ -392,3 +392,19 @@ def test_what_lies_behind_a_sequence_stays_out():
     for m in OUT[:-1]:
         assert torch.equal(d[m][clean], d2[m][clean]), m
     assert torch.equal(d["S0"][[0, 2]], d2["S0"][[0, 2]])
+
+
+def test_order_of_sequences_changes_nothing():
+    """More CTAs than run at once: the longest sequences go first, and each comes out as it does alone."""
+    lengths = [3, 130, 0, 64, 200, 1, 130, 70, 5, 260, 31, 90]
+    x, off = make(lengths, 4, 2, 128, 128, "bf16", seed=23)
+    out, S_T, ws, rec = forward(x, off, record=True)
+    d = backward(x, off, torch.ones_like(out), torch.ones_like(S_T), ws, rec)
+    for s, n in enumerate(lengths):
+        a, b = int(off[s]), int(off[s + 1])
+        y = {m: (v[s:s + 1] if m == "S0" else v[a:b]).contiguous() for m, v in x.items()}
+        o1, S1, ws1, rec1 = forward(y, torch.tensor([0, n], dtype=torch.int32).cuda(), record=True)
+        assert torch.equal(out[a:b], o1) and torch.equal(S_T[s:s + 1], S1), s
+        if n:
+            d1 = backward(y, torch.tensor([0, n], dtype=torch.int32).cuda(), torch.ones_like(o1), torch.ones_like(S1), ws1, rec1)
+            assert torch.equal(d["v"][a:b], d1["v"]) and torch.equal(d["S0"][s:s + 1], d1["S0"]), s
