@@ -1195,23 +1195,28 @@ struct GradGeom {
     // blocks of a slot: dO, dV hi, zero, dV lo, -, or eps hi twice, zero, eps lo twice; then S or dS+, or eps hi, lo
     static constexpr uint32_t kImg = 5 * kBlk;
     static constexpr uint32_t kSlot = kImg + 2 * DK * kW;
-    static constexpr int kSlots = NV == 16 ? 4 : 2;
+    // two CTAs on an SM where d_k leaves room for their TMEM: one streams while the other scales and writes
+    static constexpr int kCtas = DK <= 128 ? 2 : 1;
+    static constexpr int kSlots = (NV == 16 ? 4 : 2) / (DK == 128 ? 2 : 1);
     static constexpr uint32_t kGates = kSlot0 + kSlots * kSlot;
     static constexpr uint32_t kMisc = kGates + kOpGates;          // four floats
     static constexpr uint32_t kBar = kMisc + 16;
     static constexpr uint32_t kUsed = kBar + 256 + 1024;
-    static constexpr uint32_t kSmem = kUsed > 116 * 1024 ? kUsed : 116 * 1024;      // one CTA per SM: it takes the whole TMEM
-    static constexpr int kDa = 0, kDw = DK, kE = 2 * DK <= 256 ? 256 : 0;
+    static constexpr uint32_t kSmem = kCtas == 2 || kUsed > 116 * 1024 ? kUsed : 116 * 1024;      // no more CTAs than TMEM
+    static constexpr int kDa = 0, kDw = DK, kE = 0;       // E and F are read before the others begin
+    static constexpr int kAlloc = 2 * DK <= 128 ? 128 : 2 * DK <= 256 ? 256 : 512;
+    static_assert(kSmem <= (kCtas == 2 ? 113 : 227) * 1024 && (kCtas == 1 || 3 * kSmem > 227 * 1024), "CTAs");
     static_assert(kSmem <= 227 * 1024 && kSlot % 1024 == 0, "slots");
 };
 
 template <int DK, int NV>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
     seq_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmO, SeqArgs a, const char* ops, const char* recS, const char* recE,
                     const char* wsS, const char* wsV, const float* part, const float* phi, float* dqf, float* dkf) {
     using G = GradGeom<DK, NV>;
     constexpr int W = G::kW, HC = DK / 2;                 // HC: columns of d_k of a thread
+    constexpr int CS = G::kCtas == 2 ? 16 : 32;           // columns at a time
     extern __shared__ unsigned char raw[];
     const uint32_t r0 = smem_u32(raw), base = (r0 + 1023u) & ~1023u;
     unsigned char* sm = raw + (base - r0);
@@ -1234,7 +1239,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (uint32_t o = tid * 16; o < G::kBlk; o += kFwdThreads * 16)
             st_shared16(base + G::kSlot0 + sl * G::kSlot + 2 * G::kBlk + o, 0, 0, 0, 0);
     fence_proxy_async_smem();
-    if (warp == 9) tmem_alloc(smem_u32(holder), 512);
+    if (warp == 9) tmem_alloc(smem_u32(holder), G::kAlloc);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1442,23 +1447,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 tc_fence_after();
                 const float eg = gates[kGEg + t], bt = gates[kGBt + t];
                 {
-                    uint32_t e0[32], e1[32];
-                    tmem_ld_n(tmem + G::kE + lanes + 32 * wg, e0);
-                    tmem_ld_n(tmem + G::kE + lanes + 64 + 32 * wg, e1);
-                    tmem_wait_ld();
+                    float m[32];
+#pragma unroll
+                    for (int g = 0; g < 32; g += CS) {
+                        uint32_t e0[CS], e1[CS];
+                        tmem_ld_n(tmem + G::kE + lanes + 32 * wg + g, e0);
+                        tmem_ld_n(tmem + G::kE + lanes + 64 + 32 * wg + g, e1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < CS; ++j) m[g + j] = __uint_as_float(e0[j]) + __uint_as_float(e1[j]);
+                    }
                     tc_fence_before();
                     __syncwarp();
                     asm volatile("bar.arrive 1, 288;\n" ::: "memory");
                     const float gh = gates[kGHi + t], gl = gates[kGLo + t];
-                    float m[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         const int c = 32 * wg + j;
-                        m[j] = 0.f;
-                        if (t < rows && (is_k ? c < t : c <= t)) {
-                            const float e = __uint_as_float(e0[j]) + __uint_as_float(e1[j]);
-                            m[j] = (is_k ? -e : e) * expf((gh - gates[kGHi + c]) + (gl - gates[kGLo + c])) * gates[kGBeta + c];
-                        }
+                        m[j] = t < rows && (is_k ? c < t : c <= t)
+                                   ? (is_k ? -m[j] : m[j]) * expf((gh - gates[kGHi + c]) + (gl - gates[kGLo + c])) * gates[kGBeta + c]
+                                   : 0.f;
                     }
                     put_terms<128, 2>(base + G::kM, 16384, L, 32 * wg, m);
                 }
@@ -1472,19 +1480,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 tc_fence_after();
                 const float fa = is_k ? -eg : eg;
 #pragma unroll 1
-                for (int g = 0; g < HC / 32; ++g) {
-                    const int c0 = HC * wg + 32 * g;
-                    uint32_t x[32], y[32];
+                for (int g = 0; g < HC / CS; ++g) {
+                    const int c0 = HC * wg + CS * g;
+                    uint32_t x[CS], y[CS];
                     tmem_ld_n(tmem + G::kDa + lanes + c0, x);
                     tmem_ld_n(tmem + G::kDw + lanes + c0, y);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
+                    for (int j = 0; j < CS; ++j) {
                         x[j] = __float_as_uint(fa * __uint_as_float(x[j]));
                         y[j] = __float_as_uint(bt * __uint_as_float(y[j]));
                     }
-                    tmem_st32(tmem + G::kDa + lanes + c0, x);
-                    tmem_st32(tmem + G::kDw + lanes + c0, y);
+                    tmem_st_n(tmem + G::kDa + lanes + c0, x);
+                    tmem_st_n(tmem + G::kDw + lanes + c0, y);
                 }
                 tmem_wait_st();
                 operand_ready(2, 288);
@@ -1495,14 +1503,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 __nv_bfloat16* out = static_cast<__nv_bfloat16*>(is_k ? a.dk : a.dq) + at;
                 float* acc = (is_k ? dkf : dqf) + at;
 #pragma unroll 1
-                for (int g = 0; g < HC / 32; ++g) {
-                    const int c0 = HC * wg + 32 * g;
-                    uint32_t x[32], y[32];
+                for (int g = 0; g < HC / CS; ++g) {
+                    const int c0 = HC * wg + CS * g;
+                    uint32_t x[CS], y[CS];
                     tmem_ld_n(tmem + G::kDa + lanes + c0, x);
                     if (is_k) tmem_ld_n(tmem + G::kDw + lanes + c0, y);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) {
+                    for (int p = 0; p < CS / 8; ++p) {
                         const int c = c0 + 8 * p;
                         float o[8];
 #pragma unroll
@@ -1538,7 +1546,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     __syncthreads();
     if (warp == 9) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, G::kAlloc);
     }
 }
 
@@ -1641,8 +1649,8 @@ cudaError_t bwd_go(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs& a,
                       bwd_smem<DK, NV>(), st, false, q, k, o, a, ops, (const char*)(a.rec + L.rec_S), (const char*)(a.rec + L.rec_eps),
                       (const float*)(a.rec + L.rec_o), a.ws + L.ws_dS, a.ws + L.ws_dV, part, phi);
     if (e != cudaSuccess) return e;
-    const long long items = (long long)seq_slots(sh.nseq, sh.total) * sh.Hk;
-    return launch_kernel(seq_grad_kernel<DK, NV>, dim3((unsigned)(items < kSMs ? items : kSMs)), dim3(kFwdThreads),
+    const long long items = (long long)seq_slots(sh.nseq, sh.total) * sh.Hk, ctas = GradGeom<DK, NV>::kCtas * kSMs;
+    return launch_kernel(seq_grad_kernel<DK, NV>, dim3((unsigned)(items < ctas ? items : ctas)), dim3(kFwdThreads),
                          GradGeom<DK, NV>::kSmem, st, true, q, k, o, a, ops, (const char*)(a.rec + L.rec_S),
                          (const char*)(a.rec + L.rec_eps), (const char*)(a.ws + L.ws_dS), (const char*)(a.ws + L.ws_dV),
                          (const float*)part, (const float*)phi, reinterpret_cast<float*>(a.ws + L.ws_dq),
