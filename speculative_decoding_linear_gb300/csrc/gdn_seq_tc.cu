@@ -1189,7 +1189,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // left them, E = dO eps^T, F = dV eps^T, MP = lower G E beta, ME = strictly lower G F beta:
 //   dq      = e^g dO S^T + MP K                     lanes 0..63 of one accumulator, rows dO and MP,
 //   k_read  = -e^g dV S^T - ME K                    lanes 64..127, rows dV and -ME
-//   k_write = bt eps dS+^T + MP^T Q - ME^T K        of another (in both halves)
+//   k_write = bt eps dS+^T + MP^T Q - ME^T K        lanes 64..127 of another, whose others nobody reads
 // and dk their sum.  The rows' factors e^g and bt are applied in place between the products over
 // d_v and those over the chunk's tokens: the operands stay what the scans stored, dO exact.
 // The gates' gradients are added up here from the parts that the backward scan left.
@@ -1204,7 +1204,8 @@ struct GradGeom {
     static constexpr uint32_t kBlk = 64 * kW;                     // 64 rows of an operand over d_v
     static constexpr uint32_t kM = (DK / 64) * kTile;             // [MP; -ME], two terms
     static constexpr uint32_t kSlot0 = kM + 2 * 16384;
-    // blocks of a slot: dO, dV hi, zero, dV lo, -, or eps hi twice, zero, eps lo twice; then S or dS+, or eps hi, lo
+    // blocks of a slot: dO, dV hi, zero, dV lo, -, or what was there, eps hi, zero, what was there, eps lo; then S or
+    // dS+, or eps hi, lo
     static constexpr uint32_t kImg = 5 * kBlk;
     static constexpr uint32_t kSlot = kImg + 2 * DK * kW;
     // two CTAs on an SM where d_k leaves room for their TMEM: one streams while the other scales and writes
@@ -1293,10 +1294,8 @@ __global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
                                 bulk_copy_g2s(sl + G::kImg, recS + (sh_at * tiles + v) * (3 * DK * W), 2 * DK * W, f);
                             }
                         } else {
-                            mbar_expect_tx(f, 4 * G::kBlk + 2 * DK * W);
-                            bulk_copy_g2s(sl, e, G::kBlk, f);
+                            mbar_expect_tx(f, 2 * G::kBlk + 2 * DK * W);
                             bulk_copy_g2s(sl + G::kBlk, e, G::kBlk, f);
-                            bulk_copy_g2s(sl + 3 * G::kBlk, e + G::kBlk, G::kBlk, f);
                             bulk_copy_g2s(sl + 4 * G::kBlk, e + G::kBlk, G::kBlk, f);
                             bulk_copy_g2s(sl + G::kImg, wsS + (sh_at * tiles + v) * (2 * DK * W), 2 * DK * W, f);
                         }
