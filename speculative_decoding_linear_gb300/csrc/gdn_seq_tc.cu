@@ -1234,7 +1234,7 @@ __global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
     const uint32_t r0 = smem_u32(raw), base = (r0 + 1023u) & ~1023u;
     unsigned char* sm = raw + (base - r0);
     const uint32_t kqf = base + G::kBar, kqe = kqf + 8, ef = kqf + 16, p2 = kqf + 24, fin = kqf + 32,
-                   drain = kqf + 40, full0 = kqf + 48, empty0 = full0 + 8 * G::kSlots;
+                   drain = kqf + 40, p3 = kqf + 48, full0 = kqf + 56, empty0 = full0 + 8 * G::kSlots;
     uint32_t* holder = reinterpret_cast<uint32_t*>(sm + G::kBar + 128);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const SeqShape& sh = a.sh;
@@ -1243,7 +1243,7 @@ __global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
     const int items = seq_slots(sh.nseq, sh.total) * sh.Hk;
 
     if (tid == 0) {
-        for (int i = 0; i < 6 + 2 * G::kSlots; ++i) mbar_init(kqf + 8 * i, 1);
+        for (int i = 0; i < 7 + 2 * G::kSlots; ++i) mbar_init(kqf + 8 * i, 1);
         mbar_init(kqe, 8);
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -1281,9 +1281,9 @@ __global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
                     for (int j = 0; j < 3 * tiles; ++j, ++it) {
                         const uint32_t sl = base + G::kSlot0 + (it % G::kSlots) * G::kSlot, f = full0 + 8 * (it % G::kSlots);
                         if (it >= G::kSlots && !(ok = wait_or_dead(empty0 + 8 * (it % G::kSlots), ((it / G::kSlots) & 1) ^ 1, a.err, dead))) break;
-                        const int v = (j < tiles ? j : (j - tiles) >> 1), v0 = v * NV;
+                        const int v = j % tiles, v0 = v * NV;
                         const char *e = recE + (sh_at * tiles + v) * (3 * G::kBlk), *w = wsV + (sh_at * tiles + v) * (2 * G::kBlk);
-                        if (j < tiles || ((j - tiles) & 1) == 0) {
+                        if (j < tiles || j >= 2 * tiles) {
                             mbar_expect_tx(f, 3 * G::kBlk + (j < tiles ? 2 * G::kBlk : 2 * DK * W));
                             tma_2d(sl, &tmO, h * sh.dv + v0, first, f);
                             bulk_copy_g2s(sl + G::kBlk, w, G::kBlk, f);
@@ -1337,38 +1337,49 @@ __global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
                 }
                 if (leader) mma_commit(ef);
                 __syncwarp();
-                named_sync(1, 288);                       // E and F are read
+                if constexpr (DK < 128) named_sync(1, 288);                       // E and F are read
                 tc_fence_after();
                 for (int j = 0; j < 2 * tiles; ++j, ++it) {
-                    const uint32_t sl = base + G::kSlot0 + (it % G::kSlots) * G::kSlot, d = tmem + (j & 1 ? G::kDw : G::kDa);
+                    const int second = j < tiles;         // k_write's product over d_v first: its rows are scaled meanwhile
+                    if (DK >= 128 && j == tiles) {
+                        named_sync(1, 288);
+                        tc_fence_after();
+                    }
+                    const uint32_t sl = base + G::kSlot0 + (it % G::kSlots) * G::kSlot, d = tmem + (second ? G::kDw : G::kDa);
                     wait_or_dead(full0 + 8 * (it % G::kSlots), (it / G::kSlots) & 1, a.err, dead);
                     __syncwarp();
                     if (leader) {
                         const uint64_t dA = k_desc<W>(sl), dB = k_desc<W>(sl + G::kImg),
-                                       dA2 = dA + ((j & 1 ? 3 : 2) * G::kBlk >> 4);
+                                       dA2 = dA + ((second ? 3 : 2) * G::kBlk >> 4);
 #pragma unroll
                         for (int k = 0; k < NV / 16; ++k) {
-                            mma_bf16(d, dA + 2 * k, dB + 2 * k, idesc_bf16(128, DK), (j >> 1) + k != 0);
+                            mma_bf16(d, dA + 2 * k, dB + 2 * k, idesc_bf16(128, DK), (second ? j : j - tiles) + k != 0);
                             mma_bf16(d, dA + 2 * k, dB + (DK * W >> 4) + 2 * k, idesc_bf16(128, DK), 1);
                             mma_bf16(d, dA2 + 2 * k, dB + 2 * k, idesc_bf16(128, DK), 1);
                         }
                         mma_commit(empty0 + 8 * (it % G::kSlots));
+                        if (j + 1 == tiles) mma_commit(p2);
                     }
                     __syncwarp();
                 }
-                if (leader) mma_commit(p2);
+                if (leader) mma_commit(p3);
                 __syncwarp();
-                named_sync(2, 288);                       // rows scaled, [MP; -ME] written
+                named_sync(2, 288);                       // k_write's rows scaled, [MP; -ME] written
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)          // [MP; -ME]^T [Q; K]
+                        mma_bf16(tmem + G::kDw, dMt + (k / 8) * 1024 + ((k % 8) * 2048 >> 4), dQKt + ((k % 8) * 2048 >> 4),
+                                 idesc_bf16(128, DK) | kAMn | kBMn, 1);
+                }
+                __syncwarp();
+                named_sync(5, 288);                       // the others' rows scaled
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)           // [MP; -ME] K
                         mma_bf16(tmem + G::kDa, dM + (k / 4) * 1024 + 2 * (k % 4), dQKt + (8192 + (k % 4) * 2048 >> 4),
                                  idesc_bf16(128, DK) | kBMn, 1);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)          // [MP; -ME]^T [Q; K]
-                        mma_bf16(tmem + G::kDw, dMt + (k / 8) * 1024 + ((k % 8) * 2048 >> 4), dQKt + ((k % 8) * 2048 >> 4),
-                                 idesc_bf16(128, DK) | kAMn | kBMn, 1);
                     mma_commit(fin);
                 }
                 __syncwarp();
@@ -1498,27 +1509,28 @@ __global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
                         const int p = j & 7, q = rows + (j >> 3) % (kChunk - rows), b = (j >> 3) / (kChunk - rows);
                         st_shared16(base + b * 8192 + q * 128 + p * 16, 0, 0, 0, 0);
                     }
+                auto scale = [&](uint32_t col, float f) {
+#pragma unroll 1
+                    for (int g = 0; g < HC / CS; ++g) {
+                        uint32_t x[CS];
+                        tmem_ld_n(tmem + col + lanes + HC * wg + CS * g, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < CS; ++j) x[j] = __float_as_uint(f * __uint_as_float(x[j]));
+                        tmem_st_n(tmem + col + lanes + HC * wg + CS * g, x);
+                    }
+                    tmem_wait_st();
+                };
                 wait_or_dead(p2, n & 1, a.err, dead);
                 __syncwarp();
                 tc_fence_after();
-                const float fa = is_k ? -eg : eg;
-#pragma unroll 1
-                for (int g = 0; g < HC / CS; ++g) {
-                    const int c0 = HC * wg + CS * g;
-                    uint32_t x[CS], y[CS];
-                    tmem_ld_n(tmem + G::kDa + lanes + c0, x);
-                    tmem_ld_n(tmem + G::kDw + lanes + c0, y);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < CS; ++j) {
-                        x[j] = __float_as_uint(fa * __uint_as_float(x[j]));
-                        y[j] = __float_as_uint(bt * __uint_as_float(y[j]));
-                    }
-                    tmem_st_n(tmem + G::kDa + lanes + c0, x);
-                    tmem_st_n(tmem + G::kDw + lanes + c0, y);
-                }
-                tmem_wait_st();
+                if (is_k) scale(G::kDw, bt);
                 operand_ready(2, 288);
+                wait_or_dead(p3, n & 1, a.err, dead);
+                __syncwarp();
+                tc_fence_after();
+                scale(G::kDa, is_k ? -eg : eg);
+                operand_ready(5, 288);
                 wait_or_dead(fin, n & 1, a.err, dead);
                 __syncwarp();
                 tc_fence_after();
