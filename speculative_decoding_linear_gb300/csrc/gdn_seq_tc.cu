@@ -1195,8 +1195,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // The gates' gradients are added up here from the parts that the backward scan left.
 //
 // Bound by its reads: 4 bytes for each element of S and dS+ of every chunk.  One CTA per SM goes
-// through the chunks; a ring of slots, 100 KB in all, takes NV columns of d_v at a time.  4 x 1024 tokens, 8
-// heads of 256: 113 us, 398 MB read (3.5 TB/s); 4 x 2048: 194 us.
+// (two for d_k up to 128) goes through the chunks; a ring of slots, 100 KB in all, takes NV columns of d_v at a time.
 template <int DK, int NV>
 struct GradGeom {
     static constexpr int kW = NV * 2;
@@ -1261,7 +1260,7 @@ __global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
 
     if (warp == 8) {
         if (elect_one()) {
-            int n = 0, it = 0;
+            int n = 0, it = 0, kq_issued = 0;
             bool ok = true;
             for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
                 int s, first, rows;
@@ -1270,15 +1269,20 @@ __global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
                 for (int r = 0; r < rep && ok; ++r, ++n) {
                     const int h = hk * rep + r;
                     const size_t sh_at = (size_t)(item / sh.Hk) * sh.H + h;
-                    if (n >= 1 && !(ok = wait_or_dead(kqe, (n - 1) & 1, a.err, dead))) break;
-                    mbar_expect_tx(kqf, 2 * DK * 128 + kOpGates);
-#pragma unroll
-                    for (int b = 0; b < DK / 64; ++b) {
-                        tma_3d(base + b * G::kTile, &tmQ, 64 * b, hk, first, kqf);
-                        tma_3d(base + b * G::kTile + 8192, &tmK, 64 * b, hk, first, kqf);
-                    }
-                    bulk_copy_g2s(base + G::kGates, ops + sh_at * kOpRecord, kOpGates, kqf);
+                    // Q, K and the gates behind the first slots: their place is free only when the item before has ended
+                    const int kq_at = min(G::kSlots, 3 * tiles - 1);
                     for (int j = 0; j < 3 * tiles; ++j, ++it) {
+                        if (j == kq_at) {
+                            if (n >= 1 && !(ok = wait_or_dead(kqe, (n - 1) & 1, a.err, dead))) break;
+                            mbar_expect_tx(kqf, 2 * DK * 128 + kOpGates);
+                            ++kq_issued;
+#pragma unroll
+                            for (int b = 0; b < DK / 64; ++b) {
+                                tma_3d(base + b * G::kTile, &tmQ, 64 * b, hk, first, kqf);
+                                tma_3d(base + b * G::kTile + 8192, &tmK, 64 * b, hk, first, kqf);
+                            }
+                            bulk_copy_g2s(base + G::kGates, ops + sh_at * kOpRecord, kOpGates, kqf);
+                        }
                         const uint32_t sl = base + G::kSlot0 + (it % G::kSlots) * G::kSlot, f = full0 + 8 * (it % G::kSlots);
                         if (it >= G::kSlots && !(ok = wait_or_dead(empty0 + 8 * (it % G::kSlots), ((it / G::kSlots) & 1) ^ 1, a.err, dead))) break;
                         const int v = j % tiles, v0 = v * NV;
@@ -1303,7 +1307,7 @@ __global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
                 }
             }
             if (*dead) {                                  // copies in flight land before the CTA ends
-                mbar_wait(kqf, n & 1, a.err);
+                if (kq_issued > 0) mbar_wait(kqf, (kq_issued - 1) & 1, a.err);
                 for (int j = it > G::kSlots ? it - G::kSlots : 0; j < it; ++j)
                     mbar_wait(full0 + 8 * (j % G::kSlots), (j / G::kSlots) & 1, a.err);
             }
@@ -1318,8 +1322,6 @@ __global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
             int s, first, rows;
             if (!slot_chunk(sh, item / sh.Hk, s, first, rows, a.err)) continue;
             for (int r = 0; r < rep; ++r, ++n) {
-                wait_or_dead(kqf, n & 1, a.err, dead);
-                __syncwarp();
                 for (int j = 0; j < tiles; ++j, ++it) {
                     const uint32_t sl = base + G::kSlot0 + (it % G::kSlots) * G::kSlot;
                     wait_or_dead(full0 + 8 * (it % G::kSlots), (it / G::kSlots) & 1, a.err, dead);
@@ -1363,6 +1365,8 @@ __global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
                     __syncwarp();
                 }
                 if (leader) mma_commit(p3);
+                __syncwarp();
+                wait_or_dead(kqf, n & 1, a.err, dead);
                 __syncwarp();
                 named_sync(2, 288);                       // k_write's rows scaled, [MP; -ME] written
                 tc_fence_after();
