@@ -653,7 +653,7 @@ SeqLayout seq_layout(const SeqShape& s, int dtype) {
     L.ws_op = 0;
     L.ws_part = align_up(L.ws_op + (tc ? slots * s.H * seqtc::kOpBytes : 0), kSectionAlign);
     L.ws_phi = align_up(L.ws_part + (tc ? tiles * 4 * kChunk * 4 : 0), kSectionAlign);
-    L.ws_dS = align_up(L.ws_phi + (tc ? tiles * seqtc::kPhi * 4 : 0), kSectionAlign);
+    L.ws_dS = align_up(L.ws_phi + (tc ? tiles * 8 * 4 : 0), kSectionAlign);
     L.ws_dV = align_up(L.ws_dS + state, kSectionAlign);
     L.ws_dq = align_up(L.ws_dV + rows, kSectionAlign);
     L.ws_dk = align_up(L.ws_dq + heads, kSectionAlign);

@@ -721,17 +721,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 // The gates' gradients are dots over d_v and come from here, where w and dS are fp32:
 //   dbeta_t = w_t.eps_t,   dlog_alpha_t = dlog_alpha_{t+1} + dO_t.o_t - dV_t.v_t,
 // the second since <S_t, dS_t> changes from token to token by just these; its value at a chunk's
-// first token is <S, dS>, S the chunk's start state.  Each CTA writes its columns' parts.  S has to be read for it,
-// and where a thread has 32 columns of S its chain waits for them: there every fourth chunk takes <S, dS> and the others
-// add the steps between (4 x 2048, 8 heads of 256: backward 440 us against 486; dlog_alpha 1.5e-6 of its size off
-// against 8e-7), elsewhere every chunk (1 x 8192 490 us against 496 by steps, 16 x 1024 with heads of 128 385
-// against 390).
+// first token is <S, dS>, S the chunk's start state.  Each CTA writes its columns' parts.
 //
 // Bound like the forward scan by a chunk's chain, 2.3 us with 16 columns and heads of 256: 1 x 8192, 8 heads of 256
 // 289 us, 4 x 2048 (32 columns) 283 us.
-template <int DK, int NV>
-constexpr int kAnchor = DK > 128 && NV == 32 ? 4 : 1;
-
 template <int DK, int NV>
 struct BwdGeom {
     static constexpr int kMH = DK > 128 ? 2 : 1;
@@ -862,7 +855,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             __syncwarp();
             // read: the next chunk's products may come
             if (i + 1 < chunks) asm volatile("bar.arrive 1, 352;\n" ::: "memory");
-            float dy = 0.f;                               // the chunk's sum of dlog_alpha's steps
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int vc = half * NH;
@@ -906,10 +898,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 float* q = part + (at * 2 + half) * (2 * kChunk) + tok;
                 q[0] = db;
                 q[kChunk] = dl;
-                dy += dl;
             }
-            if constexpr (kAnchor<DK, NV> > 1) dy = warp_sum(dy);
-            if (kAnchor<DK, NV> > 1 && lane == 0) phi[at * kPhi + 8 + (warp & 1)] = dy;
             __syncwarp();
             if (lane == 0) mbar_arrive(he0 + 8 * (i & 1));               // dO and the gates may be overwritten
             __syncwarp();
@@ -932,7 +921,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const size_t at = ((slot0 + c) * sh.H + h) * tiles + tile;     // what the compute warps will read themselves
                 bulk_prefetch_l2(recE + at * (3 * kChunk * W), 3 * kChunk * W);
                 bulk_prefetch_l2(recO + at * (kChunk * NV), kChunk * NV * 4);
-                if (c % kAnchor<DK, NV> == 0) bulk_prefetch_l2(recS + at * (3 * G::kSTerm), 3 * G::kSTerm);
+                bulk_prefetch_l2(recS + at * (3 * G::kSTerm), 3 * G::kSTerm);
                 issued = i + 1;
                 if (i >= 1 && !wait_or_dead(qe, (i - 1) & 1, a.err, dead)) break;
                 mbar_expect_tx(qf, DK * 128);
@@ -1072,7 +1061,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         };
         auto store_phi = [&](int c, float d) {
             d = warp_sum(d);
-            if (lane == 0) phi[(((slot0 + c) * sh.H + h) * tiles + tile) * kPhi + warp] = d;
+            if (lane == 0) phi[(((slot0 + c) * sh.H + h) * tiles + tile) * 8 + warp] = d;
         };
         auto state_dot = [&](int c) {
             float d = 0.f;
@@ -1121,8 +1110,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             // The warps that read K load the state that belongs to dS now and form its dot behind the third
             // product's start, the others at once.
             uint4 pre[SC / N][3][N / 8];
-            const bool anchor = i > 0 && (c + 1) % kAnchor<DK, NV> == 0;
-            if (anchor) {
+            if (i > 0) {
                 if (reads_k)
 #pragma unroll
                     for (int g = 0; g < SC / N; ++g) load_state(c + 1, g * N, pre[g]);
@@ -1146,7 +1134,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 for (int j = 0; j < NH; ++j) x[j] *= -eg * beta;
                 put_terms<W, 3>(base + G::kR, G::kRTerm, tok, vc, x);
                 operand_ready(3, 160);
-                if (anchor) {
+                if (i > 0) {
                     float d = 0.f;
 #pragma unroll
                     for (int g = 0; g < SC / N; ++g) d += dot_state(g * N, pre[g]);
@@ -1412,25 +1400,13 @@ __global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
                 const int h = hk * rep + r;
                 const size_t sh_at = (size_t)(item / sh.Hk) * sh.H + h;
                 if (warp == 7) {
-                    // <S, dS> at this chunk's first token and at the next one's, from the nearest chunk that has it
-                    const int c = item / sh.Hk - seq_slot0(sh, s), left = seq_end(sh, s) - first;
-                    const long long step = (long long)sh.H * tiles * kPhi;
-                    const float* p = phi + sh_at * tiles * kPhi;
+                    // <S, dS> at this chunk's first token and at the next one's
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        constexpr int A = kAnchor<DK, NV>;
-                        const int m = (c + i) % A;
-                        const bool later = 2 * m > A && left > kChunk * (i + A - m);
-                        const int from = later ? i + A - m : i - m;
+                        const float* p = phi + (sh_at + (size_t)i * sh.H) * tiles * 8;
                         float ph = 0.f, pl = 0.f;
-                        if (i == 0 || more) {
-                            for (int j = lane; j < 8 * tiles; j += 32) add2(ph, pl, p[from * step + j / 8 * kPhi + j % 8], 0.f);
-                            for (int k = later ? i : from; k < (later ? from : i); ++k)
-                                for (int j = lane; j < 2 * tiles; j += 32) {
-                                    const float y = p[k * step + j / 2 * kPhi + 8 + j % 2];
-                                    add2(ph, pl, later ? y : -y, 0.f);
-                                }
-                        }
+                        if (i == 0 || more)
+                            for (int j = lane; j < 8 * tiles; j += 32) add2(ph, pl, p[j], 0.f);
 #pragma unroll
                         for (int o = 16; o > 0; o >>= 1) {
                             const float qh = __shfl_xor_sync(0xffffffffu, ph, o), ql = __shfl_xor_sync(0xffffffffu, pl, o);

@@ -288,8 +288,6 @@ constexpr uint32_t kOpBytes = kOpGates + 2 * kOpTerm;       // without a record
 constexpr uint32_t kOpBack = kOpGates + 3 * kOpTerm;        // tpb's place in a record
 constexpr uint32_t kOpRecord = kOpBack + 3 * kOpTerm;
 constexpr int kGBt = 0, kGEg = 64, kGEnd = 128, kGTail = 132, kGBeta = 196, kGHi = 260, kGLo = 324;
-// a scan CTA's parts of <S, dS> (eight warps) and of the chunk's sum of dlog_alpha's steps (two warps)
-constexpr int kPhi = 10;
 constexpr uint32_t kGateFwd = 528;                          // bytes that the forward scan takes
 constexpr uint32_t kGateBwd = 784;                          // and the backward scan, from kGEg
 
