@@ -724,7 +724,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 // first token is <S, dS>, S the chunk's start state.  Each CTA writes its columns' parts.
 //
 // Bound like the forward scan by a chunk's chain, 2.3 us with 16 columns and heads of 256: 1 x 8192, 8 heads of 256
-// 289 us, 4 x 2048 (32 columns) 283 us.
+// 288 us, 4 x 2048 (32 columns) 283 us.  <S, dS> at every fourth chunk, with sums of the steps between, took 45 us less
+// of 4 x 2048 and left dlog_alpha 1.5e-6 of its size off instead of 8e-7.
 template <int DK, int NV>
 struct BwdGeom {
     static constexpr int kMH = DK > 128 ? 2 : 1;
@@ -1107,14 +1108,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 put_terms<W, 3>(base + G::kE, G::kRTerm, tok, vc, x);
             }
             operand_ready(1, 352);
-            // The warps that read K load the state that belongs to dS now and form its dot behind the third
+            // All load the state that belongs to dS now; the warps that read K form its dot behind the third
             // product's start, the others at once.
             uint4 pre[SC / N][3][N / 8];
-            if (i > 0) {
-                if (reads_k)
+            if (i > 0)
 #pragma unroll
-                    for (int g = 0; g < SC / N; ++g) load_state(c + 1, g * N, pre[g]);
-                else state_dot(c + 1);
+                for (int g = 0; g < SC / N; ++g) load_state(c + 1, g * N, pre[g]);
+            if (i > 0 && !reads_k) {
+                float d = 0.f;
+#pragma unroll
+                for (int g = 0; g < SC / N; ++g) d += dot_state(g * N, pre[g]);
+                store_phi(c + 1, d);
             }
             if (reads_k) {
                 wait_or_dead(b1, ph, a.err, dead);
@@ -1182,7 +1186,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // d_v and those over the chunk's tokens: the operands stay what the scans stored, dO exact.
 // The gates' gradients are added up here from the parts that the backward scan left.
 //
-// Bound by its reads: 4 bytes for each element of S and dS+ of every chunk.  One CTA per SM goes
+// Bound by its reads, 4 bytes for each element of S and dS+ of every chunk, and by what an item does after them.
+// 4 x 1024 tokens, 8 heads of 256: 106 us, 405 MB read (3.8 TB/s); 1 x 8192 174 us, 4 x 2048 182 us; 16 x 1024, heads
+// of 128: 161 us.  One CTA per SM (two for d_k up to 128) goes
 // (two for d_k up to 128) goes through the chunks; a ring of slots, 100 KB in all, takes NV columns of d_v at a time.
 template <int DK, int NV>
 struct GradGeom {
