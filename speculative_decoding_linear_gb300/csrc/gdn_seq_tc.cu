@@ -1689,8 +1689,8 @@ bool seq_tc_takes(int dtype) { return dtype == GDN_DTYPE_BF16; }
 
 // Value columns of a scan's CTA.  A chunk takes some 1.4 times as long with 32 as with 16, so 16 where they all
 // run at once, one CTA an SM, and 32 where 16 would take another turn.  Prep and scan of 8 heads of 256, with a record
-// and then backward: 1 x 8192 314 and 491 us with 16, 442 and 713 with 32; 4 x 2048 321 and 518 with 16, 259 and
-// 488 with 32.
+// and then backward: 1 x 8192 314 and 468 us with 16, 442 and 694 with 32; 4 x 2048 321 and 493 with 16, 259 and
+// 470 with 32.
 int seq_tc_cols(const SeqShape& s) {
     return s.dv % 32 == 0 && (size_t)s.nseq * s.H * (s.dv / 16) > kSMs ? 32 : 16;
 }
