@@ -463,7 +463,8 @@ int gdn_gla_commit(const float* S0, const void* factors, const int32_t* accepted
  *              outputs are not written
  *   out        dtype [total][H][d_v]
  *   S_T        fp32 [nseq][H][d_v][d_k], or null; may be S0 itself
- *   record     gdn_seq_record_bytes bytes for gdn_seq_backward, or null
+ *   record     gdn_seq_record_bytes bytes for gdn_seq_backward, or null; with bf16 inputs 32-byte
+ *              aligned
  *   workspace  gdn_seq_workspace_bytes bytes, scratch during the call
  * log_alpha, beta and offsets need 4-byte alignment only (here and in gdn_seq_step).
  * 0 <= total, d_k and d_v in {16, 32, ..., 256}; outputs do not overlap inputs or one another.

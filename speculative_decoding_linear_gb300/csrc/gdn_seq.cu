@@ -665,6 +665,8 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool given(const void* p) { return p != nullptr && aligned16(p); }
+// the tensor-core kernels write and read a record by 32 bytes
+bool record_ok(const void* p, bool tc) { return (reinterpret_cast<uintptr_t>(p) & (tc ? 31u : 15u)) == 0; }
 // gates and offsets are read one by one: any row of a larger tensor will do
 bool words(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool dim_ok(int d) { return d >= 16 && d <= kMaxDim && d % 16 == 0; }
@@ -737,7 +739,8 @@ int gdn_seq_forward(const void* q, int ldq, const void* k, int ldk, const void* 
     const SeqShape s = {nseq, total, H, Hk, dk, dv, offsets, ldq, ldk, ldv};
     if ((dtype != GDN_DTYPE_BF16 && dtype != GDN_DTYPE_F32) || !shape_ok(s) || !strides_ok(s, dtype)) return GDN_ERR_ARG;
     if (offsets == nullptr && total % nseq != 0) return GDN_ERR_ARG;
-    if (!aligned16(S0) || !aligned16(S_T) || !aligned16(record) || !words(offsets) || !given(workspace)) return GDN_ERR_ARG;
+    const bool tc = total > 0 && seq_tc_takes(dtype);
+    if (!aligned16(S0) || !aligned16(S_T) || !record_ok(record, tc) || !words(offsets) || !given(workspace)) return GDN_ERR_ARG;
     if (total > 0 && (!given(q) || !given(k) || !given(v) || log_alpha == nullptr || !words(log_alpha) || beta == nullptr || !words(beta) || !given(out)))
         return GDN_ERR_ARG;
     const SeqLayout L = seq_layout(s, dtype);
@@ -767,7 +770,6 @@ int gdn_seq_forward(const void* q, int ldq, const void* k, int ldk, const void* 
     a.S_T = S_T;
     a.rec = static_cast<char*>(record);
     a.ws = static_cast<char*>(workspace);
-    const bool tc = total > 0 && seq_tc_takes(dtype);
     const cudaError_t rc = tc ? launch_seq_forward_tc(a, stream) : launch_seq_forward_f32(a, dtype, stream);
     return rc == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -780,7 +782,9 @@ int gdn_seq_backward(const void* q, int ldq, const void* k, int ldk, const void*
     const SeqShape s = {nseq, total, H, Hk, dk, dv, offsets, ldq, ldk, ldv};
     if ((dtype != GDN_DTYPE_BF16 && dtype != GDN_DTYPE_F32) || !shape_ok(s) || !strides_ok(s, dtype)) return GDN_ERR_ARG;
     if (offsets == nullptr && total % nseq != 0) return GDN_ERR_ARG;
-    if (!aligned16(dS_T) || !aligned16(dS0) || !words(offsets) || !given(workspace) || !given(record)) return GDN_ERR_ARG;
+    const bool tc = total > 0 && seq_tc_takes(dtype);
+    if (!aligned16(dS_T) || !aligned16(dS0) || !words(offsets) || !given(workspace) || record == nullptr || !record_ok(record, tc))
+        return GDN_ERR_ARG;
     if (total > 0 && (!given(q) || !given(k) || !given(v) || log_alpha == nullptr || !words(log_alpha) || beta == nullptr || !words(beta) || !given(dout) ||
                       !given(dq) || !given(dk_out) || !given(dv_out) || !given(dlog_alpha) || !given(dbeta)))
         return GDN_ERR_ARG;
@@ -815,7 +819,6 @@ int gdn_seq_backward(const void* q, int ldq, const void* k, int ldk, const void*
     a.dbeta = dbeta;
     a.dS0 = dS0;
     a.ws = static_cast<char*>(workspace);
-    const bool tc = total > 0 && seq_tc_takes(dtype);
     const cudaError_t rc = tc ? launch_seq_backward_tc(a, stream) : launch_seq_backward_f32(a, dtype, stream);
     return rc == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

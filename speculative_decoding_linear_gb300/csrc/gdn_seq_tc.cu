@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         uint4 u[NH / 8];
 #pragma unroll
                         for (int i = 0; i < NH / 8; ++i) u[i] = make_uint4(p[4 * i][t], p[4 * i + 1][t], p[4 * i + 2][t], p[4 * i + 3][t]);
-                        stg_pieces(e + t * kChunk * W, u, swap);
+                        stg_pieces(e + t * kChunk * W, u, swap, true);
                     }
                 }
             } else {
@@ -667,17 +667,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 for (int i = 0; i < NH / 8; ++i)
                     u[i] = make_uint4(pack_bf16(y[8 * i], y[8 * i + 1]), pack_bf16(y[8 * i + 2], y[8 * i + 3]), pack_bf16(y[8 * i + 4], y[8 * i + 5]),
                                       pack_bf16(y[8 * i + 6], y[8 * i + 7]));
-                if (tok < rows) {
-                    if (whole) stg_pieces(o, u, false);
-                    else
-#pragma unroll
-                        for (int i = 0; i < NH / 8; ++i) reinterpret_cast<uint4*>(o)[i] = u[i];
-                }
+                if (tok < rows) stg_pieces(o, u, false, whole);
                 if constexpr (ST == 3) {                  // unrounded, for the gates' gradient
 #pragma unroll
                     for (int i = 0; i < NH / 4; ++i)
                         f[i] = make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]), __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3]));
-                    stg_pieces(e, f, false);
+                    stg_pieces(e, f, false, true);
                 }
             }
             __syncwarp();
@@ -823,6 +818,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int w4 = warp & 3, tok = 32 * (w4 & 1) + lane;
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
         const bool whole = (reinterpret_cast<uintptr_t>(a.dv) & 31u) == 0;      // 32-byte rows of columns
+        const bool ws_whole = (reinterpret_cast<uintptr_t>(wsV) & 31u) == 0;
         if (chunks > 0) asm volatile("bar.arrive 1, 352;\n" ::: "memory");
         for (int i = 0; i < chunks; ++i) {
             const int c = chunks - 1 - i;
@@ -888,14 +884,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 bool turn;
                 char* e = wsV + at * (size_t)(2 * kChunk * W) + pieces_at<W, NH>(tok, vc, turn);
                 __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.dv) + (((size_t)first + c * kChunk + tok) * sh.H + h) * sh.dv + v0 + vc;
-                stg_pieces(e, hi, turn);
-                stg_pieces(e + kChunk * W, lo, turn);
-                if (tok < rows) {
-                    if (whole) stg_pieces(o, hi, false);
-                    else
-#pragma unroll
-                        for (int p = 0; p < NH / 8; ++p) reinterpret_cast<uint4*>(o)[p] = hi[p];
-                }
+                stg_pieces(e, hi, turn, ws_whole);
+                stg_pieces(e + kChunk * W, lo, turn, ws_whole);
+                if (tok < rows) stg_pieces(o, hi, false, whole);
                 float* q = part + (at * 2 + half) * (2 * kChunk) + tok;
                 q[0] = db;
                 q[kChunk] = dl;

@@ -225,22 +225,28 @@ __device__ __forceinline__ void tmem_st_n(uint32_t t, const uint32_t (&r)[16]) {
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
 // N/8 pieces of 16 bytes that are neighbours in memory: whole sectors where there are two, with a
-// 32-byte access (a warp's rows lie apart, so that half sectors cost as much as whole ones).  `swap`:
-// the pieces of a pair change places.
+// 32-byte access (a warp's rows lie apart, so that half sectors cost as much as whole ones), unless the
+// place is not `wide`, aligned to 16 bytes only.  `swap`: the pieces of a pair change places.
 template <int P>
-__device__ __forceinline__ void stg_pieces(void* p, const uint4 (&x)[P], bool swap) {
+__device__ __forceinline__ void stg_pieces(void* p, const uint4 (&x)[P], bool swap, bool wide) {
     if constexpr (P == 1) {
         *reinterpret_cast<uint4*>(p) = x[0];
     } else {
 #pragma unroll
         for (int i = 0; i < P; i += 2) {
             const uint4 a = swap ? x[i + 1] : x[i], b = swap ? x[i] : x[i + 1];
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(static_cast<char*>(p) + 16 * i), "r"(a.x), "r"(a.y),
-                         "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-                         : "memory");
+            if (wide) {
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(static_cast<char*>(p) + 16 * i), "r"(a.x),
+                             "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                             : "memory");
+            } else {
+                static_cast<uint4*>(p)[i] = a;
+                static_cast<uint4*>(p)[i + 1] = b;
+            }
         }
     }
 }
+// at a 32-byte boundary
 template <int P>
 __device__ __forceinline__ void ldg_pieces(const void* p, uint4 (&x)[P]) {
     if constexpr (P == 1) {

@@ -1,0 +1,33 @@
+"""Argument checks of the sequence operators beyond shapes: alignment, sizes and products of sizes (CPU, no kernel runs)."""
+import pytest
+import torch
+
+from speculative_decoding_linear_gb300 import build as gbuild
+from speculative_decoding_linear_gb300 import gdnspec
+from test_seq_oracle import backward_args, far, forward_args
+
+NO_GPU = (gdnspec.ERR_CUDA, gdnspec.ERR_DEVICE)
+without_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="a valid call would launch on made-up addresses")
+
+
+@pytest.fixture(scope="module")
+def L():
+    gbuild.build()
+    return gdnspec.lib()
+
+
+@pytest.mark.parametrize("at", [4, 8, 16, 48])
+def test_record_of_bf16_calls_starts_on_32_bytes(L, at):
+    """The kernels take a record in 32-byte accesses."""
+    assert L.gdn_seq_forward(*forward_args(rec=far(9) + at)) == gdnspec.ERR_ARG
+    assert L.gdn_seq_backward(*backward_args(rec=far(8) + at)) == gdnspec.ERR_ARG
+
+
+@without_gpu
+def test_what_16_bytes_are_enough_for(L):
+    for dtype in (0, 1):
+        assert L.gdn_seq_forward(*forward_args(dtype=dtype, ws=far(10) + 16)) in NO_GPU
+        assert L.gdn_seq_backward(*backward_args(dtype=dtype, ws=far(15) + 16)) in NO_GPU
+    assert L.gdn_seq_forward(*forward_args(rec=far(9) + 32)) in NO_GPU
+    assert L.gdn_seq_forward(*forward_args(dtype=1, rec=far(9) + 16)) in NO_GPU
+    assert L.gdn_seq_backward(*backward_args(dtype=1, rec=far(8) + 16)) in NO_GPU
