@@ -441,10 +441,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const size_t slot0 = (size_t)(first / kChunk + s);
 
     if (tid == 0) {
-        for (int i = 0; i < 16; ++i) mbar_init(full0 + 8 * i, 1);
-        mbar_init(ve, 4);
-        mbar_init(ge0, 8);
-        mbar_init(ge0 + 8, 8);
+        init_barriers(full0, 16, [&](uint32_t bar) { return bar == ve ? 4 : bar >= ge0 ? 8 : 1; });
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -785,8 +782,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const size_t slot0 = (size_t)(first / kChunk + s);
 
     if (tid == 0) {
-        for (int i = 0; i < 14; ++i) mbar_init(full0 + 8 * i, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(he0 + 8 * i, 2);
+        init_barriers(full0, 14, [&](uint32_t bar) { return bar >= he0 ? 2 : 1; });
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -1227,8 +1223,7 @@ __global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
     const int items = seq_slots(sh.nseq, sh.total) * sh.Hk;
 
     if (tid == 0) {
-        for (int i = 0; i < 7 + 2 * G::kSlots; ++i) mbar_init(kqf + 8 * i, 1);
-        mbar_init(kqe, 8);
+        init_barriers(kqf, 7 + 2 * G::kSlots, [&](uint32_t bar) { return bar == kqe ? 8 : 1; });
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }

@@ -189,6 +189,14 @@ __device__ __forceinline__ bool elect_one() {
     return e != 0;
 }
 
+// n barriers behind one another, each initialised once (again, on a live one, is undefined): arrivals(its address).
+template <class Arrivals>
+__device__ __forceinline__ void init_barriers(uint32_t first, int n, Arrivals&& arrivals) {
+    for (int i = 0; i < n; ++i) {
+        const uint32_t bar = first + 8 * i;
+        mbar_init(bar, arrivals(bar));
+    }
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
