@@ -1,4 +1,13 @@
-"""Forms of the sequence operators that a call's sizes and addresses choose, on the GPU against the fp64 oracle."""
+"""Forms of the sequence operators that a call's sizes and addresses choose, on the GPU against the fp64 oracle.
+
+Results in fp32 are held to relative root mean squares, derived before any run (u = 2^-24).  Operands of three bf16
+terms leave u of themselves, and the fp32 sums of a product, of its terms and of a chunk's step a few u each, which
+decays with the state: 16 u for states and their gradients.  dbeta is a dot product of two such vectors: 32 u.
+dlog_alpha is a difference of sums that nearly cancel, kept as pairs of floats, of terms each a few u off: 3e-6, a third
+of what two terms leave of it.  Without a record S and [That; Phat] have two terms, 3e-6 of them in the mean square: 64 u
+for S_T.  A lost term would leave 2^-9, or 2^-17, of an operand.  The fp32 kernels take a token's roundings and those of
+64-token sums: 32 u, 64 u for dlog_alpha.
+"""
 import numpy as np
 import pytest
 import torch
@@ -28,3 +37,64 @@ def test_workspace_that_starts_on_16_bytes(dk, dv, n):
     d2 = backward(x, off, dout, None, moved, rec)
     for m in OUT:
         assert torch.equal(d[m], d2[m]), m
+
+
+U = 2.0 ** -24
+RECORD = dict(S_T=16 * U, S0=16 * U, beta=32 * U, log_alpha=3e-6)
+F32 = dict(out=32 * U, S_T=32 * U, q=32 * U, k=32 * U, v=32 * U, S0=32 * U, beta=32 * U, log_alpha=64 * U)
+
+
+def near(got, ref, bound, what):
+    e = np.sqrt(np.mean((got.double().cpu().numpy() - ref) ** 2)) / max(np.sqrt(np.mean(ref ** 2)), 1e-30)
+    assert e <= bound, "%s: %.3g of its size off, allowed %.3g" % (what, e, bound)
+
+
+def both_ways(lengths, H, Hk, dk, dv, dtype, bounds, seed, slow=False):
+    x, off = make(lengths, H, Hk, dk, dv, dtype, seed=seed, slow=slow)
+    out, S_T, ws, rec = forward(x, off, record=True)
+    y, n = wide64(x), dk + dv + 64
+    ref, refS = seq.seq_forward(**y, lengths=lengths)
+    rng = np.random.default_rng(seed + 1)
+    dout = torch.from_numpy(rng.standard_normal(out.shape)).to(out.dtype).cuda()
+    dS = torch.from_numpy(0.1 * rng.standard_normal(S_T.shape)).float().cuda()
+    d = backward(x, off, dout, dS, ws, rec)
+    want = seq.seq_backward(**y, lengths=lengths, dout=dout.double().cpu().numpy(), dS_T=dS.double().cpu().numpy())
+    check(out, ref, "out", n)
+    for m in OUT:
+        check(d[m], want[m], "d" + m, n * (H // Hk if m in ("q", "k") else 1))
+    for m, got, r in [("out", out, ref), ("S_T", S_T, refS)] + [(m, d[m], want[m]) for m in OUT]:
+        if m in bounds:
+            near(got, r, bounds[m], m)
+
+
+@pytest.mark.parametrize("dk,dv,H,Hk", [(64, 128, 8, 4), (128, 128, 8, 8), (192, 128, 8, 2), (256, 256, 8, 8), (48, 160, 8, 8), (80, 128, 8, 1)])
+def test_record_and_gradients_with_32_columns(dk, dv, H, Hk):
+    lengths = [130, 70, 0, 64]
+    assert len(lengths) * H * dv // 16 > 152
+    both_ways(lengths, H, Hk, dk, dv, "bf16", RECORD, seed=61)
+
+
+@pytest.mark.parametrize("slow", [False, True])
+@pytest.mark.parametrize("dk,dv", [(256, 256), (128, 64), (64, 48)])
+def test_record_and_gradients_with_16_columns(dk, dv, slow):
+    both_ways([330, 65], 2, 2, dk, dv, "bf16", RECORD, seed=63, slow=slow)
+
+
+@pytest.mark.parametrize("slow", [False, True])
+@pytest.mark.parametrize("lengths,H,Hk,dk,dv", [([130, 70, 0, 64], 8, 8, 256, 128), ([130, 70, 0, 64], 8, 4, 192, 128), ([300, 1], 2, 1, 192, 80),
+                                                ([130, 70, 0, 64], 8, 2, 128, 128), ([330], 2, 2, 128, 128), ([130, 70, 0, 64], 8, 8, 64, 128),
+                                                ([65, 190], 4, 1, 64, 64), ([200], 3, 3, 16, 48), ([400], 1, 1, 256, 256)])
+def test_prefill_without_a_record(lengths, H, Hk, dk, dv, slow):
+    x, off = make(lengths, H, Hk, dk, dv, "bf16", seed=67, slow=slow)
+    out, S_T, _, _ = forward(x, off)
+    ref, refS = seq.seq_forward(**wide64(x), lengths=lengths)
+    check(out, ref, "out", dk + dv + 64)
+    near(S_T, refS, 64 * U, "S_T")
+
+
+@pytest.mark.parametrize("n,Hk,dk,dv", [(8, 8, 64, 128), (8, 2, 16, 128), (5, 4, 128, 128), (8, 8, 96, 64), (3, 8, 256, 96)])
+def test_f32_with_two_rows_a_lane(n, Hk, dk, dv):
+    lanes = 8 if dk <= 64 else 16 if dk <= 128 else 32
+    lengths = [70, 3, 65, 0, 20, 1, 64, 9][:n]
+    assert dv % (256 // lanes) == 0 and n * 8 * dv * lanes // 32 > 12 * 152
+    both_ways(lengths, 8, Hk, dk, dv, "f32", F32, seed=71)
