@@ -459,6 +459,8 @@ int gdn_gla_commit(const float* S0, const void* factors, const int32_t* accepted
  *   S0         fp32 [nseq][H][d_v][d_k], or null for zero
  *   offsets    int32 [nseq + 1]: sequence s has the tokens offsets[s] .. offsets[s + 1] - 1 (none
  *              is allowed: its state passes through).  Null: total / nseq tokens each.
+ *              Tokens before offsets[0] and from offsets[nseq] on (padding) belong to none: their rows
+ *              of out, and of the gradients, are zero.
  *              Offsets that decrease or leave [0, total] -> GDN_ERR_INDEX; those sequences'
  *              outputs are not written
  *   out        dtype [total][H][d_v]

@@ -169,6 +169,8 @@ template <int LPR, int R>
 __global__ void __launch_bounds__(Scan<LPR, R>::kAll, 4) seq_scan_kernel(SeqArgs a, float* recS, float* eps) {
     using C = Scan<LPR, R>;
     const SeqShape& sh = a.sh;
+    int out_b, out_e;
+    if (seq_outside(sh, out_b, out_e)) zero_rows<float4>(a.out, (size_t)sh.H * sh.dv / 4, out_b, out_e, sh.total);
     Place<LPR, R> at;
     if (!at.find(a)) return;
     const int l = at.l;
@@ -353,7 +355,12 @@ __global__ void __launch_bounds__(kGradThreads)
     const SeqShape& sh = a.sh;
     const int h = blockIdx.x % sh.H, slot = blockIdx.x / sh.H, hk = h / (sh.H / sh.Hk);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ty = tid / 16 * 4, tx = tid % 16 * 4;
-    int s, first, rows;
+    int s, first, rows, out_b, out_e;
+    if (seq_outside(sh, out_b, out_e)) {
+        for (float* p : {dqo, dko}) zero_rows<float4>(p, (size_t)sh.H * sh.dk / 4, out_b, out_e, sh.total);
+        zero_rows<float4>(a.dv, (size_t)sh.H * sh.dv / 4, out_b, out_e, sh.total);
+        for (float* p : {a.dla, a.dbeta}) zero_rows<float>(p, sh.H, out_b, out_e, sh.total);
+    }
     if (!slot_chunk(sh, slot, s, first, rows, a.err)) return;
     const float* q = static_cast<const float*>(a.q) + (size_t)first * sh.ldq + (size_t)hk * sh.dk;
     const float* k = static_cast<const float*>(a.k) + (size_t)first * sh.ldk + (size_t)hk * sh.dk;

@@ -47,6 +47,23 @@ __device__ __forceinline__ int seq_end(const SeqShape& a, int s) {
     return a.offsets == nullptr ? (s + 1) * (a.total / a.nseq) : a.offsets[s + 1];
 }
 
+// Tokens of no sequence lie before `b`, the first offset, and from `e`, the last, on (a batch padded to a fixed
+// number of tokens).  False where there are none.
+__device__ __forceinline__ bool seq_outside(const SeqShape& a, int& b, int& e) {
+    if (a.offsets == nullptr) return false;
+    b = min(max(a.offsets[0], 0), a.total);
+    e = min(max(a.offsets[a.nseq], b), a.total);
+    return b > 0 || e < a.total;
+}
+
+// Those tokens' rows of `row` elements become zero, by all threads of the grid.
+template <typename T>
+static __device__ __noinline__ void zero_rows(void* p, size_t row, int b, int e, int total) {
+    const size_t i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x, n = (size_t)gridDim.x * blockDim.x;
+    for (size_t i = i0; i < b * row; i += n) static_cast<T*>(p)[i] = T{};
+    for (size_t i = e * row + i0; i < total * row; i += n) static_cast<T*>(p)[i] = T{};
+}
+
 // Sequence and chunk of a slot: false for an empty slot.  The search is for the last
 // sequence whose first slot is not behind `slot`; it ends for any content of the offsets,
 // and seq_range checks the one that it finds.

@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(kPrepThreads, REC ? 2 : 3)
     const SeqShape& sh = a.sh;
     const int h = blockIdx.x % sh.H, slot = blockIdx.x / sh.H, hk = h / (sh.H / sh.Hk);
     const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
-    int s, first, rows;
+    int s, first, rows, out_b, out_e;
+    if (seq_outside(sh, out_b, out_e)) zero_rows<uint4>(a.out, (size_t)sh.H * sh.dv / 8, out_b, out_e, sh.total);
     if (!slot_chunk(sh, slot, s, first, rows, a.err)) {
         griddep_launch();
         return;
@@ -769,6 +770,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint32_t* holder = reinterpret_cast<uint32_t*>(sm + G::kBar + 128);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     const SeqShape& sh = a.sh;
+    {
+        int b, e;
+        if (seq_outside(sh, b, e)) {
+            for (void* p : {a.dq, a.dk}) zero_rows<uint4>(p, (size_t)sh.Hk * sh.dk / 8, b, e, sh.total);
+            zero_rows<uint4>(a.dv, (size_t)sh.H * sh.dv / 8, b, e, sh.total);
+            for (float* p : {a.dla, a.dbeta}) zero_rows<float>(p, sh.H, b, e, sh.total);
+        }
+    }
     const int tiles = sh.dv / NV;
     const int tile = blockIdx.x % tiles, h = (blockIdx.x / tiles) % sh.H;
     const int s = seq_by_length(sh, blockIdx.x / (tiles * sh.H), reinterpret_cast<int*>(sm + G::kS));

@@ -98,3 +98,32 @@ def test_f32_with_two_rows_a_lane(n, Hk, dk, dv):
     lengths = [70, 3, 65, 0, 20, 1, 64, 9][:n]
     assert dv % (256 // lanes) == 0 and n * 8 * dv * lanes // 32 > 12 * 152
     both_ways(lengths, 8, Hk, dk, dv, "f32", F32, seed=71)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,Hk,dk,dv", [(4, 2, 128, 128), (2, 2, 64, 48), (8, 1, 256, 256)])
+@pytest.mark.parametrize("first,lengths,total", [(5, [70, 0, 31], 140), (0, [66], 100), (64, [64, 1], 129), (7, [0, 0], 20)])
+def test_tokens_of_no_sequence(first, lengths, total, H, Hk, dk, dv, dtype):
+    """Tokens before the first offset and behind the last: zeros in every output, whatever lies in the inputs there."""
+    x, _ = make([total], H, Hk, dk, dv, dtype, seed=73)
+    x["S0"] = 0.1 * torch.randn((len(lengths), H, dv, dk), device="cuda")
+    a, b = first, first + sum(lengths)
+    dout = torch.randn_like(x["v"])
+    for m in ("q", "k", "v", "log_alpha", "beta"):
+        x[m][:a], x[m][b:] = float("nan"), float("inf")
+    dout[:a], dout[b:] = float("inf"), float("nan")
+    off = torch.tensor(np.cumsum([first] + lengths), dtype=torch.int32).cuda()
+    inside = {m: (y if m == "S0" else y[a:b]).contiguous() for m, y in x.items()}
+    y = wide64(inside)
+    ref, refS = seq.seq_forward(**y, lengths=lengths)
+    want = seq.seq_backward(**y, lengths=lengths, dout=dout[a:b].double().cpu().numpy(), dS_T=np.zeros_like(y["S0"]))
+    out, S_T, ws, rec = forward(x, off, record=True)
+    plain, _, _, _ = forward(x, off)
+    ws.fill_(0xFF)
+    d = backward(x, off, dout, None, ws, rec)
+    n = dk + dv + 64
+    for got, r, what in [(out, ref, "out"), (plain, ref, "out without a record")] + [(d[m], want[m], "d" + m) for m in OUT[:-1]]:
+        check(got[a:b], r, what, n * (H // Hk))
+        assert (got[:a] == 0).all() and (got[b:] == 0).all(), what
+    check(S_T, refS, "S_T", n)
+    check(d["S0"], want["S0"], "dS0", n)
