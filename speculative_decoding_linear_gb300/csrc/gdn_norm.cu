@@ -78,12 +78,14 @@ __device__ __forceinline__ float lanes_sum(float x) {
     return x;
 }
 
-// bf16 results are rounded by 2^-8: the hardware's exponential and reciprocal (some 2^-21 here) do for
-// them, and the exact ones would take as long as the reads; fp32 results take the exact ones.
-template <typename T>
+// For results in types TO and T beside gates in T.  bf16 results are rounded by 2^-8: the hardware's exponential and
+// reciprocal do for them (2^-21, and 2^-23 |z| of the exponential), and the exact ones would take as long as the reads.
+// An fp32 gradient beside bf16 gates takes the exact exponential, and the reciprocal, 2^-22, from the hardware (8192 x 8
+// rows of 256 43 us; with both exact 54, registers spill); fp32 throughout both exact ones.  dweight, fp32 always, adds up what its rows were computed with.
+template <typename TO, typename T>
 __device__ __forceinline__ float sigmoid(float z) {
-    if constexpr (sizeof(T) == 2) return __fdividef(1.f, 1.f + __expf(-z));
-    return 1.f / (1.f + expf(-z));
+    const float e = sizeof(TO) == 2 && sizeof(T) == 2 ? __expf(-z) : expf(-z);
+    return sizeof(T) == 2 ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e);
 }
 
 // ---------------------------------------------------------------------------
@@ -114,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) gated_norm_kernel(GatedArgs a) {
     for (int i = 0; i < 8; ++i) s = fmaf(o[i], o[i], s);
     const float r = rsqrtf(lanes_sum<LANES>(s) / a.d + a.eps);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = o[i] * r * w[i] * (z[i] * sigmoid<T>(z[i]));
+    for (int i = 0; i < 8; ++i) o[i] = o[i] * r * w[i] * (z[i] * sigmoid<T, T>(z[i]));
     if (in) st8<T>(static_cast<T*>(a.y) + row * a.d + c, o);
 }
 
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 3) gated_norm_back_kernel(GatedArgs 
         float s = 0.f, t = 0.f, sg[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            sg[i] = sigmoid<T>(z[i]);
+            sg[i] = sigmoid<TO, T>(z[i]);
             s = fmaf(o[i], o[i], s);
             t = fmaf(o[i], y[i] * w[i] * (z[i] * sg[i]), t);
         }

@@ -44,3 +44,17 @@ def test_gated_norm_gradients_over_many_rows(rows, d, t):
     check(do, a, "do", 2 * d + 8)
     check(dz, b, "dz", d + 8)
     check(dw, c, "dw", d + 8 + int(np.sqrt(rows)) * 4)
+
+
+@pytest.mark.parametrize("gate", [-60.0, -20.0, -3.0, 2.0])
+def test_f32_gradient_beside_bf16_gates(gate):
+    """d_o is fp32 where o is: some 16 roundings of 2^-24 in the mean square of a row, whatever the gates' type."""
+    torch.manual_seed(5)
+    rows, d = 300, 128
+    o, w, dy = rand(rows, d), rand(d, t=torch.bfloat16), rand(rows, d, t=torch.bfloat16)
+    z = rand(rows, d, t=torch.bfloat16, mean=gate)
+    do, dz, dw = torch.empty_like(o), torch.empty_like(z), torch.empty(d, device="cuda")
+    gdnspec.gdn_gated_norm_backward(o, z, w, dy, do, dz, dw, gdnspec.empty_norm_workspace(rows, d), eps=EPS)
+    ref, _, _ = seq.gated_norm_backward(*w64(o, z, w, dy), EPS)
+    err = np.sqrt(((do.double().cpu().numpy() - ref) ** 2).sum(-1) / (ref ** 2).sum(-1))
+    assert err.max() <= 16 * 2.0 ** -24
