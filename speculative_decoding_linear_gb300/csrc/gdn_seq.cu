@@ -688,8 +688,8 @@ bool shape_ok(const SeqShape& s) {
 
 bool strides_ok(const SeqShape& s, int dtype) {
     const int unit = 16 / elem_bytes(dtype);
-    return s.ldq >= s.Hk * s.dk && s.ldk >= s.Hk * s.dk && s.ldv >= s.H * s.dv && s.ldq % unit == 0 &&
-           s.ldk % unit == 0 && s.ldv % unit == 0;
+    const long long qk = (long long)s.Hk * s.dk, v = (long long)s.H * s.dv;      // a row: what fits a stride fits an int
+    return s.ldq >= qk && s.ldk >= qk && s.ldv >= v && s.ldq % unit == 0 && s.ldk % unit == 0 && s.ldv % unit == 0;
 }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {

@@ -31,3 +31,11 @@ def test_what_16_bytes_are_enough_for(L):
     assert L.gdn_seq_forward(*forward_args(rec=far(9) + 32)) in NO_GPU
     assert L.gdn_seq_forward(*forward_args(dtype=1, rec=far(9) + 16)) in NO_GPU
     assert L.gdn_seq_backward(*backward_args(dtype=1, rec=far(8) + 16)) in NO_GPU
+
+
+@pytest.mark.parametrize("Hk,dk", [(1 << 23, 256), (1 << 24, 256), (1 << 24, 128)])
+def test_rows_wider_than_an_int_counts(L, Hk, dk):
+    """No stride is as long as such a row: Hk d_k does not wrap to something smaller."""
+    shape = dict(nseq=1, total=1, H=Hk, Hk=Hk, dk=dk, dv=16, ldq=8, ldk=8, ldv=16 * Hk, off=None)
+    assert L.gdn_seq_forward(*forward_args(**shape)) == gdnspec.ERR_ARG
+    assert L.gdn_seq_backward(*backward_args(**shape)) == gdnspec.ERR_ARG
