@@ -36,6 +36,6 @@ def test_what_16_bytes_are_enough_for(L):
 @pytest.mark.parametrize("Hk,dk", [(1 << 23, 256), (1 << 24, 256), (1 << 24, 128)])
 def test_rows_wider_than_an_int_counts(L, Hk, dk):
     """No stride is as long as such a row: Hk d_k does not wrap to something smaller."""
-    shape = dict(nseq=1, total=1, H=Hk, Hk=Hk, dk=dk, dv=16, ldq=8, ldk=8, ldv=16 * Hk, off=None)
+    shape = dict(nseq=1, total=1, H=Hk, Hk=Hk, dk=dk, dv=16, ldq=8, ldk=8, ldv=16 * Hk, off=None, dtype=1)
     assert L.gdn_seq_forward(*forward_args(**shape)) == gdnspec.ERR_ARG
     assert L.gdn_seq_backward(*backward_args(**shape)) == gdnspec.ERR_ARG
