@@ -321,6 +321,12 @@ __global__ void __launch_bounds__(kPrepThreads, REC ? 2 : 3)
     wait_or_dead(bar3, 0, a.err, dead);
     __syncwarp();
     tc_fence_after();
+    if (tid == 0 && *dead) {                              // copies and products in flight end before the CTA does
+        mbar_wait(bar, 0, a.err);
+        mbar_wait(bar2, 0, a.err);
+        mbar_wait(bar3, 0, a.err);
+    }
+    __syncwarp();
     if ((warp & 2) == 0) {
         const int t = 32 * (warp & 1) + lane, c0 = 32 * (warp >> 2);
         float y[32];
@@ -435,7 +441,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int hk = h / (sh.H / sh.Hk), v0 = tile * NV;
     const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
     int first, len;
-    if (!seq_range(sh, s, first, len, a.err)) return;     // the whole CTA
+    if (!seq_range(sh, s, first, len, a.err)) {           // the whole CTA
+        griddep_wait();                                   // the operands' kernel ends before this one
+        return;
+    }
     first = warp_uniform(first);
     len = warp_uniform(len);
     const int chunks = (len + kChunk - 1) / kChunk;
@@ -496,12 +505,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 bulk_copy_g2s(base + G::kTP, op + kOpGates, ST * kOpTerm, tpf);
                 ops_issued = c + 1;
             }
-            if (*dead) {                                  // copies in flight land before the CTA ends
-                for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) mbar_wait(full0 + 8 * (c & 1), (c >> 1) & 1, a.err);
-                if (q_issued > 0) mbar_wait(qf, (q_issued - 1) & 1, a.err);
-                if (v_issued > 0) mbar_wait(vf, (v_issued - 1) & 1, a.err);
-                if (ops_issued > 0) mbar_wait(tpf, (ops_issued - 1) & 1, a.err);
-            }
+            // copies in flight land before the CTA ends, though a warp that waits for them may give up
+            for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) mbar_wait(full0 + 8 * (c & 1), (c >> 1) & 1, a.err);
+            if (q_issued > 0) mbar_wait(qf, (q_issued - 1) & 1, a.err);
+            if (v_issued > 0) mbar_wait(vf, (v_issued - 1) & 1, a.err);
+            if (ops_issued > 0) mbar_wait(tpf, (ops_issued - 1) & 1, a.err);
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -560,10 +568,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         if (leader) {
             if (ST == 3) bulk_all_done();
-            if (*dead) {                                  // products in flight end before their TMEM is freed
-                mma_commit(drain);
-                mbar_wait(drain, 0, a.err);
-            }
+            mma_commit(drain);                            // products in flight end before their TMEM is freed, as above
+            mbar_wait(drain, 0, a.err);
         }
         __syncwarp();
     } else {
@@ -930,11 +936,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 bulk_copy_g2s(base + G::kTP, op + kOpBack, 3 * kOpTerm, tpf);
                 ops_issued = i + 1;
             }
-            if (*dead) {                                  // copies in flight land before the CTA ends
-                for (int i = issued > 2 ? issued - 2 : 0; i < issued; ++i) mbar_wait(full0 + 8 * (i & 1), (i >> 1) & 1, a.err);
-                if (q_issued > 0) mbar_wait(qf, (q_issued - 1) & 1, a.err);
-                if (ops_issued > 0) mbar_wait(tpf, (ops_issued - 1) & 1, a.err);
-            }
+            // copies in flight land before the CTA ends, though a warp that waits for them may give up
+            for (int i = issued > 2 ? issued - 2 : 0; i < issued; ++i) mbar_wait(full0 + 8 * (i & 1), (i >> 1) & 1, a.err);
+            if (q_issued > 0) mbar_wait(qf, (q_issued - 1) & 1, a.err);
+            if (ops_issued > 0) mbar_wait(tpf, (ops_issued - 1) & 1, a.err);
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -1005,10 +1010,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         if (leader) {
             bulk_all_done();
-            if (*dead) {                                  // products in flight end before their TMEM is freed
-                mma_commit(drain);
-                mbar_wait(drain, 0, a.err);
-            }
+            mma_commit(drain);                            // products in flight end before their TMEM is freed, as above
+            mbar_wait(drain, 0, a.err);
         }
         __syncwarp();
     } else {
@@ -1295,11 +1298,10 @@ __global__ void __launch_bounds__(kFwdThreads, GradGeom<DK, NV>::kCtas)
                     }
                 }
             }
-            if (*dead) {                                  // copies in flight land before the CTA ends
-                if (kq_issued > 0) mbar_wait(kqf, (kq_issued - 1) & 1, a.err);
-                for (int j = it > G::kSlots ? it - G::kSlots : 0; j < it; ++j)
-                    mbar_wait(full0 + 8 * (j % G::kSlots), (j / G::kSlots) & 1, a.err);
-            }
+            // copies in flight land before the CTA ends, though a warp that waits for them may give up
+            if (kq_issued > 0) mbar_wait(kqf, (kq_issued - 1) & 1, a.err);
+            for (int j = it > G::kSlots ? it - G::kSlots : 0; j < it; ++j)
+                mbar_wait(full0 + 8 * (j % G::kSlots), (j / G::kSlots) & 1, a.err);
         }
         __syncwarp();
     } else if (warp == 9) {

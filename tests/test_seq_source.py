@@ -24,3 +24,18 @@ def test_every_barrier_is_initialised_once(kernel):
     assert len(set(single)) == len(single)
     assert single or ranges
     assert ranges == 0 or (ranges == 1 and not [a for a in single if "*i" not in a])
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_copies_and_products_end_before_the_cta_does(kernel):
+    """After a wait that gave up the CTA waits once more, with a limit: nothing may write to its shared memory or TMEM later."""
+    text = body(kernel)
+    copies = {re.sub(r"\W.*", "", a.strip()) for a in re.findall(r"\b(?:tma_[23]d|bulk_copy_g2s)\([^;]*,\s*([^,;()]*(?:\([^()]*\))?)\);", text)}
+    copies = {"full0" if c == "f" else c for c in copies}
+    waited = {re.sub(r"\W.*", "", a.strip()) for a in re.findall(r"\bmbar_wait\(([^,;]*),", text)}
+    assert copies and copies <= waited
+    # every barrier that a commit arrives on is waited for by all, or the products are by the last commit of their thread
+    assert "drain" in waited or waited >= {"bar2", "bar3"}
+    # the scans' products may be in flight when their thread ends its loop, whoever gives up later
+    drained = re.search(r"(if \(leader && \*dead\)|if \(\*dead\))\s*\{[^{}]*mma_commit\(drain\)", text)
+    assert not (kernel in ("seq_fwd_kernel", "seq_bwd_kernel") and drained)
