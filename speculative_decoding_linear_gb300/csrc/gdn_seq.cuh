@@ -56,10 +56,11 @@ __device__ __forceinline__ bool seq_outside(const SeqShape& a, int& b, int& e) {
     return b > 0 || e < a.total;
 }
 
-// Those tokens' rows of `row` elements become zero, by all threads of the grid.
+// Those tokens' rows of `row` elements become zero, by all threads of the grid from `skip` of a CTA on.
 template <typename T>
-static __device__ __noinline__ void zero_rows(void* p, size_t row, int b, int e, int total) {
-    const size_t i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x, n = (size_t)gridDim.x * blockDim.x;
+static __device__ __noinline__ void zero_rows(void* p, size_t row, int b, int e, int total, int skip = 0) {
+    const int each = blockDim.x - skip;
+    const size_t i0 = (size_t)blockIdx.x * each + (threadIdx.x - skip), n = (size_t)gridDim.x * each;
     for (size_t i = i0; i < b * row; i += n) static_cast<T*>(p)[i] = T{};
     for (size_t i = e * row + i0; i < total * row; i += n) static_cast<T*>(p)[i] = T{};
 }

@@ -83,9 +83,14 @@ __global__ void __launch_bounds__(kPrepThreads, REC ? 2 : 3)
     const SeqShape& sh = a.sh;
     const int h = blockIdx.x % sh.H, slot = blockIdx.x / sh.H, hk = h / (sh.H / sh.Hk);
     const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
-    int s, first, rows, out_b, out_e;
-    if (seq_outside(sh, out_b, out_e)) zero_rows<uint4>(a.out, (size_t)sh.H * sh.dv / 8, out_b, out_e, sh.total);
+    int s, first, rows;
+    // by warps that have nothing to do before the product
+    const auto zero_outside = [&] {
+        int b, e;
+        if (tid >= 128 && seq_outside(sh, b, e)) zero_rows<uint4>(a.out, (size_t)sh.H * sh.dv / 8, b, e, sh.total, 128);
+    };
     if (!slot_chunk(sh, slot, s, first, rows, a.err)) {
+        zero_outside();
         griddep_launch();
         return;
     }
@@ -103,6 +108,7 @@ __global__ void __launch_bounds__(kPrepThreads, REC ? 2 : 3)
             tma_3d(base + b * G::kTile + 8192, &tmQ, 64 * b, hk, first, bar);
         }
     }
+    zero_outside();
     if (warp == 1) tmem_alloc(smem_u32(holder), 128);
     if (warp == 2) {
         // inclusive sum of the log gates as two floats, their difference exact to 2^-48 of the sum: the
