@@ -68,7 +68,7 @@ def forward(params, x, offsets, states=None, keep=False):
     layers, last = params
     n, total = offsets.numel() - 1, x.shape[0]
     dims = (n, total, H, HK, DK, DV, BF16)
-    ws = gdnspec.empty_seq_workspace(*dims)
+    ws = gdnspec.empty_seq_workspace(*dims, backward=keep)
     h, out_states, kept = norm_in(x, layers[0]["pre"]), [], []
     for i, p in enumerate(layers):
         q, k, v, z, la, b = split(h @ p["w_in"])

@@ -467,7 +467,8 @@ int gdn_gla_commit(const float* S0, const void* factors, const int32_t* accepted
  *   S_T        fp32 [nseq][H][d_v][d_k], or null; may be S0 itself
  *   record     gdn_seq_record_bytes bytes for gdn_seq_backward, or null; with bf16 inputs 32-byte
  *              aligned
- *   workspace  gdn_seq_workspace_bytes bytes, scratch during the call
+ *   workspace  scratch during the call: gdn_seq_forward_workspace_bytes bytes (none with fp32
+ *              inputs: may be null), backward gdn_seq_workspace_bytes, which serve both
  * log_alpha, beta and offsets need 4-byte alignment only (here and in gdn_seq_step).
  * 0 <= total, d_k and d_v in {16, 32, ..., 256}; outputs do not overlap inputs or one another.
  * States and sums are fp32.  With bf16 inputs the fp32 operands of the tensor core's products are
@@ -483,6 +484,7 @@ int gdn_gla_commit(const float* S0, const void* factors, const int32_t* accepted
  * Equal inputs give equal bits (no atomics).
  */
 int gdn_seq_workspace_bytes(int nseq, int total, int H, int Hk, int dk, int dv, int dtype, size_t* bytes);
+int gdn_seq_forward_workspace_bytes(int nseq, int total, int H, int Hk, int dk, int dv, int dtype, size_t* bytes);
 int gdn_seq_record_bytes(int nseq, int total, int H, int Hk, int dk, int dv, int dtype, size_t* bytes);
 int gdn_seq_forward(const void* q, int ldq, const void* k, int ldk, const void* v, int ldv, int dtype,
                     const float* log_alpha, const float* beta, const float* S0, const int32_t* offsets, void* out,

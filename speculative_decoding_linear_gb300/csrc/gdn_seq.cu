@@ -732,6 +732,13 @@ int gdn_seq_workspace_bytes(int nseq, int total, int H, int Hk, int dk, int dv, 
     return GDN_OK;
 }
 
+int gdn_seq_forward_workspace_bytes(int nseq, int total, int H, int Hk, int dk, int dv, int dtype, size_t* bytes) {
+    const SeqShape s = {nseq, total, H, Hk, dk, dv, nullptr, 0, 0, 0};
+    if (bytes == nullptr || !shape_ok(s) || (dtype != GDN_DTYPE_BF16 && dtype != GDN_DTYPE_F32)) return GDN_ERR_ARG;
+    *bytes = seq_layout(s, dtype).ws_forward();
+    return GDN_OK;
+}
+
 int gdn_seq_record_bytes(int nseq, int total, int H, int Hk, int dk, int dv, int dtype, size_t* bytes) {
     const SeqShape s = {nseq, total, H, Hk, dk, dv, nullptr, 0, 0, 0};
     if (bytes == nullptr || !shape_ok(s) || (dtype != GDN_DTYPE_BF16 && dtype != GDN_DTYPE_F32)) return GDN_ERR_ARG;
@@ -747,13 +754,15 @@ int gdn_seq_forward(const void* q, int ldq, const void* k, int ldk, const void* 
     if ((dtype != GDN_DTYPE_BF16 && dtype != GDN_DTYPE_F32) || !shape_ok(s) || !strides_ok(s, dtype)) return GDN_ERR_ARG;
     if (offsets == nullptr && total % nseq != 0) return GDN_ERR_ARG;
     const bool tc = total > 0 && seq_tc_takes(dtype);
-    if (!aligned16(S0) || !aligned16(S_T) || !record_ok(record, tc) || !words(offsets) || !given(workspace)) return GDN_ERR_ARG;
+    const SeqLayout L = seq_layout(s, dtype);
+    if (L.ws_forward() == 0) workspace = nullptr;          // not touched
+    if (!aligned16(S0) || !aligned16(S_T) || !record_ok(record, tc) || !words(offsets) || (L.ws_forward() > 0 && !given(workspace)))
+        return GDN_ERR_ARG;
     if (total > 0 && (!given(q) || !given(k) || !given(v) || log_alpha == nullptr || !words(log_alpha) || beta == nullptr || !words(beta) || !given(out)))
         return GDN_ERR_ARG;
-    const SeqLayout L = seq_layout(s, dtype);
     const size_t e = elem_bytes(dtype), vo = (size_t)total * H * dv * e, gb = (size_t)total * H * 4,
                  sb = (size_t)nseq * H * dv * dk * 4;
-    const Span w[] = {{out, vo}, {record, L.rec_total}, {workspace, L.ws_total}, {S_T, sb}};
+    const Span w[] = {{out, vo}, {record, L.rec_total}, {workspace, L.ws_forward()}, {S_T, sb}};
     const Span r[] = {{q, strided_bytes(total, ldq, Hk * dk, (int)e)}, {k, strided_bytes(total, ldk, Hk * dk, (int)e)},
                       {v, strided_bytes(total, ldv, H * dv, (int)e)}, {log_alpha, gb}, {beta, gb},
                       {offsets, ((size_t)nseq + 1) * 4}};

@@ -119,6 +119,7 @@ struct SeqArgs {
 struct SeqLayout {
     size_t rec_S, rec_eps, rec_o, rec_op, rec_total;     // record: chunk start states, errors, outputs, chunk operands
     size_t ws_dS, ws_dV, ws_dq, ws_dk, ws_op, ws_part, ws_phi, ws_total;   // workspace
+    size_t ws_forward() const { return ws_part; }        // what a forward pass takes of it: the chunk operands
 };
 
 SeqLayout seq_layout(const SeqShape& s, int dtype);

@@ -63,6 +63,7 @@ SIGNATURES = {
     "gdn_gla_tree_verify": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
     "gdn_gla_commit": (_I, [_P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P]),
     "gdn_seq_workspace_bytes": (_I, [_I] * 7 + [ctypes.POINTER(_S)]),
+    "gdn_seq_forward_workspace_bytes": (_I, [_I] * 7 + [ctypes.POINTER(_S)]),
     "gdn_seq_record_bytes": (_I, [_I] * 7 + [ctypes.POINTER(_S)]),
     "gdn_seq_forward": (_I, [_P, _I, _P, _I, _P, _I, _I] + [_P] * 8 + [_I] * 6 + [_P]),
     "gdn_seq_backward": (_I, [_P, _I, _P, _I, _P, _I, _I] + [_P] * 13 + [_I] * 6 + [_P]),
@@ -442,6 +443,13 @@ def gdn_seq_workspace_bytes(nseq, total, H, Hk, dk, dv, dtype) -> int:
     return out.value
 
 
+def gdn_seq_forward_workspace_bytes(nseq, total, H, Hk, dk, dv, dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().gdn_seq_forward_workspace_bytes(nseq, total, H, Hk, dk, dv, dtype_code(dtype), ctypes.byref(out)),
+           "gdn_seq_forward_workspace_bytes")
+    return out.value
+
+
 def gdn_seq_record_bytes(nseq, total, H, Hk, dk, dv, dtype) -> int:
     out = ctypes.c_size_t(0)
     _check(lib().gdn_seq_record_bytes(nseq, total, H, Hk, dk, dv, dtype_code(dtype), ctypes.byref(out)),
@@ -449,8 +457,10 @@ def gdn_seq_record_bytes(nseq, total, H, Hk, dk, dv, dtype) -> int:
     return out.value
 
 
-def empty_seq_workspace(nseq, total, H, Hk, dk, dv, dtype, device="cuda"):
-    return torch.empty(max(16, gdn_seq_workspace_bytes(nseq, total, H, Hk, dk, dv, dtype)), dtype=torch.uint8, device=device)
+def empty_seq_workspace(nseq, total, H, Hk, dk, dv, dtype, device="cuda", backward=True):
+    """Workspace of the sequence calls; with backward=False what gdn_seq_forward takes, a tenth of it."""
+    size = gdn_seq_workspace_bytes if backward else gdn_seq_forward_workspace_bytes
+    return torch.empty(max(16, size(nseq, total, H, Hk, dk, dv, dtype)), dtype=torch.uint8, device=device)
 
 
 def empty_seq_record(nseq, total, H, Hk, dk, dv, dtype, device="cuda"):
@@ -509,7 +519,7 @@ def gdn_seq_forward(q, k, v, log_alpha, beta, S0, out, S_T, workspace, offsets=N
     _same(out, v.shape, v.dtype, "out")
     _same(S0, (nseq, H, dv, dk), torch.float32, "S0")
     _same(S_T, (nseq, H, dv, dk), torch.float32, "S_T")
-    _sized(workspace, gdn_seq_workspace_bytes(*dims, q.dtype), "workspace")
+    _sized(workspace, gdn_seq_forward_workspace_bytes(*dims, q.dtype), "workspace")
     if record is not None:
         _sized(record, gdn_seq_record_bytes(*dims, q.dtype), "record")
     qp, ldq = _tokens(q, "q")

@@ -127,3 +127,24 @@ def test_tokens_of_no_sequence(first, lengths, total, H, Hk, dk, dv, dtype):
         assert (got[:a] == 0).all() and (got[b:] == 0).all(), what
     check(S_T, refS, "S_T", n)
     check(d["S0"], want["S0"], "dS0", n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths,H,Hk,dk,dv", [([130, 0, 65], 2, 1, 256, 256), ([70] * 4, 8, 8, 128, 128), ([5], 3, 3, 48, 16), ([0, 0], 2, 1, 64, 64)])
+def test_forward_stays_in_its_workspace(lengths, H, Hk, dk, dv, dtype):
+    x, off = make(lengths, H, Hk, dk, dv, dtype, seed=79)
+    out, S_T, _, _ = forward(x, off)
+    dims = (len(lengths), sum(lengths), H, Hk, dk, dv, dtype)
+    n = gdnspec.gdn_seq_forward_workspace_bytes(*dims)
+    room = torch.full((n + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    for record in (None, gdnspec.empty_seq_record(*dims)):
+        o2, S2 = torch.empty_like(out), torch.empty_like(S_T)
+        gdnspec.gdn_seq_forward(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], x["S0"], o2, S2, room[256:256 + n], offsets=off, record=record)
+        assert gdnspec.gdn_last_error() == 0
+        assert (room[:256] == 0x5A).all() and (room[256 + n:] == 0x5A).all()
+        if record is None:
+            assert torch.equal(out, o2) and torch.equal(S_T, S2)
+    if dtype == "f32":
+        o2, S2 = torch.empty_like(out), torch.empty_like(S_T)
+        gdnspec.gdn_seq_forward(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], x["S0"], o2, S2, None, offsets=off)
+        assert torch.equal(out, o2) and torch.equal(S_T, S2)
