@@ -472,8 +472,13 @@ int gdn_gla_commit(const float* S0, const void* factors, const int32_t* accepted
  * log_alpha, beta and offsets need 4-byte alignment only (here and in gdn_seq_step).
  * 0 <= total, d_k and d_v in {16, 32, ..., 256}; outputs do not overlap inputs or one another.
  * States and sums are fp32.  With bf16 inputs the fp32 operands of the tensor core's products are
- * carried as bf16 terms: the state that a chunk's products read as two (2^-16 of it), or three with
- * a record, everything else of the scans as three.  With fp32 inputs all is fp32.
+ * carried as bf16 terms, three of them (2^-24 of an operand are left) but for:
+ *   - without a record, two (2^-16) of the state that a chunk's products read and of the chunk's own
+ *     64 x 64 operands.  out is bf16 either way and as near; S_T, fp32, is 2e-7 of its size off with
+ *     ordinary decays and 8e-7 with slow ones (0.98 and more a token), with a record 2e-7 and 3e-7,
+ *     and its last bits differ between the two
+ *   - two of the operands of dq and dk, which are bf16 themselves
+ * With fp32 inputs all is fp32.
  *
  * gdn_seq_backward: gradients for dout (dtype [total][H][d_v]) and dS_T (null: zero).  The first
  * arguments and the record are those of the forward call, unchanged.
@@ -514,8 +519,8 @@ int gdn_seq_step(const void* q, const void* k, const void* v, int dtype, const f
  * r = (mean o^2 + eps)^{-1/2}; rows = tokens x heads of d values (d in {16, 32, ..., 256}).
  *   o o_dtype [rows][d];  gate, out dtype [rows][d];  weight dtype [d];  rows >= 1, eps > 0
  * out may be o or gate itself where the types agree.
- * Backward: dout_y dtype; d_o o_dtype, dgate dtype, dweight fp32 [d], apart from the inputs and
- * one another.  workspace: gdn_norm_workspace_bytes(rows, d) bytes.
+ * Backward: dout_y dtype; d_o o_dtype, dgate dtype, dweight fp32 [d] (an fp32 sum over the rows, of
+ * terms 2^-21 off where o and gate are bf16), apart from the inputs and one another.  workspace: gdn_norm_workspace_bytes(rows, d) bytes.
  */
 int gdn_norm_workspace_bytes(long long rows, int width, size_t* bytes);
 int gdn_gated_norm(const void* o, int o_dtype, const void* gate, const void* weight, void* out, int dtype,
@@ -548,7 +553,10 @@ int gdn_block_norm_backward(const void* x_out, const void* z, const void* post_w
 
 /*
  * Launch overlap between consecutive calls (process-wide switch, default off;
- * returns the previous setting).  When on, the first kernel of every call is
+ * returns the previous setting).  The calls of the sequence operators and of
+ * the norms (gdn_seq_*, gdn_gated_norm*, gdn_block_norm*) do not take part:
+ * with the switch on or off they begin when what is before them on the stream
+ * has ended.  When on, the first kernel of every other call is
  * launched as a programmatic dependent of the kernel before it on the stream:
  * it starts streaming its state tiles and pending-commit factors (and may
  * write the committed state back) while that kernel finishes, and waits for it

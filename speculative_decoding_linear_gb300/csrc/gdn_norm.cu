@@ -22,9 +22,11 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-// CTAs of a gradient kernel at most, each a row of partial sums (the block norm: two): as many as are
-// resident together, so that none begins when others have ended.  The block norm's kernel holds two rows
-// in some 128 registers a thread: 512 threads an SM.
+// CTAs of a gradient kernel at most, each a row of partial sums (the block norm: two): in bf16 as many as are
+// resident together, so that none begins when others have ended.  The block norm's kernel holds two rows in up
+// to 128 registers a thread, 512 threads an SM.  Its fp32 forms take 132 to 151 up to 2048 values: one CTA fewer
+// is resident, and the last ones begin when others have ended (8192 x 2048 136 us, 3.0 TB/s).  The gated norm's
+// gradients beside fp32 gates spill some 100 bytes at their 80 registers (8192 x 8 rows of 256 in fp32 73 us, 4.6 TB/s).
 constexpr int kSMs = 152, kGatedCtas = 3 * kSMs;
 constexpr int block_ctas(int threads) { return kSMs * (512 / threads); }
 
@@ -81,7 +83,8 @@ __device__ __forceinline__ float lanes_sum(float x) {
 // For results in types TO and T beside gates in T.  bf16 results are rounded by 2^-8: the hardware's exponential and
 // reciprocal do for them (2^-21, and 2^-23 |z| of the exponential), and the exact ones would take as long as the reads.
 // An fp32 gradient beside bf16 gates takes the exact exponential, and the reciprocal, 2^-22, from the hardware (8192 x 8
-// rows of 256 43 us; with both exact 54, registers spill); fp32 throughout both exact ones.  dweight, fp32 always, adds up what its rows were computed with.
+// rows of 256 43 us; with both exact 54, registers spill); fp32 throughout both exact ones.  dweight, fp32 always,
+// adds up what its rows were computed with.
 template <typename TO, typename T>
 __device__ __forceinline__ float sigmoid(float z) {
     const float e = sizeof(TO) == 2 && sizeof(T) == 2 ? __expf(-z) : expf(-z);
@@ -488,7 +491,10 @@ cudaError_t block_go(const BlockArgs& a, float* dw, float* dwp, float* dgate, bo
                          a.D, dw, static_cast<const T*>(a.gate), dwp, static_cast<const T*>(a.wp), dgate);
 }
 
-// The fewest threads that hold a row in one vector of eight values each, from 4096 values on in two
+// The fewest threads that hold a row in one vector of eight values each, past 4096 values in two.  The gradients
+// of two spill (with the post-norm bf16 304 bytes of stores a thread, fp32 440) and read no row ahead: 2048 x 8192 97 us (2.1 TB/s)
+// in bf16 and 132 (3.1) in fp32, 3200 x 5120, where a quarter of the vectors is past the row's end, 122 and 151;
+// 4096 x 4096 in one vector 53 and 110.
 template <typename T, bool POST>
 cudaError_t block_v(const BlockArgs& a, float* dw, float* dwp, float* dgate, bool back, cudaStream_t st) {
     if (a.D <= 256) return block_go<T, 32, 1, POST>(a, dw, dwp, dgate, back, st);

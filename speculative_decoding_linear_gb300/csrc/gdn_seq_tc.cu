@@ -12,8 +12,8 @@
 //   [K; Q] S  ->  [That; Phat] r  ->  K^T (bt eps),
 // and what bounds a long sequence is their latency: a chain of T / 64 chunks.  S stays in
 // registers in fp32 (a row of d_k for each thread, NV columns of it) and goes to shared memory as
-// two bf16 terms for the first product; r and bt eps as three.  A pass that keeps a record takes three
-// of S as well: the gates' gradients are differences of dots with o and eps.
+// two bf16 terms for the first product; That and Phat have two as well, r and bt eps three.  A pass that
+// keeps a record takes three of all: the gates' gradients are differences of dots with o and eps.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -1193,8 +1193,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 //
 // Bound by its reads, 4 bytes for each element of S and dS+ of every chunk, and by what an item does after them.
 // 4 x 1024 tokens, 8 heads of 256: 106 us, 405 MB read (3.8 TB/s); 1 x 8192 174 us, 4 x 2048 182 us; 16 x 1024, heads
-// of 128: 161 us.  One CTA per SM (two for d_k up to 128) goes
-// (two for d_k up to 128) goes through the chunks; a ring of slots, 100 KB in all, takes NV columns of d_v at a time.
+// of 128: 161 us.  One CTA per SM (two for d_k up to 128) goes through the chunks.  Slots of shared memory take NV
+// columns of d_v at a time: with 32 columns two of 28 KB (d_k 64), one of 36 (128), two of 44 or 52 (192, 256), with 16
+// four of 14, two of 18, four of 22 or 26.  The single slot is no ring: there a copy waits for the products before it,
+// and the SM's other CTA works meanwhile.
 template <int DK, int NV>
 struct GradGeom {
     static constexpr int kW = NV * 2;
@@ -1651,7 +1653,9 @@ cudaError_t forward_dk(const CUtensorMap& q, const CUtensorMap& k, const SeqArgs
     if (e != cudaSuccess) return e;
     if (a.rec != nullptr) return seq_tc_cols(a.sh) == 32 ? fwd_go<DK, 32, 3>(q, k, a, st) : fwd_go<DK, 16, 3>(q, k, a, st);
     // without a record two CTAs of 16 columns fit an SM where d_k is no more than 128, and what one waits the other
-    // works: prep and scan of 16 x 1024, 8 heads of 128, 174 us against 187 with 32 columns
+    // works.  Prep and scan with 16 and with 32 columns, us: 8 heads of 128, 16 x 1024 175 and 188, 64 x 256 192 and
+    // 204; 16 heads of 128, 32 x 1024 594 and 642; 8 heads of 64, 16 x 1024 115 and 121, 64 x 1024 397 and 414; d_k 64 and
+    // d_v 128, 16 x 1024 162 and 176; d_k 128 and d_v 256, 8 x 2048 268 and 297
     if constexpr (DK <= 128)
         return fwd_go<DK, 16, 2>(q, k, a, st);
     else
