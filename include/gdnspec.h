@@ -478,7 +478,8 @@ int gdn_gla_commit(const float* S0, const void* factors, const int32_t* accepted
  *     ordinary decays and 8e-7 with slow ones (0.98 and more a token), with a record 2e-7 and 3e-7,
  *     and its last bits differ between the two
  *   - two of the operands of dq and dk, which are bf16 themselves
- * With fp32 inputs all is fp32.
+ * With fp32 inputs all is fp32.  A NaN or an infinity stays in its sequence; with bf16 inputs it
+ * reaches the whole chunk of 64 tokens that it lies in, the tokens before it too.
  *
  * gdn_seq_backward: gradients for dout (dtype [total][H][d_v]) and dS_T (null: zero).  The first
  * arguments and the record are those of the forward call, unchanged.
