@@ -516,6 +516,64 @@ int gdn_seq_step(const void* q, const void* k, const void* v, int dtype, const f
                  cudaStream_t stream);
 
 /*
+ * Decay-gated linear attention over packed sequences: prefill and training of the family that
+ * gdn_linear_tree_verify verifies drafts of.
+ *   S_t = e^{log_alpha_t} S_{t-1} + beta_t v_t k_t^T,  o_t = S_t q_t
+ * for each (sequence, head), from S0 to the state after the last token (the S0 of a draft's
+ * verification).  Arguments, layouts, strides, offsets, padding and errors are those of
+ * gdn_seq_forward and gdn_seq_backward, but for
+ *   record     gdn_linear_seq_record_bytes bytes for gdn_linear_seq_backward, or null
+ *   workspace  scratch during the call, gdn_linear_seq_forward_workspace_bytes bytes, backward
+ *              gdn_linear_seq_workspace_bytes, which serve both
+ * and record and workspace are 16-byte aligned.  A decay that is the same for all tokens (a constant
+ * of each head) is given for each token too, and its gradient is the sum over the tokens; for a write
+ * strength of one, beta holds ones.
+ * Equal inputs give equal bits (no atomics).
+ */
+int gdn_linear_seq_workspace_bytes(int nseq, int total, int H, int Hk, int dk, int dv, int dtype, size_t* bytes);
+int gdn_linear_seq_forward_workspace_bytes(int nseq, int total, int H, int Hk, int dk, int dv, int dtype, size_t* bytes);
+int gdn_linear_seq_record_bytes(int nseq, int total, int H, int Hk, int dk, int dv, int dtype, size_t* bytes);
+int gdn_linear_seq_forward(const void* q, int ldq, const void* k, int ldk, const void* v, int ldv, int dtype,
+                           const float* log_alpha, const float* beta, const float* S0, const int32_t* offsets, void* out,
+                           float* S_T, void* record, void* workspace, int nseq, int total, int H, int Hk, int dk, int dv,
+                           cudaStream_t stream);
+int gdn_linear_seq_backward(const void* q, int ldq, const void* k, int ldk, const void* v, int ldv, int dtype,
+                            const float* log_alpha, const float* beta, const int32_t* offsets, const void* dout,
+                            const float* dS_T, const void* record, void* dq, void* dk_out, void* dv_out, float* dlog_alpha,
+                            float* dbeta, float* dS0, void* workspace, int nseq, int total, int H, int Hk, int dk, int dv,
+                            cudaStream_t stream);
+
+/* One token of it for each of B sequences, states updated in place (decode): arguments as gdn_seq_step. */
+int gdn_linear_seq_step(const void* q, const void* k, const void* v, int dtype, const float* log_alpha, const float* beta,
+                        float* S, const int32_t* state_index, void* out, int B, int slots, int H, int Hk, int dk, int dv,
+                        cudaStream_t stream);
+
+/*
+ * Rotary positions of q and k (before the recurrence, or of a draft's nodes at the position of the
+ * state plus their depth).  Pair i of a head's first `rot` elements, (x, y), becomes at position p
+ *   scale (x cos a - y sin a, x sin a + y cos a),   a = p inv_freq[i];
+ * the pairs are elements i and i + rot / 2, or (interleaved = 1) 2 i and 2 i + 1.  The other d - rot
+ * elements are copied.  inverse = 1 turns by -a: the gradient of the input from that of the output.
+ *   q          dtype, token t's row at q + t ldq: [H][d];  k likewise [Hk][d], or null with Hk = 0
+ *   q_out, k_out  with strides of their own; may be q and k themselves (same stride), and all may be
+ *              columns of one wider tensor that do not meet.  Strides: at least a row, a multiple of
+ *              16 bytes
+ *   positions  int32 [total], any values;  inv_freq fp32 [rot / 2], each below 2^26 in size (a NaN, an
+ *              infinity or more gives NaN).  Both need 4-byte alignment only
+ *   d in {16, 32, ..., 256}, rot even, 2 <= rot <= d; 0 <= total; H + Hk <= 65535
+ * The angle is exact to 1e-9 turns at any position; sines, products and sums are fp32.
+ *
+ * gdn_rotary_frequencies writes the rot / 2 frequencies base^{-2 i / rot}, scaled for contexts
+ * `factor` times as long as the `original` one (in tokens), into HOST memory: a frequency that turns
+ * `high` times and more in the original context stays, one that turns `low` times and less is divided
+ * by factor, between them in proportion.  original = 0: all are divided (factor 1: none are).
+ */
+int gdn_rotary_frequencies(int rot, double base, double factor, double original, double low, double high, float* inv_freq);
+int gdn_rotary(const void* q, int ldq, const void* k, int ldk, int dtype, const int32_t* positions, const float* inv_freq,
+               float scale, void* q_out, int ldq_out, void* k_out, int ldk_out, int total, int H, int Hk, int d, int rot,
+               int interleaved, int inverse, cudaStream_t stream);
+
+/*
  * Norm of each head's output, with its weight and its gate: y = weight (o r) silu(gate),
  * r = (mean o^2 + eps)^{-1/2}; rows = tokens x heads of d values (d in {16, 32, ..., 256}).
  *   o o_dtype [rows][d];  gate, out dtype [rows][d];  weight dtype [d];  rows >= 1, eps > 0
@@ -555,7 +613,7 @@ int gdn_block_norm_backward(const void* x_out, const void* z, const void* post_w
 /*
  * Launch overlap between consecutive calls (process-wide switch, default off;
  * returns the previous setting).  The calls of the sequence operators and of
- * the norms (gdn_seq_*, gdn_gated_norm*, gdn_block_norm*) do not take part:
+ * the norms (gdn_seq_*, gdn_linear_seq_*, gdn_rotary, gdn_gated_norm*, gdn_block_norm*) do not take part:
  * with the switch on or off they begin when what is before them on the stream
  * has ended.  When on, the first kernel of every other call is
  * launched as a programmatic dependent of the kernel before it on the stream:

@@ -68,6 +68,14 @@ SIGNATURES = {
     "gdn_seq_forward": (_I, [_P, _I, _P, _I, _P, _I, _I] + [_P] * 8 + [_I] * 6 + [_P]),
     "gdn_seq_backward": (_I, [_P, _I, _P, _I, _P, _I, _I] + [_P] * 13 + [_I] * 6 + [_P]),
     "gdn_seq_step": (_I, [_P, _P, _P, _I] + [_P] * 5 + [_I] * 6 + [_P]),
+    "gdn_linear_seq_workspace_bytes": (_I, [_I] * 7 + [ctypes.POINTER(_S)]),
+    "gdn_linear_seq_forward_workspace_bytes": (_I, [_I] * 7 + [ctypes.POINTER(_S)]),
+    "gdn_linear_seq_record_bytes": (_I, [_I] * 7 + [ctypes.POINTER(_S)]),
+    "gdn_linear_seq_forward": (_I, [_P, _I, _P, _I, _P, _I, _I] + [_P] * 8 + [_I] * 6 + [_P]),
+    "gdn_linear_seq_backward": (_I, [_P, _I, _P, _I, _P, _I, _I] + [_P] * 13 + [_I] * 6 + [_P]),
+    "gdn_linear_seq_step": (_I, [_P, _P, _P, _I] + [_P] * 5 + [_I] * 6 + [_P]),
+    "gdn_rotary_frequencies": (_I, [_I] + [ctypes.c_double] * 5 + [_P]),
+    "gdn_rotary": (_I, [_P, _I, _P, _I, _I, _P, _P, ctypes.c_float, _P, _I, _P, _I] + [_I] * 7 + [_P]),
     "gdn_norm_workspace_bytes": (_I, [ctypes.c_longlong, _I, ctypes.POINTER(_S)]),
     "gdn_gated_norm": (_I, [_P, _I, _P, _P, _P, _I, ctypes.c_longlong, _I, ctypes.c_float, _P]),
     "gdn_gated_norm_backward": (_I, [_P, _I] + [_P] * 7 + [_I, ctypes.c_longlong, _I, ctypes.c_float, _P]),
@@ -550,9 +558,8 @@ def gdn_seq_backward(q, k, v, log_alpha, beta, dout, dS_T, record, dq, dk, dv, d
            "gdn_seq_backward")
 
 
-def gdn_seq_step(q, k, v, log_alpha, beta, S, out, state_index=None, stream=None):
-    """One token for each of B sequences, the states S [slots, H, dv, dk] fp32 updated in place (see
-    include/gdnspec.h); state_index int32 [B], -1 for an empty row."""
+def _step_dims(q, k, v, log_alpha, beta, S, out, state_index):
+    """(B, slots, H, Hk, dk, dv) of a single-token call, its shapes checked against one another."""
     qs, vs, ss, t, f32 = q.shape, v.shape, S.shape, q.dtype, torch.float32
     B, Hk, dk = qs
     _, H, dv = vs
@@ -567,10 +574,137 @@ def gdn_seq_step(q, k, v, log_alpha, beta, S, out, state_index=None, stream=None
         raise ValueError("out must be %s %s" % (t, tuple(vs)))
     if state_index is not None and (state_index.shape != (B,) or state_index.dtype is not torch.int32):
         raise ValueError("state_index must be int32 [%d]" % B)
+    return B, ss[0], H, Hk, dk, dv
+
+
+def gdn_seq_step(q, k, v, log_alpha, beta, S, out, state_index=None, stream=None):
+    """One token for each of B sequences, the states S [slots, H, dv, dk] fp32 updated in place (see
+    include/gdnspec.h); state_index int32 [B], -1 for an empty row."""
+    B, slots, H, Hk, dk, dv = _step_dims(q, k, v, log_alpha, beta, S, out, state_index)
     rc = lib().gdn_seq_step(_ptr(q), _ptr(k), _ptr(v), dtype_code(q.dtype), _ptr(log_alpha), _ptr(beta), _ptr(S),
-                            _ptr(state_index), _ptr(out), B, ss[0], H, Hk, dk, dv, _stream(stream))
+                            _ptr(state_index), _ptr(out), B, slots, H, Hk, dk, dv, _stream(stream))
     if rc != OK:
         raise GdnError(rc, "gdn_seq_step")
+
+
+def _here(*tensors):
+    """Every tensor on the current device, whose stream the call goes to: a kernel cannot read another's memory."""
+    on = {x.get_device() for x in tensors if x is not None}
+    if -1 in on or on != {_current_device()}:
+        raise ValueError("expected CUDA tensors on the current device")
+
+
+def _linear_seq_bytes(name, *dims_dtype):
+    out = ctypes.c_size_t(0)
+    *dims, dtype = dims_dtype
+    _check(getattr(lib(), name)(*dims, dtype_code(dtype), ctypes.byref(out)), name)
+    return out.value
+
+
+def gdn_linear_seq_workspace_bytes(nseq, total, H, Hk, dk, dv, dtype) -> int:
+    return _linear_seq_bytes("gdn_linear_seq_workspace_bytes", nseq, total, H, Hk, dk, dv, dtype)
+
+
+def gdn_linear_seq_forward_workspace_bytes(nseq, total, H, Hk, dk, dv, dtype) -> int:
+    return _linear_seq_bytes("gdn_linear_seq_forward_workspace_bytes", nseq, total, H, Hk, dk, dv, dtype)
+
+
+def gdn_linear_seq_record_bytes(nseq, total, H, Hk, dk, dv, dtype) -> int:
+    return _linear_seq_bytes("gdn_linear_seq_record_bytes", nseq, total, H, Hk, dk, dv, dtype)
+
+
+def empty_linear_seq_workspace(nseq, total, H, Hk, dk, dv, dtype, device="cuda", backward=True):
+    """Workspace of the linear-attention sequence calls; with backward=False what gdn_linear_seq_forward takes."""
+    size = gdn_linear_seq_workspace_bytes if backward else gdn_linear_seq_forward_workspace_bytes
+    return torch.empty(size(nseq, total, H, Hk, dk, dv, dtype), dtype=torch.uint8, device=device)
+
+
+def empty_linear_seq_record(nseq, total, H, Hk, dk, dv, dtype, device="cuda"):
+    """Caller-owned record that gdn_linear_seq_forward writes for gdn_linear_seq_backward."""
+    return torch.empty(gdn_linear_seq_record_bytes(nseq, total, H, Hk, dk, dv, dtype), dtype=torch.uint8, device=device)
+
+
+def gdn_linear_seq_forward(q, k, v, log_alpha, beta, S0, out, S_T, workspace, offsets=None, record=None, stream=None):
+    """Decay-gated linear attention over packed sequences (see include/gdnspec.h): arguments as gdn_seq_forward."""
+    nseq, total, H, Hk, dk, dv = dims = _seq_dims(q, k, v, log_alpha, beta, offsets)
+    _same(out, v.shape, v.dtype, "out")
+    _same(S0, (nseq, H, dv, dk), torch.float32, "S0")
+    _same(S_T, (nseq, H, dv, dk), torch.float32, "S_T")
+    _sized(workspace, gdn_linear_seq_forward_workspace_bytes(*dims, q.dtype), "workspace")
+    if record is not None:
+        _sized(record, gdn_linear_seq_record_bytes(*dims, q.dtype), "record")
+    qp, ldq = _tokens(q, "q")
+    kp, ldk = _tokens(k, "k")
+    vp, ldv = _tokens(v, "v")
+    _here(q, k, v, log_alpha, beta, S0, out, S_T, workspace, offsets, record)
+    _check(lib().gdn_linear_seq_forward(qp, ldq, kp, ldk, vp, ldv, dtype_code(q.dtype), _ptr(log_alpha), _ptr(beta), _ptr(S0),
+                                        _ptr(offsets), _ptr(out), _ptr(S_T), _ptr(record), _ptr(workspace), *dims,
+                                        _stream(stream)), "gdn_linear_seq_forward")
+
+
+def gdn_linear_seq_backward(q, k, v, log_alpha, beta, dout, dS_T, record, dq, dk, dv, dlog_alpha, dbeta, dS0, workspace,
+                            offsets=None, stream=None):
+    """Gradients of gdn_linear_seq_forward at the record that it wrote (see include/gdnspec.h); dS_T and dS0 may be None."""
+    dims = nseq, total, H, Hk, d_k, d_v = _seq_dims(q, k, v, log_alpha, beta, offsets)
+    for x, like, what in ((dout, v, "dout"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv"), (dlog_alpha, log_alpha, "dlog_alpha"),
+                          (dbeta, beta, "dbeta")):
+        _same(x, like.shape, like.dtype, what)
+    _same(dS_T, (nseq, H, d_v, d_k), torch.float32, "dS_T")
+    _same(dS0, (nseq, H, d_v, d_k), torch.float32, "dS0")
+    _sized(workspace, gdn_linear_seq_workspace_bytes(*dims, q.dtype), "workspace")
+    _sized(record, gdn_linear_seq_record_bytes(*dims, q.dtype), "record")
+    qp, ldq = _tokens(q, "q")
+    kp, ldk = _tokens(k, "k")
+    vp, ldv = _tokens(v, "v")
+    _here(q, k, v, log_alpha, beta, dout, dS_T, record, dq, dk, dv, dlog_alpha, dbeta, dS0, workspace, offsets)
+    _check(lib().gdn_linear_seq_backward(qp, ldq, kp, ldk, vp, ldv, dtype_code(q.dtype), _ptr(log_alpha), _ptr(beta),
+                                         _ptr(offsets), _ptr(dout), _ptr(dS_T), _ptr(record), _ptr(dq), _ptr(dk), _ptr(dv),
+                                         _ptr(dlog_alpha), _ptr(dbeta), _ptr(dS0), _ptr(workspace), *dims, _stream(stream)),
+           "gdn_linear_seq_backward")
+
+
+def gdn_linear_seq_step(q, k, v, log_alpha, beta, S, out, state_index=None, stream=None):
+    """One token of decay-gated linear attention for each of B sequences: arguments as gdn_seq_step."""
+    B, slots, H, Hk, dk, dv = _step_dims(q, k, v, log_alpha, beta, S, out, state_index)
+    _here(q, k, v, log_alpha, beta, S, out, state_index)
+    rc = lib().gdn_linear_seq_step(_ptr(q), _ptr(k), _ptr(v), dtype_code(q.dtype), _ptr(log_alpha), _ptr(beta), _ptr(S),
+                                   _ptr(state_index), _ptr(out), B, slots, H, Hk, dk, dv, _stream(stream))
+    if rc != OK:
+        raise GdnError(rc, "gdn_linear_seq_step")
+
+
+def gdn_rotary_frequencies(rot, base=10000.0, factor=1.0, original=0.0, low=1.0, high=32.0, device="cuda"):
+    """fp32 [rot / 2] frequencies of gdn_rotary, scaled for contexts `factor` times as long (see include/gdnspec.h)."""
+    f = torch.empty(max(0, rot // 2), dtype=torch.float32)
+    _check(lib().gdn_rotary_frequencies(rot, base, factor, original, low, high, f.data_ptr() or None), "gdn_rotary_frequencies")
+    return f.to(device)
+
+
+def gdn_rotary(q, k, positions, inv_freq, q_out, k_out, scale=1.0, interleaved=False, inverse=False, stream=None):
+    """Rotary positions of q [.., H, d] and k [.., Hk, d] (k and k_out may be None), with positions int32 [..] and
+    inv_freq fp32 [rot / 2] (see include/gdnspec.h); q_out and k_out may be q and k."""
+    if q.dim() not in (3, 4) or positions.shape != q.shape[:-2] or positions.dtype is not torch.int32:
+        raise ValueError("q must be [.., H, d] and positions int32 of its leading dimensions")
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    if k is not None and (k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1] or k.dtype is not q.dtype):
+        raise ValueError("k must be as q but for its heads")
+    if inv_freq.dim() != 1 or inv_freq.dtype is not torch.float32:
+        raise ValueError("inv_freq must be fp32 [rot / 2]")
+    _same(q_out, q.shape, q.dtype, "q_out")
+    qp, ldq = _tokens(q, "q")
+    qo, ldqo = _tokens(q_out, "q_out")
+    kp = ko = None
+    ldk = ldko = Hk = 0
+    if k is not None:
+        _same(k_out, k.shape, k.dtype, "k_out")
+        kp, ldk = _tokens(k, "k")
+        ko, ldko = _tokens(k_out, "k_out")
+        Hk = k.shape[-2]
+    _here(q, k, positions, inv_freq, q_out, k_out)
+    _check(lib().gdn_rotary(qp, ldq, kp, ldk, dtype_code(q.dtype), _ptr(positions), _ptr(inv_freq), scale, qo, ldqo, ko, ldko,
+                            positions.numel(), q.shape[-2], Hk, q.shape[-1], 2 * inv_freq.numel(), int(interleaved), int(inverse),
+                            _stream(stream)), "gdn_rotary")
 
 
 def empty_norm_workspace(rows, width, device="cuda"):
