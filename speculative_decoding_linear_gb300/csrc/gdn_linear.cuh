@@ -51,6 +51,8 @@ struct LinLayout {
     size_t ws_local, ws_gend, ws_start, ws_forward, ws_end, ws_phi, ws_part, ws_heads, ws_total;
 };
 LinLayout lin_layout(const SeqShape& s, int dtype);
+LinLayout lin_layout_tc(const SeqShape& s);
+constexpr int kLinSegment = 512;                     // tokens of a segment with bf16 inputs
 
 constexpr int kScanThreads = 256;
 constexpr int kScanTile = kScanThreads * 4;          // elements of a state that one CTA of the scan takes
@@ -77,6 +79,8 @@ __device__ __forceinline__ double warp_scan(double x) {
     return x;
 }
 
+cudaError_t launch_linear_forward_tc(const SeqArgs& a, cudaStream_t st);
+cudaError_t launch_linear_backward_tc(const SeqArgs& a, cudaStream_t st);
 cudaError_t launch_linear_scan(const SeqShape& sh, int L, int terms, bool back, const float* local, const float* gend, const float* S0, void* out,
                                size_t apart, const void* start, float* phi, float* last, int* err, cudaStream_t st);
 

@@ -454,38 +454,36 @@ cudaError_t launch_linear_scan(const SeqShape& sh, int L, int terms, bool back, 
 
 namespace {
 
-template <typename T>
-cudaError_t forward_simt(const SeqArgs& a, int dtype, cudaStream_t st) {
+cudaError_t forward_f32(const SeqArgs& a, cudaStream_t st) {
     const SeqShape& sh = a.sh;
-    const LinLayout L = lin_layout(sh, dtype);
+    const LinLayout L = lin_layout(sh, GDN_DTYPE_F32);
     float* states = reinterpret_cast<float*>(a.rec != nullptr ? a.rec : a.ws + L.ws_local);
     float* gend = reinterpret_cast<float*>(a.ws + L.ws_gend);
     const unsigned sth = (unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSegF) * sh.H), tk = (sh.dk + 63) / 64, tv = (sh.dv + 63) / 64;
-    cudaError_t e = launch_kernel(lin_local_kernel<T, false>, dim3(sth, tk * tv), dim3(kT), 0, st, false, a, states, gend);
+    cudaError_t e = launch_kernel(lin_local_kernel<float, false>, dim3(sth, tk * tv), dim3(kT), 0, st, false, a, states, gend);
     if (e == cudaSuccess) e = launch_linear_scan(sh, kSegF, 0, false, states, gend, a.S0, states, 0, nullptr, nullptr, a.S_T, a.err, st);
     if (e == cudaSuccess && sh.total > 0)
-        e = launch_kernel(lin_rows_kernel<T, kOut>, dim3(sth, tv), dim3(kT), 0, st, false, a, (const float*)states, (float*)nullptr);
+        e = launch_kernel(lin_rows_kernel<float, kOut>, dim3(sth, tv), dim3(kT), 0, st, false, a, (const float*)states, (float*)nullptr);
     return e;
 }
 
-template <typename T>
-cudaError_t backward_simt(const SeqArgs& a, int dtype, cudaStream_t st) {
+cudaError_t backward_f32(const SeqArgs& a, cudaStream_t st) {
     const SeqShape& sh = a.sh;
-    const LinLayout L = lin_layout(sh, dtype);
+    const LinLayout L = lin_layout(sh, GDN_DTYPE_F32);
     const float* starts = reinterpret_cast<const float*>(a.rec);
     float *ends = reinterpret_cast<float*>(a.ws + L.ws_local), *gend = reinterpret_cast<float*>(a.ws + L.ws_gend),
           *phi = reinterpret_cast<float*>(a.ws + L.ws_phi);
     const size_t slots = seg_slots(sh.nseq, sh.total, kSegF);
     const unsigned sth = (unsigned)(slots * sh.H), stk = (unsigned)(slots * sh.Hk), tk = (sh.dk + 63) / 64, tv = (sh.dv + 63) / 64;
     float *part_q = reinterpret_cast<float*>(a.ws + L.ws_part), *part_k = part_q + slots * sh.H * tk * kSegF;
-    cudaError_t e = launch_kernel(lin_local_kernel<T, true>, dim3(sth, tk * tv), dim3(kT), 0, st, false, a, ends, gend);
+    cudaError_t e = launch_kernel(lin_local_kernel<float, true>, dim3(sth, tk * tv), dim3(kT), 0, st, false, a, ends, gend);
     if (e == cudaSuccess) e = launch_linear_scan(sh, kSegF, 0, true, ends, gend, a.dS_T, ends, 0, starts, phi, a.dS0, a.err, st);
     if (e != cudaSuccess || sh.total == 0) return e;
-    e = launch_kernel(lin_rows_kernel<T, kDq>, dim3(stk, tk), dim3(kT), 0, st, false, a, starts, part_q);
-    if (e == cudaSuccess) e = launch_kernel(lin_rows_kernel<T, kDk>, dim3(stk, tk), dim3(kT), 0, st, false, a, (const float*)ends, (float*)nullptr);
-    if (e == cudaSuccess) e = launch_kernel(lin_rows_kernel<T, kDv>, dim3(sth, tv), dim3(kT), 0, st, false, a, (const float*)ends, part_k);
+    e = launch_kernel(lin_rows_kernel<float, kDq>, dim3(stk, tk), dim3(kT), 0, st, false, a, starts, part_q);
+    if (e == cudaSuccess) e = launch_kernel(lin_rows_kernel<float, kDk>, dim3(stk, tk), dim3(kT), 0, st, false, a, (const float*)ends, (float*)nullptr);
+    if (e == cudaSuccess) e = launch_kernel(lin_rows_kernel<float, kDv>, dim3(sth, tv), dim3(kT), 0, st, false, a, (const float*)ends, part_k);
     if (e == cudaSuccess)
-        e = launch_kernel(lin_gates_kernel<T>, dim3(sth), dim3(kT), 0, st, false, a, (const float*)part_q, (int)tk, (const float*)part_k,
+        e = launch_kernel(lin_gates_kernel<float>, dim3(sth), dim3(kT), 0, st, false, a, (const float*)part_q, (int)tk, (const float*)part_k,
                           (int)tv, (const float*)phi, scan_tiles(sh));
     return e;
 }
@@ -493,6 +491,7 @@ cudaError_t backward_simt(const SeqArgs& a, int dtype, cudaStream_t st) {
 }  // namespace
 
 LinLayout lin_layout(const SeqShape& s, int dtype) {
+    if (dtype == GDN_DTYPE_BF16) return lin_layout_tc(s);
     LinLayout L = {};
     const size_t slots = seg_slots(s.nseq, s.total, kSegF), sth = slots * s.H, state = sth * s.dv * s.dk * 4;
     L.rec_total = align_up(state, kSectionAlign);
@@ -511,8 +510,9 @@ using namespace check;
 bool shape_ok(const SeqShape& s) {
     if (s.nseq < 1 || s.total < 0 || s.H < 1 || s.Hk < 1 || s.H % s.Hk != 0 || !dim_ok(s.dk) || !dim_ok(s.dv)) return false;
     if ((long long)s.nseq + s.total > (1LL << 30)) return false;
-    // grid sizes: (sequence, head, piece of the state) and (slot, head)
-    return (long long)s.nseq * s.H * scan_tiles(s) <= 0x7fffffffLL && (long long)seg_slots(s.nseq, s.total, kSegF) * s.H <= 0x7fffffffLL;
+    // grid sizes: (sequence, head, piece of the state), and (slot, head) or four blocks of it
+    return (long long)s.nseq * s.H * scan_tiles(s) <= 0x7fffffffLL && (long long)seg_slots(s.nseq, s.total, kSegF) * s.H <= 0x7fffffffLL &&
+           (long long)seg_slots(s.nseq, s.total, kLinSegment) * s.H * 4 <= 0x7fffffffLL;
 }
 
 bool strides_ok(const SeqShape& s, int dtype) {
@@ -578,7 +578,7 @@ int gdn_linear_seq_forward(const void* q, int ldq, const void* k, int ldk, const
     a.S_T = S_T;
     a.rec = static_cast<char*>(record);
     a.ws = static_cast<char*>(workspace);
-    const cudaError_t rc = dtype == GDN_DTYPE_F32 ? forward_simt<float>(a, dtype, stream) : forward_simt<__nv_bfloat16>(a, dtype, stream);
+    const cudaError_t rc = dtype == GDN_DTYPE_F32 ? forward_f32(a, stream) : launch_linear_forward_tc(a, stream);
     return rc == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -623,7 +623,7 @@ int gdn_linear_seq_backward(const void* q, int ldq, const void* k, int ldk, cons
     a.dbeta = dbeta;
     a.dS0 = dS0;
     a.ws = static_cast<char*>(workspace);
-    const cudaError_t rc = dtype == GDN_DTYPE_F32 ? backward_simt<float>(a, dtype, stream) : backward_simt<__nv_bfloat16>(a, dtype, stream);
+    const cudaError_t rc = dtype == GDN_DTYPE_F32 ? backward_f32(a, stream) : launch_linear_backward_tc(a, stream);
     return rc == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -1,0 +1,1110 @@
+// gdn_linear_tc.cu -- decay-gated linear attention over packed sequences with bf16 inputs, on the tensor core.
+//
+// Segments of 512 tokens, blocks of 128.  Five kinds of kernels a pass:
+//   lin_local_tc_kernel   what a segment adds to the state (or to its gradient): one product over its tokens
+//   lin_scan_kernel       the states between the segments (gdn_linear_seq.cu), left as bf16 terms
+//   lin_rows_tc_kernel    128 rows of o, dq, dk or dv: the state's product, scaled by row, and then for each block of
+//                         the segment the scores, masked and decayed, and their product
+//   lin_pairs_tc_kernel   the row and column sums of (q.k)(dO.v) that the gates' gradients are made of
+//   lin_gates_tc_kernel   dlog_alpha and dbeta from them
+//
+// Inside a segment the masked scores are formed outright, as an attention without a softmax: at 512 tokens that is
+// about the work of carrying the state from block to block (10 of 16 blocks' scores and their products, against four
+// products with the state and four updates in two terms), and it leaves no chain: every block of rows is on its own.
+//
+// Decays enter as products of numbers up to one: e^{g_t - g_s} between blocks is e^{(from t's block's start to t)} times
+// e^{(from s to t's block's start)}, and inside a block a difference of sums of two floats each.
+#include <cudaTypedefs.h>
+
+#include "gdn_linear.cuh"
+#include "gdn_seq_tc.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace seqtc;
+
+constexpr int kSeg = kLinSegment, kBlk = 128;
+
+// D (+)= A B with the A operand in TMEM: lane = row, two neighbours of K in each 32-bit column.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Gates of a segment by blocks of 128 tokens, four tokens a lane of warp b (b < 4): sums of log2 decays, in doubles,
+// inclusive from the block's start; total: each block's, left in shared memory.
+struct BlockSums {
+    double pre[4];
+};
+__device__ __forceinline__ BlockSums block_sums(const SeqArgs& a, int first, int rows, int h, int b, double* total) {
+    const int lane = threadIdx.x & 31;
+    BlockSums s;
+    float la[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int t = b * kBlk + 4 * lane + e;
+        la[e] = t < rows ? a.la[(size_t)(first + t) * a.sh.H + h] : 0.f;
+    }
+    double x = 0.0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x += (double)gate_log(la[e]);
+        s.pre[e] = x;
+    }
+    const double upto = warp_scan(x) - x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s.pre[e] = (s.pre[e] + upto) * 1.4426950408889634;
+    if (lane == 31) total[b] = s.pre[3];
+    return s;
+}
+
+// Tokens of a head as 64-element by 64-token boxes of shared memory, rows of 128 swizzled bytes.
+constexpr uint32_t kBox = 64 * 128;
+
+// ---------------------------------------------------------------------------
+// C = sum_t c_t a_t b_t^T over a segment's tokens: 128 rows of d_v by 128 columns of d_k a CTA, two CTAs an SM.
+//   forward  c_t = beta_t e^{G - g_t}, a = v, b = k;   BACK  c_t = e^{g_t}, a = dO, b = q
+// c_t a_t is an fp32 operand: three bf16 terms of it (2^-24 of it are left), as the sum is an fp32 output after up to
+// 2^17 tokens; the terms go to TMEM, where each thread holds one row of d_v.  b is bf16 and exact.
+// Warps 0-3 form the terms (32 tokens at a time, two buffers) and store the sum, warp 4 copies, warp 5 multiplies.
+// ---------------------------------------------------------------------------
+constexpr int kLocalThreads = 192, kLocalStages = 3, kLocalTok = 64;
+constexpr uint32_t kLocalStage = 4 * kBox;                       // two boxes of a, two of b
+constexpr uint32_t kLocalBars = kLocalStages * kLocalStage, kLocalCoef = kLocalBars + 128, kLocalSmem = kLocalCoef + kSeg * 4 + 64;
+constexpr uint32_t kLocalA = 128, kLocalABuf = 48, kLocalCols = 256;      // TMEM: sum, then two buffers of three terms of 16
+
+template <bool BACK>
+__global__ void __launch_bounds__(kLocalThreads, 2)
+    lin_local_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, SeqArgs a, float* local, float* gend) {
+    extern __shared__ __align__(1024) char sm[];
+    const SeqShape& sh = a.sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = warp_uniform(tid >> 5);
+    const int slot = blockIdx.x / sh.H, h = blockIdx.x % sh.H, hk = h / (sh.H / sh.Hk);
+    const int tiles_k = (sh.dk + 127) / 128, r0 = blockIdx.y / tiles_k * 128, c0 = blockIdx.y % tiles_k * 128;
+    int s, c, first, rows;
+    if (!slot_segment(sh, kSeg, slot, s, c, first, rows, a.err)) return;
+    const uint32_t base = smem_u32(sm), bars = base + kLocalBars;
+    const uint32_t full0 = bars, empty0 = bars + 24, a_full = bars + 48, a_free = bars + 64, done = bars + 80;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(sm + kLocalBars + 96);
+    volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
+    double* total = reinterpret_cast<double*>(sm + kLocalCoef + kSeg * 4);
+    float* coef = reinterpret_cast<float*>(sm + kLocalCoef);
+    const int n = min(128, sh.dk - c0), m = min(128, sh.dv - r0);       // columns and rows of this tile
+    const int steps = (rows + kLocalTok - 1) / kLocalTok;
+    if (tid == 0) {
+        // full: the copy; empty: the products and the four warps that read a; a_full: four warps; a_free, done: products
+        init_barriers(bars, 11, [&](uint32_t b) { return b >= empty0 && b < a_full ? 5u : b >= a_full && b < a_free ? 4u : 1u; });
+        *dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 5) tmem_alloc(smem_u32(holder), kLocalCols);
+    __syncthreads();
+    const uint32_t tmem = *holder;
+    tc_fence_after();
+    if (warp == 4) {
+        if (elect_one()) {
+            const int na = (m + 63) / 64, nb = (n + 63) / 64;
+            int i = 0;
+            for (; i < steps; ++i) {
+                const int st = i % kLocalStages;
+                if (i >= kLocalStages && !wait_or_dead(empty0 + 8 * st, (i / kLocalStages + 1) & 1, a.err, dead)) break;
+                mbar_expect_tx(full0 + 8 * st, (na + nb) * kBox);
+                const uint32_t at = base + st * kLocalStage;
+                for (int x = 0; x < na; ++x) tma_3d(at + x * kBox, &ma, r0 + 64 * x, h, first + i * kLocalTok, full0 + 8 * st);
+                for (int x = 0; x < nb; ++x) tma_3d(at + (2 + x) * kBox, &mb, c0 + 64 * x, hk, first + i * kLocalTok, full0 + 8 * st);
+            }
+            if (*dead)                                    // copies in flight end before the CTA does
+                for (int j = max(0, i - kLocalStages); j < i; ++j) mbar_wait(full0 + 8 * (j % kLocalStages), (j / kLocalStages) & 1, a.err);
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        const bool leader = elect_one();
+        bool ok = true;
+        for (int i = 0; ok && i < 2 * steps; ++i) {       // 32 tokens
+            const int st = (i >> 1) % kLocalStages, b = i & 1, left = min(32, rows - 32 * i);
+            if (b == 0) ok = wait_or_dead(full0 + 8 * st, ((i >> 1) / kLocalStages) & 1, a.err, dead);
+            if (left > 0) ok = ok && wait_or_dead(a_full + 8 * b, (i >> 1) & 1, a.err, dead);
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+                if (left > 0) {
+                    const uint64_t db = mn_desc<128>(base + st * kLocalStage + 2 * kBox + (i & 1) * 32 * 128, kBox);
+                    const uint32_t id = idesc_bf16(128, n) | kBMn;
+                    for (int k = 0; k < (left + 15) / 16; ++k)
+#pragma unroll
+                        for (int t = 2; t >= 0; --t)      // the small terms first
+                            mma_bf16_ts(tmem, tmem + kLocalA + b * kLocalABuf + 16 * t + 8 * k, db + (k * 2048 >> 4), id, i + k > 0 || t < 2);
+                    mma_commit(a_free + 8 * b);
+                }
+                if (b == 1) mma_commit(empty0 + 8 * st);
+            }
+            __syncwarp();
+        }
+        if (leader) {
+            mma_commit(done);                             // and products in flight end before their TMEM is freed
+            mbar_wait(done, 0, a.err);
+        }
+        __syncwarp();
+    } else {
+        const BlockSums sums = block_sums(a, first, rows, h, warp, total);
+        named_sync(1, 128);
+        {
+            double before = 0.0, behind = 0.0;            // blocks before and behind this warp's
+            for (int b = 0; b < 4; ++b) {
+                if (b < warp) before += total[b];
+                if (b > warp) behind += total[b];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = warp * kBlk + 4 * lane + e;
+                const float d = exp2f((float)(BACK ? before + sums.pre[e] : total[warp] - sums.pre[e] + behind));
+                coef[t] = t >= rows ? 0.f : BACK ? d : d * a.beta[(size_t)(first + t) * sh.H + h];
+            }
+            if (tid == 0 && blockIdx.y == 0) gend[(size_t)slot * sh.H + h] = exp2f((float)(total[0] + behind));
+        }
+        named_sync(1, 128);
+        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+        const int r = 32 * warp + lane;                   // row of the tile
+        for (int i = 0; i < 2 * steps; ++i) {
+            const int st = (i >> 1) % kLocalStages, b = i & 1, left = min(32, rows - 32 * i);
+            if (b == 0) {
+                wait_or_dead(full0 + 8 * st, ((i >> 1) / kLocalStages) & 1, a.err, dead);
+                const int live = rows - (i >> 1) * kLocalTok;
+                if (live < kLocalTok) {                   // tokens of what lies behind: rows of zero, up to whole products
+                    const int upto = (live + 15) & ~15;
+                    for (int x = tid; x < (upto - live) * 16; x += 128)
+                        st_shared16(base + st * kLocalStage + (2 + (x >> 3 & 1)) * kBox + (live + (x >> 4)) * 128 + (x & 7) * 16, 0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+            }
+            if (left > 0) {
+                if (i >= 2) wait_or_dead(a_free + 8 * b, ((i >> 1) + 1) & 1, a.err, dead);
+                __syncwarp();
+                tc_fence_after();
+                const char* raw = sm + st * kLocalStage + (r >> 6) * kBox + (r & 7) * 2;
+                const float* cf = coef + 32 * i;
+                uint32_t p[3][16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float x[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int t = 2 * j + e, at = b * 32 + t;
+                        const uint32_t u = *reinterpret_cast<const unsigned short*>(raw + at * 128 + (((r >> 3 & 7) ^ (at & 7)) << 4));
+                        x[e] = t < left && r < m ? cf[t] * __uint_as_float(u << 16) : 0.f;
+                    }
+                    uint32_t q[3];
+                    split_pair<3>(x[0], x[1], q);
+                    p[0][j] = q[0];
+                    p[1][j] = q[1];
+                    p[2][j] = q[2];
+                }
+#pragma unroll
+                for (int t = 0; t < 3; ++t) tmem_st_n(tmem + kLocalA + b * kLocalABuf + 16 * t + lanes, p[t]);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(a_full + 8 * b);
+            }
+            if (b == 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty0 + 8 * st);
+            }
+        }
+        wait_or_dead(done, 0, a.err, dead);
+        __syncwarp();
+        tc_fence_after();
+        float* out = local + (((size_t)slot * sh.H + h) * sh.dv + r0 + r) * sh.dk + c0;
+#pragma unroll 1
+        for (int x = 0; x < n; x += 16) {
+            uint32_t y[16];
+            tmem_ld_n(tmem + lanes + x, y);
+            tmem_wait_ld();
+            if (r < m) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<uint4*>(out + x + 4 * j) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kLocalCols);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 128 rows of o, dq, dk or dv.
+//   kOut  o_t  = e^{g_t} S q_t + sum_{s <= t} beta_s e^{g_t - g_s} (q_t.k_s) v_s
+//   kDq   dq_t = e^{g_t} S^T dO_t + sum_{s <= t} beta_s e^{g_t - g_s} (dO_t.v_s) k_s
+//   kDk   dk_s = beta_s (e^{G - g_s} dS^T v_s + sum_{t >= s} e^{g_t - g_s} (v_s.dO_t) q_t)
+//   kDv   dv_s = beta_s (e^{G - g_s} dS k_s + sum_{t >= s} e^{g_t - g_s} (k_s.q_t) dO_t)
+// with S the state at the segment's start, dS the gradient at its end.
+//
+// The sum of products stays in TMEM: first the state's product, whose rows the workers scale there, then for each
+// block of 128 tokens the scores (A and B from shared memory), which the workers read, decay, round to bf16 and write
+// back in place as the A operand of the product with X (tokens x columns, from shared memory as it lies).
+// kDq and kDv carry the state as three bf16 terms: q_t.(e^{g_t} S^T dO_t) and v_s.(e^{G - g_s} dS k_s), which the gates'
+// fp32 gradients need, are taken from those fp32 sums.  kOut and kDk read one term, and all round the scores once: each
+// term of a bf16 output is off by one rounding of half a step, beside the output's own.
+//
+// Warps 0-7 work (four a half of the columns), warp 8 copies, warp 9 multiplies.  Where shared memory holds one CTA an
+// SM two blocks' scores are in flight; else two CTAs, one block's scores each.
+// ---------------------------------------------------------------------------
+enum { kOut, kDq, kDk, kDv };
+constexpr int kRowThreads = 320, kMaxRing = 8;
+
+struct RowsPlan {              // shared memory of a launch
+    int ring, rows_x;          // stages; tokens of a stage of X
+    bool two;                  // two blocks' scores in flight
+    uint32_t stage, r, bars, smem;
+};
+
+struct RowsArgs {
+    RowsPlan p;
+    float* part;               // kDq, kDv: the row's dot by halves of the columns, [slot][H][2][512]
+    size_t part_apart;         // floats from one (slot, head) to the next
+    float* heads;              // kDq, kDk where heads share q and k: [total][H][d_k], else null
+    int terms;
+};
+
+// offsets behind the barriers
+constexpr uint32_t kRowHolder = 2 * kMaxRing * 8 + 10 * 8, kRowTotal = kRowHolder + 16, kRowCf = kRowTotal + 32,
+                   kRowHi = kRowCf + kSeg * 4, kRowLo = kRowHi + kBlk * 4, kRowTail = kRowLo + kBlk * 2;
+static_assert(kRowCf % 16 == 0, "read by 16 bytes");
+
+template <int MODE>
+__global__ void __launch_bounds__(kRowThreads, 2)
+    lin_rows_tc_kernel(const __grid_constant__ CUtensorMap mr, const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mx,
+                       const __grid_constant__ CUtensorMap ms, SeqArgs a, RowsArgs ra) {
+    constexpr bool keys = MODE == kDk || MODE == kDv, values = MODE == kOut || MODE == kDv;     // rows are keys; columns d_v
+    extern __shared__ __align__(1024) char sm[];
+    const SeqShape& sh = a.sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = warp_uniform(tid >> 5);
+    void* out = MODE == kOut ? a.out : MODE == kDq ? a.dq : MODE == kDk ? a.dk : a.dv;
+    const int rep = sh.H / sh.Hk, out_heads = values ? sh.H : sh.Hk;
+    const int da = values ? sh.dk : sh.dv, dx = values ? sh.dv : sh.dk;
+    const int slots = seg_slots(sh.nseq, sh.total, kSeg);
+    {
+        int ob, oe;
+        if (seq_outside(sh, ob, oe)) zero_rows<__nv_bfloat16>(out, (size_t)out_heads * dx, ob, oe, sh.total);
+    }
+    // blocks with the most to do first
+    const int at = blockIdx.x % (slots * sh.H), nth = blockIdx.x / (slots * sh.H), rb = keys ? nth : 3 - nth;
+    const int slot = at / sh.H, h = at % sh.H, hk = h / rep;
+    int s, c, first, rows;
+    if (!slot_segment(sh, kSeg, slot, s, c, first, rows, a.err)) return;
+    if (rb * kBlk >= rows) return;
+    const RowsPlan& p = ra.p;
+    const int row_n = min(kBlk, rows - rb * kBlk), last = (rows - 1) / kBlk;
+    const int nblk = keys ? last - rb + 1 : rb + 1;       // blocks of columns: rb .. last, or 0 .. rb
+    const uint32_t base = smem_u32(sm), bars = base + p.bars;
+    const uint32_t full0 = bars, empty0 = bars + 8 * kMaxRing, rfull = bars + 16 * kMaxRing, inter_done = rfull + 8, acc_ready = rfull + 16,
+                   s_full = rfull + 24, p_full = rfull + 40, x_done = rfull + 56, acc_done = rfull + 72;
+    char* tail = sm + p.bars;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(tail + kRowHolder);
+    volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
+    double* total = reinterpret_cast<double*>(tail + kRowTotal);
+    float* cf = reinterpret_cast<float*>(tail + kRowCf);              // a column's factor, blocks other than rb; in rb: beta
+    float* hi = reinterpret_cast<float*>(tail + kRowHi);              // block rb's sums, and what is left of them
+    __nv_bfloat16* lo = reinterpret_cast<__nv_bfloat16*>(tail + kRowLo);
+    const int G = p.two ? 2 : 1;
+    const uint32_t cols = p.two ? 512 : 256, scores = dx > 128 ? 256 : 128;
+    const int n_inter = ra.terms * ((da + 63) / 64), nb = (da + 127) / 128;
+    const auto col_block = [&](int j) { return keys ? rb + j : j; };
+    const auto col_rows = [&](int j) { return min(kBlk, rows - col_block(j) * kBlk); };
+    const auto x_stages = [&](int j) { return (col_rows(j) + p.rows_x - 1) / p.rows_x; };
+    // stage number of block j's first X piece: all blocks but the last have whole ones
+    const auto x_first = [&](int j) {
+        const int g = j / G, in = min(G, nblk - g * G), whole = kBlk / p.rows_x;
+        return n_inter + g * G * (nb + whole) + in * nb + (j - g * G) * whole;
+    };
+    if (tid == 0) {
+        init_barriers(bars, 2 * kMaxRing + 10, [&](uint32_t b) { return b == acc_ready || (b >= p_full && b < x_done) ? 8u : 1u; });
+        *dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 9) tmem_alloc(smem_u32(holder), cols);
+    __syncthreads();
+    const uint32_t tmem = *holder;
+    tc_fence_after();
+    if (warp == 8) {
+        if (elect_one()) {
+            const int hr = MODE == kOut || MODE == kDv ? hk : h, hx = MODE == kOut || MODE == kDv ? h : hk;      // heads of R and B; of X
+            const int na = (da + 63) / 64, nx = (dx + 63) / 64;
+            // tokens of a box beyond the sequence's are read and never used, boxes of none are left out
+            const auto boxes = [&](uint32_t dst, const CUtensorMap* m, int head, int t0, int n, int x0, int nslab, int from, int upto, uint32_t bar) {
+                for (int x = 0; x < nslab; ++x)
+                    for (int y = from; y < upto; ++y)
+                        if (64 * y < n) tma_3d(dst + (x * (upto - from) + y - from) * kBox, m, 64 * (x0 + x), head, t0 + 64 * y, bar);
+            };
+            const int halves = row_n > 64 ? 2 : 1;
+            mbar_expect_tx(rfull, na * halves * kBox);
+            boxes(base + p.r, &mr, hr, first + rb * kBlk, row_n, 0, na, 0, 2, rfull);
+            int it = 0;
+            bool ok = true;
+            const auto stage = [&]() {
+                const int st = it % p.ring;
+                if (ok && it >= p.ring) ok = wait_or_dead(empty0 + 8 * st, (it / p.ring + 1) & 1, a.err, dead);
+                return st;
+            };
+            const size_t apart = (size_t)slots * sh.H;
+            for (int t = ra.terms - 1; ok && t >= 0; --t)             // the small terms first
+                for (int x = 0; ok && x < na; ++x) {
+                    const int st = stage(), z = (int)(t * apart + (size_t)slot * sh.H + h);
+                    if (!ok) break;
+                    const uint32_t dst = base + st * p.stage, bar = full0 + 8 * st;
+                    if (values) {                         // rows of d_v, 64 of d_k along the row
+                        mbar_expect_tx(bar, dx * 128);
+                        tma_3d(dst, &ms, 64 * x, 0, z, bar);
+                    } else {                              // 64 rows of d_v, d_k along the row
+                        mbar_expect_tx(bar, nx * kBox);
+                        for (int y = 0; y < nx; ++y) tma_3d(dst + y * kBox, &ms, 64 * y, 64 * x, z, bar);
+                    }
+                    ++it;
+                }
+            for (int j0 = 0; ok && j0 < nblk; j0 += G) {
+                const int in = min(G, nblk - j0);
+                for (int j = j0; ok && j < j0 + in; ++j)
+                    for (int x = 0; ok && x < nb; ++x) {
+                        const int st = stage();
+                        if (!ok) break;
+                        const int sl = min(2, na - 2 * x), n = col_rows(j);
+                        mbar_expect_tx(full0 + 8 * st, sl * (n > 64 ? 2 : 1) * kBox);
+                        boxes(base + st * p.stage, &mb, hr, first + col_block(j) * kBlk, n, 2 * x, sl, 0, 2, full0 + 8 * st);
+                        ++it;
+                    }
+                for (int j = j0; ok && j < j0 + in; ++j)
+                    for (int x = 0; ok && x < x_stages(j); ++x) {
+                        const int st = stage();
+                        if (!ok) break;
+                        const int n = col_rows(j), from = x * p.rows_x / 64, upto = from + p.rows_x / 64;
+                        int live = 0;
+                        for (int y = from; y < upto; ++y) live += 64 * y < n;
+                        mbar_expect_tx(full0 + 8 * st, nx * live * kBox);
+                        boxes(base + st * p.stage, &mx, hx, first + col_block(j) * kBlk, n, 0, nx, from, upto, full0 + 8 * st);
+                        ++it;
+                    }
+            }
+            if (*dead) {                                  // copies in flight end before the CTA does
+                mbar_wait(rfull, 0, a.err);
+                for (int j = max(0, it - p.ring); j < it; ++j) mbar_wait(full0 + 8 * (j % p.ring), (j / p.ring) & 1, a.err);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        const bool leader = elect_one();
+        int it = 0;
+        bool ok = true;
+        const auto wait = [&](uint32_t bar, uint32_t parity) {
+            const bool w = ok && wait_or_dead(bar, parity, a.err, dead);
+            ok = __all_sync(0xffffffffu, w);
+            tc_fence_after();
+        };
+        wait(rfull, 0);
+        const uint32_t R = base + p.r;
+        for (int t = 0; ok && t < ra.terms; ++t)
+            for (int x = 0; ok && x < (da + 63) / 64; ++x, ++it) {
+                const int st = it % p.ring;
+                wait(full0 + 8 * st, (it / p.ring) & 1);
+                if (leader && ok) {
+                    const uint32_t sb = base + st * p.stage;
+                    for (int k = 0; k < min(4, (da - 64 * x) / 16); ++k)
+                        mma_bf16(tmem, k_desc<128>(R + x * 2 * kBox + 32 * k),
+                                 values ? k_desc<128>(sb + 32 * k) : mn_desc<128>(sb + 2048 * k, kBox),
+                                 idesc_bf16(128, dx) | (values ? 0u : kBMn), t + x + k > 0);
+                    mma_commit(empty0 + 8 * st);
+                }
+                __syncwarp();
+            }
+        if (leader && ok) mma_commit(inter_done);
+        __syncwarp();
+        for (int j0 = 0; ok && j0 < nblk; j0 += G) {
+            const int in = min(G, nblk - j0);
+            const uint32_t use = j0 / G;
+            for (int u = 0; ok && u < in; ++u) {
+                const uint32_t D = tmem + scores + 128 * u;
+                if (use > 0) wait(x_done + 8 * u, (use - 1) & 1);     // the scores before are used up
+                const int n = (col_rows(j0 + u) + 15) & ~15;
+                for (int x = 0; ok && x < nb; ++x, ++it) {
+                    const int st = it % p.ring;
+                    wait(full0 + 8 * st, (it / p.ring) & 1);
+                    if (leader && ok) {
+                        const uint32_t sb = base + st * p.stage;
+                        for (int k = 0; k < min(8, (da - 128 * x) / 16); ++k)
+                            mma_bf16(D, k_desc<128>(R + (2 * x + (k >> 2)) * 2 * kBox + 32 * (k & 3)),
+                                     k_desc<128>(sb + (k >> 2) * 2 * kBox + 32 * (k & 3)), idesc_bf16(128, n), x + k > 0);
+                        mma_commit(empty0 + 8 * st);
+                    }
+                    __syncwarp();
+                }
+                if (leader && ok) mma_commit(s_full + 8 * u);
+                __syncwarp();
+            }
+            if (j0 == 0) wait(acc_ready, 0);
+            for (int u = 0; ok && u < in; ++u) {
+                const uint32_t A = tmem + scores + 128 * u;
+                wait(p_full + 8 * u, use & 1);
+                for (int x = 0; ok && x < x_stages(j0 + u); ++x, ++it) {
+                    const int st = it % p.ring;
+                    wait(full0 + 8 * st, (it / p.ring) & 1);
+                    if (leader && ok) {
+                        const uint32_t sb = base + st * p.stage;
+                        const int k0 = x * p.rows_x / 16, k1 = min(k0 + p.rows_x / 16, (col_rows(j0 + u) + 15) / 16);
+                        for (int k = k0; k < k1; ++k)
+                            mma_bf16_ts(tmem, A + 64 * (k >> 2) + 8 * (k & 3), mn_desc<128>(sb + 2048 * (k - k0), p.rows_x * 128),
+                                        idesc_bf16(128, dx) | kBMn, 1);
+                        mma_commit(empty0 + 8 * st);
+                    }
+                    __syncwarp();
+                }
+                if (leader && ok) mma_commit(x_done + 8 * u);
+                __syncwarp();
+            }
+        }
+        if (leader) {
+            mma_commit(acc_done);                         // and products in flight end before their TMEM is freed
+            mbar_wait(acc_done, 0, a.err);
+        }
+        __syncwarp();
+    } else {
+        const int g = warp >> 2, w4 = warp & 3, row = 32 * w4 + lane;
+        const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+        if (warp < 4) {
+            const BlockSums sums = block_sums(a, first, rows, h, warp, total);
+            named_sync(1, 128);
+            double between = 0.0;                         // blocks between this warp's and rb
+            for (int b = 0; b < 4; ++b)
+                if (b > min(warp, rb) && b < max(warp, rb)) between += total[b];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = warp * kBlk + 4 * lane + e;
+                const float beta = !keys && t < rows ? a.beta[(size_t)(first + t) * sh.H + h] : 1.f;
+                if (warp == rb) {
+                    hi[4 * lane + e] = (float)sums.pre[e];
+                    lo[4 * lane + e] = __float2bfloat16_rn((float)(sums.pre[e] - (double)(float)sums.pre[e]));
+                    cf[t] = beta;
+                } else {
+                    cf[t] = beta * exp2f((float)(keys ? between + sums.pre[e] : total[warp] - sums.pre[e] + between));
+                }
+            }
+        }
+        named_sync(2, 256);
+        double before = 0.0, behind = 0.0;
+        for (int b = 0; b < 4; ++b) {
+            if (b < rb) before += total[b];
+            if (b > rb) behind += total[b];
+        }
+        const float mine = hi[row], mine_lo = __bfloat162float(lo[row]);
+        const double pre = (double)mine + (double)mine_lo;
+        // from the row's block's start, or to its end; and of the state
+        const float rf = exp2f((float)(keys ? total[rb] - pre : pre));
+        const float sf = exp2f((float)(keys ? total[rb] - pre + behind : before + pre));
+        const bool live = row < row_n;
+        const size_t token = (size_t)first + rb * kBlk + row;
+        const int chunks = dx / 16, ch0 = g == 0 ? 0 : (chunks + 1) / 2, ch1 = g == 0 ? (chunks + 1) / 2 : chunks;      // of 16 columns
+        wait_or_dead(inter_done, 0, a.err, dead);
+        __syncwarp();
+        tc_fence_after();
+        {
+            const __nv_bfloat16* z = MODE == kDq ? static_cast<const __nv_bfloat16*>(a.q) + token * sh.ldq + (size_t)hk * sh.dk
+                                                 : static_cast<const __nv_bfloat16*>(a.v) + token * sh.ldv + (size_t)h * sh.dv;
+            float dot = 0.f;
+#pragma unroll 1
+            for (int ch = ch0; ch < ch1; ++ch) {
+                uint32_t x[16];
+                tmem_ld_n(tmem + lanes + 16 * ch, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(sf * __uint_as_float(x[i]));
+                tmem_st_n(tmem + lanes + 16 * ch, x);
+                if ((MODE == kDq || MODE == kDv) && live) {       // q's or v's columns
+                    float y[8];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        ld8<__nv_bfloat16>(z + 16 * ch + 8 * half, y);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dot = fmaf(__uint_as_float(x[8 * half + i]), y[i], dot);
+                    }
+                }
+                __syncwarp();
+            }
+            if ((MODE == kDq || MODE == kDv) && live) ra.part[((size_t)slot * sh.H + h) * ra.part_apart + g * kSeg + rb * kBlk + row] = dot;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_ready);
+        }
+        for (int j = 0; j < nblk; ++j) {
+            const int u = j % G, cb = col_block(j), n = col_rows(j);
+            const uint32_t S = tmem + lanes + scores + 128 * u + 64 * g;
+            wait_or_dead(s_full + 8 * u, (j / G) & 1, a.err, dead);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {                 // 32 columns
+                const int c0 = 64 * g + 32 * q;
+                uint32_t x[32], y[16];
+                if (c0 >= ((n + 15) & ~15) || (cb == rb && (keys ? c0 + 31 < 32 * w4 : c0 > 32 * w4 + 31))) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) y[i] = 0;            // behind the segment, or masked altogether
+                } else {
+                    tmem_ld_n(S + 32 * q, x);
+                    tmem_wait_ld();
+                    if (cb == rb || n < kBlk) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int col = c0 + i;
+                            float f;
+                            if (cb == rb) {
+                                const float d = (hi[col] - mine) + (__bfloat162float(lo[col]) - mine_lo);
+                                f = keys ? exp2f(d) : cf[cb * kBlk + col] * exp2f(-d);
+                            } else {
+                                f = rf * cf[cb * kBlk + col];
+                            }
+                            const bool seen = col < n && (cb != rb || (keys ? col >= row : col <= row));
+                            x[i] = seen ? __float_as_uint(f * __uint_as_float(x[i])) : 0u;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(cf + cb * kBlk + c0 + i);
+                            x[i] = __float_as_uint(rf * __uint_as_float(x[i]) * f.x);
+                            x[i + 1] = __float_as_uint(rf * __uint_as_float(x[i + 1]) * f.y);
+                            x[i + 2] = __float_as_uint(rf * __uint_as_float(x[i + 2]) * f.z);
+                            x[i + 3] = __float_as_uint(rf * __uint_as_float(x[i + 3]) * f.w);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) y[i] = pack_bf16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                }
+                tmem_st_n(S + 16 * q, y);                 // over columns that are read
+            }
+            tmem_wait_st();
+            if (n % 16 != 0) {                            // X's tokens of what lies behind: rows of zero, up to whole products
+                const int stage = x_first(j) + (n - 1) / p.rows_x, at = n % p.rows_x, cnt = 16 - n % 16, pieces = (dx + 63) / 64 * 8;
+                wait_or_dead(full0 + 8 * (stage % p.ring), (stage / p.ring) & 1, a.err, dead);
+                for (int i = tid; i < cnt * pieces; i += 256)
+                    st_shared16(base + stage % p.ring * p.stage + (i % pieces >> 3) * p.rows_x * 128 + (at + i / pieces) * 128 + (i & 7) * 16, 0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full + 8 * u);
+        }
+        wait_or_dead(acc_done, 0, a.err, dead);
+        __syncwarp();
+        tc_fence_after();
+        const float of = keys && live ? a.beta[token * sh.H + h] : 1.f;
+        const bool shared = !values && rep > 1;
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + token * out_heads * dx + (size_t)(values ? h : hk) * dx;
+        float* of32 = shared ? ra.heads + (token * sh.H + h) * dx : nullptr;
+        const bool whole = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+#pragma unroll 1
+        for (int ch = ch0; ch < ch1; ++ch) {
+            uint32_t x[16];
+            tmem_ld_n(tmem + lanes + 16 * ch, x);
+            tmem_wait_ld();
+            float y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = of * __uint_as_float(x[i]);
+            if (live && shared) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<float4*>(of32 + 16 * ch + 4 * i) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            } else if (live) {
+                uint4 v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    v[i] = make_uint4(pack_bf16(y[8 * i], y[8 * i + 1]), pack_bf16(y[8 * i + 2], y[8 * i + 3]), pack_bf16(y[8 * i + 4], y[8 * i + 5]),
+                                      pack_bf16(y[8 * i + 6], y[8 * i + 7]));
+                stg_pieces<2>(o + 16 * ch, v, false, whole);
+            }
+            __syncwarp();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, cols);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Sums of F_ts = e^{g_t - g_s} (q_t.k_s) (dO_t.v_s), s < t, of 128 rows t with the segment's blocks up to theirs: by
+// rows with beta_s, by columns without, and F_tt.  Both scores are products of bf16 inputs, exact but for fp32 sums.
+// Warps 0-7 work, warp 8 copies, warp 9 multiplies.
+// ---------------------------------------------------------------------------
+// floats of a (slot, head): rows, F_tt, q's and v's dots by halves, columns by block of rows
+constexpr int kPartRow = 0, kPartDiag = kSeg, kPartQ = 2 * kSeg, kPartK = 4 * kSeg, kPartCol = 6 * kSeg, kPartAll = 10 * kSeg;
+
+struct PairsPlan {
+    int ring;
+    bool two;
+    uint32_t r2, stages, bars, smem;
+};
+constexpr uint32_t kPairHolder = 2 * kMaxRing * 8 + 6 * 8, kPairTotal = kPairHolder + 16, kPairCf = kPairTotal + 32, kPairBeta = kPairCf + kSeg * 4,
+                   kPairHi = kPairBeta + kSeg * 4, kPairLo = kPairHi + kBlk * 4, kPairCol = kPairLo + kBlk * 4, kPairTail = kPairCol + 2 * 4 * kBlk * 4;
+static_assert(kPairCf % 16 == 0 && kPairBeta % 16 == 0, "read by 16 bytes");
+
+__global__ void __launch_bounds__(kRowThreads, 2)
+    lin_pairs_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mk,
+                        const __grid_constant__ CUtensorMap mv, SeqArgs a, PairsPlan p, float* part) {
+    extern __shared__ __align__(1024) char sm[];
+    const SeqShape& sh = a.sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = warp_uniform(tid >> 5);
+    const int slots = seg_slots(sh.nseq, sh.total, kSeg);
+    const int at = blockIdx.x % (slots * sh.H), rb = 3 - blockIdx.x / (slots * sh.H), slot = at / sh.H, h = at % sh.H, hk = h / (sh.H / sh.Hk);
+    int s, c, first, rows;
+    if (!slot_segment(sh, kSeg, slot, s, c, first, rows, a.err)) return;
+    if (rb * kBlk >= rows) return;
+    const int row_n = min(kBlk, rows - rb * kBlk), nk = (sh.dk + 63) / 64, nv = (sh.dv + 63) / 64;
+    const auto col_rows = [&](int j) { return j == rb ? row_n : kBlk; };
+    const uint32_t base = smem_u32(sm), bars = base + p.bars;
+    const uint32_t full0 = bars, empty0 = bars + 8 * kMaxRing, rfull = bars + 16 * kMaxRing, s_full = rfull + 8, s_used = rfull + 24, done = rfull + 40;
+    char* tail = sm + p.bars;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(tail + kPairHolder);
+    volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
+    double* total = reinterpret_cast<double*>(tail + kPairTotal);
+    float *cf = reinterpret_cast<float*>(tail + kPairCf), *beta = reinterpret_cast<float*>(tail + kPairBeta),
+          *hi = reinterpret_cast<float*>(tail + kPairHi), *lo = reinterpret_cast<float*>(tail + kPairLo), *col = reinterpret_cast<float*>(tail + kPairCol);
+    const int G = p.two ? 2 : 1;
+    const uint32_t cols = p.two ? 512 : 256;
+    if (tid == 0) {
+        init_barriers(bars, 2 * kMaxRing + 6, [&](uint32_t b) { return b >= s_used && b < done ? 8u : 1u; });
+        *dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 9) tmem_alloc(smem_u32(holder), cols);
+    __syncthreads();
+    const uint32_t tmem = *holder;
+    tc_fence_after();
+    if (warp == 8) {
+        if (elect_one()) {
+            const auto slab = [&](uint32_t dst, const CUtensorMap* m, int x, int head, int t0, int n, uint32_t bar) {
+                tma_3d(dst, m, 64 * x, head, t0, bar);
+                if (n > 64) tma_3d(dst + kBox, m, 64 * x, head, t0 + 64, bar);
+            };
+            mbar_expect_tx(rfull, (nk + nv) * (row_n > 64 ? 2 : 1) * kBox);
+            for (int x = 0; x < nk; ++x) slab(base + x * 2 * kBox, &mq, x, hk, first + rb * kBlk, row_n, rfull);
+            for (int x = 0; x < nv; ++x) slab(base + p.r2 + x * 2 * kBox, &mo, x, h, first + rb * kBlk, row_n, rfull);
+            int it = 0;
+            bool ok = true;
+            for (int j = 0; ok && j <= rb; ++j)
+                for (int x = 0; ok && x < nk + nv; ++x) {
+                    const int st = it % p.ring;
+                    if (it >= p.ring && !(ok = wait_or_dead(empty0 + 8 * st, (it / p.ring + 1) & 1, a.err, dead))) break;
+                    mbar_expect_tx(full0 + 8 * st, (col_rows(j) > 64 ? 2 : 1) * kBox);
+                    if (x < nk) slab(base + p.stages + st * 2 * kBox, &mk, x, hk, first + j * kBlk, col_rows(j), full0 + 8 * st);
+                    else slab(base + p.stages + st * 2 * kBox, &mv, x - nk, h, first + j * kBlk, col_rows(j), full0 + 8 * st);
+                    ++it;
+                }
+            if (*dead) {                                  // copies in flight end before the CTA does
+                mbar_wait(rfull, 0, a.err);
+                for (int j = max(0, it - p.ring); j < it; ++j) mbar_wait(full0 + 8 * (j % p.ring), (j / p.ring) & 1, a.err);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        const bool leader = elect_one();
+        int it = 0;
+        bool ok = true;
+        const auto wait = [&](uint32_t bar, uint32_t parity) {
+            const bool w = ok && wait_or_dead(bar, parity, a.err, dead);
+            ok = __all_sync(0xffffffffu, w);
+            tc_fence_after();
+        };
+        wait(rfull, 0);
+        for (int j = 0; ok && j <= rb; ++j) {
+            const int u = j % G;
+            if (j >= G) wait(s_used + 8 * u, (j / G + 1) & 1);
+            const uint32_t id = idesc_bf16(128, (col_rows(j) + 15) & ~15);
+            for (int x = 0; ok && x < nk + nv; ++x, ++it) {
+                const int st = it % p.ring;
+                wait(full0 + 8 * st, (it / p.ring) & 1);
+                if (leader && ok) {
+                    const bool first_score = x < nk;
+                    const int y = first_score ? x : x - nk, left = (first_score ? sh.dk : sh.dv) - 64 * y;
+                    const uint32_t R = base + (first_score ? 0 : p.r2) + y * 2 * kBox, B = base + p.stages + st * 2 * kBox;
+                    for (int k = 0; k < min(4, left / 16); ++k)
+                        mma_bf16(tmem + 256 * u + (first_score ? 0 : 128), k_desc<128>(R + 32 * k), k_desc<128>(B + 32 * k), id, y + k > 0);
+                    mma_commit(empty0 + 8 * st);
+                }
+                __syncwarp();
+            }
+            if (leader && ok) mma_commit(s_full + 8 * u);
+            __syncwarp();
+        }
+        if (leader) {
+            mma_commit(done);                             // and products in flight end before their TMEM is freed
+            mbar_wait(done, 0, a.err);
+        }
+        __syncwarp();
+    } else {
+        const int g = warp >> 2, w4 = warp & 3, row = 32 * w4 + lane;
+        const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+        if (warp < 4) {
+            const BlockSums sums = block_sums(a, first, rows, h, warp, total);
+            named_sync(1, 128);
+            double between = 0.0;
+            for (int b = warp + 1; b < rb; ++b) between += total[b];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = warp * kBlk + 4 * lane + e;
+                beta[t] = t < rows ? a.beta[(size_t)(first + t) * sh.H + h] : 0.f;
+                cf[t] = exp2f((float)(total[warp] - sums.pre[e] + between));
+                if (warp == rb) {
+                    hi[4 * lane + e] = (float)sums.pre[e];
+                    lo[4 * lane + e] = (float)(sums.pre[e] - (double)(float)sums.pre[e]);
+                }
+            }
+        }
+        named_sync(2, 256);
+        const float mine = hi[row], mine_lo = lo[row], rf = exp2f((float)((double)mine + (double)mine_lo));
+        const bool live = row < row_n;
+        float* out = part + ((size_t)slot * sh.H + h) * kPartAll;
+        float sum = 0.f, diag = 0.f;
+        for (int j = 0; j <= rb; ++j) {
+            const int u = j % G, n = col_rows(j);
+            wait_or_dead(s_full + 8 * u, (j / G) & 1, a.err, dead);
+            __syncwarp();
+            tc_fence_after();
+            float* cj = col + (j & 1) * 4 * kBlk + w4 * kBlk;
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+                const int c0 = 64 * g + 32 * q;
+                float f[32];
+                if (c0 >= ((n + 15) & ~15) || (j == rb && c0 > 32 * w4 + 31)) {
+                    f[0] = 0.f;
+                } else {
+                    const uint32_t D = tmem + lanes + 256 * u + c0;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 16) {
+                        uint32_t x[16], y[16];
+                        tmem_ld_n(D + e, x);
+                        tmem_ld_n(D + 128 + e, y);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int cc = c0 + e + i;
+                            const float w = j == rb ? exp2f((mine - hi[cc]) + (mine_lo - lo[cc])) : rf * cf[j * kBlk + cc];
+                            const bool seen = live && cc < n && (j != rb || cc <= row);
+                            const float v = seen ? w * __uint_as_float(x[i]) * __uint_as_float(y[i]) : 0.f;
+                            const bool own = j == rb && cc == row;
+                            if (own) diag = v;
+                            f[e + i] = own ? 0.f : v;
+                            sum = fmaf(beta[j * kBlk + cc], f[e + i], sum);
+                        }
+                    }
+                    // each lane's column: halves of what is left change places between lanes
+#pragma unroll
+                    for (int half = 16; half > 0; half >>= 1) {
+                        const bool up = (lane & half) != 0;
+#pragma unroll
+                        for (int i = 0; i < half; ++i) {
+                            const float send = up ? f[i] : f[i + half], keep = up ? f[i + half] : f[i];
+                            f[i] = keep + __shfl_xor_sync(0xffffffffu, send, half);
+                        }
+                    }
+                }
+                cj[c0 + lane] = f[0];
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_used + 8 * u);
+            named_sync(3 + g, 128);
+            const int i = tid & 127;
+            if (i < 64) {
+                const float* q = col + (j & 1) * 4 * kBlk + 64 * g + i;
+                out[kPartCol + rb * kSeg + j * kBlk + 64 * g + i] = (q[0] + q[kBlk]) + (q[2 * kBlk] + q[3 * kBlk]);
+            }
+        }
+        // both halves' row sums, one after the other
+        named_sync(2, 256);
+        if (g == 1) {
+            cf[row] = sum;
+            hi[row] = diag;
+        }
+        named_sync(2, 256);
+        if (g == 0 && live) {
+            out[kPartRow + rb * kBlk + row] = sum + cf[row];
+            out[kPartDiag + rb * kBlk + row] = diag + hi[row];
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, cols);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dlog_alpha and dbeta of one (segment, head) from those sums (E_ts = beta_s F_ts), four tokens a thread:
+//   dlog_alpha_u = sum_{s < u <= t} E_ts + sum_{t >= u} q_t.(e^{g_t} S^T dO_t) + sum_{s < u} beta_s v_s.(e^{G - g_s} dS k_s) + e^G <dS, S>
+//   dbeta_s      = sum_{t >= s} F_ts + v_s.(e^{G - g_s} dS k_s)
+// The first is the sum of rows minus columns from u on: terms of one segment only, in fp32.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kBlk) lin_gates_tc_kernel(SeqArgs a, const float* part, const float* phi, int tiles) {
+    const SeqShape& sh = a.sh;
+    int ob, oe;
+    if (seq_outside(sh, ob, oe)) {
+        zero_rows<float>(a.dla, sh.H, ob, oe, sh.total);
+        zero_rows<float>(a.dbeta, sh.H, ob, oe, sh.total);
+    }
+    const int slot = blockIdx.x / sh.H, h = blockIdx.x % sh.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int s, c, first, rows;
+    if (!slot_segment(sh, kSeg, slot, s, c, first, rows, a.err)) return;
+    const size_t at = (size_t)slot * sh.H + h;
+    const float* p = part + at * kPartAll;
+    __shared__ float sums[3][4];
+    float from[4], before[4], beta[4], ph = 0.f;
+    for (int i = tid; i < tiles; i += kBlk) ph += phi[at * tiles + i];
+    const int last = (rows - 1) / kBlk;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int t = 4 * tid + e;
+        from[e] = before[e] = 0.f;
+        if (t >= rows) continue;
+        beta[e] = a.beta[(size_t)(first + t) * sh.H + h];
+        float cc = 0.f;
+        for (int i = t / kBlk; i <= last; ++i) cc += p[kPartCol + i * kSeg + t];
+        const float iq = p[kPartQ + t] + p[kPartQ + kSeg + t], ik = p[kPartK + t] + p[kPartK + kSeg + t];
+        from[e] = p[kPartRow + t] - beta[e] * cc + iq;
+        before[e] = beta[e] * ik;
+        a.dbeta[(size_t)(first + t) * sh.H + h] = cc + p[kPartDiag + t] + ik;
+    }
+    const float f0 = (from[0] + from[1]) + (from[2] + from[3]), b0 = (before[0] + before[1]) + (before[2] + before[3]);
+    float f = f0, b = b0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float fo = __shfl_down_sync(0xffffffffu, f, o), bo = __shfl_up_sync(0xffffffffu, b, o);
+        if (lane + o < 32) f += fo;
+        if (lane >= o) b += bo;
+    }
+    ph = warp_sum(ph);
+    if (lane == 0) {
+        sums[0][warp] = f;
+        sums[2][warp] = ph;
+    }
+    if (lane == 31) sums[1][warp] = b;
+    __syncthreads();
+    // f: from the warp's first token behind this thread's on; b: up to the token before this thread's
+    f -= f0;
+    b -= b0;
+    ph = (sums[2][0] + sums[2][1]) + (sums[2][2] + sums[2][3]);
+    for (int w = 0; w < 4; ++w) {
+        if (w > warp) f += sums[0][w];
+        if (w < warp) b += sums[1][w];
+    }
+    float after[4];
+    after[3] = f + from[3];
+#pragma unroll
+    for (int e = 2; e >= 0; --e) after[e] = after[e + 1] + from[e];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (4 * tid + e < rows) a.dla[(size_t)(first + 4 * tid + e) * sh.H + h] = (after[e] + b) + ph;
+        b += before[e];
+    }
+}
+
+// dq (blockIdx.y 0) and dk of heads that share q and k: the sum of theirs, in their order.
+__global__ void __launch_bounds__(256) lin_heads_kernel(SeqArgs a, const float* dq, const float* dk) {
+    const SeqShape& sh = a.sh;
+    int b = 0, e = sh.total;
+    if (sh.offsets != nullptr) seq_outside(sh, b, e);
+    const float* in = blockIdx.y == 0 ? dq : dk;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(blockIdx.y == 0 ? a.dq : a.dk);
+    const int rep = sh.H / sh.Hk;
+    const long long row = (long long)sh.Hk * sh.dk / 8, n = (e - b) * row;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+        const long long t = b + i / row;
+        const int x = (int)(i % row) * 8, hk = x / sh.dk, d = x % sh.dk;
+        const float* p = in + ((size_t)t * sh.H + (size_t)hk * rep) * sh.dk + d;
+        float y[8], z[8];
+        ld8<float>(p, y);
+        for (int r = 1; r < rep; ++r) {
+            ld8<float>(p + (size_t)r * sh.dk, z);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] += z[j];
+        }
+        *reinterpret_cast<uint4*>(out + (size_t)t * sh.Hk * sh.dk + x) =
+            make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+bool map_3d(CUtensorMap* m, const void* p, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2], uint32_t rows) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
+    }();
+    if (enc == nullptr) return false;
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    // boxes of 64 elements: by `rows` of the second dimension, or (0) one of it and 64 of the third
+    const cuuint32_t box[3] = {64u, rows > 0 ? rows : 1u, rows > 0 ? 1u : 64u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// (d, head, token): what lies behind d comes as zeros, so that any multiple of 16 is one of 64
+bool token_map(CUtensorMap* m, const void* p, const SeqShape& sh, int d, int heads, long long ld) {
+    return map_3d(m, p, {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)sh.total}, {(cuuint64_t)d * 2, (cuuint64_t)ld * 2}, 0);
+}
+// (d_k, d_v, term and slot and head)
+bool state_map(CUtensorMap* m, const void* p, const SeqShape& sh, int terms, int rows) {
+    const cuuint64_t n = (cuuint64_t)terms * seg_slots(sh.nseq, sh.total, kSeg) * sh.H;
+    return map_3d(m, p, {(cuuint64_t)sh.dk, (cuuint64_t)sh.dv, n}, {(cuuint64_t)sh.dk * 2, (cuuint64_t)sh.dk * sh.dv * 2}, (uint32_t)rows);
+}
+
+struct Maps {
+    CUtensorMap q, k, v, o;
+};
+bool token_maps(const SeqArgs& a, bool back, Maps* m) {
+    const SeqShape& sh = a.sh;
+    return token_map(&m->q, a.q, sh, sh.dk, sh.Hk, sh.ldq) && token_map(&m->k, a.k, sh, sh.dk, sh.Hk, sh.ldk) &&
+           token_map(&m->v, a.v, sh, sh.dv, sh.H, sh.ldv) && (!back || token_map(&m->o, a.dout, sh, sh.dv, sh.H, (long long)sh.H * sh.dv));
+}
+
+constexpr uint32_t kSmemMost = 227 * 1024, kSmemHalf = 113 * 1024;      // one CTA an SM, two
+
+RowsPlan rows_plan(int da, int dx) {
+    RowsPlan p = {};
+    const int na = (da + 63) / 64, nx = (dx + 63) / 64;
+    p.rows_x = dx > 128 ? 64 : 128;
+    p.stage = 2 * kBox * (na > 1 || nx > 1 ? 2 : 1);
+    const uint32_t r = na * 2 * kBox;
+    // three stages are what a block's scores and their product take
+    p.two = dx > 128 || r + 3 * p.stage + kRowTail > kSmemHalf;
+    const uint32_t room = (p.two ? kSmemMost : kSmemHalf) - r - kRowTail;
+    p.ring = (int)(room / p.stage) < kMaxRing ? (int)(room / p.stage) : kMaxRing;
+    p.r = p.ring * p.stage;            // behind the ring
+    p.bars = p.r + r;
+    p.smem = p.bars + kRowTail;
+    return p;
+}
+
+template <int MODE>
+cudaError_t rows_go(const Maps& m, const CUtensorMap& ms, const SeqArgs& a, float* part, float* heads, int terms, cudaStream_t st) {
+    static bool done[64];
+    const SeqShape& sh = a.sh;
+    constexpr bool values = MODE == kOut || MODE == kDv;
+    const RowsArgs ra = {rows_plan(values ? sh.dk : sh.dv, values ? sh.dv : sh.dk), part, (size_t)kPartAll, heads, terms};
+    const cudaError_t e = ensure_smem(lin_rows_tc_kernel<MODE>, kSmemMost, done);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * (kSeg / kBlk)));
+    const CUtensorMap &mr = MODE == kOut ? m.q : MODE == kDq ? m.o : MODE == kDk ? m.v : m.k, &mb = MODE == kOut ? m.k : MODE == kDq ? m.v : MODE == kDk ? m.o : m.q,
+                      &mx = MODE == kOut ? m.v : MODE == kDq ? m.k : MODE == kDk ? m.q : m.o;
+    return launch_kernel(lin_rows_tc_kernel<MODE>, grid, dim3(kRowThreads), ra.p.smem, st, false, mr, mb, mx, ms, a, ra);
+}
+
+template <bool BACK>
+cudaError_t local_go(const Maps& m, const SeqArgs& a, float* local, float* gend, cudaStream_t st) {
+    static bool done[64];
+    const SeqShape& sh = a.sh;
+    const cudaError_t e = ensure_smem(lin_local_tc_kernel<BACK>, kLocalSmem, done);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H), ((sh.dv + 127) / 128) * ((sh.dk + 127) / 128));
+    return launch_kernel(lin_local_tc_kernel<BACK>, grid, dim3(kLocalThreads), kLocalSmem, st, false, BACK ? m.o : m.v, BACK ? m.q : m.k, a, local, gend);
+}
+
+cudaError_t pairs_go(const Maps& m, const SeqArgs& a, float* part, cudaStream_t st) {
+    static bool done[64];
+    const SeqShape& sh = a.sh;
+    PairsPlan p = {};
+    p.r2 = (sh.dk + 63) / 64 * 2 * kBox;
+    p.stages = p.r2 + (sh.dv + 63) / 64 * 2 * kBox;
+    p.two = p.stages + 2 * 2 * kBox + kPairTail > kSmemHalf;
+    const uint32_t room = (p.two ? kSmemMost : kSmemHalf) - p.stages - kPairTail;
+    p.ring = (int)(room / (2 * kBox)) < kMaxRing ? (int)(room / (2 * kBox)) : kMaxRing;
+    p.bars = p.stages + p.ring * 2 * kBox;
+    p.smem = p.bars + kPairTail;
+    const cudaError_t e = ensure_smem(lin_pairs_tc_kernel, kSmemMost, done);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * (kSeg / kBlk)));
+    return launch_kernel(lin_pairs_tc_kernel, grid, dim3(kRowThreads), p.smem, st, false, m.q, m.o, m.k, m.v, a, p, part);
+}
+
+}  // namespace
+
+LinLayout lin_layout_tc(const SeqShape& s) {
+    LinLayout L = {};
+    const size_t slots = seg_slots(s.nseq, s.total, kSeg), sth = slots * s.H, state = sth * s.dv * s.dk;
+    L.rec_total = align_up(3 * state * 2, kSectionAlign);
+    L.ws_gend = align_up(L.ws_local + state * 4, kSectionAlign);
+    L.ws_start = align_up(L.ws_gend + sth * 4, kSectionAlign);
+    L.ws_forward = align_up(L.ws_start + state * 2, kSectionAlign);
+    // the backward pass's own, from ws_start on
+    L.ws_end = L.ws_start;
+    L.ws_phi = align_up(L.ws_end + 3 * state * 2, kSectionAlign);
+    L.ws_part = align_up(L.ws_phi + sth * scan_tiles(s) * 4, kSectionAlign);
+    L.ws_heads = align_up(L.ws_part + sth * kPartAll * 4, kSectionAlign);
+    L.ws_total = align_up(L.ws_heads + (s.H > s.Hk ? 2 * (size_t)s.total * s.H * s.dk * 4 : 0), kSectionAlign);
+    return L;
+}
+
+cudaError_t launch_linear_forward_tc(const SeqArgs& a, cudaStream_t st) {
+    const SeqShape& sh = a.sh;
+    const LinLayout L = lin_layout_tc(sh);
+    const int terms = a.rec != nullptr ? 3 : 1;
+    float *local = reinterpret_cast<float*>(a.ws + L.ws_local), *gend = reinterpret_cast<float*>(a.ws + L.ws_gend);
+    char* starts = a.rec != nullptr ? a.rec : a.ws + L.ws_start;
+    const size_t apart = (size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * sh.dv * sh.dk;
+    if (sh.total == 0)           // the states pass through
+        return launch_linear_scan(sh, kSeg, terms, false, local, gend, a.S0, starts, apart, nullptr, nullptr, a.S_T, a.err, st);
+    Maps m;
+    CUtensorMap ms;
+    if (!token_maps(a, false, &m) || !state_map(&ms, starts, sh, 1, sh.dv)) return cudaErrorInvalidValue;
+    cudaError_t e = local_go<false>(m, a, local, gend, st);
+    if (e == cudaSuccess) e = launch_linear_scan(sh, kSeg, terms, false, local, gend, a.S0, starts, apart, nullptr, nullptr, a.S_T, a.err, st);
+    if (e == cudaSuccess) e = rows_go<kOut>(m, ms, a, nullptr, nullptr, 1, st);
+    return e;
+}
+
+cudaError_t launch_linear_backward_tc(const SeqArgs& a, cudaStream_t st) {
+    const SeqShape& sh = a.sh;
+    const LinLayout L = lin_layout_tc(sh);
+    float *local = reinterpret_cast<float*>(a.ws + L.ws_local), *gend = reinterpret_cast<float*>(a.ws + L.ws_gend),
+          *phi = reinterpret_cast<float*>(a.ws + L.ws_phi), *part = reinterpret_cast<float*>(a.ws + L.ws_part), *dq = nullptr, *dk = nullptr;
+    char* ends = a.ws + L.ws_end;
+    if (sh.H > sh.Hk) {
+        dq = reinterpret_cast<float*>(a.ws + L.ws_heads);
+        dk = dq + (size_t)sh.total * sh.H * sh.dk;
+    }
+    const size_t apart = (size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * sh.dv * sh.dk;
+    if (sh.total == 0) return launch_linear_scan(sh, kSeg, 3, true, local, gend, a.dS_T, ends, apart, a.rec, phi, a.dS0, a.err, st);
+    Maps m;
+    CUtensorMap ms, me_keys, me_values;      // the starts by 64 rows of d_v; the ends so and by all
+    if (!token_maps(a, true, &m) || !state_map(&ms, a.rec, sh, 3, 64) || !state_map(&me_keys, ends, sh, 1, 64) || !state_map(&me_values, ends, sh, 3, sh.dv))
+        return cudaErrorInvalidValue;
+    cudaError_t e = local_go<true>(m, a, local, gend, st);
+    if (e == cudaSuccess) e = launch_linear_scan(sh, kSeg, 3, true, local, gend, a.dS_T, ends, apart, a.rec, phi, a.dS0, a.err, st);
+    if (e == cudaSuccess) e = rows_go<kDq>(m, ms, a, part + kPartQ, dq, 3, st);
+    if (e == cudaSuccess) e = rows_go<kDk>(m, me_keys, a, nullptr, dk, 1, st);
+    if (e == cudaSuccess) e = rows_go<kDv>(m, me_values, a, part + kPartK, nullptr, 3, st);
+    if (e == cudaSuccess) e = pairs_go(m, a, part, st);
+    if (e == cudaSuccess)
+        e = launch_kernel(lin_gates_tc_kernel, dim3((unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H)), dim3(kBlk), 0, st, false, a,
+                          (const float*)part, (const float*)phi, scan_tiles(sh));
+    if (e == cudaSuccess && sh.H > sh.Hk) {
+        const long long n = (long long)sh.total * sh.Hk * sh.dk / 8;
+        e = launch_kernel(lin_heads_kernel, dim3((unsigned)((n + 255) / 256 < 16 * kSMs ? (n + 255) / 256 : 16 * kSMs), 2), dim3(256), 0, st, false, a,
+                          (const float*)dq, (const float*)dk);
+    }
+    return e;
+}
+
+}  // namespace gdn
