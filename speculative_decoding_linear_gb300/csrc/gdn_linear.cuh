@@ -40,15 +40,16 @@ __device__ __forceinline__ bool slot_segment(const SeqShape& a, int L, int slot,
 }
 
 // Places in the record (kept from the forward pass to the backward one) and in the workspace.
-//   start   states at the segments' starts, for the rows' kernels: fp32, or bf16 terms
-//   end     gradients of the states at the segments' ends, likewise
+//   start   states at the segments' starts, for the rows' kernels: fp32, or bf16 terms (in the record, if there is one)
+//   gates   what the gates of each (slot, head) give, and where each slot's segment lies (likewise)
+//   end     gradients of the states at the segments' ends
 //   local   what each segment adds to the state (or to its gradient), fp32
 //   gend    e^G of each (slot, head)
 //   phi     e^G <dS_end, S_start> by pieces of the state
 //   part    per token: sums that the gates' gradients are made of
 struct LinLayout {
-    size_t rec_total;
-    size_t ws_local, ws_gend, ws_start, ws_forward, ws_end, ws_phi, ws_part, ws_heads, ws_total;
+    size_t rec_gates, rec_total;
+    size_t ws_local, ws_gend, ws_start, ws_gates, ws_forward, ws_end, ws_phi, ws_part, ws_heads, ws_total;
 };
 LinLayout lin_layout(const SeqShape& s, int dtype);
 LinLayout lin_layout_tc(const SeqShape& s);
@@ -58,30 +59,34 @@ constexpr int kScanThreads = 256;
 constexpr int kScanTile = kScanThreads * 4;          // elements of a state that one CTA of the scan takes
 inline int scan_tiles(const SeqShape& s) { return (s.dk * s.dv + kScanTile - 1) / kScanTile; }
 
-// A sum of logarithms as two floats (times log2 e): what is left of differences of long sums stays exact.
-struct Gate2 {
+// A sum of log decays as two floats (48 bits: differences of long sums stay exact; doubles would take sixteen cycles
+// an operation of a warp), added with the error of each addition kept.
+struct LogSum {
     float hi, lo;
 };
-__device__ __forceinline__ Gate2 gate2(double g) {
-    const double x = g * 1.4426950408889634;
-    const float hi = (float)x;
-    return {hi, (float)(x - hi)};
+__device__ __forceinline__ LogSum operator+(LogSum a, LogSum b) {
+    const float s = a.hi + b.hi, y = s - a.hi;
+    const float e = ((a.hi - (s - y)) + (b.hi - y)) + (a.lo + b.lo);
+    const float hi = s + e;
+    return {hi, e - (hi - s)};
 }
-__device__ __forceinline__ float gate_decay(const Gate2& a, const Gate2& b) { return exp2f((a.hi - b.hi) + (a.lo - b.lo)); }
+__device__ __forceinline__ LogSum operator-(LogSum a, LogSum b) { return a + LogSum{-b.hi, -b.lo}; }
+__device__ __forceinline__ float decay_of(float d) { return exp2f(d * 1.44269504f); }
+__device__ __forceinline__ float decay_of(LogSum a) { return decay_of(a.hi + a.lo); }
 
 // Inclusive sums over a warp's lanes.
-__device__ __forceinline__ double warp_scan(double x) {
+__device__ __forceinline__ LogSum warp_scan(LogSum x) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, x, o);
-        if ((int)(threadIdx.x & 31) >= o) x += y;
+        const LogSum y = {__shfl_up_sync(0xffffffffu, x.hi, o), __shfl_up_sync(0xffffffffu, x.lo, o)};
+        if ((int)(threadIdx.x & 31) >= o) x = x + y;
     }
     return x;
 }
 
 cudaError_t launch_linear_forward_tc(const SeqArgs& a, cudaStream_t st);
 cudaError_t launch_linear_backward_tc(const SeqArgs& a, cudaStream_t st);
-cudaError_t launch_linear_scan(const SeqShape& sh, int L, int terms, bool back, const float* local, const float* gend, const float* S0, void* out,
-                               size_t apart, const void* start, float* phi, float* last, int* err, cudaStream_t st);
+cudaError_t launch_linear_scan(const SeqShape& sh, int L, int terms, bool back, const float* local, const float* gend, int gend_apart, const float* S0,
+                               void* out, size_t apart, const void* start, float* phi, float* last, int* err, cudaStream_t st);
 
 }  // namespace gdn

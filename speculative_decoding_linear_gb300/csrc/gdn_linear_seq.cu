@@ -98,30 +98,30 @@ struct Gates {
 __device__ void load_gates(Gates& g, const SeqArgs& a, int first, int rows, int h) {
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        double x[2];
+        LogSum x[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int t = 2 * lane + j;
-            x[j] = t < rows ? (double)gate_log(a.la[(size_t)(first + t) * a.sh.H + h]) : 0.0;
+            x[j] = {t < rows ? gate_log(a.la[(size_t)(first + t) * a.sh.H + h]) : 0.f, 0.f};
             g.beta[t] = t < rows ? a.beta[(size_t)(first + t) * a.sh.H + h] : 0.f;
         }
-        x[1] += x[0];
-        const double upto = warp_scan(x[1]) - x[1], end = __shfl_sync(0xffffffffu, upto + x[1], 31);
+        x[1] = x[1] + x[0];
+        const LogSum all = warp_scan(x[1]), upto = all - x[1], end = {__shfl_sync(0xffffffffu, all.hi, 31), __shfl_sync(0xffffffffu, all.lo, 31)};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int t = 2 * lane + j;
-            const Gate2 p = gate2(upto + x[j]);
+            const LogSum p = upto + x[j];
             g.hi[t] = p.hi;
             g.lo[t] = p.lo;
-            g.head[t] = exp2f(p.hi);
-            g.tail[t] = gate_decay(gate2(end), p);
+            g.head[t] = decay_of(p);
+            g.tail[t] = decay_of(end - p);
         }
-        if (lane == 0) g.end = exp2f(gate2(end).hi);
+        if (lane == 0) g.end = decay_of(end);
     }
     __syncthreads();
 }
 __device__ __forceinline__ float decay(const Gates& g, int t, int s) {      // e^{g_t - g_s}, s <= t
-    return exp2f((g.hi[t] - g.hi[s]) + (g.lo[t] - g.lo[s]));
+    return decay_of((g.hi[t] - g.hi[s]) + (g.lo[t] - g.lo[s]));
 }
 
 template <typename T>
@@ -388,7 +388,7 @@ __device__ __forceinline__ float4 get_state(const void* in, size_t at, size_t ap
 }
 
 template <int TERMS, bool BACK>
-__global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(SeqShape sh, int L, const float* local, const float* gend, const float* S0,
+__global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(SeqShape sh, int L, const float* local, const float* gend, int gend_apart, const float* S0,
                                                                  void* out, size_t apart, const void* start, float* phi, float* last, int* err) {
     const int state = sh.dv * sh.dk, tiles = (state + kScanTile - 1) / kScanTile;
     const int tile = blockIdx.x % tiles, h = blockIdx.x / tiles % sh.H, s = blockIdx.x / (tiles * sh.H);
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(SeqShape sh, int
             const bool live = mine && c0 + j < n;
             y[j] = live ? ld4<float>(local, at * state + e) : make_float4(0.f, 0.f, 0.f, 0.f);
             if (BACK) z[j] = live ? get_state<TERMS>(start, at * state + e, apart) : make_float4(0.f, 0.f, 0.f, 0.f);
-            ge[j] = c0 + j < n ? gend[at] : 0.f;
+            ge[j] = c0 + j < n ? gend[at * gend_apart] : 0.f;
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
@@ -443,13 +443,13 @@ __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(SeqShape sh, int
 
 }  // namespace
 
-cudaError_t launch_linear_scan(const SeqShape& sh, int L, int terms, bool back, const float* local, const float* gend, const float* S0, void* out,
-                               size_t apart, const void* start, float* phi, float* last, int* err, cudaStream_t st) {
+cudaError_t launch_linear_scan(const SeqShape& sh, int L, int terms, bool back, const float* local, const float* gend, int gend_apart, const float* S0,
+                               void* out, size_t apart, const void* start, float* phi, float* last, int* err, cudaStream_t st) {
     const dim3 grid((unsigned)((size_t)sh.nseq * sh.H * scan_tiles(sh)));
     const auto k = terms == 0 ? (back ? lin_scan_kernel<0, true> : lin_scan_kernel<0, false>)
                    : terms == 1 ? lin_scan_kernel<1, false>
                                 : (back ? lin_scan_kernel<3, true> : lin_scan_kernel<3, false>);
-    return launch_kernel(k, grid, dim3(kScanThreads), 0, st, false, sh, L, local, gend, S0, out, apart, start, phi, last, err);
+    return launch_kernel(k, grid, dim3(kScanThreads), 0, st, false, sh, L, local, gend, gend_apart, S0, out, apart, start, phi, last, err);
 }
 
 namespace {
@@ -461,7 +461,7 @@ cudaError_t forward_f32(const SeqArgs& a, cudaStream_t st) {
     float* gend = reinterpret_cast<float*>(a.ws + L.ws_gend);
     const unsigned sth = (unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSegF) * sh.H), tk = (sh.dk + 63) / 64, tv = (sh.dv + 63) / 64;
     cudaError_t e = launch_kernel(lin_local_kernel<float, false>, dim3(sth, tk * tv), dim3(kT), 0, st, false, a, states, gend);
-    if (e == cudaSuccess) e = launch_linear_scan(sh, kSegF, 0, false, states, gend, a.S0, states, 0, nullptr, nullptr, a.S_T, a.err, st);
+    if (e == cudaSuccess) e = launch_linear_scan(sh, kSegF, 0, false, states, gend, 1, a.S0, states, 0, nullptr, nullptr, a.S_T, a.err, st);
     if (e == cudaSuccess && sh.total > 0)
         e = launch_kernel(lin_rows_kernel<float, kOut>, dim3(sth, tv), dim3(kT), 0, st, false, a, (const float*)states, (float*)nullptr);
     return e;
@@ -477,7 +477,7 @@ cudaError_t backward_f32(const SeqArgs& a, cudaStream_t st) {
     const unsigned sth = (unsigned)(slots * sh.H), stk = (unsigned)(slots * sh.Hk), tk = (sh.dk + 63) / 64, tv = (sh.dv + 63) / 64;
     float *part_q = reinterpret_cast<float*>(a.ws + L.ws_part), *part_k = part_q + slots * sh.H * tk * kSegF;
     cudaError_t e = launch_kernel(lin_local_kernel<float, true>, dim3(sth, tk * tv), dim3(kT), 0, st, false, a, ends, gend);
-    if (e == cudaSuccess) e = launch_linear_scan(sh, kSegF, 0, true, ends, gend, a.dS_T, ends, 0, starts, phi, a.dS0, a.err, st);
+    if (e == cudaSuccess) e = launch_linear_scan(sh, kSegF, 0, true, ends, gend, 1, a.dS_T, ends, 0, starts, phi, a.dS0, a.err, st);
     if (e != cudaSuccess || sh.total == 0) return e;
     e = launch_kernel(lin_rows_kernel<float, kDq>, dim3(stk, tk), dim3(kT), 0, st, false, a, starts, part_q);
     if (e == cudaSuccess) e = launch_kernel(lin_rows_kernel<float, kDk>, dim3(stk, tk), dim3(kT), 0, st, false, a, (const float*)ends, (float*)nullptr);

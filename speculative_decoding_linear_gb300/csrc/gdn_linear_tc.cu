@@ -1,6 +1,7 @@
 // gdn_linear_tc.cu -- decay-gated linear attention over packed sequences with bf16 inputs, on the tensor core.
 //
-// Segments of 512 tokens, blocks of 128.  Five kinds of kernels a pass:
+// Segments of 512 tokens, blocks of 128.  Six kinds of kernels a pass:
+//   lin_prep_kernel       the decays of each segment's tokens
 //   lin_local_tc_kernel   what a segment adds to the state (or to its gradient): one product over its tokens
 //   lin_scan_kernel       the states between the segments (gdn_linear_seq.cu), left as bf16 terms
 //   lin_rows_tc_kernel    128 rows of o, dq, dk or dv: the state's product, scaled by row, and then for each block of
@@ -36,209 +37,350 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-// Gates of a segment by blocks of 128 tokens, four tokens a lane of warp b (b < 4): sums of log2 decays, in doubles,
-// inclusive from the block's start; total: each block's, left in shared memory.
-struct BlockSums {
-    double pre[4];
-};
-__device__ __forceinline__ BlockSums block_sums(const SeqArgs& a, int first, int rows, int h, int b, double* total) {
-    const int lane = threadIdx.x & 31;
-    BlockSums s;
-    float la[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int t = b * kBlk + 4 * lane + e;
-        la[e] = t < rows ? a.la[(size_t)(first + t) * a.sh.H + h] : 0.f;
-    }
-    double x = 0.0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        x += (double)gate_log(la[e]);
-        s.pre[e] = x;
-    }
-    const double upto = warp_scan(x) - x;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s.pre[e] = (s.pre[e] + upto) * 1.4426950408889634;
-    if (lane == 31) total[b] = s.pre[3];
-    return s;
+// What the gates of a (slot, head) give, floats by token; g the sum of log decays from the segment's start to the token
+// and with it, G to the segment's end, b that from the block's start, B to the block's end.
+constexpr int kGCoef = 0,                    // beta e^{G - g}: what the token adds to the state at the segment's end
+    kGHead = kSeg,                           // e^g
+    kGTail = 2 * kSeg,                       // e^{G - g}
+    kGPre = 3 * kSeg,                        // e^b
+    kGPost = 4 * kSeg,                       // e^{B - b}
+    kGHi = 5 * kSeg, kGLo = 6 * kSeg,        // b as two floats
+    kGBeta = 7 * kSeg,                       // beta; zero behind the segment, as kGCoef
+    kGTot = 8 * kSeg,                        // e^B of the four blocks, e^G
+    kGAll = 8 * kSeg + 32;
+// Behind the gates of all (slot, head): each slot's first token and its tokens, none for an empty slot.
+__device__ __forceinline__ const int2* slot_table(const float* gates, int slots, int H) {
+    return reinterpret_cast<const int2*>(gates + (size_t)slots * H * kGAll);
 }
+
+// A slot's first token and tokens; none where they are not the call's (a record that is not this call's own).
+__device__ __forceinline__ int2 slot_entry(const int2* table, int slot, int total) {
+    const int2 e = table[slot];
+    return e.x < 0 || e.y < 0 || e.y > kSeg || e.x > total - e.y ? make_int2(0, 0) : e;
+}
+
+__global__ void __launch_bounds__(kBlk) lin_prep_kernel(SeqArgs a, float* gates) {
+    const SeqShape& sh = a.sh;
+    const int slot = blockIdx.x / sh.H, h = blockIdx.x % sh.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int s, c, first = 0, rows = 0;
+    const bool is = slot_segment(sh, kSeg, slot, s, c, first, rows, a.err);
+    if (h == 0 && tid == 0) const_cast<int2*>(slot_table(gates, gridDim.x / sh.H, sh.H))[slot] = make_int2(is ? first : 0, is ? rows : 0);
+    if (!is) return;
+    __shared__ LogSum total[4];
+    float la[4], beta[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int t = 4 * tid + e;
+        la[e] = t < rows ? a.la[(size_t)(first + t) * sh.H + h] : 0.f;
+        beta[e] = t < rows ? a.beta[(size_t)(first + t) * sh.H + h] : 0.f;
+    }
+    LogSum pre[4], x = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x = x + LogSum{gate_log(la[e]), 0.f};
+        pre[e] = x;
+    }
+    const LogSum upto = warp_scan(x) - x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) pre[e] = pre[e] + upto;
+    if (lane == 31) total[warp] = pre[3];
+    __syncthreads();
+    LogSum before = {0.f, 0.f}, behind = {0.f, 0.f};
+    for (int b = 0; b < 4; ++b) {
+        if (b < warp) before = before + total[b];
+        if (b > warp) behind = behind + total[b];
+    }
+    float* out = gates + (size_t)blockIdx.x * kGAll;
+    float y[8][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const LogSum left = total[warp] - pre[e];
+        y[2][e] = decay_of(left + behind);
+        y[0][e] = beta[e] * y[2][e];
+        y[1][e] = decay_of(before + pre[e]);
+        y[3][e] = decay_of(pre[e]);
+        y[4][e] = decay_of(left);
+        y[5][e] = pre[e].hi;
+        y[6][e] = pre[e].lo;
+        y[7][e] = beta[e];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(out + i * kSeg + 4 * tid) = make_float4(y[i][0], y[i][1], y[i][2], y[i][3]);
+    if (lane == 31) out[kGTot + warp] = y[3][3];
+    if (tid == 0) out[kGTot + 4] = decay_of(total[0] + behind);
+}
+
+__device__ __forceinline__ float ex2(float x) {      // 2^x, to 2^-22 of it; below 2^-126 zero
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.44269504f;
+
+__device__ __forceinline__ void tmem_st_n(uint32_t t, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+using seqtc::tmem_st_n;
+
+// Place in a ring of n stages and the parity of its use; products are issued from values that the compiler knows to be
+// the same in the whole warp (no division, no early end of a loop).
+struct Ring {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++st == n) {
+            st = 0;
+            ph ^= 1;
+        }
+    }
+};
 
 // Tokens of a head as 64-element by 64-token boxes of shared memory, rows of 128 swizzled bytes.
 constexpr uint32_t kBox = 64 * 128;
 
 // ---------------------------------------------------------------------------
-// C = sum_t c_t a_t b_t^T over a segment's tokens: 128 rows of d_v by 128 columns of d_k a CTA, two CTAs an SM.
-//   forward  c_t = beta_t e^{G - g_t}, a = v, b = k;   BACK  c_t = e^{g_t}, a = dO, b = q
+// C = sum_t c_t a_t b_t^T over a segment's tokens, in tiles of 128 rows of d_v by 128 columns of d_k; one CTA an SM takes
+// tile after tile.   forward  c_t = beta_t e^{G - g_t}, a = v, b = k;   BACK  c_t = e^{g_t}, a = dO, b = q
 // c_t a_t is an fp32 operand: three bf16 terms of it (2^-24 of it are left), as the sum is an fp32 output after up to
-// 2^17 tokens; the terms go to TMEM, where each thread holds one row of d_v.  b is bf16 and exact.
-// Warps 0-3 form the terms (32 tokens at a time, two buffers) and store the sum, warp 4 copies, warp 5 multiplies.
+// 2^17 tokens; the terms go to TMEM, where each thread holds one row of d_v.  b is bf16 and exact.  The tensor core cuts
+// off what does not fit 24 bits at each addition, always toward zero, 1.5e-8 of the sum: so a sum is of 256 tokens, and
+// the second half's is added to the first's in memory, rounded (1.7e-6 of the sum off after 512 tokens in one sum, 9e-7 so).
+// Bound by the products: three for each of the state's, 6.2 k cycles a tile.  Warps 0-7 form the terms (four warps 32
+// tokens, two buffers each), 8-11 move the sums out (two in TMEM) by way of shared memory, 12 copies, 13 multiplies.
 // ---------------------------------------------------------------------------
-constexpr int kLocalThreads = 192, kLocalStages = 3, kLocalTok = 64;
+constexpr int kLocalThreads = 448, kLocalStages = 5, kLocalTok = 64, kLocalHalf = 256;
 constexpr uint32_t kLocalStage = 4 * kBox;                       // two boxes of a, two of b
-constexpr uint32_t kLocalBars = kLocalStages * kLocalStage, kLocalCoef = kLocalBars + 128, kLocalSmem = kLocalCoef + kSeg * 4 + 64;
-constexpr uint32_t kLocalA = 128, kLocalABuf = 48, kLocalCols = 256;      // TMEM: sum, then two buffers of three terms of 16
+constexpr uint32_t kLocalOut = kLocalStages * kLocalStage, kLocalCoef = kLocalOut + 128 * 128 * 4, kLocalBars = kLocalCoef + kLocalStages * kLocalTok * 4,
+                   kLocalNBars = 2 * kLocalStages + 13, kLocalSmem = kLocalBars + 8 * kLocalNBars + 16;
+constexpr uint32_t kLocalA = 256, kLocalABuf = 48;               // TMEM: two sums, then four buffers of three terms of 16
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, bool add) {
+    if (add)
+        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n" ::"l"(reinterpret_cast<uint64_t>(map)),
+                     "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src),
+                     "r"(c0), "r"(c1), "r"(c2)
+                     : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;\n" ::: "memory"); }
+
+struct LocalItems {            // tile i of the launch; empty slots have none
+    int H, tiles_v, tiles_k, slots, total;
+    const int2* table;
+    __device__ __forceinline__ int count() const { return slots * H * tiles_v * tiles_k; }
+    __device__ __forceinline__ int get(int i, int& slot, int& h, int& r0, int& c0, int& first) const {
+        const int tiles = tiles_v * tiles_k, t = i % tiles, sh = i / tiles;
+        slot = sh / H;
+        h = sh % H;
+        r0 = t / tiles_k * 128;
+        c0 = t % tiles_k * 128;
+        const int2 e = slot_entry(table, slot, total);
+        first = warp_uniform(e.x);
+        return warp_uniform(e.y);
+    }
+};
 
 template <bool BACK>
-__global__ void __launch_bounds__(kLocalThreads, 2)
-    lin_local_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, SeqArgs a, float* local, float* gend) {
+__global__ void __launch_bounds__(kLocalThreads, 1)
+    lin_local_tc_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mo, SeqArgs a,
+                        const float* gates) {
     extern __shared__ __align__(1024) char sm[];
     const SeqShape& sh = a.sh;
-    const int tid = threadIdx.x, lane = tid & 31, warp = warp_uniform(tid >> 5);
-    const int slot = blockIdx.x / sh.H, h = blockIdx.x % sh.H, hk = h / (sh.H / sh.Hk);
-    const int tiles_k = (sh.dk + 127) / 128, r0 = blockIdx.y / tiles_k * 128, c0 = blockIdx.y % tiles_k * 128;
-    int s, c, first, rows;
-    if (!slot_segment(sh, kSeg, slot, s, c, first, rows, a.err)) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = warp_uniform(tid >> 5), rep = sh.H / sh.Hk;
+    const int slots = seg_slots(sh.nseq, sh.total, kSeg);
+    const LocalItems items = {sh.H, (sh.dv + 127) / 128, (sh.dk + 127) / 128, slots, sh.total, slot_table(gates, slots, sh.H)};
+    const int count = items.count();
     const uint32_t base = smem_u32(sm), bars = base + kLocalBars;
-    const uint32_t full0 = bars, empty0 = bars + 24, a_full = bars + 48, a_free = bars + 64, done = bars + 80;
-    uint32_t* holder = reinterpret_cast<uint32_t*>(sm + kLocalBars + 96);
+    const uint32_t full0 = bars, empty0 = bars + 8 * kLocalStages, a_full = bars + 16 * kLocalStages, a_free = a_full + 32, acc_full = a_full + 64,
+                   acc_free = a_full + 80, drain = a_full + 96;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(sm + kLocalBars + 8 * kLocalNBars);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
-    double* total = reinterpret_cast<double*>(sm + kLocalCoef + kSeg * 4);
-    float* coef = reinterpret_cast<float*>(sm + kLocalCoef);
-    const int n = min(128, sh.dk - c0), m = min(128, sh.dv - r0);       // columns and rows of this tile
-    const int steps = (rows + kLocalTok - 1) / kLocalTok;
     if (tid == 0) {
-        // full: the copy; empty: the products and the four warps that read a; a_full: four warps; a_free, done: products
-        init_barriers(bars, 11, [&](uint32_t b) { return b >= empty0 && b < a_full ? 5u : b >= a_full && b < a_free ? 4u : 1u; });
+        // full: the copy; empty: the products and the eight warps that read a; a_full, acc_free: four warps; else products
+        init_barriers(bars, kLocalNBars, [&](uint32_t b) { return b >= empty0 && b < a_full ? 9u : (b >= a_full && b < a_free) || (b >= acc_free && b < drain) ? 4u : 1u; });
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    if (warp == 5) tmem_alloc(smem_u32(holder), kLocalCols);
+    if (warp == 13) tmem_alloc(smem_u32(holder), 512);
     __syncthreads();
-    const uint32_t tmem = *holder;
+    const uint32_t tmem = warp_uniform(*holder);
     tc_fence_after();
-    if (warp == 4) {
+    int slot, h, r0, c0, first;
+    Ring ring;
+    if (warp == 12) {
         if (elect_one()) {
-            const int na = (m + 63) / 64, nb = (n + 63) / 64;
-            int i = 0;
-            for (; i < steps; ++i) {
-                const int st = i % kLocalStages;
-                if (i >= kLocalStages && !wait_or_dead(empty0 + 8 * st, (i / kLocalStages + 1) & 1, a.err, dead)) break;
-                mbar_expect_tx(full0 + 8 * st, (na + nb) * kBox);
-                const uint32_t at = base + st * kLocalStage;
-                for (int x = 0; x < na; ++x) tma_3d(at + x * kBox, &ma, r0 + 64 * x, h, first + i * kLocalTok, full0 + 8 * st);
-                for (int x = 0; x < nb; ++x) tma_3d(at + (2 + x) * kBox, &mb, c0 + 64 * x, hk, first + i * kLocalTok, full0 + 8 * st);
+            int issued = 0;
+            bool ok = true;
+            for (int i = blockIdx.x; ok && i < count; i += gridDim.x) {
+                // one thread: no shuffles here
+                const int tiles = items.tiles_v * items.tiles_k, t = i % tiles, s_h = i / tiles;
+                slot = s_h / sh.H;
+                h = s_h % sh.H;
+                r0 = t / items.tiles_k * 128;
+                c0 = t % items.tiles_k * 128;
+                const int2 e = slot_entry(items.table, slot, sh.total);
+                const int na = (min(128, sh.dv - r0) + 63) / 64, nb = (min(128, sh.dk - c0) + 63) / 64;
+                for (int k = 0; ok && k < e.y; k += kLocalTok, ring.next(kLocalStages)) {
+                    const uint32_t at = base + ring.st * kLocalStage, bar = full0 + 8 * ring.st;
+                    if (issued >= kLocalStages && !(ok = wait_or_dead(empty0 + 8 * ring.st, ring.ph ^ 1, a.err, dead))) break;
+                    mbar_expect_tx(bar, (na + nb) * kBox + kLocalTok * 4);
+                    bulk_copy_g2s(base + kLocalCoef + ring.st * kLocalTok * 4, gates + (size_t)s_h * kGAll + (BACK ? kGHead : kGCoef) + k, kLocalTok * 4, bar);
+                    for (int x = 0; x < na; ++x) tma_3d(at + x * kBox, &ma, r0 + 64 * x, h, e.x + k, bar);
+                    for (int x = 0; x < nb; ++x) tma_3d(at + (2 + x) * kBox, &mb, c0 + 64 * x, h / rep, e.x + k, bar);
+                    ++issued;
+                }
             }
             if (*dead)                                    // copies in flight end before the CTA does
-                for (int j = max(0, i - kLocalStages); j < i; ++j) mbar_wait(full0 + 8 * (j % kLocalStages), (j / kLocalStages) & 1, a.err);
+                for (int j = max(0, issued - kLocalStages); j < issued; ++j) mbar_wait(full0 + 8 * (j % kLocalStages), (j / kLocalStages) & 1, a.err);
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == 13) {
         const bool leader = elect_one();
-        bool ok = true;
-        for (int i = 0; ok && i < 2 * steps; ++i) {       // 32 tokens
-            const int st = (i >> 1) % kLocalStages, b = i & 1, left = min(32, rows - 32 * i);
-            if (b == 0) ok = wait_or_dead(full0 + 8 * st, ((i >> 1) / kLocalStages) & 1, a.err, dead);
-            if (left > 0) ok = ok && wait_or_dead(a_full + 8 * b, (i >> 1) & 1, a.err, dead);
-            __syncwarp();
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            if (leader) {
-                if (left > 0) {
-                    const uint64_t db = mn_desc<128>(base + st * kLocalStage + 2 * kBox + (i & 1) * 32 * 128, kBox);
-                    const uint32_t id = idesc_bf16(128, n) | kBMn;
-                    for (int k = 0; k < (left + 15) / 16; ++k)
+        uint32_t unit = 0, step = 0;                      // sums and stages so far
+        for (int i = blockIdx.x; i < count; i += gridDim.x) {
+            const int rows = items.get(i, slot, h, r0, c0, first);
+            const uint32_t id = idesc_bf16(128, min(128, sh.dk - c0)) | kBMn;
+            for (int k = 0; k < rows; k += kLocalTok, ring.next(kLocalStages), ++step) {
+                const uint32_t acc = tmem + 128 * (unit & 1);
+                const int at = k % kLocalHalf;
+                if (at == 0 && unit >= 2) wait_or_dead(acc_free + 8 * (unit & 1), (unit >> 1 & 1) ^ 1, a.err, dead);
+                wait_or_dead(full0 + 8 * ring.st, ring.ph, a.err, dead);
+                const uint64_t db = mn_desc<128>(base + ring.st * kLocalStage + 2 * kBox, kBox);
 #pragma unroll
-                        for (int t = 2; t >= 0; --t)      // the small terms first
-                            mma_bf16_ts(tmem, tmem + kLocalA + b * kLocalABuf + 16 * t + 8 * k, db + (k * 2048 >> 4), id, i + k > 0 || t < 2);
-                    mma_commit(a_free + 8 * b);
+                for (int b = 0; b < 2; ++b) {             // 32 tokens
+                    const int left = rows - k - 32 * b;
+                    const uint32_t buf = 2 * b + (step & 1);
+                    wait_or_dead(a_full + 8 * buf, step >> 1 & 1, a.err, dead);
+                    __syncwarp();
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            if (16 * y < left)
+#pragma unroll
+                                for (int t = 2; t >= 0; --t)      // the small terms first
+                                    mma_bf16_ts(acc, tmem + kLocalA + buf * kLocalABuf + 16 * t + 8 * y, db + ((b * 4096 + y * 2048) >> 4), id,
+                                                at + b + y > 0 || t < 2);
+                        mma_commit(a_free + 8 * buf);
+                        if (b == 1) mma_commit(empty0 + 8 * ring.st);
+                    }
+                    __syncwarp();
                 }
-                if (b == 1) mma_commit(empty0 + 8 * st);
+                if (at + kLocalTok == kLocalHalf || k + kLocalTok >= rows) {
+                    if (leader) mma_commit(acc_full + 8 * (unit & 1));
+                    __syncwarp();
+                    ++unit;
+                }
             }
-            __syncwarp();
         }
-        if (leader) {
-            mma_commit(done);                             // and products in flight end before their TMEM is freed
-            mbar_wait(done, 0, a.err);
+        if (leader) {                                     // products in flight end before their TMEM is freed
+            mma_commit(drain);
+            mbar_wait(drain, 0, a.err);
         }
         __syncwarp();
-    } else {
-        const BlockSums sums = block_sums(a, first, rows, h, warp, total);
-        named_sync(1, 128);
-        {
-            double before = 0.0, behind = 0.0;            // blocks before and behind this warp's
-            for (int b = 0; b < 4; ++b) {
-                if (b < warp) before += total[b];
-                if (b > warp) behind += total[b];
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = warp * kBlk + 4 * lane + e;
-                const float d = exp2f((float)(BACK ? before + sums.pre[e] : total[warp] - sums.pre[e] + behind));
-                coef[t] = t >= rows ? 0.f : BACK ? d : d * a.beta[(size_t)(first + t) * sh.H + h];
-            }
-            if (tid == 0 && blockIdx.y == 0) gend[(size_t)slot * sh.H + h] = exp2f((float)(total[0] + behind));
-        }
-        named_sync(1, 128);
-        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-        const int r = 32 * warp + lane;                   // row of the tile
-        for (int i = 0; i < 2 * steps; ++i) {
-            const int st = (i >> 1) % kLocalStages, b = i & 1, left = min(32, rows - 32 * i);
-            if (b == 0) {
-                wait_or_dead(full0 + 8 * st, ((i >> 1) / kLocalStages) & 1, a.err, dead);
-                const int live = rows - (i >> 1) * kLocalTok;
-                if (live < kLocalTok) {                   // tokens of what lies behind: rows of zero, up to whole products
-                    const int upto = (live + 15) & ~15;
-                    for (int x = tid; x < (upto - live) * 16; x += 128)
-                        st_shared16(base + st * kLocalStage + (2 + (x >> 3 & 1)) * kBox + (live + (x >> 4)) * 128 + (x & 7) * 16, 0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                }
-            }
-            if (left > 0) {
-                if (i >= 2) wait_or_dead(a_free + 8 * b, ((i >> 1) + 1) & 1, a.err, dead);
+    } else if (warp < 8) {
+        const int g = warp >> 2, w4 = warp & 3, r = 32 * w4 + lane, piece = r >> 3 & 7;      // 32 tokens of a stage; row of the tile
+        const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+        uint32_t step = 0;
+        for (int i = blockIdx.x; i < count; i += gridDim.x) {
+            const int rows = items.get(i, slot, h, r0, c0, first);
+            for (int k = 0; k < rows; k += kLocalTok, ring.next(kLocalStages), ++step) {
+                const int left = rows - k - 32 * g;
+                const uint32_t buf = 2 * g + (step & 1), A = tmem + kLocalA + buf * kLocalABuf + lanes;
+                wait_or_dead(full0 + 8 * ring.st, ring.ph, a.err, dead);
+                if (step >= 2) wait_or_dead(a_free + 8 * buf, (step >> 1 & 1) ^ 1, a.err, dead);
                 __syncwarp();
                 tc_fence_after();
-                const char* raw = sm + st * kLocalStage + (r >> 6) * kBox + (r & 7) * 2;
-                const float* cf = coef + 32 * i;
-                uint32_t p[3][16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float x[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int t = 2 * j + e, at = b * 32 + t;
-                        const uint32_t u = *reinterpret_cast<const unsigned short*>(raw + at * 128 + (((r >> 3 & 7) ^ (at & 7)) << 4));
-                        x[e] = t < left && r < m ? cf[t] * __uint_as_float(u << 16) : 0.f;
-                    }
-                    uint32_t q[3];
-                    split_pair<3>(x[0], x[1], q);
-                    p[0][j] = q[0];
-                    p[1][j] = q[1];
-                    p[2][j] = q[2];
+                if (left > 0 && left < 32 && left % 16 != 0) {        // tokens of what lies behind: rows of zero, up to whole products
+                    for (int x = tid & 127; x < (16 - left % 16) * 16; x += 128)
+                        st_shared16(base + ring.st * kLocalStage + (2 + (x >> 3 & 1)) * kBox + (32 * g + left + (x >> 4)) * 128 + (x & 7) * 16, 0, 0, 0, 0);
+                    fence_proxy_async_smem();
                 }
+                const char* raw = sm + ring.st * kLocalStage + (r >> 6) * kBox + 32 * g * 128 + (r & 7) * 2;
+                const float4* cf = reinterpret_cast<const float4*>(sm + kLocalCoef + ring.st * kLocalTok * 4 + 32 * g * 4);
+                if (left > 0) {
 #pragma unroll
-                for (int t = 0; t < 3; ++t) tmem_st_n(tmem + kLocalA + b * kLocalABuf + 16 * t + lanes, p[t]);
-                tmem_wait_st();
+                    for (int half = 0; half < 2; ++half) {            // 16 tokens
+                        uint32_t u[16], p[3][8];
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) u[t] = *reinterpret_cast<const unsigned short*>(raw + (16 * half + t) * 128 + ((piece ^ (t & 7)) << 4));
+                        if (left < 32) {                  // nothing of the tokens behind (their factors are zero, they may be NaN)
+#pragma unroll
+                            for (int t = 0; t < 16; ++t)
+                                if (16 * half + t >= left) u[t] = 0;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 f = cf[4 * half + j / 2];
+                            float2 x = fmul2(j % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y), make_float2(__uint_as_float(u[2 * j] << 16), __uint_as_float(u[2 * j + 1] << 16)));
+#pragma unroll
+                            for (int t = 0; t < 3; ++t) {
+                                p[t][j] = pack_bf16(x.x, x.y);
+                                if (t < 2) x = ffma2(make_float2(__uint_as_float(p[t][j] << 16), __uint_as_float(p[t][j] & 0xffff0000u)), make_float2(-1.f, -1.f), x);
+                            }
+                        }
+#pragma unroll
+                        for (int t = 0; t < 3; ++t) tmem_st_n(A + 16 * t + 8 * half, p[t]);
+                    }
+                    tmem_wait_st();
+                }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(a_full + 8 * b);
-            }
-            if (b == 1) {
+                if (lane == 0) {
+                    mbar_arrive(a_full + 8 * buf);
+                    mbar_arrive(empty0 + 8 * ring.st);
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(empty0 + 8 * st);
             }
         }
-        wait_or_dead(done, 0, a.err, dead);
-        __syncwarp();
-        tc_fence_after();
-        float* out = local + (((size_t)slot * sh.H + h) * sh.dv + r0 + r) * sh.dk + c0;
-#pragma unroll 1
-        for (int x = 0; x < n; x += 16) {
-            uint32_t y[16];
-            tmem_ld_n(tmem + lanes + x, y);
-            tmem_wait_ld();
-            if (r < m) {
+    } else {
+        const int w4 = warp & 3, r = 32 * w4 + lane;
+        const uint32_t lanes = (uint32_t)(32 * w4) << 16, mine = base + kLocalOut + r * 128;
+        uint32_t unit = 0;
+        for (int i = blockIdx.x; i < count; i += gridDim.x) {
+            const int rows = items.get(i, slot, h, r0, c0, first), n = min(128, sh.dk - c0);
+            for (int k = 0; k < rows; k += kLocalHalf, ++unit) {
+                if (unit > 0) {                           // what was there has left shared memory; a first half, arrived
+                    if (warp == 8) bulk_all_done();
+                    named_sync(1, 128);
+                }
+                wait_or_dead(acc_full + 8 * (unit & 1), unit >> 1 & 1, a.err, dead);
+                __syncwarp();
+                tc_fence_after();
+                for (int x = 0; x < n; x += 16) {         // four pieces of 16 bytes, in images of 32 columns, swizzled
+                    uint32_t y[16];
+                    tmem_ld_n(tmem + 128 * (unit & 1) + lanes + x, y);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<uint4*>(out + x + 4 * j) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                    for (int j = 0; j < 4; ++j)
+                        st_shared16(mine + (x >> 5) * 16384 + ((((x >> 2 & 7) + j) ^ (r & 7)) << 4), y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                }
+                tc_fence_before();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_free + 8 * (unit & 1));
+                named_sync(1, 128);
+                if (warp == 8) {
+                    if (lane == 0) {
+                        for (int x = 0; x < n; x += 32) tma_store_3d(&mo, base + kLocalOut + (x >> 5) * 16384, c0 + x, r0, slot * sh.H + h, k > 0);
+                        bulk_commit();
+                    }
+                    __syncwarp();
+                }
             }
         }
+        if (warp == 8) bulk_all_done();
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == 13) {
         tc_fence_after();
-        tmem_dealloc(tmem, kLocalCols);
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -274,18 +416,18 @@ struct RowsArgs {
     float* part;               // kDq, kDv: the row's dot by halves of the columns, [slot][H][2][512]
     size_t part_apart;         // floats from one (slot, head) to the next
     float* heads;              // kDq, kDk where heads share q and k: [total][H][d_k], else null
+    const float* gates;
     int terms;
 };
 
 // offsets behind the barriers
-constexpr uint32_t kRowHolder = 2 * kMaxRing * 8 + 10 * 8, kRowTotal = kRowHolder + 16, kRowCf = kRowTotal + 32,
-                   kRowHi = kRowCf + kSeg * 4, kRowLo = kRowHi + kBlk * 4, kRowTail = kRowLo + kBlk * 2;
+constexpr uint32_t kRowHolder = 2 * kMaxRing * 8 + 10 * 8, kRowCf = kRowHolder + 16, kRowHi = kRowCf + kSeg * 4, kRowLo = kRowHi + kBlk * 4, kRowTail = kRowLo + kBlk * 2;
 static_assert(kRowCf % 16 == 0, "read by 16 bytes");
 
 template <int MODE>
 __global__ void __launch_bounds__(kRowThreads, 2)
     lin_rows_tc_kernel(const __grid_constant__ CUtensorMap mr, const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mx,
-                       const __grid_constant__ CUtensorMap ms, SeqArgs a, RowsArgs ra) {
+                       const __grid_constant__ CUtensorMap ms, const __grid_constant__ CUtensorMap mo, SeqArgs a, RowsArgs ra) {
     constexpr bool keys = MODE == kDk || MODE == kDv, values = MODE == kOut || MODE == kDv;     // rows are keys; columns d_v
     extern __shared__ __align__(1024) char sm[];
     const SeqShape& sh = a.sh;
@@ -301,9 +443,30 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     // blocks with the most to do first
     const int at = blockIdx.x % (slots * sh.H), nth = blockIdx.x / (slots * sh.H), rb = keys ? nth : 3 - nth;
     const int slot = at / sh.H, h = at % sh.H, hk = h / rep;
-    int s, c, first, rows;
-    if (!slot_segment(sh, kSeg, slot, s, c, first, rows, a.err)) return;
+    const int2 seg = slot_entry(slot_table(ra.gates, slots, sh.H), slot, sh.total);
+    const int first = seg.x, rows = warp_uniform(seg.y);
     if (rb * kBlk >= rows) return;
+    // the workers' gates, on their way
+    const float* gt = ra.gates + ((size_t)slot * sh.H + h) * kGAll;
+    const int row = 32 * (warp & 3) + lane;
+    float g_row[5], g_col[2][2], g_tot[4], g_block[2];
+    if (warp < 8) {
+        const int r = rb * kBlk + row;
+        g_row[0] = gt[kGHi + r];
+        g_row[1] = gt[kGLo + r];
+        g_row[2] = gt[(keys ? kGPost : kGPre) + r];
+        g_row[3] = gt[(keys ? kGTail : kGHead) + r];
+        g_row[4] = gt[kGBeta + r];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            g_col[i][0] = gt[(keys ? kGPre : kGPost) + tid + 256 * i];
+            g_col[i][1] = gt[kGBeta + tid + 256 * i];
+        }
+        const float4 t4 = *reinterpret_cast<const float4*>(gt + kGTot);
+        g_tot[0] = t4.x; g_tot[1] = t4.y; g_tot[2] = t4.z; g_tot[3] = t4.w;
+        g_block[0] = tid < kBlk ? gt[kGHi + rb * kBlk + tid] : 0.f;
+        g_block[1] = tid < kBlk ? gt[kGLo + rb * kBlk + tid] : 0.f;
+    }
     const RowsPlan& p = ra.p;
     const int row_n = min(kBlk, rows - rb * kBlk), last = (rows - 1) / kBlk;
     const int nblk = keys ? last - rb + 1 : rb + 1;       // blocks of columns: rb .. last, or 0 .. rb
@@ -313,7 +476,6 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     char* tail = sm + p.bars;
     uint32_t* holder = reinterpret_cast<uint32_t*>(tail + kRowHolder);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
-    double* total = reinterpret_cast<double*>(tail + kRowTotal);
     float* cf = reinterpret_cast<float*>(tail + kRowCf);              // a column's factor, blocks other than rb; in rb: beta
     float* hi = reinterpret_cast<float*>(tail + kRowHi);              // block rb's sums, and what is left of them
     __nv_bfloat16* lo = reinterpret_cast<__nv_bfloat16*>(tail + kRowLo);
@@ -335,7 +497,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     }
     if (warp == 9) tmem_alloc(smem_u32(holder), cols);
     __syncthreads();
-    const uint32_t tmem = *holder;
+    const uint32_t tmem = warp_uniform(*holder);
     tc_fence_after();
     if (warp == 8) {
         if (elect_one()) {
@@ -403,71 +565,68 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         __syncwarp();
     } else if (warp == 9) {
         const bool leader = elect_one();
-        int it = 0;
-        bool ok = true;
+        Ring ring;
         const auto wait = [&](uint32_t bar, uint32_t parity) {
-            const bool w = ok && wait_or_dead(bar, parity, a.err, dead);
-            ok = __all_sync(0xffffffffu, w);
+            wait_or_dead(bar, parity, a.err, dead);
+            __syncwarp();
             tc_fence_after();
         };
         wait(rfull, 0);
-        const uint32_t R = base + p.r;
-        for (int t = 0; ok && t < ra.terms; ++t)
-            for (int x = 0; ok && x < (da + 63) / 64; ++x, ++it) {
-                const int st = it % p.ring;
-                wait(full0 + 8 * st, (it / p.ring) & 1);
-                if (leader && ok) {
-                    const uint32_t sb = base + st * p.stage;
-                    for (int k = 0; k < min(4, (da - 64 * x) / 16); ++k)
-                        mma_bf16(tmem, k_desc<128>(R + x * 2 * kBox + 32 * k),
-                                 values ? k_desc<128>(sb + 32 * k) : mn_desc<128>(sb + 2048 * k, kBox),
-                                 idesc_bf16(128, dx) | (values ? 0u : kBMn), t + x + k > 0);
-                    mma_commit(empty0 + 8 * st);
+        const uint64_t dR = k_desc<128>(base + p.r);
+        for (int t = 0; t < ra.terms; ++t)
+            for (int x = 0; x < (da + 63) / 64; ++x, ring.next(p.ring)) {
+                wait(full0 + 8 * ring.st, ring.ph);
+                if (leader) {
+                    const uint32_t sb = base + ring.st * p.stage;
+                    const uint64_t dA = dR + (x * 2 * kBox >> 4), dB = values ? k_desc<128>(sb) : mn_desc<128>(sb, kBox);
+                    const uint32_t id = idesc_bf16(128, dx) | (values ? 0u : kBMn);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (64 * x + 16 * k < da) mma_bf16(tmem, dA + 2 * k, dB + (values ? 2 * k : 128 * k), id, t + x + k > 0);
+                    mma_commit(empty0 + 8 * ring.st);
                 }
                 __syncwarp();
             }
-        if (leader && ok) mma_commit(inter_done);
+        if (leader) mma_commit(inter_done);
         __syncwarp();
-        for (int j0 = 0; ok && j0 < nblk; j0 += G) {
+        uint32_t use = 0;
+        for (int j0 = 0; j0 < nblk; j0 += G, ++use) {
             const int in = min(G, nblk - j0);
-            const uint32_t use = j0 / G;
-            for (int u = 0; ok && u < in; ++u) {
-                const uint32_t D = tmem + scores + 128 * u;
+            for (int u = 0; u < in; ++u) {
+                const uint32_t D = tmem + scores + 128 * u, id = idesc_bf16(128, (col_rows(j0 + u) + 15) & ~15);
                 if (use > 0) wait(x_done + 8 * u, (use - 1) & 1);     // the scores before are used up
-                const int n = (col_rows(j0 + u) + 15) & ~15;
-                for (int x = 0; ok && x < nb; ++x, ++it) {
-                    const int st = it % p.ring;
-                    wait(full0 + 8 * st, (it / p.ring) & 1);
-                    if (leader && ok) {
-                        const uint32_t sb = base + st * p.stage;
-                        for (int k = 0; k < min(8, (da - 128 * x) / 16); ++k)
-                            mma_bf16(D, k_desc<128>(R + (2 * x + (k >> 2)) * 2 * kBox + 32 * (k & 3)),
-                                     k_desc<128>(sb + (k >> 2) * 2 * kBox + 32 * (k & 3)), idesc_bf16(128, n), x + k > 0);
-                        mma_commit(empty0 + 8 * st);
+                for (int x = 0; x < nb; ++x, ring.next(p.ring)) {
+                    wait(full0 + 8 * ring.st, ring.ph);
+                    if (leader) {
+                        const uint64_t dA = dR + (x * 4 * kBox >> 4), dB = k_desc<128>(base + ring.st * p.stage);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (128 * x + 16 * k < da)
+                                mma_bf16(D, dA + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), dB + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), id, x + k > 0);
+                        mma_commit(empty0 + 8 * ring.st);
                     }
                     __syncwarp();
                 }
-                if (leader && ok) mma_commit(s_full + 8 * u);
+                if (leader) mma_commit(s_full + 8 * u);
                 __syncwarp();
             }
             if (j0 == 0) wait(acc_ready, 0);
-            for (int u = 0; ok && u < in; ++u) {
-                const uint32_t A = tmem + scores + 128 * u;
+            for (int u = 0; u < in; ++u) {
+                const uint32_t A = tmem + scores + 128 * u, id = idesc_bf16(128, dx) | kBMn;
                 wait(p_full + 8 * u, use & 1);
-                for (int x = 0; ok && x < x_stages(j0 + u); ++x, ++it) {
-                    const int st = it % p.ring;
-                    wait(full0 + 8 * st, (it / p.ring) & 1);
-                    if (leader && ok) {
-                        const uint32_t sb = base + st * p.stage;
-                        const int k0 = x * p.rows_x / 16, k1 = min(k0 + p.rows_x / 16, (col_rows(j0 + u) + 15) / 16);
-                        for (int k = k0; k < k1; ++k)
-                            mma_bf16_ts(tmem, A + 64 * (k >> 2) + 8 * (k & 3), mn_desc<128>(sb + 2048 * (k - k0), p.rows_x * 128),
-                                        idesc_bf16(128, dx) | kBMn, 1);
-                        mma_commit(empty0 + 8 * st);
+                for (int left = col_rows(j0 + u), x = 0; left > 0; left -= p.rows_x, x += p.rows_x, ring.next(p.ring)) {
+                    wait(full0 + 8 * ring.st, ring.ph);
+                    if (leader) {
+                        const uint64_t dB = mn_desc<128>(base + ring.st * p.stage, p.rows_x * 128);
+                        const uint32_t A0 = A + x;        // 64 tokens, 32 of their 64 columns
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (16 * k < min(left, p.rows_x)) mma_bf16_ts(tmem, A0 + 64 * (k >> 2) + 8 * (k & 3), dB + 128 * k, id, 1);
+                        mma_commit(empty0 + 8 * ring.st);
                     }
                     __syncwarp();
                 }
-                if (leader && ok) mma_commit(x_done + 8 * u);
+                if (leader) mma_commit(x_done + 8 * u);
                 __syncwarp();
             }
         }
@@ -477,38 +636,24 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         }
         __syncwarp();
     } else {
-        const int g = warp >> 2, w4 = warp & 3, row = 32 * w4 + lane;
+        const int g = warp >> 2, w4 = warp & 3;
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
-        if (warp < 4) {
-            const BlockSums sums = block_sums(a, first, rows, h, warp, total);
-            named_sync(1, 128);
-            double between = 0.0;                         // blocks between this warp's and rb
-            for (int b = 0; b < 4; ++b)
-                if (b > min(warp, rb) && b < max(warp, rb)) between += total[b];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = warp * kBlk + 4 * lane + e;
-                const float beta = !keys && t < rows ? a.beta[(size_t)(first + t) * sh.H + h] : 1.f;
-                if (warp == rb) {
-                    hi[4 * lane + e] = (float)sums.pre[e];
-                    lo[4 * lane + e] = __float2bfloat16_rn((float)(sums.pre[e] - (double)(float)sums.pre[e]));
-                    cf[t] = beta;
-                } else {
-                    cf[t] = beta * exp2f((float)(keys ? between + sums.pre[e] : total[warp] - sums.pre[e] + between));
-                }
-            }
+        for (int i = 0; i < 2; ++i) {
+            const int t = tid + 256 * i, b = t / kBlk;
+            float f = keys ? 1.f : g_col[i][1];
+            if (b != rb) f *= g_col[i][0];
+#pragma unroll
+            for (int m = 1; m < 3; ++m)                   // blocks between
+                if (m > min(b, rb) && m < max(b, rb)) f *= g_tot[m];
+            cf[t] = f;
+        }
+        if (tid < kBlk) {
+            hi[tid] = g_block[0];
+            lo[tid] = __float2bfloat16_rn(g_block[1]);
         }
         named_sync(2, 256);
-        double before = 0.0, behind = 0.0;
-        for (int b = 0; b < 4; ++b) {
-            if (b < rb) before += total[b];
-            if (b > rb) behind += total[b];
-        }
-        const float mine = hi[row], mine_lo = __bfloat162float(lo[row]);
-        const double pre = (double)mine + (double)mine_lo;
-        // from the row's block's start, or to its end; and of the state
-        const float rf = exp2f((float)(keys ? total[rb] - pre : pre));
-        const float sf = exp2f((float)(keys ? total[rb] - pre + behind : before + pre));
+        const float mine = g_row[0], mine_lo = g_row[1], rf = g_row[2], sf = g_row[3];
         const bool live = row < row_n;
         const size_t token = (size_t)first + rb * kBlk + row;
         const int chunks = dx / 16, ch0 = g == 0 ? 0 : (chunks + 1) / 2, ch1 = g == 0 ? (chunks + 1) / 2 : chunks;      // of 16 columns
@@ -520,23 +665,29 @@ __global__ void __launch_bounds__(kRowThreads, 2)
                                                  : static_cast<const __nv_bfloat16*>(a.v) + token * sh.ldv + (size_t)h * sh.dv;
             float dot = 0.f;
 #pragma unroll 1
-            for (int ch = ch0; ch < ch1; ++ch) {
-                uint32_t x[16];
-                tmem_ld_n(tmem + lanes + 16 * ch, x);
+            for (int ch = ch0; ch < ch1; ch += 2) {
+                uint32_t x[2][16];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (ch + e < ch1) tmem_ld_n(tmem + lanes + 16 * (ch + e), x[e]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(sf * __uint_as_float(x[i]));
-                tmem_st_n(tmem + lanes + 16 * ch, x);
-                if ((MODE == kDq || MODE == kDv) && live) {       // q's or v's columns
-                    float y[8];
+                for (int e = 0; e < 2; ++e)
+                    if (ch + e < ch1) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        ld8<__nv_bfloat16>(z + 16 * ch + 8 * half, y);
+                        for (int i = 0; i < 16; ++i) x[e][i] = __float_as_uint(sf * __uint_as_float(x[e][i]));
+                        tmem_st_n(tmem + lanes + 16 * (ch + e), x[e]);
+                        if ((MODE == kDq || MODE == kDv) && live) {       // q's or v's columns
+                            float y[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dot = fmaf(__uint_as_float(x[8 * half + i]), y[i], dot);
+                            for (int half = 0; half < 2; ++half) {
+                                ld8<__nv_bfloat16>(z + 16 * (ch + e) + 8 * half, y);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) dot = fmaf(__uint_as_float(x[e][8 * half + i]), y[i], dot);
+                            }
+                        }
+                        __syncwarp();
                     }
-                }
-                __syncwarp();
             }
             if ((MODE == kDq || MODE == kDv) && live) ra.part[((size_t)slot * sh.H + h) * ra.part_apart + g * kSeg + rb * kBlk + row] = dot;
             tmem_wait_st();
@@ -560,28 +711,39 @@ __global__ void __launch_bounds__(kRowThreads, 2)
                 } else {
                     tmem_ld_n(S + 32 * q, x);
                     tmem_wait_ld();
-                    if (cb == rb || n < kBlk) {
+                    if (cb == rb) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int col = c0 + i;
-                            float f;
-                            if (cb == rb) {
-                                const float d = (hi[col] - mine) + (__bfloat162float(lo[col]) - mine_lo);
-                                f = keys ? exp2f(d) : cf[cb * kBlk + col] * exp2f(-d);
-                            } else {
-                                f = rf * cf[cb * kBlk + col];
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 h4 = *reinterpret_cast<const float4*>(hi + c0 + i), f4 = *reinterpret_cast<const float4*>(cf + cb * kBlk + c0 + i);
+                            const uint2 l2 = *reinterpret_cast<const uint2*>(lo + c0 + i);
+                            const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, fs[4] = {f4.x, f4.y, f4.z, f4.w},
+                                        ls[4] = {__uint_as_float(l2.x << 16), __uint_as_float(l2.x & 0xffff0000u), __uint_as_float(l2.y << 16),
+                                                 __uint_as_float(l2.y & 0xffff0000u)};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int col = c0 + i + e;
+                                const float d = (hs[e] - mine) + (ls[e] - mine_lo);
+                                float f = ex2(keys ? d * kLog2e : d * -kLog2e);
+                                if (!keys) f *= fs[e];
+                                x[i + e] = col < n && (keys ? col >= row : col <= row) ? __float_as_uint(f * __uint_as_float(x[i + e])) : 0u;
                             }
-                            const bool seen = col < n && (cb != rb || (keys ? col >= row : col <= row));
-                            x[i] = seen ? __float_as_uint(f * __uint_as_float(x[i])) : 0u;
                         }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
                             const float4 f = *reinterpret_cast<const float4*>(cf + cb * kBlk + c0 + i);
-                            x[i] = __float_as_uint(rf * __uint_as_float(x[i]) * f.x);
-                            x[i + 1] = __float_as_uint(rf * __uint_as_float(x[i + 1]) * f.y);
-                            x[i + 2] = __float_as_uint(rf * __uint_as_float(x[i + 2]) * f.z);
-                            x[i + 3] = __float_as_uint(rf * __uint_as_float(x[i + 3]) * f.w);
+                            const float2 r2 = make_float2(rf, rf);
+                            const float2 u = fmul2(fmul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), r2), make_float2(f.x, f.y)),
+                                         v = fmul2(fmul2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), r2), make_float2(f.z, f.w));
+                            x[i] = __float_as_uint(u.x);
+                            x[i + 1] = __float_as_uint(u.y);
+                            x[i + 2] = __float_as_uint(v.x);
+                            x[i + 3] = __float_as_uint(v.y);
+                        }
+                        if (n < kBlk) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c0 + i >= n) x[i] = 0u;
                         }
                     }
 #pragma unroll
@@ -604,32 +766,59 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         wait_or_dead(acc_done, 0, a.err, dead);
         __syncwarp();
         tc_fence_after();
-        const float of = keys && live ? a.beta[token * sh.H + h] : 1.f;
-        const bool shared = !values && rep > 1;
+        const float of = keys ? g_row[4] : 1.f;
+        const bool shared = !values && rep > 1, staged = !shared && row_n == kBlk;
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + token * out_heads * dx + (size_t)(values ? h : hk) * dx;
         float* of32 = shared ? ra.heads + (token * sh.H + h) * dx : nullptr;
         const bool whole = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
 #pragma unroll 1
-        for (int ch = ch0; ch < ch1; ++ch) {
-            uint32_t x[16];
-            tmem_ld_n(tmem + lanes + 16 * ch, x);
+        for (int ch = ch0; ch < ch1; ch += 2) {
+            uint32_t x[2][16];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (ch + e < ch1) tmem_ld_n(tmem + lanes + 16 * (ch + e), x[e]);
             tmem_wait_ld();
-            float y[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = of * __uint_as_float(x[i]);
-            if (live && shared) {
+            for (int e = 0; e < 2; ++e)
+                if (ch + e < ch1 && live) {
+                    const int col = 16 * (ch + e);
+                    float y[16];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<float4*>(of32 + 16 * ch + 4 * i) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-            } else if (live) {
-                uint4 v[2];
+                    for (int i = 0; i < 16; ++i) y[i] = of * __uint_as_float(x[e][i]);
+                    if (shared) {
+                        const uint4* v = reinterpret_cast<const uint4*>(y);
+                        const uint4 w[4] = {v[0], v[1], v[2], v[3]};
+                        stg_pieces<4>(of32 + col, w, false, true);
+                    } else {
+                        uint4 v[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    v[i] = make_uint4(pack_bf16(y[8 * i], y[8 * i + 1]), pack_bf16(y[8 * i + 2], y[8 * i + 3]), pack_bf16(y[8 * i + 4], y[8 * i + 5]),
-                                      pack_bf16(y[8 * i + 6], y[8 * i + 7]));
-                stg_pieces<2>(o + 16 * ch, v, false, whole);
-            }
+                        for (int i = 0; i < 2; ++i)
+                            v[i] = make_uint4(pack_bf16(y[8 * i], y[8 * i + 1]), pack_bf16(y[8 * i + 2], y[8 * i + 3]), pack_bf16(y[8 * i + 4], y[8 * i + 5]),
+                                              pack_bf16(y[8 * i + 6], y[8 * i + 7]));
+                        if (staged) {                     // the ring, which nothing reads any more, as boxes of 64 columns
+                            const uint32_t to = base + (col >> 6) * 2 * kBox + row * 128;
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) st_shared16(to + ((((col >> 3 & 7) + i) ^ (row & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+                        } else {
+                            stg_pieces<2>(o + col, v, false, whole);
+                        }
+                    }
+                }
             __syncwarp();
+        }
+        if (staged) {
+            fence_proxy_async_smem();
+            named_sync(2, 256);
+            if (warp == 0) {
+                if (lane == 0) {
+                    for (int x = 0; x < (dx + 63) / 64; ++x)
+                        for (int y = 0; y < 2; ++y)
+                            tma_store_3d(&mo, base + (2 * x + y) * kBox, 64 * x, values ? h : hk, first + rb * kBlk + 64 * y, false);
+                    bulk_commit();
+                    bulk_all_done();
+                }
+                __syncwarp();
+            }
         }
     }
     tc_fence_before();
@@ -653,21 +842,37 @@ struct PairsPlan {
     bool two;
     uint32_t r2, stages, bars, smem;
 };
-constexpr uint32_t kPairHolder = 2 * kMaxRing * 8 + 6 * 8, kPairTotal = kPairHolder + 16, kPairCf = kPairTotal + 32, kPairBeta = kPairCf + kSeg * 4,
+constexpr uint32_t kPairHolder = 2 * kMaxRing * 8 + 6 * 8, kPairCf = kPairHolder + 16, kPairBeta = kPairCf + kSeg * 4,
                    kPairHi = kPairBeta + kSeg * 4, kPairLo = kPairHi + kBlk * 4, kPairCol = kPairLo + kBlk * 4, kPairTail = kPairCol + 2 * 4 * kBlk * 4;
 static_assert(kPairCf % 16 == 0 && kPairBeta % 16 == 0, "read by 16 bytes");
 
 __global__ void __launch_bounds__(kRowThreads, 2)
     lin_pairs_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mk,
-                        const __grid_constant__ CUtensorMap mv, SeqArgs a, PairsPlan p, float* part) {
+                        const __grid_constant__ CUtensorMap mv, SeqArgs a, PairsPlan p, const float* gates, float* part) {
     extern __shared__ __align__(1024) char sm[];
     const SeqShape& sh = a.sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_uniform(tid >> 5);
     const int slots = seg_slots(sh.nseq, sh.total, kSeg);
     const int at = blockIdx.x % (slots * sh.H), rb = 3 - blockIdx.x / (slots * sh.H), slot = at / sh.H, h = at % sh.H, hk = h / (sh.H / sh.Hk);
-    int s, c, first, rows;
-    if (!slot_segment(sh, kSeg, slot, s, c, first, rows, a.err)) return;
+    const int2 seg = slot_entry(slot_table(gates, slots, sh.H), slot, sh.total);
+    const int first = seg.x, rows = warp_uniform(seg.y);
     if (rb * kBlk >= rows) return;
+    // the workers' gates, on their way
+    const float* gt = gates + ((size_t)slot * sh.H + h) * kGAll;
+    float g_col[2][2], g_tot[4], g_hi = 0.f, g_lo = 0.f;
+    if (warp < 8) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            g_col[i][0] = gt[kGPost + tid + 256 * i];
+            g_col[i][1] = gt[kGBeta + tid + 256 * i];
+        }
+        const float4 t4 = *reinterpret_cast<const float4*>(gt + kGTot);
+        g_tot[0] = t4.x; g_tot[1] = t4.y; g_tot[2] = t4.z; g_tot[3] = t4.w;
+        if (tid < kBlk) {
+            g_hi = gt[kGHi + rb * kBlk + tid];
+            g_lo = gt[kGLo + rb * kBlk + tid];
+        }
+    }
     const int row_n = min(kBlk, rows - rb * kBlk), nk = (sh.dk + 63) / 64, nv = (sh.dv + 63) / 64;
     const auto col_rows = [&](int j) { return j == rb ? row_n : kBlk; };
     const uint32_t base = smem_u32(sm), bars = base + p.bars;
@@ -675,7 +880,6 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     char* tail = sm + p.bars;
     uint32_t* holder = reinterpret_cast<uint32_t*>(tail + kPairHolder);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
-    double* total = reinterpret_cast<double*>(tail + kPairTotal);
     float *cf = reinterpret_cast<float*>(tail + kPairCf), *beta = reinterpret_cast<float*>(tail + kPairBeta),
           *hi = reinterpret_cast<float*>(tail + kPairHi), *lo = reinterpret_cast<float*>(tail + kPairLo), *col = reinterpret_cast<float*>(tail + kPairCol);
     const int G = p.two ? 2 : 1;
@@ -687,7 +891,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     }
     if (warp == 9) tmem_alloc(smem_u32(holder), cols);
     __syncthreads();
-    const uint32_t tmem = *holder;
+    const uint32_t tmem = warp_uniform(*holder);
     tc_fence_after();
     if (warp == 8) {
         if (elect_one()) {
@@ -717,33 +921,39 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         __syncwarp();
     } else if (warp == 9) {
         const bool leader = elect_one();
-        int it = 0;
-        bool ok = true;
+        Ring ring;
         const auto wait = [&](uint32_t bar, uint32_t parity) {
-            const bool w = ok && wait_or_dead(bar, parity, a.err, dead);
-            ok = __all_sync(0xffffffffu, w);
+            wait_or_dead(bar, parity, a.err, dead);
+            __syncwarp();
             tc_fence_after();
         };
         wait(rfull, 0);
-        for (int j = 0; ok && j <= rb; ++j) {
-            const int u = j % G;
-            if (j >= G) wait(s_used + 8 * u, (j / G + 1) & 1);
+        uint32_t use = 0;
+        for (int j = 0, u = 0; j <= rb; ++j) {
+            if (use > 0) wait(s_used + 8 * u, (use - 1) & 1);
             const uint32_t id = idesc_bf16(128, (col_rows(j) + 15) & ~15);
-            for (int x = 0; ok && x < nk + nv; ++x, ++it) {
-                const int st = it % p.ring;
-                wait(full0 + 8 * st, (it / p.ring) & 1);
-                if (leader && ok) {
-                    const bool first_score = x < nk;
-                    const int y = first_score ? x : x - nk, left = (first_score ? sh.dk : sh.dv) - 64 * y;
-                    const uint32_t R = base + (first_score ? 0 : p.r2) + y * 2 * kBox, B = base + p.stages + st * 2 * kBox;
-                    for (int k = 0; k < min(4, left / 16); ++k)
-                        mma_bf16(tmem + 256 * u + (first_score ? 0 : 128), k_desc<128>(R + 32 * k), k_desc<128>(B + 32 * k), id, y + k > 0);
-                    mma_commit(empty0 + 8 * st);
+            for (int half = 0; half < 2; ++half) {
+                const int d = half == 0 ? sh.dk : sh.dv;
+                const uint32_t D = tmem + 256 * u + 128 * half;
+                const uint64_t dR = k_desc<128>(base + (half == 0 ? 0 : p.r2));
+                for (int x = 0; 64 * x < d; ++x, ring.next(p.ring)) {
+                    wait(full0 + 8 * ring.st, ring.ph);
+                    if (leader) {
+                        const uint64_t dA = dR + (x * 2 * kBox >> 4), dB = k_desc<128>(base + p.stages + ring.st * 2 * kBox);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (64 * x + 16 * k < d) mma_bf16(D, dA + 2 * k, dB + 2 * k, id, x + k > 0);
+                        mma_commit(empty0 + 8 * ring.st);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
-            if (leader && ok) mma_commit(s_full + 8 * u);
+            if (leader) mma_commit(s_full + 8 * u);
             __syncwarp();
+            if (++u == G) {
+                u = 0;
+                ++use;
+            }
         }
         if (leader) {
             mma_commit(done);                             // and products in flight end before their TMEM is freed
@@ -753,24 +963,22 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     } else {
         const int g = warp >> 2, w4 = warp & 3, row = 32 * w4 + lane;
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
-        if (warp < 4) {
-            const BlockSums sums = block_sums(a, first, rows, h, warp, total);
-            named_sync(1, 128);
-            double between = 0.0;
-            for (int b = warp + 1; b < rb; ++b) between += total[b];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = warp * kBlk + 4 * lane + e;
-                beta[t] = t < rows ? a.beta[(size_t)(first + t) * sh.H + h] : 0.f;
-                cf[t] = exp2f((float)(total[warp] - sums.pre[e] + between));
-                if (warp == rb) {
-                    hi[4 * lane + e] = (float)sums.pre[e];
-                    lo[4 * lane + e] = (float)(sums.pre[e] - (double)(float)sums.pre[e]);
-                }
-            }
+        for (int i = 0; i < 2; ++i) {
+            const int t = tid + 256 * i, b = t / kBlk;
+            float f = g_col[i][0];
+#pragma unroll
+            for (int m = 1; m < 3; ++m)                   // blocks between
+                if (m > b && m < rb) f *= g_tot[m];
+            cf[t] = f;
+            beta[t] = g_col[i][1];
+        }
+        if (tid < kBlk) {
+            hi[tid] = g_hi;
+            lo[tid] = g_lo;
         }
         named_sync(2, 256);
-        const float mine = hi[row], mine_lo = lo[row], rf = exp2f((float)((double)mine + (double)mine_lo));
+        const float mine = hi[row], mine_lo = lo[row], rf = decay_of(mine + mine_lo);
         const bool live = row < row_n;
         float* out = part + ((size_t)slot * sh.H + h) * kPartAll;
         float sum = 0.f, diag = 0.f;
@@ -794,17 +1002,23 @@ __global__ void __launch_bounds__(kRowThreads, 2)
                         tmem_ld_n(D + e, x);
                         tmem_ld_n(D + 128 + e, y);
                         tmem_wait_ld();
+                        const float* bt = beta + j * kBlk + c0 + e;
+                        if (j == rb) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int cc = c0 + e + i;
-                            const float w = j == rb ? exp2f((mine - hi[cc]) + (mine_lo - lo[cc])) : rf * cf[j * kBlk + cc];
-                            const bool seen = live && cc < n && (j != rb || cc <= row);
-                            const float v = seen ? w * __uint_as_float(x[i]) * __uint_as_float(y[i]) : 0.f;
-                            const bool own = j == rb && cc == row;
-                            if (own) diag = v;
-                            f[e + i] = own ? 0.f : v;
-                            sum = fmaf(beta[j * kBlk + cc], f[e + i], sum);
+                            for (int i = 0; i < 16; ++i) {
+                                const int cc = c0 + e + i;
+                                const float w = ex2(((mine - hi[cc]) + (mine_lo - lo[cc])) * kLog2e);
+                                const float v = live && cc < n && cc <= row ? w * __uint_as_float(x[i]) * __uint_as_float(y[i]) : 0.f;
+                                diag = cc == row ? v : diag;
+                                f[e + i] = cc == row ? 0.f : v;
+                            }
+                        } else {
+                            const float* cj4 = cf + j * kBlk + c0 + e;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) f[e + i] = live ? rf * cj4[i] * __uint_as_float(x[i]) * __uint_as_float(y[i]) : 0.f;
                         }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) sum = fmaf(bt[i], f[e + i], sum);
                     }
                     // each lane's column: halves of what is left change places between lanes
 #pragma unroll
@@ -946,7 +1160,7 @@ __global__ void __launch_bounds__(256) lin_heads_kernel(SeqArgs a, const float* 
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-bool map_3d(CUtensorMap* m, const void* p, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2], uint32_t rows) {
+bool map_3d(CUtensorMap* m, const void* p, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2], uint32_t rows, bool f32 = false) {
     static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -955,9 +1169,9 @@ bool map_3d(CUtensorMap* m, const void* p, const cuuint64_t (&dims)[3], const cu
     }();
     if (enc == nullptr) return false;
     const cuuint32_t estr[3] = {1u, 1u, 1u};
-    // boxes of 64 elements: by `rows` of the second dimension, or (0) one of it and 64 of the third
-    const cuuint32_t box[3] = {64u, rows > 0 ? rows : 1u, rows > 0 ? 1u : 64u};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    // boxes of 128 bytes: by `rows` of the second dimension, or (0) one of it and 64 of the third
+    const cuuint32_t box[3] = {f32 ? 32u : 64u, rows > 0 ? rows : 1u, rows > 0 ? 1u : 64u};
+    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // (d, head, token): what lies behind d comes as zeros, so that any multiple of 16 is one of 64
@@ -968,6 +1182,12 @@ bool token_map(CUtensorMap* m, const void* p, const SeqShape& sh, int d, int hea
 bool state_map(CUtensorMap* m, const void* p, const SeqShape& sh, int terms, int rows) {
     const cuuint64_t n = (cuuint64_t)terms * seg_slots(sh.nseq, sh.total, kSeg) * sh.H;
     return map_3d(m, p, {(cuuint64_t)sh.dk, (cuuint64_t)sh.dv, n}, {(cuuint64_t)sh.dk * 2, (cuuint64_t)sh.dk * sh.dv * 2}, (uint32_t)rows);
+}
+
+// (d_k, d_v, slot and head) of what the segments add
+bool local_map(CUtensorMap* m, const float* p, const SeqShape& sh) {
+    const cuuint64_t n = (cuuint64_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H;
+    return map_3d(m, p, {(cuuint64_t)sh.dk, (cuuint64_t)sh.dv, n}, {(cuuint64_t)sh.dk * 4, (cuuint64_t)sh.dk * sh.dv * 4}, sh.dv < 128 ? sh.dv : 128, true);
 }
 
 struct Maps {
@@ -998,30 +1218,41 @@ RowsPlan rows_plan(int da, int dx) {
 }
 
 template <int MODE>
-cudaError_t rows_go(const Maps& m, const CUtensorMap& ms, const SeqArgs& a, float* part, float* heads, int terms, cudaStream_t st) {
+cudaError_t rows_go(const Maps& m, const CUtensorMap& ms, const SeqArgs& a, const float* gates, float* part, float* heads, int terms, cudaStream_t st) {
     static bool done[64];
     const SeqShape& sh = a.sh;
     constexpr bool values = MODE == kOut || MODE == kDv;
-    const RowsArgs ra = {rows_plan(values ? sh.dk : sh.dv, values ? sh.dv : sh.dk), part, (size_t)kPartAll, heads, terms};
+    const RowsArgs ra = {rows_plan(values ? sh.dk : sh.dv, values ? sh.dv : sh.dk), part, (size_t)kPartAll, heads, gates, terms};
     const cudaError_t e = ensure_smem(lin_rows_tc_kernel<MODE>, kSmemMost, done);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * (kSeg / kBlk)));
     const CUtensorMap &mr = MODE == kOut ? m.q : MODE == kDq ? m.o : MODE == kDk ? m.v : m.k, &mb = MODE == kOut ? m.k : MODE == kDq ? m.v : MODE == kDk ? m.o : m.q,
                       &mx = MODE == kOut ? m.v : MODE == kDq ? m.k : MODE == kDk ? m.q : m.o;
-    return launch_kernel(lin_rows_tc_kernel<MODE>, grid, dim3(kRowThreads), ra.p.smem, st, false, mr, mb, mx, ms, a, ra);
+    const int d = values ? sh.dv : sh.dk, out_heads = values ? sh.H : sh.Hk;
+    CUtensorMap mo;
+    if (!token_map(&mo, MODE == kOut ? a.out : MODE == kDq ? a.dq : MODE == kDk ? a.dk : a.dv, sh, d, out_heads, (long long)out_heads * d)) return cudaErrorInvalidValue;
+    return launch_kernel(lin_rows_tc_kernel<MODE>, grid, dim3(kRowThreads), ra.p.smem, st, false, mr, mb, mx, ms, mo, a, ra);
+}
+
+cudaError_t prep_go(const SeqArgs& a, float* gates, cudaStream_t st) {
+    const unsigned grid = (unsigned)((size_t)seg_slots(a.sh.nseq, a.sh.total, kSeg) * a.sh.H);
+    return launch_kernel(lin_prep_kernel, dim3(grid), dim3(kBlk), 0, st, false, a, gates);
 }
 
 template <bool BACK>
-cudaError_t local_go(const Maps& m, const SeqArgs& a, float* local, float* gend, cudaStream_t st) {
+cudaError_t local_go(const Maps& m, const SeqArgs& a, const float* gates, float* local, cudaStream_t st) {
     static bool done[64];
     const SeqShape& sh = a.sh;
+    CUtensorMap mo;
+    if (!local_map(&mo, local, sh)) return cudaErrorInvalidValue;
     const cudaError_t e = ensure_smem(lin_local_tc_kernel<BACK>, kLocalSmem, done);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H), ((sh.dv + 127) / 128) * ((sh.dk + 127) / 128));
-    return launch_kernel(lin_local_tc_kernel<BACK>, grid, dim3(kLocalThreads), kLocalSmem, st, false, BACK ? m.o : m.v, BACK ? m.q : m.k, a, local, gend);
+    const long long tiles = (long long)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * ((sh.dv + 127) / 128) * ((sh.dk + 127) / 128);
+    return launch_kernel(lin_local_tc_kernel<BACK>, dim3((unsigned)(tiles < kSMs ? tiles : kSMs)), dim3(kLocalThreads), kLocalSmem, st, false,
+                         BACK ? m.o : m.v, BACK ? m.q : m.k, mo, a, gates);
 }
 
-cudaError_t pairs_go(const Maps& m, const SeqArgs& a, float* part, cudaStream_t st) {
+cudaError_t pairs_go(const Maps& m, const SeqArgs& a, const float* gates, float* part, cudaStream_t st) {
     static bool done[64];
     const SeqShape& sh = a.sh;
     PairsPlan p = {};
@@ -1035,67 +1266,76 @@ cudaError_t pairs_go(const Maps& m, const SeqArgs& a, float* part, cudaStream_t 
     const cudaError_t e = ensure_smem(lin_pairs_tc_kernel, kSmemMost, done);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * (kSeg / kBlk)));
-    return launch_kernel(lin_pairs_tc_kernel, grid, dim3(kRowThreads), p.smem, st, false, m.q, m.o, m.k, m.v, a, p, part);
+    return launch_kernel(lin_pairs_tc_kernel, grid, dim3(kRowThreads), p.smem, st, false, m.q, m.o, m.k, m.v, a, p, gates, part);
 }
 
 }  // namespace
 
 LinLayout lin_layout_tc(const SeqShape& s) {
     LinLayout L = {};
-    const size_t slots = seg_slots(s.nseq, s.total, kSeg), sth = slots * s.H, state = sth * s.dv * s.dk;
-    L.rec_total = align_up(3 * state * 2, kSectionAlign);
-    L.ws_gend = align_up(L.ws_local + state * 4, kSectionAlign);
-    L.ws_start = align_up(L.ws_gend + sth * 4, kSectionAlign);
-    L.ws_forward = align_up(L.ws_start + state * 2, kSectionAlign);
+    const size_t slots = seg_slots(s.nseq, s.total, kSeg), sth = slots * s.H, state = sth * s.dv * s.dk, gates = sth * kGAll * 4 + slots * 8;
+    L.rec_gates = align_up(3 * state * 2, kSectionAlign);
+    L.rec_total = align_up(L.rec_gates + gates, kSectionAlign);
+    L.ws_start = align_up(L.ws_local + state * 4, kSectionAlign);
+    L.ws_gates = align_up(L.ws_start + state * 2, kSectionAlign);
+    L.ws_forward = align_up(L.ws_gates + gates, kSectionAlign);
     // the backward pass's own, from ws_start on
     L.ws_end = L.ws_start;
     L.ws_phi = align_up(L.ws_end + 3 * state * 2, kSectionAlign);
     L.ws_part = align_up(L.ws_phi + sth * scan_tiles(s) * 4, kSectionAlign);
     L.ws_heads = align_up(L.ws_part + sth * kPartAll * 4, kSectionAlign);
     L.ws_total = align_up(L.ws_heads + (s.H > s.Hk ? 2 * (size_t)s.total * s.H * s.dk * 4 : 0), kSectionAlign);
+    if (L.ws_total < L.ws_forward) L.ws_total = L.ws_forward;
     return L;
 }
 
 cudaError_t launch_linear_forward_tc(const SeqArgs& a, cudaStream_t st) {
     const SeqShape& sh = a.sh;
     const LinLayout L = lin_layout_tc(sh);
-    const int terms = a.rec != nullptr ? 3 : 1;
-    float *local = reinterpret_cast<float*>(a.ws + L.ws_local), *gend = reinterpret_cast<float*>(a.ws + L.ws_gend);
-    char* starts = a.rec != nullptr ? a.rec : a.ws + L.ws_start;
+    const bool keep = a.rec != nullptr;
+    float *local = reinterpret_cast<float*>(a.ws + L.ws_local), *gates = reinterpret_cast<float*>(keep ? a.rec + L.rec_gates : a.ws + L.ws_gates);
+    char* starts = keep ? a.rec : a.ws + L.ws_start;
     const size_t apart = (size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * sh.dv * sh.dk;
-    if (sh.total == 0)           // the states pass through
-        return launch_linear_scan(sh, kSeg, terms, false, local, gend, a.S0, starts, apart, nullptr, nullptr, a.S_T, a.err, st);
+    const auto scan = [&]() {
+        return launch_linear_scan(sh, kSeg, keep ? 3 : 1, false, local, gates + kGTot + 4, kGAll, a.S0, starts, apart, nullptr, nullptr, a.S_T, a.err, st);
+    };
+    if (sh.total == 0) return scan();            // the states pass through
     Maps m;
     CUtensorMap ms;
     if (!token_maps(a, false, &m) || !state_map(&ms, starts, sh, 1, sh.dv)) return cudaErrorInvalidValue;
-    cudaError_t e = local_go<false>(m, a, local, gend, st);
-    if (e == cudaSuccess) e = launch_linear_scan(sh, kSeg, terms, false, local, gend, a.S0, starts, apart, nullptr, nullptr, a.S_T, a.err, st);
-    if (e == cudaSuccess) e = rows_go<kOut>(m, ms, a, nullptr, nullptr, 1, st);
+    cudaError_t e = prep_go(a, gates, st);
+    if (e == cudaSuccess) e = local_go<false>(m, a, gates, local, st);
+    if (e == cudaSuccess) e = scan();
+    if (e == cudaSuccess) e = rows_go<kOut>(m, ms, a, gates, nullptr, nullptr, 1, st);
     return e;
 }
 
 cudaError_t launch_linear_backward_tc(const SeqArgs& a, cudaStream_t st) {
     const SeqShape& sh = a.sh;
     const LinLayout L = lin_layout_tc(sh);
-    float *local = reinterpret_cast<float*>(a.ws + L.ws_local), *gend = reinterpret_cast<float*>(a.ws + L.ws_gend),
-          *phi = reinterpret_cast<float*>(a.ws + L.ws_phi), *part = reinterpret_cast<float*>(a.ws + L.ws_part), *dq = nullptr, *dk = nullptr;
+    const float* gates = reinterpret_cast<const float*>(a.rec + L.rec_gates);
+    float *local = reinterpret_cast<float*>(a.ws + L.ws_local), *phi = reinterpret_cast<float*>(a.ws + L.ws_phi),
+          *part = reinterpret_cast<float*>(a.ws + L.ws_part), *dq = nullptr, *dk = nullptr;
     char* ends = a.ws + L.ws_end;
     if (sh.H > sh.Hk) {
         dq = reinterpret_cast<float*>(a.ws + L.ws_heads);
         dk = dq + (size_t)sh.total * sh.H * sh.dk;
     }
     const size_t apart = (size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * sh.dv * sh.dk;
-    if (sh.total == 0) return launch_linear_scan(sh, kSeg, 3, true, local, gend, a.dS_T, ends, apart, a.rec, phi, a.dS0, a.err, st);
+    const auto scan = [&]() {
+        return launch_linear_scan(sh, kSeg, 3, true, local, gates + kGTot + 4, kGAll, a.dS_T, ends, apart, a.rec, phi, a.dS0, a.err, st);
+    };
+    if (sh.total == 0) return scan();
     Maps m;
     CUtensorMap ms, me_keys, me_values;      // the starts by 64 rows of d_v; the ends so and by all
     if (!token_maps(a, true, &m) || !state_map(&ms, a.rec, sh, 3, 64) || !state_map(&me_keys, ends, sh, 1, 64) || !state_map(&me_values, ends, sh, 3, sh.dv))
         return cudaErrorInvalidValue;
-    cudaError_t e = local_go<true>(m, a, local, gend, st);
-    if (e == cudaSuccess) e = launch_linear_scan(sh, kSeg, 3, true, local, gend, a.dS_T, ends, apart, a.rec, phi, a.dS0, a.err, st);
-    if (e == cudaSuccess) e = rows_go<kDq>(m, ms, a, part + kPartQ, dq, 3, st);
-    if (e == cudaSuccess) e = rows_go<kDk>(m, me_keys, a, nullptr, dk, 1, st);
-    if (e == cudaSuccess) e = rows_go<kDv>(m, me_values, a, part + kPartK, nullptr, 3, st);
-    if (e == cudaSuccess) e = pairs_go(m, a, part, st);
+    cudaError_t e = local_go<true>(m, a, gates, local, st);
+    if (e == cudaSuccess) e = scan();
+    if (e == cudaSuccess) e = rows_go<kDq>(m, ms, a, gates, part + kPartQ, dq, 3, st);
+    if (e == cudaSuccess) e = rows_go<kDk>(m, me_keys, a, gates, nullptr, dk, 1, st);
+    if (e == cudaSuccess) e = rows_go<kDv>(m, me_values, a, gates, part + kPartK, nullptr, 3, st);
+    if (e == cudaSuccess) e = pairs_go(m, a, gates, part, st);
     if (e == cudaSuccess)
         e = launch_kernel(lin_gates_tc_kernel, dim3((unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H)), dim3(kBlk), 0, st, false, a,
                           (const float*)part, (const float*)phi, scan_tiles(sh));
