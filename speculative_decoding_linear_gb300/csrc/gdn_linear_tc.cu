@@ -440,8 +440,8 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         int ob, oe;
         if (seq_outside(sh, ob, oe)) zero_rows<__nv_bfloat16>(out, (size_t)out_heads * dx, ob, oe, sh.total);
     }
-    // blocks with the most to do first
-    const int at = blockIdx.x % (slots * sh.H), nth = blockIdx.x / (slots * sh.H), rb = keys ? nth : 3 - nth;
+    // a segment's four blocks at once, that with the most to do first: they read the same tiles
+    const int at = blockIdx.x / 4, rb = keys ? blockIdx.x % 4 : 3 - blockIdx.x % 4;
     const int slot = at / sh.H, h = at % sh.H, hk = h / rep;
     const int2 seg = slot_entry(slot_table(ra.gates, slots, sh.H), slot, sh.total);
     const int first = seg.x, rows = warp_uniform(seg.y);
@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     const SeqShape& sh = a.sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_uniform(tid >> 5);
     const int slots = seg_slots(sh.nseq, sh.total, kSeg);
-    const int at = blockIdx.x % (slots * sh.H), rb = 3 - blockIdx.x / (slots * sh.H), slot = at / sh.H, h = at % sh.H, hk = h / (sh.H / sh.Hk);
+    const int at = blockIdx.x / 4, rb = 3 - blockIdx.x % 4, slot = at / sh.H, h = at % sh.H, hk = h / (sh.H / sh.Hk);
     const int2 seg = slot_entry(slot_table(gates, slots, sh.H), slot, sh.total);
     const int first = seg.x, rows = warp_uniform(seg.y);
     if (rb * kBlk >= rows) return;
