@@ -399,8 +399,9 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
 // fp32 gradients need, are taken from those fp32 sums.  kOut and kDk read one term, and all round the scores once: each
 // term of a bf16 output is off by one rounding of half a step, beside the output's own.
 //
-// Warps 0-7 work (four a half of the columns), warp 8 copies, warp 9 multiplies.  Where shared memory holds one CTA an
-// SM two blocks' scores are in flight; else two CTAs, one block's scores each.
+// A CTA takes block after block of rows, and the copies and scores of the next run while the last leaves: warps 0-7
+// work (four a half of the columns), warp 8 copies, warp 9 multiplies.  TWO: one CTA an SM, two blocks' scores in flight
+// and the rows out by way of shared memory; else two CTAs, where theirs fit an SM.
 // ---------------------------------------------------------------------------
 enum { kOut, kDq, kDk, kDv };
 constexpr int kRowThreads = 320, kMaxRing = 8;
@@ -408,7 +409,7 @@ constexpr int kRowThreads = 320, kMaxRing = 8;
 struct RowsPlan {              // shared memory of a launch
     int ring, rows_x;          // stages; tokens of a stage of X
     bool two;                  // two blocks' scores in flight
-    uint32_t stage, r, bars, smem;
+    uint32_t stage, r, out, bars, smem;
 };
 
 struct RowsArgs {
@@ -421,77 +422,66 @@ struct RowsArgs {
 };
 
 // offsets behind the barriers
-constexpr uint32_t kRowHolder = 2 * kMaxRing * 8 + 10 * 8, kRowCf = kRowHolder + 16, kRowHi = kRowCf + kSeg * 4, kRowLo = kRowHi + kBlk * 4, kRowTail = kRowLo + kBlk * 2;
+constexpr int kRowNBars = 2 * kMaxRing + 13;
+constexpr uint32_t kRowHolder = kRowNBars * 8, kRowCf = (kRowHolder + 8 + 15) / 16 * 16, kRowHi = kRowCf + kSeg * 4, kRowLo = kRowHi + kBlk * 4,
+                   kRowTail = kRowLo + kBlk * 2;
 static_assert(kRowCf % 16 == 0, "read by 16 bytes");
 
 template <int MODE>
-__global__ void __launch_bounds__(kRowThreads, 2)
+struct RowsItem {
+    int slot, h, rb, first, rows, row_n, nblk;
+    // Item i: four neighbours are a segment's blocks (they read the same tiles), in another order each turn of the grid,
+    // so that every CTA gets long and short ones.  False where there is none.
+    __device__ __forceinline__ bool get(int i, const int2* table, const SeqShape& sh) {
+        constexpr bool keys = MODE == kDk || MODE == kDv;
+        const int at = i >> 2, q = ((i & 3) + i / (int)gridDim.x) & 3;
+        rb = keys ? q : 3 - q;
+        slot = at / sh.H;
+        h = at % sh.H;
+        const int2 e = slot_entry(table, slot, sh.total);
+        first = e.x;
+        rows = e.y;
+        row_n = min(kBlk, rows - rb * kBlk);
+        nblk = keys ? (rows - 1) / kBlk - rb + 1 : rb + 1;       // blocks of columns: rb .. last, or 0 .. rb
+        return rb * kBlk < rows;
+    }
+    __device__ __forceinline__ int col_block(int j) const { return MODE == kDk || MODE == kDv ? rb + j : j; }
+    __device__ __forceinline__ int col_rows(int j) const { return min(kBlk, rows - col_block(j) * kBlk); }
+};
+
+template <int MODE, bool TWO>
+__global__ void __launch_bounds__(kRowThreads, TWO ? 1 : 2)
     lin_rows_tc_kernel(const __grid_constant__ CUtensorMap mr, const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mx,
                        const __grid_constant__ CUtensorMap ms, const __grid_constant__ CUtensorMap mo, SeqArgs a, RowsArgs ra) {
     constexpr bool keys = MODE == kDk || MODE == kDv, values = MODE == kOut || MODE == kDv;     // rows are keys; columns d_v
+    constexpr int G = TWO ? 2 : 1;
+    constexpr uint32_t cols = TWO ? 512 : 256;
     extern __shared__ __align__(1024) char sm[];
     const SeqShape& sh = a.sh;
+    const RowsPlan& p = ra.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_uniform(tid >> 5);
     void* out = MODE == kOut ? a.out : MODE == kDq ? a.dq : MODE == kDk ? a.dk : a.dv;
     const int rep = sh.H / sh.Hk, out_heads = values ? sh.H : sh.Hk;
     const int da = values ? sh.dk : sh.dv, dx = values ? sh.dv : sh.dk;
-    const int slots = seg_slots(sh.nseq, sh.total, kSeg);
+    const int slots = seg_slots(sh.nseq, sh.total, kSeg), count = slots * sh.H * 4;
+    const int2* table = slot_table(ra.gates, slots, sh.H);
     {
         int ob, oe;
         if (seq_outside(sh, ob, oe)) zero_rows<__nv_bfloat16>(out, (size_t)out_heads * dx, ob, oe, sh.total);
     }
-    // a segment's four blocks at once, that with the most to do first: they read the same tiles
-    const int at = blockIdx.x / 4, rb = keys ? blockIdx.x % 4 : 3 - blockIdx.x % 4;
-    const int slot = at / sh.H, h = at % sh.H, hk = h / rep;
-    const int2 seg = slot_entry(slot_table(ra.gates, slots, sh.H), slot, sh.total);
-    const int first = seg.x, rows = warp_uniform(seg.y);
-    if (rb * kBlk >= rows) return;
-    // the workers' gates, on their way
-    const float* gt = ra.gates + ((size_t)slot * sh.H + h) * kGAll;
-    const int row = 32 * (warp & 3) + lane;
-    float g_row[5], g_col[2][2], g_tot[4], g_block[2];
-    if (warp < 8) {
-        const int r = rb * kBlk + row;
-        g_row[0] = gt[kGHi + r];
-        g_row[1] = gt[kGLo + r];
-        g_row[2] = gt[(keys ? kGPost : kGPre) + r];
-        g_row[3] = gt[(keys ? kGTail : kGHead) + r];
-        g_row[4] = gt[kGBeta + r];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            g_col[i][0] = gt[(keys ? kGPre : kGPost) + tid + 256 * i];
-            g_col[i][1] = gt[kGBeta + tid + 256 * i];
-        }
-        const float4 t4 = *reinterpret_cast<const float4*>(gt + kGTot);
-        g_tot[0] = t4.x; g_tot[1] = t4.y; g_tot[2] = t4.z; g_tot[3] = t4.w;
-        g_block[0] = tid < kBlk ? gt[kGHi + rb * kBlk + tid] : 0.f;
-        g_block[1] = tid < kBlk ? gt[kGLo + rb * kBlk + tid] : 0.f;
-    }
-    const RowsPlan& p = ra.p;
-    const int row_n = min(kBlk, rows - rb * kBlk), last = (rows - 1) / kBlk;
-    const int nblk = keys ? last - rb + 1 : rb + 1;       // blocks of columns: rb .. last, or 0 .. rb
     const uint32_t base = smem_u32(sm), bars = base + p.bars;
-    const uint32_t full0 = bars, empty0 = bars + 8 * kMaxRing, rfull = bars + 16 * kMaxRing, inter_done = rfull + 8, acc_ready = rfull + 16,
-                   s_full = rfull + 24, p_full = rfull + 40, x_done = rfull + 56, acc_done = rfull + 72;
+    const uint32_t full0 = bars, empty0 = bars + 8 * kMaxRing, rfull = bars + 16 * kMaxRing, rfree = rfull + 8, inter_done = rfull + 16,
+                   acc_ready = rfull + 24, acc_free = rfull + 32, acc_done = rfull + 40, s_full = rfull + 48, p_full = rfull + 64, x_done = rfull + 80, drain = rfull + 96;
     char* tail = sm + p.bars;
     uint32_t* holder = reinterpret_cast<uint32_t*>(tail + kRowHolder);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
     float* cf = reinterpret_cast<float*>(tail + kRowCf);              // a column's factor, blocks other than rb; in rb: beta
     float* hi = reinterpret_cast<float*>(tail + kRowHi);              // block rb's sums, and what is left of them
     __nv_bfloat16* lo = reinterpret_cast<__nv_bfloat16*>(tail + kRowLo);
-    const int G = p.two ? 2 : 1;
-    const uint32_t cols = p.two ? 512 : 256, scores = dx > 128 ? 256 : 128;
-    const int n_inter = ra.terms * ((da + 63) / 64), nb = (da + 127) / 128;
-    const auto col_block = [&](int j) { return keys ? rb + j : j; };
-    const auto col_rows = [&](int j) { return min(kBlk, rows - col_block(j) * kBlk); };
-    const auto x_stages = [&](int j) { return (col_rows(j) + p.rows_x - 1) / p.rows_x; };
-    // stage number of block j's first X piece: all blocks but the last have whole ones
-    const auto x_first = [&](int j) {
-        const int g = j / G, in = min(G, nblk - g * G), whole = kBlk / p.rows_x;
-        return n_inter + g * G * (nb + whole) + in * nb + (j - g * G) * whole;
-    };
+    const uint32_t scores = dx > 128 ? 256 : 128;
+    const int na = (da + 63) / 64, nb = (da + 127) / 128, nx = (dx + 63) / 64, n_inter = ra.terms * na;
     if (tid == 0) {
-        init_barriers(bars, 2 * kMaxRing + 10, [&](uint32_t b) { return b == acc_ready || (b >= p_full && b < x_done) ? 8u : 1u; });
+        init_barriers(bars, kRowNBars, [&](uint32_t b) { return b == acc_ready || b == acc_free || (b >= p_full && b < x_done) ? 8u : 1u; });
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -499,67 +489,68 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     __syncthreads();
     const uint32_t tmem = warp_uniform(*holder);
     tc_fence_after();
+    RowsItem<MODE> it;
     if (warp == 8) {
         if (elect_one()) {
-            const int hr = MODE == kOut || MODE == kDv ? hk : h, hx = MODE == kOut || MODE == kDv ? h : hk;      // heads of R and B; of X
-            const int na = (da + 63) / 64, nx = (dx + 63) / 64;
             // tokens of a box beyond the sequence's are read and never used, boxes of none are left out
             const auto boxes = [&](uint32_t dst, const CUtensorMap* m, int head, int t0, int n, int x0, int nslab, int from, int upto, uint32_t bar) {
                 for (int x = 0; x < nslab; ++x)
                     for (int y = from; y < upto; ++y)
                         if (64 * y < n) tma_3d(dst + (x * (upto - from) + y - from) * kBox, m, 64 * (x0 + x), head, t0 + 64 * y, bar);
             };
-            const int halves = row_n > 64 ? 2 : 1;
-            mbar_expect_tx(rfull, na * halves * kBox);
-            boxes(base + p.r, &mr, hr, first + rb * kBlk, row_n, 0, na, 0, 2, rfull);
-            int it = 0;
+            Ring ring;
+            int issued = 0, items = 0;
             bool ok = true;
-            const auto stage = [&]() {
-                const int st = it % p.ring;
-                if (ok && it >= p.ring) ok = wait_or_dead(empty0 + 8 * st, (it / p.ring + 1) & 1, a.err, dead);
-                return st;
+            // the next stage, `bytes` of it expected; false once a wait has run out
+            const auto stage = [&](uint32_t bytes) {
+                if (ok && issued >= p.ring) ok = wait_or_dead(empty0 + 8 * ring.st, ring.ph ^ 1, a.err, dead);
+                if (ok) mbar_expect_tx(full0 + 8 * ring.st, bytes);
+                return ok;
+            };
+            const auto done = [&]() {
+                ring.next(p.ring);
+                ++issued;
             };
             const size_t apart = (size_t)slots * sh.H;
-            for (int t = ra.terms - 1; ok && t >= 0; --t)             // the small terms first
-                for (int x = 0; ok && x < na; ++x) {
-                    const int st = stage(), z = (int)(t * apart + (size_t)slot * sh.H + h);
-                    if (!ok) break;
-                    const uint32_t dst = base + st * p.stage, bar = full0 + 8 * st;
-                    if (values) {                         // rows of d_v, 64 of d_k along the row
-                        mbar_expect_tx(bar, dx * 128);
-                        tma_3d(dst, &ms, 64 * x, 0, z, bar);
-                    } else {                              // 64 rows of d_v, d_k along the row
-                        mbar_expect_tx(bar, nx * kBox);
-                        for (int y = 0; y < nx; ++y) tma_3d(dst + y * kBox, &ms, 64 * y, 64 * x, z, bar);
-                    }
-                    ++it;
+            for (int i = blockIdx.x; ok && i < count; i += gridDim.x) {
+                if (!it.get(i, table, sh)) continue;
+                const int hk = it.h / rep, hr = values ? hk : it.h, hx = values ? it.h : hk;      // heads of R and B; of X
+                if (items > 0 && !(ok = wait_or_dead(rfree, (items - 1) & 1, a.err, dead))) break;
+                mbar_expect_tx(rfull, na * (it.row_n > 64 ? 2 : 1) * kBox);
+                boxes(base + p.r, &mr, hr, it.first + it.rb * kBlk, it.row_n, 0, na, 0, 2, rfull);
+                ++items;
+                for (int j0 = 0; ok && j0 < it.nblk; j0 += G) {
+                    const int in = min(G, it.nblk - j0);
+                    for (int j = j0; ok && j < j0 + in; ++j)
+                        for (int x = 0; x < nb; ++x, done()) {
+                            const int sl = min(2, na - 2 * x), n = it.col_rows(j);
+                            if (!stage(sl * (n > 64 ? 2 : 1) * kBox)) break;
+                            boxes(base + ring.st * p.stage, &mb, hr, it.first + it.col_block(j) * kBlk, n, 2 * x, sl, 0, 2, full0 + 8 * ring.st);
+                        }
+                    if (j0 == 0)
+                        for (int t = ra.terms - 1; ok && t >= 0; --t)         // the small terms first
+                            for (int x = 0; x < na; ++x, done()) {
+                                if (!stage(values ? dx * 128 : nx * kBox)) break;
+                                const uint32_t dst = base + ring.st * p.stage, bar = full0 + 8 * ring.st;
+                                const int z = (int)(t * apart + (size_t)it.slot * sh.H + it.h);
+                                if (values)               // rows of d_v, 64 of d_k along the row
+                                    tma_3d(dst, &ms, 64 * x, 0, z, bar);
+                                else                      // 64 rows of d_v, d_k along the row
+                                    for (int y = 0; y < nx; ++y) tma_3d(dst + y * kBox, &ms, 64 * y, 64 * x, z, bar);
+                            }
+                    for (int j = j0; ok && j < j0 + in; ++j)
+                        for (int x = 0; ok && x * p.rows_x < it.col_rows(j); ++x, done()) {
+                            const int n = it.col_rows(j), from = x * p.rows_x / 64, upto = from + p.rows_x / 64;
+                            int live = 0;
+                            for (int y = from; y < upto; ++y) live += 64 * y < n;
+                            if (!stage(nx * live * kBox)) break;
+                            boxes(base + ring.st * p.stage, &mx, hx, it.first + it.col_block(j) * kBlk, n, 0, nx, from, upto, full0 + 8 * ring.st);
+                        }
                 }
-            for (int j0 = 0; ok && j0 < nblk; j0 += G) {
-                const int in = min(G, nblk - j0);
-                for (int j = j0; ok && j < j0 + in; ++j)
-                    for (int x = 0; ok && x < nb; ++x) {
-                        const int st = stage();
-                        if (!ok) break;
-                        const int sl = min(2, na - 2 * x), n = col_rows(j);
-                        mbar_expect_tx(full0 + 8 * st, sl * (n > 64 ? 2 : 1) * kBox);
-                        boxes(base + st * p.stage, &mb, hr, first + col_block(j) * kBlk, n, 2 * x, sl, 0, 2, full0 + 8 * st);
-                        ++it;
-                    }
-                for (int j = j0; ok && j < j0 + in; ++j)
-                    for (int x = 0; ok && x < x_stages(j); ++x) {
-                        const int st = stage();
-                        if (!ok) break;
-                        const int n = col_rows(j), from = x * p.rows_x / 64, upto = from + p.rows_x / 64;
-                        int live = 0;
-                        for (int y = from; y < upto; ++y) live += 64 * y < n;
-                        mbar_expect_tx(full0 + 8 * st, nx * live * kBox);
-                        boxes(base + st * p.stage, &mx, hx, first + col_block(j) * kBlk, n, 0, nx, from, upto, full0 + 8 * st);
-                        ++it;
-                    }
             }
             if (*dead) {                                  // copies in flight end before the CTA does
-                mbar_wait(rfull, 0, a.err);
-                for (int j = max(0, it - p.ring); j < it; ++j) mbar_wait(full0 + 8 * (j % p.ring), (j / p.ring) & 1, a.err);
+                if (items > 0) mbar_wait(rfull, (items - 1) & 1, a.err);
+                for (int j = max(0, issued - p.ring); j < issued; ++j) mbar_wait(full0 + 8 * (j % p.ring), (j / p.ring) & 1, a.err);
             }
         }
         __syncwarp();
@@ -571,255 +562,326 @@ __global__ void __launch_bounds__(kRowThreads, 2)
             __syncwarp();
             tc_fence_after();
         };
-        wait(rfull, 0);
         const uint64_t dR = k_desc<128>(base + p.r);
-        for (int t = 0; t < ra.terms; ++t)
-            for (int x = 0; x < (da + 63) / 64; ++x, ring.next(p.ring)) {
-                wait(full0 + 8 * ring.st, ring.ph);
-                if (leader) {
-                    const uint32_t sb = base + ring.st * p.stage;
-                    const uint64_t dA = dR + (x * 2 * kBox >> 4), dB = values ? k_desc<128>(sb) : mn_desc<128>(sb, kBox);
-                    const uint32_t id = idesc_bf16(128, dx) | (values ? 0u : kBMn);
+        const uint32_t id_x = idesc_bf16(128, dx) | kBMn, id_i = idesc_bf16(128, dx) | (values ? 0u : kBMn);
+        uint32_t items = 0, used[2] = {0, 0};             // scores so far in each buffer
+        for (int i = blockIdx.x; i < count; i += gridDim.x) {
+            if (!it.get(i, table, sh)) continue;
+            it.rows = warp_uniform(it.rows);
+            const int nblk = warp_uniform(it.nblk);
+            wait(rfull, items & 1);
+            for (int j0 = 0; j0 < nblk; j0 += G) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (64 * x + 16 * k < da) mma_bf16(tmem, dA + 2 * k, dB + (values ? 2 * k : 128 * k), id, t + x + k > 0);
-                    mma_commit(empty0 + 8 * ring.st);
-                }
-                __syncwarp();
-            }
-        if (leader) mma_commit(inter_done);
-        __syncwarp();
-        uint32_t use = 0;
-        for (int j0 = 0; j0 < nblk; j0 += G, ++use) {
-            const int in = min(G, nblk - j0);
-            for (int u = 0; u < in; ++u) {
-                const uint32_t D = tmem + scores + 128 * u, id = idesc_bf16(128, (col_rows(j0 + u) + 15) & ~15);
-                if (use > 0) wait(x_done + 8 * u, (use - 1) & 1);     // the scores before are used up
-                for (int x = 0; x < nb; ++x, ring.next(p.ring)) {
-                    wait(full0 + 8 * ring.st, ring.ph);
-                    if (leader) {
-                        const uint64_t dA = dR + (x * 4 * kBox >> 4), dB = k_desc<128>(base + ring.st * p.stage);
+                for (int u = 0; u < G; ++u)
+                    if (j0 + u < nblk) {
+                        const uint32_t D = tmem + scores + 128 * u, id = idesc_bf16(128, (it.col_rows(j0 + u) + 15) & ~15);
+                        if (used[u] > 0) wait(x_done + 8 * u, (used[u] - 1) & 1);     // the scores before are used up
+                        ++used[u];
+                        for (int x = 0; x < nb; ++x, ring.next(p.ring)) {
+                            wait(full0 + 8 * ring.st, ring.ph);
+                            if (leader) {
+                                const uint64_t dA = dR + (x * 4 * kBox >> 4), dB = k_desc<128>(base + ring.st * p.stage);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (128 * x + 16 * k < da)
-                                mma_bf16(D, dA + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), dB + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), id, x + k > 0);
-                        mma_commit(empty0 + 8 * ring.st);
-                    }
-                    __syncwarp();
-                }
-                if (leader) mma_commit(s_full + 8 * u);
-                __syncwarp();
-            }
-            if (j0 == 0) wait(acc_ready, 0);
-            for (int u = 0; u < in; ++u) {
-                const uint32_t A = tmem + scores + 128 * u, id = idesc_bf16(128, dx) | kBMn;
-                wait(p_full + 8 * u, use & 1);
-                for (int left = col_rows(j0 + u), x = 0; left > 0; left -= p.rows_x, x += p.rows_x, ring.next(p.ring)) {
-                    wait(full0 + 8 * ring.st, ring.ph);
-                    if (leader) {
-                        const uint64_t dB = mn_desc<128>(base + ring.st * p.stage, p.rows_x * 128);
-                        const uint32_t A0 = A + x;        // 64 tokens, 32 of their 64 columns
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (16 * k < min(left, p.rows_x)) mma_bf16_ts(tmem, A0 + 64 * (k >> 2) + 8 * (k & 3), dB + 128 * k, id, 1);
-                        mma_commit(empty0 + 8 * ring.st);
-                    }
-                    __syncwarp();
-                }
-                if (leader) mma_commit(x_done + 8 * u);
-                __syncwarp();
-            }
-        }
-        if (leader) {
-            mma_commit(acc_done);                         // and products in flight end before their TMEM is freed
-            mbar_wait(acc_done, 0, a.err);
-        }
-        __syncwarp();
-    } else {
-        const int g = warp >> 2, w4 = warp & 3;
-        const uint32_t lanes = (uint32_t)(32 * w4) << 16;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = tid + 256 * i, b = t / kBlk;
-            float f = keys ? 1.f : g_col[i][1];
-            if (b != rb) f *= g_col[i][0];
-#pragma unroll
-            for (int m = 1; m < 3; ++m)                   // blocks between
-                if (m > min(b, rb) && m < max(b, rb)) f *= g_tot[m];
-            cf[t] = f;
-        }
-        if (tid < kBlk) {
-            hi[tid] = g_block[0];
-            lo[tid] = __float2bfloat16_rn(g_block[1]);
-        }
-        named_sync(2, 256);
-        const float mine = g_row[0], mine_lo = g_row[1], rf = g_row[2], sf = g_row[3];
-        const bool live = row < row_n;
-        const size_t token = (size_t)first + rb * kBlk + row;
-        const int chunks = dx / 16, ch0 = g == 0 ? 0 : (chunks + 1) / 2, ch1 = g == 0 ? (chunks + 1) / 2 : chunks;      // of 16 columns
-        wait_or_dead(inter_done, 0, a.err, dead);
-        __syncwarp();
-        tc_fence_after();
-        {
-            const __nv_bfloat16* z = MODE == kDq ? static_cast<const __nv_bfloat16*>(a.q) + token * sh.ldq + (size_t)hk * sh.dk
-                                                 : static_cast<const __nv_bfloat16*>(a.v) + token * sh.ldv + (size_t)h * sh.dv;
-            float dot = 0.f;
-#pragma unroll 1
-            for (int ch = ch0; ch < ch1; ch += 2) {
-                uint32_t x[2][16];
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (ch + e < ch1) tmem_ld_n(tmem + lanes + 16 * (ch + e), x[e]);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (ch + e < ch1) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x[e][i] = __float_as_uint(sf * __uint_as_float(x[e][i]));
-                        tmem_st_n(tmem + lanes + 16 * (ch + e), x[e]);
-                        if ((MODE == kDq || MODE == kDv) && live) {       // q's or v's columns
-                            float y[8];
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                ld8<__nv_bfloat16>(z + 16 * (ch + e) + 8 * half, y);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) dot = fmaf(__uint_as_float(x[e][8 * half + i]), y[i], dot);
+                                for (int k = 0; k < 8; ++k)
+                                    if (128 * x + 16 * k < da)
+                                        mma_bf16(D, dA + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), dB + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), id, x + k > 0);
+                                mma_commit(empty0 + 8 * ring.st);
                             }
+                            __syncwarp();
                         }
+                        if (leader) mma_commit(s_full + 8 * u);
+                        __syncwarp();
+                    }
+                // the state's product after the first scores: the sum before it is moved out meanwhile
+                if (j0 == 0) {
+                    if (items > 0) wait(acc_free, (items - 1) & 1);
+                    for (int t = 0; t < ra.terms; ++t)
+                        for (int x = 0; x < na; ++x, ring.next(p.ring)) {
+                            wait(full0 + 8 * ring.st, ring.ph);
+                            if (leader) {
+                                const uint32_t sb = base + ring.st * p.stage;
+                                const uint64_t dA = dR + (x * 2 * kBox >> 4), dB = values ? k_desc<128>(sb) : mn_desc<128>(sb, kBox);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (64 * x + 16 * k < da) mma_bf16(tmem, dA + 2 * k, dB + (values ? 2 * k : 128 * k), id_i, t + x + k > 0);
+                                mma_commit(empty0 + 8 * ring.st);
+                            }
+                            __syncwarp();
+                        }
+                    if (leader) mma_commit(inter_done);
+                    __syncwarp();
+                }
+                if (j0 + G >= nblk) {
+                    if (leader) mma_commit(rfree);
+                    __syncwarp();
+                }
+                if (j0 == 0) wait(acc_ready, items & 1);
+#pragma unroll
+                for (int u = 0; u < G; ++u)
+                    if (j0 + u < nblk) {
+                        const uint32_t A = tmem + scores + 128 * u;
+                        wait(p_full + 8 * u, (used[u] - 1) & 1);
+                        for (int left = it.col_rows(j0 + u), x = 0; left > 0; left -= p.rows_x, x += p.rows_x, ring.next(p.ring)) {
+                            wait(full0 + 8 * ring.st, ring.ph);
+                            if (leader) {
+                                const uint64_t dB = mn_desc<128>(base + ring.st * p.stage, p.rows_x * 128);
+                                const uint32_t A0 = A + x;            // 64 tokens, 32 of their 64 columns
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    if (16 * k < min(left, p.rows_x)) mma_bf16_ts(tmem, A0 + 64 * (k >> 2) + 8 * (k & 3), dB + 128 * k, id_x, 1);
+                                mma_commit(empty0 + 8 * ring.st);
+                            }
+                            __syncwarp();
+                        }
+                        if (leader) mma_commit(x_done + 8 * u);
                         __syncwarp();
                     }
             }
-            if ((MODE == kDq || MODE == kDv) && live) ra.part[((size_t)slot * sh.H + h) * ra.part_apart + g * kSeg + rb * kBlk + row] = dot;
-            tmem_wait_st();
-            tc_fence_before();
+            if (leader) mma_commit(acc_done);
             __syncwarp();
-            if (lane == 0) mbar_arrive(acc_ready);
+            ++items;
         }
-        for (int j = 0; j < nblk; ++j) {
-            const int u = j % G, cb = col_block(j), n = col_rows(j);
-            const uint32_t S = tmem + lanes + scores + 128 * u + 64 * g;
-            wait_or_dead(s_full + 8 * u, (j / G) & 1, a.err, dead);
-            __syncwarp();
-            tc_fence_after();
+        if (leader) {                                     // products in flight end before their TMEM is freed
+            mma_commit(drain);
+            mbar_wait(drain, 0, a.err);
+        }
+        __syncwarp();
+    } else {
+        const int g = warp >> 2, w4 = warp & 3, row = 32 * w4 + lane;
+        const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+        const int chunks = dx / 16, ch0 = g == 0 ? 0 : (chunks + 1) / 2, ch1 = g == 0 ? (chunks + 1) / 2 : chunks;      // of 16 columns
+        const bool shared = !values && rep > 1, whole = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+        const uint32_t stg = base + p.out + g * 2 * kBox;             // this half's 64 columns of 128 rows on their way out
+        const int stages_x = kBlk / p.rows_x;
+        uint32_t items = 0, used = 0;                                 // parity of each buffer's scores so far
+        int stages = 0;                                               // before this item
+        // an item's gates: its row's, two columns', the blocks'
+        float g_row[5], g_col[2][2], g_tot[4], g_block[2];
+        const auto load_gates = [&]() {
+            const float* gt = ra.gates + ((size_t)it.slot * sh.H + it.h) * kGAll;
+            const int r = it.rb * kBlk + row;
+            g_row[0] = gt[kGHi + r];
+            g_row[1] = gt[kGLo + r];
+            g_row[2] = gt[(keys ? kGPost : kGPre) + r];
+            g_row[3] = gt[(keys ? kGTail : kGHead) + r];
+            g_row[4] = gt[kGBeta + r];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                g_col[i][0] = gt[(keys ? kGPre : kGPost) + tid + 256 * i];
+                g_col[i][1] = gt[kGBeta + tid + 256 * i];
+            }
+            const float4 t4 = *reinterpret_cast<const float4*>(gt + kGTot);
+            g_tot[0] = t4.x; g_tot[1] = t4.y; g_tot[2] = t4.z; g_tot[3] = t4.w;
+            g_block[0] = tid < kBlk ? gt[kGHi + it.rb * kBlk + tid] : 0.f;
+            g_block[1] = tid < kBlk ? gt[kGLo + it.rb * kBlk + tid] : 0.f;
+        };
+        int i = blockIdx.x;
+        const auto next = [&]() {                                     // the next item that there is, its gates on their way
+            while (i < count && !it.get(i, table, sh)) i += gridDim.x;
+            if (TWO && i < count) load_gates();
+        };
+        next();
+        while (i < count) {
+            const int rb = it.rb, nblk = it.nblk, rows = it.rows, hk = it.h / rep;
+            const bool live = row < it.row_n, staged = TWO && !shared && it.row_n == kBlk;
+            const size_t token = (size_t)it.first + rb * kBlk + row;
+            const int token0 = it.first + rb * kBlk, head = values ? it.h : hk;
+            const size_t at = (size_t)it.slot * sh.H + it.h;
+            if (!TWO) load_gates();                                   // ahead they would take registers that two CTAs do not have
+            named_sync(2, 256);                                       // the last item's factors are used up
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int t = tid + 256 * c, b = t / kBlk;
+                float f = keys ? 1.f : g_col[c][1];
+                if (b != rb) f *= g_col[c][0];
+#pragma unroll
+                for (int m = 1; m < 3; ++m)               // blocks between
+                    if (m > min(b, rb) && m < max(b, rb)) f *= g_tot[m];
+                cf[t] = f;
+            }
+            if (tid < kBlk) {
+                hi[tid] = g_block[0];
+                lo[tid] = __float2bfloat16_rn(g_block[1]);
+            }
+            named_sync(2, 256);
+            const float mine = g_row[0], mine_lo = g_row[1], rf = g_row[2], sf = g_row[3], of = keys ? g_row[4] : 1.f;
+            for (int j = 0; j < nblk; ++j) {
+                const int u = j % G, cb = it.col_block(j), n = it.col_rows(j);
+                const uint32_t S = tmem + lanes + scores + 128 * u + 64 * g;
+                wait_or_dead(s_full + 8 * u, used >> u & 1, a.err, dead);
+                used ^= 1u << u;
+                __syncwarp();
+                tc_fence_after();
 #pragma unroll 1
-            for (int q = 0; q < 2; ++q) {                 // 32 columns
-                const int c0 = 64 * g + 32 * q;
-                uint32_t x[32], y[16];
-                if (c0 >= ((n + 15) & ~15) || (cb == rb && (keys ? c0 + 31 < 32 * w4 : c0 > 32 * w4 + 31))) {
+                for (int q = 0; q < 2; ++q) {             // 32 columns
+                    const int c0 = 64 * g + 32 * q;
+                    uint32_t x[32], y[16];
+                    if (c0 >= ((n + 15) & ~15) || (cb == rb && (keys ? c0 + 31 < 32 * w4 : c0 > 32 * w4 + 31))) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] = 0;            // behind the segment, or masked altogether
-                } else {
-                    tmem_ld_n(S + 32 * q, x);
-                    tmem_wait_ld();
-                    if (cb == rb) {
+                        for (int e = 0; e < 16; ++e) y[e] = 0;        // behind the segment, or masked altogether
+                    } else {
+                        tmem_ld_n(S + 32 * q, x);
+                        tmem_wait_ld();
+                        if (cb == rb) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 h4 = *reinterpret_cast<const float4*>(hi + c0 + i), f4 = *reinterpret_cast<const float4*>(cf + cb * kBlk + c0 + i);
-                            const uint2 l2 = *reinterpret_cast<const uint2*>(lo + c0 + i);
-                            const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, fs[4] = {f4.x, f4.y, f4.z, f4.w},
-                                        ls[4] = {__uint_as_float(l2.x << 16), __uint_as_float(l2.x & 0xffff0000u), __uint_as_float(l2.y << 16),
-                                                 __uint_as_float(l2.y & 0xffff0000u)};
+                            for (int e0 = 0; e0 < 32; e0 += 4) {
+                                const float4 h4 = *reinterpret_cast<const float4*>(hi + c0 + e0), f4 = *reinterpret_cast<const float4*>(cf + cb * kBlk + c0 + e0);
+                                const uint2 l2 = *reinterpret_cast<const uint2*>(lo + c0 + e0);
+                                const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, fs[4] = {f4.x, f4.y, f4.z, f4.w},
+                                            ls[4] = {__uint_as_float(l2.x << 16), __uint_as_float(l2.x & 0xffff0000u), __uint_as_float(l2.y << 16),
+                                                     __uint_as_float(l2.y & 0xffff0000u)};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int col = c0 + i + e;
-                                const float d = (hs[e] - mine) + (ls[e] - mine_lo);
-                                float f = ex2(keys ? d * kLog2e : d * -kLog2e);
-                                if (!keys) f *= fs[e];
-                                x[i + e] = col < n && (keys ? col >= row : col <= row) ? __float_as_uint(f * __uint_as_float(x[i + e])) : 0u;
+                                for (int e = 0; e < 4; ++e) {
+                                    const int col = c0 + e0 + e;
+                                    const float d = (hs[e] - mine) + (ls[e] - mine_lo);
+                                    float f = ex2(keys ? d * kLog2e : d * -kLog2e);
+                                    if (!keys) f *= fs[e];
+                                    x[e0 + e] = col < n && (keys ? col >= row : col <= row) ? __float_as_uint(f * __uint_as_float(x[e0 + e])) : 0u;
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 f = *reinterpret_cast<const float4*>(cf + cb * kBlk + c0 + e);
+                                const float2 r2 = make_float2(rf, rf);
+                                const float2 y0 = fmul2(fmul2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), r2), make_float2(f.x, f.y)),
+                                             y1 = fmul2(fmul2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), r2), make_float2(f.z, f.w));
+                                x[e] = __float_as_uint(y0.x);
+                                x[e + 1] = __float_as_uint(y0.y);
+                                x[e + 2] = __float_as_uint(y1.x);
+                                x[e + 3] = __float_as_uint(y1.y);
+                            }
+                            if (n < kBlk) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (c0 + e >= n) x[e] = 0u;
                             }
                         }
-                    } else {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(cf + cb * kBlk + c0 + i);
-                            const float2 r2 = make_float2(rf, rf);
-                            const float2 u = fmul2(fmul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), r2), make_float2(f.x, f.y)),
-                                         v = fmul2(fmul2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), r2), make_float2(f.z, f.w));
-                            x[i] = __float_as_uint(u.x);
-                            x[i + 1] = __float_as_uint(u.y);
-                            x[i + 2] = __float_as_uint(v.x);
-                            x[i + 3] = __float_as_uint(v.y);
-                        }
-                        if (n < kBlk) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c0 + i >= n) x[i] = 0u;
-                        }
+                        for (int e = 0; e < 16; ++e) y[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] = pack_bf16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                    tmem_st_n(S + 16 * q, y);             // over columns that are read
                 }
-                tmem_st_n(S + 16 * q, y);                 // over columns that are read
+                tmem_wait_st();
+                if (j + 1 == min(G, nblk)) {              // the state's product: its rows scaled
+                    wait_or_dead(inter_done, items & 1, a.err, dead);
+                    __syncwarp();
+                    tc_fence_after();
+                    const __nv_bfloat16* z = MODE == kDq ? static_cast<const __nv_bfloat16*>(a.q) + token * sh.ldq + (size_t)hk * sh.dk
+                                                         : static_cast<const __nv_bfloat16*>(a.v) + token * sh.ldv + (size_t)it.h * sh.dv;
+                    float dot = 0.f;
+#pragma unroll 1
+                    for (int ch = ch0; ch < ch1; ch += 2) {
+                        uint32_t x[2][16];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (ch + e < ch1) tmem_ld_n(tmem + lanes + 16 * (ch + e), x[e]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (ch + e < ch1) {
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) x[e][c] = __float_as_uint(sf * __uint_as_float(x[e][c]));
+                                tmem_st_n(tmem + lanes + 16 * (ch + e), x[e]);
+                                if ((MODE == kDq || MODE == kDv) && live) {       // q's or v's columns
+                                    float y[8];
+#pragma unroll
+                                    for (int half = 0; half < 2; ++half) {
+                                        ld8<__nv_bfloat16>(z + 16 * (ch + e) + 8 * half, y);
+#pragma unroll
+                                        for (int c = 0; c < 8; ++c) dot = fmaf(__uint_as_float(x[e][8 * half + c]), y[c], dot);
+                                    }
+                                }
+                                __syncwarp();
+                            }
+                    }
+                    if ((MODE == kDq || MODE == kDv) && live) ra.part[at * ra.part_apart + g * kSeg + rb * kBlk + row] = dot;
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acc_ready);
+                }
+                if (n % 16 != 0) {                        // X's tokens of what lies behind: rows of zero, up to whole products.  Not before the
+                                                          // products have used what was in their stage (the state's have, or the scores of this group)
+                    // whole blocks before it; the state's stages behind the first scores
+                    const int j0 = j - u, stage = stages + n_inter + j0 * (nb + stages_x) + min(G, nblk - j0) * nb + u * stages_x + (n - 1) / p.rows_x;
+                    const int at_row = n % p.rows_x, cnt = 16 - n % 16, pieces = nx * 8;
+                    wait_or_dead(full0 + 8 * (stage % p.ring), (stage / p.ring) & 1, a.err, dead);
+                    for (int e = tid; e < cnt * pieces; e += 256)
+                        st_shared16(base + stage % p.ring * p.stage + (e % pieces >> 3) * p.rows_x * 128 + (at_row + e / pieces) * 128 + (e & 7) * 16, 0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * u);
             }
-            tmem_wait_st();
-            if (n % 16 != 0) {                            // X's tokens of what lies behind: rows of zero, up to whole products
-                const int stage = x_first(j) + (n - 1) / p.rows_x, at = n % p.rows_x, cnt = 16 - n % 16, pieces = (dx + 63) / 64 * 8;
-                wait_or_dead(full0 + 8 * (stage % p.ring), (stage / p.ring) & 1, a.err, dead);
-                for (int i = tid; i < cnt * pieces; i += 256)
-                    st_shared16(base + stage % p.ring * p.stage + (i % pieces >> 3) * p.rows_x * 128 + (at + i / pieces) * 128 + (i & 7) * 16, 0, 0, 0, 0);
-                fence_proxy_async_smem();
+            stages += n_inter + nblk * nb + (nblk - 1) * stages_x + (it.col_rows(nblk - 1) + p.rows_x - 1) / p.rows_x;
+            i += gridDim.x;
+            next();
+            wait_or_dead(acc_done, items & 1, a.err, dead);
+            __syncwarp();
+            tc_fence_after();
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + token * out_heads * dx + (size_t)head * dx;
+            float* o32 = shared ? ra.heads + (token * sh.H + at % sh.H) * dx : nullptr;
+            for (int x = g; x < nx; x += 2) {             // 64 columns
+                const int n16 = min(4, (dx - 64 * x) / 16);
+                if (staged) {                             // what was there has left
+                    if ((tid & 127) == 0) bulk_read_done();
+                    named_sync(3 + g, 128);
+                }
+#pragma unroll
+                for (int e0 = 0; e0 < 4; e0 += 2) {
+                    uint32_t v[2][16];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (e0 + e < n16) tmem_ld_n(tmem + lanes + 64 * x + 16 * (e0 + e), v[e]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (e0 + e < n16 && live) {
+                            const int col = 64 * x + 16 * (e0 + e);
+                            float y[16];
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) y[c] = of * __uint_as_float(v[e][c]);
+                            if (shared) {
+                                uint4 w[4];
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    w[c] = make_uint4(__float_as_uint(y[4 * c]), __float_as_uint(y[4 * c + 1]), __float_as_uint(y[4 * c + 2]), __float_as_uint(y[4 * c + 3]));
+                                stg_pieces<4>(o32 + col, w, false, true);
+                            } else {
+                                uint4 w[2];
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    w[c] = make_uint4(pack_bf16(y[8 * c], y[8 * c + 1]), pack_bf16(y[8 * c + 2], y[8 * c + 3]),
+                                                      pack_bf16(y[8 * c + 4], y[8 * c + 5]), pack_bf16(y[8 * c + 6], y[8 * c + 7]));
+                                if (staged) {
+#pragma unroll
+                                    for (int c = 0; c < 2; ++c) st_shared16(stg + row * 128 + (((2 * (e0 + e) + c) ^ (row & 7)) << 4), w[c].x, w[c].y, w[c].z, w[c].w);
+                                } else {
+                                    stg_pieces<2>(o + col, w, false, whole);
+                                }
+                            }
+                        }
+                    __syncwarp();
+                }
+                if (staged) {
+                    fence_proxy_async_smem();
+                    named_sync(3 + g, 128);
+                    if ((tid & 127) == 0) {
+                        for (int y = 0; y < 2; ++y) tma_store_3d(&mo, stg + y * kBox, 64 * x, head, token0 + 64 * y, false);
+                        bulk_commit();
+                    }
+                    __syncwarp();
+                }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full + 8 * u);
+            if (lane == 0) mbar_arrive(acc_free);
+            ++items;
         }
-        wait_or_dead(acc_done, 0, a.err, dead);
+        if ((tid & 127) == 0) bulk_all_done();
         __syncwarp();
-        tc_fence_after();
-        const float of = keys ? g_row[4] : 1.f;
-        const bool shared = !values && rep > 1, staged = !shared && row_n == kBlk;
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + token * out_heads * dx + (size_t)(values ? h : hk) * dx;
-        float* of32 = shared ? ra.heads + (token * sh.H + h) * dx : nullptr;
-        const bool whole = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
-#pragma unroll 1
-        for (int ch = ch0; ch < ch1; ch += 2) {
-            uint32_t x[2][16];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (ch + e < ch1) tmem_ld_n(tmem + lanes + 16 * (ch + e), x[e]);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (ch + e < ch1 && live) {
-                    const int col = 16 * (ch + e);
-                    float y[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] = of * __uint_as_float(x[e][i]);
-                    if (shared) {
-                        const uint4* v = reinterpret_cast<const uint4*>(y);
-                        const uint4 w[4] = {v[0], v[1], v[2], v[3]};
-                        stg_pieces<4>(of32 + col, w, false, true);
-                    } else {
-                        uint4 v[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            v[i] = make_uint4(pack_bf16(y[8 * i], y[8 * i + 1]), pack_bf16(y[8 * i + 2], y[8 * i + 3]), pack_bf16(y[8 * i + 4], y[8 * i + 5]),
-                                              pack_bf16(y[8 * i + 6], y[8 * i + 7]));
-                        if (staged) {                     // the ring, which nothing reads any more, as boxes of 64 columns
-                            const uint32_t to = base + (col >> 6) * 2 * kBox + row * 128;
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) st_shared16(to + ((((col >> 3 & 7) + i) ^ (row & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
-                        } else {
-                            stg_pieces<2>(o + col, v, false, whole);
-                        }
-                    }
-                }
-            __syncwarp();
-        }
-        if (staged) {
-            fence_proxy_async_smem();
-            named_sync(2, 256);
-            if (warp == 0) {
-                if (lane == 0) {
-                    for (int x = 0; x < (dx + 63) / 64; ++x)
-                        for (int y = 0; y < 2; ++y)
-                            tma_store_3d(&mo, base + (2 * x + y) * kBox, 64 * x, values ? h : hk, first + rb * kBlk + 64 * y, false);
-                    bulk_commit();
-                    bulk_all_done();
-                }
-                __syncwarp();
-            }
-        }
     }
     tc_fence_before();
     __syncthreads();
@@ -1207,31 +1269,34 @@ RowsPlan rows_plan(int da, int dx) {
     p.rows_x = dx > 128 ? 64 : 128;
     p.stage = 2 * kBox * (na > 1 || nx > 1 ? 2 : 1);
     const uint32_t r = na * 2 * kBox;
-    // three stages are what a block's scores and their product take
-    p.two = dx > 128 || r + 3 * p.stage + kRowTail > kSmemHalf;
-    const uint32_t room = (p.two ? kSmemMost : kSmemHalf) - r - kRowTail;
+    // two CTAs an SM where TMEM holds both's sums and shared memory two stages each
+    p.two = dx > 128 || r + 2 * p.stage + kRowTail > kSmemHalf;
+    const uint32_t out = p.two ? 4 * kBox : 0, room = (p.two ? kSmemMost : kSmemHalf) - r - out - kRowTail;
     p.ring = (int)(room / p.stage) < kMaxRing ? (int)(room / p.stage) : kMaxRing;
     p.r = p.ring * p.stage;            // behind the ring
-    p.bars = p.r + r;
+    p.out = p.r + r;
+    p.bars = p.out + out;
     p.smem = p.bars + kRowTail;
     return p;
 }
 
 template <int MODE>
 cudaError_t rows_go(const Maps& m, const CUtensorMap& ms, const SeqArgs& a, const float* gates, float* part, float* heads, int terms, cudaStream_t st) {
-    static bool done[64];
+    static bool done[2][64];
     const SeqShape& sh = a.sh;
     constexpr bool values = MODE == kOut || MODE == kDv;
     const RowsArgs ra = {rows_plan(values ? sh.dk : sh.dv, values ? sh.dv : sh.dk), part, (size_t)kPartAll, heads, gates, terms};
-    const cudaError_t e = ensure_smem(lin_rows_tc_kernel<MODE>, kSmemMost, done);
+    const auto kernel = ra.p.two ? lin_rows_tc_kernel<MODE, true> : lin_rows_tc_kernel<MODE, false>;
+    const cudaError_t e = ensure_smem(kernel, kSmemMost, done[ra.p.two]);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * (kSeg / kBlk)));
+    const size_t items = (size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * (kSeg / kBlk), most = (ra.p.two ? 1 : 2) * kSMs;      // both fours
+    const dim3 grid((unsigned)(items < most ? items : most));
     const CUtensorMap &mr = MODE == kOut ? m.q : MODE == kDq ? m.o : MODE == kDk ? m.v : m.k, &mb = MODE == kOut ? m.k : MODE == kDq ? m.v : MODE == kDk ? m.o : m.q,
                       &mx = MODE == kOut ? m.v : MODE == kDq ? m.k : MODE == kDk ? m.q : m.o;
     const int d = values ? sh.dv : sh.dk, out_heads = values ? sh.H : sh.Hk;
     CUtensorMap mo;
     if (!token_map(&mo, MODE == kOut ? a.out : MODE == kDq ? a.dq : MODE == kDk ? a.dk : a.dv, sh, d, out_heads, (long long)out_heads * d)) return cudaErrorInvalidValue;
-    return launch_kernel(lin_rows_tc_kernel<MODE>, grid, dim3(kRowThreads), ra.p.smem, st, false, mr, mb, mx, ms, mo, a, ra);
+    return launch_kernel(kernel, grid, dim3(kRowThreads), ra.p.smem, st, false, mr, mb, mx, ms, mo, a, ra);
 }
 
 cudaError_t prep_go(const SeqArgs& a, float* gates, cudaStream_t st) {
