@@ -166,6 +166,12 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
                      "r"(c0), "r"(c1), "r"(c2)
                      : "memory");
 }
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;\n" ::: "memory"); }
 
 struct LocalItems {            // tile i of the launch; empty slots have none
@@ -399,16 +405,16 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
 // fp32 gradients need, are taken from those fp32 sums.  kOut and kDk read one term, and all round the scores once: each
 // term of a bf16 output is off by one rounding of half a step, beside the output's own.
 //
-// A CTA takes block after block of rows, and the copies and scores of the next run while the last leaves: warps 0-7
-// work (four a half of the columns), warp 8 copies, warp 9 multiplies.  TWO: one CTA an SM, two blocks' scores in flight
-// and the rows out by way of shared memory; else two CTAs, where theirs fit an SM.
+// A CTA an SM takes block after block of rows; the scores of a block of columns, be it the next rows' first, are formed
+// before the product of the one before it, so that the workers' pass over scores runs beside products.  Warps 0-7 work
+// (four a half of the columns), 8-11 move finished sums out (by way of shared memory where all rows are there), 12
+// copies, 13 multiplies.
 // ---------------------------------------------------------------------------
 enum { kOut, kDq, kDk, kDv };
-constexpr int kRowThreads = 320, kMaxRing = 8;
+constexpr int kRowThreads = 448, kMaxRing = 8;
 
 struct RowsPlan {              // shared memory of a launch
-    int ring, rows_x;          // stages; tokens of a stage of X
-    bool two;                  // two blocks' scores in flight
+    int ring, rows_x, nr;      // stages; tokens of a stage of X; buffers of row operands
     uint32_t stage, r, out, bars, smem;
 };
 
@@ -421,11 +427,16 @@ struct RowsArgs {
     int terms;
 };
 
-// offsets behind the barriers
-constexpr int kRowNBars = 2 * kMaxRing + 13;
-constexpr uint32_t kRowHolder = kRowNBars * 8, kRowCf = (kRowHolder + 8 + 15) / 16 * 16, kRowHi = kRowCf + kSeg * 4, kRowLo = kRowHi + kBlk * 4,
-                   kRowTail = kRowLo + kBlk * 2;
-static_assert(kRowCf % 16 == 0, "read by 16 bytes");
+// What the workers keep of an item's gates, twice: factors of the columns of blocks other than rb; in block rb, by quarters
+// of 32 rows, factors of its columns for the quarter's rows (both with beta where rows are queries); its sums as two floats.
+struct RowGates {
+    float cf[kSeg], quarter[4][kBlk], beta[kBlk], hi[kBlk];
+    __nv_bfloat16 lo[kBlk];
+};
+// behind the barriers
+constexpr int kRowNBars = 2 * kMaxRing + 17;
+constexpr uint32_t kRowHolder = kRowNBars * 8, kRowGates = (kRowHolder + 8 + 15) / 16 * 16, kRowTail = kRowGates + 2 * sizeof(RowGates);
+static_assert(sizeof(RowGates) % 16 == 0, "read by 16 bytes");
 
 template <int MODE>
 struct RowsItem {
@@ -445,17 +456,23 @@ struct RowsItem {
         nblk = keys ? (rows - 1) / kBlk - rb + 1 : rb + 1;       // blocks of columns: rb .. last, or 0 .. rb
         return rb * kBlk < rows;
     }
+    // The first there is from i on; i becomes its number, `count` where there is none.
+    __device__ __forceinline__ bool seek(int& i, int count, const int2* table, const SeqShape& sh) {
+        for (; i < count; i += gridDim.x)
+            if (get(i, table, sh)) return true;
+        i = count;
+        return false;
+    }
     __device__ __forceinline__ int col_block(int j) const { return MODE == kDk || MODE == kDv ? rb + j : j; }
     __device__ __forceinline__ int col_rows(int j) const { return min(kBlk, rows - col_block(j) * kBlk); }
 };
 
-template <int MODE, bool TWO>
-__global__ void __launch_bounds__(kRowThreads, TWO ? 1 : 2)
+template <int MODE>
+__global__ void __launch_bounds__(kRowThreads, 1)
     lin_rows_tc_kernel(const __grid_constant__ CUtensorMap mr, const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mx,
                        const __grid_constant__ CUtensorMap ms, const __grid_constant__ CUtensorMap mo, SeqArgs a, RowsArgs ra) {
     constexpr bool keys = MODE == kDk || MODE == kDv, values = MODE == kOut || MODE == kDv;     // rows are keys; columns d_v
-    constexpr int G = TWO ? 2 : 1;
-    constexpr uint32_t cols = TWO ? 512 : 256;
+    constexpr uint32_t scores = 256;                      // TMEM: one sum of 256 columns or two of 128, then two blocks' scores
     extern __shared__ __align__(1024) char sm[];
     const SeqShape& sh = a.sh;
     const RowsPlan& p = ra.p;
@@ -470,36 +487,36 @@ __global__ void __launch_bounds__(kRowThreads, TWO ? 1 : 2)
         if (seq_outside(sh, ob, oe)) zero_rows<__nv_bfloat16>(out, (size_t)out_heads * dx, ob, oe, sh.total);
     }
     const uint32_t base = smem_u32(sm), bars = base + p.bars;
-    const uint32_t full0 = bars, empty0 = bars + 8 * kMaxRing, rfull = bars + 16 * kMaxRing, rfree = rfull + 8, inter_done = rfull + 16,
-                   acc_ready = rfull + 24, acc_free = rfull + 32, acc_done = rfull + 40, s_full = rfull + 48, p_full = rfull + 64, x_done = rfull + 80, drain = rfull + 96;
+    const uint32_t full0 = bars, empty0 = bars + 8 * kMaxRing, rfull = bars + 16 * kMaxRing, rfree = rfull + 16, acc_free = rfull + 32, acc_done = rfull + 48,
+                   s_full = rfull + 64, p_full = rfull + 80, x_done = rfull + 96, inter_done = rfull + 112, acc_ready = rfull + 120, drain = rfull + 128;
     char* tail = sm + p.bars;
     uint32_t* holder = reinterpret_cast<uint32_t*>(tail + kRowHolder);
     volatile int* dead = reinterpret_cast<volatile int*>(holder + 1);
-    float* cf = reinterpret_cast<float*>(tail + kRowCf);              // a column's factor, blocks other than rb; in rb: beta
-    float* hi = reinterpret_cast<float*>(tail + kRowHi);              // block rb's sums, and what is left of them
-    __nv_bfloat16* lo = reinterpret_cast<__nv_bfloat16*>(tail + kRowLo);
-    const uint32_t scores = dx > 128 ? 256 : 128;
     const int na = (da + 63) / 64, nb = (da + 127) / 128, nx = (dx + 63) / 64, n_inter = ra.terms * na;
+    const int two_sums = dx <= 128;                       // sums in TMEM, less one; the second 128 columns on
+    const uint32_t r_bytes = na * 2 * kBox;
     if (tid == 0) {
-        init_barriers(bars, kRowNBars, [&](uint32_t b) { return b == acc_ready || b == acc_free || (b >= p_full && b < x_done) ? 8u : 1u; });
+        init_barriers(bars, kRowNBars, [&](uint32_t b) { return (b >= p_full && b < x_done) || b == acc_ready ? 8u : b >= acc_free && b < acc_done ? 4u : 1u; });
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    if (warp == 9) tmem_alloc(smem_u32(holder), cols);
+    if (warp == 13) tmem_alloc(smem_u32(holder), 512);
     __syncthreads();
     const uint32_t tmem = warp_uniform(*holder);
     tc_fence_after();
-    RowsItem<MODE> it;
-    if (warp == 8) {
+    RowsItem<MODE> it = {};
+    int i = blockIdx.x;
+    if (warp == 12) {
         if (elect_one()) {
-            // tokens of a box beyond the sequence's are read and never used, boxes of none are left out
-            const auto boxes = [&](uint32_t dst, const CUtensorMap* m, int head, int t0, int n, int x0, int nslab, int from, int upto, uint32_t bar) {
-                for (int x = 0; x < nslab; ++x)
-                    for (int y = from; y < upto; ++y)
-                        if (64 * y < n) tma_3d(dst + (x * (upto - from) + y - from) * kBox, m, 64 * (x0 + x), head, t0 + 64 * y, bar);
+            // `rows` tokens of slabs x0, x0 + 1, .. (64 columns each): those beyond the sequence's are read and never used
+            const auto load = [&](uint32_t dst, const CUtensorMap* m, bool whole, int head, int t0, int x0, int nslab, int rows, uint32_t bar) {
+                if (whole) tma_4d(dst, m, 0, head, t0, x0, bar);
+                else
+                    for (int x = 0; x < nslab; ++x) tma_4d(dst + x * rows * 128, m, 64 * (x0 + x), head, t0, 0, bar);
             };
-            Ring ring;
-            int issued = 0, items = 0;
+            const bool whole_a = da % 64 == 0, whole_x = dx % 64 == 0;
+            Ring ring, rr;
+            int issued = 0, r_issued = 0;
             bool ok = true;
             // the next stage, `bytes` of it expected; false once a wait has run out
             const auto stage = [&](uint32_t bytes) {
@@ -507,103 +524,142 @@ __global__ void __launch_bounds__(kRowThreads, TWO ? 1 : 2)
                 if (ok) mbar_expect_tx(full0 + 8 * ring.st, bytes);
                 return ok;
             };
-            const auto done = [&]() {
+            const auto next_stage = [&]() {
                 ring.next(p.ring);
                 ++issued;
             };
+            // block j's score operand, behind the rows' own where it is their first
+            const auto score_operand = [&](int j) {
+                const int hr = values ? it.h / rep : it.h;
+                if (j == 0) {
+                    if (r_issued >= p.nr && !(ok = ok && wait_or_dead(rfree + 8 * rr.st, rr.ph ^ 1, a.err, dead))) return;
+                    mbar_expect_tx(rfull + 8 * rr.st, r_bytes);
+                    load(base + p.r + rr.st * r_bytes, &mr, whole_a, hr, it.first + it.rb * kBlk, 0, na, kBlk, rfull + 8 * rr.st);
+                    rr.next(p.nr);
+                    ++r_issued;
+                }
+                for (int x = 0; x < nb; ++x, next_stage()) {
+                    const int sl = whole_a ? min(2, na) : min(2, na - 2 * x);         // of a whole box those behind the last come as zeros
+                    if (!stage(sl * 2 * kBox)) return;
+                    load(base + ring.st * p.stage, &mb, whole_a, hr, it.first + it.col_block(j) * kBlk, 2 * x, sl, kBlk, full0 + 8 * ring.st);
+                }
+            };
             const size_t apart = (size_t)slots * sh.H;
-            for (int i = blockIdx.x; ok && i < count; i += gridDim.x) {
-                if (!it.get(i, table, sh)) continue;
-                const int hk = it.h / rep, hr = values ? hk : it.h, hx = values ? it.h : hk;      // heads of R and B; of X
-                if (items > 0 && !(ok = wait_or_dead(rfree, (items - 1) & 1, a.err, dead))) break;
-                mbar_expect_tx(rfull, na * (it.row_n > 64 ? 2 : 1) * kBox);
-                boxes(base + p.r, &mr, hr, it.first + it.rb * kBlk, it.row_n, 0, na, 0, 2, rfull);
-                ++items;
-                for (int j0 = 0; ok && j0 < it.nblk; j0 += G) {
-                    const int in = min(G, it.nblk - j0);
-                    for (int j = j0; ok && j < j0 + in; ++j)
-                        for (int x = 0; x < nb; ++x, done()) {
-                            const int sl = min(2, na - 2 * x), n = it.col_rows(j);
-                            if (!stage(sl * (n > 64 ? 2 : 1) * kBox)) break;
-                            boxes(base + ring.st * p.stage, &mb, hr, it.first + it.col_block(j) * kBlk, n, 2 * x, sl, 0, 2, full0 + 8 * ring.st);
-                        }
-                    if (j0 == 0)
+            bool more = it.seek(i, count, table, sh);
+            if (more) score_operand(0);
+            while (ok && more) {
+                const RowsItem<MODE> cur = it;
+                const auto next_item = [&]() {
+                    i += gridDim.x;
+                    more = it.seek(i, count, table, sh);
+                    if (more) score_operand(0);
+                };
+                // the order that the products take them in
+                for (int j = 0; ok && j < cur.nblk; ++j) {
+                    if (j == 0)
                         for (int t = ra.terms - 1; ok && t >= 0; --t)         // the small terms first
-                            for (int x = 0; x < na; ++x, done()) {
+                            for (int x = 0; x < na; ++x, next_stage()) {
                                 if (!stage(values ? dx * 128 : nx * kBox)) break;
                                 const uint32_t dst = base + ring.st * p.stage, bar = full0 + 8 * ring.st;
-                                const int z = (int)(t * apart + (size_t)it.slot * sh.H + it.h);
+                                const int z = (int)(t * apart + (size_t)cur.slot * sh.H + cur.h);
                                 if (values)               // rows of d_v, 64 of d_k along the row
                                     tma_3d(dst, &ms, 64 * x, 0, z, bar);
                                 else                      // 64 rows of d_v, d_k along the row
                                     for (int y = 0; y < nx; ++y) tma_3d(dst + y * kBox, &ms, 64 * y, 64 * x, z, bar);
                             }
-                    for (int j = j0; ok && j < j0 + in; ++j)
-                        for (int x = 0; ok && x * p.rows_x < it.col_rows(j); ++x, done()) {
-                            const int n = it.col_rows(j), from = x * p.rows_x / 64, upto = from + p.rows_x / 64;
-                            int live = 0;
-                            for (int y = from; y < upto; ++y) live += 64 * y < n;
-                            if (!stage(nx * live * kBox)) break;
-                            boxes(base + ring.st * p.stage, &mx, hx, it.first + it.col_block(j) * kBlk, n, 0, nx, from, upto, full0 + 8 * ring.st);
-                        }
+                    if (j + 1 < cur.nblk) score_operand(j + 1);
+                    else if (p.nr > 1) next_item();
+                    const int n = cur.col_rows(j);
+                    for (int x = 0; ok && x * p.rows_x < n; ++x, next_stage()) {
+                        if (!stage(nx * p.rows_x * 128)) break;
+                        load(base + ring.st * p.stage, &mx, whole_x, values ? cur.h : cur.h / rep, cur.first + cur.col_block(j) * kBlk + x * p.rows_x, 0, nx, p.rows_x,
+                             full0 + 8 * ring.st);
+                    }
+                    if (ok && j + 1 == cur.nblk && p.nr == 1) next_item();
                 }
             }
             if (*dead) {                                  // copies in flight end before the CTA does
-                if (items > 0) mbar_wait(rfull, (items - 1) & 1, a.err);
+                for (int j = max(0, r_issued - p.nr); j < r_issued; ++j) mbar_wait(rfull + 8 * (j % p.nr), (j / p.nr) & 1, a.err);
                 for (int j = max(0, issued - p.ring); j < issued; ++j) mbar_wait(full0 + 8 * (j % p.ring), (j / p.ring) & 1, a.err);
             }
         }
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == 13) {
         const bool leader = elect_one();
-        Ring ring;
+        Ring ring, rr;
         const auto wait = [&](uint32_t bar, uint32_t parity) {
             wait_or_dead(bar, parity, a.err, dead);
             __syncwarp();
             tc_fence_after();
         };
-        const uint64_t dR = k_desc<128>(base + p.r);
         const uint32_t id_x = idesc_bf16(128, dx) | kBMn, id_i = idesc_bf16(128, dx) | (values ? 0u : kBMn);
-        uint32_t items = 0, used[2] = {0, 0};             // scores so far in each buffer
-        for (int i = blockIdx.x; i < count; i += gridDim.x) {
-            if (!it.get(i, table, sh)) continue;
-            it.rows = warp_uniform(it.rows);
-            const int nblk = warp_uniform(it.nblk);
-            wait(rfull, items & 1);
-            for (int j0 = 0; j0 < nblk; j0 += G) {
+        uint32_t items = 0, blocks = 0;                   // sums and blocks of scores so far
+        // scores of block j, the blocks'-th, of `it`
+        const auto score = [&](int j, uint32_t n) {
+            const uint32_t u = n & 1, D = tmem + scores + 128 * u, id = idesc_bf16(128, (it.col_rows(j) + 15) & ~15);
+            if (j == 0) wait(rfull + 8 * rr.st, rr.ph);
+            if (n > 1) wait(x_done + 8 * u, (n >> 1 & 1) ^ 1);        // the scores before are used up
+            const uint64_t dR = k_desc<128>(base + p.r + rr.st * r_bytes);
+            for (int x = 0; x < nb; ++x, ring.next(p.ring)) {
+                wait(full0 + 8 * ring.st, ring.ph);
+                if (leader) {
+                    const uint64_t dA = dR + (x * 4 * kBox >> 4), dB = k_desc<128>(base + ring.st * p.stage);
+                    if (da - 128 * x >= 128) {
 #pragma unroll
-                for (int u = 0; u < G; ++u)
-                    if (j0 + u < nblk) {
-                        const uint32_t D = tmem + scores + 128 * u, id = idesc_bf16(128, (it.col_rows(j0 + u) + 15) & ~15);
-                        if (used[u] > 0) wait(x_done + 8 * u, (used[u] - 1) & 1);     // the scores before are used up
-                        ++used[u];
-                        for (int x = 0; x < nb; ++x, ring.next(p.ring)) {
-                            wait(full0 + 8 * ring.st, ring.ph);
-                            if (leader) {
-                                const uint64_t dA = dR + (x * 4 * kBox >> 4), dB = k_desc<128>(base + ring.st * p.stage);
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    if (128 * x + 16 * k < da)
-                                        mma_bf16(D, dA + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), dB + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), id, x + k > 0);
-                                mma_commit(empty0 + 8 * ring.st);
-                            }
-                            __syncwarp();
-                        }
-                        if (leader) mma_commit(s_full + 8 * u);
-                        __syncwarp();
+                        for (int k = 0; k < 8; ++k)
+                            mma_bf16(D, dA + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), dB + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), id, x + k > 0);
+                    } else {
+                        for (int k = 0; 128 * x + 16 * k < da; ++k)
+                            mma_bf16(D, dA + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), dB + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), id, x + k > 0);
                     }
-                // the state's product after the first scores: the sum before it is moved out meanwhile
-                if (j0 == 0) {
-                    if (items > 0) wait(acc_free, (items - 1) & 1);
+                    mma_commit(empty0 + 8 * ring.st);
+                }
+                __syncwarp();
+            }
+            if (leader) mma_commit(s_full + 8 * u);
+            __syncwarp();
+        };
+        const auto uniform = [&]() {
+            it.rows = warp_uniform(it.rows);
+            it.nblk = warp_uniform(it.nblk);
+        };
+        bool more = it.seek(i, count, table, sh);
+        if (more) {
+            uniform();
+            score(0, 0);
+        }
+        while (more) {
+            const RowsItem<MODE> cur = it;
+            const uint32_t acc = tmem + (two_sums ? 128 * (items & 1) : 0), ab = two_sums ? items & 1 : 0, ap = two_sums ? items >> 1 & 1 : items & 1;
+            for (int j = 0; j < cur.nblk; ++j, ++blocks) {
+                // the next rows' first scores: their operand has this item's place once all scores and the state's product
+                // have read it, or one of its own
+                const auto next_item = [&]() {
+                    if (leader) mma_commit(rfree + 8 * rr.st);
+                    __syncwarp();
+                    rr.next(p.nr);
+                    i += gridDim.x;
+                    more = it.seek(i, count, table, sh);
+                    if (more) {
+                        uniform();
+                        score(0, blocks + 1);
+                    }
+                };
+                if (j == 0) {
+                    if (items > (uint32_t)two_sums) wait(acc_free + 8 * ab, ap ^ 1);
+                    const uint64_t dR = k_desc<128>(base + p.r + rr.st * r_bytes);
                     for (int t = 0; t < ra.terms; ++t)
                         for (int x = 0; x < na; ++x, ring.next(p.ring)) {
                             wait(full0 + 8 * ring.st, ring.ph);
                             if (leader) {
                                 const uint32_t sb = base + ring.st * p.stage;
                                 const uint64_t dA = dR + (x * 2 * kBox >> 4), dB = values ? k_desc<128>(sb) : mn_desc<128>(sb, kBox);
+                                if (da - 64 * x >= 64) {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    if (64 * x + 16 * k < da) mma_bf16(tmem, dA + 2 * k, dB + (values ? 2 * k : 128 * k), id_i, t + x + k > 0);
+                                    for (int k = 0; k < 4; ++k) mma_bf16(acc, dA + 2 * k, dB + (values ? 2 * k : 128 * k), id_i, t + x + k > 0);
+                                } else {
+                                    for (int k = 0; 64 * x + 16 * k < da; ++k) mma_bf16(acc, dA + 2 * k, dB + (values ? 2 * k : 128 * k), id_i, t + x + k > 0);
+                                }
                                 mma_commit(empty0 + 8 * ring.st);
                             }
                             __syncwarp();
@@ -611,34 +667,37 @@ __global__ void __launch_bounds__(kRowThreads, TWO ? 1 : 2)
                     if (leader) mma_commit(inter_done);
                     __syncwarp();
                 }
-                if (j0 + G >= nblk) {
-                    if (leader) mma_commit(rfree);
+                // the next block's scores before this one's product
+                if (j + 1 < cur.nblk) score(j + 1, blocks + 1);
+                else if (p.nr > 1) next_item();
+                if (j == 0) wait(acc_ready, items & 1);
+                const uint32_t u = blocks & 1, A = tmem + scores + 128 * u;
+                wait(p_full + 8 * u, blocks >> 1 & 1);
+                for (int left = cur.col_rows(j), x = 0; left > 0; left -= p.rows_x, x += p.rows_x, ring.next(p.ring)) {
+                    wait(full0 + 8 * ring.st, ring.ph);
+                    if (leader) {
+                        const uint64_t dB = mn_desc<128>(base + ring.st * p.stage, p.rows_x * 128);
+                        const uint32_t A0 = A + x;        // 64 tokens, 32 of their 64 columns
+                        if (left >= 128 && p.rows_x == 128) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) mma_bf16_ts(acc, A0 + 64 * (k >> 2) + 8 * (k & 3), dB + 128 * k, id_x, 1);
+                        } else if (left >= 64 && p.rows_x == 64) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) mma_bf16_ts(acc, A0 + 8 * k, dB + 128 * k, id_x, 1);
+                        } else {
+                            for (int k = 0; 16 * k < left && 16 * k < p.rows_x; ++k) mma_bf16_ts(acc, A0 + 64 * (k >> 2) + 8 * (k & 3), dB + 128 * k, id_x, 1);
+                        }
+                        mma_commit(empty0 + 8 * ring.st);
+                    }
                     __syncwarp();
                 }
-                if (j0 == 0) wait(acc_ready, items & 1);
-#pragma unroll
-                for (int u = 0; u < G; ++u)
-                    if (j0 + u < nblk) {
-                        const uint32_t A = tmem + scores + 128 * u;
-                        wait(p_full + 8 * u, (used[u] - 1) & 1);
-                        for (int left = it.col_rows(j0 + u), x = 0; left > 0; left -= p.rows_x, x += p.rows_x, ring.next(p.ring)) {
-                            wait(full0 + 8 * ring.st, ring.ph);
-                            if (leader) {
-                                const uint64_t dB = mn_desc<128>(base + ring.st * p.stage, p.rows_x * 128);
-                                const uint32_t A0 = A + x;            // 64 tokens, 32 of their 64 columns
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    if (16 * k < min(left, p.rows_x)) mma_bf16_ts(tmem, A0 + 64 * (k >> 2) + 8 * (k & 3), dB + 128 * k, id_x, 1);
-                                mma_commit(empty0 + 8 * ring.st);
-                            }
-                            __syncwarp();
-                        }
-                        if (leader) mma_commit(x_done + 8 * u);
-                        __syncwarp();
-                    }
+                if (leader) {
+                    mma_commit(x_done + 8 * u);
+                    if (j + 1 == cur.nblk) mma_commit(acc_done + 8 * ab);
+                }
+                __syncwarp();
+                if (j + 1 == cur.nblk && p.nr == 1) next_item();
             }
-            if (leader) mma_commit(acc_done);
-            __syncwarp();
             ++items;
         }
         if (leader) {                                     // products in flight end before their TMEM is freed
@@ -646,87 +705,94 @@ __global__ void __launch_bounds__(kRowThreads, TWO ? 1 : 2)
             mbar_wait(drain, 0, a.err);
         }
         __syncwarp();
-    } else {
+    } else if (warp < 8) {
         const int g = warp >> 2, w4 = warp & 3, row = 32 * w4 + lane;
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
         const int chunks = dx / 16, ch0 = g == 0 ? 0 : (chunks + 1) / 2, ch1 = g == 0 ? (chunks + 1) / 2 : chunks;      // of 16 columns
-        const bool shared = !values && rep > 1, whole = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
-        const uint32_t stg = base + p.out + g * 2 * kBox;             // this half's 64 columns of 128 rows on their way out
-        const int stages_x = kBlk / p.rows_x;
-        uint32_t items = 0, used = 0;                                 // parity of each buffer's scores so far
-        int stages = 0;                                               // before this item
-        // an item's gates: its row's, two columns', the blocks'
-        float g_row[5], g_col[2][2], g_tot[4], g_block[2];
+        RowGates* gates = reinterpret_cast<RowGates*>(tail + kRowGates);
+        uint32_t items = 0, blocks = 0;
+        int stages = nb;                                  // of the ring, up to this block's next scores'
+        // an item's gates on their way: its row's, two columns', the blocks', block rb's
+        float g_row[6], g_col[2][2], g_tot[4], g_blk[3], g_m[2][2];
         const auto load_gates = [&]() {
             const float* gt = ra.gates + ((size_t)it.slot * sh.H + it.h) * kGAll;
-            const int r = it.rb * kBlk + row;
+            const int r = it.rb * kBlk + row, c = it.rb * kBlk + (tid & 127);
             g_row[0] = gt[kGHi + r];
             g_row[1] = gt[kGLo + r];
             g_row[2] = gt[(keys ? kGPost : kGPre) + r];
             g_row[3] = gt[(keys ? kGTail : kGHead) + r];
-            g_row[4] = gt[kGBeta + r];
+            // the sums that a quarter's factors are relative to: at its last key, or before its first query
+            const int m = it.rb * kBlk + 32 * w4 + (keys ? 31 : -1);
+            g_row[4] = !keys && w4 == 0 ? 0.f : gt[kGHi + m];
+            g_row[5] = !keys && w4 == 0 ? 0.f : gt[kGLo + m];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                g_col[i][0] = gt[(keys ? kGPre : kGPost) + tid + 256 * i];
-                g_col[i][1] = gt[kGBeta + tid + 256 * i];
+            for (int e = 0; e < 2; ++e) {
+                g_col[e][0] = gt[(keys ? kGPre : kGPost) + tid + 256 * e];
+                g_col[e][1] = gt[kGBeta + tid + 256 * e];
+                const int w = 2 * (tid >> 7) + e, mw = it.rb * kBlk + 32 * w + (keys ? 31 : -1);
+                g_m[e][0] = !keys && w == 0 ? 0.f : gt[kGHi + mw];
+                g_m[e][1] = !keys && w == 0 ? 0.f : gt[kGLo + mw];
             }
             const float4 t4 = *reinterpret_cast<const float4*>(gt + kGTot);
             g_tot[0] = t4.x; g_tot[1] = t4.y; g_tot[2] = t4.z; g_tot[3] = t4.w;
-            g_block[0] = tid < kBlk ? gt[kGHi + it.rb * kBlk + tid] : 0.f;
-            g_block[1] = tid < kBlk ? gt[kGLo + it.rb * kBlk + tid] : 0.f;
+            g_blk[0] = gt[kGHi + c];
+            g_blk[1] = gt[kGLo + c];
+            g_blk[2] = keys ? 1.f : gt[kGBeta + c];
         };
-        int i = blockIdx.x;
-        const auto next = [&]() {                                     // the next item that there is, its gates on their way
-            while (i < count && !it.get(i, table, sh)) i += gridDim.x;
-            if (TWO && i < count) load_gates();
-        };
-        next();
-        while (i < count) {
-            const int rb = it.rb, nblk = it.nblk, rows = it.rows, hk = it.h / rep;
-            const bool live = row < it.row_n, staged = TWO && !shared && it.row_n == kBlk;
-            const size_t token = (size_t)it.first + rb * kBlk + row;
-            const int token0 = it.first + rb * kBlk, head = values ? it.h : hk;
-            const size_t at = (size_t)it.slot * sh.H + it.h;
-            if (!TWO) load_gates();                                   // ahead they would take registers that two CTAs do not have
-            named_sync(2, 256);                                       // the last item's factors are used up
+        bool more = it.seek(i, count, table, sh);
+        if (more) load_gates();
+        while (more) {
+            const RowsItem<MODE> cur = it;
+            const int rb = cur.rb, hk = cur.h / rep;
+            const bool live = row < cur.row_n;
+            const size_t token = (size_t)cur.first + rb * kBlk + row, at = (size_t)cur.slot * sh.H + cur.h;
+            RowGates& G = gates[items & 1];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int t = tid + 256 * c, b = t / kBlk;
-                float f = keys ? 1.f : g_col[c][1];
-                if (b != rb) f *= g_col[c][0];
+            for (int e = 0; e < 2; ++e) {
+                const int t = tid + 256 * e, b = t / kBlk, w = 2 * (tid >> 7) + e;
+                float f = keys ? g_col[e][0] : g_col[e][0] * g_col[e][1];
 #pragma unroll
                 for (int m = 1; m < 3; ++m)               // blocks between
                     if (m > min(b, rb) && m < max(b, rb)) f *= g_tot[m];
-                cf[t] = f;
+                G.cf[t] = f;
+                const float d = (g_m[e][0] - g_blk[0]) + (g_m[e][1] - g_blk[1]);
+                G.quarter[w][tid & 127] = g_blk[2] * ex2(keys ? d * -kLog2e : d * kLog2e);
             }
             if (tid < kBlk) {
-                hi[tid] = g_block[0];
-                lo[tid] = __float2bfloat16_rn(g_block[1]);
+                G.beta[tid] = g_blk[2];
+                G.hi[tid] = g_blk[0];
+                G.lo[tid] = __float2bfloat16_rn(g_blk[1]);
             }
+            const float mine = g_row[0], mine_lo = g_row[1], rf = g_row[2], sf = g_row[3];
+            const float dm = (mine - g_row[4]) + (mine_lo - g_row[5]), qf = ex2(keys ? dm * -kLog2e : dm * kLog2e);
+            const int nblk = cur.nblk;
+            i += gridDim.x;
+            more = it.seek(i, count, table, sh);
+            if (more) load_gates();
             named_sync(2, 256);
-            const float mine = g_row[0], mine_lo = g_row[1], rf = g_row[2], sf = g_row[3], of = keys ? g_row[4] : 1.f;
-            for (int j = 0; j < nblk; ++j) {
-                const int u = j % G, cb = it.col_block(j), n = it.col_rows(j);
+            const uint32_t acc = tmem + (two_sums ? 128 * (items & 1) : 0) + lanes;
+            for (int j = 0; j < nblk; ++j, ++blocks) {
+                const uint32_t u = blocks & 1;
+                const int cb = cur.col_block(j), n = cur.col_rows(j);
                 const uint32_t S = tmem + lanes + scores + 128 * u + 64 * g;
-                wait_or_dead(s_full + 8 * u, used >> u & 1, a.err, dead);
-                used ^= 1u << u;
+                wait_or_dead(s_full + 8 * u, blocks >> 1 & 1, a.err, dead);
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll 1
                 for (int q = 0; q < 2; ++q) {             // 32 columns
-                    const int c0 = 64 * g + 32 * q;
+                    const int c0 = 64 * g + 32 * q, cq = 2 * g + q;
                     uint32_t x[32], y[16];
-                    if (c0 >= ((n + 15) & ~15) || (cb == rb && (keys ? c0 + 31 < 32 * w4 : c0 > 32 * w4 + 31))) {
+                    if (c0 >= ((n + 15) & ~15) || (cb == rb && (keys ? cq < w4 : cq > w4))) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) y[e] = 0;        // behind the segment, or masked altogether
                     } else {
                         tmem_ld_n(S + 32 * q, x);
                         tmem_wait_ld();
-                        if (cb == rb) {
+                        if (cb == rb && cq == w4) {       // around the diagonal
 #pragma unroll
                             for (int e0 = 0; e0 < 32; e0 += 4) {
-                                const float4 h4 = *reinterpret_cast<const float4*>(hi + c0 + e0), f4 = *reinterpret_cast<const float4*>(cf + cb * kBlk + c0 + e0);
-                                const uint2 l2 = *reinterpret_cast<const uint2*>(lo + c0 + e0);
+                                const float4 h4 = *reinterpret_cast<const float4*>(G.hi + c0 + e0), f4 = *reinterpret_cast<const float4*>(G.beta + c0 + e0);
+                                const uint2 l2 = *reinterpret_cast<const uint2*>(G.lo + c0 + e0);
                                 const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, fs[4] = {f4.x, f4.y, f4.z, f4.w},
                                             ls[4] = {__uint_as_float(l2.x << 16), __uint_as_float(l2.x & 0xffff0000u), __uint_as_float(l2.y << 16),
                                                      __uint_as_float(l2.y & 0xffff0000u)};
@@ -740,10 +806,11 @@ __global__ void __launch_bounds__(kRowThreads, TWO ? 1 : 2)
                                 }
                             }
                         } else {
+                            const float* tab = cb == rb ? G.quarter[w4] + c0 : G.cf + cb * kBlk + c0;
+                            const float2 r2 = cb == rb ? make_float2(qf, qf) : make_float2(rf, rf);
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
-                                const float4 f = *reinterpret_cast<const float4*>(cf + cb * kBlk + c0 + e);
-                                const float2 r2 = make_float2(rf, rf);
+                                const float4 f = *reinterpret_cast<const float4*>(tab + e);
                                 const float2 y0 = fmul2(fmul2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), r2), make_float2(f.x, f.y)),
                                              y1 = fmul2(fmul2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), r2), make_float2(f.z, f.w));
                                 x[e] = __float_as_uint(y0.x);
@@ -763,26 +830,26 @@ __global__ void __launch_bounds__(kRowThreads, TWO ? 1 : 2)
                     tmem_st_n(S + 16 * q, y);             // over columns that are read
                 }
                 tmem_wait_st();
-                if (j + 1 == min(G, nblk)) {              // the state's product: its rows scaled
+                if (j == 0) {                             // the state's product: its rows scaled
                     wait_or_dead(inter_done, items & 1, a.err, dead);
                     __syncwarp();
                     tc_fence_after();
                     const __nv_bfloat16* z = MODE == kDq ? static_cast<const __nv_bfloat16*>(a.q) + token * sh.ldq + (size_t)hk * sh.dk
-                                                         : static_cast<const __nv_bfloat16*>(a.v) + token * sh.ldv + (size_t)it.h * sh.dv;
+                                                         : static_cast<const __nv_bfloat16*>(a.v) + token * sh.ldv + (size_t)cur.h * sh.dv;
                     float dot = 0.f;
 #pragma unroll 1
                     for (int ch = ch0; ch < ch1; ch += 2) {
                         uint32_t x[2][16];
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            if (ch + e < ch1) tmem_ld_n(tmem + lanes + 16 * (ch + e), x[e]);
+                            if (ch + e < ch1) tmem_ld_n(acc + 16 * (ch + e), x[e]);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
                             if (ch + e < ch1) {
 #pragma unroll
                                 for (int c = 0; c < 16; ++c) x[e][c] = __float_as_uint(sf * __uint_as_float(x[e][c]));
-                                tmem_st_n(tmem + lanes + 16 * (ch + e), x[e]);
+                                tmem_st_n(acc + 16 * (ch + e), x[e]);
                                 if ((MODE == kDq || MODE == kDv) && live) {       // q's or v's columns
                                     float y[8];
 #pragma unroll
@@ -801,45 +868,61 @@ __global__ void __launch_bounds__(kRowThreads, TWO ? 1 : 2)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(acc_ready);
                 }
-                if (n % 16 != 0) {                        // X's tokens of what lies behind: rows of zero, up to whole products.  Not before the
-                                                          // products have used what was in their stage (the state's have, or the scores of this group)
-                    // whole blocks before it; the state's stages behind the first scores
-                    const int j0 = j - u, stage = stages + n_inter + j0 * (nb + stages_x) + min(G, nblk - j0) * nb + u * stages_x + (n - 1) / p.rows_x;
-                    const int at_row = n % p.rows_x, cnt = 16 - n % 16, pieces = nx * 8;
+                // the ring's stages: the state's, the next scores', X's
+                if (j == 0) stages += n_inter;
+                if (j + 1 < nblk || (p.nr > 1 && more)) stages += nb;
+                if (n % 16 != 0) {                        // X's tokens of what lies behind: rows of zero, up to whole products
+                    // not before what was in X's stage is used up: the state's terms, or the X before
+                    if (j > 0) wait_or_dead(x_done + 8 * (u ^ 1), (blocks - 1) >> 1 & 1, a.err, dead);
+                    const int stage = stages + (n - 1) / p.rows_x, at_row = n % p.rows_x, cnt = 16 - n % 16, pieces = nx * 8;
                     wait_or_dead(full0 + 8 * (stage % p.ring), (stage / p.ring) & 1, a.err, dead);
                     for (int e = tid; e < cnt * pieces; e += 256)
                         st_shared16(base + stage % p.ring * p.stage + (e % pieces >> 3) * p.rows_x * 128 + (at_row + e / pieces) * 128 + (e & 7) * 16, 0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
+                stages += (n + p.rows_x - 1) / p.rows_x + (j + 1 == nblk && p.nr == 1 ? nb : 0);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * u);
             }
-            stages += n_inter + nblk * nb + (nblk - 1) * stages_x + (it.col_rows(nblk - 1) + p.rows_x - 1) / p.rows_x;
-            i += gridDim.x;
-            next();
-            wait_or_dead(acc_done, items & 1, a.err, dead);
+            ++items;
+        }
+    } else {
+        const int w4 = warp & 3, row = 32 * w4 + lane;
+        const uint32_t lanes = (uint32_t)(32 * w4) << 16, mine = base + p.out + row * 128;
+        const bool shared = !values && rep > 1, whole = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+        uint32_t items = 0;
+        while (it.seek(i, count, table, sh)) {
+            const uint32_t acc = tmem + (two_sums ? 128 * (items & 1) : 0) + lanes, ab = two_sums ? items & 1 : 0, ap = two_sums ? items >> 1 & 1 : items & 1;
+            const bool live = row < it.row_n, staged = false;
+            const size_t token = (size_t)it.first + it.rb * kBlk + row;
+            const int head = values ? it.h : it.h / rep;
+            const float of = keys ? ra.gates[((size_t)it.slot * sh.H + it.h) * kGAll + kGBeta + it.rb * kBlk + row] : 1.f;
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + token * out_heads * dx + (size_t)head * dx;
+            float* o32 = shared ? ra.heads + (token * sh.H + it.h) * dx : nullptr;
+            wait_or_dead(acc_done + 8 * ab, ap, a.err, dead);
             __syncwarp();
             tc_fence_after();
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + token * out_heads * dx + (size_t)head * dx;
-            float* o32 = shared ? ra.heads + (token * sh.H + at % sh.H) * dx : nullptr;
-            for (int x = g; x < nx; x += 2) {             // 64 columns
+            for (int x = 0; x < nx; ++x) {                // 64 columns
                 const int n16 = min(4, (dx - 64 * x) / 16);
-                if (staged) {                             // what was there has left
-                    if ((tid & 127) == 0) bulk_read_done();
-                    named_sync(3 + g, 128);
+                uint32_t v[4][16];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < n16) tmem_ld_n(acc + 64 * x + 16 * e, v[e]);
+                tmem_wait_ld();
+                if (x + 1 == nx) {                        // the sum's place is free
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acc_free + 8 * ab);
                 }
+                if (staged) {                             // what was there has left
+                    if (warp == 8 && lane == 0) bulk_read_done();
+                    named_sync(1, 128);
+                }
+                if (live) {
 #pragma unroll
-                for (int e0 = 0; e0 < 4; e0 += 2) {
-                    uint32_t v[2][16];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (e0 + e < n16) tmem_ld_n(tmem + lanes + 64 * x + 16 * (e0 + e), v[e]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (e0 + e < n16 && live) {
-                            const int col = 64 * x + 16 * (e0 + e);
+                    for (int e = 0; e < 4; ++e)
+                        if (e < n16) {
                             float y[16];
 #pragma unroll
                             for (int c = 0; c < 16; ++c) y[c] = of * __uint_as_float(v[e][c]);
@@ -848,7 +931,7 @@ __global__ void __launch_bounds__(kRowThreads, TWO ? 1 : 2)
 #pragma unroll
                                 for (int c = 0; c < 4; ++c)
                                     w[c] = make_uint4(__float_as_uint(y[4 * c]), __float_as_uint(y[4 * c + 1]), __float_as_uint(y[4 * c + 2]), __float_as_uint(y[4 * c + 3]));
-                                stg_pieces<4>(o32 + col, w, false, true);
+                                stg_pieces<4>(o32 + 64 * x + 16 * e, w, false, true);
                             } else {
                                 uint4 w[2];
 #pragma unroll
@@ -857,37 +940,35 @@ __global__ void __launch_bounds__(kRowThreads, TWO ? 1 : 2)
                                                       pack_bf16(y[8 * c + 4], y[8 * c + 5]), pack_bf16(y[8 * c + 6], y[8 * c + 7]));
                                 if (staged) {
 #pragma unroll
-                                    for (int c = 0; c < 2; ++c) st_shared16(stg + row * 128 + (((2 * (e0 + e) + c) ^ (row & 7)) << 4), w[c].x, w[c].y, w[c].z, w[c].w);
+                                    for (int c = 0; c < 2; ++c) st_shared16(mine + (((2 * e + c) ^ (row & 7)) << 4), w[c].x, w[c].y, w[c].z, w[c].w);
                                 } else {
-                                    stg_pieces<2>(o + col, w, false, whole);
+                                    stg_pieces<2>(o + 64 * x + 16 * e, w, false, whole);
                                 }
                             }
                         }
-                    __syncwarp();
                 }
+                __syncwarp();
                 if (staged) {
                     fence_proxy_async_smem();
-                    named_sync(3 + g, 128);
-                    if ((tid & 127) == 0) {
-                        for (int y = 0; y < 2; ++y) tma_store_3d(&mo, stg + y * kBox, 64 * x, head, token0 + 64 * y, false);
+                    named_sync(1, 128);
+                    if (warp == 8 && lane == 0) {
+                        for (int y = 0; y < 2; ++y) tma_store_3d(&mo, base + p.out + y * kBox, 64 * x, head, it.first + it.rb * kBlk + 64 * y, false);
                         bulk_commit();
                     }
                     __syncwarp();
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_free);
             ++items;
+            i += gridDim.x;
         }
-        if ((tid & 127) == 0) bulk_all_done();
+        if (warp == 8 && lane == 0) bulk_all_done();
         __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 13) {
         tc_fence_after();
-        tmem_dealloc(tmem, cols);
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -899,6 +980,7 @@ __global__ void __launch_bounds__(kRowThreads, TWO ? 1 : 2)
 // floats of a (slot, head): rows, F_tt, q's and v's dots by halves, columns by block of rows
 constexpr int kPartRow = 0, kPartDiag = kSeg, kPartQ = 2 * kSeg, kPartK = 4 * kSeg, kPartCol = 6 * kSeg, kPartAll = 10 * kSeg;
 
+constexpr int kPairThreads = 320;
 struct PairsPlan {
     int ring;
     bool two;
@@ -908,7 +990,7 @@ constexpr uint32_t kPairHolder = 2 * kMaxRing * 8 + 6 * 8, kPairCf = kPairHolder
                    kPairHi = kPairBeta + kSeg * 4, kPairLo = kPairHi + kBlk * 4, kPairCol = kPairLo + kBlk * 4, kPairTail = kPairCol + 2 * 4 * kBlk * 4;
 static_assert(kPairCf % 16 == 0 && kPairBeta % 16 == 0, "read by 16 bytes");
 
-__global__ void __launch_bounds__(kRowThreads, 2)
+__global__ void __launch_bounds__(kPairThreads, 2)
     lin_pairs_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mk,
                         const __grid_constant__ CUtensorMap mv, SeqArgs a, PairsPlan p, const float* gates, float* part) {
     extern __shared__ __align__(1024) char sm[];
@@ -1222,7 +1304,7 @@ __global__ void __launch_bounds__(256) lin_heads_kernel(SeqArgs a, const float* 
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-bool map_3d(CUtensorMap* m, const void* p, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2], uint32_t rows, bool f32 = false) {
+bool map_nd(CUtensorMap* m, int rank, const void* p, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box, bool f32) {
     static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -1230,11 +1312,23 @@ bool map_3d(CUtensorMap* m, const void* p, const cuuint64_t (&dims)[3], const cu
         return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
     }();
     if (enc == nullptr) return false;
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    // boxes of 128 bytes: by `rows` of the second dimension, or (0) one of it and 64 of the third
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(p), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// boxes of 128 bytes by `rows` of the second dimension, or (0) one of it and 64 of the third
+bool map_3d(CUtensorMap* m, const void* p, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2], uint32_t rows, bool f32 = false) {
     const cuuint32_t box[3] = {f32 ? 32u : 64u, rows > 0 ? rows : 1u, rows > 0 ? 1u : 64u};
-    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return map_nd(m, 3, p, dims, strides, box, f32);
+}
+// Tokens of a head by slabs of 64 columns, `rows` tokens and `slabs` slabs a box: (column, head, token, slab).  Where d is not a
+// whole number of slabs, one slab a box, and what lies behind d comes as zeros.
+bool slab_map(CUtensorMap* m, const void* p, const SeqShape& sh, int d, int heads, long long ld, int rows, int slabs) {
+    const bool whole = d % 64 == 0;
+    const cuuint64_t dims[4] = {(cuuint64_t)(whole ? 64 : d), (cuuint64_t)heads, (cuuint64_t)sh.total, (cuuint64_t)(whole ? d / 64 : 1)},
+                     strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2, 128};
+    const cuuint32_t box[4] = {64u, 1u, (cuuint32_t)rows, (cuuint32_t)(whole ? slabs : 1)};
+    return map_nd(m, 4, p, dims, strides, box, false);
 }
 // (d, head, token): what lies behind d comes as zeros, so that any multiple of 16 is one of 64
 bool token_map(CUtensorMap* m, const void* p, const SeqShape& sh, int d, int heads, long long ld) {
@@ -1268,35 +1362,44 @@ RowsPlan rows_plan(int da, int dx) {
     const int na = (da + 63) / 64, nx = (dx + 63) / 64;
     p.rows_x = dx > 128 ? 64 : 128;
     p.stage = 2 * kBox * (na > 1 || nx > 1 ? 2 : 1);
-    const uint32_t r = na * 2 * kBox;
-    // two CTAs an SM where TMEM holds both's sums and shared memory two stages each
-    p.two = dx > 128 || r + 2 * p.stage + kRowTail > kSmemHalf;
-    const uint32_t out = p.two ? 4 * kBox : 0, room = (p.two ? kSmemMost : kSmemHalf) - r - out - kRowTail;
-    p.ring = (int)(room / p.stage) < kMaxRing ? (int)(room / p.stage) : kMaxRing;
+    const uint32_t r = na * 2 * kBox, rest = 2 * kBox + kRowTail;
+    // two buffers of row operands where they leave the ring what two blocks' scores and X take
+    p.nr = (int)((kSmemMost - rest - 2 * r) / p.stage) >= 2 * ((da + 127) / 128 + kBlk / p.rows_x) ? 2 : 1;
+    const int room = (int)((kSmemMost - rest - p.nr * r) / p.stage);
+    p.ring = room < kMaxRing ? room : kMaxRing;
     p.r = p.ring * p.stage;            // behind the ring
-    p.out = p.r + r;
-    p.bars = p.out + out;
+    p.out = p.r + p.nr * r;
+    p.bars = p.out + 2 * kBox;
     p.smem = p.bars + kRowTail;
     return p;
 }
 
 template <int MODE>
-cudaError_t rows_go(const Maps& m, const CUtensorMap& ms, const SeqArgs& a, const float* gates, float* part, float* heads, int terms, cudaStream_t st) {
-    static bool done[2][64];
+cudaError_t rows_go(const CUtensorMap& ms, const SeqArgs& a, const float* gates, float* part, float* heads, int terms, cudaStream_t st) {
+    static bool done[64];
     const SeqShape& sh = a.sh;
     constexpr bool values = MODE == kOut || MODE == kDv;
     const RowsArgs ra = {rows_plan(values ? sh.dk : sh.dv, values ? sh.dv : sh.dk), part, (size_t)kPartAll, heads, gates, terms};
-    const auto kernel = ra.p.two ? lin_rows_tc_kernel<MODE, true> : lin_rows_tc_kernel<MODE, false>;
-    const cudaError_t e = ensure_smem(kernel, kSmemMost, done[ra.p.two]);
+    const cudaError_t e = ensure_smem(lin_rows_tc_kernel<MODE>, kSmemMost, done);
     if (e != cudaSuccess) return e;
-    const size_t items = (size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * (kSeg / kBlk), most = (ra.p.two ? 1 : 2) * kSMs;      // both fours
-    const dim3 grid((unsigned)(items < most ? items : most));
-    const CUtensorMap &mr = MODE == kOut ? m.q : MODE == kDq ? m.o : MODE == kDk ? m.v : m.k, &mb = MODE == kOut ? m.k : MODE == kDq ? m.v : MODE == kDk ? m.o : m.q,
-                      &mx = MODE == kOut ? m.v : MODE == kDq ? m.k : MODE == kDk ? m.q : m.o;
+    const size_t items = (size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * (kSeg / kBlk);      // fours, as the grid's size is
+    const dim3 grid((unsigned)(items < kSMs ? items : kSMs));
+    struct Operand {
+        const void* p;
+        int d, heads;
+        long long ld;
+    } const q = {a.q, sh.dk, sh.Hk, sh.ldq}, k = {a.k, sh.dk, sh.Hk, sh.ldk}, v = {a.v, sh.dv, sh.H, sh.ldv}, o = {a.dout, sh.dv, sh.H, (long long)sh.H * sh.dv},
+      r = MODE == kOut ? q : MODE == kDq ? o : MODE == kDk ? v : k, b = MODE == kOut ? k : MODE == kDq ? v : MODE == kDk ? o : q,
+      x = MODE == kOut ? v : MODE == kDq ? k : MODE == kDk ? q : o;
+    const int na = (r.d + 63) / 64, nx = (x.d + 63) / 64;
+    CUtensorMap mr, mb, mx;
+    if (!slab_map(&mr, r.p, sh, r.d, r.heads, r.ld, kBlk, na) || !slab_map(&mb, b.p, sh, b.d, b.heads, b.ld, kBlk, na < 2 ? na : 2) ||
+        !slab_map(&mx, x.p, sh, x.d, x.heads, x.ld, ra.p.rows_x, nx))
+        return cudaErrorInvalidValue;
     const int d = values ? sh.dv : sh.dk, out_heads = values ? sh.H : sh.Hk;
     CUtensorMap mo;
     if (!token_map(&mo, MODE == kOut ? a.out : MODE == kDq ? a.dq : MODE == kDk ? a.dk : a.dv, sh, d, out_heads, (long long)out_heads * d)) return cudaErrorInvalidValue;
-    return launch_kernel(kernel, grid, dim3(kRowThreads), ra.p.smem, st, false, mr, mb, mx, ms, mo, a, ra);
+    return launch_kernel(lin_rows_tc_kernel<MODE>, grid, dim3(kRowThreads), ra.p.smem, st, false, mr, mb, mx, ms, mo, a, ra);
 }
 
 cudaError_t prep_go(const SeqArgs& a, float* gates, cudaStream_t st) {
@@ -1331,7 +1434,7 @@ cudaError_t pairs_go(const Maps& m, const SeqArgs& a, const float* gates, float*
     const cudaError_t e = ensure_smem(lin_pairs_tc_kernel, kSmemMost, done);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * (kSeg / kBlk)));
-    return launch_kernel(lin_pairs_tc_kernel, grid, dim3(kRowThreads), p.smem, st, false, m.q, m.o, m.k, m.v, a, p, gates, part);
+    return launch_kernel(lin_pairs_tc_kernel, grid, dim3(kPairThreads), p.smem, st, false, m.q, m.o, m.k, m.v, a, p, gates, part);
 }
 
 }  // namespace
@@ -1371,7 +1474,7 @@ cudaError_t launch_linear_forward_tc(const SeqArgs& a, cudaStream_t st) {
     cudaError_t e = prep_go(a, gates, st);
     if (e == cudaSuccess) e = local_go<false>(m, a, gates, local, st);
     if (e == cudaSuccess) e = scan();
-    if (e == cudaSuccess) e = rows_go<kOut>(m, ms, a, gates, nullptr, nullptr, 1, st);
+    if (e == cudaSuccess) e = rows_go<kOut>(ms, a, gates, nullptr, nullptr, 1, st);
     return e;
 }
 
@@ -1397,9 +1500,9 @@ cudaError_t launch_linear_backward_tc(const SeqArgs& a, cudaStream_t st) {
         return cudaErrorInvalidValue;
     cudaError_t e = local_go<true>(m, a, gates, local, st);
     if (e == cudaSuccess) e = scan();
-    if (e == cudaSuccess) e = rows_go<kDq>(m, ms, a, gates, part + kPartQ, dq, 3, st);
-    if (e == cudaSuccess) e = rows_go<kDk>(m, me_keys, a, gates, nullptr, dk, 1, st);
-    if (e == cudaSuccess) e = rows_go<kDv>(m, me_values, a, gates, part + kPartK, nullptr, 3, st);
+    if (e == cudaSuccess) e = rows_go<kDq>(ms, a, gates, part + kPartQ, dq, 3, st);
+    if (e == cudaSuccess) e = rows_go<kDk>(me_keys, a, gates, nullptr, dk, 1, st);
+    if (e == cudaSuccess) e = rows_go<kDv>(me_values, a, gates, part + kPartK, nullptr, 3, st);
     if (e == cudaSuccess) e = pairs_go(m, a, gates, part, st);
     if (e == cudaSuccess)
         e = launch_kernel(lin_gates_tc_kernel, dim3((unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H)), dim3(kBlk), 0, st, false, a,
