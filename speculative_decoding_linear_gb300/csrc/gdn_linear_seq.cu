@@ -138,6 +138,8 @@ __device__ __forceinline__ Mat<T> columns(const Mat<T>& m, int c0) { return {m.p
 template <typename T, bool BACK>
 __global__ void __launch_bounds__(kT) lin_local_kernel(SeqArgs a, float* local, float* gend) {
     const SeqShape& sh = a.sh;
+    griddep_wait();
+    griddep_launch();
     const int slot = blockIdx.x / sh.H, h = blockIdx.x % sh.H, hk = h / (sh.H / sh.Hk);
     const int tiles_k = (sh.dk + 63) / 64, r0 = blockIdx.y / tiles_k * 64, c0 = blockIdx.y % tiles_k * 64;
     int s, c, first, rows;
@@ -182,6 +184,8 @@ template <typename T, int MODE>
 __global__ void __launch_bounds__(kT) lin_rows_kernel(SeqArgs a, const float* states, float* part) {
     constexpr bool keys = MODE == kDk || MODE == kDv, value_cols = MODE == kOut || MODE == kDv;
     const SeqShape& sh = a.sh;
+    griddep_wait();
+    griddep_launch();
     const int rep = sh.H / sh.Hk, heads = value_cols ? sh.H : sh.Hk, dx = value_cols ? sh.dv : sh.dk, dc = value_cols ? sh.dk : sh.dv;
     const int slot = blockIdx.x / heads, head = blockIdx.x % heads, n0 = blockIdx.y * 64;
     void* out = MODE == kOut ? a.out : MODE == kDq ? a.dq : MODE == kDk ? a.dk : a.dv;
@@ -272,6 +276,8 @@ template <typename T>
 __global__ void __launch_bounds__(kT) lin_gates_kernel(SeqArgs a, const float* part_q, int tiles_q, const float* part_k, int tiles_k,
                                                        const float* phi, int tiles_phi) {
     const SeqShape& sh = a.sh;
+    griddep_wait();
+    griddep_launch();
     int ob, oe;
     if (seq_outside(sh, ob, oe)) {
         zero_rows<float>(a.dla, sh.H, ob, oe, sh.total);
@@ -390,6 +396,8 @@ __device__ __forceinline__ float4 get_state(const void* in, size_t at, size_t ap
 template <int TERMS, bool BACK>
 __global__ void __launch_bounds__(kScanThreads) lin_scan_kernel(SeqShape sh, int L, const float* local, const float* gend, int gend_apart, const float* S0,
                                                                  void* out, size_t apart, const void* start, float* phi, float* last, int* err) {
+    griddep_wait();
+    griddep_launch();
     const int state = sh.dv * sh.dk, tiles = (state + kScanTile - 1) / kScanTile;
     const int tile = blockIdx.x % tiles, h = blockIdx.x / tiles % sh.H, s = blockIdx.x / (tiles * sh.H);
     const int e = tile * kScanTile + threadIdx.x * 4;
@@ -449,7 +457,7 @@ cudaError_t launch_linear_scan(const SeqShape& sh, int L, int terms, bool back, 
     const auto k = terms == 0 ? (back ? lin_scan_kernel<0, true> : lin_scan_kernel<0, false>)
                    : terms == 1 ? lin_scan_kernel<1, false>
                                 : (back ? lin_scan_kernel<3, true> : lin_scan_kernel<3, false>);
-    return launch_kernel(k, grid, dim3(kScanThreads), 0, st, false, sh, L, local, gend, gend_apart, S0, out, apart, start, phi, last, err);
+    return launch_kernel(k, grid, dim3(kScanThreads), 0, st, sh.total > 0, sh, L, local, gend, gend_apart, S0, out, apart, start, phi, last, err);
 }
 
 namespace {
@@ -463,7 +471,7 @@ cudaError_t forward_f32(const SeqArgs& a, cudaStream_t st) {
     cudaError_t e = launch_kernel(lin_local_kernel<float, false>, dim3(sth, tk * tv), dim3(kT), 0, st, false, a, states, gend);
     if (e == cudaSuccess) e = launch_linear_scan(sh, kSegF, 0, false, states, gend, 1, a.S0, states, 0, nullptr, nullptr, a.S_T, a.err, st);
     if (e == cudaSuccess && sh.total > 0)
-        e = launch_kernel(lin_rows_kernel<float, kOut>, dim3(sth, tv), dim3(kT), 0, st, false, a, (const float*)states, (float*)nullptr);
+        e = launch_kernel(lin_rows_kernel<float, kOut>, dim3(sth, tv), dim3(kT), 0, st, true, a, (const float*)states, (float*)nullptr);
     return e;
 }
 
@@ -479,11 +487,11 @@ cudaError_t backward_f32(const SeqArgs& a, cudaStream_t st) {
     cudaError_t e = launch_kernel(lin_local_kernel<float, true>, dim3(sth, tk * tv), dim3(kT), 0, st, false, a, ends, gend);
     if (e == cudaSuccess) e = launch_linear_scan(sh, kSegF, 0, true, ends, gend, 1, a.dS_T, ends, 0, starts, phi, a.dS0, a.err, st);
     if (e != cudaSuccess || sh.total == 0) return e;
-    e = launch_kernel(lin_rows_kernel<float, kDq>, dim3(stk, tk), dim3(kT), 0, st, false, a, starts, part_q);
-    if (e == cudaSuccess) e = launch_kernel(lin_rows_kernel<float, kDk>, dim3(stk, tk), dim3(kT), 0, st, false, a, (const float*)ends, (float*)nullptr);
-    if (e == cudaSuccess) e = launch_kernel(lin_rows_kernel<float, kDv>, dim3(sth, tv), dim3(kT), 0, st, false, a, (const float*)ends, part_k);
+    e = launch_kernel(lin_rows_kernel<float, kDq>, dim3(stk, tk), dim3(kT), 0, st, true, a, starts, part_q);
+    if (e == cudaSuccess) e = launch_kernel(lin_rows_kernel<float, kDk>, dim3(stk, tk), dim3(kT), 0, st, true, a, (const float*)ends, (float*)nullptr);
+    if (e == cudaSuccess) e = launch_kernel(lin_rows_kernel<float, kDv>, dim3(sth, tv), dim3(kT), 0, st, true, a, (const float*)ends, part_k);
     if (e == cudaSuccess)
-        e = launch_kernel(lin_gates_kernel<float>, dim3(sth), dim3(kT), 0, st, false, a, (const float*)part_q, (int)tk, (const float*)part_k,
+        e = launch_kernel(lin_gates_kernel<float>, dim3(sth), dim3(kT), 0, st, true, a, (const float*)part_q, (int)tk, (const float*)part_k,
                           (int)tv, (const float*)phi, scan_tiles(sh));
     return e;
 }

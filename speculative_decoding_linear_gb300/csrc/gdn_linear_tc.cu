@@ -61,6 +61,8 @@ __device__ __forceinline__ int2 slot_entry(const int2* table, int slot, int tota
 
 __global__ void __launch_bounds__(kBlk) lin_prep_kernel(SeqArgs a, float* gates) {
     const SeqShape& sh = a.sh;
+    griddep_wait();
+    griddep_launch();
     const int slot = blockIdx.x / sh.H, h = blockIdx.x % sh.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int s, c, first = 0, rows = 0;
     const bool is = slot_segment(sh, kSeg, slot, s, c, first, rows, a.err);
@@ -215,6 +217,8 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
     __syncthreads();
     const uint32_t tmem = warp_uniform(*holder);
     tc_fence_after();
+    griddep_wait();
+    griddep_launch();
     int slot, h, r0, c0, first;
     Ring ring;
     if (warp == 12) {
@@ -482,10 +486,6 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     const int da = values ? sh.dk : sh.dv, dx = values ? sh.dv : sh.dk;
     const int slots = seg_slots(sh.nseq, sh.total, kSeg), count = slots * sh.H * 4;
     const int2* table = slot_table(ra.gates, slots, sh.H);
-    {
-        int ob, oe;
-        if (seq_outside(sh, ob, oe)) zero_rows<__nv_bfloat16>(out, (size_t)out_heads * dx, ob, oe, sh.total);
-    }
     const uint32_t base = smem_u32(sm), bars = base + p.bars;
     const uint32_t full0 = bars, empty0 = bars + 8 * kMaxRing, rfull = bars + 16 * kMaxRing, rfree = rfull + 16, acc_free = rfull + 32, acc_done = rfull + 48,
                    s_full = rfull + 64, p_full = rfull + 80, x_done = rfull + 96, inter_done = rfull + 112, acc_ready = rfull + 120, drain = rfull + 128;
@@ -504,6 +504,12 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     __syncthreads();
     const uint32_t tmem = warp_uniform(*holder);
     tc_fence_after();
+    griddep_wait();
+    griddep_launch();
+    {
+        int ob, oe;
+        if (seq_outside(sh, ob, oe)) zero_rows<__nv_bfloat16>(out, (size_t)out_heads * dx, ob, oe, sh.total);
+    }
     RowsItem<MODE> it = {};
     int i = blockIdx.x;
     if (warp == 12) {
@@ -998,6 +1004,8 @@ __global__ void __launch_bounds__(kPairThreads, 2)
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_uniform(tid >> 5);
     const int slots = seg_slots(sh.nseq, sh.total, kSeg);
     const int at = blockIdx.x / 4, rb = 3 - blockIdx.x % 4, slot = at / sh.H, h = at % sh.H, hk = h / (sh.H / sh.Hk);
+    griddep_wait();
+    griddep_launch();
     const int2 seg = slot_entry(slot_table(gates, slots, sh.H), slot, sh.total);
     const int first = seg.x, rows = warp_uniform(seg.y);
     if (rb * kBlk >= rows) return;
@@ -1215,6 +1223,8 @@ __global__ void __launch_bounds__(kPairThreads, 2)
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kBlk) lin_gates_tc_kernel(SeqArgs a, const float* part, const float* phi, int tiles) {
     const SeqShape& sh = a.sh;
+    griddep_wait();
+    griddep_launch();
     int ob, oe;
     if (seq_outside(sh, ob, oe)) {
         zero_rows<float>(a.dla, sh.H, ob, oe, sh.total);
@@ -1279,6 +1289,8 @@ __global__ void __launch_bounds__(kBlk) lin_gates_tc_kernel(SeqArgs a, const flo
 // dq (blockIdx.y 0) and dk of heads that share q and k: the sum of theirs, in their order.
 __global__ void __launch_bounds__(256) lin_heads_kernel(SeqArgs a, const float* dq, const float* dk) {
     const SeqShape& sh = a.sh;
+    griddep_wait();
+    griddep_launch();
     int b = 0, e = sh.total;
     if (sh.offsets != nullptr) seq_outside(sh, b, e);
     const float* in = blockIdx.y == 0 ? dq : dk;
@@ -1346,15 +1358,6 @@ bool local_map(CUtensorMap* m, const float* p, const SeqShape& sh) {
     return map_3d(m, p, {(cuuint64_t)sh.dk, (cuuint64_t)sh.dv, n}, {(cuuint64_t)sh.dk * 4, (cuuint64_t)sh.dk * sh.dv * 4}, sh.dv < 128 ? sh.dv : 128, true);
 }
 
-struct Maps {
-    CUtensorMap q, k, v, o;
-};
-bool token_maps(const SeqArgs& a, bool back, Maps* m) {
-    const SeqShape& sh = a.sh;
-    return token_map(&m->q, a.q, sh, sh.dk, sh.Hk, sh.ldq) && token_map(&m->k, a.k, sh, sh.dk, sh.Hk, sh.ldk) &&
-           token_map(&m->v, a.v, sh, sh.dv, sh.H, sh.ldv) && (!back || token_map(&m->o, a.dout, sh, sh.dv, sh.H, (long long)sh.H * sh.dv));
-}
-
 constexpr uint32_t kSmemMost = 227 * 1024, kSmemHalf = 113 * 1024;      // one CTA an SM, two
 
 RowsPlan rows_plan(int da, int dx) {
@@ -1399,7 +1402,7 @@ cudaError_t rows_go(const CUtensorMap& ms, const SeqArgs& a, const float* gates,
     const int d = values ? sh.dv : sh.dk, out_heads = values ? sh.H : sh.Hk;
     CUtensorMap mo;
     if (!token_map(&mo, MODE == kOut ? a.out : MODE == kDq ? a.dq : MODE == kDk ? a.dk : a.dv, sh, d, out_heads, (long long)out_heads * d)) return cudaErrorInvalidValue;
-    return launch_kernel(lin_rows_tc_kernel<MODE>, grid, dim3(kRowThreads), ra.p.smem, st, false, mr, mb, mx, ms, mo, a, ra);
+    return launch_kernel(lin_rows_tc_kernel<MODE>, grid, dim3(kRowThreads), ra.p.smem, st, true, mr, mb, mx, ms, mo, a, ra);
 }
 
 cudaError_t prep_go(const SeqArgs& a, float* gates, cudaStream_t st) {
@@ -1408,21 +1411,28 @@ cudaError_t prep_go(const SeqArgs& a, float* gates, cudaStream_t st) {
 }
 
 template <bool BACK>
-cudaError_t local_go(const Maps& m, const SeqArgs& a, const float* gates, float* local, cudaStream_t st) {
+cudaError_t local_go(const SeqArgs& a, const float* gates, float* local, cudaStream_t st) {
     static bool done[64];
     const SeqShape& sh = a.sh;
-    CUtensorMap mo;
-    if (!local_map(&mo, local, sh)) return cudaErrorInvalidValue;
+    CUtensorMap ma, mb, mo;
+    if (!(BACK ? token_map(&ma, a.dout, sh, sh.dv, sh.H, (long long)sh.H * sh.dv) && token_map(&mb, a.q, sh, sh.dk, sh.Hk, sh.ldq)
+               : token_map(&ma, a.v, sh, sh.dv, sh.H, sh.ldv) && token_map(&mb, a.k, sh, sh.dk, sh.Hk, sh.ldk)) ||
+        !local_map(&mo, local, sh))
+        return cudaErrorInvalidValue;
     const cudaError_t e = ensure_smem(lin_local_tc_kernel<BACK>, kLocalSmem, done);
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * ((sh.dv + 127) / 128) * ((sh.dk + 127) / 128);
-    return launch_kernel(lin_local_tc_kernel<BACK>, dim3((unsigned)(tiles < kSMs ? tiles : kSMs)), dim3(kLocalThreads), kLocalSmem, st, false,
-                         BACK ? m.o : m.v, BACK ? m.q : m.k, mo, a, gates);
+    return launch_kernel(lin_local_tc_kernel<BACK>, dim3((unsigned)(tiles < kSMs ? tiles : kSMs)), dim3(kLocalThreads), kLocalSmem, st, !BACK,
+                         ma, mb, mo, a, gates);
 }
 
-cudaError_t pairs_go(const Maps& m, const SeqArgs& a, const float* gates, float* part, cudaStream_t st) {
+cudaError_t pairs_go(const SeqArgs& a, const float* gates, float* part, cudaStream_t st) {
     static bool done[64];
     const SeqShape& sh = a.sh;
+    CUtensorMap q, k, v, o;
+    if (!token_map(&q, a.q, sh, sh.dk, sh.Hk, sh.ldq) || !token_map(&k, a.k, sh, sh.dk, sh.Hk, sh.ldk) || !token_map(&v, a.v, sh, sh.dv, sh.H, sh.ldv) ||
+        !token_map(&o, a.dout, sh, sh.dv, sh.H, (long long)sh.H * sh.dv))
+        return cudaErrorInvalidValue;
     PairsPlan p = {};
     p.r2 = (sh.dk + 63) / 64 * 2 * kBox;
     p.stages = p.r2 + (sh.dv + 63) / 64 * 2 * kBox;
@@ -1434,7 +1444,7 @@ cudaError_t pairs_go(const Maps& m, const SeqArgs& a, const float* gates, float*
     const cudaError_t e = ensure_smem(lin_pairs_tc_kernel, kSmemMost, done);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * (kSeg / kBlk)));
-    return launch_kernel(lin_pairs_tc_kernel, grid, dim3(kPairThreads), p.smem, st, false, m.q, m.o, m.k, m.v, a, p, gates, part);
+    return launch_kernel(lin_pairs_tc_kernel, grid, dim3(kPairThreads), p.smem, st, true, q, o, k, v, a, p, gates, part);
 }
 
 }  // namespace
@@ -1468,11 +1478,10 @@ cudaError_t launch_linear_forward_tc(const SeqArgs& a, cudaStream_t st) {
         return launch_linear_scan(sh, kSeg, keep ? 3 : 1, false, local, gates + kGTot + 4, kGAll, a.S0, starts, apart, nullptr, nullptr, a.S_T, a.err, st);
     };
     if (sh.total == 0) return scan();            // the states pass through
-    Maps m;
     CUtensorMap ms;
-    if (!token_maps(a, false, &m) || !state_map(&ms, starts, sh, 1, sh.dv)) return cudaErrorInvalidValue;
+    if (!state_map(&ms, starts, sh, 1, sh.dv)) return cudaErrorInvalidValue;
     cudaError_t e = prep_go(a, gates, st);
-    if (e == cudaSuccess) e = local_go<false>(m, a, gates, local, st);
+    if (e == cudaSuccess) e = local_go<false>(a, gates, local, st);
     if (e == cudaSuccess) e = scan();
     if (e == cudaSuccess) e = rows_go<kOut>(ms, a, gates, nullptr, nullptr, 1, st);
     return e;
@@ -1494,22 +1503,21 @@ cudaError_t launch_linear_backward_tc(const SeqArgs& a, cudaStream_t st) {
         return launch_linear_scan(sh, kSeg, 3, true, local, gates + kGTot + 4, kGAll, a.dS_T, ends, apart, a.rec, phi, a.dS0, a.err, st);
     };
     if (sh.total == 0) return scan();
-    Maps m;
     CUtensorMap ms, me_keys, me_values;      // the starts by 64 rows of d_v; the ends so and by all
-    if (!token_maps(a, true, &m) || !state_map(&ms, a.rec, sh, 3, 64) || !state_map(&me_keys, ends, sh, 1, 64) || !state_map(&me_values, ends, sh, 3, sh.dv))
+    if (!state_map(&ms, a.rec, sh, 3, 64) || !state_map(&me_keys, ends, sh, 1, 64) || !state_map(&me_values, ends, sh, 3, sh.dv))
         return cudaErrorInvalidValue;
-    cudaError_t e = local_go<true>(m, a, gates, local, st);
+    cudaError_t e = local_go<true>(a, gates, local, st);
     if (e == cudaSuccess) e = scan();
     if (e == cudaSuccess) e = rows_go<kDq>(ms, a, gates, part + kPartQ, dq, 3, st);
     if (e == cudaSuccess) e = rows_go<kDk>(me_keys, a, gates, nullptr, dk, 1, st);
     if (e == cudaSuccess) e = rows_go<kDv>(me_values, a, gates, part + kPartK, nullptr, 3, st);
-    if (e == cudaSuccess) e = pairs_go(m, a, gates, part, st);
+    if (e == cudaSuccess) e = pairs_go(a, gates, part, st);
     if (e == cudaSuccess)
-        e = launch_kernel(lin_gates_tc_kernel, dim3((unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H)), dim3(kBlk), 0, st, false, a,
+        e = launch_kernel(lin_gates_tc_kernel, dim3((unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H)), dim3(kBlk), 0, st, true, a,
                           (const float*)part, (const float*)phi, scan_tiles(sh));
     if (e == cudaSuccess && sh.H > sh.Hk) {
         const long long n = (long long)sh.total * sh.Hk * sh.dk / 8;
-        e = launch_kernel(lin_heads_kernel, dim3((unsigned)((n + 255) / 256 < 16 * kSMs ? (n + 255) / 256 : 16 * kSMs), 2), dim3(256), 0, st, false, a,
+        e = launch_kernel(lin_heads_kernel, dim3((unsigned)((n + 255) / 256 < 16 * kSMs ? (n + 255) / 256 : 16 * kSMs), 2), dim3(256), 0, st, true, a,
                           (const float*)dq, (const float*)dk);
     }
     return e;

@@ -12,6 +12,7 @@ streams only); plain integer device addresses are accepted as well.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -589,15 +590,34 @@ def gdn_seq_step(q, k, v, log_alpha, beta, S, out, state_index=None, stream=None
 
 def _here(*tensors):
     """Every tensor on the current device, whose stream the call goes to: a kernel cannot read another's memory."""
-    on = {x.get_device() for x in tensors if x is not None}
-    if -1 in on or on != {_current_device()}:
-        raise ValueError("expected CUDA tensors on the current device")
+    dev = tensors[0].get_device()
+    for x in tensors:
+        if x is not None and (x.get_device() != dev or dev < 0):
+            raise ValueError("expected CUDA tensors on one device")
+    if dev != _current_device():
+        raise ValueError("expected tensors on the current device")
 
 
-def _linear_seq_bytes(name, *dims_dtype):
+def _dense(x):
+    """Pointer of a contiguous tensor that _here has seen, or None."""
+    if x is None:
+        return None
+    if not x.is_contiguous():
+        raise ValueError("expected a contiguous CUDA tensor")
+    return x.data_ptr() or None
+
+
+def _rows(x, what):
+    """_tokens, at once where the tensor is dense."""
+    if x.is_contiguous() and x.is_cuda:
+        return x.data_ptr() or None, x.shape[-1] * x.shape[-2]
+    return _tokens(x, what)
+
+
+@functools.lru_cache(maxsize=256)
+def _linear_seq_bytes(name, nseq, total, H, Hk, dk, dv, dtype):
     out = ctypes.c_size_t(0)
-    *dims, dtype = dims_dtype
-    _check(getattr(lib(), name)(*dims, dtype_code(dtype), ctypes.byref(out)), name)
+    _check(getattr(lib(), name)(nseq, total, H, Hk, dk, dv, dtype_code(dtype), ctypes.byref(out)), name)
     return out.value
 
 
@@ -633,12 +653,12 @@ def gdn_linear_seq_forward(q, k, v, log_alpha, beta, S0, out, S_T, workspace, of
     _sized(workspace, gdn_linear_seq_forward_workspace_bytes(*dims, q.dtype), "workspace")
     if record is not None:
         _sized(record, gdn_linear_seq_record_bytes(*dims, q.dtype), "record")
-    qp, ldq = _tokens(q, "q")
-    kp, ldk = _tokens(k, "k")
-    vp, ldv = _tokens(v, "v")
     _here(q, k, v, log_alpha, beta, S0, out, S_T, workspace, offsets, record)
-    _check(lib().gdn_linear_seq_forward(qp, ldq, kp, ldk, vp, ldv, dtype_code(q.dtype), _ptr(log_alpha), _ptr(beta), _ptr(S0),
-                                        _ptr(offsets), _ptr(out), _ptr(S_T), _ptr(record), _ptr(workspace), *dims,
+    qp, ldq = _rows(q, "q")
+    kp, ldk = _rows(k, "k")
+    vp, ldv = _rows(v, "v")
+    _check(lib().gdn_linear_seq_forward(qp, ldq, kp, ldk, vp, ldv, dtype_code(q.dtype), _dense(log_alpha), _dense(beta), _dense(S0),
+                                        _dense(offsets), _dense(out), _dense(S_T), _dense(record), _dense(workspace), *dims,
                                         _stream(stream)), "gdn_linear_seq_forward")
 
 
@@ -653,13 +673,13 @@ def gdn_linear_seq_backward(q, k, v, log_alpha, beta, dout, dS_T, record, dq, dk
     _same(dS0, (nseq, H, d_v, d_k), torch.float32, "dS0")
     _sized(workspace, gdn_linear_seq_workspace_bytes(*dims, q.dtype), "workspace")
     _sized(record, gdn_linear_seq_record_bytes(*dims, q.dtype), "record")
-    qp, ldq = _tokens(q, "q")
-    kp, ldk = _tokens(k, "k")
-    vp, ldv = _tokens(v, "v")
     _here(q, k, v, log_alpha, beta, dout, dS_T, record, dq, dk, dv, dlog_alpha, dbeta, dS0, workspace, offsets)
-    _check(lib().gdn_linear_seq_backward(qp, ldq, kp, ldk, vp, ldv, dtype_code(q.dtype), _ptr(log_alpha), _ptr(beta),
-                                         _ptr(offsets), _ptr(dout), _ptr(dS_T), _ptr(record), _ptr(dq), _ptr(dk), _ptr(dv),
-                                         _ptr(dlog_alpha), _ptr(dbeta), _ptr(dS0), _ptr(workspace), *dims, _stream(stream)),
+    qp, ldq = _rows(q, "q")
+    kp, ldk = _rows(k, "k")
+    vp, ldv = _rows(v, "v")
+    _check(lib().gdn_linear_seq_backward(qp, ldq, kp, ldk, vp, ldv, dtype_code(q.dtype), _dense(log_alpha), _dense(beta),
+                                         _dense(offsets), _dense(dout), _dense(dS_T), _dense(record), _dense(dq), _dense(dk), _dense(dv),
+                                         _dense(dlog_alpha), _dense(dbeta), _dense(dS0), _dense(workspace), *dims, _stream(stream)),
            "gdn_linear_seq_backward")
 
 
@@ -667,8 +687,8 @@ def gdn_linear_seq_step(q, k, v, log_alpha, beta, S, out, state_index=None, stre
     """One token of decay-gated linear attention for each of B sequences: arguments as gdn_seq_step."""
     B, slots, H, Hk, dk, dv = _step_dims(q, k, v, log_alpha, beta, S, out, state_index)
     _here(q, k, v, log_alpha, beta, S, out, state_index)
-    rc = lib().gdn_linear_seq_step(_ptr(q), _ptr(k), _ptr(v), dtype_code(q.dtype), _ptr(log_alpha), _ptr(beta), _ptr(S),
-                                   _ptr(state_index), _ptr(out), B, slots, H, Hk, dk, dv, _stream(stream))
+    rc = lib().gdn_linear_seq_step(_dense(q), _dense(k), _dense(v), dtype_code(q.dtype), _dense(log_alpha), _dense(beta), _dense(S),
+                                   _dense(state_index), _dense(out), B, slots, H, Hk, dk, dv, _stream(stream))
     if rc != OK:
         raise GdnError(rc, "gdn_linear_seq_step")
 
@@ -692,17 +712,18 @@ def gdn_rotary(q, k, positions, inv_freq, q_out, k_out, scale=1.0, interleaved=F
     if inv_freq.dim() != 1 or inv_freq.dtype is not torch.float32:
         raise ValueError("inv_freq must be fp32 [rot / 2]")
     _same(q_out, q.shape, q.dtype, "q_out")
-    qp, ldq = _tokens(q, "q")
-    qo, ldqo = _tokens(q_out, "q_out")
+    if k is not None:
+        _same(k_out, k.shape, k.dtype, "k_out")
+    _here(q, k, positions, inv_freq, q_out, k_out)
+    qp, ldq = _rows(q, "q")
+    qo, ldqo = _rows(q_out, "q_out")
     kp = ko = None
     ldk = ldko = Hk = 0
     if k is not None:
-        _same(k_out, k.shape, k.dtype, "k_out")
-        kp, ldk = _tokens(k, "k")
-        ko, ldko = _tokens(k_out, "k_out")
+        kp, ldk = _rows(k, "k")
+        ko, ldko = _rows(k_out, "k_out")
         Hk = k.shape[-2]
-    _here(q, k, positions, inv_freq, q_out, k_out)
-    _check(lib().gdn_rotary(qp, ldq, kp, ldk, dtype_code(q.dtype), _ptr(positions), _ptr(inv_freq), scale, qo, ldqo, ko, ldko,
+    _check(lib().gdn_rotary(qp, ldq, kp, ldk, dtype_code(q.dtype), _dense(positions), _dense(inv_freq), scale, qo, ldqo, ko, ldko,
                             positions.numel(), q.shape[-2], Hk, q.shape[-1], 2 * inv_freq.numel(), int(interleaved), int(inverse),
                             _stream(stream)), "gdn_rotary")
 
