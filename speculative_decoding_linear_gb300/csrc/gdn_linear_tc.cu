@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
 //
 // A CTA an SM takes block after block of rows; the scores of a block of columns, be it the next rows' first, are formed
 // before the product of the one before it, so that the workers' pass over scores runs beside products.  Warps 0-7 work
-// (four a half of the columns), 8-11 move finished sums out (by way of shared memory where all rows are there), 12
+// (four a half of the columns), 8-11 move finished sums out, 12
 // copies, 13 multiplies.
 // ---------------------------------------------------------------------------
 enum { kOut, kDq, kDk, kDv };
@@ -419,7 +419,7 @@ constexpr int kRowThreads = 448, kMaxRing = 8;
 
 struct RowsPlan {              // shared memory of a launch
     int ring, rows_x, nr;      // stages; tokens of a stage of X; buffers of row operands
-    uint32_t stage, r, out, bars, smem;
+    uint32_t stage, r, bars, smem;
 };
 
 struct RowsArgs {
@@ -442,30 +442,50 @@ constexpr int kRowNBars = 2 * kMaxRing + 17;
 constexpr uint32_t kRowHolder = kRowNBars * 8, kRowGates = (kRowHolder + 8 + 15) / 16 * 16, kRowTail = kRowGates + 2 * sizeof(RowGates);
 static_assert(sizeof(RowGates) % 16 == 0, "read by 16 bytes");
 
+// A CTA's items one after another: number i of (slot, head, block).  Four neighbours are a segment's blocks (they read the
+// same tiles), in another order each turn of the grid, so that every CTA gets long and short ones.
 template <int MODE>
 struct RowsItem {
-    int slot, h, rb, first, rows, row_n, nblk;
-    // Item i: four neighbours are a segment's blocks (they read the same tiles), in another order each turn of the grid,
-    // so that every CTA gets long and short ones.  False where there is none.
-    __device__ __forceinline__ bool get(int i, const int2* table, const SeqShape& sh) {
+    int slot, h, turn, rb, first, rows, row_n, nblk;
+    bool there;
+    __device__ __forceinline__ void begin(const int2* table, const SeqShape& sh, int slots) {
+        slot = (int)(blockIdx.x >> 2) / sh.H;
+        h = (int)(blockIdx.x >> 2) % sh.H;
+        turn = 0;
+        look(table, sh, slots, 0, 0);
+    }
+    // On to the next that there is: grid / 4 (slot, head) on each time.
+    __device__ __forceinline__ void look(const int2* table, const SeqShape& sh, int slots, int ds, int dh) {
         constexpr bool keys = MODE == kDk || MODE == kDv;
-        const int at = i >> 2, q = ((i & 3) + i / (int)gridDim.x) & 3;
-        rb = keys ? q : 3 - q;
-        slot = at / sh.H;
-        h = at % sh.H;
-        const int2 e = slot_entry(table, slot, sh.total);
-        first = e.x;
-        rows = e.y;
+        there = false;
+#pragma unroll 1
+        for (bool step = ds + dh > 0;; step = true) {
+            if (step) {
+                slot += ds;
+                h += dh;
+                if (h >= sh.H) {
+                    h -= sh.H;
+                    ++slot;
+                }
+                ++turn;
+            }
+            if (slot >= slots) return;
+            const int2 e = slot_entry(table, slot, sh.total);
+            const int q = ((blockIdx.x & 3) + turn) & 3;
+            rb = keys ? q : 3 - q;
+            if (rb * kBlk < e.y) {
+                first = e.x;
+                rows = e.y;
+                break;
+            }
+            if (ds + dh == 0) {
+                ds = (int)(gridDim.x >> 2) / sh.H;
+                dh = (int)(gridDim.x >> 2) % sh.H;
+            }
+        }
+        there = true;
         row_n = min(kBlk, rows - rb * kBlk);
         nblk = keys ? (rows - 1) / kBlk - rb + 1 : rb + 1;       // blocks of columns: rb .. last, or 0 .. rb
-        return rb * kBlk < rows;
-    }
-    // The first there is from i on; i becomes its number, `count` where there is none.
-    __device__ __forceinline__ bool seek(int& i, int count, const int2* table, const SeqShape& sh) {
-        for (; i < count; i += gridDim.x)
-            if (get(i, table, sh)) return true;
-        i = count;
-        return false;
     }
     __device__ __forceinline__ int col_block(int j) const { return MODE == kDk || MODE == kDv ? rb + j : j; }
     __device__ __forceinline__ int col_rows(int j) const { return min(kBlk, rows - col_block(j) * kBlk); }
@@ -474,7 +494,7 @@ struct RowsItem {
 template <int MODE>
 __global__ void __launch_bounds__(kRowThreads, 1)
     lin_rows_tc_kernel(const __grid_constant__ CUtensorMap mr, const __grid_constant__ CUtensorMap mb, const __grid_constant__ CUtensorMap mx,
-                       const __grid_constant__ CUtensorMap ms, const __grid_constant__ CUtensorMap mo, SeqArgs a, RowsArgs ra) {
+                       const __grid_constant__ CUtensorMap ms, SeqArgs a, RowsArgs ra) {
     constexpr bool keys = MODE == kDk || MODE == kDv, values = MODE == kOut || MODE == kDv;     // rows are keys; columns d_v
     constexpr uint32_t scores = 256;                      // TMEM: one sum of 256 columns or two of 128, then two blocks' scores
     extern __shared__ __align__(1024) char sm[];
@@ -484,7 +504,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     void* out = MODE == kOut ? a.out : MODE == kDq ? a.dq : MODE == kDk ? a.dk : a.dv;
     const int rep = sh.H / sh.Hk, out_heads = values ? sh.H : sh.Hk;
     const int da = values ? sh.dk : sh.dv, dx = values ? sh.dv : sh.dk;
-    const int slots = seg_slots(sh.nseq, sh.total, kSeg), count = slots * sh.H * 4;
+    const int slots = seg_slots(sh.nseq, sh.total, kSeg), ds = (int)(gridDim.x >> 2) / sh.H, dh = (int)(gridDim.x >> 2) % sh.H;
     const int2* table = slot_table(ra.gates, slots, sh.H);
     const uint32_t base = smem_u32(sm), bars = base + p.bars;
     const uint32_t full0 = bars, empty0 = bars + 8 * kMaxRing, rfull = bars + 16 * kMaxRing, rfree = rfull + 16, acc_free = rfull + 32, acc_done = rfull + 48,
@@ -510,8 +530,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         int ob, oe;
         if (seq_outside(sh, ob, oe)) zero_rows<__nv_bfloat16>(out, (size_t)out_heads * dx, ob, oe, sh.total);
     }
-    RowsItem<MODE> it = {};
-    int i = blockIdx.x;
+    // Scores and products of a CTA's blocks of columns, one after another over its items, interleaved: the scores of a
+    // block before the product of the one before it, the state's product behind the first scores of its rows.  With one
+    // buffer of row operands an item's first scores come behind the last product of the item before.
+    RowsItem<MODE> it;
+    it.begin(table, sh, slots);
     if (warp == 12) {
         if (elect_one()) {
             // `rows` tokens of slabs x0, x0 + 1, .. (64 columns each): those beyond the sequence's are read and never used
@@ -521,67 +544,54 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                     for (int x = 0; x < nslab; ++x) tma_4d(dst + x * rows * 128, m, 64 * (x0 + x), head, t0, 0, bar);
             };
             const bool whole_a = da % 64 == 0, whole_x = dx % 64 == 0;
+            const size_t apart = (size_t)slots * sh.H;
             Ring ring, rr;
             int issued = 0, r_issued = 0;
             bool ok = true;
-            // the next stage, `bytes` of it expected; false once a wait has run out
-            const auto stage = [&](uint32_t bytes) {
-                if (ok && issued >= p.ring) ok = wait_or_dead(empty0 + 8 * ring.st, ring.ph ^ 1, a.err, dead);
-                if (ok) mbar_expect_tx(full0 + 8 * ring.st, bytes);
-                return ok;
-            };
-            const auto next_stage = [&]() {
-                ring.next(p.ring);
-                ++issued;
-            };
-            // block j's score operand, behind the rows' own where it is their first
-            const auto score_operand = [&](int j) {
-                const int hr = values ? it.h / rep : it.h;
-                if (j == 0) {
-                    if (r_issued >= p.nr && !(ok = ok && wait_or_dead(rfree + 8 * rr.st, rr.ph ^ 1, a.err, dead))) return;
-                    mbar_expect_tx(rfull + 8 * rr.st, r_bytes);
-                    load(base + p.r + rr.st * r_bytes, &mr, whole_a, hr, it.first + it.rb * kBlk, 0, na, kBlk, rfull + 8 * rr.st);
-                    rr.next(p.nr);
-                    ++r_issued;
-                }
-                for (int x = 0; x < nb; ++x, next_stage()) {
-                    const int sl = whole_a ? min(2, na) : min(2, na - 2 * x);         // of a whole box those behind the last come as zeros
-                    if (!stage(sl * 2 * kBox)) return;
-                    load(base + ring.st * p.stage, &mb, whole_a, hr, it.first + it.col_block(j) * kBlk, 2 * x, sl, kBlk, full0 + 8 * ring.st);
-                }
-            };
-            const size_t apart = (size_t)slots * sh.H;
-            bool more = it.seek(i, count, table, sh);
-            if (more) score_operand(0);
-            while (ok && more) {
-                const RowsItem<MODE> cur = it;
-                const auto next_item = [&]() {
-                    i += gridDim.x;
-                    more = it.seek(i, count, table, sh);
-                    if (more) score_operand(0);
-                };
-                // the order that the products take them in
-                for (int j = 0; ok && j < cur.nblk; ++j) {
-                    if (j == 0)
-                        for (int t = ra.terms - 1; ok && t >= 0; --t)         // the small terms first
-                            for (int x = 0; x < na; ++x, next_stage()) {
-                                if (!stage(values ? dx * 128 : nx * kBox)) break;
-                                const uint32_t dst = base + ring.st * p.stage, bar = full0 + 8 * ring.st;
-                                const int z = (int)(t * apart + (size_t)cur.slot * sh.H + cur.h);
-                                if (values)               // rows of d_v, 64 of d_k along the row
-                                    tma_3d(dst, &ms, 64 * x, 0, z, bar);
-                                else                      // 64 rows of d_v, d_k along the row
-                                    for (int y = 0; y < nx; ++y) tma_3d(dst + y * kBox, &ms, 64 * y, 64 * x, z, bar);
-                            }
-                    if (j + 1 < cur.nblk) score_operand(j + 1);
-                    else if (p.nr > 1) next_item();
-                    const int n = cur.col_rows(j);
-                    for (int x = 0; ok && x * p.rows_x < n; ++x, next_stage()) {
-                        if (!stage(nx * p.rows_x * 128)) break;
-                        load(base + ring.st * p.stage, &mx, whole_x, values ? cur.h : cur.h / rep, cur.first + cur.col_block(j) * kBlk + x * p.rows_x, 0, nx, p.rows_x,
-                             full0 + 8 * ring.st);
+            RowsItem<MODE> prev;
+            bool last = false;
+            for (int j = 0, pj = -1; ok && !last;) {          // it's block j; the block before it, prev's pj
+                last = !it.there;
+                const bool x_first = last || (j == 0 && p.nr == 1);
+                const int n0 = pj == 0 ? n_inter : 0, nxt = pj >= 0 ? (prev.col_rows(pj) + p.rows_x - 1) / p.rows_x : 0, ns = last ? 0 : nb;
+#pragma unroll 1
+                for (int e = 0; ok && e < n0 + ns + nxt; ++e) {
+                    // which: the state's stages, then scores' and X's in their order
+                    const int w = e - n0, s_at = x_first ? w - nxt : w, x_at = x_first ? w : w - ns;
+                    const bool state = e < n0, score = !state && s_at >= 0 && s_at < ns;
+                    if (score && j == 0 && s_at == 0) {
+                        if (r_issued >= p.nr && !(ok = wait_or_dead(rfree + 8 * rr.st, rr.ph ^ 1, a.err, dead))) break;
+                        mbar_expect_tx(rfull + 8 * rr.st, r_bytes);
+                        load(base + p.r + rr.st * r_bytes, &mr, whole_a, values ? it.h / rep : it.h, it.first + it.rb * kBlk, 0, na, kBlk, rfull + 8 * rr.st);
+                        rr.next(p.nr);
+                        ++r_issued;
                     }
-                    if (ok && j + 1 == cur.nblk && p.nr == 1) next_item();
+                    if (issued >= p.ring && !(ok = wait_or_dead(empty0 + 8 * ring.st, ring.ph ^ 1, a.err, dead))) break;
+                    const uint32_t dst = base + ring.st * p.stage, bar = full0 + 8 * ring.st;
+                    if (state) {                              // the small terms first
+                        const int x = e % na, z = (int)((ra.terms - 1 - e / na) * apart + (size_t)prev.slot * sh.H + prev.h);
+                        mbar_expect_tx(bar, values ? dx * 128 : nx * kBox);
+                        if (values)                           // rows of d_v, 64 of d_k along the row
+                            tma_3d(dst, &ms, 64 * x, 0, z, bar);
+                        else                                  // 64 rows of d_v, d_k along the row
+                            for (int y = 0; y < nx; ++y) tma_3d(dst + y * kBox, &ms, 64 * y, 64 * x, z, bar);
+                    } else {
+                        // of a whole box of score operands those slabs behind the last come as zeros
+                        const int slabs = !score ? nx : whole_a ? min(2, na) : min(2, na - 2 * s_at), rows = score ? kBlk : p.rows_x;
+                        const int head = score ? (values ? it.h / rep : it.h) : values ? prev.h : prev.h / rep;
+                        const int t0 = score ? it.first + it.col_block(j) * kBlk : prev.first + prev.col_block(pj) * kBlk + x_at * p.rows_x;
+                        mbar_expect_tx(bar, slabs * rows * 128);
+                        load(dst, score ? &mb : &mx, score ? whole_a : whole_x, head, t0, score ? 2 * s_at : 0, slabs, rows, bar);
+                    }
+                    ring.next(p.ring);
+                    ++issued;
+                }
+                if (last) break;
+                prev = it;
+                pj = j;
+                if (++j == it.nblk) {
+                    j = 0;
+                    it.look(table, sh, slots, ds, dh);
                 }
             }
             if (*dead) {                                  // copies in flight end before the CTA does
@@ -599,112 +609,112 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             tc_fence_after();
         };
         const uint32_t id_x = idesc_bf16(128, dx) | kBMn, id_i = idesc_bf16(128, dx) | (values ? 0u : kBMn);
-        uint32_t items = 0, blocks = 0;                   // sums and blocks of scores so far
-        // scores of block j, the blocks'-th, of `it`
-        const auto score = [&](int j, uint32_t n) {
-            const uint32_t u = n & 1, D = tmem + scores + 128 * u, id = idesc_bf16(128, (it.col_rows(j) + 15) & ~15);
-            if (j == 0) wait(rfull + 8 * rr.st, rr.ph);
-            if (n > 1) wait(x_done + 8 * u, (n >> 1 & 1) ^ 1);        // the scores before are used up
-            const uint64_t dR = k_desc<128>(base + p.r + rr.st * r_bytes);
-            for (int x = 0; x < nb; ++x, ring.next(p.ring)) {
-                wait(full0 + 8 * ring.st, ring.ph);
-                if (leader) {
-                    const uint64_t dA = dR + (x * 4 * kBox >> 4), dB = k_desc<128>(base + ring.st * p.stage);
-                    if (da - 128 * x >= 128) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_bf16(D, dA + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), dB + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), id, x + k > 0);
-                    } else {
-                        for (int k = 0; 128 * x + 16 * k < da; ++k)
-                            mma_bf16(D, dA + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), dB + ((k >> 2) * 2 * kBox >> 4) + 2 * (k & 3), id, x + k > 0);
-                    }
-                    mma_commit(empty0 + 8 * ring.st);
-                }
-                __syncwarp();
-            }
-            if (leader) mma_commit(s_full + 8 * u);
-            __syncwarp();
-        };
-        const auto uniform = [&]() {
-            it.rows = warp_uniform(it.rows);
-            it.nblk = warp_uniform(it.nblk);
-        };
-        bool more = it.seek(i, count, table, sh);
-        if (more) {
-            uniform();
-            score(0, 0);
-        }
-        while (more) {
-            const RowsItem<MODE> cur = it;
-            const uint32_t acc = tmem + (two_sums ? 128 * (items & 1) : 0), ab = two_sums ? items & 1 : 0, ap = two_sums ? items >> 1 & 1 : items & 1;
-            for (int j = 0; j < cur.nblk; ++j, ++blocks) {
-                // the next rows' first scores: their operand has this item's place once all scores and the state's product
-                // have read it, or one of its own
-                const auto next_item = [&]() {
-                    if (leader) mma_commit(rfree + 8 * rr.st);
-                    __syncwarp();
-                    rr.next(p.nr);
-                    i += gridDim.x;
-                    more = it.seek(i, count, table, sh);
-                    if (more) {
-                        uniform();
-                        score(0, blocks + 1);
-                    }
-                };
-                if (j == 0) {
-                    if (items > (uint32_t)two_sums) wait(acc_free + 8 * ab, ap ^ 1);
-                    const uint64_t dR = k_desc<128>(base + p.r + rr.st * r_bytes);
-                    for (int t = 0; t < ra.terms; ++t)
-                        for (int x = 0; x < na; ++x, ring.next(p.ring)) {
-                            wait(full0 + 8 * ring.st, ring.ph);
-                            if (leader) {
-                                const uint32_t sb = base + ring.st * p.stage;
-                                const uint64_t dA = dR + (x * 2 * kBox >> 4), dB = values ? k_desc<128>(sb) : mn_desc<128>(sb, kBox);
-                                if (da - 64 * x >= 64) {
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) mma_bf16(acc, dA + 2 * k, dB + (values ? 2 * k : 128 * k), id_i, t + x + k > 0);
-                                } else {
-                                    for (int k = 0; 64 * x + 16 * k < da; ++k) mma_bf16(acc, dA + 2 * k, dB + (values ? 2 * k : 128 * k), id_i, t + x + k > 0);
-                                }
-                                mma_commit(empty0 + 8 * ring.st);
-                            }
-                            __syncwarp();
-                        }
-                    if (leader) mma_commit(inter_done);
-                    __syncwarp();
-                }
-                // the next block's scores before this one's product
-                if (j + 1 < cur.nblk) score(j + 1, blocks + 1);
-                else if (p.nr > 1) next_item();
-                if (j == 0) wait(acc_ready, items & 1);
-                const uint32_t u = blocks & 1, A = tmem + scores + 128 * u;
-                wait(p_full + 8 * u, blocks >> 1 & 1);
-                for (int left = cur.col_rows(j), x = 0; left > 0; left -= p.rows_x, x += p.rows_x, ring.next(p.ring)) {
+        uint32_t items = 0, blocks = 0;                   // sums, and blocks of scores, so far
+        int p_rows = 0;                                   // tokens of the block of columns before
+        bool p_last = false;
+        for (int j = 0, pj = -1;;) {
+            const bool last = !warp_uniform(it.there);
+            const bool x_first = last || (j == 0 && p.nr == 1);
+            const uint32_t ab = two_sums ? items & 1 : 0, ap = two_sums ? items >> 1 & 1 : items & 1, acc = tmem + 128 * ab;
+            if (pj == 0) {
+                if (items > (uint32_t)two_sums) wait(acc_free + 8 * ab, ap ^ 1);
+                const uint64_t dR = k_desc<128>(base + p.r + rr.st * r_bytes);
+#pragma unroll 1
+                for (int e = 0, x = 0; e < n_inter; ++e, ring.next(p.ring)) {
                     wait(full0 + 8 * ring.st, ring.ph);
                     if (leader) {
-                        const uint64_t dB = mn_desc<128>(base + ring.st * p.stage, p.rows_x * 128);
-                        const uint32_t A0 = A + x;        // 64 tokens, 32 of their 64 columns
-                        if (left >= 128 && p.rows_x == 128) {
+                        const uint32_t sb = base + ring.st * p.stage;
+                        const uint64_t dA = dR + (x * 2 * kBox >> 4), dB = values ? k_desc<128>(sb) : mn_desc<128>(sb, kBox);
+                        if (da - 64 * x >= 64) {
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) mma_bf16_ts(acc, A0 + 64 * (k >> 2) + 8 * (k & 3), dB + 128 * k, id_x, 1);
-                        } else if (left >= 64 && p.rows_x == 64) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) mma_bf16_ts(acc, A0 + 8 * k, dB + 128 * k, id_x, 1);
+                            for (int k = 0; k < 4; ++k) mma_bf16(acc, dA + 2 * k, dB + (values ? 2 * k : 128 * k), id_i, e + k > 0);
                         } else {
-                            for (int k = 0; 16 * k < left && 16 * k < p.rows_x; ++k) mma_bf16_ts(acc, A0 + 64 * (k >> 2) + 8 * (k & 3), dB + 128 * k, id_x, 1);
+#pragma unroll 1
+                            for (int k = 0; 64 * x + 16 * k < da; ++k) mma_bf16(acc, dA + 2 * k, dB + (values ? 2 * k : 128 * k), id_i, e + k > 0);
                         }
                         mma_commit(empty0 + 8 * ring.st);
                     }
                     __syncwarp();
+                    if (++x == na) x = 0;
                 }
-                if (leader) {
-                    mma_commit(x_done + 8 * u);
-                    if (j + 1 == cur.nblk) mma_commit(acc_done + 8 * ab);
-                }
+                if (leader) mma_commit(inter_done);
                 __syncwarp();
-                if (j + 1 == cur.nblk && p.nr == 1) next_item();
             }
-            ++items;
+            if (j == 0 && pj >= 0) {                      // the rows' operand before is used up
+                if (leader) mma_commit(rfree + 8 * rr.st);
+                __syncwarp();
+                rr.next(p.nr);
+            }
+#pragma unroll 1
+            for (int ph = 0; ph < 2; ++ph) {
+                if ((ph == 0) == x_first) {               // the product of the block before
+                    if (pj < 0) continue;
+                    const uint32_t n = blocks - 1, u = n & 1;
+                    if (pj == 0) wait(acc_ready, items & 1);
+                    wait(p_full + 8 * u, n >> 1 & 1);
+#pragma unroll 1
+                    for (int x = 0; x < p_rows; x += 64) {            // 64 tokens, 32 of their 64 columns
+                        if (x % p.rows_x == 0) wait(full0 + 8 * ring.st, ring.ph);
+                        const bool more = x + 64 < p_rows && (x + 64) % p.rows_x != 0;       // of the stage
+                        if (leader) {
+                            const uint64_t dB = mn_desc<128>(base + ring.st * p.stage, p.rows_x * 128) + x % p.rows_x * 8;
+                            const uint32_t A = tmem + scores + 128 * u + x;
+                            if (p_rows - x >= 64) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) mma_bf16_ts(acc, A + 8 * k, dB + 128 * k, id_x, 1);
+                            } else {
+#pragma unroll 1
+                                for (int k = 0; 16 * k < p_rows - x; ++k) mma_bf16_ts(acc, A + 8 * k, dB + 128 * k, id_x, 1);
+                            }
+                            if (!more) mma_commit(empty0 + 8 * ring.st);
+                        }
+                        __syncwarp();
+                        if (!more) ring.next(p.ring);
+                    }
+                    if (leader) {
+                        mma_commit(x_done + 8 * u);
+                        if (p_last) mma_commit(acc_done + 8 * ab);
+                    }
+                    __syncwarp();
+                } else if (!last) {                       // scores of it's block j
+                    const uint32_t u = blocks & 1, D = tmem + scores + 128 * u, id = idesc_bf16(128, (warp_uniform(it.col_rows(j)) + 15) & ~15);
+                    if (j == 0) wait(rfull + 8 * rr.st, rr.ph);
+                    if (blocks > 1) wait(x_done + 8 * u, (blocks >> 1 & 1) ^ 1);      // the scores before are used up
+                    const uint64_t dR = k_desc<128>(base + p.r + rr.st * r_bytes);
+#pragma unroll 1
+                    for (int x = 0; x < na; ++x) {
+                        if ((x & 1) == 0) wait(full0 + 8 * ring.st, ring.ph);
+                        const bool more = (x & 1) == 0 && x + 1 < na;
+                        if (leader) {
+                            const uint64_t dA = dR + (x * 2 * kBox >> 4), dB = k_desc<128>(base + ring.st * p.stage) + ((x & 1) * 2 * kBox >> 4);
+                            if (da - 64 * x >= 64) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) mma_bf16(D, dA + 2 * k, dB + 2 * k, id, x + k > 0);
+                            } else {
+#pragma unroll 1
+                                for (int k = 0; 64 * x + 16 * k < da; ++k) mma_bf16(D, dA + 2 * k, dB + 2 * k, id, x + k > 0);
+                            }
+                            if (!more) mma_commit(empty0 + 8 * ring.st);
+                        }
+                        __syncwarp();
+                        if (!more) ring.next(p.ring);
+                    }
+                    if (leader) mma_commit(s_full + 8 * u);
+                    __syncwarp();
+                }
+            }
+            if (pj >= 0 && p_last) ++items;
+            if (last) break;
+            ++blocks;
+            p_rows = warp_uniform(it.col_rows(j));
+            p_last = warp_uniform(j + 1 == it.nblk);
+            pj = j;
+            if (p_last) {
+                j = 0;
+                it.look(table, sh, slots, ds, dh);
+            } else {
+                ++j;
+            }
         }
         if (leader) {                                     // products in flight end before their TMEM is freed
             mma_commit(drain);
@@ -745,9 +755,8 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             g_blk[1] = gt[kGLo + c];
             g_blk[2] = keys ? 1.f : gt[kGBeta + c];
         };
-        bool more = it.seek(i, count, table, sh);
-        if (more) load_gates();
-        while (more) {
+        if (it.there) load_gates();
+        while (it.there) {
             const RowsItem<MODE> cur = it;
             const int rb = cur.rb, hk = cur.h / rep;
             const bool live = row < cur.row_n;
@@ -772,8 +781,8 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             const float mine = g_row[0], mine_lo = g_row[1], rf = g_row[2], sf = g_row[3];
             const float dm = (mine - g_row[4]) + (mine_lo - g_row[5]), qf = ex2(keys ? dm * -kLog2e : dm * kLog2e);
             const int nblk = cur.nblk;
-            i += gridDim.x;
-            more = it.seek(i, count, table, sh);
+            it.look(table, sh, slots, ds, dh);
+            const bool more = it.there;
             if (more) load_gates();
             named_sync(2, 256);
             const uint32_t acc = tmem + (two_sums ? 128 * (items & 1) : 0) + lanes;
@@ -785,18 +794,18 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll 1
-                for (int q = 0; q < 2; ++q) {             // 32 columns
-                    const int c0 = 64 * g + 32 * q, cq = 2 * g + q;
-                    uint32_t x[32], y[16];
-                    if (c0 >= ((n + 15) & ~15) || (cb == rb && (keys ? cq < w4 : cq > w4))) {
+                for (int q = 0; q < 4; ++q) {             // 16 columns
+                    const int c0 = 64 * g + 16 * q, cq = c0 >> 5;
+                    uint32_t x[16], y[8];
+                    if (c0 >= n || (cb == rb && (keys ? cq < w4 : cq > w4))) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) y[e] = 0;        // behind the segment, or masked altogether
+                        for (int e = 0; e < 8; ++e) y[e] = 0;         // behind the segment, or masked altogether
                     } else {
-                        tmem_ld_n(S + 32 * q, x);
+                        tmem_ld_n(S + 16 * q, x);
                         tmem_wait_ld();
                         if (cb == rb && cq == w4) {       // around the diagonal
 #pragma unroll
-                            for (int e0 = 0; e0 < 32; e0 += 4) {
+                            for (int e0 = 0; e0 < 16; e0 += 4) {
                                 const float4 h4 = *reinterpret_cast<const float4*>(G.hi + c0 + e0), f4 = *reinterpret_cast<const float4*>(G.beta + c0 + e0);
                                 const uint2 l2 = *reinterpret_cast<const uint2*>(G.lo + c0 + e0);
                                 const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, fs[4] = {f4.x, f4.y, f4.z, f4.w},
@@ -806,17 +815,17 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                                 for (int e = 0; e < 4; ++e) {
                                     const int col = c0 + e0 + e;
                                     const float d = (hs[e] - mine) + (ls[e] - mine_lo);
-                                    float f = ex2(keys ? d * kLog2e : d * -kLog2e);
-                                    if (!keys) f *= fs[e];
+                                    const float f = fs[e] * ex2(keys ? d * kLog2e : d * -kLog2e);
                                     x[e0 + e] = col < n && (keys ? col >= row : col <= row) ? __float_as_uint(f * __uint_as_float(x[e0 + e])) : 0u;
                                 }
                             }
                         } else {
                             const float* tab = cb == rb ? G.quarter[w4] + c0 : G.cf + cb * kBlk + c0;
-                            const float2 r2 = cb == rb ? make_float2(qf, qf) : make_float2(rf, rf);
+                            const float r1 = cb == rb ? qf : rf;
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
+                            for (int e = 0; e < 16; e += 4) {
                                 const float4 f = *reinterpret_cast<const float4*>(tab + e);
+                                const float2 r2 = make_float2(r1, r1);
                                 const float2 y0 = fmul2(fmul2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), r2), make_float2(f.x, f.y)),
                                              y1 = fmul2(fmul2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), r2), make_float2(f.z, f.w));
                                 x[e] = __float_as_uint(y0.x);
@@ -824,16 +833,16 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                                 x[e + 2] = __float_as_uint(y1.x);
                                 x[e + 3] = __float_as_uint(y1.y);
                             }
-                            if (n < kBlk) {
+                            if (c0 + 16 > n) {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
+                                for (int e = 0; e < 16; ++e)
                                     if (c0 + e >= n) x[e] = 0u;
                             }
                         }
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) y[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                        for (int e = 0; e < 8; ++e) y[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
                     }
-                    tmem_st_n(S + 16 * q, y);             // over columns that are read
+                    tmem_st_n(S + 8 * q, y);              // over columns that are read
                 }
                 tmem_wait_st();
                 if (j == 0) {                             // the state's product: its rows scaled
@@ -895,12 +904,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         }
     } else {
         const int w4 = warp & 3, row = 32 * w4 + lane;
-        const uint32_t lanes = (uint32_t)(32 * w4) << 16, mine = base + p.out + row * 128;
+        const uint32_t lanes = (uint32_t)(32 * w4) << 16;
         const bool shared = !values && rep > 1, whole = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
-        uint32_t items = 0;
-        while (it.seek(i, count, table, sh)) {
-            const uint32_t acc = tmem + (two_sums ? 128 * (items & 1) : 0) + lanes, ab = two_sums ? items & 1 : 0, ap = two_sums ? items >> 1 & 1 : items & 1;
-            const bool live = row < it.row_n, staged = false;
+        for (uint32_t items = 0; it.there; ++items, it.look(table, sh, slots, ds, dh)) {
+            const uint32_t ab = two_sums ? items & 1 : 0, ap = two_sums ? items >> 1 & 1 : items & 1, acc = tmem + 128 * ab + lanes;
+            const bool live = row < it.row_n;
             const size_t token = (size_t)it.first + it.rb * kBlk + row;
             const int head = values ? it.h : it.h / rep;
             const float of = keys ? ra.gates[((size_t)it.slot * sh.H + it.h) * kGAll + kGBeta + it.rb * kBlk + row] : 1.f;
@@ -909,66 +917,36 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             wait_or_dead(acc_done + 8 * ab, ap, a.err, dead);
             __syncwarp();
             tc_fence_after();
-            for (int x = 0; x < nx; ++x) {                // 64 columns
-                const int n16 = min(4, (dx - 64 * x) / 16);
-                uint32_t v[4][16];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (e < n16) tmem_ld_n(acc + 64 * x + 16 * e, v[e]);
+#pragma unroll 1
+            for (int c = 0; c < dx; c += 16) {
+                uint32_t v[16];
+                tmem_ld_n(acc + c, v);
                 tmem_wait_ld();
-                if (x + 1 == nx) {                        // the sum's place is free
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(acc_free + 8 * ab);
-                }
-                if (staged) {                             // what was there has left
-                    if (warp == 8 && lane == 0) bulk_read_done();
-                    named_sync(1, 128);
-                }
                 if (live) {
+                    float y[16];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (e < n16) {
-                            float y[16];
+                    for (int e = 0; e < 16; ++e) y[e] = of * __uint_as_float(v[e]);
+                    if (shared) {
+                        uint4 w[4];
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) y[c] = of * __uint_as_float(v[e][c]);
-                            if (shared) {
-                                uint4 w[4];
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = make_uint4(__float_as_uint(y[4 * e]), __float_as_uint(y[4 * e + 1]), __float_as_uint(y[4 * e + 2]), __float_as_uint(y[4 * e + 3]));
+                        stg_pieces<4>(o32 + c, w, false, true);
+                    } else {
+                        uint4 w[2];
 #pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    w[c] = make_uint4(__float_as_uint(y[4 * c]), __float_as_uint(y[4 * c + 1]), __float_as_uint(y[4 * c + 2]), __float_as_uint(y[4 * c + 3]));
-                                stg_pieces<4>(o32 + 64 * x + 16 * e, w, false, true);
-                            } else {
-                                uint4 w[2];
-#pragma unroll
-                                for (int c = 0; c < 2; ++c)
-                                    w[c] = make_uint4(pack_bf16(y[8 * c], y[8 * c + 1]), pack_bf16(y[8 * c + 2], y[8 * c + 3]),
-                                                      pack_bf16(y[8 * c + 4], y[8 * c + 5]), pack_bf16(y[8 * c + 6], y[8 * c + 7]));
-                                if (staged) {
-#pragma unroll
-                                    for (int c = 0; c < 2; ++c) st_shared16(mine + (((2 * e + c) ^ (row & 7)) << 4), w[c].x, w[c].y, w[c].z, w[c].w);
-                                } else {
-                                    stg_pieces<2>(o + 64 * x + 16 * e, w, false, whole);
-                                }
-                            }
-                        }
+                        for (int e = 0; e < 2; ++e)
+                            w[e] = make_uint4(pack_bf16(y[8 * e], y[8 * e + 1]), pack_bf16(y[8 * e + 2], y[8 * e + 3]), pack_bf16(y[8 * e + 4], y[8 * e + 5]),
+                                              pack_bf16(y[8 * e + 6], y[8 * e + 7]));
+                        stg_pieces<2>(o + c, w, false, whole);
+                    }
                 }
                 __syncwarp();
-                if (staged) {
-                    fence_proxy_async_smem();
-                    named_sync(1, 128);
-                    if (warp == 8 && lane == 0) {
-                        for (int y = 0; y < 2; ++y) tma_store_3d(&mo, base + p.out + y * kBox, 64 * x, head, it.first + it.rb * kBlk + 64 * y, false);
-                        bulk_commit();
-                    }
-                    __syncwarp();
-                }
             }
-            ++items;
-            i += gridDim.x;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_free + 8 * ab);
         }
-        if (warp == 8 && lane == 0) bulk_all_done();
-        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -1365,14 +1343,13 @@ RowsPlan rows_plan(int da, int dx) {
     const int na = (da + 63) / 64, nx = (dx + 63) / 64;
     p.rows_x = dx > 128 ? 64 : 128;
     p.stage = 2 * kBox * (na > 1 || nx > 1 ? 2 : 1);
-    const uint32_t r = na * 2 * kBox, rest = 2 * kBox + kRowTail;
+    const uint32_t r = na * 2 * kBox, rest = kRowTail;
     // two buffers of row operands where they leave the ring what two blocks' scores and X take
     p.nr = (int)((kSmemMost - rest - 2 * r) / p.stage) >= 2 * ((da + 127) / 128 + kBlk / p.rows_x) ? 2 : 1;
     const int room = (int)((kSmemMost - rest - p.nr * r) / p.stage);
     p.ring = room < kMaxRing ? room : kMaxRing;
     p.r = p.ring * p.stage;            // behind the ring
-    p.out = p.r + p.nr * r;
-    p.bars = p.out + 2 * kBox;
+    p.bars = p.r + p.nr * r;
     p.smem = p.bars + kRowTail;
     return p;
 }
@@ -1399,10 +1376,7 @@ cudaError_t rows_go(const CUtensorMap& ms, const SeqArgs& a, const float* gates,
     if (!slab_map(&mr, r.p, sh, r.d, r.heads, r.ld, kBlk, na) || !slab_map(&mb, b.p, sh, b.d, b.heads, b.ld, kBlk, na < 2 ? na : 2) ||
         !slab_map(&mx, x.p, sh, x.d, x.heads, x.ld, ra.p.rows_x, nx))
         return cudaErrorInvalidValue;
-    const int d = values ? sh.dv : sh.dk, out_heads = values ? sh.H : sh.Hk;
-    CUtensorMap mo;
-    if (!token_map(&mo, MODE == kOut ? a.out : MODE == kDq ? a.dq : MODE == kDk ? a.dk : a.dv, sh, d, out_heads, (long long)out_heads * d)) return cudaErrorInvalidValue;
-    return launch_kernel(lin_rows_tc_kernel<MODE>, grid, dim3(kRowThreads), ra.p.smem, st, true, mr, mb, mx, ms, mo, a, ra);
+    return launch_kernel(lin_rows_tc_kernel<MODE>, grid, dim3(kRowThreads), ra.p.smem, st, true, mr, mb, mx, ms, a, ra);
 }
 
 cudaError_t prep_go(const SeqArgs& a, float* gates, cudaStream_t st) {
