@@ -37,6 +37,26 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
+// A bounded wait with nothing called: around a call the compiler saves what a role holds, some 150 instructions a wait, and
+// these kernels' roles together have to stay within the instruction cache (70 KB of code ran at a third of its time behind
+// misses of it).  Gives up at once after any wait of the CTA has given up; `dead` null: by its own limit only.
+__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, int* err, volatile int* dead) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t n = 1; !mbar_test(bar, parity); ++n)
+        if ((n & 1023) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (n == 1024) t0 = now;
+            if (dead != nullptr && *dead) return false;
+            if (now - t0 > wait_limit_ns(err)) {
+                set_error(err, GDN_ERR_TIMEOUT);
+                if (dead != nullptr) *dead = 1;
+                return false;
+            }
+        }
+    return true;
+}
+
 // What the gates of a (slot, head) give, floats by token; g the sum of log decays from the segment's start to the token
 // and with it, G to the segment's end, b that from the block's start, B to the block's end.
 constexpr int kGCoef = 0,                    // beta e^{G - g}: what the token adds to the state at the segment's end
@@ -236,7 +256,7 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
                 const int na = (min(128, sh.dv - r0) + 63) / 64, nb = (min(128, sh.dk - c0) + 63) / 64;
                 for (int k = 0; ok && k < e.y; k += kLocalTok, ring.next(kLocalStages)) {
                     const uint32_t at = base + ring.st * kLocalStage, bar = full0 + 8 * ring.st;
-                    if (issued >= kLocalStages && !(ok = wait_or_dead(empty0 + 8 * ring.st, ring.ph ^ 1, a.err, dead))) break;
+                    if (issued >= kLocalStages && !(ok = wait_here(empty0 + 8 * ring.st, ring.ph ^ 1, a.err, dead))) break;
                     mbar_expect_tx(bar, (na + nb) * kBox + kLocalTok * 4);
                     bulk_copy_g2s(base + kLocalCoef + ring.st * kLocalTok * 4, gates + (size_t)s_h * kGAll + (BACK ? kGHead : kGCoef) + k, kLocalTok * 4, bar);
                     for (int x = 0; x < na; ++x) tma_3d(at + x * kBox, &ma, r0 + 64 * x, h, e.x + k, bar);
@@ -245,7 +265,7 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
                 }
             }
             if (*dead)                                    // copies in flight end before the CTA does
-                for (int j = max(0, issued - kLocalStages); j < issued; ++j) mbar_wait(full0 + 8 * (j % kLocalStages), (j / kLocalStages) & 1, a.err);
+                for (int j = max(0, issued - kLocalStages); j < issued; ++j) wait_here(full0 + 8 * (j % kLocalStages), (j / kLocalStages) & 1, a.err, nullptr);
         }
         __syncwarp();
     } else if (warp == 13) {
@@ -257,14 +277,14 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
             for (int k = 0; k < rows; k += kLocalTok, ring.next(kLocalStages), ++step) {
                 const uint32_t acc = tmem + 128 * (unit & 1);
                 const int at = k % kLocalHalf;
-                if (at == 0 && unit >= 2) wait_or_dead(acc_free + 8 * (unit & 1), (unit >> 1 & 1) ^ 1, a.err, dead);
-                wait_or_dead(full0 + 8 * ring.st, ring.ph, a.err, dead);
+                if (at == 0 && unit >= 2) wait_here(acc_free + 8 * (unit & 1), (unit >> 1 & 1) ^ 1, a.err, dead);
+                wait_here(full0 + 8 * ring.st, ring.ph, a.err, dead);
                 const uint64_t db = mn_desc<128>(base + ring.st * kLocalStage + 2 * kBox, kBox);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {             // 32 tokens
                     const int left = rows - k - 32 * b;
                     const uint32_t buf = 2 * b + (step & 1);
-                    wait_or_dead(a_full + 8 * buf, step >> 1 & 1, a.err, dead);
+                    wait_here(a_full + 8 * buf, step >> 1 & 1, a.err, dead);
                     __syncwarp();
                     tc_fence_after();
                     if (leader) {
@@ -289,7 +309,7 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
         }
         if (leader) {                                     // products in flight end before their TMEM is freed
             mma_commit(drain);
-            mbar_wait(drain, 0, a.err);
+            wait_here(drain, 0, a.err, nullptr);
         }
         __syncwarp();
     } else if (warp < 8) {
@@ -301,8 +321,8 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
             for (int k = 0; k < rows; k += kLocalTok, ring.next(kLocalStages), ++step) {
                 const int left = rows - k - 32 * g;
                 const uint32_t buf = 2 * g + (step & 1), A = tmem + kLocalA + buf * kLocalABuf + lanes;
-                wait_or_dead(full0 + 8 * ring.st, ring.ph, a.err, dead);
-                if (step >= 2) wait_or_dead(a_free + 8 * buf, (step >> 1 & 1) ^ 1, a.err, dead);
+                wait_here(full0 + 8 * ring.st, ring.ph, a.err, dead);
+                if (step >= 2) wait_here(a_free + 8 * buf, (step >> 1 & 1) ^ 1, a.err, dead);
                 __syncwarp();
                 tc_fence_after();
                 if (left > 0 && left < 32 && left % 16 != 0) {        // tokens of what lies behind: rows of zero, up to whole products
@@ -358,7 +378,7 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
                     if (warp == 8) bulk_all_done();
                     named_sync(1, 128);
                 }
-                wait_or_dead(acc_full + 8 * (unit & 1), unit >> 1 & 1, a.err, dead);
+                wait_here(acc_full + 8 * (unit & 1), unit >> 1 & 1, a.err, dead);
                 __syncwarp();
                 tc_fence_after();
                 for (int x = 0; x < n; x += 16) {         // four pieces of 16 bytes, in images of 32 columns, swizzled
@@ -418,7 +438,7 @@ enum { kOut, kDq, kDk, kDv };
 constexpr int kRowThreads = 448, kMaxRing = 8;
 
 struct RowsPlan {              // shared memory of a launch
-    int ring, rows_x, nr;      // stages; tokens of a stage of X; buffers of row operands
+    int ring, x_log, nr;       // stages; log2 of the tokens of a stage of X; buffers of row operands
     uint32_t stage, r, bars, smem;
 };
 
@@ -442,51 +462,51 @@ constexpr int kRowNBars = 2 * kMaxRing + 17;
 constexpr uint32_t kRowHolder = kRowNBars * 8, kRowGates = (kRowHolder + 8 + 15) / 16 * 16, kRowTail = kRowGates + 2 * sizeof(RowGates);
 static_assert(sizeof(RowGates) % 16 == 0, "read by 16 bytes");
 
-// A CTA's items one after another: number i of (slot, head, block).  Four neighbours are a segment's blocks (they read the
-// same tiles), in another order each turn of the grid, so that every CTA gets long and short ones.
+// The first of a CTA's items from number i on: (its number, slot, first token, rows + 1024 x its head of q and k), rows 0
+// where there is none left.
+// Four neighbours are a segment's blocks (they read the same tiles), in another order each turn of the grid, so that every
+// CTA gets long and short ones.  Called, not inlined: five roles look for items, and the instruction cache is small.
+__device__ __forceinline__ int rows_block(int i, bool keys) {
+    const int q = (i + i / (int)gridDim.x) & 3;
+    return keys ? q : 3 - q;
+}
+__device__ __noinline__ int4 rows_item(int i, const int2* table, int slots, int H, int rep, int total, bool keys) {
+#pragma unroll 1
+    for (;; i += gridDim.x) {
+        const int slot = (i >> 2) / H;
+        if (slot >= slots) return make_int4(i, slot, 0, 0);
+        const int2 e = slot_entry(table, slot, total);
+        if (rows_block(i, keys) * kBlk < e.y) return make_int4(i, slot, e.x, e.y + ((i >> 2) - slot * H) / rep * 1024);
+    }
+}
+// Rows of a stage of X that lie behind the sequence, up to whole products of 16: zero, since zero scores do not undo a NaN.
+__device__ __forceinline__ void zero_tail(uint32_t base, uint32_t full0, int ring, uint32_t stage_bytes, int stage, int rows, int from, int slabs, int* err,
+                                       volatile int* dead) {
+    const uint32_t st = stage % ring;
+    wait_here(full0 + 8 * st, (stage / ring) & 1, err, dead);
+    for (int e = threadIdx.x; e < slabs * (16 - (from & 15)) * 8; e += 256) {         // by rows of 8 pieces, slab after slab
+        const int r = e >> 3, x = r % slabs;
+        st_shared16(base + st * stage_bytes + x * rows * 128 + (from + r / slabs) * 128 + (e & 7) * 16, 0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+}
 template <int MODE>
 struct RowsItem {
-    int slot, h, turn, rb, first, rows, row_n, nblk;
-    bool there;
-    __device__ __forceinline__ void begin(const int2* table, const SeqShape& sh, int slots) {
-        slot = (int)(blockIdx.x >> 2) / sh.H;
-        h = (int)(blockIdx.x >> 2) % sh.H;
-        turn = 0;
-        look(table, sh, slots, 0, 0);
-    }
-    // On to the next that there is: grid / 4 (slot, head) on each time.
-    __device__ __forceinline__ void look(const int2* table, const SeqShape& sh, int slots, int ds, int dh) {
+    int i, slot, h, hk, rb, first, rows, row_n, nblk;
+    __device__ __forceinline__ void look(int from, const int2* table, const SeqShape& sh, int slots, int rep) {
         constexpr bool keys = MODE == kDk || MODE == kDv;
-        there = false;
-#pragma unroll 1
-        for (bool step = ds + dh > 0;; step = true) {
-            if (step) {
-                slot += ds;
-                h += dh;
-                if (h >= sh.H) {
-                    h -= sh.H;
-                    ++slot;
-                }
-                ++turn;
-            }
-            if (slot >= slots) return;
-            const int2 e = slot_entry(table, slot, sh.total);
-            const int q = ((blockIdx.x & 3) + turn) & 3;
-            rb = keys ? q : 3 - q;
-            if (rb * kBlk < e.y) {
-                first = e.x;
-                rows = e.y;
-                break;
-            }
-            if (ds + dh == 0) {
-                ds = (int)(gridDim.x >> 2) / sh.H;
-                dh = (int)(gridDim.x >> 2) % sh.H;
-            }
-        }
-        there = true;
+        const int4 e = rows_item(from, table, slots, sh.H, rep, sh.total, keys);
+        i = e.x;
+        slot = e.y;
+        first = e.z;
+        rows = e.w & 1023;
+        hk = e.w >> 10;
+        h = (i >> 2) - slot * sh.H;
+        rb = rows_block(i, keys);
         row_n = min(kBlk, rows - rb * kBlk);
         nblk = keys ? (rows - 1) / kBlk - rb + 1 : rb + 1;       // blocks of columns: rb .. last, or 0 .. rb
     }
+    __device__ __forceinline__ bool there() const { return rows > 0; }
     __device__ __forceinline__ int col_block(int j) const { return MODE == kDk || MODE == kDv ? rb + j : j; }
     __device__ __forceinline__ int col_rows(int j) const { return min(kBlk, rows - col_block(j) * kBlk); }
 };
@@ -504,7 +524,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     void* out = MODE == kOut ? a.out : MODE == kDq ? a.dq : MODE == kDk ? a.dk : a.dv;
     const int rep = sh.H / sh.Hk, out_heads = values ? sh.H : sh.Hk;
     const int da = values ? sh.dk : sh.dv, dx = values ? sh.dv : sh.dk;
-    const int slots = seg_slots(sh.nseq, sh.total, kSeg), ds = (int)(gridDim.x >> 2) / sh.H, dh = (int)(gridDim.x >> 2) % sh.H;
+    const int slots = seg_slots(sh.nseq, sh.total, kSeg);
     const int2* table = slot_table(ra.gates, slots, sh.H);
     const uint32_t base = smem_u32(sm), bars = base + p.bars;
     const uint32_t full0 = bars, empty0 = bars + 8 * kMaxRing, rfull = bars + 16 * kMaxRing, rfree = rfull + 16, acc_free = rfull + 32, acc_done = rfull + 48,
@@ -515,8 +535,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     const int na = (da + 63) / 64, nb = (da + 127) / 128, nx = (dx + 63) / 64, n_inter = ra.terms * na;
     const int two_sums = dx <= 128;                       // sums in TMEM, less one; the second 128 columns on
     const uint32_t r_bytes = na * 2 * kBox;
+    const int rows_x = 1 << p.x_log;
     if (tid == 0) {
-        init_barriers(bars, kRowNBars, [&](uint32_t b) { return (b >= p_full && b < x_done) || b == acc_ready ? 8u : b >= acc_free && b < acc_done ? 4u : 1u; });
+#pragma unroll 1
+        for (uint32_t b = bars; b < bars + 8 * kRowNBars; b += 8)
+            mbar_init(b, (b >= p_full && b < x_done) || b == acc_ready ? 8u : b >= acc_free && b < acc_done ? 4u : 1u);
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -534,15 +557,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     // block before the product of the one before it, the state's product behind the first scores of its rows.  With one
     // buffer of row operands an item's first scores come behind the last product of the item before.
     RowsItem<MODE> it;
-    it.begin(table, sh, slots);
+    it.look(blockIdx.x, table, sh, slots, rep);
     if (warp == 12) {
         if (elect_one()) {
-            // `rows` tokens of slabs x0, x0 + 1, .. (64 columns each): those beyond the sequence's are read and never used
-            const auto load = [&](uint32_t dst, const CUtensorMap* m, bool whole, int head, int t0, int x0, int nslab, int rows, uint32_t bar) {
-                if (whole) tma_4d(dst, m, 0, head, t0, x0, bar);
-                else
-                    for (int x = 0; x < nslab; ++x) tma_4d(dst + x * rows * 128, m, 64 * (x0 + x), head, t0, 0, bar);
-            };
             const bool whole_a = da % 64 == 0, whole_x = dx % 64 == 0;
             const size_t apart = (size_t)slots * sh.H;
             Ring ring, rr;
@@ -551,52 +568,59 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             RowsItem<MODE> prev;
             bool last = false;
             for (int j = 0, pj = -1; ok && !last;) {          // it's block j; the block before it, prev's pj
-                last = !it.there;
+                last = !it.there();
                 const bool x_first = last || (j == 0 && p.nr == 1);
-                const int n0 = pj == 0 ? n_inter : 0, nxt = pj >= 0 ? (prev.col_rows(pj) + p.rows_x - 1) / p.rows_x : 0, ns = last ? 0 : nb;
+                const int n0 = pj == 0 ? n_inter : 0, nxt = pj >= 0 ? (prev.col_rows(pj) + rows_x - 1) >> p.x_log : 0, ns = last ? 0 : nb;
+                // the state's stages, then scores' and X's in their order; the rows' own operand before its first scores (e
+                // stays where it is)
+                bool row_op = j == 0 && !last;
 #pragma unroll 1
-                for (int e = 0; ok && e < n0 + ns + nxt; ++e) {
-                    // which: the state's stages, then scores' and X's in their order
+                for (int e = 0; e < n0 + ns + nxt;) {
                     const int w = e - n0, s_at = x_first ? w - nxt : w, x_at = x_first ? w : w - ns;
-                    const bool state = e < n0, score = !state && s_at >= 0 && s_at < ns;
-                    if (score && j == 0 && s_at == 0) {
-                        if (r_issued >= p.nr && !(ok = wait_or_dead(rfree + 8 * rr.st, rr.ph ^ 1, a.err, dead))) break;
-                        mbar_expect_tx(rfull + 8 * rr.st, r_bytes);
-                        load(base + p.r + rr.st * r_bytes, &mr, whole_a, values ? it.h / rep : it.h, it.first + it.rb * kBlk, 0, na, kBlk, rfull + 8 * rr.st);
+                    const bool state = e < n0, score = !state && s_at >= 0 && s_at < ns, r = score && row_op;
+                    const uint32_t st = r ? rr.st : ring.st, ph = (r ? rr.ph : ring.ph) ^ 1, bar = (r ? rfull : full0) + 8 * st, dst = base + (r ? p.r + st * r_bytes : st * p.stage);
+                    if ((r ? r_issued >= p.nr : issued >= p.ring) && !(ok = wait_here((r ? rfree : empty0) + 8 * st, ph, a.err, dead))) break;
+                    // boxes of 64 columns (all of them in one where the map has whole boxes: slabs behind the last come as zeros);
+                    // tokens that they hold beyond the sequence's are read and never used
+                    const bool one = state ? values : score ? whole_a : whole_x;
+                    const int slabs = state || !score ? nx : r ? na : whole_a ? min(2, na) : min(2, na - 2 * s_at), rows = state ? 64 : score ? kBlk : rows_x;
+                    mbar_expect_tx(bar, state && values ? dx * 128 : slabs * rows * 128);
+                    const CUtensorMap* m = state ? &ms : r ? &mr : score ? &mb : &mx;
+                    const int head = score ? (values ? it.hk : it.h) : values ? prev.h : prev.hk;
+                    const int t0 = r ? it.first + it.rb * kBlk
+                                     : score ? it.first + it.col_block(j) * kBlk : prev.first + prev.col_block(pj) * kBlk + x_at * rows_x;
+                    const int x0 = score && !r ? 2 * s_at : 0;
+                    // the state's, small terms first: rows of d_v by 64 of d_k along the row, or 64 rows of d_v by d_k
+                    const int sx = e % na, sz = (int)((ra.terms - 1 - e / na) * apart + (size_t)prev.slot * sh.H + prev.h);
+#pragma unroll 1
+                    for (int x = 0; x < (one ? 1 : slabs); ++x) {
+                        const uint32_t to = dst + x * rows * 128;
+                        if (state) tma_3d(to, m, values ? 64 * sx : 64 * x, values ? 0 : 64 * sx, sz, bar);
+                        else tma_4d(to, m, one ? 0 : 64 * (x0 + x), head, t0, one ? x0 : 0, bar);
+                    }
+                    if (r) {
                         rr.next(p.nr);
                         ++r_issued;
-                    }
-                    if (issued >= p.ring && !(ok = wait_or_dead(empty0 + 8 * ring.st, ring.ph ^ 1, a.err, dead))) break;
-                    const uint32_t dst = base + ring.st * p.stage, bar = full0 + 8 * ring.st;
-                    if (state) {                              // the small terms first
-                        const int x = e % na, z = (int)((ra.terms - 1 - e / na) * apart + (size_t)prev.slot * sh.H + prev.h);
-                        mbar_expect_tx(bar, values ? dx * 128 : nx * kBox);
-                        if (values)                           // rows of d_v, 64 of d_k along the row
-                            tma_3d(dst, &ms, 64 * x, 0, z, bar);
-                        else                                  // 64 rows of d_v, d_k along the row
-                            for (int y = 0; y < nx; ++y) tma_3d(dst + y * kBox, &ms, 64 * y, 64 * x, z, bar);
+                        row_op = false;
                     } else {
-                        // of a whole box of score operands those slabs behind the last come as zeros
-                        const int slabs = !score ? nx : whole_a ? min(2, na) : min(2, na - 2 * s_at), rows = score ? kBlk : p.rows_x;
-                        const int head = score ? (values ? it.h / rep : it.h) : values ? prev.h : prev.h / rep;
-                        const int t0 = score ? it.first + it.col_block(j) * kBlk : prev.first + prev.col_block(pj) * kBlk + x_at * p.rows_x;
-                        mbar_expect_tx(bar, slabs * rows * 128);
-                        load(dst, score ? &mb : &mx, score ? whole_a : whole_x, head, t0, score ? 2 * s_at : 0, slabs, rows, bar);
+                        ring.next(p.ring);
+                        ++issued;
+                        ++e;
                     }
-                    ring.next(p.ring);
-                    ++issued;
                 }
                 if (last) break;
                 prev = it;
                 pj = j;
                 if (++j == it.nblk) {
                     j = 0;
-                    it.look(table, sh, slots, ds, dh);
+                    it.look(it.i + gridDim.x, table, sh, slots, rep);
                 }
             }
             if (*dead) {                                  // copies in flight end before the CTA does
-                for (int j = max(0, r_issued - p.nr); j < r_issued; ++j) mbar_wait(rfull + 8 * (j % p.nr), (j / p.nr) & 1, a.err);
-                for (int j = max(0, issued - p.ring); j < issued; ++j) mbar_wait(full0 + 8 * (j % p.ring), (j / p.ring) & 1, a.err);
+#pragma unroll 1
+                for (int j = max(0, r_issued - p.nr); j < r_issued; ++j) wait_here(rfull + 8 * (j % p.nr), (j / p.nr) & 1, a.err, nullptr);
+#pragma unroll 1
+                for (int j = max(0, issued - p.ring); j < issued; ++j) wait_here(full0 + 8 * (j % p.ring), (j / p.ring) & 1, a.err, nullptr);
             }
         }
         __syncwarp();
@@ -604,7 +628,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         const bool leader = elect_one();
         Ring ring, rr;
         const auto wait = [&](uint32_t bar, uint32_t parity) {
-            wait_or_dead(bar, parity, a.err, dead);
+            wait_here(bar, parity, a.err, dead);
             __syncwarp();
             tc_fence_after();
         };
@@ -613,7 +637,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         int p_rows = 0;                                   // tokens of the block of columns before
         bool p_last = false;
         for (int j = 0, pj = -1;;) {
-            const bool last = !warp_uniform(it.there);
+            const bool last = !warp_uniform(it.there());
             const bool x_first = last || (j == 0 && p.nr == 1);
             const uint32_t ab = two_sums ? items & 1 : 0, ap = two_sums ? items >> 1 & 1 : items & 1, acc = tmem + 128 * ab;
             if (pj == 0) {
@@ -625,13 +649,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                     if (leader) {
                         const uint32_t sb = base + ring.st * p.stage;
                         const uint64_t dA = dR + (x * 2 * kBox >> 4), dB = values ? k_desc<128>(sb) : mn_desc<128>(sb, kBox);
-                        if (da - 64 * x >= 64) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) mma_bf16(acc, dA + 2 * k, dB + (values ? 2 * k : 128 * k), id_i, e + k > 0);
-                        } else {
-#pragma unroll 1
-                            for (int k = 0; 64 * x + 16 * k < da; ++k) mma_bf16(acc, dA + 2 * k, dB + (values ? 2 * k : 128 * k), id_i, e + k > 0);
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            if (64 * x + 16 * k < da) mma_bf16(acc, dA + 2 * k, dB + (values ? 2 * k : 128 * k), id_i, e + k > 0);
                         mma_commit(empty0 + 8 * ring.st);
                     }
                     __syncwarp();
@@ -654,18 +674,14 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                     wait(p_full + 8 * u, n >> 1 & 1);
 #pragma unroll 1
                     for (int x = 0; x < p_rows; x += 64) {            // 64 tokens, 32 of their 64 columns
-                        if (x % p.rows_x == 0) wait(full0 + 8 * ring.st, ring.ph);
-                        const bool more = x + 64 < p_rows && (x + 64) % p.rows_x != 0;       // of the stage
+                        if ((x & rows_x - 1) == 0) wait(full0 + 8 * ring.st, ring.ph);
+                        const bool more = x + 64 < p_rows && (x + 64 & rows_x - 1) != 0;       // of the stage
                         if (leader) {
-                            const uint64_t dB = mn_desc<128>(base + ring.st * p.stage, p.rows_x * 128) + x % p.rows_x * 8;
+                            const uint64_t dB = mn_desc<128>(base + ring.st * p.stage, rows_x * 128) + (x & rows_x - 1) * 8;
                             const uint32_t A = tmem + scores + 128 * u + x;
-                            if (p_rows - x >= 64) {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) mma_bf16_ts(acc, A + 8 * k, dB + 128 * k, id_x, 1);
-                            } else {
-#pragma unroll 1
-                                for (int k = 0; 16 * k < p_rows - x; ++k) mma_bf16_ts(acc, A + 8 * k, dB + 128 * k, id_x, 1);
-                            }
+                            for (int k = 0; k < 4; ++k)
+                                if (x + 16 * k < p_rows) mma_bf16_ts(acc, A + 8 * k, dB + 128 * k, id_x, 1);
                             if (!more) mma_commit(empty0 + 8 * ring.st);
                         }
                         __syncwarp();
@@ -687,13 +703,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                         const bool more = (x & 1) == 0 && x + 1 < na;
                         if (leader) {
                             const uint64_t dA = dR + (x * 2 * kBox >> 4), dB = k_desc<128>(base + ring.st * p.stage) + ((x & 1) * 2 * kBox >> 4);
-                            if (da - 64 * x >= 64) {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) mma_bf16(D, dA + 2 * k, dB + 2 * k, id, x + k > 0);
-                            } else {
-#pragma unroll 1
-                                for (int k = 0; 64 * x + 16 * k < da; ++k) mma_bf16(D, dA + 2 * k, dB + 2 * k, id, x + k > 0);
-                            }
+                            for (int k = 0; k < 4; ++k)
+                                if (64 * x + 16 * k < da) mma_bf16(D, dA + 2 * k, dB + 2 * k, id, x + k > 0);
                             if (!more) mma_commit(empty0 + 8 * ring.st);
                         }
                         __syncwarp();
@@ -711,14 +723,14 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             pj = j;
             if (p_last) {
                 j = 0;
-                it.look(table, sh, slots, ds, dh);
+                it.look(it.i + gridDim.x, table, sh, slots, rep);
             } else {
                 ++j;
             }
         }
         if (leader) {                                     // products in flight end before their TMEM is freed
             mma_commit(drain);
-            mbar_wait(drain, 0, a.err);
+            wait_here(drain, 0, a.err, nullptr);
         }
         __syncwarp();
     } else if (warp < 8) {
@@ -755,42 +767,56 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             g_blk[1] = gt[kGLo + c];
             g_blk[2] = keys ? 1.f : gt[kGBeta + c];
         };
-        if (it.there) load_gates();
-        while (it.there) {
-            const RowsItem<MODE> cur = it;
-            const int rb = cur.rb, hk = cur.h / rep;
+        // An item's gates are loaded while the one before is worked on; the loads stand in one place, so the first turn has
+        // nothing else.
+        RowsItem<MODE> cur = it;
+        float mine = 0.f, mine_lo = 0.f, rf = 0.f, sf = 0.f, qf = 0.f;
+#pragma unroll 1
+        for (bool have = false;;) {
+            RowGates& G = gates[items & 1];
+            if (have) {
+                cur = it;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = tid + 256 * e, b = t / kBlk, w = 2 * (tid >> 7) + e;
+                    float f = keys ? g_col[e][0] : g_col[e][0] * g_col[e][1];
+#pragma unroll
+                    for (int m = 1; m < 3; ++m)           // blocks between
+                        if (m > min(b, cur.rb) && m < max(b, cur.rb)) f *= g_tot[m];
+                    G.cf[t] = f;
+                    const float d = (g_m[e][0] - g_blk[0]) + (g_m[e][1] - g_blk[1]);
+                    G.quarter[w][tid & 127] = g_blk[2] * ex2(keys ? d * -kLog2e : d * kLog2e);
+                }
+                if (tid < kBlk) {
+                    G.beta[tid] = g_blk[2];
+                    G.hi[tid] = g_blk[0];
+                    G.lo[tid] = __float2bfloat16_rn(g_blk[1]);
+                }
+                mine = g_row[0];
+                mine_lo = g_row[1];
+                rf = g_row[2];
+                sf = g_row[3];
+                const float dm = (mine - g_row[4]) + (mine_lo - g_row[5]);
+                qf = ex2(keys ? dm * -kLog2e : dm * kLog2e);
+                it.look(it.i + gridDim.x, table, sh, slots, rep);
+            }
+            const bool more = it.there();
+            if (more) load_gates();
+            if (!have) {
+                if (!more) break;
+                have = true;
+                continue;
+            }
+            const int rb = cur.rb, hk = cur.hk, nblk = cur.nblk;
             const bool live = row < cur.row_n;
             const size_t token = (size_t)cur.first + rb * kBlk + row, at = (size_t)cur.slot * sh.H + cur.h;
-            RowGates& G = gates[items & 1];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int t = tid + 256 * e, b = t / kBlk, w = 2 * (tid >> 7) + e;
-                float f = keys ? g_col[e][0] : g_col[e][0] * g_col[e][1];
-#pragma unroll
-                for (int m = 1; m < 3; ++m)               // blocks between
-                    if (m > min(b, rb) && m < max(b, rb)) f *= g_tot[m];
-                G.cf[t] = f;
-                const float d = (g_m[e][0] - g_blk[0]) + (g_m[e][1] - g_blk[1]);
-                G.quarter[w][tid & 127] = g_blk[2] * ex2(keys ? d * -kLog2e : d * kLog2e);
-            }
-            if (tid < kBlk) {
-                G.beta[tid] = g_blk[2];
-                G.hi[tid] = g_blk[0];
-                G.lo[tid] = __float2bfloat16_rn(g_blk[1]);
-            }
-            const float mine = g_row[0], mine_lo = g_row[1], rf = g_row[2], sf = g_row[3];
-            const float dm = (mine - g_row[4]) + (mine_lo - g_row[5]), qf = ex2(keys ? dm * -kLog2e : dm * kLog2e);
-            const int nblk = cur.nblk;
-            it.look(table, sh, slots, ds, dh);
-            const bool more = it.there;
-            if (more) load_gates();
             named_sync(2, 256);
             const uint32_t acc = tmem + (two_sums ? 128 * (items & 1) : 0) + lanes;
             for (int j = 0; j < nblk; ++j, ++blocks) {
                 const uint32_t u = blocks & 1;
                 const int cb = cur.col_block(j), n = cur.col_rows(j);
                 const uint32_t S = tmem + lanes + scores + 128 * u + 64 * g;
-                wait_or_dead(s_full + 8 * u, blocks >> 1 & 1, a.err, dead);
+                wait_here(s_full + 8 * u, blocks >> 1 & 1, a.err, dead);
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll 1
@@ -846,7 +872,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                 }
                 tmem_wait_st();
                 if (j == 0) {                             // the state's product: its rows scaled
-                    wait_or_dead(inter_done, items & 1, a.err, dead);
+                    wait_here(inter_done, items & 1, a.err, dead);
                     __syncwarp();
                     tc_fence_after();
                     const __nv_bfloat16* z = MODE == kDq ? static_cast<const __nv_bfloat16*>(a.q) + token * sh.ldq + (size_t)hk * sh.dk
@@ -888,33 +914,30 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                 if (j + 1 < nblk || (p.nr > 1 && more)) stages += nb;
                 if (n % 16 != 0) {                        // X's tokens of what lies behind: rows of zero, up to whole products
                     // not before what was in X's stage is used up: the state's terms, or the X before
-                    if (j > 0) wait_or_dead(x_done + 8 * (u ^ 1), (blocks - 1) >> 1 & 1, a.err, dead);
-                    const int stage = stages + (n - 1) / p.rows_x, at_row = n % p.rows_x, cnt = 16 - n % 16, pieces = nx * 8;
-                    wait_or_dead(full0 + 8 * (stage % p.ring), (stage / p.ring) & 1, a.err, dead);
-                    for (int e = tid; e < cnt * pieces; e += 256)
-                        st_shared16(base + stage % p.ring * p.stage + (e % pieces >> 3) * p.rows_x * 128 + (at_row + e / pieces) * 128 + (e & 7) * 16, 0, 0, 0, 0);
-                    fence_proxy_async_smem();
+                    if (j > 0) wait_here(x_done + 8 * (u ^ 1), (blocks - 1) >> 1 & 1, a.err, dead);
+                    zero_tail(base, full0, p.ring, p.stage, stages + (n - 1 >> p.x_log), rows_x, n & rows_x - 1, nx, a.err, dead);
                 }
-                stages += (n + p.rows_x - 1) / p.rows_x + (j + 1 == nblk && p.nr == 1 ? nb : 0);
+                stages += (n + rows_x - 1 >> p.x_log) + (j + 1 == nblk && p.nr == 1 ? nb : 0);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * u);
             }
             ++items;
+            if (!more) break;
         }
     } else {
         const int w4 = warp & 3, row = 32 * w4 + lane;
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
         const bool shared = !values && rep > 1, whole = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
-        for (uint32_t items = 0; it.there; ++items, it.look(table, sh, slots, ds, dh)) {
+        for (uint32_t items = 0; it.there(); ++items, it.look(it.i + gridDim.x, table, sh, slots, rep)) {
             const uint32_t ab = two_sums ? items & 1 : 0, ap = two_sums ? items >> 1 & 1 : items & 1, acc = tmem + 128 * ab + lanes;
             const bool live = row < it.row_n;
             const size_t token = (size_t)it.first + it.rb * kBlk + row;
-            const int head = values ? it.h : it.h / rep;
+            const int head = values ? it.h : it.hk;
             const float of = keys ? ra.gates[((size_t)it.slot * sh.H + it.h) * kGAll + kGBeta + it.rb * kBlk + row] : 1.f;
             __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + token * out_heads * dx + (size_t)head * dx;
             float* o32 = shared ? ra.heads + (token * sh.H + it.h) * dx : nullptr;
-            wait_or_dead(acc_done + 8 * ab, ap, a.err, dead);
+            wait_here(acc_done + 8 * ab, ap, a.err, dead);
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
@@ -1037,15 +1060,15 @@ __global__ void __launch_bounds__(kPairThreads, 2)
             for (int j = 0; ok && j <= rb; ++j)
                 for (int x = 0; ok && x < nk + nv; ++x) {
                     const int st = it % p.ring;
-                    if (it >= p.ring && !(ok = wait_or_dead(empty0 + 8 * st, (it / p.ring + 1) & 1, a.err, dead))) break;
+                    if (it >= p.ring && !(ok = wait_here(empty0 + 8 * st, (it / p.ring + 1) & 1, a.err, dead))) break;
                     mbar_expect_tx(full0 + 8 * st, (col_rows(j) > 64 ? 2 : 1) * kBox);
                     if (x < nk) slab(base + p.stages + st * 2 * kBox, &mk, x, hk, first + j * kBlk, col_rows(j), full0 + 8 * st);
                     else slab(base + p.stages + st * 2 * kBox, &mv, x - nk, h, first + j * kBlk, col_rows(j), full0 + 8 * st);
                     ++it;
                 }
             if (*dead) {                                  // copies in flight end before the CTA does
-                mbar_wait(rfull, 0, a.err);
-                for (int j = max(0, it - p.ring); j < it; ++j) mbar_wait(full0 + 8 * (j % p.ring), (j / p.ring) & 1, a.err);
+                wait_here(rfull, 0, a.err, nullptr);
+                for (int j = max(0, it - p.ring); j < it; ++j) wait_here(full0 + 8 * (j % p.ring), (j / p.ring) & 1, a.err, nullptr);
             }
         }
         __syncwarp();
@@ -1053,7 +1076,7 @@ __global__ void __launch_bounds__(kPairThreads, 2)
         const bool leader = elect_one();
         Ring ring;
         const auto wait = [&](uint32_t bar, uint32_t parity) {
-            wait_or_dead(bar, parity, a.err, dead);
+            wait_here(bar, parity, a.err, dead);
             __syncwarp();
             tc_fence_after();
         };
@@ -1087,7 +1110,7 @@ __global__ void __launch_bounds__(kPairThreads, 2)
         }
         if (leader) {
             mma_commit(done);                             // and products in flight end before their TMEM is freed
-            mbar_wait(done, 0, a.err);
+            wait_here(done, 0, a.err, nullptr);
         }
         __syncwarp();
     } else {
@@ -1114,7 +1137,7 @@ __global__ void __launch_bounds__(kPairThreads, 2)
         float sum = 0.f, diag = 0.f;
         for (int j = 0; j <= rb; ++j) {
             const int u = j % G, n = col_rows(j);
-            wait_or_dead(s_full + 8 * u, (j / G) & 1, a.err, dead);
+            wait_here(s_full + 8 * u, (j / G) & 1, a.err, dead);
             __syncwarp();
             tc_fence_after();
             float* cj = col + (j & 1) * 4 * kBlk + w4 * kBlk;
@@ -1341,11 +1364,11 @@ constexpr uint32_t kSmemMost = 227 * 1024, kSmemHalf = 113 * 1024;      // one C
 RowsPlan rows_plan(int da, int dx) {
     RowsPlan p = {};
     const int na = (da + 63) / 64, nx = (dx + 63) / 64;
-    p.rows_x = dx > 128 ? 64 : 128;
+    p.x_log = dx > 128 ? 6 : 7;
     p.stage = 2 * kBox * (na > 1 || nx > 1 ? 2 : 1);
     const uint32_t r = na * 2 * kBox, rest = kRowTail;
     // two buffers of row operands where they leave the ring what two blocks' scores and X take
-    p.nr = (int)((kSmemMost - rest - 2 * r) / p.stage) >= 2 * ((da + 127) / 128 + kBlk / p.rows_x) ? 2 : 1;
+    p.nr = (int)((kSmemMost - rest - 2 * r) / p.stage) >= 2 * ((da + 127) / 128 + (kBlk >> p.x_log)) ? 2 : 1;
     const int room = (int)((kSmemMost - rest - p.nr * r) / p.stage);
     p.ring = room < kMaxRing ? room : kMaxRing;
     p.r = p.ring * p.stage;            // behind the ring
@@ -1374,7 +1397,7 @@ cudaError_t rows_go(const CUtensorMap& ms, const SeqArgs& a, const float* gates,
     const int na = (r.d + 63) / 64, nx = (x.d + 63) / 64;
     CUtensorMap mr, mb, mx;
     if (!slab_map(&mr, r.p, sh, r.d, r.heads, r.ld, kBlk, na) || !slab_map(&mb, b.p, sh, b.d, b.heads, b.ld, kBlk, na < 2 ? na : 2) ||
-        !slab_map(&mx, x.p, sh, x.d, x.heads, x.ld, ra.p.rows_x, nx))
+        !slab_map(&mx, x.p, sh, x.d, x.heads, x.ld, 1 << ra.p.x_log, nx))
         return cudaErrorInvalidValue;
     return launch_kernel(lin_rows_tc_kernel<MODE>, grid, dim3(kRowThreads), ra.p.smem, st, true, mr, mb, mx, ms, a, ra);
 }
