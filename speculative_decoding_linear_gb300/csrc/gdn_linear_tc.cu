@@ -139,6 +139,9 @@ __device__ __forceinline__ float ex2(float x) {      // 2^x, to 2^-22 of it; bel
 }
 constexpr float kLog2e = 1.44269504f;
 
+__device__ __forceinline__ void tmem_st_n(uint32_t t, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
 __device__ __forceinline__ void tmem_st_n(uint32_t t, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
                  "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -479,17 +482,6 @@ __device__ __noinline__ int4 rows_item(int i, const int2* table, int slots, int 
         if (rows_block(i, keys) * kBlk < e.y) return make_int4(i, slot, e.x, e.y + ((i >> 2) - slot * H) / rep * 1024);
     }
 }
-// Rows of a stage of X that lie behind the sequence, up to whole products of 16: zero, since zero scores do not undo a NaN.
-__device__ __forceinline__ void zero_tail(uint32_t base, uint32_t full0, int ring, uint32_t stage_bytes, int stage, int rows, int from, int slabs, int* err,
-                                       volatile int* dead) {
-    const uint32_t st = stage % ring;
-    wait_here(full0 + 8 * st, (stage / ring) & 1, err, dead);
-    for (int e = threadIdx.x; e < slabs * (16 - (from & 15)) * 8; e += 256) {         // by rows of 8 pieces, slab after slab
-        const int r = e >> 3, x = r % slabs;
-        st_shared16(base + st * stage_bytes + x * rows * 128 + (from + r / slabs) * 128 + (e & 7) * 16, 0, 0, 0, 0);
-    }
-    fence_proxy_async_smem();
-}
 template <int MODE>
 struct RowsItem {
     int i, slot, h, hk, rb, first, rows, row_n, nblk;
@@ -739,7 +731,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         const int chunks = dx / 16, ch0 = g == 0 ? 0 : (chunks + 1) / 2, ch1 = g == 0 ? (chunks + 1) / 2 : chunks;      // of 16 columns
         RowGates* gates = reinterpret_cast<RowGates*>(tail + kRowGates);
         uint32_t items = 0, blocks = 0;
-        int stages = nb;                                  // of the ring, up to this block's next scores'
+        int at_stage = nb, stage_ph = 0;                  // of the ring, behind this block's scores, and their turn's parity
+        const auto turn = [&]() {
+#pragma unroll 1
+            for (; at_stage >= p.ring; at_stage -= p.ring) stage_ph ^= 1;
+        };
         // an item's gates on their way: its row's, two columns', the blocks', block rb's
         float g_row[6], g_col[2][2], g_tot[4], g_blk[3], g_m[2][2];
         const auto load_gates = [&]() {
@@ -822,6 +818,34 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {             // 16 columns
                     const int c0 = 64 * g + 16 * q, cq = c0 >> 5;
+                    if (cb == rb && cq == w4 && c0 < n) { // around the diagonal
+#pragma unroll 1
+                        for (int e0 = 0; e0 < 16; e0 += 8) {
+                            uint32_t x[8], y[4];
+                            tmem_ld_n(S + 16 * q + e0, x);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e1 = 0; e1 < 8; e1 += 4) {
+                                const int at4 = c0 + e0 + e1;
+                                const float4 h4 = *reinterpret_cast<const float4*>(G.hi + at4), f4 = *reinterpret_cast<const float4*>(G.beta + at4);
+                                const uint2 l2 = *reinterpret_cast<const uint2*>(G.lo + at4);
+                                const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, fs[4] = {f4.x, f4.y, f4.z, f4.w},
+                                            ls[4] = {__uint_as_float(l2.x << 16), __uint_as_float(l2.x & 0xffff0000u), __uint_as_float(l2.y << 16),
+                                                     __uint_as_float(l2.y & 0xffff0000u)};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int col = at4 + e;
+                                    const float d = (hs[e] - mine) + (ls[e] - mine_lo);
+                                    const float f = fs[e] * ex2(keys ? d * kLog2e : d * -kLog2e);
+                                    x[e1 + e] = col < n && (keys ? col >= row : col <= row) ? __float_as_uint(f * __uint_as_float(x[e1 + e])) : 0u;
+                                }
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) y[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                            tmem_st_n(S + 8 * q + e0 / 2, y);         // over columns that are read
+                        }
+                        continue;
+                    }
                     uint32_t x[16], y[8];
                     if (c0 >= n || (cb == rb && (keys ? cq < w4 : cq > w4))) {
 #pragma unroll
@@ -829,46 +853,23 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                     } else {
                         tmem_ld_n(S + 16 * q, x);
                         tmem_wait_ld();
-                        if (cb == rb && cq == w4) {       // around the diagonal
+                        const float* tab = cb == rb ? G.quarter[w4] + c0 : G.cf + cb * kBlk + c0;
+                        const float r1 = cb == rb ? qf : rf;
+                        const float2 r2 = make_float2(r1, r1);
 #pragma unroll
-                            for (int e0 = 0; e0 < 16; e0 += 4) {
-                                const float4 h4 = *reinterpret_cast<const float4*>(G.hi + c0 + e0), f4 = *reinterpret_cast<const float4*>(G.beta + c0 + e0);
-                                const uint2 l2 = *reinterpret_cast<const uint2*>(G.lo + c0 + e0);
-                                const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, fs[4] = {f4.x, f4.y, f4.z, f4.w},
-                                            ls[4] = {__uint_as_float(l2.x << 16), __uint_as_float(l2.x & 0xffff0000u), __uint_as_float(l2.y << 16),
-                                                     __uint_as_float(l2.y & 0xffff0000u)};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const int col = c0 + e0 + e;
-                                    const float d = (hs[e] - mine) + (ls[e] - mine_lo);
-                                    const float f = fs[e] * ex2(keys ? d * kLog2e : d * -kLog2e);
-                                    x[e0 + e] = col < n && (keys ? col >= row : col <= row) ? __float_as_uint(f * __uint_as_float(x[e0 + e])) : 0u;
-                                }
-                            }
-                        } else {
-                            const float* tab = cb == rb ? G.quarter[w4] + c0 : G.cf + cb * kBlk + c0;
-                            const float r1 = cb == rb ? qf : rf;
-#pragma unroll
-                            for (int e = 0; e < 16; e += 4) {
-                                const float4 f = *reinterpret_cast<const float4*>(tab + e);
-                                const float2 r2 = make_float2(r1, r1);
-                                const float2 y0 = fmul2(fmul2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), r2), make_float2(f.x, f.y)),
-                                             y1 = fmul2(fmul2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), r2), make_float2(f.z, f.w));
-                                x[e] = __float_as_uint(y0.x);
-                                x[e + 1] = __float_as_uint(y0.y);
-                                x[e + 2] = __float_as_uint(y1.x);
-                                x[e + 3] = __float_as_uint(y1.y);
-                            }
-                            if (c0 + 16 > n) {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    if (c0 + e >= n) x[e] = 0u;
-                            }
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(tab + e);
+                            const float2 y0 = fmul2(fmul2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), r2), make_float2(f.x, f.y)),
+                                         y1 = fmul2(fmul2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), r2), make_float2(f.z, f.w));
+                            y[e / 2] = pack_bf16(y0.x, y0.y);
+                            y[e / 2 + 1] = pack_bf16(y1.x, y1.y);
                         }
+                        if (c0 + 16 > n) {                // a tail: pairs of columns
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                            for (int e = 0; e < 8; ++e) y[e] = c0 + 2 * e + 1 < n ? y[e] : c0 + 2 * e < n ? y[e] & 0xffffu : 0u;
+                        }
                     }
-                    tmem_st_n(S + 8 * q, y);              // over columns that are read
+                    tmem_st_n(S + 8 * q, y);
                 }
                 tmem_wait_st();
                 if (j == 0) {                             // the state's product: its rows scaled
@@ -879,29 +880,23 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                                                          : static_cast<const __nv_bfloat16*>(a.v) + token * sh.ldv + (size_t)cur.h * sh.dv;
                     float dot = 0.f;
 #pragma unroll 1
-                    for (int ch = ch0; ch < ch1; ch += 2) {
-                        uint32_t x[2][16];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (ch + e < ch1) tmem_ld_n(acc + 16 * (ch + e), x[e]);
+                    for (int ch = ch0; ch < ch1; ++ch) {
+                        uint32_t x[16];
+                        tmem_ld_n(acc + 16 * ch, x);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (ch + e < ch1) {
+                        for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(sf * __uint_as_float(x[c]));
+                        tmem_st_n(acc + 16 * ch, x);
+                        if ((MODE == kDq || MODE == kDv) && live) {   // q's or v's columns
+                            float y[8];
 #pragma unroll
-                                for (int c = 0; c < 16; ++c) x[e][c] = __float_as_uint(sf * __uint_as_float(x[e][c]));
-                                tmem_st_n(acc + 16 * (ch + e), x[e]);
-                                if ((MODE == kDq || MODE == kDv) && live) {       // q's or v's columns
-                                    float y[8];
+                            for (int half = 0; half < 2; ++half) {
+                                ld8<__nv_bfloat16>(z + 16 * ch + 8 * half, y);
 #pragma unroll
-                                    for (int half = 0; half < 2; ++half) {
-                                        ld8<__nv_bfloat16>(z + 16 * (ch + e) + 8 * half, y);
-#pragma unroll
-                                        for (int c = 0; c < 8; ++c) dot = fmaf(__uint_as_float(x[e][8 * half + c]), y[c], dot);
-                                    }
-                                }
-                                __syncwarp();
+                                for (int c = 0; c < 8; ++c) dot = fmaf(__uint_as_float(x[8 * half + c]), y[c], dot);
                             }
+                        }
+                        __syncwarp();
                     }
                     if ((MODE == kDq || MODE == kDv) && live) ra.part[at * ra.part_apart + g * kSeg + rb * kBlk + row] = dot;
                     tmem_wait_st();
@@ -910,14 +905,22 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                     if (lane == 0) mbar_arrive(acc_ready);
                 }
                 // the ring's stages: the state's, the next scores', X's
-                if (j == 0) stages += n_inter;
-                if (j + 1 < nblk || (p.nr > 1 && more)) stages += nb;
+                if (j == 0) at_stage += n_inter;
+                if (j + 1 < nblk || (p.nr > 1 && more)) at_stage += nb;
+                turn();
                 if (n % 16 != 0) {                        // X's tokens of what lies behind: rows of zero, up to whole products
                     // not before what was in X's stage is used up: the state's terms, or the X before
                     if (j > 0) wait_here(x_done + 8 * (u ^ 1), (blocks - 1) >> 1 & 1, a.err, dead);
-                    zero_tail(base, full0, p.ring, p.stage, stages + (n - 1 >> p.x_log), rows_x, n & rows_x - 1, nx, a.err, dead);
+                    const int last = (n - 1) >> p.x_log, over = at_stage + last >= p.ring, st = at_stage + last - (over ? p.ring : 0);
+                    wait_here(full0 + 8 * st, stage_ph ^ over, a.err, dead);
+                    const int r = (n & 15) + (tid >> 3);
+                    if (r < 16)
+#pragma unroll 1
+                        for (int x = 0; x < nx; ++x) st_shared16(base + st * p.stage + (x * rows_x + (n & rows_x - 16) + r) * 128 + (tid & 7) * 16, 0, 0, 0, 0);
+                    fence_proxy_async_smem();
                 }
-                stages += (n + rows_x - 1 >> p.x_log) + (j + 1 == nblk && p.nr == 1 ? nb : 0);
+                at_stage += ((n + rows_x - 1) >> p.x_log) + (j + 1 == nblk && p.nr == 1 ? nb : 0);
+                turn();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * u);
