@@ -79,6 +79,25 @@ __device__ __forceinline__ int2 slot_entry(const int2* table, int slot, int tota
     return e.x < 0 || e.y < 0 || e.y > kSeg || e.x > total - e.y ? make_int2(0, 0) : e;
 }
 
+// Behind the table: how many slots have b blocks or more (b = 1 .. 4), and the slots by blocks, most first.  One warp.
+__device__ __forceinline__ const int* slot_order(const int2* table, int slots) { return reinterpret_cast<const int*>(table + slots); }
+__device__ __noinline__ void order_slots(const int2* table, int slots, int total) {
+    int* order = const_cast<int*>(slot_order(table, slots));
+    const int lane = threadIdx.x & 31;
+    int at = 0;
+#pragma unroll 1
+    for (int b = kSeg / kBlk; b > 0; --b) {
+#pragma unroll 4
+        for (int s0 = 0; s0 < slots; s0 += 32) {
+            const bool is = s0 + lane < slots && (slot_entry(table, s0 + lane, total).y + kBlk - 1) / kBlk == b;
+            const unsigned m = __ballot_sync(0xffffffffu, is);
+            if (is) order[kSeg / kBlk + at + __popc(m & ((1u << lane) - 1))] = s0 + lane;
+            at += __popc(m);
+        }
+        if (lane == 0) order[b - 1] = at;
+    }
+}
+
 __global__ void __launch_bounds__(kBlk) lin_prep_kernel(SeqArgs a, float* gates) {
     const SeqShape& sh = a.sh;
     griddep_wait();
@@ -373,6 +392,7 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
     } else {
         const int w4 = warp & 3, r = 32 * w4 + lane;
         const uint32_t lanes = (uint32_t)(32 * w4) << 16, mine = base + kLocalOut + r * 128;
+        if (!BACK && blockIdx.x == gridDim.x - 1 && warp == 8) order_slots(items.table, slots, sh.total);       // for the rows' kernels
         uint32_t unit = 0;
         for (int i = blockIdx.x; i < count; i += gridDim.x) {
             const int rows = items.get(i, slot, h, r0, c0, first), n = min(128, sh.dk - c0);
@@ -465,38 +485,46 @@ constexpr int kRowNBars = 2 * kMaxRing + 17;
 constexpr uint32_t kRowHolder = kRowNBars * 8, kRowGates = (kRowHolder + 8 + 15) / 16 * 16, kRowTail = kRowGates + 2 * sizeof(RowGates);
 static_assert(sizeof(RowGates) % 16 == 0, "read by 16 bytes");
 
-// The first of a CTA's items from number i on: (its number, slot, first token, rows + 1024 x its head of q and k), rows 0
-// where there is none left.
-// Four neighbours are a segment's blocks (they read the same tiles), in another order each turn of the grid, so that every
-// CTA gets long and short ones.  Called, not inlined: five roles look for items, and the instruction cache is small.
-__device__ __forceinline__ int rows_block(int i, bool keys) {
-    const int q = (i + i / (int)gridDim.x) & 3;
-    return keys ? q : 3 - q;
-}
-__device__ __noinline__ int4 rows_item(int i, const int2* table, int slots, int H, int rep, int total, bool keys) {
+// A CTA's item of a turn: (slot, first token, rows + 1024 x blocks of columns + 8192 x its head of q and k, head), rows 0
+// where there is none.  First segments of four blocks, whose four items are neighbours (they read the same tiles), in
+// another order each turn, so that a CTA's turns bring long and short ones; then the shorter segments' items from the
+// longest to the shortest.  (Everything from the longest to the shortest balances as well but reads all tiles at once:
+// 4 x 2048 tokens forward and backward 440 us for 410.  Shorter segments by segment too: packed prompts 99 us for 87.)
+// Called, not inlined: four roles look for items, and the instruction cache is small.
+__device__ __noinline__ int4 rows_item(int turn, const int* order, const int2* table, int slots, int H, int rep, int total) {
+    constexpr int kMost = kSeg / kBlk;
+    const int i = turn * gridDim.x + blockIdx.x, n_most = min(max(order[kMost - 1], 0), slots);
+    int m = i / kMost, b = kMost - (i + turn) % kMost, from = 0;
+    if (m >= n_most * H) {
+        m = i - n_most * H * kMost;
+        from = n_most;
 #pragma unroll 1
-    for (;; i += gridDim.x) {
-        const int slot = (i >> 2) / H;
-        if (slot >= slots) return make_int4(i, slot, 0, 0);
-        const int2 e = slot_entry(table, slot, total);
-        if (rows_block(i, keys) * kBlk < e.y) return make_int4(i, slot, e.x, e.y + ((i >> 2) - slot * H) / rep * 1024);
+        for (b = kMost - 1; b > 0; --b) {
+            const int k = (min(max(order[b - 1], n_most), slots) - n_most) * H;
+            if (m < k) break;
+            m -= k;
+        }
+        if (b == 0) return make_int4(0, 0, 0, 0);
     }
+    const int at = m / H, slot = order[kMost + from + at], h = m - at * H;
+    if ((unsigned)slot >= (unsigned)slots) return make_int4(0, 0, 0, 0);
+    const int2 e = slot_entry(table, slot, total);
+    return (e.y + kBlk - 1) / kBlk < b ? make_int4(0, 0, 0, 0) : make_int4(slot, e.x, e.y + b * 1024 + h / rep * 8192, h);
 }
 template <int MODE>
 struct RowsItem {
-    int i, slot, h, hk, rb, first, rows, row_n, nblk;
-    __device__ __forceinline__ void look(int from, const int2* table, const SeqShape& sh, int slots, int rep) {
+    int slot, h, hk, rb, first, rows, row_n, nblk;
+    __device__ __forceinline__ void look(int turn, const int2* table, const SeqShape& sh, int slots, int rep) {
         constexpr bool keys = MODE == kDk || MODE == kDv;
-        const int4 e = rows_item(from, table, slots, sh.H, rep, sh.total, keys);
-        i = e.x;
-        slot = e.y;
-        first = e.z;
-        rows = e.w & 1023;
-        hk = e.w >> 10;
-        h = (i >> 2) - slot * sh.H;
-        rb = rows_block(i, keys);
+        const int4 e = rows_item(turn, slot_order(table, slots), table, slots, sh.H, rep, sh.total);
+        slot = e.x;
+        first = e.y;
+        rows = e.z & 1023;
+        nblk = e.z >> 10 & 7;                             // blocks of columns: rb .. last, or 0 .. rb
+        hk = e.z >> 13;
+        h = e.w;
+        rb = keys ? (rows + kBlk - 1) / kBlk - nblk : nblk - 1;
         row_n = min(kBlk, rows - rb * kBlk);
-        nblk = keys ? (rows - 1) / kBlk - rb + 1 : rb + 1;       // blocks of columns: rb .. last, or 0 .. rb
     }
     __device__ __forceinline__ bool there() const { return rows > 0; }
     __device__ __forceinline__ int col_block(int j) const { return MODE == kDk || MODE == kDv ? rb + j : j; }
@@ -546,10 +574,13 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         if (seq_outside(sh, ob, oe)) zero_rows<__nv_bfloat16>(out, (size_t)out_heads * dx, ob, oe, sh.total);
     }
     // Scores and products of a CTA's blocks of columns, one after another over its items, interleaved: the scores of a
-    // block before the product of the one before it, the state's product behind the first scores of its rows.  With one
-    // buffer of row operands an item's first scores come behind the last product of the item before.
+    // block before the product of the one before it, the state's product behind the first scores of its rows.  The rows'
+    // operand is used up by its last scores (or the state's product): the next rows' arrives while the workers have those,
+    // and with one place for it an item's first scores come behind the last product of the item before (75 k cycles a CTA
+    // of 8192 tokens for 70 the other way around).
+    // A next item is looked up while its predecessor's first block is on its way.
     RowsItem<MODE> it;
-    it.look(blockIdx.x, table, sh, slots, rep);
+    it.look(0, table, sh, slots, rep);
     if (warp == 12) {
         if (elect_one()) {
             const bool whole_a = da % 64 == 0, whole_x = dx % 64 == 0;
@@ -557,19 +588,19 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             Ring ring, rr;
             int issued = 0, r_issued = 0;
             bool ok = true;
-            RowsItem<MODE> prev;
+            RowsItem<MODE> prev, after;
+            int turns = 0;
             bool last = false;
             for (int j = 0, pj = -1; ok && !last;) {          // it's block j; the block before it, prev's pj
                 last = !it.there();
                 const bool x_first = last || (j == 0 && p.nr == 1);
                 const int n0 = pj == 0 ? n_inter : 0, nxt = pj >= 0 ? (prev.col_rows(pj) + rows_x - 1) >> p.x_log : 0, ns = last ? 0 : nb;
-                // the state's stages, then scores' and X's in their order; the rows' own operand before its first scores (e
-                // stays where it is)
+                // the state's stages, then scores' and X's in their order; new rows' own operand before both (e stays where it is)
                 bool row_op = j == 0 && !last;
 #pragma unroll 1
                 for (int e = 0; e < n0 + ns + nxt;) {
                     const int w = e - n0, s_at = x_first ? w - nxt : w, x_at = x_first ? w : w - ns;
-                    const bool state = e < n0, score = !state && s_at >= 0 && s_at < ns, r = score && row_op;
+                    const bool state = e < n0, r = !state && row_op, score = r || (!state && s_at >= 0 && s_at < ns);
                     const uint32_t st = r ? rr.st : ring.st, ph = (r ? rr.ph : ring.ph) ^ 1, bar = (r ? rfull : full0) + 8 * st, dst = base + (r ? p.r + st * r_bytes : st * p.stage);
                     if ((r ? r_issued >= p.nr : issued >= p.ring) && !(ok = wait_here((r ? rfree : empty0) + 8 * st, ph, a.err, dead))) break;
                     // boxes of 64 columns (all of them in one where the map has whole boxes: slabs behind the last come as zeros);
@@ -601,11 +632,12 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                     }
                 }
                 if (last) break;
+                if (j == 0) after.look(++turns, table, sh, slots, rep);
                 prev = it;
                 pj = j;
                 if (++j == it.nblk) {
                     j = 0;
-                    it.look(it.i + gridDim.x, table, sh, slots, rep);
+                    it = after;
                 }
             }
             if (*dead) {                                  // copies in flight end before the CTA does
@@ -625,12 +657,17 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             tc_fence_after();
         };
         const uint32_t id_x = idesc_bf16(128, dx) | kBMn, id_i = idesc_bf16(128, dx) | (values ? 0u : kBMn);
+        const auto free_r = [&]() {                       // the rows' operand is used up
+            if (leader) mma_commit(rfree + 8 * rr.st);
+            __syncwarp();
+            rr.next(p.nr);
+        };
         uint32_t items = 0, blocks = 0;                   // sums, and blocks of scores, so far
-        int p_rows = 0;                                   // tokens of the block of columns before
+        RowsItem<MODE> after;
+        int turns = 0, p_rows = 0;                                   // tokens of the block of columns before
         bool p_last = false;
         for (int j = 0, pj = -1;;) {
-            const bool last = !warp_uniform(it.there());
-            const bool x_first = last || (j == 0 && p.nr == 1);
+            const bool last = !warp_uniform(it.there()), x_first = last || (j == 0 && p.nr == 1);
             const uint32_t ab = two_sums ? items & 1 : 0, ap = two_sums ? items >> 1 & 1 : items & 1, acc = tmem + 128 * ab;
             if (pj == 0) {
                 if (items > (uint32_t)two_sums) wait(acc_free + 8 * ab, ap ^ 1);
@@ -651,16 +688,34 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                 }
                 if (leader) mma_commit(inter_done);
                 __syncwarp();
-            }
-            if (j == 0 && pj >= 0) {                      // the rows' operand before is used up
-                if (leader) mma_commit(rfree + 8 * rr.st);
-                __syncwarp();
-                rr.next(p.nr);
+                if (p_last) free_r();
             }
 #pragma unroll 1
             for (int ph = 0; ph < 2; ++ph) {
-                if ((ph == 0) == x_first) {               // the product of the block before
-                    if (pj < 0) continue;
+                if ((ph == 0) != x_first && !last) {      // scores of it's block j
+                    const uint32_t u = blocks & 1, D = tmem + scores + 128 * u, id = idesc_bf16(128, (warp_uniform(it.col_rows(j)) + 15) & ~15);
+                    if (j == 0) wait(rfull + 8 * rr.st, rr.ph);
+                    if (blocks > 1) wait(x_done + 8 * u, (blocks >> 1 & 1) ^ 1);      // the scores before are used up
+                    const uint64_t dR = k_desc<128>(base + p.r + rr.st * r_bytes);
+#pragma unroll 1
+                    for (int x = 0; x < na; ++x) {
+                        if ((x & 1) == 0) wait(full0 + 8 * ring.st, ring.ph);
+                        const bool more = (x & 1) == 0 && x + 1 < na;
+                        if (leader) {
+                            const uint64_t dA = dR + (x * 2 * kBox >> 4), dB = k_desc<128>(base + ring.st * p.stage) + ((x & 1) * 2 * kBox >> 4);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (64 * x + 16 * k < da) mma_bf16(D, dA + 2 * k, dB + 2 * k, id, x + k > 0);
+                            if (!more) mma_commit(empty0 + 8 * ring.st);
+                        }
+                        __syncwarp();
+                        if (!more) ring.next(p.ring);
+                    }
+                    if (leader) mma_commit(s_full + 8 * u);
+                    __syncwarp();
+                    if (j > 0 && j + 1 == warp_uniform(it.nblk)) free_r();
+                }
+                if ((ph == 0) == x_first && pj >= 0) {    // the product of the block before
                     const uint32_t n = blocks - 1, u = n & 1;
                     if (pj == 0) wait(acc_ready, items & 1);
                     wait(p_full + 8 * u, n >> 1 & 1);
@@ -684,38 +739,18 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                         if (p_last) mma_commit(acc_done + 8 * ab);
                     }
                     __syncwarp();
-                } else if (!last) {                       // scores of it's block j
-                    const uint32_t u = blocks & 1, D = tmem + scores + 128 * u, id = idesc_bf16(128, (warp_uniform(it.col_rows(j)) + 15) & ~15);
-                    if (j == 0) wait(rfull + 8 * rr.st, rr.ph);
-                    if (blocks > 1) wait(x_done + 8 * u, (blocks >> 1 & 1) ^ 1);      // the scores before are used up
-                    const uint64_t dR = k_desc<128>(base + p.r + rr.st * r_bytes);
-#pragma unroll 1
-                    for (int x = 0; x < na; ++x) {
-                        if ((x & 1) == 0) wait(full0 + 8 * ring.st, ring.ph);
-                        const bool more = (x & 1) == 0 && x + 1 < na;
-                        if (leader) {
-                            const uint64_t dA = dR + (x * 2 * kBox >> 4), dB = k_desc<128>(base + ring.st * p.stage) + ((x & 1) * 2 * kBox >> 4);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (64 * x + 16 * k < da) mma_bf16(D, dA + 2 * k, dB + 2 * k, id, x + k > 0);
-                            if (!more) mma_commit(empty0 + 8 * ring.st);
-                        }
-                        __syncwarp();
-                        if (!more) ring.next(p.ring);
-                    }
-                    if (leader) mma_commit(s_full + 8 * u);
-                    __syncwarp();
                 }
             }
             if (pj >= 0 && p_last) ++items;
             if (last) break;
             ++blocks;
+            if (j == 0) after.look(++turns, table, sh, slots, rep);
             p_rows = warp_uniform(it.col_rows(j));
             p_last = warp_uniform(j + 1 == it.nblk);
             pj = j;
             if (p_last) {
                 j = 0;
-                it.look(it.i + gridDim.x, table, sh, slots, rep);
+                it = after;
             } else {
                 ++j;
             }
@@ -731,6 +766,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         const int chunks = dx / 16, ch0 = g == 0 ? 0 : (chunks + 1) / 2, ch1 = g == 0 ? (chunks + 1) / 2 : chunks;      // of 16 columns
         RowGates* gates = reinterpret_cast<RowGates*>(tail + kRowGates);
         uint32_t items = 0, blocks = 0;
+        int turns = 0;
         int at_stage = nb, stage_ph = 0;                  // of the ring, behind this block's scores, and their turn's parity
         const auto turn = [&]() {
 #pragma unroll 1
@@ -763,46 +799,29 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             g_blk[1] = gt[kGLo + c];
             g_blk[2] = keys ? 1.f : gt[kGBeta + c];
         };
-        // An item's gates are loaded while the one before is worked on; the loads stand in one place, so the first turn has
-        // nothing else.
-        RowsItem<MODE> cur = it;
-        float mine = 0.f, mine_lo = 0.f, rf = 0.f, sf = 0.f, qf = 0.f;
-#pragma unroll 1
-        for (bool have = false;;) {
+        // An item's gates are loaded while the one before is worked on.
+        if (it.there()) load_gates();
+        while (it.there()) {
+            const RowsItem<MODE> cur = it;
             RowGates& G = gates[items & 1];
-            if (have) {
-                cur = it;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = tid + 256 * e, b = t / kBlk, w = 2 * (tid >> 7) + e;
-                    float f = keys ? g_col[e][0] : g_col[e][0] * g_col[e][1];
+            for (int e = 0; e < 2; ++e) {
+                const int t = tid + 256 * e, b = t / kBlk, w = 2 * (tid >> 7) + e;
+                float f = keys ? g_col[e][0] : g_col[e][0] * g_col[e][1];
 #pragma unroll
-                    for (int m = 1; m < 3; ++m)           // blocks between
-                        if (m > min(b, cur.rb) && m < max(b, cur.rb)) f *= g_tot[m];
-                    G.cf[t] = f;
-                    const float d = (g_m[e][0] - g_blk[0]) + (g_m[e][1] - g_blk[1]);
-                    G.quarter[w][tid & 127] = g_blk[2] * ex2(keys ? d * -kLog2e : d * kLog2e);
-                }
-                if (tid < kBlk) {
-                    G.beta[tid] = g_blk[2];
-                    G.hi[tid] = g_blk[0];
-                    G.lo[tid] = __float2bfloat16_rn(g_blk[1]);
-                }
-                mine = g_row[0];
-                mine_lo = g_row[1];
-                rf = g_row[2];
-                sf = g_row[3];
-                const float dm = (mine - g_row[4]) + (mine_lo - g_row[5]);
-                qf = ex2(keys ? dm * -kLog2e : dm * kLog2e);
-                it.look(it.i + gridDim.x, table, sh, slots, rep);
+                for (int m = 1; m < 3; ++m)           // blocks between
+                    if (m > min(b, cur.rb) && m < max(b, cur.rb)) f *= g_tot[m];
+                G.cf[t] = f;
+                const float d = (g_m[e][0] - g_blk[0]) + (g_m[e][1] - g_blk[1]);
+                G.quarter[w][tid & 127] = g_blk[2] * ex2(keys ? d * -kLog2e : d * kLog2e);
             }
-            const bool more = it.there();
-            if (more) load_gates();
-            if (!have) {
-                if (!more) break;
-                have = true;
-                continue;
+            if (tid < kBlk) {
+                G.beta[tid] = g_blk[2];
+                G.hi[tid] = g_blk[0];
+                G.lo[tid] = __float2bfloat16_rn(g_blk[1]);
             }
+            const float mine = g_row[0], mine_lo = g_row[1], rf = g_row[2], sf = g_row[3];
+            const float dm = (mine - g_row[4]) + (mine_lo - g_row[5]), qf = ex2(keys ? dm * -kLog2e : dm * kLog2e);
             const int rb = cur.rb, hk = cur.hk, nblk = cur.nblk;
             const bool live = row < cur.row_n;
             const size_t token = (size_t)cur.first + rb * kBlk + row, at = (size_t)cur.slot * sh.H + cur.h;
@@ -872,7 +891,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                     tmem_st_n(S + 8 * q, y);
                 }
                 tmem_wait_st();
-                if (j == 0) {                             // the state's product: its rows scaled
+                if (j == 0) {                             // the next item's gates; the state's product: its rows scaled
+                    it.look(++turns, table, sh, slots, rep);
+                    if (it.there()) load_gates();
                     wait_here(inter_done, items & 1, a.err, dead);
                     __syncwarp();
                     tc_fence_after();
@@ -906,7 +927,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                 }
                 // the ring's stages: the state's, the next scores', X's
                 if (j == 0) at_stage += n_inter;
-                if (j + 1 < nblk || (p.nr > 1 && more)) at_stage += nb;
+                if (j + 1 < nblk || (p.nr > 1 && it.there())) at_stage += nb;
                 turn();
                 if (n % 16 != 0) {                        // X's tokens of what lies behind: rows of zero, up to whole products
                     // not before what was in X's stage is used up: the state's terms, or the X before
@@ -926,13 +947,12 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                 if (lane == 0) mbar_arrive(p_full + 8 * u);
             }
             ++items;
-            if (!more) break;
         }
     } else {
         const int w4 = warp & 3, row = 32 * w4 + lane;
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
         const bool shared = !values && rep > 1, whole = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
-        for (uint32_t items = 0; it.there(); ++items, it.look(it.i + gridDim.x, table, sh, slots, rep)) {
+        for (uint32_t items = 0; it.there(); it.look(++items, table, sh, slots, rep)) {
             const uint32_t ab = two_sums ? items & 1 : 0, ap = two_sums ? items >> 1 & 1 : items & 1, acc = tmem + 128 * ab + lanes;
             const bool live = row < it.row_n;
             const size_t token = (size_t)it.first + it.rb * kBlk + row;
@@ -1451,7 +1471,7 @@ cudaError_t pairs_go(const SeqArgs& a, const float* gates, float* part, cudaStre
 
 LinLayout lin_layout_tc(const SeqShape& s) {
     LinLayout L = {};
-    const size_t slots = seg_slots(s.nseq, s.total, kSeg), sth = slots * s.H, state = sth * s.dv * s.dk, gates = sth * kGAll * 4 + slots * 8;
+    const size_t slots = seg_slots(s.nseq, s.total, kSeg), sth = slots * s.H, state = sth * s.dv * s.dk, gates = sth * kGAll * 4 + slots * 12 + 16;
     L.rec_gates = align_up(3 * state * 2, kSectionAlign);
     L.rec_total = align_up(L.rec_gates + gates, kSectionAlign);
     L.ws_start = align_up(L.ws_local + state * 4, kSectionAlign);
