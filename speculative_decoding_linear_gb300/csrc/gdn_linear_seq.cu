@@ -455,7 +455,7 @@ cudaError_t launch_linear_scan(const SeqShape& sh, int L, int terms, bool back, 
                                void* out, size_t apart, const void* start, float* phi, float* last, int* err, cudaStream_t st) {
     const dim3 grid((unsigned)((size_t)sh.nseq * sh.H * scan_tiles(sh)));
     const auto k = terms == 0 ? (back ? lin_scan_kernel<0, true> : lin_scan_kernel<0, false>)
-                   : terms == 1 ? lin_scan_kernel<1, false>
+                   : terms == 2 ? lin_scan_kernel<2, false>
                                 : (back ? lin_scan_kernel<3, true> : lin_scan_kernel<3, false>);
     return launch_kernel(k, grid, dim3(kScanThreads), 0, st, sh.total > 0, sh, L, local, gend, gend_apart, S0, out, apart, start, phi, last, err);
 }

@@ -158,9 +158,6 @@ __device__ __forceinline__ float ex2(float x) {      // 2^x, to 2^-22 of it; bel
 }
 constexpr float kLog2e = 1.44269504f;
 
-__device__ __forceinline__ void tmem_st_n(uint32_t t, const uint32_t (&r)[4]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
-}
 __device__ __forceinline__ void tmem_st_n(uint32_t t, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
                  "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -720,15 +717,18 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                     if (pj == 0) wait(acc_ready, items & 1);
                     wait(p_full + 8 * u, n >> 1 & 1);
 #pragma unroll 1
-                    for (int x = 0; x < p_rows; x += 64) {            // 64 tokens, 32 of their 64 columns
+                    for (int x = 0; x < p_rows; x += 64) {            // 64 tokens
                         if ((x & rows_x - 1) == 0) wait(full0 + 8 * ring.st, ring.ph);
                         const bool more = x + 64 < p_rows && (x + 64 & rows_x - 1) != 0;       // of the stage
                         if (leader) {
                             const uint64_t dB = mn_desc<128>(base + ring.st * p.stage, rows_x * 128) + (x & rows_x - 1) * 8;
-                            const uint32_t A = tmem + scores + 128 * u + x;
+                            const uint32_t A = tmem + scores + 128 * u + x;           // 16 tokens: 8 columns of first terms, 8 of second
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                if (x + 16 * k < p_rows) mma_bf16_ts(acc, A + 8 * k, dB + 128 * k, id_x, 1);
+                                if (x + 16 * k < p_rows) {
+                                    mma_bf16_ts(acc, A + 16 * k + 8, dB + 128 * k, id_x, 1);
+                                    mma_bf16_ts(acc, A + 16 * k, dB + 128 * k, id_x, 1);
+                                }
                             if (!more) mma_commit(empty0 + 8 * ring.st);
                         }
                         __syncwarp();
@@ -837,58 +837,56 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {             // 16 columns
                     const int c0 = 64 * g + 16 * q, cq = c0 >> 5;
-                    if (cb == rb && cq == w4 && c0 < n) { // around the diagonal
-#pragma unroll 1
-                        for (int e0 = 0; e0 < 16; e0 += 8) {
-                            uint32_t x[8], y[4];
-                            tmem_ld_n(S + 16 * q + e0, x);
-                            tmem_wait_ld();
+                    uint32_t x[16], y[16];                // 16 tokens' pairs, first terms and second terms
+                    if (c0 >= n || (cb == rb && (keys ? cq < w4 : cq > w4))) {
 #pragma unroll
-                            for (int e1 = 0; e1 < 8; e1 += 4) {
-                                const int at4 = c0 + e0 + e1;
-                                const float4 h4 = *reinterpret_cast<const float4*>(G.hi + at4), f4 = *reinterpret_cast<const float4*>(G.beta + at4);
-                                const uint2 l2 = *reinterpret_cast<const uint2*>(G.lo + at4);
+                        for (int e = 0; e < 16; ++e) y[e] = 0;        // behind the segment, or masked altogether
+                    } else {
+                        tmem_ld_n(S + 16 * q, x);
+                        tmem_wait_ld();
+                        if (cb == rb && cq == w4) {       // around the diagonal
+#pragma unroll
+                            for (int e0 = 0; e0 < 16; e0 += 4) {
+                                const float4 h4 = *reinterpret_cast<const float4*>(G.hi + c0 + e0), f4 = *reinterpret_cast<const float4*>(G.beta + c0 + e0);
+                                const uint2 l2 = *reinterpret_cast<const uint2*>(G.lo + c0 + e0);
                                 const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, fs[4] = {f4.x, f4.y, f4.z, f4.w},
                                             ls[4] = {__uint_as_float(l2.x << 16), __uint_as_float(l2.x & 0xffff0000u), __uint_as_float(l2.y << 16),
                                                      __uint_as_float(l2.y & 0xffff0000u)};
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
-                                    const int col = at4 + e;
+                                    const int col = c0 + e0 + e;
                                     const float d = (hs[e] - mine) + (ls[e] - mine_lo);
                                     const float f = fs[e] * ex2(keys ? d * kLog2e : d * -kLog2e);
-                                    x[e1 + e] = col < n && (keys ? col >= row : col <= row) ? __float_as_uint(f * __uint_as_float(x[e1 + e])) : 0u;
+                                    x[e0 + e] = (keys ? col >= row : col <= row) ? __float_as_uint(f * __uint_as_float(x[e0 + e])) : 0u;
                                 }
                             }
+                        } else {
+                            const float* tab = cb == rb ? G.quarter[w4] + c0 : G.cf + cb * kBlk + c0;
+                            const float r1 = cb == rb ? qf : rf;
+                            const float2 r2 = make_float2(r1, r1);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) y[e] = pack_bf16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-                            tmem_st_n(S + 8 * q + e0 / 2, y);         // over columns that are read
+                            for (int e = 0; e < 16; e += 4) {
+                                const float4 f = *reinterpret_cast<const float4*>(tab + e);
+                                const float2 y0 = fmul2(fmul2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), r2), make_float2(f.x, f.y)),
+                                             y1 = fmul2(fmul2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), r2), make_float2(f.z, f.w));
+                                x[e] = __float_as_uint(y0.x);
+                                x[e + 1] = __float_as_uint(y0.y);
+                                x[e + 2] = __float_as_uint(y1.x);
+                                x[e + 3] = __float_as_uint(y1.y);
+                            }
                         }
-                        continue;
-                    }
-                    uint32_t x[16], y[8];
-                    if (c0 >= n || (cb == rb && (keys ? cq < w4 : cq > w4))) {
+                        if (c0 + 16 > n) {                // a tail
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = 0;         // behind the segment, or masked altogether
-                    } else {
-                        tmem_ld_n(S + 16 * q, x);
-                        tmem_wait_ld();
-                        const float* tab = cb == rb ? G.quarter[w4] + c0 : G.cf + cb * kBlk + c0;
-                        const float r1 = cb == rb ? qf : rf;
-                        const float2 r2 = make_float2(r1, r1);
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(tab + e);
-                            const float2 y0 = fmul2(fmul2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), r2), make_float2(f.x, f.y)),
-                                         y1 = fmul2(fmul2(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), r2), make_float2(f.z, f.w));
-                            y[e / 2] = pack_bf16(y0.x, y0.y);
-                            y[e / 2 + 1] = pack_bf16(y1.x, y1.y);
+                            for (int e = 0; e < 16; ++e) x[e] = c0 + e < n ? x[e] : 0u;
                         }
-                        if (c0 + 16 > n) {                // a tail: pairs of columns
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) y[e] = c0 + 2 * e + 1 < n ? y[e] : c0 + 2 * e < n ? y[e] & 0xffffu : 0u;
+                        for (int e = 0; e < 8; ++e) {
+                            const float x0 = __uint_as_float(x[2 * e]), x1 = __uint_as_float(x[2 * e + 1]);
+                            y[e] = pack_bf16(x0, x1);
+                            y[8 + e] = pack_bf16(x0 - __uint_as_float(y[e] << 16), x1 - __uint_as_float(y[e] & 0xffff0000u));
                         }
                     }
-                    tmem_st_n(S + 8 * q, y);
+                    tmem_st_n(S + 16 * q, y);             // over the columns just read
                 }
                 tmem_wait_st();
                 if (j == 0) {                             // the next item's gates; the state's product: its rows scaled
@@ -1475,7 +1473,7 @@ LinLayout lin_layout_tc(const SeqShape& s) {
     L.rec_gates = align_up(3 * state * 2, kSectionAlign);
     L.rec_total = align_up(L.rec_gates + gates, kSectionAlign);
     L.ws_start = align_up(L.ws_local + state * 4, kSectionAlign);
-    L.ws_gates = align_up(L.ws_start + state * 2, kSectionAlign);
+    L.ws_gates = align_up(L.ws_start + 2 * state * 2, kSectionAlign);
     L.ws_forward = align_up(L.ws_gates + gates, kSectionAlign);
     // the backward pass's own, from ws_start on
     L.ws_end = L.ws_start;
@@ -1495,15 +1493,15 @@ cudaError_t launch_linear_forward_tc(const SeqArgs& a, cudaStream_t st) {
     char* starts = keep ? a.rec : a.ws + L.ws_start;
     const size_t apart = (size_t)seg_slots(sh.nseq, sh.total, kSeg) * sh.H * sh.dv * sh.dk;
     const auto scan = [&]() {
-        return launch_linear_scan(sh, kSeg, keep ? 3 : 1, false, local, gates + kGTot + 4, kGAll, a.S0, starts, apart, nullptr, nullptr, a.S_T, a.err, st);
+        return launch_linear_scan(sh, kSeg, keep ? 3 : 2, false, local, gates + kGTot + 4, kGAll, a.S0, starts, apart, nullptr, nullptr, a.S_T, a.err, st);
     };
     if (sh.total == 0) return scan();            // the states pass through
     CUtensorMap ms;
-    if (!state_map(&ms, starts, sh, 1, sh.dv)) return cudaErrorInvalidValue;
+    if (!state_map(&ms, starts, sh, 2, sh.dv)) return cudaErrorInvalidValue;
     cudaError_t e = prep_go(a, gates, st);
     if (e == cudaSuccess) e = local_go<false>(a, gates, local, st);
     if (e == cudaSuccess) e = scan();
-    if (e == cudaSuccess) e = rows_go<kOut>(ms, a, gates, nullptr, nullptr, 1, st);
+    if (e == cudaSuccess) e = rows_go<kOut>(ms, a, gates, nullptr, nullptr, 2, st);
     return e;
 }
 
@@ -1524,12 +1522,12 @@ cudaError_t launch_linear_backward_tc(const SeqArgs& a, cudaStream_t st) {
     };
     if (sh.total == 0) return scan();
     CUtensorMap ms, me_keys, me_values;      // the starts by 64 rows of d_v; the ends so and by all
-    if (!state_map(&ms, a.rec, sh, 3, 64) || !state_map(&me_keys, ends, sh, 1, 64) || !state_map(&me_values, ends, sh, 3, sh.dv))
+    if (!state_map(&ms, a.rec, sh, 3, 64) || !state_map(&me_keys, ends, sh, 2, 64) || !state_map(&me_values, ends, sh, 3, sh.dv))
         return cudaErrorInvalidValue;
     cudaError_t e = local_go<true>(a, gates, local, st);
     if (e == cudaSuccess) e = scan();
     if (e == cudaSuccess) e = rows_go<kDq>(ms, a, gates, part + kPartQ, dq, 3, st);
-    if (e == cudaSuccess) e = rows_go<kDk>(me_keys, a, gates, nullptr, dk, 1, st);
+    if (e == cudaSuccess) e = rows_go<kDk>(me_keys, a, gates, nullptr, dk, 2, st);
     if (e == cudaSuccess) e = rows_go<kDv>(me_values, a, gates, part + kPartK, nullptr, 3, st);
     if (e == cudaSuccess) e = pairs_go(a, gates, part, st);
     if (e == cudaSuccess)
