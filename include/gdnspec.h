@@ -527,7 +527,13 @@ int gdn_seq_step(const void* q, const void* k, const void* v, int dtype, const f
  *              gdn_linear_seq_workspace_bytes, which serve both
  * and record and workspace are 16-byte aligned.  A decay that is the same for all tokens (a constant
  * of each head) is given for each token too, and its gradient is the sum over the tokens; for a write
- * strength of one, beta holds ones.
+ * strength of one, beta holds ones.  H_k is at most 2^18.
+ * States and sums are fp32.  With bf16 inputs the fp32 operands of the tensor core's products are
+ * carried as bf16 terms: three of them (2^-24 of an operand are left) where the result is fp32 (what a
+ * segment adds to a state, the gates' gradients), two (2^-17) of the decayed scores and of the states
+ * where it is bf16.  S_T and dS0 are 9e-7 of their size off with slow decays.  With fp32 inputs all is
+ * fp32.  A NaN or an infinity stays in its sequence; it reaches the whole segment that it lies in (512
+ * tokens with bf16 inputs, 64 with fp32), the tokens before it too, and an infinity may become a NaN.
  * Equal inputs give equal bits (no atomics).
  */
 int gdn_linear_seq_workspace_bytes(int nseq, int total, int H, int Hk, int dk, int dv, int dtype, size_t* bytes);

@@ -19,19 +19,17 @@ constexpr int kT = 256;                     // threads
 constexpr int kK = 32;                      // depth of a staged tile
 constexpr int kLd = 68;                     // floats from one staged row to the next
 
-template <typename T>
 struct Mat {                                // element (r, c) is p[r ld + c]; zero outside rows x cols
-    const T* p;
+    const float* p;
     size_t ld;
     int rows, cols;
     __device__ __forceinline__ float4 at(int r, int c) const {        // cols and c are multiples of four
-        return r < rows && c < cols ? ld4<T>(p + (size_t)r * ld, c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        return r < rows && c < cols ? ld4<float>(p + (size_t)r * ld, c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 };
 
 // s[k][m] of a 64 x 32 piece whose k index runs along the row, from column k0 on
-template <typename T>
-__device__ __forceinline__ void stage_k(float (*s)[kLd], const Mat<T>& m, int k0) {
+__device__ __forceinline__ void stage_k(float (*s)[kLd], const Mat& m, int k0) {
 #pragma unroll
     for (int i = threadIdx.x; i < 64 * kK / 4; i += kT) {
         const int r = i / (kK / 4), k = i % (kK / 4) * 4;
@@ -43,8 +41,7 @@ __device__ __forceinline__ void stage_k(float (*s)[kLd], const Mat<T>& m, int k0
     }
 }
 // s[k][n] of a 32 x 64 piece whose n index runs along the row, from row k0 on, its rows scaled
-template <typename T>
-__device__ __forceinline__ void stage_n(float (*s)[kLd], const Mat<T>& m, int k0, const float* scale = nullptr) {
+__device__ __forceinline__ void stage_n(float (*s)[kLd], const Mat& m, int k0, const float* scale = nullptr) {
 #pragma unroll
     for (int i = threadIdx.x; i < 64 * kK / 4; i += kT) {
         const int k = i / 16, n = i % 16 * 4;
@@ -79,8 +76,8 @@ struct alignas(16) Stage {               // read by 16 bytes
     float a[kK][kLd], b[kK][kLd];
 };
 // c += A B^T, both with k along the row; A B with `along_n`
-template <bool along_n, typename TA, typename TB>
-__device__ __forceinline__ void product(Acc& c, Stage& s, const Mat<TA>& A, const Mat<TB>& B, int K) {
+template <bool along_n>
+__device__ __forceinline__ void product(Acc& c, Stage& s, const Mat& A, const Mat& B, int K) {
     for (int k = 0; k < K; k += kK) {
         __syncthreads();
         stage_k(s.a, A, k);
@@ -124,18 +121,16 @@ __device__ __forceinline__ float decay(const Gates& g, int t, int s) {      // e
     return decay_of((g.hi[t] - g.hi[s]) + (g.lo[t] - g.lo[s]));
 }
 
-template <typename T>
-__device__ __forceinline__ Mat<T> token_rows(const void* p, size_t ld, int first, int rows, int head, int d) {
-    return {static_cast<const T*>(p) + (size_t)first * ld + (size_t)head * d, ld, rows, d};
+__device__ __forceinline__ Mat token_rows(const void* p, size_t ld, int first, int rows, int head, int d) {
+    return {static_cast<const float*>(p) + (size_t)first * ld + (size_t)head * d, ld, rows, d};
 }
-template <typename T>
-__device__ __forceinline__ Mat<T> columns(const Mat<T>& m, int c0) { return {m.p + c0, m.ld, m.rows, m.cols - c0}; }
+__device__ __forceinline__ Mat columns(const Mat& m, int c0) { return {m.p + c0, m.ld, m.rows, m.cols - c0}; }
 
 // ---------------------------------------------------------------------------
 // what a segment adds to the state: sum_t beta_t e^{G - g_t} v_t k_t^T; or, BACK, to the gradient of the
 // state: sum_t e^{g_t} dO_t q_t^T.  One CTA a 64 x 64 tile.
 // ---------------------------------------------------------------------------
-template <typename T, bool BACK>
+template <bool BACK>
 __global__ void __launch_bounds__(kT) lin_local_kernel(SeqArgs a, float* local, float* gend) {
     const SeqShape& sh = a.sh;
     griddep_wait();
@@ -150,8 +145,8 @@ __global__ void __launch_bounds__(kT) lin_local_kernel(SeqArgs a, float* local, 
     load_gates(g, a, first, rows, h);
     if (threadIdx.x < kSegF) w[threadIdx.x] = BACK ? g.head[threadIdx.x] : g.beta[threadIdx.x] * g.tail[threadIdx.x];
     if (threadIdx.x == 0 && blockIdx.y == 0) gend[(size_t)slot * sh.H + h] = g.end;
-    const Mat<T> A = columns(token_rows<T>(BACK ? a.dout : a.v, BACK ? (size_t)sh.H * sh.dv : sh.ldv, first, rows, h, sh.dv), r0);
-    const Mat<T> B = columns(token_rows<T>(BACK ? a.q : a.k, BACK ? sh.ldq : sh.ldk, first, rows, hk, sh.dk), c0);
+    const Mat A = columns(token_rows(BACK ? a.dout : a.v, BACK ? (size_t)sh.H * sh.dv : sh.ldv, first, rows, h, sh.dv), r0);
+    const Mat B = columns(token_rows(BACK ? a.q : a.k, BACK ? sh.ldq : sh.ldk, first, rows, hk, sh.dk), c0);
     Acc acc;
     clear(acc);
     for (int k = 0; k < kSegF; k += kK) {
@@ -180,7 +175,7 @@ __global__ void __launch_bounds__(kT) lin_local_kernel(SeqArgs a, float* local, 
 // ---------------------------------------------------------------------------
 enum { kOut, kDq, kDk, kDv };
 
-template <typename T, int MODE>
+template <int MODE>
 __global__ void __launch_bounds__(kT) lin_rows_kernel(SeqArgs a, const float* states, float* part) {
     constexpr bool keys = MODE == kDk || MODE == kDv, value_cols = MODE == kOut || MODE == kDv;
     const SeqShape& sh = a.sh;
@@ -190,7 +185,7 @@ __global__ void __launch_bounds__(kT) lin_rows_kernel(SeqArgs a, const float* st
     const int slot = blockIdx.x / heads, head = blockIdx.x % heads, n0 = blockIdx.y * 64;
     void* out = MODE == kOut ? a.out : MODE == kDq ? a.dq : MODE == kDk ? a.dk : a.dv;
     int ob, oe;
-    if (blockIdx.y == 0 && seq_outside(sh, ob, oe)) zero_rows<T>(out, (size_t)heads * dx, ob, oe, sh.total);
+    if (blockIdx.y == 0 && seq_outside(sh, ob, oe)) zero_rows<float>(out, (size_t)heads * dx, ob, oe, sh.total);
     int s, c, first, rows;
     if (!slot_segment(sh, kSegF, slot, s, c, first, rows, a.err)) return;
     __shared__ Gates g;
@@ -204,18 +199,18 @@ __global__ void __launch_bounds__(kT) lin_rows_kernel(SeqArgs a, const float* st
         const int h = value_cols ? head : head * rep + r, hk = value_cols ? head / rep : head;
         __syncthreads();
         load_gates(g, a, first, rows, h);
-        const Mat<T> q = token_rows<T>(a.q, sh.ldq, first, rows, hk, sh.dk), k = token_rows<T>(a.k, sh.ldk, first, rows, hk, sh.dk),
-                     v = token_rows<T>(a.v, sh.ldv, first, rows, h, sh.dv), o = token_rows<T>(a.dout, ldo, first, rows, h, sh.dv);
-        const Mat<T> A = MODE == kOut ? q : MODE == kDq ? o : MODE == kDk ? v : k, B = MODE == kOut ? k : MODE == kDq ? v : MODE == kDk ? o : q,
-                     X = columns(MODE == kOut ? v : MODE == kDq ? k : MODE == kDk ? q : o, n0);
+        const Mat q = token_rows(a.q, sh.ldq, first, rows, hk, sh.dk), k = token_rows(a.k, sh.ldk, first, rows, hk, sh.dk),
+                  v = token_rows(a.v, sh.ldv, first, rows, h, sh.dv), o = token_rows(a.dout, ldo, first, rows, h, sh.dv);
+        const Mat A = MODE == kOut ? q : MODE == kDq ? o : MODE == kDk ? v : k, B = MODE == kOut ? k : MODE == kDq ? v : MODE == kDk ? o : q,
+                  X = columns(MODE == kOut ? v : MODE == kDq ? k : MODE == kDk ? q : o, n0);
         const float* S = states + ((size_t)slot * sh.H + h) * sh.dv * sh.dk;
         Acc y;
         clear(y);
         if (value_cols) {
-            const Mat<float> M = {S + (size_t)n0 * sh.dk, (size_t)sh.dk, sh.dv - n0, sh.dk};
+            const Mat M = {S + (size_t)n0 * sh.dk, (size_t)sh.dk, sh.dv - n0, sh.dk};
             product<false>(y, st, A, M, dc);
         } else {
-            const Mat<float> M = {S + n0, (size_t)sh.dk, sh.dv, sh.dk - n0};
+            const Mat M = {S + n0, (size_t)sh.dk, sh.dv, sh.dk - n0};
             product<true>(y, st, A, M, dc);
         }
 #pragma unroll
@@ -228,7 +223,7 @@ __global__ void __launch_bounds__(kT) lin_rows_kernel(SeqArgs a, const float* st
             }
         }
         if (MODE == kDq || MODE == kDv) {       // these columns' share of the row's dot with q or v
-            const Mat<T> z = columns(MODE == kDq ? q : v, n0);
+            const Mat z = columns(MODE == kDq ? q : v, n0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float4 zi = z.at(m + i, n);
@@ -258,12 +253,12 @@ __global__ void __launch_bounds__(kT) lin_rows_kernel(SeqArgs a, const float* st
             tile_mul(acc, w + k0, st.b);
         }
     }
-    T* p = static_cast<T*>(out) + ((size_t)first * heads + head) * dx;
+    float* p = static_cast<float*>(out) + ((size_t)first * heads + head) * dx;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (m + i < rows && n0 + n + j < dx) st_elem<T>(p + (size_t)(m + i) * heads * dx, n0 + n + j, acc[i][j]);
+            if (m + i < rows && n0 + n + j < dx) p[(size_t)(m + i) * heads * dx + n0 + n + j] = acc[i][j];
 }
 
 // ---------------------------------------------------------------------------
@@ -272,7 +267,6 @@ __global__ void __launch_bounds__(kT) lin_rows_kernel(SeqArgs a, const float* st
 //   dbeta_s      = sum_{t >= s} E_ts / beta_s + v_s.(e^{G - g_s} dS k_s)
 // The first sum is that of rows minus columns from u on: the terms of a segment only, in fp32.
 // ---------------------------------------------------------------------------
-template <typename T>
 __global__ void __launch_bounds__(kT) lin_gates_kernel(SeqArgs a, const float* part_q, int tiles_q, const float* part_k, int tiles_k,
                                                        const float* phi, int tiles_phi) {
     const SeqShape& sh = a.sh;
@@ -294,8 +288,8 @@ __global__ void __launch_bounds__(kT) lin_gates_kernel(SeqArgs a, const float* p
     Acc x, y;
     clear(x);
     clear(y);
-    product<false>(x, st, token_rows<T>(a.q, sh.ldq, first, rows, hk, sh.dk), token_rows<T>(a.k, sh.ldk, first, rows, hk, sh.dk), sh.dk);
-    product<false>(y, st, token_rows<T>(a.dout, (size_t)sh.H * sh.dv, first, rows, h, sh.dv), token_rows<T>(a.v, sh.ldv, first, rows, h, sh.dv), sh.dv);
+    product<false>(x, st, token_rows(a.q, sh.ldq, first, rows, hk, sh.dk), token_rows(a.k, sh.ldk, first, rows, hk, sh.dk), sh.dk);
+    product<false>(y, st, token_rows(a.dout, (size_t)sh.H * sh.dv, first, rows, h, sh.dv), token_rows(a.v, sh.ldv, first, rows, h, sh.dv), sh.dv);
     float cs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -468,10 +462,10 @@ cudaError_t forward_f32(const SeqArgs& a, cudaStream_t st) {
     float* states = reinterpret_cast<float*>(a.rec != nullptr ? a.rec : a.ws + L.ws_local);
     float* gend = reinterpret_cast<float*>(a.ws + L.ws_gend);
     const unsigned sth = (unsigned)((size_t)seg_slots(sh.nseq, sh.total, kSegF) * sh.H), tk = (sh.dk + 63) / 64, tv = (sh.dv + 63) / 64;
-    cudaError_t e = launch_kernel(lin_local_kernel<float, false>, dim3(sth, tk * tv), dim3(kT), 0, st, false, a, states, gend);
+    cudaError_t e = launch_kernel(lin_local_kernel<false>, dim3(sth, tk * tv), dim3(kT), 0, st, false, a, states, gend);
     if (e == cudaSuccess) e = launch_linear_scan(sh, kSegF, 0, false, states, gend, 1, a.S0, states, 0, nullptr, nullptr, a.S_T, a.err, st);
     if (e == cudaSuccess && sh.total > 0)
-        e = launch_kernel(lin_rows_kernel<float, kOut>, dim3(sth, tv), dim3(kT), 0, st, true, a, (const float*)states, (float*)nullptr);
+        e = launch_kernel(lin_rows_kernel<kOut>, dim3(sth, tv), dim3(kT), 0, st, true, a, (const float*)states, (float*)nullptr);
     return e;
 }
 
@@ -484,14 +478,14 @@ cudaError_t backward_f32(const SeqArgs& a, cudaStream_t st) {
     const size_t slots = seg_slots(sh.nseq, sh.total, kSegF);
     const unsigned sth = (unsigned)(slots * sh.H), stk = (unsigned)(slots * sh.Hk), tk = (sh.dk + 63) / 64, tv = (sh.dv + 63) / 64;
     float *part_q = reinterpret_cast<float*>(a.ws + L.ws_part), *part_k = part_q + slots * sh.H * tk * kSegF;
-    cudaError_t e = launch_kernel(lin_local_kernel<float, true>, dim3(sth, tk * tv), dim3(kT), 0, st, false, a, ends, gend);
+    cudaError_t e = launch_kernel(lin_local_kernel<true>, dim3(sth, tk * tv), dim3(kT), 0, st, false, a, ends, gend);
     if (e == cudaSuccess) e = launch_linear_scan(sh, kSegF, 0, true, ends, gend, 1, a.dS_T, ends, 0, starts, phi, a.dS0, a.err, st);
     if (e != cudaSuccess || sh.total == 0) return e;
-    e = launch_kernel(lin_rows_kernel<float, kDq>, dim3(stk, tk), dim3(kT), 0, st, true, a, starts, part_q);
-    if (e == cudaSuccess) e = launch_kernel(lin_rows_kernel<float, kDk>, dim3(stk, tk), dim3(kT), 0, st, true, a, (const float*)ends, (float*)nullptr);
-    if (e == cudaSuccess) e = launch_kernel(lin_rows_kernel<float, kDv>, dim3(sth, tv), dim3(kT), 0, st, true, a, (const float*)ends, part_k);
+    e = launch_kernel(lin_rows_kernel<kDq>, dim3(stk, tk), dim3(kT), 0, st, true, a, starts, part_q);
+    if (e == cudaSuccess) e = launch_kernel(lin_rows_kernel<kDk>, dim3(stk, tk), dim3(kT), 0, st, true, a, (const float*)ends, (float*)nullptr);
+    if (e == cudaSuccess) e = launch_kernel(lin_rows_kernel<kDv>, dim3(sth, tv), dim3(kT), 0, st, true, a, (const float*)ends, part_k);
     if (e == cudaSuccess)
-        e = launch_kernel(lin_gates_kernel<float>, dim3(sth), dim3(kT), 0, st, true, a, (const float*)part_q, (int)tk, (const float*)part_k,
+        e = launch_kernel(lin_gates_kernel, dim3(sth), dim3(kT), 0, st, true, a, (const float*)part_q, (int)tk, (const float*)part_k,
                           (int)tv, (const float*)phi, scan_tiles(sh));
     return e;
 }
@@ -517,7 +511,7 @@ using namespace check;
 
 bool shape_ok(const SeqShape& s) {
     if (s.nseq < 1 || s.total < 0 || s.H < 1 || s.Hk < 1 || s.H % s.Hk != 0 || !dim_ok(s.dk) || !dim_ok(s.dv)) return false;
-    if ((long long)s.nseq + s.total > (1LL << 30)) return false;
+    if ((long long)s.nseq + s.total > (1LL << 30) || s.Hk > 1 << 18) return false;
     // grid sizes: (sequence, head, piece of the state), and (slot, head) or four blocks of it
     return (long long)s.nseq * s.H * scan_tiles(s) <= 0x7fffffffLL && (long long)seg_slots(s.nseq, s.total, kSegF) * s.H <= 0x7fffffffLL &&
            (long long)seg_slots(s.nseq, s.total, kLinSegment) * s.H * 4 <= 0x7fffffffLL;

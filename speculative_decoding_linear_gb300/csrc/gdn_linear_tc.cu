@@ -188,7 +188,8 @@ constexpr uint32_t kBox = 64 * 128;
 // 2^17 tokens; the terms go to TMEM, where each thread holds one row of d_v.  b is bf16 and exact.  The tensor core cuts
 // off what does not fit 24 bits at each addition, always toward zero, 1.5e-8 of the sum: so a sum is of 256 tokens, and
 // the second half's is added to the first's in memory, rounded (1.7e-6 of the sum off after 512 tokens in one sum, 9e-7 so).
-// Bound by the products: three for each of the state's, 6.2 k cycles a tile.  Warps 0-7 form the terms (four warps 32
+// Bound by the products, three for each of the state's, and by forming their operands: 8192 tokens of 8 heads, 256 x 256, 34 us
+// (760 TFLOP/s of products, tensor core busy 40 % of the time; a CTA has 3 or 4 of the 512 tiles).  Warps 0-7 form the terms (four warps 32
 // tokens, two buffers each), 8-11 move the sums out (two in TMEM) by way of shared memory, 12 copies, 13 multiplies.
 // ---------------------------------------------------------------------------
 constexpr int kLocalThreads = 448, kLocalStages = 5, kLocalTok = 64, kLocalHalf = 256;
@@ -443,16 +444,19 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
 // with S the state at the segment's start, dS the gradient at its end.
 //
 // The sum of products stays in TMEM: first the state's product, whose rows the workers scale there, then for each
-// block of 128 tokens the scores (A and B from shared memory), which the workers read, decay, round to bf16 and write
-// back in place as the A operand of the product with X (tokens x columns, from shared memory as it lies).
-// kDq and kDv carry the state as three bf16 terms: q_t.(e^{g_t} S^T dO_t) and v_s.(e^{G - g_s} dS k_s), which the gates'
-// fp32 gradients need, are taken from those fp32 sums.  kOut and kDk read one term, and all round the scores once: each
-// term of a bf16 output is off by one rounding of half a step, beside the output's own.
+// block of 128 tokens the scores (A and B from shared memory), which the workers read, decay, split into two bf16 terms and
+// write back in place as the A operands of the products with X (tokens x columns, from shared memory as it lies).
+// Two terms of a score or a state leave 2^-17 of it, so a bf16 output has its own rounding only (with one term of each the
+// error against 64 bits was 2.3e-3 for 1.7e-3; 1 x 8192 tokens 46 us, and 54 with two).  kDq and kDv carry the state as three:
+// q_t.(e^{g_t} S^T dO_t) and v_s.(e^{G - g_s} dS k_s), which the gates' fp32 gradients need, are taken from those fp32 sums.
 //
 // A CTA an SM takes block after block of rows; the scores of a block of columns, be it the next rows' first, are formed
 // before the product of the one before it, so that the workers' pass over scores runs beside products.  Warps 0-7 work
-// (four a half of the columns), 8-11 move finished sums out, 12
-// copies, 13 multiplies.
+// (four a half of the columns), 8-11 move finished sums out, 12 copies, 13 multiplies.
+// 8192 tokens of 8 heads, 256 x 256, caches cold: kOut 54 us, kDk 57, kDq and kDv 79 (900 to 800 TFLOP/s of products; tensor
+// core busy 47 and 38 % of an SM's time).  Bound by the chain of a block: scores, the workers' pass (some 1.4 k cycles), and
+// the state's product with its scaling (4 k) at the start of each item, which the next item's scores cover in part only: two
+// sums of 256 columns do not fit TMEM beside two blocks' scores.
 // ---------------------------------------------------------------------------
 enum { kOut, kDq, kDk, kDv };
 constexpr int kRowThreads = 448, kMaxRing = 8;
@@ -661,7 +665,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         };
         uint32_t items = 0, blocks = 0;                   // sums, and blocks of scores, so far
         RowsItem<MODE> after;
-        int turns = 0, p_rows = 0;                                   // tokens of the block of columns before
+        int turns = 0, p_rows = 0;                        // p_rows: tokens of the block of columns before
         bool p_last = false;
         for (int j = 0, pj = -1;;) {
             const bool last = !warp_uniform(it.there()), x_first = last || (j == 0 && p.nr == 1);
@@ -1003,7 +1007,8 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 // ---------------------------------------------------------------------------
 // Sums of F_ts = e^{g_t - g_s} (q_t.k_s) (dO_t.v_s), s < t, of 128 rows t with the segment's blocks up to theirs: by
 // rows with beta_s, by columns without, and F_tt.  Both scores are products of bf16 inputs, exact but for fp32 sums.
-// Warps 0-7 work, warp 8 copies, warp 9 multiplies.
+// Warps 0-7 work, warp 8 copies, warp 9 multiplies; a CTA a block of rows, two an SM, the longest first.  8192 tokens of 8
+// heads, 256 x 256: 51 us, tensor core busy 22 % of the time: bound by the workers' pass over two scores of each pair.
 // ---------------------------------------------------------------------------
 // floats of a (slot, head): rows, F_tt, q's and v's dots by halves, columns by block of rows
 constexpr int kPartRow = 0, kPartDiag = kSeg, kPartQ = 2 * kSeg, kPartK = 4 * kSeg, kPartCol = 6 * kSeg, kPartAll = 10 * kSeg;
