@@ -896,11 +896,20 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                 if (j == 0) {                             // the next item's gates; the state's product: its rows scaled
                     it.look(++turns, table, sh, slots, rep);
                     if (it.there()) load_gates();
+                    const __nv_bfloat16* z = MODE == kDq ? static_cast<const __nv_bfloat16*>(a.q) + token * sh.ldq + (size_t)hk * sh.dk
+                                                         : static_cast<const __nv_bfloat16*>(a.v) + token * sh.ldv + (size_t)cur.h * sh.dv;
+                    constexpr bool dots = MODE == kDq || MODE == kDv;
+                    uint4 w[3][2] = {};                   // q's or v's columns, three chunks on their way
+                    const auto load = [&](uint4 (&x)[2], int ch) {
+                        if (!dots || !live || ch >= ch1) return;
+                        x[0] = *reinterpret_cast<const uint4*>(z + 16 * ch);
+                        x[1] = *reinterpret_cast<const uint4*>(z + 16 * ch + 8);
+                    };
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) load(w[e], ch0 + e);
                     wait_here(inter_done, items & 1, a.err, dead);
                     __syncwarp();
                     tc_fence_after();
-                    const __nv_bfloat16* z = MODE == kDq ? static_cast<const __nv_bfloat16*>(a.q) + token * sh.ldq + (size_t)hk * sh.dk
-                                                         : static_cast<const __nv_bfloat16*>(a.v) + token * sh.ldv + (size_t)cur.h * sh.dv;
                     float dot = 0.f;
 #pragma unroll 1
                     for (int ch = ch0; ch < ch1; ++ch) {
@@ -910,14 +919,19 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(sf * __uint_as_float(x[c]));
                         tmem_st_n(acc + 16 * ch, x);
-                        if ((MODE == kDq || MODE == kDv) && live) {   // q's or v's columns
-                            float y[8];
+                        if (dots) {
+                            const uint32_t y[8] = {w[0][0].x, w[0][0].y, w[0][0].z, w[0][0].w, w[0][1].x, w[0][1].y, w[0][1].z, w[0][1].w};
 #pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                ld8<__nv_bfloat16>(z + 16 * ch + 8 * half, y);
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) dot = fmaf(__uint_as_float(x[8 * half + c]), y[c], dot);
+                            for (int c = 0; c < 8; ++c) {
+                                dot = fmaf(__uint_as_float(x[2 * c]), __uint_as_float(y[c] << 16), dot);
+                                dot = fmaf(__uint_as_float(x[2 * c + 1]), __uint_as_float(y[c] & 0xffff0000u), dot);
                             }
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                w[0][e] = w[1][e];
+                                w[1][e] = w[2][e];
+                            }
+                            load(w[2], ch + 3);
                         }
                         __syncwarp();
                     }
@@ -966,11 +980,16 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < dx; c += 16) {
-                uint32_t v[16];
-                tmem_ld_n(acc + c, v);
+            for (int c0 = 0; c0 < dx; c0 += 32) {
+                uint32_t vs[2][16];
+                tmem_ld_n(acc + c0, vs[0]);
+                if (c0 + 16 < dx) tmem_ld_n(acc + c0 + 16, vs[1]);
                 tmem_wait_ld();
-                if (live) {
+#pragma unroll
+                for (int e2 = 0; e2 < 2; ++e2) {
+                    const int c = c0 + 16 * e2;
+                    const uint32_t (&v)[16] = vs[e2];
+                    if (!live || c >= dx) break;
                     float y[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) y[e] = of * __uint_as_float(v[e]);
