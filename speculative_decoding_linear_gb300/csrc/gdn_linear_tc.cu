@@ -483,7 +483,9 @@ struct RowGates {
 };
 // behind the barriers
 constexpr int kRowNBars = 2 * kMaxRing + 17;
-constexpr uint32_t kRowHolder = kRowNBars * 8, kRowGates = (kRowHolder + 8 + 15) / 16 * 16, kRowTail = kRowGates + 2 * sizeof(RowGates);
+constexpr int kRowItems = 64;  // of a CTA that stand in shared memory
+constexpr uint32_t kRowHolder = kRowNBars * 8, kRowGates = (kRowHolder + 8 + 15) / 16 * 16, kRowList = kRowGates + 2 * sizeof(RowGates),
+                   kRowTail = kRowList + kRowItems * 16;
 static_assert(sizeof(RowGates) % 16 == 0, "read by 16 bytes");
 
 // A CTA's item of a turn: (slot, first token, rows + 1024 x blocks of columns + 8192 x its head of q and k, head), rows 0
@@ -491,7 +493,9 @@ static_assert(sizeof(RowGates) % 16 == 0, "read by 16 bytes");
 // another order each turn, so that a CTA's turns bring long and short ones; then the shorter segments' items from the
 // longest to the shortest.  (Everything from the longest to the shortest balances as well but reads all tiles at once:
 // 4 x 2048 tokens forward and backward 440 us for 410.  Shorter segments by segment too: packed prompts 99 us for 87.)
-// Called, not inlined: four roles look for items, and the instruction cache is small.
+// A chain of loads and divisions of some 3 k cycles: a CTA's first items are looked up at once when it starts, each by a
+// thread (by each role before its next item, a seventh of the products' issuing went there).  Called, not inlined: four roles
+// ask for items, and the instruction cache is small.
 __device__ __noinline__ int4 rows_item(int turn, const int* order, const int2* table, int slots, int H, int rep, int total) {
     constexpr int kMost = kSeg / kBlk;
     const int i = turn * gridDim.x + blockIdx.x, n_most = min(max(order[kMost - 1], 0), slots);
@@ -515,9 +519,9 @@ __device__ __noinline__ int4 rows_item(int turn, const int* order, const int2* t
 template <int MODE>
 struct RowsItem {
     int slot, h, hk, rb, first, rows, row_n, nblk;
-    __device__ __forceinline__ void look(int turn, const int2* table, const SeqShape& sh, int slots, int rep) {
+    __device__ __forceinline__ void look(int turn, const int4* list, const int2* table, const SeqShape& sh, int slots, int rep) {
         constexpr bool keys = MODE == kDk || MODE == kDv;
-        const int4 e = rows_item(turn, slot_order(table, slots), table, slots, sh.H, rep, sh.total);
+        const int4 e = turn < kRowItems ? list[turn] : rows_item(turn, slot_order(table, slots), table, slots, sh.H, rep, sh.total);
         slot = e.x;
         first = e.y;
         rows = e.z & 1023;
@@ -574,14 +578,16 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         int ob, oe;
         if (seq_outside(sh, ob, oe)) zero_rows<__nv_bfloat16>(out, (size_t)out_heads * dx, ob, oe, sh.total);
     }
+    int4* list = reinterpret_cast<int4*>(tail + kRowList);
+    if (tid < kRowItems) list[tid] = rows_item(tid, slot_order(table, slots), table, slots, sh.H, rep, sh.total);
+    __syncthreads();
     // Scores and products of a CTA's blocks of columns, one after another over its items, interleaved: the scores of a
     // block before the product of the one before it, the state's product behind the first scores of its rows.  The rows'
     // operand is used up by its last scores (or the state's product): the next rows' arrives while the workers have those,
     // and with one place for it an item's first scores come behind the last product of the item before (75 k cycles a CTA
     // of 8192 tokens for 70 the other way around).
-    // A next item is looked up while its predecessor's first block is on its way.
     RowsItem<MODE> it;
-    it.look(0, table, sh, slots, rep);
+    it.look(0, list, table, sh, slots, rep);
     if (warp == 12) {
         if (elect_one()) {
             const bool whole_a = da % 64 == 0, whole_x = dx % 64 == 0;
@@ -633,7 +639,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                     }
                 }
                 if (last) break;
-                if (j == 0) after.look(++turns, table, sh, slots, rep);
+                if (j == 0) after.look(++turns, list, table, sh, slots, rep);
                 prev = it;
                 pj = j;
                 if (++j == it.nblk) {
@@ -748,7 +754,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
             if (pj >= 0 && p_last) ++items;
             if (last) break;
             ++blocks;
-            if (j == 0) after.look(++turns, table, sh, slots, rep);
+            if (j == 0) after.look(++turns, list, table, sh, slots, rep);
             p_rows = warp_uniform(it.col_rows(j));
             p_last = warp_uniform(j + 1 == it.nblk);
             pj = j;
@@ -894,7 +900,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
                 }
                 tmem_wait_st();
                 if (j == 0) {                             // the next item's gates; the state's product: its rows scaled
-                    it.look(++turns, table, sh, slots, rep);
+                    it.look(++turns, list, table, sh, slots, rep);
                     if (it.there()) load_gates();
                     const __nv_bfloat16* z = MODE == kDq ? static_cast<const __nv_bfloat16*>(a.q) + token * sh.ldq + (size_t)hk * sh.dk
                                                          : static_cast<const __nv_bfloat16*>(a.v) + token * sh.ldv + (size_t)cur.h * sh.dv;
@@ -968,7 +974,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         const int w4 = warp & 3, row = 32 * w4 + lane;
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
         const bool shared = !values && rep > 1, whole = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
-        for (uint32_t items = 0; it.there(); it.look(++items, table, sh, slots, rep)) {
+        for (uint32_t items = 0; it.there(); it.look(++items, list, table, sh, slots, rep)) {
             const uint32_t ab = two_sums ? items & 1 : 0, ap = two_sums ? items >> 1 & 1 : items & 1, acc = tmem + 128 * ab + lanes;
             const bool live = row < it.row_n;
             const size_t token = (size_t)it.first + it.rb * kBlk + row;
