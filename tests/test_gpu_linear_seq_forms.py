@@ -150,3 +150,58 @@ def test_rows_do_not_depend_on_later_tokens():
     got = torch.empty_like(want)
     gdnspec.gdn_linear_seq_forward(*(x[m] for m in NAMES), got, S_T, ws, offsets=off)
     assert torch.equal(got[:600], want[:600])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_decay_of_zero_starts_anew(dtype):
+    """log_alpha = -inf at a token: from there on as a sequence of its own from a state of zero, gradients too."""
+    lengths, cut = [900], 333
+    x, off, dout, dS = inputs(lengths, 2, 1, 64, 64, seed=11)
+    x, dout = {m: y.to(dtype) if m in "qkv" else y for m, y in x.items()}, dout.to(dtype)
+    x["log_alpha"][cut] = -float("inf")
+    full = (1, 900, 2, 1, 64, 64, dtype)
+    d = outputs(x)
+    both(x, off, dout, dS, d, gdnspec.empty_linear_seq_workspace(*full), gdnspec.empty_linear_seq_record(*full))
+    parts = [{m: (y[:cut] if i == 0 else y[cut:]) if m != "S0" else (y if i == 0 else 0 * y) for m, y in x.items()} for i in range(2)]
+    parts[1]["log_alpha"] = parts[1]["log_alpha"].clone()
+    parts[1]["log_alpha"][0] = 0.0
+    a = plain(parts[0], [cut], dout[:cut], 0 * dS)
+    b = plain(parts[1], [900 - cut], dout[cut:], dS)
+    for m in ("out", "dq", "dk", "dv", "dbeta"):
+        held(d[m], torch.cat([a[m], b[m]]), m)
+    held(d["S_T"], b["S_T"], "S_T")
+    held(d["dS0"], a["dS0"], "dS0")
+    # Nothing passes the cut, so its gradient is zero.  It is formed as sums over the rows from the cut on minus sums over the
+    # columns: E_ts of each pair behind it stands in one of either, rounded apart, so the two cancel to their roundings only,
+    # as many as any gradient of the array has: sqrt(4096) x 2^-24 of the sums' size, which is that of the largest gradient.
+    assert d["dlog_alpha"][cut].abs().max() <= 4e-6 * d["dlog_alpha"].abs().max()
+    keep = torch.arange(900, device="cuda") != cut
+    held(d["dlog_alpha"][keep], torch.cat([a["dlog_alpha"], b["dlog_alpha"]])[keep], "dlog_alpha")
+
+
+def test_rows_past_32_bits_of_offsets():
+    """The last sequence of a batch whose rows lie beyond 2^31 elements: to the bit what it is alone."""
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("takes 70 GB")
+    dims, lengths = (8, 8, 256, 256), [(1 << 20) + 64, 700]
+    total = sum(lengths)
+    x = {m: torch.empty(total, 8, 256, dtype=torch.bfloat16, device="cuda").normal_(0, 1 / 16) for m in "qkv"}
+    x["log_alpha"] = -torch.rand(total, 8, device="cuda")
+    x["beta"] = torch.rand(total, 8, device="cuda")
+    x["S0"] = 0.1 * torch.randn(2, 8, 256, 256, device="cuda")
+    dout, dS = torch.empty_like(x["v"]).normal_(), torch.randn(2, 8, 256, 256, device="cuda")
+
+    def run(x, lengths, dout, dS):
+        full = (len(lengths), sum(lengths), *dims, torch.bfloat16)
+        d = {"out": torch.empty_like(x["v"]), "S_T": torch.empty_like(x["S0"])}
+        d.update({"d" + m: torch.empty_like(x[m]) for m in NAMES})
+        off = torch.tensor(np.cumsum([0] + lengths), dtype=torch.int32, device="cuda")
+        both(x, off, dout, dS, d, gdnspec.empty_linear_seq_workspace(*full), gdnspec.empty_linear_seq_record(*full))
+        assert gdnspec.gdn_last_error() == gdnspec.OK
+        return d
+
+    got = run(x, lengths, dout, dS)
+    want = run({m: (y[1:] if m == "S0" else y[lengths[0]:]).contiguous() for m, y in x.items()}, lengths[1:], dout[lengths[0]:].contiguous(), dS[1:].contiguous())
+    for m in want:
+        y = got[m][1:] if m in ("S_T", "dS0") else got[m][lengths[0]:]
+        assert torch.equal(y, want[m]), m
