@@ -1032,7 +1032,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 // ---------------------------------------------------------------------------
 // Sums of F_ts = e^{g_t - g_s} (q_t.k_s) (dO_t.v_s), s < t, of 128 rows t with the segment's blocks up to theirs: by
 // rows with beta_s, by columns without, and F_tt.  Both scores are products of bf16 inputs, exact but for fp32 sums.
-// Warps 0-7 work, warp 8 copies, warp 9 multiplies; a CTA a block of rows, two an SM, the longest first.  8192 tokens of 8
+// Warps 0-7 work, warp 8 copies, warp 9 multiplies; a CTA a block of rows, two an SM where both fit, the longest first.  8192 tokens of 8
 // heads, 256 x 256: 51 us, tensor core busy 22 % of the time: bound by the workers' pass over two scores of each pair.
 // ---------------------------------------------------------------------------
 // floats of a (slot, head): rows, F_tt, q's and v's dots by halves, columns by block of rows
@@ -1099,23 +1099,24 @@ __global__ void __launch_bounds__(kPairThreads, 2)
     tc_fence_after();
     if (warp == 8) {
         if (elect_one()) {
-            const auto slab = [&](uint32_t dst, const CUtensorMap* m, int x, int head, int t0, int n, uint32_t bar) {
-                tma_3d(dst, m, 64 * x, head, t0, bar);
-                if (n > 64) tma_3d(dst + kBox, m, 64 * x, head, t0 + 64, bar);
-            };
-            mbar_expect_tx(rfull, (nk + nv) * (row_n > 64 ? 2 : 1) * kBox);
-            for (int x = 0; x < nk; ++x) slab(base + x * 2 * kBox, &mq, x, hk, first + rb * kBlk, row_n, rfull);
-            for (int x = 0; x < nv; ++x) slab(base + p.r2 + x * 2 * kBox, &mo, x, h, first + rb * kBlk, row_n, rfull);
+            // slab x of 128 tokens, or (the rows' own) all slabs in one box where the map has whole ones
+            const bool whole_k = sh.dk % 64 == 0, whole_v = sh.dv % 64 == 0;
+            mbar_expect_tx(rfull, (nk + nv) * 2 * kBox);
+#pragma unroll 1
+            for (int x = 0; x < (whole_k ? 1 : nk); ++x) tma_4d(base + x * 2 * kBox, &mq, 64 * x, hk, first + rb * kBlk, 0, rfull);
+#pragma unroll 1
+            for (int x = 0; x < (whole_v ? 1 : nv); ++x) tma_4d(base + p.r2 + x * 2 * kBox, &mo, 64 * x, h, first + rb * kBlk, 0, rfull);
+            Ring ring;
             int it = 0;
             bool ok = true;
             for (int j = 0; ok && j <= rb; ++j)
-                for (int x = 0; ok && x < nk + nv; ++x) {
-                    const int st = it % p.ring;
-                    if (it >= p.ring && !(ok = wait_here(empty0 + 8 * st, (it / p.ring + 1) & 1, a.err, dead))) break;
-                    mbar_expect_tx(full0 + 8 * st, (col_rows(j) > 64 ? 2 : 1) * kBox);
-                    if (x < nk) slab(base + p.stages + st * 2 * kBox, &mk, x, hk, first + j * kBlk, col_rows(j), full0 + 8 * st);
-                    else slab(base + p.stages + st * 2 * kBox, &mv, x - nk, h, first + j * kBlk, col_rows(j), full0 + 8 * st);
-                    ++it;
+#pragma unroll 1
+                for (int x = 0; x < nk + nv; ++x, ++it, ring.next(p.ring)) {
+                    if (it >= p.ring && !(ok = wait_here(empty0 + 8 * ring.st, ring.ph ^ 1, a.err, dead))) break;
+                    const bool is_k = x < nk, whole = is_k ? whole_k : whole_v;
+                    const int sl = is_k ? x : x - nk;
+                    mbar_expect_tx(full0 + 8 * ring.st, 2 * kBox);
+                    tma_4d(base + p.stages + ring.st * 2 * kBox, is_k ? &mk : &mv, whole ? 0 : 64 * sl, is_k ? hk : h, first + j * kBlk, whole ? sl : 0, full0 + 8 * ring.st);
                 }
             if (*dead) {                                  // copies in flight end before the CTA does
                 wait_here(rfull, 0, a.err, nullptr);
@@ -1478,8 +1479,8 @@ cudaError_t pairs_go(const SeqArgs& a, const float* gates, float* part, cudaStre
     static bool done[64];
     const SeqShape& sh = a.sh;
     CUtensorMap q, k, v, o;
-    if (!token_map(&q, a.q, sh, sh.dk, sh.Hk, sh.ldq) || !token_map(&k, a.k, sh, sh.dk, sh.Hk, sh.ldk) || !token_map(&v, a.v, sh, sh.dv, sh.H, sh.ldv) ||
-        !token_map(&o, a.dout, sh, sh.dv, sh.H, (long long)sh.H * sh.dv))
+    if (!slab_map(&q, a.q, sh, sh.dk, sh.Hk, sh.ldq, kBlk, sh.dk / 64) || !slab_map(&k, a.k, sh, sh.dk, sh.Hk, sh.ldk, kBlk, 1) ||
+        !slab_map(&v, a.v, sh, sh.dv, sh.H, sh.ldv, kBlk, 1) || !slab_map(&o, a.dout, sh, sh.dv, sh.H, (long long)sh.H * sh.dv, kBlk, sh.dv / 64))
         return cudaErrorInvalidValue;
     PairsPlan p = {};
     p.r2 = (sh.dk + 63) / 64 * 2 * kBox;
