@@ -193,9 +193,10 @@ constexpr uint32_t kBox = 64 * 128;
 // tokens, two buffers each), 8-11 move the sums out (two in TMEM) by way of shared memory, 12 copies, 13 multiplies.
 // ---------------------------------------------------------------------------
 constexpr int kLocalThreads = 448, kLocalStages = 5, kLocalTok = 64, kLocalHalf = 256;
+constexpr int kLocalListed = 256;
 constexpr uint32_t kLocalStage = 4 * kBox;                       // two boxes of a, two of b
 constexpr uint32_t kLocalOut = kLocalStages * kLocalStage, kLocalCoef = kLocalOut + 128 * 128 * 4, kLocalBars = kLocalCoef + kLocalStages * kLocalTok * 4,
-                   kLocalNBars = 2 * kLocalStages + 13, kLocalSmem = kLocalBars + 8 * kLocalNBars + 16;
+                   kLocalNBars = 2 * kLocalStages + 13, kLocalList = kLocalBars + 8 * kLocalNBars + 16, kLocalSmem = kLocalList + kLocalListed;
 constexpr uint32_t kLocalA = 256, kLocalABuf = 48;               // TMEM: two sums, then four buffers of three terms of 16
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, bool add) {
@@ -216,13 +217,37 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;\n" ::: "memory"); }
 
-struct LocalItems {            // tile i of the launch; empty slots have none
+// The slots by their blocks of tokens, most first, where a list in shared memory holds them; one warp.
+__device__ __noinline__ void list_slots(const int2* table, int slots, int total, unsigned char* list) {
+    const int lane = threadIdx.x & 31;
+    int blocks[kLocalListed / 32], at = 0;
+#pragma unroll
+    for (int j = 0; j < kLocalListed / 32; ++j) {
+        const int s = 32 * j + lane;
+        blocks[j] = s < slots ? (slot_entry(table, s, total).y + kBlk - 1) / kBlk : -1;
+    }
+#pragma unroll 1
+    for (int b = kSeg / kBlk; b >= 0; --b)
+#pragma unroll
+        for (int j = 0; j < kLocalListed / 32; ++j) {
+            const unsigned m = __ballot_sync(0xffffffffu, blocks[j] == b);
+            if (blocks[j] == b) list[at + __popc(m & ((1u << lane) - 1))] = (unsigned char)(32 * j + lane);
+            at += __popc(m);
+        }
+}
+// Tile i of the launch; empty slots have none.  A CTA's tiles: one of each turn of the grid, every other turn backwards.  Where
+// lengths differ (offsets are given) and up to 256 slots, the longest come first: 24 prompts of 16 000 tokens 23.8 us, in the
+// slots' order 28; one of 8192 tokens would take 35.3 with the list and takes 33.8.
+struct LocalItems {
     int H, tiles_v, tiles_k, slots, total;
     const int2* table;
+    const unsigned char* list;             // null: the slots' order
     __device__ __forceinline__ int count() const { return slots * H * tiles_v * tiles_k; }
+    __device__ __forceinline__ int first_of(int turn) const { return turn * gridDim.x + (turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x); }
+    __device__ __forceinline__ int slot_of(int at) const { return list != nullptr ? list[at] : at; }
     __device__ __forceinline__ int get(int i, int& slot, int& h, int& r0, int& c0, int& first) const {
         const int tiles = tiles_v * tiles_k, t = i % tiles, sh = i / tiles;
-        slot = sh / H;
+        slot = slot_of(sh / H);
         h = sh % H;
         r0 = t / tiles_k * 128;
         c0 = t % tiles_k * 128;
@@ -240,7 +265,8 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
     const SeqShape& sh = a.sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = warp_uniform(tid >> 5), rep = sh.H / sh.Hk;
     const int slots = seg_slots(sh.nseq, sh.total, kSeg);
-    const LocalItems items = {sh.H, (sh.dv + 127) / 128, (sh.dk + 127) / 128, slots, sh.total, slot_table(gates, slots, sh.H)};
+    const LocalItems items = {sh.H, (sh.dv + 127) / 128, (sh.dk + 127) / 128, slots, sh.total, slot_table(gates, slots, sh.H),
+                              sh.offsets != nullptr && slots <= kLocalListed ? reinterpret_cast<const unsigned char*>(sm + kLocalList) : nullptr};
     const int count = items.count();
     const uint32_t base = smem_u32(sm), bars = base + kLocalBars;
     const uint32_t full0 = bars, empty0 = bars + 8 * kLocalStages, a_full = bars + 16 * kLocalStages, a_free = a_full + 32, acc_full = a_full + 64,
@@ -259,16 +285,20 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
     tc_fence_after();
     griddep_wait();
     griddep_launch();
+    if (items.list != nullptr) {
+        if (warp == 0) list_slots(items.table, slots, sh.total, reinterpret_cast<unsigned char*>(sm + kLocalList));
+        __syncthreads();
+    }
     int slot, h, r0, c0, first;
     Ring ring;
     if (warp == 12) {
         if (elect_one()) {
             int issued = 0;
             bool ok = true;
-            for (int i = blockIdx.x; ok && i < count; i += gridDim.x) {
+            for (int turn = 0, i; ok && (i = items.first_of(turn)) < count; ++turn) {
                 // one thread: no shuffles here
                 const int tiles = items.tiles_v * items.tiles_k, t = i % tiles, s_h = i / tiles;
-                slot = s_h / sh.H;
+                slot = items.slot_of(s_h / sh.H);
                 h = s_h % sh.H;
                 r0 = t / items.tiles_k * 128;
                 c0 = t % items.tiles_k * 128;
@@ -278,7 +308,7 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
                     const uint32_t at = base + ring.st * kLocalStage, bar = full0 + 8 * ring.st;
                     if (issued >= kLocalStages && !(ok = wait_here(empty0 + 8 * ring.st, ring.ph ^ 1, a.err, dead))) break;
                     mbar_expect_tx(bar, (na + nb) * kBox + kLocalTok * 4);
-                    bulk_copy_g2s(base + kLocalCoef + ring.st * kLocalTok * 4, gates + (size_t)s_h * kGAll + (BACK ? kGHead : kGCoef) + k, kLocalTok * 4, bar);
+                    bulk_copy_g2s(base + kLocalCoef + ring.st * kLocalTok * 4, gates + ((size_t)slot * sh.H + h) * kGAll + (BACK ? kGHead : kGCoef) + k, kLocalTok * 4, bar);
                     for (int x = 0; x < na; ++x) tma_3d(at + x * kBox, &ma, r0 + 64 * x, h, e.x + k, bar);
                     for (int x = 0; x < nb; ++x) tma_3d(at + (2 + x) * kBox, &mb, c0 + 64 * x, h / rep, e.x + k, bar);
                     ++issued;
@@ -291,7 +321,7 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
     } else if (warp == 13) {
         const bool leader = elect_one();
         uint32_t unit = 0, step = 0;                      // sums and stages so far
-        for (int i = blockIdx.x; i < count; i += gridDim.x) {
+        for (int turn = 0, i; (i = items.first_of(turn)) < count; ++turn) {
             const int rows = items.get(i, slot, h, r0, c0, first);
             const uint32_t id = idesc_bf16(128, min(128, sh.dk - c0)) | kBMn;
             for (int k = 0; k < rows; k += kLocalTok, ring.next(kLocalStages), ++step) {
@@ -336,7 +366,7 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
         const int g = warp >> 2, w4 = warp & 3, r = 32 * w4 + lane, piece = r >> 3 & 7;      // 32 tokens of a stage; row of the tile
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
         uint32_t step = 0;
-        for (int i = blockIdx.x; i < count; i += gridDim.x) {
+        for (int turn = 0, i; (i = items.first_of(turn)) < count; ++turn) {
             const int rows = items.get(i, slot, h, r0, c0, first);
             for (int k = 0; k < rows; k += kLocalTok, ring.next(kLocalStages), ++step) {
                 const int left = rows - k - 32 * g;
@@ -392,7 +422,7 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * w4) << 16, mine = base + kLocalOut + r * 128;
         if (!BACK && blockIdx.x == gridDim.x - 1 && warp == 8) order_slots(items.table, slots, sh.total);       // for the rows' kernels
         uint32_t unit = 0;
-        for (int i = blockIdx.x; i < count; i += gridDim.x) {
+        for (int turn = 0, i; (i = items.first_of(turn)) < count; ++turn) {
             const int rows = items.get(i, slot, h, r0, c0, first), n = min(128, sh.dk - c0);
             for (int k = 0; k < rows; k += kLocalHalf, ++unit) {
                 if (unit > 0) {                           // what was there has left shared memory; a first half, arrived
@@ -453,8 +483,8 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
 // A CTA an SM takes block after block of rows; the scores of a block of columns, be it the next rows' first, are formed
 // before the product of the one before it, so that the workers' pass over scores runs beside products.  Warps 0-7 work
 // (four a half of the columns), 8-11 move finished sums out, 12 copies, 13 multiplies.
-// 8192 tokens of 8 heads, 256 x 256, caches cold: kOut 54 us, kDk 57, kDq and kDv 79 (900 to 800 TFLOP/s of products; tensor
-// core busy 47 and 38 % of an SM's time).  Bound by the chain of a block: scores, the workers' pass (some 1.4 k cycles), and
+// 8192 tokens of 8 heads, 256 x 256, caches cold: kOut 54 us, kDk 56, kDq 75, kDv 72 (900 to 800 TFLOP/s of products; tensor
+// core busy 47 and 40 % of an SM's time).  Bound by the chain of a block: scores, the workers' pass (some 1.4 k cycles), and
 // the state's product with its scaling (4 k) at the start of each item, which the next item's scores cover in part only: two
 // sums of 256 columns do not fit TMEM beside two blocks' scores.
 // ---------------------------------------------------------------------------
@@ -1033,7 +1063,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 // Sums of F_ts = e^{g_t - g_s} (q_t.k_s) (dO_t.v_s), s < t, of 128 rows t with the segment's blocks up to theirs: by
 // rows with beta_s, by columns without, and F_tt.  Both scores are products of bf16 inputs, exact but for fp32 sums.
 // Warps 0-7 work, warp 8 copies, warp 9 multiplies; a CTA a block of rows, two an SM where both fit, the longest first.  8192 tokens of 8
-// heads, 256 x 256: 51 us, tensor core busy 22 % of the time: bound by the workers' pass over two scores of each pair.
+// heads, 256 x 256: 47 us, tensor core busy 25 % of the time: bound by the workers' pass over two scores of each pair.
 // ---------------------------------------------------------------------------
 // floats of a (slot, head): rows, F_tt, q's and v's dots by halves, columns by block of rows
 constexpr int kPartRow = 0, kPartDiag = kSeg, kPartQ = 2 * kSeg, kPartK = 4 * kSeg, kPartCol = 6 * kSeg, kPartAll = 10 * kSeg;
