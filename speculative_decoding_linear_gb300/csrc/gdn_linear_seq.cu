@@ -8,6 +8,8 @@
 //   lin_gates_kernel   dlog_alpha and dbeta
 // All products are fp32 on the CUDA cores, in 64 x 64 tiles of four by four values a thread: fp32 inputs carried
 // as bf16 terms would take six to nine products on the tensor core for each of these.
+// 8192 tokens of 8 heads, 256 x 256: forward 1.28 ms, backward 3.1; 4 x 2048, 64 x 64: 0.11 and 0.36; bound by shared memory's reads,
+// two of 16 bytes for 16 multiply-adds.
 #include "gdn_checks.cuh"
 #include "gdn_linear.cuh"
 
@@ -356,7 +358,8 @@ __global__ void __launch_bounds__(kT) lin_gates_kernel(SeqArgs a, const float* p
 // four neighbouring elements, all segments; the next kAhead segments' values are on their way.
 //   TERMS 0: out and start are fp32, out may be local itself; else they are bf16 terms, out_term elements apart
 //   (out TERMS of them, start three).
-// Bound by memory: 4 bytes read and 4 or 2 TERMS written for each element of a segment's state.
+// Bound by memory: 4 bytes read and 4 or 2 TERMS written for each element of a segment's state (backwards 6 more read): 8192 tokens
+// of 8 heads, 256 x 256, 12.7 us with two terms, 16.5 with three, 26 backwards, 5.1 to 5.3 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kAhead = 4;
 

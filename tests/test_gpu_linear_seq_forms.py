@@ -205,3 +205,23 @@ def test_rows_past_32_bits_of_offsets():
     for m in want:
         y = got[m][1:] if m in ("S_T", "dS0") else got[m][lengths[0]:]
         assert torch.equal(y, want[m]), m
+
+
+@pytest.mark.parametrize("dims", [(4, 2, 64, 64), (2, 2, 64, 64)])
+def test_rows_of_a_sequence_that_is_not_one_stay(dims):
+    """Offsets that leave the batch: reported, and neither outputs nor gradients of those tokens are written."""
+    lengths, total = [100, 50, 700], 850
+    x, _, dout, dS = inputs(lengths, *dims, seed=5)
+    full = (3, total, *dims, torch.bfloat16)
+    bad = torch.tensor([0, 100, 850 + 9, 850], dtype=torch.int32, device="cuda")      # the second ends behind the batch, the third before its start
+    d, ws, rec = outputs(x), gdnspec.empty_linear_seq_workspace(*full).fill_(0x3f), gdnspec.empty_linear_seq_record(*full).fill_(0x3f)
+    both(x, bad, dout, dS, d, ws, rec)
+    torch.cuda.synchronize()
+    assert gdnspec.gdn_last_error() == gdnspec.ERR_INDEX
+    assert gdnspec.gdn_last_error() == gdnspec.OK
+    first = {m: (y[:1] if m == "S0" else y[:100]) for m, y in x.items()}
+    want = plain(first, [100], dout[:100], dS[:1])
+    for m in want:
+        one = m in ("S_T", "dS0")
+        held(d[m][:1] if one else d[m][:100], want[m], m)
+        assert torch.isnan(d[m][1:] if one else d[m][100:]).all(), m
