@@ -528,18 +528,18 @@ static_assert(sizeof(RowGates) % 16 == 0, "read by 16 bytes");
 // ask for items, and the instruction cache is small.
 __device__ __noinline__ int4 rows_item(int turn, const int* order, const int2* table, int slots, int H, int rep, int total) {
     constexpr int kMost = kSeg / kBlk;
-    const int i = turn * gridDim.x + blockIdx.x, n_most = min(max(order[kMost - 1], 0), slots);
+    static_assert(kMost == 4, "counts of slots with one block to four");
+    const int2 n12 = reinterpret_cast<const int2*>(order)[0], n34 = reinterpret_cast<const int2*>(order)[1];
+    const int i = turn * gridDim.x + blockIdx.x, n_most = min(max(n34.y, 0), slots);
     int m = i / kMost, b = kMost - (i + turn) % kMost, from = 0;
     if (m >= n_most * H) {
-        m = i - n_most * H * kMost;
         from = n_most;
-#pragma unroll 1
-        for (b = kMost - 1; b > 0; --b) {
-            const int k = (min(max(order[b - 1], n_most), slots) - n_most) * H;
-            if (m < k) break;
-            m -= k;
-        }
-        if (b == 0) return make_int4(0, 0, 0, 0);
+        const int k3 = (min(max(n34.x, n_most), slots) - n_most) * H, k2 = (min(max(n12.y, n_most), slots) - n_most) * H,
+                  k1 = (min(max(n12.x, n_most), slots) - n_most) * H;
+        m = i - n_most * H * kMost;
+        b = m < k3 ? 3 : m < k3 + k2 ? 2 : 1;
+        m -= b == 3 ? 0 : b == 2 ? k3 : k3 + k2;
+        if (m >= k1) return make_int4(0, 0, 0, 0);
     }
     const int at = m / H, slot = order[kMost + from + at], h = m - at * H;
     if ((unsigned)slot >= (unsigned)slots) return make_int4(0, 0, 0, 0);
