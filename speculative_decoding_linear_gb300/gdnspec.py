@@ -607,10 +607,10 @@ def _dense(x):
     return x.data_ptr() or None
 
 
-def _rows(x, what):
-    """_tokens, at once where the tensor is dense."""
-    if x.is_contiguous() and x.is_cuda:
-        return x.data_ptr() or None, x.shape[-1] * x.shape[-2]
+def _rows(x, what, width):
+    """_tokens of a tensor that _here has seen, at once where it is dense: rows of `width` elements."""
+    if x.is_contiguous():
+        return x.data_ptr() or None, width
     return _tokens(x, what)
 
 
@@ -654,9 +654,9 @@ def gdn_linear_seq_forward(q, k, v, log_alpha, beta, S0, out, S_T, workspace, of
     if record is not None:
         _sized(record, gdn_linear_seq_record_bytes(*dims, q.dtype), "record")
     _here(q, k, v, log_alpha, beta, S0, out, S_T, workspace, offsets, record)
-    qp, ldq = _rows(q, "q")
-    kp, ldk = _rows(k, "k")
-    vp, ldv = _rows(v, "v")
+    qp, ldq = _rows(q, "q", Hk * dk)
+    kp, ldk = _rows(k, "k", Hk * dk)
+    vp, ldv = _rows(v, "v", H * dv)
     _check(lib().gdn_linear_seq_forward(qp, ldq, kp, ldk, vp, ldv, dtype_code(q.dtype), _dense(log_alpha), _dense(beta), _dense(S0),
                                         _dense(offsets), _dense(out), _dense(S_T), _dense(record), _dense(workspace), *dims,
                                         _stream(stream)), "gdn_linear_seq_forward")
@@ -674,9 +674,9 @@ def gdn_linear_seq_backward(q, k, v, log_alpha, beta, dout, dS_T, record, dq, dk
     _sized(workspace, gdn_linear_seq_workspace_bytes(*dims, q.dtype), "workspace")
     _sized(record, gdn_linear_seq_record_bytes(*dims, q.dtype), "record")
     _here(q, k, v, log_alpha, beta, dout, dS_T, record, dq, dk, dv, dlog_alpha, dbeta, dS0, workspace, offsets)
-    qp, ldq = _rows(q, "q")
-    kp, ldk = _rows(k, "k")
-    vp, ldv = _rows(v, "v")
+    qp, ldq = _rows(q, "q", Hk * d_k)
+    kp, ldk = _rows(k, "k", Hk * d_k)
+    vp, ldv = _rows(v, "v", H * d_v)
     _check(lib().gdn_linear_seq_backward(qp, ldq, kp, ldk, vp, ldv, dtype_code(q.dtype), _dense(log_alpha), _dense(beta),
                                          _dense(offsets), _dense(dout), _dense(dS_T), _dense(record), _dense(dq), _dense(dk), _dense(dv),
                                          _dense(dlog_alpha), _dense(dbeta), _dense(dS0), _dense(workspace), *dims, _stream(stream)),
@@ -703,29 +703,34 @@ def gdn_rotary_frequencies(rot, base=10000.0, factor=1.0, original=0.0, low=1.0,
 def gdn_rotary(q, k, positions, inv_freq, q_out, k_out, scale=1.0, interleaved=False, inverse=False, stream=None):
     """Rotary positions of q [.., H, d] and k [.., Hk, d] (k and k_out may be None), with positions int32 [..] and
     inv_freq fp32 [rot / 2] (see include/gdnspec.h); q_out and k_out may be q and k."""
-    if q.dim() not in (3, 4) or positions.shape != q.shape[:-2] or positions.dtype is not torch.int32:
+    qs, t = q.shape, q.dtype                  # a tensor's shape once: each look at it is some 0.2 us of a call of 10
+    lead, n = qs[:-2], len(qs)
+    if n not in (3, 4) or positions.shape != lead or positions.dtype is not torch.int32:
         raise ValueError("q must be [.., H, d] and positions int32 of its leading dimensions")
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
-    if k is not None and (k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1] or k.dtype is not q.dtype):
-        raise ValueError("k must be as q but for its heads")
-    if inv_freq.dim() != 1 or inv_freq.dtype is not torch.float32:
+    freqs = inv_freq.shape
+    if len(freqs) != 1 or inv_freq.dtype is not torch.float32:
         raise ValueError("inv_freq must be fp32 [rot / 2]")
-    _same(q_out, q.shape, q.dtype, "q_out")
-    if k is not None:
-        _same(k_out, k.shape, k.dtype, "k_out")
+    _same(q_out, qs, t, "q_out")
+    H, d = qs[-2:]
     _here(q, k, positions, inv_freq, q_out, k_out)
-    qp, ldq = _rows(q, "q")
-    qo, ldqo = _rows(q_out, "q_out")
+    qp, ldq = _rows(q, "q", H * d)
+    qo, ldqo = _rows(q_out, "q_out", H * d)
     kp = ko = None
     ldk = ldko = Hk = 0
     if k is not None:
-        kp, ldk = _rows(k, "k")
-        ko, ldko = _rows(k_out, "k_out")
-        Hk = k.shape[-2]
-    _check(lib().gdn_rotary(qp, ldq, kp, ldk, dtype_code(q.dtype), _dense(positions), _dense(inv_freq), scale, qo, ldqo, ko, ldko,
-                            positions.numel(), q.shape[-2], Hk, q.shape[-1], 2 * inv_freq.numel(), int(interleaved), int(inverse),
-                            _stream(stream)), "gdn_rotary")
+        ks = k.shape
+        if len(ks) != n or ks[:-2] != lead or ks[-1] != d or k.dtype is not t:
+            raise ValueError("k must be as q but for its heads")
+        _same(k_out, ks, t, "k_out")
+        Hk = ks[-2]
+        kp, ldk = _rows(k, "k", Hk * d)
+        ko, ldko = _rows(k_out, "k_out", Hk * d)
+    rc = lib().gdn_rotary(qp, ldq, kp, ldk, dtype_code(t), _dense(positions), _dense(inv_freq), scale, qo, ldqo, ko, ldko,
+                          positions.numel(), H, Hk, d, 2 * freqs[0], int(interleaved), int(inverse), _stream(stream))
+    if rc != OK:
+        raise GdnError(rc, "gdn_rotary")
 
 
 def empty_norm_workspace(rows, width, device="cuda"):
