@@ -8,7 +8,7 @@
 //   lin_gates_kernel   dlog_alpha and dbeta
 // All products are fp32 on the CUDA cores, in 64 x 64 tiles of four by four values a thread: fp32 inputs carried
 // as bf16 terms would take six to nine products on the tensor core for each of these.
-// 8192 tokens of 8 heads, 256 x 256: forward 1.28 ms, backward 3.1; 4 x 2048, 64 x 64: 0.11 and 0.36; bound by shared memory's reads,
+// 8192 tokens of 8 heads, 256 x 256: forward 1.14 ms, backward 2.4; 4 x 2048, 64 x 64: 0.10 and 0.31; bound by shared memory's reads,
 // two of 16 bytes for 16 multiply-adds.
 #include "gdn_checks.cuh"
 #include "gdn_linear.cuh"
@@ -30,29 +30,47 @@ struct Mat {                                // element (r, c) is p[r ld + c]; ze
     }
 };
 
-// s[k][m] of a 64 x 32 piece whose k index runs along the row, from column k0 on
-__device__ __forceinline__ void stage_k(float (*s)[kLd], const Mat& m, int k0) {
+// A thread's part of a piece of 64 x 32 on its way to shared memory: it is fetched while the piece before it is multiplied.
+constexpr int kPart = 64 * kK / 4 / kT;
+struct Part {
+    float4 x[kPart];
+};
+// s[k][m] of a piece whose k index runs along the row, from column k0 on
+__device__ __forceinline__ Part fetch_k(const Mat& m, int k0) {
+    Part p;
 #pragma unroll
-    for (int i = threadIdx.x; i < 64 * kK / 4; i += kT) {
-        const int r = i / (kK / 4), k = i % (kK / 4) * 4;
-        const float4 x = m.at(r, k0 + k);
-        s[k][r] = x.x;
-        s[k + 1][r] = x.y;
-        s[k + 2][r] = x.z;
-        s[k + 3][r] = x.w;
+    for (int j = 0; j < kPart; ++j) {
+        const int i = threadIdx.x + j * kT;
+        p.x[j] = m.at(i / (kK / 4), k0 + i % (kK / 4) * 4);
+    }
+    return p;
+}
+__device__ __forceinline__ void put_k(float (*s)[kLd], const Part& p) {
+#pragma unroll
+    for (int j = 0; j < kPart; ++j) {
+        const int i = threadIdx.x + j * kT, r = i / (kK / 4), k = i % (kK / 4) * 4;
+        s[k][r] = p.x[j].x;
+        s[k + 1][r] = p.x[j].y;
+        s[k + 2][r] = p.x[j].z;
+        s[k + 3][r] = p.x[j].w;
     }
 }
-// s[k][n] of a 32 x 64 piece whose n index runs along the row, from row k0 on, its rows scaled
-__device__ __forceinline__ void stage_n(float (*s)[kLd], const Mat& m, int k0, const float* scale = nullptr) {
+// s[k][n] of a piece whose n index runs along the row, from row k0 on; its rows scaled
+__device__ __forceinline__ Part fetch_n(const Mat& m, int k0) {
+    Part p;
 #pragma unroll
-    for (int i = threadIdx.x; i < 64 * kK / 4; i += kT) {
-        const int k = i / 16, n = i % 16 * 4;
-        float4 x = m.at(k0 + k, n);
-        if (scale != nullptr) {
-            const float f = scale[k0 + k];
-            x = make_float4(f * x.x, f * x.y, f * x.z, f * x.w);
-        }
-        *reinterpret_cast<float4*>(&s[k][n]) = x;
+    for (int j = 0; j < kPart; ++j) {
+        const int i = threadIdx.x + j * kT;
+        p.x[j] = m.at(k0 + i / 16, i % 16 * 4);
+    }
+    return p;
+}
+__device__ __forceinline__ void put_n(float (*s)[kLd], const Part& p, const float* scale = nullptr) {
+#pragma unroll
+    for (int j = 0; j < kPart; ++j) {
+        const int i = threadIdx.x + j * kT, k = i / 16, n = i % 16 * 4;
+        const float f = scale != nullptr ? scale[k] : 1.f;
+        *reinterpret_cast<float4*>(&s[k][n]) = scale != nullptr ? make_float4(f * p.x[j].x, f * p.x[j].y, f * p.x[j].z, f * p.x[j].w) : p.x[j];
     }
 }
 
@@ -80,11 +98,17 @@ struct alignas(16) Stage {               // read by 16 bytes
 // c += A B^T, both with k along the row; A B with `along_n`
 template <bool along_n>
 __device__ __forceinline__ void product(Acc& c, Stage& s, const Mat& A, const Mat& B, int K) {
+    const auto fetch_b = [&](int k) { return along_n ? fetch_n(B, k) : fetch_k(B, k); };
+    Part a = fetch_k(A, 0), b = fetch_b(0);
     for (int k = 0; k < K; k += kK) {
         __syncthreads();
-        stage_k(s.a, A, k);
-        if (along_n) stage_n(s.b, B, k); else stage_k(s.b, B, k);
+        put_k(s.a, a);
+        if (along_n) put_n(s.b, b); else put_k(s.b, b);
         __syncthreads();
+        if (k + kK < K) {
+            a = fetch_k(A, k + kK);
+            b = fetch_b(k + kK);
+        }
         tile_mul(c, s.a, s.b);
     }
 }
@@ -151,11 +175,16 @@ __global__ void __launch_bounds__(kT) lin_local_kernel(SeqArgs a, float* local, 
     const Mat B = columns(token_rows(BACK ? a.q : a.k, BACK ? sh.ldq : sh.ldk, first, rows, hk, sh.dk), c0);
     Acc acc;
     clear(acc);
+    Part x = fetch_n(A, 0), y = fetch_n(B, 0);
     for (int k = 0; k < kSegF; k += kK) {
         __syncthreads();
-        stage_n(st.a, A, k, w);
-        stage_n(st.b, B, k);
+        put_n(st.a, x, w + k);
+        put_n(st.b, y);
         __syncthreads();
+        if (k + kK < kSegF) {
+            x = fetch_n(A, k + kK);
+            y = fetch_n(B, k + kK);
+        }
         tile_mul(acc, st.a, st.b);
     }
     const int m = r0 + threadIdx.x / 16 * 4, n = c0 + threadIdx.x % 16 * 4;
@@ -237,6 +266,7 @@ __global__ void __launch_bounds__(kT) lin_rows_kernel(SeqArgs a, const float* st
             }
         }
         clear(y);
+        Part x = fetch_n(X, 0);
         product<false>(y, st, A, B, value_cols ? sh.dk : sh.dv);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -250,8 +280,9 @@ __global__ void __launch_bounds__(kT) lin_rows_kernel(SeqArgs a, const float* st
             }
         for (int k0 = 0; k0 < kSegF; k0 += kK) {
             __syncthreads();
-            stage_n(st.b, X, k0);
+            put_n(st.b, x);
             __syncthreads();
+            if (k0 + kK < kSegF) x = fetch_n(X, k0 + kK);
             tile_mul(acc, w + k0, st.b);
         }
     }
