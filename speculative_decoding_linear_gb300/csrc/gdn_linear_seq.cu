@@ -8,7 +8,7 @@
 //   lin_gates_kernel   dlog_alpha and dbeta
 // All products are fp32 on the CUDA cores, in 64 x 64 tiles of four by four values a thread: fp32 inputs carried
 // as bf16 terms would take six to nine products on the tensor core for each of these.
-// 8192 tokens of 8 heads, 256 x 256: forward 1.14 ms, backward 2.4; 4 x 2048, 64 x 64: 0.10 and 0.31; bound by shared memory's reads,
+// 8192 tokens of 8 heads, 256 x 256: forward 1.14 ms, backward 2.4; 4 x 2048, 64 x 64: 0.10 and 0.29; bound by shared memory's reads,
 // two of 16 bytes for 16 multiply-adds.
 #include "gdn_checks.cuh"
 #include "gdn_linear.cuh"
@@ -97,9 +97,9 @@ struct alignas(16) Stage {               // read by 16 bytes
 };
 // c += A B^T, both with k along the row; A B with `along_n`
 template <bool along_n>
-__device__ __forceinline__ void product(Acc& c, Stage& s, const Mat& A, const Mat& B, int K) {
-    const auto fetch_b = [&](int k) { return along_n ? fetch_n(B, k) : fetch_k(B, k); };
-    Part a = fetch_k(A, 0), b = fetch_b(0);
+__device__ __forceinline__ Part fetch_b(const Mat& B, int k) { return along_n ? fetch_n(B, k) : fetch_k(B, k); }
+template <bool along_n>              // a and b: the first pieces
+__device__ __forceinline__ void product(Acc& c, Stage& s, const Mat& A, const Mat& B, int K, Part a, Part b) {
     for (int k = 0; k < K; k += kK) {
         __syncthreads();
         put_k(s.a, a);
@@ -107,7 +107,7 @@ __device__ __forceinline__ void product(Acc& c, Stage& s, const Mat& A, const Ma
         __syncthreads();
         if (k + kK < K) {
             a = fetch_k(A, k + kK);
-            b = fetch_b(k + kK);
+            b = fetch_b<along_n>(B, k + kK);
         }
         tile_mul(c, s.a, s.b);
     }
@@ -168,14 +168,14 @@ __global__ void __launch_bounds__(kT) lin_local_kernel(SeqArgs a, float* local, 
     __shared__ Gates g;
     __shared__ Stage st;
     __shared__ float w[kSegF];
+    const Mat A = columns(token_rows(BACK ? a.dout : a.v, BACK ? (size_t)sh.H * sh.dv : sh.ldv, first, rows, h, sh.dv), r0);
+    const Mat B = columns(token_rows(BACK ? a.q : a.k, BACK ? sh.ldq : sh.ldk, first, rows, hk, sh.dk), c0);
+    Part x = fetch_n(A, 0), y = fetch_n(B, 0);            // on their way beside the gates
     load_gates(g, a, first, rows, h);
     if (threadIdx.x < kSegF) w[threadIdx.x] = BACK ? g.head[threadIdx.x] : g.beta[threadIdx.x] * g.tail[threadIdx.x];
     if (threadIdx.x == 0 && blockIdx.y == 0) gend[(size_t)slot * sh.H + h] = g.end;
-    const Mat A = columns(token_rows(BACK ? a.dout : a.v, BACK ? (size_t)sh.H * sh.dv : sh.ldv, first, rows, h, sh.dv), r0);
-    const Mat B = columns(token_rows(BACK ? a.q : a.k, BACK ? sh.ldq : sh.ldk, first, rows, hk, sh.dk), c0);
     Acc acc;
     clear(acc);
-    Part x = fetch_n(A, 0), y = fetch_n(B, 0);
     for (int k = 0; k < kSegF; k += kK) {
         __syncthreads();
         put_n(st.a, x, w + k);
@@ -228,22 +228,20 @@ __global__ void __launch_bounds__(kT) lin_rows_kernel(SeqArgs a, const float* st
     clear(acc);
     for (int r = 0; r < (value_cols ? 1 : rep); ++r) {
         const int h = value_cols ? head : head * rep + r, hk = value_cols ? head / rep : head;
-        __syncthreads();
-        load_gates(g, a, first, rows, h);
         const Mat q = token_rows(a.q, sh.ldq, first, rows, hk, sh.dk), k = token_rows(a.k, sh.ldk, first, rows, hk, sh.dk),
                   v = token_rows(a.v, sh.ldv, first, rows, h, sh.dv), o = token_rows(a.dout, ldo, first, rows, h, sh.dv);
         const Mat A = MODE == kOut ? q : MODE == kDq ? o : MODE == kDk ? v : k, B = MODE == kOut ? k : MODE == kDq ? v : MODE == kDk ? o : q,
                   X = columns(MODE == kOut ? v : MODE == kDq ? k : MODE == kDk ? q : o, n0);
         const float* S = states + ((size_t)slot * sh.H + h) * sh.dv * sh.dk;
+        const Mat M = {S + (value_cols ? (size_t)n0 * sh.dk : (size_t)n0), (size_t)sh.dk, value_cols ? sh.dv - n0 : sh.dv, value_cols ? sh.dk : sh.dk - n0};
+        Part pa = fetch_k(A, 0), pb = fetch_b<!value_cols>(M, 0);     // on their way beside the gates
+        __syncthreads();
+        load_gates(g, a, first, rows, h);
         Acc y;
         clear(y);
-        if (value_cols) {
-            const Mat M = {S + (size_t)n0 * sh.dk, (size_t)sh.dk, sh.dv - n0, sh.dk};
-            product<false>(y, st, A, M, dc);
-        } else {
-            const Mat M = {S + n0, (size_t)sh.dk, sh.dv, sh.dk - n0};
-            product<true>(y, st, A, M, dc);
-        }
+        product<!value_cols>(y, st, A, M, dc, pa, pb);
+        pa = fetch_k(A, 0);
+        pb = fetch_k(B, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float f = keys ? g.tail[m + i] : g.head[m + i], b = keys ? g.beta[m + i] : 1.f;
@@ -267,7 +265,7 @@ __global__ void __launch_bounds__(kT) lin_rows_kernel(SeqArgs a, const float* st
         }
         clear(y);
         Part x = fetch_n(X, 0);
-        product<false>(y, st, A, B, value_cols ? sh.dk : sh.dv);
+        product<false>(y, st, A, B, dc, pa, pb);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -316,13 +314,16 @@ __global__ void __launch_bounds__(kT) lin_gates_kernel(SeqArgs a, const float* p
     __shared__ Gates g;
     __shared__ Stage st;
     __shared__ float row_sum[kSegF], col[16][kSegF], diag[kSegF];
+    const Mat q = token_rows(a.q, sh.ldq, first, rows, hk, sh.dk), k = token_rows(a.k, sh.ldk, first, rows, hk, sh.dk),
+              o = token_rows(a.dout, (size_t)sh.H * sh.dv, first, rows, h, sh.dv), v = token_rows(a.v, sh.ldv, first, rows, h, sh.dv);
+    const Part pa = fetch_k(q, 0), pb = fetch_k(k, 0);               // on their way beside the gates
     load_gates(g, a, first, rows, h);
     const int m = threadIdx.x / 16 * 4, n = threadIdx.x % 16 * 4;
     Acc x, y;
     clear(x);
     clear(y);
-    product<false>(x, st, token_rows(a.q, sh.ldq, first, rows, hk, sh.dk), token_rows(a.k, sh.ldk, first, rows, hk, sh.dk), sh.dk);
-    product<false>(y, st, token_rows(a.dout, (size_t)sh.H * sh.dv, first, rows, h, sh.dv), token_rows(a.v, sh.ldv, first, rows, h, sh.dv), sh.dv);
+    product<false>(x, st, q, k, sh.dk, pa, pb);
+    product<false>(y, st, o, v, sh.dv, fetch_k(o, 0), fetch_k(v, 0));
     float cs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
