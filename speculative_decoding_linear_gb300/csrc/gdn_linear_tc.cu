@@ -1065,8 +1065,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 // Warps 0-7 work, warp 8 copies, warp 9 multiplies; a CTA a block of rows, two an SM where both fit, the longest first.  8192 tokens of 8
 // heads, 256 x 256: 47 us, tensor core busy 25 % of the time: bound by the workers' pass over two scores of each pair.
 // ---------------------------------------------------------------------------
-// floats of a (slot, head): rows, F_tt, q's and v's dots by halves, columns by block of rows
-constexpr int kPartRow = 0, kPartDiag = kSeg, kPartQ = 2 * kSeg, kPartK = 4 * kSeg, kPartCol = 6 * kSeg, kPartAll = 10 * kSeg;
+// floats of a (slot, head): rows with their own block's columns, F_tt, q's and v's dots by halves, columns by block of rows,
+// rows with the blocks before
+constexpr int kPartRow = 0, kPartDiag = kSeg, kPartQ = 2 * kSeg, kPartK = 4 * kSeg, kPartCol = 6 * kSeg, kPartOff = 10 * kSeg, kPartAll = 11 * kSeg;
 
 constexpr int kPairThreads = 320;
 struct PairsPlan {
@@ -1216,8 +1217,12 @@ __global__ void __launch_bounds__(kPairThreads, 2)
         const float mine = hi[row], mine_lo = lo[row], rf = decay_of(mine + mine_lo);
         const bool live = row < row_n;
         float* out = part + ((size_t)slot * sh.H + h) * kPartAll;
-        float sum = 0.f, diag = 0.f;
+        float sum = 0.f, diag = 0.f, off = 0.f;
         for (int j = 0; j <= rb; ++j) {
+            if (j == rb) {
+                off = sum;
+                sum = 0.f;
+            }
             const int u = j % G, n = col_rows(j);
             wait_here(s_full + 8 * u, (j / G) & 1, a.err, dead);
             __syncwarp();
@@ -1282,11 +1287,13 @@ __global__ void __launch_bounds__(kPairThreads, 2)
         named_sync(2, 256);
         if (g == 1) {
             cf[row] = sum;
+            cf[kBlk + row] = off;
             hi[row] = diag;
         }
         named_sync(2, 256);
         if (g == 0 && live) {
             out[kPartRow + rb * kBlk + row] = sum + cf[row];
+            out[kPartOff + rb * kBlk + row] = off + cf[kBlk + row];
             out[kPartDiag + rb * kBlk + row] = diag + hi[row];
         }
     }
@@ -1302,7 +1309,9 @@ __global__ void __launch_bounds__(kPairThreads, 2)
 // dlog_alpha and dbeta of one (segment, head) from those sums (E_ts = beta_s F_ts), four tokens a thread:
 //   dlog_alpha_u = sum_{s < u <= t} E_ts + sum_{t >= u} q_t.(e^{g_t} S^T dO_t) + sum_{s < u} beta_s v_s.(e^{G - g_s} dS k_s) + e^G <dS, S>
 //   dbeta_s      = sum_{t >= s} F_ts + v_s.(e^{G - g_s} dS k_s)
-// The first is the sum of rows minus columns from u on: terms of one segment only, in fp32.  Latency of a scan over 512 tokens:
+// The first sum's pairs (t, s) by blocks: t in u's block and s before it, sums of rows from u on; s in u's block and t behind it,
+// sums of columns before u; both elsewhere, whole blocks' sums; both in u's block, rows minus columns from u on.  So what cancels is
+// of one block's terms (rows minus columns of the segment left 9.7e-7 of dlog_alpha, 6.3e-7 so).  Latency of a scan over 512 tokens:
 // 8 us whether 8192 or 6001 tokens.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kBlk) lin_gates_tc_kernel(SeqArgs a, const float* part, const float* phi, int tiles) {
@@ -1319,54 +1328,80 @@ __global__ void __launch_bounds__(kBlk) lin_gates_tc_kernel(SeqArgs a, const flo
     if (!slot_segment(sh, kSeg, slot, s, c, first, rows, a.err)) return;
     const size_t at = (size_t)slot * sh.H + h;
     const float* p = part + at * kPartAll;
-    __shared__ float sums[3][4];
-    float from[4], before[4], beta[4], ph = 0.f;
+    __shared__ float sums[3][4], whole[4][4];             // whole: rows of a later block with columns of an earlier one
+    float from[4], before[4], own[4], pre[4], ph = 0.f;
     for (int i = tid; i < tiles; i += kBlk) ph += phi[at * tiles + i];
-    const int last = (rows - 1) / kBlk;
+    const int last = (rows - 1) / kBlk;                   // a warp has a block's tokens
+    float later[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int t = 4 * tid + e;
-        from[e] = before[e] = 0.f;
+        from[e] = before[e] = own[e] = pre[e] = 0.f;
         if (t >= rows) continue;
-        beta[e] = a.beta[(size_t)(first + t) * sh.H + h];
+        const float beta = a.beta[(size_t)(first + t) * sh.H + h], mine = p[kPartCol + warp * kSeg + t];
         float cc = 0.f;
-        for (int i = t / kBlk; i <= last; ++i) cc += p[kPartCol + i * kSeg + t];
-        const float iq = p[kPartQ + t] + p[kPartQ + kSeg + t], ik = p[kPartK + t] + p[kPartK + kSeg + t];
-        from[e] = p[kPartRow + t] - beta[e] * cc + iq;
-        before[e] = beta[e] * ik;
-        a.dbeta[(size_t)(first + t) * sh.H + h] = cc + p[kPartDiag + t] + ik;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+            const float x = i > warp && i <= last ? p[kPartCol + i * kSeg + t] : 0.f;
+            cc += x;
+            later[i] = fmaf(beta, x, later[i]);
+        }
+        const float ik = p[kPartK + t] + p[kPartK + kSeg + t];
+        from[e] = p[kPartQ + t] + p[kPartQ + kSeg + t];
+        own[e] = (p[kPartRow + t] - beta * mine) + p[kPartOff + t];
+        pre[e] = beta * cc;
+        before[e] = beta * ik;
+        a.dbeta[(size_t)(first + t) * sh.H + h] = (cc + mine) + p[kPartDiag + t] + ik;
     }
-    const float f0 = (from[0] + from[1]) + (from[2] + from[3]), b0 = (before[0] + before[1]) + (before[2] + before[3]);
-    float f = f0, b = b0;
+    const float f0 = (from[0] + from[1]) + (from[2] + from[3]), b0 = (before[0] + before[1]) + (before[2] + before[3]),
+                o0 = (own[0] + own[1]) + (own[2] + own[3]), p0 = (pre[0] + pre[1]) + (pre[2] + pre[3]);
+    float f = f0, b = b0, ow = o0, pr = p0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const float fo = __shfl_down_sync(0xffffffffu, f, o), bo = __shfl_up_sync(0xffffffffu, b, o);
-        if (lane + o < 32) f += fo;
-        if (lane >= o) b += bo;
+        const float fo = __shfl_down_sync(0xffffffffu, f, o), bo = __shfl_up_sync(0xffffffffu, b, o), oo = __shfl_down_sync(0xffffffffu, ow, o),
+                    po = __shfl_up_sync(0xffffffffu, pr, o);
+        if (lane + o < 32) {
+            f += fo;
+            ow += oo;
+        }
+        if (lane >= o) {
+            b += bo;
+            pr += po;
+        }
     }
     ph = warp_sum(ph);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) later[i] = warp_sum(later[i]);
     if (lane == 0) {
         sums[0][warp] = f;
         sums[2][warp] = ph;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) whole[i][warp] = later[i];
     }
     if (lane == 31) sums[1][warp] = b;
     __syncthreads();
-    // f: from the warp's first token behind this thread's on; b: up to the token before this thread's
+    // f, ow: from the first token behind this thread's on; b, pr: up to the token before this thread's
     f -= f0;
     b -= b0;
+    ow -= o0;
+    pr -= p0;
     ph = (sums[2][0] + sums[2][1]) + (sums[2][2] + sums[2][3]);
     for (int w = 0; w < 4; ++w) {
         if (w > warp) f += sums[0][w];
         if (w < warp) b += sums[1][w];
+        for (int i = warp + 1; i < 4 && w < warp; ++i) ph += whole[i][w];
     }
-    float after[4];
-    after[3] = f + from[3];
 #pragma unroll
-    for (int e = 2; e >= 0; --e) after[e] = after[e + 1] + from[e];
+    for (int e = 3; e >= 0; --e) {
+        f += from[e];
+        ow += own[e];
+        from[e] = f + ow;
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        if (4 * tid + e < rows) a.dla[(size_t)(first + 4 * tid + e) * sh.H + h] = (after[e] + b) + ph;
+        if (4 * tid + e < rows) a.dla[(size_t)(first + 4 * tid + e) * sh.H + h] = from[e] + ((b + pr) + ph);
         b += before[e];
+        pr += pre[e];
     }
 }
 
