@@ -531,7 +531,7 @@ int gdn_seq_step(const void* q, const void* k, const void* v, int dtype, const f
  * States and sums are fp32.  With bf16 inputs the fp32 operands of the tensor core's products are
  * carried as bf16 terms: three of them (2^-24 of an operand are left) where the result is fp32 (what a
  * segment adds to a state, the gates' gradients), two (2^-17) of the decayed scores and of the states
- * where it is bf16.  S_T and dS0 are 9e-7 of their size off with slow decays.  With fp32 inputs all is
+ * where it is bf16.  S_T and dS0 are 7e-7 of their size off with slow decays.  With fp32 inputs all is
  * fp32.  A NaN or an infinity stays in its sequence; it reaches the whole segment that it lies in (512
  * tokens with bf16 inputs, 64 with fp32), the tokens before it too, and an infinity may become a NaN.
  * Equal inputs give equal bits (no atomics).

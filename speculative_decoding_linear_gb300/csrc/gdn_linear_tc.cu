@@ -186,13 +186,14 @@ constexpr uint32_t kBox = 64 * 128;
 // tile after tile.   forward  c_t = beta_t e^{G - g_t}, a = v, b = k;   BACK  c_t = e^{g_t}, a = dO, b = q
 // c_t a_t is an fp32 operand: three bf16 terms of it (2^-24 of it are left), as the sum is an fp32 output after up to
 // 2^17 tokens; the terms go to TMEM, where each thread holds one row of d_v.  b is bf16 and exact.  The tensor core cuts
-// off what does not fit 24 bits at each addition, always toward zero, 1.5e-8 of the sum: so a sum is of 256 tokens, and
-// the second half's is added to the first's in memory, rounded (1.7e-6 of the sum off after 512 tokens in one sum, 9e-7 so).
-// Bound by the products, three for each of the state's, and by forming their operands: 8192 tokens of 8 heads, 256 x 256, 34 us
-// (760 TFLOP/s of products, tensor core busy 40 % of the time; a CTA has 3 or 4 of the 512 tiles).  Warps 0-7 form the terms (four warps 32
+// off what does not fit 24 bits at each addition, always toward zero, 1.5e-8 of the sum: so a sum is of 192 tokens, and what
+// follows is added to it in memory, rounded (with slow decays 1.7e-6 of the state off after 512 tokens in one sum, 9.9e-7 in sums
+// of 256, 7.3e-7 of 192, 4.9e-7 of 128; 8192 tokens forward 98.4, 101 and 108 us with sums of 256, 192 and 128).
+// Bound by the products, three for each of the state's, and by forming their operands: 8192 tokens of 8 heads, 256 x 256, 37 us
+// (700 TFLOP/s of products, tensor core busy some 38 % of the time; a CTA has 3 or 4 of the 512 tiles).  Warps 0-7 form the terms (four warps 32
 // tokens, two buffers each), 8-11 move the sums out (two in TMEM) by way of shared memory, 12 copies, 13 multiplies.
 // ---------------------------------------------------------------------------
-constexpr int kLocalThreads = 448, kLocalStages = 5, kLocalTok = 64, kLocalHalf = 256;
+constexpr int kLocalThreads = 448, kLocalStages = 5, kLocalTok = 64, kLocalSum = 192;
 constexpr int kLocalListed = 256;
 constexpr uint32_t kLocalStage = 4 * kBox;                       // two boxes of a, two of b
 constexpr uint32_t kLocalOut = kLocalStages * kLocalStage, kLocalCoef = kLocalOut + 128 * 128 * 4, kLocalBars = kLocalCoef + kLocalStages * kLocalTok * 4,
@@ -237,7 +238,7 @@ __device__ __noinline__ void list_slots(const int2* table, int slots, int total,
 }
 // Tile i of the launch; empty slots have none.  A CTA's tiles: one of each turn of the grid, every other turn backwards.  Where
 // lengths differ (offsets are given) and up to 256 slots, the longest come first: 24 prompts of 16 000 tokens 23.8 us, in the
-// slots' order 28; one of 8192 tokens would take 35.3 with the list and takes 33.8.
+// slots' order 28; one of 8192 tokens 35.3 with the list, 33.8 without (sums of 256 tokens).
 struct LocalItems {
     int H, tiles_v, tiles_k, slots, total;
     const int2* table;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
             const uint32_t id = idesc_bf16(128, min(128, sh.dk - c0)) | kBMn;
             for (int k = 0; k < rows; k += kLocalTok, ring.next(kLocalStages), ++step) {
                 const uint32_t acc = tmem + 128 * (unit & 1);
-                const int at = k % kLocalHalf;
+                const int at = k % kLocalSum;
                 if (at == 0 && unit >= 2) wait_here(acc_free + 8 * (unit & 1), (unit >> 1 & 1) ^ 1, a.err, dead);
                 wait_here(full0 + 8 * ring.st, ring.ph, a.err, dead);
                 const uint64_t db = mn_desc<128>(base + ring.st * kLocalStage + 2 * kBox, kBox);
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (at + kLocalTok == kLocalHalf || k + kLocalTok >= rows) {
+                if (at + kLocalTok == kLocalSum || k + kLocalTok >= rows) {
                     if (leader) mma_commit(acc_full + 8 * (unit & 1));
                     __syncwarp();
                     ++unit;
@@ -424,8 +425,8 @@ __global__ void __launch_bounds__(kLocalThreads, 1)
         uint32_t unit = 0;
         for (int turn = 0, i; (i = items.first_of(turn)) < count; ++turn) {
             const int rows = items.get(i, slot, h, r0, c0, first), n = min(128, sh.dk - c0);
-            for (int k = 0; k < rows; k += kLocalHalf, ++unit) {
-                if (unit > 0) {                           // what was there has left shared memory; a first half, arrived
+            for (int k = 0; k < rows; k += kLocalSum, ++unit) {
+                if (unit > 0) {                           // what was there has left shared memory; a tile's sum before this one, arrived
                     if (warp == 8) bulk_all_done();
                     named_sync(1, 128);
                 }
@@ -1312,7 +1313,7 @@ __global__ void __launch_bounds__(kPairThreads, 2)
 // The first sum's pairs (t, s) by blocks: t in u's block and s before it, sums of rows from u on; s in u's block and t behind it,
 // sums of columns before u; both elsewhere, whole blocks' sums; both in u's block, rows minus columns from u on.  So what cancels is
 // of one block's terms (rows minus columns of the segment left 9.7e-7 of dlog_alpha, 6.3e-7 so).  Latency of a scan over 512 tokens:
-// 8 us whether 8192 or 6001 tokens.
+// 7.4 us whether 8192 or 6001 tokens.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kBlk) lin_gates_tc_kernel(SeqArgs a, const float* part, const float* phi, int tiles) {
     const SeqShape& sh = a.sh;
