@@ -1004,7 +1004,8 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     } else {
         const int w4 = warp & 3, row = 32 * w4 + lane;
         const uint32_t lanes = (uint32_t)(32 * w4) << 16;
-        const bool shared = !values && rep > 1, whole = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+        const bool shared = !values && rep > 1;
+        const bool whole = (reinterpret_cast<uintptr_t>(shared ? static_cast<const void*>(ra.heads) : out) & 31u) == 0;      // by 32 bytes: both may start on 16
         for (uint32_t items = 0; it.there(); it.look(++items, list, table, sh, slots, rep)) {
             const uint32_t ab = two_sums ? items & 1 : 0, ap = two_sums ? items >> 1 & 1 : items & 1, acc = tmem + 128 * ab + lanes;
             const bool live = row < it.row_n;
@@ -1035,7 +1036,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             w[e] = make_uint4(__float_as_uint(y[4 * e]), __float_as_uint(y[4 * e + 1]), __float_as_uint(y[4 * e + 2]), __float_as_uint(y[4 * e + 3]));
-                        stg_pieces<4>(o32 + c, w, false, true);
+                        stg_pieces<4>(o32 + c, w, false, whole);
                     } else {
                         uint4 w[2];
 #pragma unroll
