@@ -375,13 +375,15 @@ __global__ void __launch_bounds__(kT) lin_gates_kernel(SeqArgs a, const float* p
         if (lane + o < 32) f += fo;
         if (lane >= o) b += bo;
     }
-    // f: from token 2 lane on; b: up to token 2 lane + 1
-    b -= before[0] + before[1];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int t = 2 * lane + j;
-        if (t < rows) a.dla[(size_t)(first + t) * sh.H + h] = (j == 0 ? f : f - from[0]) + (j == 0 ? b : b + before[0]) + ph;
-    }
+    // f: from token 2 lane + 2 on; b: up to token 2 lane - 1.  The neighbour's sums, not this lane's less its own: with fast decays
+    // its own terms are far larger than what remains.
+    f = __shfl_down_sync(0xffffffffu, f, 1);
+    b = __shfl_up_sync(0xffffffffu, b, 1);
+    if (lane == 31) f = 0.f;
+    if (lane == 0) b = 0.f;
+    f += from[1];
+    if (2 * lane + 1 < rows) a.dla[(size_t)(first + 2 * lane + 1) * sh.H + h] = f + (b + before[0]) + ph;
+    if (2 * lane < rows) a.dla[(size_t)(first + 2 * lane) * sh.H + h] = (f + from[0]) + b + ph;
 }
 
 // ---------------------------------------------------------------------------

@@ -1355,9 +1355,8 @@ __global__ void __launch_bounds__(kBlk) lin_gates_tc_kernel(SeqArgs a, const flo
         before[e] = beta * ik;
         a.dbeta[(size_t)(first + t) * sh.H + h] = (cc + mine) + p[kPartDiag + t] + ik;
     }
-    const float f0 = (from[0] + from[1]) + (from[2] + from[3]), b0 = (before[0] + before[1]) + (before[2] + before[3]),
-                o0 = (own[0] + own[1]) + (own[2] + own[3]), p0 = (pre[0] + pre[1]) + (pre[2] + pre[3]);
-    float f = f0, b = b0, ow = o0, pr = p0;
+    float f = (from[0] + from[1]) + (from[2] + from[3]), b = (before[0] + before[1]) + (before[2] + before[3]),
+          ow = (own[0] + own[1]) + (own[2] + own[3]), pr = (pre[0] + pre[1]) + (pre[2] + pre[3]);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const float fo = __shfl_down_sync(0xffffffffu, f, o), bo = __shfl_up_sync(0xffffffffu, b, o), oo = __shfl_down_sync(0xffffffffu, ow, o),
@@ -1382,11 +1381,14 @@ __global__ void __launch_bounds__(kBlk) lin_gates_tc_kernel(SeqArgs a, const flo
     }
     if (lane == 31) sums[1][warp] = b;
     __syncthreads();
-    // f, ow: from the first token behind this thread's on; b, pr: up to the token before this thread's
-    f -= f0;
-    b -= b0;
-    ow -= o0;
-    pr -= p0;
+    // f, ow: from the first token behind this thread's on; b, pr: up to the token before this thread's.  The neighbour's sums, not this
+    // thread's less its own: with fast decays its own terms are far larger than what remains.
+    f = __shfl_down_sync(0xffffffffu, f, 1);
+    ow = __shfl_down_sync(0xffffffffu, ow, 1);
+    b = __shfl_up_sync(0xffffffffu, b, 1);
+    pr = __shfl_up_sync(0xffffffffu, pr, 1);
+    if (lane == 31) f = ow = 0.f;
+    if (lane == 0) b = pr = 0.f;
     ph = (sums[2][0] + sums[2][1]) + (sums[2][2] + sums[2][3]);
     for (int w = 0; w < 4; ++w) {
         if (w > warp) f += sums[0][w];

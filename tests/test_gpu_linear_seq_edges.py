@@ -32,3 +32,47 @@ def test_workspace_and_record_on_16_bytes(lengths, dims, ws_at, rec_at):
     assert gdnspec.gdn_last_error() == gdnspec.OK
     for m in want:
         assert torch.equal(got[m], want[m]), m
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lengths", [[512], [300, 64, 130, 3]])
+@pytest.mark.parametrize("end", [True, False])
+def test_gradient_of_fast_decays_element_by_element(dtype, lengths, end):
+    """dlog_alpha where nothing but the decays' gradient from one end is left: each element is far smaller than its neighbour.
+
+    end: dO = 0, so dlog_alpha_u = sum_{s < u} beta_s v_s.(e^{G - g_s} dS k_s) + e^G <dS, S0>; the last token's own term is none
+    of its element's.  Else v = 0 and dS = 0: sum_{t >= u} q_t.(e^{g_t} S0^T dO_t).  All inputs are positive, so sums keep
+    their relative accuracy: of two products over 64 and of a segment's tokens, (64 + 64 + 512) 2^-24 = 3.8e-5, and a
+    decay e^x of |x| up to 16 x 7 is off by 2 |x| 2^-24 = 1.4e-5 of itself: 1e-4 of each element.  Held are elements above
+    1e-30: their factors are below 10^4, so the decays of what they are made of are above 1e-34, ten thousand times
+    the least normal number (2^-126 = 1.2e-38, below which fp32 has fewer bits and exponentials may be zero).
+    """
+    dims = (2, 1, 64, 64)
+    x, off, dout, dS = inputs(lengths, *dims, seed=31)
+    x = {m: y.abs().to(dtype if m in "qkv" else torch.float32) for m, y in x.items()}
+    x["log_alpha"].fill_(-7.0 if end else -5.0)
+    dout, dS = dout.abs().to(dtype), dS.abs()
+    (dout if end else dS).zero_()
+    if not end:
+        x["v"].zero_()
+    full = (len(lengths), sum(lengths), *dims, dtype)
+    d = outputs(x)
+    both(x, off, dout, dS, d, gdnspec.empty_linear_seq_workspace(*full), gdnspec.empty_linear_seq_record(*full))
+    assert gdnspec.gdn_last_error() == gdnspec.OK
+    b = 0
+    for i, n in enumerate(lengths):
+        # by the formula (differentiation by a running sum takes its end away again, 1e-16 of the largest element)
+        q, k, v, do, la, beta = (y[b:b + n].double() for y in (x["q"], x["k"], x["v"], dout, x["log_alpha"], x["beta"]))
+        g, S0, dS_T = la.cumsum(0), x["S0"][i].double(), dS[i].double()
+        if end:
+            each = beta * (g[-1] - g).exp() * torch.einsum("shv,hvk,sk->sh", v, dS_T, k[:, 0])
+            start = g[-1].exp() * (dS_T * S0).sum((-1, -2))
+            want = torch.cat([start[None], start + each.cumsum(0)[:-1]])
+        else:
+            each = g.exp() * torch.einsum("tk,hvk,thv->th", q[:, 0], S0, do)
+            want = each.flip(0).cumsum(0).flip(0)
+        rows = slice(max(0, n - 16), n) if end else slice(0, min(n, 16))
+        got, want = d["dlog_alpha"][b:b + n][rows].double(), want[rows]
+        got, want = got[want > 1e-30], want[want > 1e-30]
+        assert len(want) >= min(n, 9) and ((got - want).abs() <= 1e-4 * want).all(), (n, ((got - want) / want).abs().max())
+        b += n
