@@ -76,3 +76,19 @@ def test_gradient_of_fast_decays_element_by_element(dtype, lengths, end):
         got, want = got[want > 1e-30], want[want > 1e-30]
         assert len(want) >= min(n, 9) and ((got - want).abs() <= 1e-4 * want).all(), (n, ((got - want) / want).abs().max())
         b += n
+
+
+@pytest.mark.parametrize("cut", [0, 1, 63, 64, 100, 127, 290])
+def test_nothing_passes_a_decay_of_zero(cut):
+    """fp32, log_alpha = -inf at a token: each term of its gradient has that decay as a factor, so the gradient is zero, not
+    what differences of sums would leave."""
+    lengths, dims = [300, 70], (2, 1, 64, 48)
+    x, off, dout, dS = inputs(lengths, *dims, seed=41)
+    x, dout = {m: y.float() for m, y in x.items()}, dout.float()
+    x["log_alpha"][cut] = -float("inf")
+    full = (2, 370, *dims, torch.float32)
+    d = outputs(x)
+    both(x, off, dout, dS, d, gdnspec.empty_linear_seq_workspace(*full), gdnspec.empty_linear_seq_record(*full))
+    assert gdnspec.gdn_last_error() == gdnspec.OK
+    assert (d["dlog_alpha"][cut] == 0).all()
+    assert torch.isfinite(d["dlog_alpha"]).all() and (d["dlog_alpha"][:cut] != 0).all() and (d["dlog_alpha"][cut + 1:] != 0).all()
