@@ -71,8 +71,11 @@ __device__ __forceinline__ LogSum operator+(LogSum a, LogSum b) {
     return {hi, e - (hi - s)};
 }
 __device__ __forceinline__ LogSum operator-(LogSum a, LogSum b) { return a + LogSum{-b.hi, -b.lo}; }
-__device__ __forceinline__ float decay_of(float d) { return exp2f(d * 1.44269504f); }
-__device__ __forceinline__ float decay_of(LogSum a) { return decay_of(a.hi + a.lo); }
+// e^(hi + lo): an exponent rounded to one float would cost |hi| 2^-24 of the decay
+__device__ __forceinline__ float decay_of(LogSum a) {
+    const float e = expf(a.hi);
+    return fmaf(e, a.lo, e);
+}
 
 // Inclusive sums over a warp's lanes.
 __device__ __forceinline__ LogSum warp_scan(LogSum x) {

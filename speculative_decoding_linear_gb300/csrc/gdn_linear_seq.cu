@@ -144,7 +144,7 @@ __device__ void load_gates(Gates& g, const SeqArgs& a, int first, int rows, int 
     __syncthreads();
 }
 __device__ __forceinline__ float decay(const Gates& g, int t, int s) {      // e^{g_t - g_s}, s <= t
-    return decay_of((g.hi[t] - g.hi[s]) + (g.lo[t] - g.lo[s]));
+    return decay_of(LogSum{g.hi[t], g.lo[t]} - LogSum{g.hi[s], g.lo[s]});
 }
 
 __device__ __forceinline__ Mat token_rows(const void* p, size_t ld, int first, int rows, int head, int d) {

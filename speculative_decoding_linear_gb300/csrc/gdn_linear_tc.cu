@@ -1216,7 +1216,7 @@ __global__ void __launch_bounds__(kPairThreads, 2)
             lo[tid] = g_lo;
         }
         named_sync(2, 256);
-        const float mine = hi[row], mine_lo = lo[row], rf = decay_of(mine + mine_lo);
+        const float mine = hi[row], mine_lo = lo[row], rf = decay_of(LogSum{mine, mine_lo});
         const bool live = row < row_n;
         float* out = part + ((size_t)slot * sh.H + h) * kPartAll;
         float sum = 0.f, diag = 0.f, off = 0.f;

@@ -92,3 +92,52 @@ def test_nothing_passes_a_decay_of_zero(cut):
     assert gdnspec.gdn_last_error() == gdnspec.OK
     assert (d["dlog_alpha"][cut] == 0).all()
     assert torch.isfinite(d["dlog_alpha"]).all() and (d["dlog_alpha"][:cut] != 0).all() and (d["dlog_alpha"][cut + 1:] != 0).all()
+
+
+U = 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype,n", [(torch.float32, 64), (torch.bfloat16, 64), (torch.bfloat16, 512)])
+def test_long_decays_keep_their_bits(dtype, n):
+    """No writes (beta = 0): S_T = e^G S0 and, without dO, dS0 = e^G dS_T, with G about -80.
+
+    An exponential is off by 2 ulp (4 x 2^-24) at most, the low part's and the state's products by 2^-24 each: 6 x 2^-24 of
+    each element.  An exponent rounded to a float alone would be off by 80 x 2^-24.  Below 2^-126 (e^-87.3) a float's step is
+    2^-149 whatever its size: 2 steps of the exponential and half a one of the low part's product, times the state, and
+    half a one of the result.
+    """
+    dims = (2, 1, 16, 16)
+    x, off, dout, dS = inputs([n], *dims, seed=51)
+    x = {m: y.to(dtype) if m in "qkv" else y for m, y in x.items()}
+    x["beta"].zero_()
+    x["log_alpha"] = -(torch.rand(n, 2, generator=torch.Generator().manual_seed(1)) * 160 / n).cuda()
+    dout = torch.zeros_like(x["v"])
+    full = (1, n, *dims, dtype)
+    d = outputs(x)
+    both(x, off, dout, dS, d, gdnspec.empty_linear_seq_workspace(*full), gdnspec.empty_linear_seq_record(*full))
+    assert gdnspec.gdn_last_error() == gdnspec.OK
+    decay = x["log_alpha"].double().sum(0).exp()[None, :, None, None]
+    for got, before in ((d["S_T"], x["S0"]), (d["dS0"], dS)):
+        want = decay * before.double()
+        tol = 6 * U * want.abs() + 2.0 ** -149 * (2.5 * before.double().abs() + 0.5)
+        assert ((got.double() - want).abs() <= tol).all(), ((got.double() - want).abs() / tol).max()
+
+
+def test_far_tokens_keep_their_bits():
+    """fp32, one write: o_t = e^{g_t - g_0} beta_0 v_0 (k_0.q_t), all positive, with decays down to e^-75.
+
+    A dot over 16 (16 x 2^-24), an exponential (4), its low part, beta, the decay's and v's products (4): 24 x 2^-24 of each.
+    """
+    n, dims = 64, (2, 1, 16, 16)
+    x, off, _, _ = inputs([n], *dims, seed=52)
+    x = {m: y.abs().float() for m, y in x.items()}
+    x["S0"].zero_()
+    x["beta"][1:] = 0.0
+    x["log_alpha"] = -(1.0 + 0.4 * torch.rand(n, 2, generator=torch.Generator().manual_seed(2))).cuda()
+    out = torch.empty_like(x["v"])
+    ws = gdnspec.empty_linear_seq_workspace(1, n, *dims, torch.float32, backward=False)
+    gdnspec.gdn_linear_seq_forward(*(x[m] for m in NAMES), out, None, ws, offsets=off)
+    y = {m: z.double() for m, z in x.items()}
+    g = y["log_alpha"].cumsum(0)
+    want = (g - g[0]).exp()[..., None] * (y["beta"][0][:, None] * y["v"][0])[None] * (y["q"][:, 0] @ y["k"][0, 0])[:, None, None]
+    assert ((out.double() - want).abs() <= 24 * U * want).all(), ((out.double() - want) / want).abs().max() / U
