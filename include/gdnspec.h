@@ -567,7 +567,8 @@ int gdn_linear_seq_step(const void* q, const void* k, const void* v, int dtype, 
  *   positions  int32 [total], any values;  inv_freq fp32 [rot / 2], each below 2^26 in size (a NaN, an
  *              infinity or more gives NaN).  Both need 4-byte alignment only
  *   d in {16, 32, ..., 256}, rot even, 2 <= rot <= d; 0 <= total; H + Hk <= 65535
- * The angle is exact to 1e-9 turns at any position; sines, products and sums are fp32.
+ * The angle is off by less than 5e-9 turns at any position and any of these frequencies; sines, products and
+ * sums are fp32.
  *
  * gdn_rotary_frequencies writes the rot / 2 frequencies base^{-2 i / rot}, scaled for contexts
  * `factor` times as long as the `original` one (in tokens), into HOST memory: a frequency that turns

@@ -3,9 +3,11 @@
 //   x' = scale (x cos a - y sin a),  y' = scale (x sin a + y cos a)
 // The inverse turns by -a, which is the gradient's way back (the turn is orthogonal).
 //
-// The angle keeps its full accuracy at any int32 position without a reduction: a frequency is kept as a 64-bit
-// fraction of a turn, position times fraction wraps modulo one turn by itself, and the upper 32 bits of it (1.5e-9 rad)
-// are the angle.  A frequency's fraction is its 24-bit significand times 2^66 / 2 pi, an exact integer product.
+// The angle keeps its accuracy at any int32 position without a reduction: a frequency is kept as a 64-bit fraction of a
+// turn, position times fraction wraps modulo one turn by itself, and the upper 32 bits of it are the angle.  A
+// frequency's fraction is its 24-bit significand times 2^66 / 2 pi (96 bits of it), cut off below 2^-64 of a turn: twice that
+// times 2^31 is 2.3e-10 turns.  The quarter turn that the angle lies next to is taken off as an integer, so that what is
+// rounded to a float is at most an eighth of a turn, off by 3.7e-9 turns (as half turns up to one, 1.5e-8).
 //
 // Bound by memory: each element is read and written once.  A block of threads takes a few tokens: it forms their sines
 // and cosines in shared memory, once for all heads, and then each thread V pairs of a head at a time, 16 bytes a load
@@ -35,13 +37,13 @@ struct RotaryArgs {
 
 // A frequency in turns, modulo one turn, times 2^64; NaN, infinities and sizes of 2^26 and more have none.
 __device__ __forceinline__ unsigned long long turn_fraction(float f, bool& fine) {
-    constexpr unsigned long long kTurn = 0xa2f9836e4e44152aull;      // 2^66 / 2 pi
+    constexpr unsigned long long kTurn = 0xa2f9836e4e441529ull, kTurnLow = 0xfc2757d2ull;      // 2^66 / 2 pi, and its next 32 bits
     const uint32_t u = __float_as_uint(f);
     const int ex = (u >> 23) & 255;
     const unsigned long long m = (u & 0x7fffffu) | (ex > 0 ? 0x800000u : 0u);
     const int shift = 2 - ((ex > 0 ? ex : 1) - 150);                 // of the 88-bit product
     fine = shift >= 0;
-    const unsigned long long lo = m * kTurn, hi = __umul64hi(m, kTurn);
+    const unsigned long long low = m * kTurnLow >> 32, lo = m * kTurn + low, hi = __umul64hi(m, kTurn) + (lo < low);
     unsigned long long r = 0;
     if (shift <= 0) r = lo;
     else if (shift < 64) r = (lo >> shift) | (hi << (64 - shift));
@@ -64,12 +66,12 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryArgs a) {
         const int t = i / pairs, j = i - t * pairs;
         bool fine;
         const unsigned long long w = turn_fraction(a.inv_freq[j], fine) * (unsigned long long)(long long)a.positions[t0 + t];
+        const uint32_t turn = (uint32_t)(w >> 32), quarter = (turn + 0x20000000u) >> 30 & 3;      // the nearest quarter
         float s, c;
-        sincospif((float)(int)(w >> 32) * 0x1p-31f, &s, &c);      // upper 32 bits as half turns in [-1, 1)
-        s *= a.inverse ? -a.scale : a.scale;
-        c *= a.scale;
-        cs[i] = fine ? c : __int_as_float(0x7fffffff);
-        sn[i] = fine ? s : __int_as_float(0x7fffffff);
+        sincospif((float)(int)(turn - (quarter << 30)) * 0x1p-31f, &s, &c);      // from it, in [-1 / 4, 1 / 4) half turns
+        const float y = quarter & 1 ? c : s, x = quarter & 1 ? s : c;
+        sn[i] = !fine ? __int_as_float(0x7fffffff) : y * ((quarter & 2) != 0 != a.inverse ? -a.scale : a.scale);
+        cs[i] = !fine ? __int_as_float(0x7fffffff) : x * (quarter + 1 & 2 ? -a.scale : a.scale);
     }
     __syncthreads();
     const int n = tokens * heads * units;

@@ -141,3 +141,53 @@ def test_far_tokens_keep_their_bits():
     g = y["log_alpha"].cumsum(0)
     want = (g - g[0]).exp()[..., None] * (y["beta"][0][:, None] * y["v"][0])[None] * (y["q"][:, 0] @ y["k"][0, 0])[:, None, None]
     assert ((out.double() - want).abs() <= 24 * U * want).all(), ((out.double() - want) / want).abs().max() / U
+
+
+def turns_of(positions, freqs):
+    """position x frequency in turns, modulo one, in whole numbers: 1 / 2 pi to 300 bits (pi by Machin's formula)."""
+    bits = 320
+
+    def arctan_of_one_over(n):
+        term = total = (1 << bits) // n
+        k = 1
+        while term:
+            term //= n * n
+            total += (-term if k % 2 else term) // (2 * k + 1)
+            k += 1
+        return total
+
+    inv = (1 << 2 * bits) // (2 * 4 * (4 * arctan_of_one_over(5) - arctan_of_one_over(239)))      # 2^bits / 2 pi
+    whole = 1 << (bits + 149)
+    steps = [int(f * 2.0 ** 75) << 74 if abs(f) >= 2.0 ** -50 else int(f * 2.0 ** 149) for f in freqs]      # exact multiples of 2^-149
+    # the nearest multiple of a turn taken off
+    return np.array([[((p * m * inv + whole // 2) % whole - whole // 2) / whole for m in steps] for p in positions])
+
+
+def test_angles_of_any_position_and_frequency():
+    """(1, 0) turned: cosine and sine themselves, for all int32 positions and frequencies up to 2^26.
+
+    The angle is off by 5e-9 turns.  Near an axis (one of the two below 0.1) a rounding of both by 2 x 2^-24 of themselves
+    turns the vector by 4 x 0.1 x 2^-24 / 2 pi = 4e-9 turns at most.  And everywhere each is off by 2 x 2^-24 of itself and the
+    angle's 3.2e-8 rad.
+    """
+    g = torch.Generator().manual_seed(61)
+    freqs = [1.0, 0.7, -0.37, 2.0 ** -20, 1e-4, 1e-30, 7.3, 99.9, 3000.7, -40000.1, 123456.7, 2.0 ** 20 * 1.1, -2.0 ** 23 * 1.7, 2.0 ** 25 * 1.37, 2.0 ** 26 * (1 - U), 0.0]
+    f = torch.tensor(freqs, dtype=torch.float32)
+    pos = torch.randint(-2 ** 31, 2 ** 31, (3000,), generator=g)
+    pos[:8] = torch.tensor([2 ** 31 - 1, -2 ** 31, 2 ** 31 - 2, -2 ** 31 + 1, 0, 1, -1, 1 << 30])
+    pos[1500:] %= 1 << 20
+    t = turns_of(pos.tolist(), f.tolist())
+    x = torch.zeros(len(pos), 1, 32)
+    x[..., :16] = 1.0
+    for inverse in (False, True):
+        out = torch.empty(len(pos), 1, 32, device="cuda")
+        gdnspec.gdn_rotary(x.cuda(), None, pos.int().cuda(), f.cuda(), out, None, inverse=inverse)
+        assert gdnspec.gdn_last_error() == gdnspec.OK
+        y = out.double().cpu().numpy()[:, 0]
+        c, s = y[:, :16], y[:, 16:] * (-1 if inverse else 1)
+        d = np.arctan2(s, c) / (2 * np.pi) - t
+        d -= np.round(d)
+        near = np.minimum(np.abs(c), np.abs(s)) < 0.1
+        assert np.abs(d[near]).max() <= 9e-9, np.abs(d[near]).max()
+        for got, want in ((c, np.cos(2 * np.pi * t)), (s, np.sin(2 * np.pi * t))):
+            assert (np.abs(got - want) <= 2 * U * np.abs(want) + 3.2e-8).all(), np.abs(got - want).max() / U
