@@ -191,3 +191,34 @@ def test_angles_of_any_position_and_frequency():
         assert np.abs(d[near]).max() <= 9e-9, np.abs(d[near]).max()
         for got, want in ((c, np.cos(2 * np.pi * t)), (s, np.sin(2 * np.pi * t))):
             assert (np.abs(got - want) <= 2 * U * np.abs(want) + 3.2e-8).all(), np.abs(got - want).max() / U
+
+
+def test_hundreds_of_thousands_of_sequences():
+    """What one warp does for all sequences keeps no other waiting: with a limit of 5 ms no wait of the call runs out."""
+    n, dims = 300_000, (1, 1, 16, 16)
+    g = torch.Generator(device="cuda").manual_seed(71)
+    lengths = torch.randint(1, 4, (n,), generator=g, device="cuda")
+    lengths[::1000] = torch.randint(1, 600, (n // 1000,), generator=g, device="cuda")
+    off = torch.cat([lengths.new_zeros(1), lengths.cumsum(0)]).int()
+    total = int(off[-1])
+    x = {m: torch.randn(total, 1, 16, generator=g, device="cuda").bfloat16() for m in "qkv"}
+    x["log_alpha"], x["beta"] = -torch.rand(total, 1, generator=g, device="cuda"), torch.rand(total, 1, generator=g, device="cuda")
+    x["S0"] = torch.randn(n, 1, 16, 16, generator=g, device="cuda")
+    out, S_T = torch.empty_like(x["v"]), torch.empty_like(x["S0"])
+    ws = gdnspec.empty_linear_seq_workspace(n, total, *dims, torch.bfloat16, backward=False)
+    gdnspec.gdn_set_wait_limit_ns(5_000_000)
+    try:
+        gdnspec.gdn_linear_seq_forward(*(x[m] for m in NAMES), out, S_T, ws, offsets=off)
+        assert gdnspec.gdn_last_error() == gdnspec.OK
+    finally:
+        gdnspec.gdn_set_wait_limit_ns(1_000_000_000)
+    # a token at a time, each from the state before it
+    S, want = x["S0"].double(), torch.empty_like(out, dtype=torch.double)
+    for t in range(int(lengths.max())):
+        live = (lengths > t).nonzero()[:, 0]
+        at = off[live].long() + t
+        q, k, v, la, beta = (x[m][at].double() for m in ("q", "k", "v", "log_alpha", "beta"))
+        S[live] = la.exp()[..., None, None] * S[live] + (beta[..., None] * v)[..., None] * k[:, :, None, :]
+        want[at] = (S[live] @ q[..., None])[..., 0]
+    held(out, want, "out")
+    held(S_T, S, "S_T")
