@@ -65,12 +65,16 @@ def backward(q, k, v, log_alpha, beta, S0, lengths, dout, dS_T):
     return dict(q=fold(dq), k=fold(dk), v=dv, log_alpha=dla, beta=db, S0=dS0)
 
 
+TURN = np.longdouble("6.28318530717958647692528676655900576839")
+
+
 def rotary(x, positions, inv_freq, scale=1.0, interleaved=False, inverse=False):
     """x [total, heads, d] turned by positions [total] times inv_freq [rot / 2], the frequencies as they are given."""
     rot = 2 * len(inv_freq)
-    # whole turns taken out in extended precision: a float64 product of a far position is good to 1e-16 of it
+    # whole turns taken off in extended precision: a far position's angle in 64 bits would be off by 1e-16 of itself
     angle = np.longdouble(positions)[:, None] * np.longdouble(inv_freq)[None, :]
-    turn = scale * np.exp(1j * (-angle if inverse else angle).astype(np.float64))[:, None, :]
+    angle = (angle - np.round(angle / TURN) * TURN).astype(np.float64)
+    turn = scale * np.exp(1j * (-angle if inverse else angle))[:, None, :]
     y = np.array(x, np.float64)
     a, b = (slice(0, rot, 2), slice(1, rot, 2)) if interleaved else (slice(0, rot // 2), slice(rot // 2, rot))
     z = (y[..., a] + 1j * y[..., b]) * turn
