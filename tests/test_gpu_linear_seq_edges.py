@@ -222,3 +222,18 @@ def test_hundreds_of_thousands_of_sequences():
         want[at] = (S[live] @ q[..., None])[..., 0]
     held(out, want, "out")
     held(S_T, S, "S_T")
+
+
+@pytest.mark.parametrize("dims", [(4, 1, 16, 48), (2, 2, 96, 96), (1, 1, 192, 80), (2, 1, 48, 208), (4, 2, 240, 16)])
+@pytest.mark.parametrize("slow", [False, True])
+def test_narrow_and_odd_heads_in_their_own_rounding(dims, slow):
+    """Sizes that are no whole boxes of 64 columns, and lengths that end inside a block, a piece of 16 and a segment."""
+    lengths = [129, 300, 17, 515, 1, 0, 1100]
+    x, off, dout, dS = inputs(lengths, *dims, seed=81, slow=slow)
+    full = (len(lengths), sum(lengths), *dims, torch.bfloat16)
+    d = outputs(x)
+    both(x, off, dout, dS, d, gdnspec.empty_linear_seq_workspace(*full).fill_(0xff), gdnspec.empty_linear_seq_record(*full).fill_(0xff))
+    assert gdnspec.gdn_last_error() == gdnspec.OK
+    want = plain(x, lengths, dout, dS)
+    for m in want:
+        held(d[m], want[m], m)

@@ -2,6 +2,8 @@
 import os
 import re
 
+import pytest
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "speculative_decoding_linear_gb300", "csrc")
 
 
@@ -28,3 +30,32 @@ def test_wide_stores_ask_for_their_place():
     found = [a for a in calls(source("gdn_linear_tc.cu"), "stg_pieces")]
     assert found and all(len(a) == 4 for a in found)
     assert not [a for a in found if a[3] == "true"]
+
+
+KERNELS = ("lin_local_tc_kernel", "lin_rows_tc_kernel", "lin_pairs_tc_kernel")
+
+
+def body(kernel):
+    """A kernel's text from its opening brace to the closing one."""
+    text = source("gdn_linear_tc.cu")
+    at = re.search(r"__global__[^;{]*\b%s\([^{;]*\{" % kernel, text)
+    assert at, kernel
+    depth = 1
+    for i in range(at.end(), len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[at.end():i]
+    raise AssertionError("%s does not end" % kernel)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_a_kernels_own_text(kernel):
+    """Each kernel initialises its barriers once, allocates and frees its tensor memory, and ends copies and products after a wait that gave up."""
+    text = body(kernel)
+    assert "__global__" not in text and "cudaError_t" not in text
+    assert len(re.findall(r"\b(?:mbar_init|init_barriers)\(", text)) == 1
+    assert len(re.findall(r"\btmem_alloc\(", text)) == len(re.findall(r"\btmem_dealloc\(", text)) == 1
+    again = re.findall(r"wait_here\(([^;]*), a\.err, nullptr\)", text)
+    assert any("full0" in a for a in again) and any(re.match(r"(drain|done)\b", a) for a in again)
+    assert "rfull" not in text or any("rfull" in a for a in again)
+    assert not re.search(r"\bmbar_wait\(|while\s*\(\s*!\s*mbar_test", text)
