@@ -143,8 +143,10 @@ __device__ void load_gates(Gates& g, const SeqArgs& a, int first, int rows, int 
     }
     __syncthreads();
 }
-__device__ __forceinline__ float decay(const Gates& g, int t, int s) {      // e^{g_t - g_s}, s <= t
-    return decay_of(LogSum{g.hi[t], g.lo[t]} - LogSum{g.hi[s], g.lo[s]});
+// e^{g_t - g_s}, s <= t: sums of log decays do not grow, so the larger one's rounding error of their difference is had by two operations
+__device__ __forceinline__ float decay(const Gates& g, int t, int s) {
+    const float d = g.hi[t] - g.hi[s], off = (d - g.hi[t]) + g.hi[s], e = expf(d);
+    return fmaf(e, (g.lo[t] - g.lo[s]) - off, e);
 }
 
 __device__ __forceinline__ Mat token_rows(const void* p, size_t ld, int first, int rows, int head, int d) {
