@@ -237,3 +237,40 @@ def test_narrow_and_odd_heads_in_their_own_rounding(dims, slow):
     want = plain(x, lengths, dout, dS)
     for m in want:
         held(d[m], want[m], m)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("offsets", [[0, 0, 0], [700, 700, 700], [350, 350, 350]])
+def test_tokens_of_no_sequence(dtype, offsets):
+    """A batch that is all padding: states and their gradients pass through, rows are zero, whatever the tokens hold."""
+    dims = (4, 2, 64, 64)
+    x, _, dout, dS = inputs([700, 0], *dims, seed=91)
+    x = {m: torch.full_like(y, float("nan"), dtype=dtype if m in "qkv" else None) if m != "S0" else y for m, y in x.items()}
+    full = (2, 700, *dims, dtype)
+    d = outputs(x)
+    both(x, torch.tensor(offsets, dtype=torch.int32, device="cuda"), torch.full_like(x["v"], float("nan")), dS, d,
+         gdnspec.empty_linear_seq_workspace(*full).fill_(0xff), gdnspec.empty_linear_seq_record(*full).fill_(0xff))
+    assert gdnspec.gdn_last_error() == gdnspec.OK
+    for m, y in d.items():
+        assert torch.equal(y, x["S0"] if m == "S_T" else dS if m == "dS0" else torch.zeros_like(y)), m
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot,H,Hk", [(16, 16, 1, 0), (16, 2, 1, 1), (16, 8, 3, 2), (48, 6, 2, 1), (64, 64, 1, 1), (128, 64, 8, 2), (256, 256, 1, 2)])
+def test_rotary_by_several_tokens_a_block(dtype, interleaved, d, rot, H, Hk):
+    """Where there are many tokens a block takes up to sixteen: the same bits as a call of few, whose blocks take one."""
+    total = 9973
+    g = torch.Generator(device="cuda").manual_seed(d + rot)
+    q = torch.randn(total, H, d, generator=g, device="cuda").to(dtype)
+    k = torch.randn(total, Hk, d, generator=g, device="cuda").to(dtype) if Hk else None
+    pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (total,), generator=g, device="cuda").int()
+    f = gdnspec.gdn_rotary_frequencies(rot)
+    whole, parts = [[torch.full_like(y, float("nan")) if y is not None else None for y in (q, k)] for _ in range(2)]
+    at = lambda y, b: None if y is None else y[b:b + 499]  # noqa: E731
+    gdnspec.gdn_rotary(q, k, pos, f, *whole, scale=1.5, interleaved=interleaved)
+    for b in range(0, total, 499):
+        gdnspec.gdn_rotary(at(q, b), at(k, b), pos[b:b + 499], f, at(parts[0], b), at(parts[1], b), scale=1.5, interleaved=interleaved)
+    assert gdnspec.gdn_last_error() == gdnspec.OK
+    for y, z, x in zip(whole, parts, (q, k)):
+        assert y is None or (torch.equal(y, z) and torch.isfinite(y).all() and torch.equal(y[..., rot:], x[..., rot:]))
