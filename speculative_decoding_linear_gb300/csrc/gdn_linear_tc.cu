@@ -216,8 +216,8 @@ constexpr uint32_t kBox = 64 * 128;
 // c_t a_t is an fp32 operand: three bf16 terms of it (2^-24 of it are left), as the sum is an fp32 output after up to
 // 2^17 tokens; the terms go to TMEM, where each thread holds one row of d_v.  b is bf16 and exact.  The tensor core cuts
 // off what does not fit 24 bits at each addition, always toward zero, 1.5e-8 of the sum: so a sum is of 192 tokens, and what
-// follows is added to it in memory, rounded (with slow decays 1.7e-6 of the state off after 512 tokens in one sum, 9.9e-7 in sums
-// of 256, 7.3e-7 of 192, 4.9e-7 of 128; 8192 tokens forward 98.4, 101 and 108 us with sums of 256, 192 and 128).
+// follows is added to it in memory, rounded (with slow decays dS0 is 9.7e-7 off with sums of 256 tokens, 7.0e-7 of 192, 4.6e-7 of
+// 128, and was 1.7e-6 in one sum of 512; 8192 tokens forward 98.8, 102 and 108 us with sums of 256, 192 and 128).
 // Bound by the products, three for each of the state's, and by forming their operands: 8192 tokens of 8 heads, 256 x 256, 37 us
 // (700 TFLOP/s of products, tensor core busy some 38 % of the time; a CTA has 3 or 4 of the 512 tiles).  Warps 0-7 form the terms (four warps 32
 // tokens, two buffers each), 8-11 move the sums out (two in TMEM) by way of shared memory, 12 copies, 13 multiplies.
@@ -1342,7 +1342,7 @@ __global__ void __launch_bounds__(kPairThreads, 2)
 //   dbeta_s      = sum_{t >= s} F_ts + v_s.(e^{G - g_s} dS k_s)
 // The first sum's pairs (t, s) by blocks: t in u's block and s before it, sums of rows from u on; s in u's block and t behind it,
 // sums of columns before u; both elsewhere, whole blocks' sums; both in u's block, rows minus columns from u on.  So what cancels is
-// of one block's terms (rows minus columns of the segment left 9.7e-7 of dlog_alpha, 6.3e-7 so).  Latency of a scan over 512 tokens:
+// of one block's terms (rows minus columns of the segment left 9.7e-7 of dlog_alpha, 6.2e-7 so).  Latency of a scan over 512 tokens:
 // 7.4 us whether 8192 or 6001 tokens.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kBlk) lin_gates_tc_kernel(SeqArgs a, const float* part, const float* phi, int tiles) {
